@@ -71,6 +71,13 @@ def load():
             "moe_layer_ex": ([I, P, P, P, P, P, I64, P, I, I, I, I, I, I, P, P, P, P, P, P, SZ, S], I),
             "qg_argmax_rows": ([P, I, I64, P, S], I),
             "qg_head_argmax": ([I, P, I64, I64, P, I, P, P, S], I),
+            "qg_rope_freqs": ([I, ctypes.c_double, P, P], I),
+            "qg_kv_append": ([P, P, I, P, I64, P, I64, P, I64, P, P, ctypes.c_float, P, I, I, P, S], I),
+            "qg_attn_workspace_size": ([P, P, I], SZ),
+            "qg_attn_paged": ([P, P, I, P, I64, ctypes.c_float, P, I, P, SZ, S], I),
+            "qg_beam_workspace_size": ([I, I, I, I64], SZ),
+            "qg_beam_select": ([P, P, P, I, I, I, I, I64, P, P, P, P, P, SZ, S], I),
+            "qg_beam_reorder": ([P, I, P, I, P, S], I),
         }
         for name, (args, res) in sig.items():
             if hasattr(L, name):
@@ -305,3 +312,182 @@ def moe_layer(qtype, xn, wr, w_gate, w_up, w_down, expert_stride, slots, n_slots
           _ptr(slots), n_slots, T, H, F, E, k, _ptr(ids), _ptr(weights), _ptr(act), _ptr(x_inout),
           _ptr(workspace), _nbytes(workspace), _stream(stream))
     return x_inout
+
+
+# ---- paged cache, attention, beam search ------------------------------------------------------
+
+DT_F32, DT_F16, DT_BF16 = 0, 1, 2
+
+
+def _dtype(t):
+    import torch
+
+    try:
+        return {torch.float32: DT_F32, torch.float16: DT_F16, torch.bfloat16: DT_BF16}[t.dtype]
+    except KeyError:
+        raise ValueError(f"unsupported dtype {t.dtype}") from None
+
+
+class KVCache(ctypes.Structure):
+    """qg_kv_cache: one layer's page pools."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("dtype", ctypes.c_int), ("n_pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("n_heads", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class KVBatch(ctypes.Structure):
+    """qg_kv_batch: the sequences, their lengths and page lists, and the prefixes they share."""
+    _fields_ = [("n_seqs", ctypes.c_int), ("n_tokens", ctypes.c_int), ("n_groups", ctypes.c_int),
+                ("max_pages", ctypes.c_int), ("max_prefix_pages", ctypes.c_int), ("q_start", ctypes.c_void_p),
+                ("kv_len", ctypes.c_void_p), ("pages", ctypes.c_void_p), ("group_start", ctypes.c_void_p),
+                ("prefix_len", ctypes.c_void_p), ("prefix_pages", ctypes.c_void_p)]
+
+
+def kv_cache(k, v):
+    """A qg_kv_cache of two pools [pages][tokens][heads][D] of one f16 or bf16 type (any strides
+    with the last one 1: a head-major pool is passed as its permuted view).  Keeps them alive."""
+    if k.shape != v.shape or k.dtype != v.dtype or k.dim() != 4:
+        raise ValueError("k and v must be 4-D pools of one shape and type")
+    if k.stride() != v.stride() or k.stride(3) != 1:
+        raise ValueError("k and v must have equal strides with heads' elements side by side")
+    if k.device != v.device:
+        raise ValueError("k and v must be on one device")
+    c = KVCache(k.data_ptr(), v.data_ptr(), _dtype(k), *k.shape, *k.stride()[:3])
+    c.tensors = (k, v)
+    return c
+
+
+def kv_caches(ks, vs):
+    """The layers' caches as one array (beam_reorder)."""
+    cs = [kv_cache(k, v) for k, v in zip(ks, vs, strict=True)]
+    arr = (KVCache * len(cs))(*cs)
+    arr.tensors = [c.tensors for c in cs]
+    return arr
+
+
+def _i32(t, what, dim, device):
+    import torch
+
+    if t is None:
+        return
+    if t.dtype != torch.int32 or t.dim() != dim or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{what} must be a contiguous {dim}-D int32 tensor on {device}")
+
+
+def kv_batch(kv_len, pages, q_start=None, n_tokens=None, group_start=None, prefix_len=None, prefix_pages=None):
+    """A qg_kv_batch from int32 device tensors: kv_len [B], pages [B][max_pages], q_start [B + 1] with the
+    number of token rows (None: one token per sequence), group_start [G + 1], prefix_len [G],
+    prefix_pages [G][max_prefix_pages].  Keeps them alive."""
+    dev = kv_len.device
+    _i32(kv_len, "kv_len", 1, dev)
+    _i32(pages, "pages", 2, dev)
+    _i32(q_start, "q_start", 1, dev)
+    _i32(group_start, "group_start", 1, dev)
+    _i32(prefix_len, "prefix_len", 1, dev)
+    _i32(prefix_pages, "prefix_pages", 2, dev)
+    B = kv_len.shape[0]
+    G = 0 if prefix_len is None else prefix_len.shape[0]
+    if pages.shape[0] != B:
+        raise ValueError("pages must have a row per sequence")
+    if q_start is None:
+        if n_tokens not in (None, B):
+            raise ValueError("without q_start there is one token per sequence")
+        n_tokens = B
+    elif q_start.shape[0] != B + 1 or n_tokens is None:
+        raise ValueError("q_start must have n_seqs + 1 entries, and n_tokens be given")
+    if G and (group_start is None or group_start.shape[0] != G + 1 or
+              (prefix_pages is not None and prefix_pages.shape[0] != G)):
+        raise ValueError("group_start must have n_groups + 1 entries and prefix_pages a row per group")
+    b = KVBatch(B, n_tokens, G, pages.shape[1], 0 if prefix_pages is None else prefix_pages.shape[1],
+                *[None if t is None else t.data_ptr()
+                  for t in (q_start, kv_len, pages, group_start, prefix_len, prefix_pages)])
+    b.tensors = (kv_len, pages, q_start, group_start, prefix_len, prefix_pages)
+    return b
+
+
+def rope_freqs(rot, theta, factors=None):
+    """The rotation table of kv_append (qg_rope_freqs), int64 [rot / 2] on the host."""
+    import torch
+
+    out = torch.empty((max(rot // 2, 1),), dtype=torch.int64)
+    f = None if factors is None else torch.as_tensor(factors, dtype=torch.float32).contiguous()
+    if f is not None and f.numel() != rot // 2:
+        raise ValueError("one factor per pair")
+    _call("qg_rope_freqs", rot, float(theta), _ptr(f), _ptr(out))
+    return out
+
+
+def _rows(t, T, n, what):
+    """Row stride of a tensor whose T rows of n elements may be slices of wider ones."""
+    if t is None:
+        return 0
+    if t.dim() == 3 and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2])):
+        raise ValueError(f"{what}: a token's heads must lie side by side")
+    if t.dim() not in (2, 3) or t.stride(-1) != 1 or t.shape[0] != T or t.numel() != T * n:
+        raise ValueError(f"{what} must have {T} rows of {n} elements")
+    return t.stride(0) if T > 1 else n
+
+
+def kv_append(cache, batch, q, k, v, q_out, freqs, pairs=False, q_norm=None, k_norm=None, eps=1e-6, stream=None):
+    """Norm, rotate and append a step's tokens (qg_kv_append).  q [T][Hq*D], k, v [T][heads*D]: f32, rows
+    may be slices of one projection's; q_out [T][Hq][D] of the cache's type; freqs a device copy of
+    rope_freqs (None: no rotation)."""
+    T, D, Hkv = batch.n_tokens, cache.head_dim, cache.n_heads
+    Hq = 0 if q is None else q_out.numel() // max(T * D, 1) if T else Hkv
+    for t, what in ((q, "q"), (k, "k"), (v, "v"), (q_norm, "q_norm"), (k_norm, "k_norm")):
+        if t is not None and _dtype(t) != DT_F32:
+            raise ValueError(f"{what} must be f32")
+    if q is not None and (_dtype(q_out) != cache.dtype or not q_out.is_contiguous()):
+        raise ValueError("q_out must be contiguous and of the cache's type")
+    for t, what in ((q_norm, "q_norm"), (k_norm, "k_norm")):
+        if t is not None and (t.numel() != D or not t.is_contiguous()):
+            raise ValueError(f"{what} must have head_dim elements")
+    _call("qg_kv_append", ctypes.byref(cache), ctypes.byref(batch), Hq, _ptr(q), _rows(q, T, Hq * D, "q"), _ptr(k),
+          _rows(k, T, Hkv * D, "k"), _ptr(v), _rows(v, T, Hkv * D, "v"), _ptr(q_norm), _ptr(k_norm), float(eps),
+          _ptr(freqs), 0 if freqs is None else 2 * freqs.numel(), int(bool(pairs)), _ptr(q_out), _stream(stream))
+    return q_out
+
+
+def attn_workspace_size(cache, batch, Hq) -> int:
+    return int(load().qg_attn_workspace_size(ctypes.byref(cache), ctypes.byref(batch), Hq))
+
+
+def attn_paged(cache, batch, q, out, scale, workspace, stream=None):
+    """Causal attention of the batch's new tokens over the cache (qg_attn_paged).  q [T][Hq][D] of the
+    cache's type (rows may be slices), out [T][Hq][D] of that type or f32."""
+    T, D = batch.n_tokens, cache.head_dim
+    Hq = out.numel() // (T * D) if T else cache.n_heads
+    if _dtype(q) != cache.dtype or not out.is_contiguous():
+        raise ValueError("q must be of the cache's type and out contiguous")
+    if out.numel() != T * Hq * D:
+        raise ValueError(f"out must have {T} rows of whole heads")
+    _call("qg_attn_paged", ctypes.byref(cache), ctypes.byref(batch), Hq, _ptr(q), _rows(q, T, Hq * D, "q"), float(scale),
+          _ptr(out), _dtype(out), _ptr(workspace), _nbytes(workspace), _stream(stream))
+    return out
+
+
+def beam_workspace_size(N, W, K, V) -> int:
+    return int(load().qg_beam_workspace_size(N, W, K, V))
+
+
+def beam_select(logits, scores, N, W, out_scores, parents, tokens, workspace, done=None, eos=-1, done_out=None,
+                stream=None):
+    """The K best continuations of N requests' W beams (qg_beam_select); K from the outputs' [N][K]."""
+    V, K = logits.shape[-1], out_scores.shape[-1]
+    if logits.numel() != N * W * V or scores.numel() != N * W or not logits.is_contiguous():
+        raise ValueError("logits must be contiguous [N*W][V] and scores [N*W]")
+    if any(t is not None and t.numel() != N * K for t in (out_scores, parents, tokens, done_out)):
+        raise ValueError("outputs must be [N][K]")
+    if done is not None and done.numel() != N * W:
+        raise ValueError("done must be [N*W]")
+    _call("qg_beam_select", _ptr(logits), _ptr(scores), _ptr(done), int(eos), N, W, K, V, _ptr(out_scores),
+          _ptr(parents), _ptr(tokens), _ptr(done_out), _ptr(workspace), _nbytes(workspace), _stream(stream))
+    return out_scores, parents, tokens
+
+
+def beam_reorder(caches, batch, parents, W, stream=None):
+    """Beam i of each request takes the cached tokens of beam parents[n][i], in place (qg_beam_reorder).
+    caches: kv_caches of all layers; batch: kv_batch(kv_len, pages)."""
+    if parents.numel() != batch.n_seqs:
+        raise ValueError("parents must be [N][W]")
+    _call("qg_beam_reorder", caches, len(caches), ctypes.byref(batch), W, _ptr(parents), _stream(stream))

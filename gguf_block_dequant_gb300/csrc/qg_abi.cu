@@ -141,7 +141,8 @@ qg_status qg_device_status(uint32_t *status_out, int clear) {
   const unsigned int w[] = {qg::read_status_gemv(clear != 0), qg::read_status_gemv1(clear != 0),
                             qg::read_status_mt(clear != 0),   qg::read_status_head(clear != 0),
                             qg::read_status_moe(clear != 0),  qg::read_status_gemm(clear != 0),
-                            qg::read_status_moetc(clear != 0)};
+                            qg::read_status_moetc(clear != 0), qg::read_status_kv(clear != 0),
+                            qg::read_status_attn(clear != 0), qg::read_status_attn_tc(clear != 0)};
   unsigned int all = 0;
   for (const unsigned int v : w) {
     if (v == 0xFFFFFFFFu) return QG_ECUDA;

@@ -1,0 +1,593 @@
+// qg_attn.cu -- causal attention over the paged cache: the kernel for few rows per segment (a
+// decode step's tokens), the kernel that joins the pieces of a row, and the entry points.
+//
+// o = sum_j p_j V_j / sum_j p_j with p_j = 2^(c q.K_j - m), m the running maximum, in one pass over
+// the keys.  A decode step reads every cached row once and does 4 operations per cached value
+// and query head, far below the tensor cores' rate, so HBM bounds it: the design keeps
+// asynchronous copies in flight on every SM and spends few instructions per byte.
+#include <math.h>
+
+#include <algorithm>
+
+#include "qg_attn.cuh"
+#include "qg_mma.cuh"
+
+__device__ unsigned int g_qg_status_attn;  // this translation unit's device status word
+
+namespace {
+
+using namespace qg;
+
+template <int D>
+struct NarrowCfg {
+  static constexpr int NW = D == 256 ? 4 : 8;                 // warps per CTA
+  static constexpr uint32_t TILE = kNarrowKeys * D * 2;       // bytes of a key (or value) tile
+  static constexpr int NST = D == 64 ? 6 : 3;                 // tiles a warp has room for
+  static constexpr uint32_t SMEM = NW * NST * 2 * TILE;       // 192 KB
+};
+
+// Each warp is a worker of its own: it walks its pieces with a private ring of key and value
+// tiles (16 keys, cp.async, no barrier wider than the warp), the piece's 16 query rows in
+// mma fragments, and writes the piece's unnormalised output, maximum and sum.  mma.sync
+// m16n8k16 fits here where tcgen05's 128-row tiles would be nearly empty.
+template <int D, bool BF16, bool OUT32>
+__global__ void __launch_bounds__(NarrowCfg<D>::NW * 32, 1) attn_narrow_kernel(const __grid_constant__ AttnArgs a) {
+  using C = NarrowCfg<D>;
+  constexpr int NT = C::NW * 32;
+  constexpr int KS = D / 16;       // 16-element steps of q.K
+  constexpr int DT = D / 8;        // 8-column tiles of the output
+  constexpr int CH = D / 8;        // 16-byte chunks per row
+  constexpr int RPI = 32 / CH;     // rows per copy instruction of the warp
+  static_assert(CH <= 32, "a row is at most one chunk per lane");
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ LineScan<NT> scan;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_wait();
+  pdl_launch_dependents();
+  const Line &ln = a.narrow;
+  const long long total = line_scan<NT>(a, ln, &scan, blockIdx.x == 0);
+  if (blockIdx.x == 0) {  // lengths outside the page lists are cut there and reported
+    for (int i = threadIdx.x; i < a.b.G + a.b.B; i += NT) {
+      const int raw = i < a.b.G ? __ldg(a.b.prefix_len + i) : __ldg(a.b.kv_len + i - a.b.G);
+      const int cap = kv_cap(i < a.b.G ? a.b.max_prefix_pages : a.b.max_pages, a.pool.page_shift);
+      if (raw < 0 || raw > cap) atomicOr(&g_qg_status_attn, QG_STATUS_BIT_ID);
+    }
+  }
+  if (total == 0) return;
+  const int nw = line_workers(ln, total);
+  const int w = warp * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
+  if (w >= nw) return;
+  long long at = line_start(w, total, nw);
+  const long long end = line_start(w + 1, total, nw);
+  if (at >= end) return;
+  Place pl;
+  if (!place_find(a, ln, scan, at, &pl)) return;
+
+  const uint32_t ring = smem_u32(smem) + static_cast<uint32_t>(warp) * (C::NST * 2 * C::TILE);
+  const int shift = a.pool.page_shift;
+  const int qr = lane >> 2, qc = lane & 3;      // fragment row and column pair
+  const int crow = lane / CH, cchunk = lane % CH;  // copy: row within an instruction, chunk
+
+  while (at < end) {
+    while (at >= pl.pos + a.pool.Hkv * pl.cost)
+      if (!place_next(a, ln, &pl)) return;
+    const UnitAt u = unit_at(ln, pl, at - pl.pos);
+    const int j0 = u.j, j1 = static_cast<int>(min(static_cast<long long>(u.n), u.j + (end - at)));
+    const Seg g = pl.g;
+
+    // ---- this lane's two rows: query fragments and key limits
+    const int tile_t0 = u.r * ln.tpt;
+    const int tokens = min(ln.tpt, g.nt - tile_t0);
+    const int nrows = tokens * a.Gq;
+    int lim[2];
+    uint32_t qf[KS][4];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int row = qr + 8 * e;
+      lim[e] = 0;
+      const uint16_t *qp = nullptr;
+      if (row < nrows) {
+        const int t = g.t0 + tile_t0 + row / a.Gq;
+        lim[e] = row_limit(a, g, t);
+        qp = a.q + t * a.q_stride + static_cast<long long>(u.h * a.Gq + row % a.Gq) * D + 2 * qc;
+      }
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        qf[ks][e] = qp ? __ldg(reinterpret_cast<const uint32_t *>(qp + 16 * ks)) : 0u;
+        qf[ks][2 + e] = qp ? __ldg(reinterpret_cast<const uint32_t *>(qp + 16 * ks + 8)) : 0u;
+      }
+    }
+    // keys below every valid row's limit need no mask
+    int all = min(qr < nrows ? lim[0] : 0x7FFFFFFF, qr + 8 < nrows ? lim[1] : 0x7FFFFFFF);
+    all = __reduce_min_sync(0xFFFFFFFFu, all);
+
+    // lane r < 16: element offset of key row 16 j + r, -1 past the end
+    const long long hoff = u.h * a.pool.head_stride;
+    auto row_off = [&](int j) -> long long {
+      const int key = 16 * j + (lane & 15);
+      if (key >= g.len || j >= j1) return -1;
+      const int page = __ldg(g.table + (key >> shift));
+      if (page < 0 || page >= a.pool.n_pages) {
+        atomicOr(&g_qg_status_attn, QG_STATUS_BIT_ID);
+        return -1;
+      }
+      return page * a.pool.page_stride + (key & ((1 << shift) - 1)) * a.pool.token_stride + hoff;
+    };
+    auto issue = [&](int j, long long off) {
+      if (j < j1) {
+        const uint32_t kb = ring + static_cast<uint32_t>(j % C::NST) * (2 * C::TILE);
+#pragma unroll
+        for (int i = 0; i < kNarrowKeys / RPI; ++i) {
+          const int row = i * RPI + crow;
+          const long long o = __shfl_sync(0xFFFFFFFFu, off, row & 15);
+          const uint32_t dst = kb + static_cast<uint32_t>(row) * (D * 2) + static_cast<uint32_t>((cchunk ^ (row & 7)) * 16);
+          const long long src = (o < 0 ? 0 : o) + 8 * cchunk;
+          const uint32_t n = o < 0 ? 0u : 16u;
+          cp_async16_zfill(dst, a.pool.k + src, n);
+          cp_async16_zfill(dst + C::TILE, a.pool.v + src, n);
+        }
+      }
+      cp_async_commit();
+    };
+
+    float o[DT][4];
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[d][e] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+
+    long long off = row_off(j0);
+#pragma unroll
+    for (int i = 0; i < C::NST - 1; ++i) {
+      const long long nx = row_off(j0 + i + 1);
+      issue(j0 + i, off);
+      off = nx;
+    }
+    for (int j = j0; j < j1; ++j) {
+      const long long nx = row_off(j + C::NST);
+      cp_async_wait<C::NST - 2>();
+      __syncwarp();  // tile j has landed, and every lane has read tile j - 1, which the next copy replaces
+      issue(j + C::NST - 1, off);
+      off = nx;
+      const uint32_t kb = ring + static_cast<uint32_t>(j % C::NST) * (2 * C::TILE), vb = kb + C::TILE;
+      // ---- scores of 16 rows x 16 keys
+      float s[2][4], s2[2][4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[0][e] = s[1][e] = s2[0][e] = s2[1][e] = 0.f;
+      const int mat = lane >> 3, krow = (lane & 7) + ((mat >> 1) << 3);
+      const uint32_t ka = kb + static_cast<uint32_t>(krow) * (D * 2);
+#pragma unroll
+      for (int ks = 0; ks < KS; ks += 2) {
+        uint32_t b[4];
+        ldsm4(b, ka + static_cast<uint32_t>(((2 * ks + (mat & 1)) ^ (krow & 7)) * 16));
+        mma16816<BF16>(s[0], qf[ks], b[0], b[1]);
+        mma16816<BF16>(s[1], qf[ks], b[2], b[3]);
+        ldsm4(b, ka + static_cast<uint32_t>(((2 * ks + 2 + (mat & 1)) ^ (krow & 7)) * 16));
+        mma16816<BF16>(s2[0], qf[ks + 1], b[0], b[1]);
+        mma16816<BF16>(s2[1], qf[ks + 1], b[2], b[3]);
+      }
+      float x[2][4];
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[nt][e] = (s[nt][e] + s2[nt][e]) * a.scale_log2;
+      if (16 * j + 16 > all) {  // masked keys by selection: whatever the products hold
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (16 * j + 8 * nt + 2 * qc + (e & 1) >= lim[e >> 1]) x[nt][e] = -INFINITY;
+      }
+      // ---- running maximum and sum of each row (four lanes share a row)
+      uint32_t ph[4], plo[4];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float mx = fmaxf(fmaxf(x[0][2 * e], x[0][2 * e + 1]), fmaxf(x[1][2 * e], x[1][2 * e + 1]));
+        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
+        const float mn = fmaxf(m[e], mx);
+        const float ms = mn == -INFINITY ? 0.f : mn;
+        if (__any_sync(0xFFFFFFFFu, mn > m[e])) {
+          const float al = ex2(m[e] - ms);
+          l[e] *= al;
+#pragma unroll
+          for (int d = 0; d < DT; ++d) {
+            o[d][2 * e] *= al;
+            o[d][2 * e + 1] *= al;
+          }
+        }
+        m[e] = mn;
+        const float p0 = ex2(x[0][2 * e] - ms), p1 = ex2(x[0][2 * e + 1] - ms);
+        const float p2 = ex2(x[1][2 * e] - ms), p3 = ex2(x[1][2 * e + 1] - ms);
+        l[e] += (p0 + p1) + (p2 + p3);
+        ph[e] = pack16<BF16>(p0, p1);
+        ph[2 + e] = pack16<BF16>(p2, p3);
+        if constexpr (OUT32) {  // what the rounding left, as a second operand
+          plo[e] = pack16<BF16>(p0 - lo16<BF16>(ph[e]), p1 - hi16<BF16>(ph[e]));
+          plo[2 + e] = pack16<BF16>(p2 - lo16<BF16>(ph[2 + e]), p3 - hi16<BF16>(ph[2 + e]));
+        }
+      }
+      // ---- o += p V
+      const int vrow = (lane & 7) + ((mat & 1) << 3);
+      const uint32_t va = vb + static_cast<uint32_t>(vrow) * (D * 2);
+#pragma unroll
+      for (int d = 0; d < DT; d += 2) {
+        uint32_t b[4];
+        ldsm4_t(b, va + static_cast<uint32_t>(((d + (mat >> 1)) ^ (vrow & 7)) * 16));
+        mma16816<BF16>(o[d], ph, b[0], b[1]);
+        mma16816<BF16>(o[d + 1], ph, b[2], b[3]);
+        if constexpr (OUT32) {
+          mma16816<BF16>(o[d], plo, b[0], b[1]);
+          mma16816<BF16>(o[d + 1], plo, b[2], b[3]);
+        }
+      }
+    }
+    cp_async_wait<0>();
+    __syncwarp();  // every lane has read the last tiles: the next piece's copies may replace them
+
+    // ---- write the piece
+    const bool alone = !g.prefix && j0 == 0 && j1 == u.n && [&] {
+      const int gr = kv_group_of(a.b, pl.s - a.b.G);
+      return gr < 0 || kv_clamp(__ldg(a.b.prefix_len + gr), 0, kv_cap(a.b.max_prefix_pages, shift)) == 0;
+    }();
+    const size_t slot = static_cast<size_t>(pl.unit + u.h * pl.rt + u.r) + static_cast<size_t>(w);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float ls = l[e];
+      ls += __shfl_xor_sync(0xFFFFFFFFu, ls, 1);
+      ls += __shfl_xor_sync(0xFFFFFFFFu, ls, 2);
+      const int row = qr + 8 * e;
+      if (row >= nrows) continue;
+      if (alone) {
+        const float inv = ls > 0.f ? 1.0f / ls : 0.f;
+        const int t = g.t0 + tile_t0 + row / a.Gq;
+        const size_t base = (static_cast<size_t>(t) * a.Hq + u.h * a.Gq + row % a.Gq) * D + 2 * qc;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+          if constexpr (OUT32)
+            *reinterpret_cast<float2 *>(static_cast<float *>(a.out) + base + 8 * d) =
+                make_float2(o[d][2 * e] * inv, o[d][2 * e + 1] * inv);
+          else
+            *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.out) + base + 8 * d) =
+                pack16<BF16>(o[d][2 * e] * inv, o[d][2 * e + 1] * inv);
+        }
+      } else {
+        float *po = ln.part_o + (slot * kNarrowRows + row) * D + 2 * qc;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+          *reinterpret_cast<float2 *>(po + 8 * d) = make_float2(o[d][2 * e], o[d][2 * e + 1]);
+        if (qc == 0) ln.part_ml[slot * kNarrowRows + row] = make_float2(m[e], ls);
+      }
+    }
+    at += j1 - j0;
+  }
+}
+
+// ---- joining ------------------------------------------------------------------------------------
+// The pieces of one row: slots first, first + 1, ... (count of them), row `row` of a `rows`-row tile.
+struct Pieces {
+  const float *o;
+  const float2 *ml;
+  size_t first;
+  int count, rows, row;
+};
+
+QG_DEVICE Pieces pieces_of(const AttnArgs &a, int s, int t, int h, int gq) {
+  Pieces p;
+  p.count = 0;
+  const Seg g = seg_load(a, s);
+  const bool nar = seg_in(a.narrow, g);
+  if (!nar && !(a.wide.workers && seg_in(a.wide, g))) return p;
+  const Line &l = nar ? a.narrow : a.wide;
+  const int r = (t - g.t0) / l.tpt;
+  const int n = unit_cost(l, g, r);
+  if (n == 0) return p;
+  const long long total = l.seg_pos[a.b.G + a.b.B];
+  const int nw = line_workers(l, total);
+  const int rt = seg_tiles(l, g);
+  const long long p0 = l.seg_pos[s] + h * seg_cost_to(l, g, rt) + seg_cost_to(l, g, r);
+  const int w0 = line_owner(p0, total, nw), w1 = line_owner(p0 + n - 1, total, nw);
+  p.o = l.part_o;
+  p.ml = l.part_ml;
+  p.first = static_cast<size_t>(l.seg_unit[s] + h * rt + r) + static_cast<size_t>(w0);
+  p.count = w1 - w0 + 1;
+  p.rows = l.rows;
+  p.row = (t - g.t0 - r * l.tpt) * a.Gq + gq;
+  return p;
+}
+
+// Online softmax over pieces i0, i0 + step, ...: lane holds D/32 consecutive outputs.
+template <int NV>
+struct Acc {
+  float m, l, o[NV];
+};
+template <int NV>
+QG_DEVICE void acc_add(Acc<NV> &x, float m, float l, const float (&o)[NV]) {
+  const float mn = fmaxf(x.m, m);
+  if (mn == -INFINITY) return;
+  const float fa = ex2(x.m - mn), fb = ex2(m - mn);
+  x.m = mn;
+  x.l = x.l * fa + l * fb;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) x.o[i] = x.o[i] * fa + o[i] * fb;
+}
+template <int D>
+QG_DEVICE void load_o(const Pieces &p, int i, int lane, float (&v)[D / 32]) {
+  const float *src = p.o + ((p.first + i) * p.rows + p.row) * D + lane * (D / 32);
+  if constexpr (D == 64) {
+    const float2 u = __ldcg(reinterpret_cast<const float2 *>(src));
+    v[0] = u.x;
+    v[1] = u.y;
+  } else {
+#pragma unroll
+    for (int q = 0; q < D / 128; ++q) {
+      const float4 u = __ldcg(reinterpret_cast<const float4 *>(src) + q);
+      v[4 * q] = u.x;
+      v[4 * q + 1] = u.y;
+      v[4 * q + 2] = u.z;
+      v[4 * q + 3] = u.w;
+    }
+  }
+}
+template <int D>
+QG_DEVICE void acc_pieces(Acc<D / 32> &x, const Pieces &p, int i0, int step, int lane) {
+  constexpr int U = 4;  // pieces in flight
+  for (int i = i0; i < p.count; i += U * step) {
+    float v[U][D / 32];
+    float2 ml[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      ml[k] = make_float2(-INFINITY, 0.f);
+      if (i + k * step < p.count) {
+        ml[k] = __ldcg(p.ml + (p.first + i + k * step) * p.rows + p.row);
+        load_o<D>(p, i + k * step, lane, v[k]);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k)
+      if (i + k * step < p.count) acc_add(x, ml[k].x, ml[k].y, v[k]);
+  }
+}
+
+template <int D, bool BF16, bool OUT32>
+QG_DEVICE void write_row(const AttnArgs &a, int t, int hq, int lane, const Acc<D / 32> &x) {
+  constexpr int NV = D / 32;
+  const float inv = x.l > 0.f ? 1.0f / x.l : 0.f;
+  const size_t base = (static_cast<size_t>(t) * a.Hq + hq) * D + lane * NV;
+  if constexpr (OUT32) {
+#pragma unroll
+    for (int i = 0; i < NV; i += 2)
+      *reinterpret_cast<float2 *>(static_cast<float *>(a.out) + base + i) = make_float2(x.o[i] * inv, x.o[i + 1] * inv);
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; i += 2)
+      *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.out) + base + i) =
+          pack16<BF16>(x.o[i] * inv, x.o[i + 1] * inv);
+  }
+}
+
+// ROW: one block of 8 warps per row, the row's pieces spread over the warps (few rows, many
+// pieces each); otherwise a warp per (token, cached head) (many rows, a piece or two each).
+template <int D, bool BF16, bool OUT32, bool ROW>
+__global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ AttnArgs a) {
+  constexpr int NV = D / 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_wait();
+  pdl_launch_dependents();
+  long long id = ROW ? blockIdx.x : static_cast<long long>(blockIdx.x) * 8 + warp;
+  const int per = ROW ? a.Hq : a.pool.Hkv;
+  const int t = static_cast<int>(id / per), hh = static_cast<int>(id - static_cast<long long>(t) * per);
+  if (t >= a.b.T) return;
+  const int b = kv_seq_of(a.b, t);
+  const int gr = b >= 0 ? kv_group_of(a.b, b) : -1;
+  if (b < 0 && (ROW ? threadIdx.x == 0 : lane == 0)) atomicOr(&g_qg_status_attn, QG_STATUS_BIT_ID);
+  const int h = ROW ? hh / a.Gq : hh;
+  Pieces own, pre;
+  own.count = pre.count = 0;
+  if (b >= 0) own = pieces_of(a, a.b.G + b, t, h, ROW ? hh % a.Gq : 0);
+  if (gr >= 0) pre = pieces_of(a, gr, t, h, ROW ? hh % a.Gq : 0);
+  if (own.count == 1 && pre.count == 0) return;  // its worker wrote the row
+  if constexpr (ROW) {
+    __shared__ float so[8][D];
+    __shared__ float2 sml[8];
+    Acc<NV> x;
+    x.m = -INFINITY;
+    x.l = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) x.o[i] = 0.f;
+    acc_pieces<D>(x, own, warp, 8, lane);
+    acc_pieces<D>(x, pre, warp, 8, lane);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) so[warp][lane * NV + i] = x.o[i];
+    if (lane == 0) sml[warp] = make_float2(x.m, x.l);
+    __syncthreads();
+    if (warp) return;
+#pragma unroll
+    for (int q = 1; q < 8; ++q) {
+      float v[NV];
+#pragma unroll
+      for (int i = 0; i < NV; ++i) v[i] = so[q][lane * NV + i];
+      acc_add(x, sml[q].x, sml[q].y, v);
+    }
+    write_row<D, BF16, OUT32>(a, t, hh, lane, x);
+  } else {
+    for (int q = 0; q < a.Gq; ++q) {
+      Acc<NV> x;
+      x.m = -INFINITY;
+      x.l = 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) x.o[i] = 0.f;
+      acc_pieces<D>(x, own, 0, 1, lane);
+      acc_pieces<D>(x, pre, 0, 1, lane);
+      write_row<D, BF16, OUT32>(a, t, h * a.Gq + q, lane, x);
+      ++own.row;
+      ++pre.row;
+    }
+  }
+}
+
+// ---- workspace ----------------------------------------------------------------------------------
+constexpr size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+struct Plan {
+  size_t bytes;
+  size_t n_pos, n_unit, n_o, n_ml;  // offsets of the narrow line's arrays
+  size_t w_pos, w_unit, w_o, w_ml;  // of the wide line's
+  int wide_workers, narrow_workers;
+};
+
+// rows bound: a unit per (cached head, row tile); tiles of a segment: tokens / tpt + 1
+Plan make_plan(const KvPool &pool, const KvBatch &b, int Gq, int sms) {
+  Plan p = {};
+  const int tn = kNarrowRows / Gq, tw = kWideRows / Gq;
+  const long long nseg = static_cast<long long>(b.G) + b.B;
+  const bool wide = attn_wide_supported(pool.D) && b.T > tn;
+  p.narrow_workers = sms * (pool.D == 256 ? 4 : 8);
+  p.wide_workers = wide ? sms : 0;
+  // a token is in its own segment and in its group's: 2 T tokens at most over all segments
+  long long un = nseg;                                            // wide line there: one row tile each
+  if (!wide) un = nseg + (b.G ? 2 : 1) * (static_cast<long long>(b.T) / tn);
+  const long long sn = un * pool.Hkv + p.narrow_workers;
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    const size_t r = at;
+    at += up256(n);
+    return r;
+  };
+  p.n_pos = take((nseg + 1) * 8);
+  p.n_unit = take((nseg + 1) * 4);
+  p.n_ml = take(static_cast<size_t>(sn) * kNarrowRows * 8);
+  p.n_o = take(static_cast<size_t>(sn) * kNarrowRows * pool.D * 4);
+  if (wide) {
+    // segments of more than tn tokens: at most T / (tn + 1) sequences (none when each has one
+    // token), and every group
+    const long long segs = b.G + (b.q_start ? std::min<long long>(b.B, b.T / (tn + 1)) : 0);
+    const long long uw = segs + (b.G ? 1 : 0) * (static_cast<long long>(b.T) / tw) +
+                         (b.q_start ? static_cast<long long>(b.T) / tw : 0);
+    const long long sw = uw * pool.Hkv + p.wide_workers;
+    p.w_pos = take((nseg + 1) * 8);
+    p.w_unit = take((nseg + 1) * 4);
+    p.w_ml = take(static_cast<size_t>(sw) * kWideRows * 8);
+    p.w_o = take(static_cast<size_t>(sw) * kWideRows * pool.D * 4);
+  }
+  p.bytes = at;
+  return p;
+}
+
+qg_status attn_check(const qg_kv_cache *cache, const qg_kv_batch *batch, int Hq, AttnArgs *a) {
+  qg_status st = kv_check_cache(cache, &a->pool);
+  if (st != QG_OK) return st;
+  st = kv_check_batch(batch, true, true, &a->b);
+  if (st != QG_OK) return st;
+  if (Hq < 1 || Hq % a->pool.Hkv) return QG_EINVAL_SHAPE;
+  if (Hq / a->pool.Hkv > kNarrowRows) return QG_EUNSUPPORTED;
+  a->Hq = Hq;
+  a->Gq = Hq / a->pool.Hkv;
+  a->D = a->pool.D;
+  return QG_OK;
+}
+
+template <int D, bool BF16, bool OUT32>
+qg_status attn_run(const AttnArgs &a, int sms, cudaStream_t s) {
+  using C = NarrowCfg<D>;
+  auto narrow = attn_narrow_kernel<D, BF16, OUT32>;
+  if (!set_smem_attr(reinterpret_cast<const void *>(narrow), C::SMEM)) return QG_ECUDA;
+  if (launch_pdl(narrow, dim3(static_cast<unsigned>(sms)), dim3(C::NW * 32), C::SMEM, s, a) != cudaSuccess)
+    return QG_ECUDA;
+  if (a.wide.workers) {
+    const qg_status st = attn_wide_launch(a, BF16, s);
+    if (st != QG_OK) return st;
+  }
+  const long long rows = static_cast<long long>(a.b.T) * a.Hq, tasks = static_cast<long long>(a.b.T) * a.pool.Hkv;
+  cudaError_t e;
+  if (rows <= 8192)
+    e = launch_pdl(attn_join_kernel<D, BF16, OUT32, true>, dim3(static_cast<unsigned>(rows)), dim3(256), 0, s, a);
+  else
+    e = launch_pdl(attn_join_kernel<D, BF16, OUT32, false>, dim3(static_cast<unsigned>((tasks + 7) / 8)), dim3(256), 0, s,
+                   a);
+  if (e != cudaSuccess) return QG_ECUDA;
+  return cudaGetLastError() == cudaSuccess ? QG_OK : QG_ECUDA;
+}
+
+template <int D>
+qg_status attn_dispatch(const AttnArgs &a, bool bf16, int sms, cudaStream_t s) {
+  if (bf16) return a.out32 ? attn_run<D, true, true>(a, sms, s) : attn_run<D, true, false>(a, sms, s);
+  return a.out32 ? attn_run<D, false, true>(a, sms, s) : attn_run<D, false, false>(a, sms, s);
+}
+
+}  // namespace
+
+namespace qg {
+unsigned int read_status_attn(bool clear) {
+  unsigned int v = 0;
+  if (cudaMemcpyFromSymbol(&v, g_qg_status_attn, sizeof(v)) != cudaSuccess) return 0xFFFFFFFFu;
+  if (clear) {
+    const unsigned int z = 0;
+    cudaMemcpyToSymbol(g_qg_status_attn, &z, sizeof(z));
+  }
+  return v;
+}
+}  // namespace qg
+
+extern "C" {
+
+size_t qg_attn_workspace_size(const qg_kv_cache *cache, const qg_kv_batch *batch, int Hq) {
+  AttnArgs a = {};
+  if (attn_check(cache, batch, Hq, &a) != QG_OK) return 0;
+  const DeviceInfo &dev = device_info();
+  return make_plan(a.pool, a.b, a.Gq, dev.ok ? dev.sms : 152).bytes;
+}
+
+qg_status qg_attn_paged(const qg_kv_cache *cache, const qg_kv_batch *batch, int Hq, const void *q, int64_t q_stride,
+                        float scale, void *out, int out_dtype, void *workspace, size_t workspace_bytes,
+                        qg_stream_t stream) {
+  AttnArgs a = {};
+  const qg_status st = attn_check(cache, batch, Hq, &a);
+  if (st != QG_OK) return st;
+  if (a.b.T == 0) return QG_OK;
+  if (!q || !out) return QG_EINVAL_PTR;
+  if (out_dtype != QG_DT_F32 && out_dtype != cache->dtype) return QG_EUNSUPPORTED;
+  if (!isfinite(scale) || q_stride < static_cast<int64_t>(Hq) * a.D || q_stride > (int64_t(1) << 38))
+    return QG_EINVAL_SHAPE;
+  if (!aligned16(q) || !aligned16(out) || q_stride % 8) return QG_EALIGN;
+  const DeviceInfo &dev = device_info();
+  const Plan p = make_plan(a.pool, a.b, a.Gq, dev.ok ? dev.sms : 152);
+  if (!workspace || workspace_bytes < p.bytes) return QG_EWORKSPACE;
+  if (!aligned16(workspace)) return QG_EALIGN;
+  if (!dev.ok) return QG_ECUDA;
+  a.q = static_cast<const uint16_t *>(q);
+  a.q_stride = q_stride;
+  a.out = out;
+  a.out32 = out_dtype == QG_DT_F32;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  auto line = [&](int rows, int keys, int workers, size_t pos, size_t unit, size_t o, size_t ml) {
+    Line l = {};
+    l.rows = rows;
+    l.keys = keys;
+    l.tpt = rows / a.Gq;
+    l.workers = workers;
+    l.seg_pos = reinterpret_cast<long long *>(ws + pos);
+    l.seg_unit = reinterpret_cast<int *>(ws + unit);
+    l.part_o = reinterpret_cast<float *>(ws + o);
+    l.part_ml = reinterpret_cast<float2 *>(ws + ml);
+    return l;
+  };
+  a.narrow = line(kNarrowRows, kNarrowKeys, p.narrow_workers, p.n_pos, p.n_unit, p.n_o, p.n_ml);
+  a.narrow.hi = p.wide_workers ? a.narrow.tpt : INT32_MAX;
+  if (p.wide_workers) {
+    a.wide = line(kWideRows, kWideKeys, p.wide_workers, p.w_pos, p.w_unit, p.w_o, p.w_ml);
+    a.wide.lo = a.narrow.tpt;
+    a.wide.hi = INT32_MAX;
+  }
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const bool bf16 = cache->dtype == QG_DT_BF16;
+  switch (a.D) {
+    case 64: return attn_dispatch<64>(a, bf16, dev.sms, s);
+    case 128: return attn_dispatch<128>(a, bf16, dev.sms, s);
+    default: return attn_dispatch<256>(a, bf16, dev.sms, s);
+  }
+}
+
+}  // extern "C"

@@ -1,0 +1,296 @@
+// qg_attn.cuh -- the work of one attention call, as its kernels share it.
+//
+// A SEGMENT is a list of cached keys with the query tokens that read it: a group's prefix with
+// all tokens of the group's sequences, or a sequence's own keys with its own tokens.  The rows
+// of a segment and a cached head are its (token, query head of that cached head) pairs; they
+// are cut into ROW TILES of `tpt` whole tokens.  A UNIT is (segment, cached head, row tile),
+// and its cost is the number of key tiles its last row sees.  All units in (segment, head, row
+// tile) order, tile by tile, form one line of tiles; worker w of n takes the part
+// [w*total/n, (w+1)*total/n) of it.  So ragged lengths balance without the host knowing
+// them, and every kernel can work out from the lengths alone who did what.  A worker's part of
+// one unit is a PIECE; unit u and worker w rise along the line and one of them rises from piece
+// to piece, so u + w numbers the pieces' slots in the workspace without gaps mattering.
+//
+// Two kernels with a line each share a call: segments with few rows (at most one row tile of 16)
+// and segments with more (row tiles of 128).  The joining kernel reads both lines.
+#pragma once
+
+#include "qg_kv.cuh"
+
+namespace qg {
+
+constexpr int kNarrowRows = 16, kNarrowKeys = 16;
+constexpr int kWideRows = 128, kWideKeys = 128;
+
+// A line of tiles: row and key tile sizes, and which segments belong to it.
+struct Line {
+  int rows, keys;        // rows and keys per tile
+  int tpt;               // tokens per row tile: rows / Gq
+  int lo, hi;            // segments with lo < tokens <= hi belong to it
+  int workers;
+  float *part_o;         // [slot][rows][D]
+  float2 *part_ml;       // [slot][rows]: running maximum (log2 units) and sum
+  long long *seg_pos;    // [segments + 1] first tile of each segment
+  int *seg_unit;         // [segments + 1] first unit of each segment
+};
+
+struct AttnArgs {
+  KvPool pool;
+  KvBatch b;
+  const uint16_t *q;
+  void *out;
+  long long q_stride;
+  float scale_log2;      // scale * log2(e): exponentials are powers of two
+  int Hq, Gq, D;
+  int out32;
+  Line narrow, wide;     // wide.workers == 0: the narrow line has every segment
+};
+
+struct Seg {
+  int t0, nt;            // token rows
+  int len;               // keys
+  int prefix;
+  const int32_t *table;
+};
+
+QG_DEVICE Seg seg_load(const AttnArgs &a, int s) {
+  Seg g;
+  int b0, b1;
+  if (s < a.b.G) {
+    b0 = kv_clamp(__ldg(a.b.group_start + s), 0, a.b.B);
+    b1 = kv_clamp(__ldg(a.b.group_start + s + 1), b0, a.b.B);
+    g.len = kv_clamp(__ldg(a.b.prefix_len + s), 0, kv_cap(a.b.max_prefix_pages, a.pool.page_shift));
+    g.table = a.b.prefix_pages + static_cast<size_t>(s) * a.b.max_prefix_pages;
+    g.prefix = 1;
+  } else {
+    b0 = s - a.b.G;
+    b1 = b0 + 1;
+    g.len = kv_own_len(a.b, a.pool.page_shift, b0);
+    g.table = a.b.pages + static_cast<size_t>(b0) * a.b.max_pages;
+    g.prefix = 0;
+  }
+  g.t0 = kv_tok(a.b, b0);
+  g.nt = max(0, kv_tok(a.b, b1) - g.t0);
+  return g;
+}
+
+QG_DEVICE bool seg_in(const Line &l, const Seg &g) { return g.nt > l.lo && g.nt <= l.hi && g.len > 0; }
+QG_DEVICE int seg_tiles(const Line &l, const Seg &g) { return (g.nt + l.tpt - 1) / l.tpt; }  // row tiles
+
+// key tiles of row tile r: up to the last key its last token sees
+QG_DEVICE int unit_cost(const Line &l, const Seg &g, int r) {
+  int seen = g.len;
+  if (!g.prefix) seen = kv_clamp(g.len - g.nt + min(g.nt, (r + 1) * l.tpt), 0, g.len);
+  return (seen + l.keys - 1) / l.keys;
+}
+// sum of floor((a i + b) / m) over i < n, by the Euclidean recursion (a, b, n >= 0, m > 0)
+QG_DEVICE long long floor_sum(long long n, int m, int a, int b) {
+  long long r = 0;
+  while (n > 0) {
+    if (a >= m) {
+      r += n * (n - 1) / 2 * (a / m);
+      a %= m;
+    }
+    if (b >= m) {
+      r += n * (b / m);
+      b %= m;
+    }
+    const long long y = a * n + b;
+    if (y < m) break;
+    n = y / m;
+    b = static_cast<int>(y % m);
+    const int t = m;
+    m = a;
+    a = t;
+  }
+  return r;
+}
+
+// key tiles of row tiles 0 .. r-1
+QG_DEVICE long long seg_cost_to(const Line &l, const Seg &g, int r) {
+  const int rt = seg_tiles(l, g);
+  if (g.prefix || rt == 1) return static_cast<long long>(r) * unit_cost(l, g, 0);
+  // own keys: tile i < rt - 1 sees base + (i + 1) tpt of them (none while that is not positive)
+  const int base = g.len - g.nt;
+  const int m = min(r, rt - 1);
+  const int i0 = base < 0 ? min(m, -base / l.tpt) : 0;  // tiles that see nothing
+  long long c = floor_sum(m - i0, l.keys, l.tpt, base + (i0 + 1) * l.tpt + l.keys - 1);
+  if (r == rt) c += unit_cost(l, g, rt - 1);
+  return c;
+}
+
+// workers that take part: at least `kMinTiles` tiles each
+constexpr int kMinTiles = 2;
+QG_DEVICE int line_workers(const Line &l, long long total) {
+  const long long n = (total + kMinTiles - 1) / kMinTiles;
+  return n < l.workers ? static_cast<int>(n) : l.workers;
+}
+QG_DEVICE long long line_start(long long w, long long total, int n) { return w * total / n; }
+QG_DEVICE int line_owner(long long p, long long total, int n) {
+  return static_cast<int>(((p + 1) * n + total - 1) / total - 1);
+}
+
+// keys of the segment that token t sees (t in the segment's token rows)
+QG_DEVICE int row_limit(const AttnArgs &a, const Seg &g, int t) {
+  if (!g.prefix) return kv_clamp(g.len - g.nt + (t - g.t0) + 1, 0, g.len);
+  const int b = kv_seq_of(a.b, t);
+  if (b < 0) return 0;
+  const int t0 = kv_tok(a.b, b), n = kv_tok(a.b, b + 1) - t0;
+  const long long seen = static_cast<long long>(g.len) + kv_own_len(a.b, a.pool.page_shift, b) - n + (t - t0) + 1;
+  return seen < 0 ? 0 : seen > g.len ? g.len : static_cast<int>(seen);
+}
+
+// ---- the block's view of a line ---------------------------------------------------------------
+// Thread i of the block owns segments [i*chunk, (i+1)*chunk); pos[i], unit[i] are the line's
+// tiles and units before them.  Filled by all threads of the block.
+template <int NT>
+struct LineScan {
+  long long pos[NT + 1];
+  int unit[NT + 1];
+};
+
+template <int NT>
+QG_DEVICE long long line_scan(const AttnArgs &a, const Line &l, LineScan<NT> *sc, bool publish) {
+  const int nseg = a.b.G + a.b.B;
+  const int chunk = (nseg + NT - 1) / NT;
+  const int s0 = min(nseg, static_cast<int>(threadIdx.x) * chunk), s1 = min(nseg, s0 + chunk);
+  long long c = 0;
+  int u = 0;
+  for (int s = s0; s < s1; ++s) {
+    const Seg g = seg_load(a, s);
+    if (!seg_in(l, g)) continue;
+    const int rt = seg_tiles(l, g);
+    c += a.pool.Hkv * seg_cost_to(l, g, rt);
+    u += a.pool.Hkv * rt;
+  }
+  // inclusive scan over the block: within warps, then over the warps' totals
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long ci = c;
+  int ui = u;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long pc = __shfl_up_sync(0xFFFFFFFFu, ci, o);
+    const int pu = __shfl_up_sync(0xFFFFFFFFu, ui, o);
+    if (lane >= o) {
+      ci += pc;
+      ui += pu;
+    }
+  }
+  __shared__ long long wc[NT / 32];
+  __shared__ int wu[NT / 32];
+  if (lane == 31) {
+    wc[warp] = ci;
+    wu[warp] = ui;
+  }
+  __syncthreads();
+  long long bc = 0;
+  int bu = 0;
+  for (int w = 0; w < warp; ++w) {
+    bc += wc[w];
+    bu += wu[w];
+  }
+  sc->pos[threadIdx.x] = bc + ci - c;
+  sc->unit[threadIdx.x] = bu + ui - u;
+  if (threadIdx.x == NT - 1) {
+    sc->pos[NT] = bc + ci;
+    sc->unit[NT] = bu + ui;
+  }
+  if (publish) {
+    long long p = bc + ci - c;
+    int uu = bu + ui - u;
+    for (int s = s0; s < s1; ++s) {
+      l.seg_pos[s] = p;
+      l.seg_unit[s] = uu;
+      const Seg g = seg_load(a, s);
+      if (!seg_in(l, g)) continue;
+      const int rt = seg_tiles(l, g);
+      p += a.pool.Hkv * seg_cost_to(l, g, rt);
+      uu += a.pool.Hkv * rt;
+    }
+    if (threadIdx.x == NT - 1) {
+      l.seg_pos[nseg] = bc + ci;
+      l.seg_unit[nseg] = bu + ui;
+    }
+  }
+  __syncthreads();
+  return sc->pos[NT];
+}
+
+// A place on the line: segment s (g), its first tile and unit, head, row tile and key tile.
+struct Place {
+  int s;
+  Seg g;
+  long long pos;   // first tile of the segment
+  int unit;        // first unit of the segment
+  long long cost;  // tiles of one head of the segment
+  int rt;          // row tiles
+};
+
+// moves to the next segment of the line at or after s
+QG_DEVICE bool place_at(const AttnArgs &a, const Line &l, Place *p, int s) {
+  const int nseg = a.b.G + a.b.B;
+  for (; s < nseg; ++s) {
+    p->g = seg_load(a, s);
+    if (!seg_in(l, p->g)) continue;
+    p->s = s;
+    p->rt = seg_tiles(l, p->g);
+    p->cost = seg_cost_to(l, p->g, p->rt);
+    if (p->cost > 0) return true;
+    p->unit += a.pool.Hkv * p->rt;
+  }
+  return false;
+}
+QG_DEVICE bool place_next(const AttnArgs &a, const Line &l, Place *p) {
+  p->pos += a.pool.Hkv * p->cost;
+  p->unit += a.pool.Hkv * p->rt;
+  return place_at(a, l, p, p->s + 1);
+}
+template <int NT>
+QG_DEVICE bool place_find(const AttnArgs &a, const Line &l, const LineScan<NT> &sc, long long at, Place *p) {
+  int lo = 0, hi = NT;  // the last thread whose segments start at or before `at`
+  while (hi - lo > 1) {
+    const int m = (lo + hi) / 2;
+    if (sc.pos[m] <= at) lo = m;
+    else hi = m;
+  }
+  const int chunk = (a.b.G + a.b.B + NT - 1) / NT;
+  p->pos = sc.pos[lo];
+  p->unit = sc.unit[lo];
+  if (!place_at(a, l, p, lo * chunk)) return false;
+  while (p->pos + a.pool.Hkv * p->cost <= at)
+    if (!place_next(a, l, p)) return false;
+  return true;
+}
+
+// unit of the segment that holds its tile `local`: head, row tile, key tile, tiles of the unit
+struct UnitAt {
+  int h, r, j, n;
+};
+QG_DEVICE UnitAt unit_at(const Line &l, const Place &p, long long local) {
+  UnitAt u;
+  u.h = static_cast<int>(local / p.cost);
+  const long long rem = local - u.h * p.cost;
+  if (p.rt == 1 || p.g.prefix) {
+    u.n = unit_cost(l, p.g, 0);
+    u.r = static_cast<int>(rem / u.n);
+    u.j = static_cast<int>(rem - static_cast<long long>(u.r) * u.n);
+    return u;
+  }
+  int lo = 0, hi = p.rt;  // the last row tile that starts at or before rem
+  while (hi - lo > 1) {
+    const int m = (lo + hi) / 2;
+    if (seg_cost_to(l, p.g, m) <= rem) lo = m;
+    else hi = m;
+  }
+  u.r = lo;
+  u.n = unit_cost(l, p.g, lo);
+  const long long c = seg_cost_to(l, p.g, lo);
+  u.j = static_cast<int>(rem - c);
+  return u;
+}
+
+// attention over many rows per segment on the tcgen05 tensor cores (qg_attn_tc.cu)
+qg_status attn_wide_launch(const AttnArgs &a, bool bf16, cudaStream_t s);
+bool attn_wide_supported(int D);
+
+}  // namespace qg

@@ -1,0 +1,381 @@
+// qg_beam.cu -- one beam-search selection: the K best continuations of each request's W beams
+// over the vocabulary.
+//
+// cand(w, v) = score_w + (logit[w][v] - m_w) - log sum_v exp(logit[w][v] - m_w).  Within a row the order is the logits' order, so the
+// first kernel needs one pass over the logits (the bytes that bound it): each CTA takes a slice
+// of one row into registers, forms the slice's maximum and sum of exponentials and keeps its K
+// largest (logit, lowest index first).  The second joins a request's slices: the row sums in 64
+// bits, each row's K best, then the K best of W*K candidates ranked in 64 bits.
+#include <math.h>
+
+#include <algorithm>
+
+#include "qg_common.cuh"
+#include "qg_host.h"
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxK = 64;
+constexpr int kList = 1024;  // candidates a slice can hold before the exact fallback
+
+// f32 -> unsigned that rises with the value; NaN counts as -inf
+QG_DEVICE uint32_t ord_of(float x) {
+  if (isnan(x)) x = -INFINITY;
+  const uint32_t u = __float_as_uint(x);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+QG_DEVICE float ord_val(uint32_t o) { return __uint_as_float(o & 0x80000000u ? o & 0x7FFFFFFFu : ~o); }
+// one 64-bit key per (value, index): larger is better, equal values by the lowest index.  0 is
+// below every key of a real value.
+QG_DEVICE unsigned long long key_of(float x, uint32_t idx) {
+  return (static_cast<unsigned long long>(ord_of(x)) << 32) | (0xFFFFFFFFu - idx);
+}
+QG_DEVICE uint32_t key_idx(unsigned long long k) { return 0xFFFFFFFFu - static_cast<uint32_t>(k); }
+QG_DEVICE float key_val(unsigned long long k) { return ord_val(static_cast<uint32_t>(k >> 32)); }
+
+struct SelectArgs {
+  const float *logits, *scores;
+  const uint8_t *done;
+  float *out_scores;
+  int32_t *parents, *tokens;
+  uint8_t *done_out;
+  unsigned long long *keys;  // [N*W][S][K], 0: none
+  float2 *ms;                // [N*W][S] slice maximum and sum of exp(x - maximum)
+  long long V;
+  int N, W, K, S, eos, slice, vec4;
+};
+
+QG_DEVICE unsigned long long warp_max64(unsigned long long v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const unsigned long long u = __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    v = u > v ? u : v;
+  }
+  return v;
+}
+
+// PT values per thread: the slice is PT * 256 values.  Value i of thread t is element
+// 1024 (i / 4) + 4 t + i % 4 of the slice.
+template <int PT>
+__global__ void __launch_bounds__(kThreads) select_slice_kernel(const SelectArgs a) {
+  __shared__ float red[8];
+  __shared__ uint32_t wmax[8], wmin[8];
+  __shared__ unsigned long long list[kList], best[8];
+  __shared__ int count;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int row = blockIdx.y, sl = blockIdx.x;
+  const size_t out = static_cast<size_t>(row) * a.S + sl;
+  unsigned long long *keys = a.keys + out * a.K;
+  if (a.done && __ldg(a.done + row)) {
+    // an ended beam: eos at probability 1, every other token at none; slice 0 tells it all
+    if (sl == 0) {
+      const bool has = a.eos >= 0 && a.eos < a.V;
+      for (int i = threadIdx.x; i < a.K; i += kThreads) {
+        unsigned long long k = 0;
+        if (has && i == 0) k = key_of(0.f, static_cast<uint32_t>(a.eos));
+        else {
+          long long v = has ? i - 1 : i;  // the lowest indices other than eos
+          if (has && v >= a.eos) ++v;
+          if (v < a.V) k = key_of(-INFINITY, static_cast<uint32_t>(v));
+        }
+        keys[i] = k;
+      }
+      if (threadIdx.x == 0) a.ms[out] = make_float2(0.f, 1.f);
+    } else {
+      for (int i = threadIdx.x; i < a.K; i += kThreads) keys[i] = 0;
+      if (threadIdx.x == 0) a.ms[out] = make_float2(-INFINITY, 0.f);
+    }
+    return;
+  }
+  const long long base = static_cast<long long>(sl) * a.slice;
+  const int n = static_cast<int>(min(static_cast<long long>(a.slice), a.V - base));
+  const float *x = a.logits + static_cast<size_t>(row) * a.V + base;
+  float v[PT];
+#pragma unroll
+  for (int i = 0; i < PT; i += 4) {
+    const int e = 256 * i + 4 * static_cast<int>(threadIdx.x);
+    if (a.vec4 && e + 4 <= n) {
+      const float4 q = __ldg(reinterpret_cast<const float4 *>(x + e));
+      v[i] = q.x + 0.0f;  // -0 and +0 are one value
+      v[i + 1] = q.y + 0.0f;
+      v[i + 2] = q.z + 0.0f;
+      v[i + 3] = q.w + 0.0f;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[i + j] = e + j < n ? __ldg(x + e + j) + 0.0f : -INFINITY;
+    }
+  }
+  // ---- maximum and sum of exponentials
+  float mx = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < PT; ++i) mx = fmaxf(mx, v[i]);  // fmaxf drops NaN
+  const uint32_t mo = ord_of(mx);
+  const uint32_t wm = __reduce_max_sync(0xFFFFFFFFu, mo), wn = __reduce_min_sync(0xFFFFFFFFu, mo);
+  if (lane == 0) {
+    wmax[warp] = wm;
+    wmin[warp] = wn;
+  }
+  if (threadIdx.x == 0) count = 0;
+  __syncthreads();
+  uint32_t hi = 0, lo = 0xFFFFFFFFu;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    hi = max(hi, wmax[q]);
+    lo = min(lo, wmin[q]);
+  }
+  const float bm = ord_val(hi);
+  float sum = 0.f;
+  if (isfinite(bm)) {
+#pragma unroll
+    for (int i = 0; i < PT; ++i) sum += isnan(v[i]) ? 0.f : expf(v[i] - bm);
+  }
+  sum = warp_sum(sum);
+  if (lane == 0) red[warp] = sum;
+
+  // ---- a value t that at least K threads' maxima reach (so K values do), as high as a few
+  // halvings of [lowest, highest maximum] bring it: few values pass it
+  const int K = min(a.K, n);
+  uint32_t tl = lo, th = hi;  // count(tl) >= K; th not known to have it
+  {
+    int c = __syncthreads_count(mo >= th);
+    if (c >= K) tl = th;
+    while (tl < th && th - tl > 1) {
+      const uint32_t m = tl + (th - tl) / 2;
+      c = __syncthreads_count(mo >= m);
+      if (c >= K) {
+        tl = m;
+        if (c <= K + 16) break;
+      } else {
+        th = m;
+      }
+    }
+  }
+  if (threadIdx.x == 0) {
+    float s = 0.f;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) s += red[q];
+    a.ms[out] = make_float2(bm, s);
+  }
+  if (mo >= tl) {
+#pragma unroll
+    for (int i = 0; i < PT; ++i) {
+      const int e = 256 * (i & ~3) + 4 * static_cast<int>(threadIdx.x) + (i & 3);
+      if (e < n && ord_of(v[i]) >= tl) {
+        const int at = atomicAdd(&count, 1);
+        if (at < kList) list[at] = key_of(v[i], static_cast<uint32_t>(base + e));
+      }
+    }
+  }
+  __syncthreads();
+  const int c = count;
+  if (c >= K && c <= kList) {
+    // keys differ, so a key's rank is the number of larger ones
+    for (int i = threadIdx.x; i < c; i += kThreads) {
+      const unsigned long long k = list[i];
+      int r = 0;
+      for (int j = 0; j < c; ++j) r += list[j] > k;
+      if (r < K) keys[r] = k;
+    }
+  } else {
+    // many equal values (or fewer threads than K hold values): one maximum at a time
+    unsigned long long last = ~0ull;
+    for (int r = 0; r < K; ++r) {
+      unsigned long long k = 0;
+#pragma unroll
+      for (int i = 0; i < PT; ++i) {
+        const int e = 256 * (i & ~3) + 4 * static_cast<int>(threadIdx.x) + (i & 3);
+        if (e < n) {
+          const unsigned long long u = key_of(v[i], static_cast<uint32_t>(base + e));
+          if (u < last && u > k) k = u;
+        }
+      }
+      k = warp_max64(k);
+      if (lane == 0) best[warp] = k;
+      __syncthreads();
+      k = best[0];
+#pragma unroll
+      for (int q = 1; q < 8; ++q) k = best[q] > k ? best[q] : k;
+      if (threadIdx.x == 0) keys[r] = k;
+      last = k;
+      __syncthreads();
+    }
+  }
+  for (int i = K + threadIdx.x; i < a.K; i += kThreads) keys[i] = 0;
+}
+
+// One CTA per request.  A warp takes a row at a time: its slices' sums, then its K best keys (the
+// slices' lists fall, so a list's next key is the only one that can come next; lane q holds the
+// heads of lists q, q + 32, ...), then all W*K candidates are ranked against each other.
+constexpr int kMergeThreads = 512;
+__global__ void __launch_bounds__(kMergeThreads) select_merge_kernel(const SelectArgs a) {
+  extern __shared__ uint8_t smem[];
+  double *cand = reinterpret_cast<double *>(smem);                                      // [W*K]
+  uint32_t *tok = reinterpret_cast<uint32_t *>(cand + static_cast<size_t>(a.W) * a.K);  // [W*K]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nwarps = kMergeThreads / 32;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int req = blockIdx.x;
+  for (int w = warp; w < a.W; w += nwarps) {
+    const int row = req * a.W + w;
+    const float2 *ms = a.ms + static_cast<size_t>(row) * a.S;
+    float m = -INFINITY;
+    for (int s = lane; s < a.S; s += 32) m = fmaxf(m, __ldcg(&ms[s]).x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    double sum = 0.0;
+    if (isfinite(m))
+      for (int s = lane; s < a.S; s += 32) {
+        const float2 p = __ldcg(&ms[s]);
+        if (p.y > 0.f) sum += static_cast<double>(p.y) * static_cast<double>(expf(p.x - m));
+      }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    const float sc = __ldg(a.scores + row);
+    const bool none = !isfinite(m) || !isfinite(sc);  // no distribution, or a beam not continued
+    // candidate = off + (logit - m): a row of huge equal logits would absorb the rest otherwise
+    const double off = none ? 0.0 : static_cast<double>(sc) - log(sum);
+    const unsigned long long *kr = a.keys + static_cast<size_t>(row) * a.S * a.K;
+    if (none) {
+      for (int i = lane; i < a.K; i += 32) {
+        cand[w * a.K + i] = -INFINITY;
+        tok[w * a.K + i] = i < a.V ? static_cast<uint32_t>(i) : 0xFFFFFFFFu;
+      }
+      continue;
+    }
+    // lane's lists: positions and heads (S <= 32 * kHeads lists)
+    constexpr int kHeads = 4;
+    int at[kHeads];
+    unsigned long long head[kHeads];
+#pragma unroll
+    for (int q = 0; q < kHeads; ++q) {
+      const int s = lane + 32 * q;
+      at[q] = 0;
+      head[q] = s < a.S ? __ldcg(kr + static_cast<size_t>(s) * a.K) : 0ull;
+    }
+    for (int r = 0; r < a.K; ++r) {
+      unsigned long long k = 0;
+#pragma unroll
+      for (int q = 0; q < kHeads; ++q) k = head[q] > k ? head[q] : k;
+      k = warp_max64(k);
+      if (lane == 0) {
+        cand[w * a.K + r] = k ? off + (static_cast<double>(key_val(k)) - static_cast<double>(m)) : -INFINITY;
+        tok[w * a.K + r] = k ? key_idx(k) : 0xFFFFFFFFu;
+      }
+      if (k) {
+#pragma unroll
+        for (int q = 0; q < kHeads; ++q)
+          if (head[q] == k) {
+            ++at[q];
+            head[q] = at[q] < a.K ? __ldcg(kr + static_cast<size_t>(lane + 32 * q) * a.K + at[q]) : 0ull;
+          }
+      }
+    }
+  }
+  __syncthreads();
+  const int total = a.W * a.K;
+  for (int i = threadIdx.x; i < total; i += kMergeThreads) {
+    const double x = cand[i];
+    const uint32_t v = tok[i];
+    if (v == 0xFFFFFFFFu) continue;
+    const int w = i / a.K;
+    int r = 0;
+    for (int j = 0; j < total; ++j) {
+      const double y = cand[j];
+      if (y > x) {
+        ++r;
+      } else if (y == x) {
+        const uint32_t u = tok[j];
+        const int wj = j / a.K;
+        if (u != 0xFFFFFFFFu && (wj < w || (wj == w && u < v))) ++r;
+      }
+    }
+    if (r < a.K) {
+      const size_t o = static_cast<size_t>(req) * a.K + r;
+      a.out_scores[o] = static_cast<float>(x);
+      a.parents[o] = w;
+      a.tokens[o] = static_cast<int32_t>(v);
+      if (a.done_out)
+        a.done_out[o] = (a.done && __ldg(a.done + req * a.W + w)) || static_cast<int>(v) == a.eos ? 1 : 0;
+    }
+  }
+}
+
+// Values per thread of a slice: as many slices as fill the device twice, 8 to 32 values a thread,
+// and no more than 128 slices a row (what the merge holds).
+int slice_values(long long rows, long long V, int sms) {
+  int pt = 8;
+  while (pt < 32 && rows * ((V + kThreads * pt - 1) / (kThreads * pt)) > 8LL * sms) pt *= 2;
+  while (pt < 512 && (V + kThreads * pt - 1) / (kThreads * pt) > 128) pt *= 2;
+  return pt;
+}
+
+bool select_shape(int N, int W, int K, int64_t V) {
+  return N >= 0 && W >= 1 && W <= 64 && K >= 1 && K <= kMaxK && V >= 1 && V <= (1 << 20) &&
+         static_cast<long long>(W) * V >= K && static_cast<long long>(N) * W <= 65535;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t qg_beam_workspace_size(int N, int W, int K, int64_t V) {
+  if (!select_shape(N, W, K, V)) return 0;
+  const qg::DeviceInfo &dev = qg::device_info();
+  const long long rows = static_cast<long long>(N) * W;
+  const int slice = kThreads * slice_values(rows, V, dev.ok ? dev.sms : 152);
+  const size_t S = static_cast<size_t>((V + slice - 1) / slice);
+  return (rows * S * 8 + 255) / 256 * 256 + rows * S * K * 8;
+}
+
+qg_status qg_beam_select(const float *logits, const float *scores, const uint8_t *done, int eos, int N, int W, int K,
+                         int64_t V, float *out_scores, int32_t *parents, int32_t *tokens, uint8_t *done_out,
+                         void *workspace, size_t workspace_bytes, qg_stream_t stream) {
+  if (!select_shape(N, W, K, V) || eos >= V) return QG_EINVAL_SHAPE;
+  if (N == 0) return QG_OK;
+  if (!logits || !scores || !out_scores || !parents || !tokens) return QG_EINVAL_PTR;
+  auto odd = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; };
+  if (odd(logits) || odd(scores) || odd(out_scores) || odd(parents) || odd(tokens)) return QG_EALIGN;
+  if (!workspace || workspace_bytes < qg_beam_workspace_size(N, W, K, V)) return QG_EWORKSPACE;
+  if (!qg::aligned16(workspace)) return QG_EALIGN;
+  const qg::DeviceInfo &dev = qg::device_info();
+  if (!dev.ok) return QG_ECUDA;
+  SelectArgs a = {};
+  const long long rows = static_cast<long long>(N) * W;
+  const int pt = slice_values(rows, V, dev.sms);
+  a.slice = kThreads * pt;
+  a.S = static_cast<int>((V + a.slice - 1) / a.slice);
+  a.logits = logits;
+  a.scores = scores;
+  a.done = done;
+  a.out_scores = out_scores;
+  a.parents = parents;
+  a.tokens = tokens;
+  a.done_out = done_out;
+  a.ms = static_cast<float2 *>(workspace);
+  a.keys = reinterpret_cast<unsigned long long *>(static_cast<uint8_t *>(workspace) +
+                                                  (static_cast<size_t>(rows) * a.S * 8 + 255) / 256 * 256);
+  a.V = V;
+  a.N = N;
+  a.W = W;
+  a.K = K;
+  a.eos = eos;
+  a.vec4 = V % 4 == 0 && qg::aligned16(logits);
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const dim3 grid(static_cast<unsigned>(a.S), static_cast<unsigned>(rows)), block(kThreads);
+  cudaError_t e;
+  if (pt == 8) e = qg::launch_pdl(select_slice_kernel<8>, grid, block, 0, s, a);
+  else if (pt == 16) e = qg::launch_pdl(select_slice_kernel<16>, grid, block, 0, s, a);
+  else e = qg::launch_pdl(select_slice_kernel<32>, grid, block, 0, s, a);
+  if (e != cudaSuccess) return QG_ECUDA;
+  const size_t smem = static_cast<size_t>(W) * K * 12;
+  if (smem > 48 * 1024 && !qg::set_smem_attr(reinterpret_cast<const void *>(select_merge_kernel), 64 * 64 * 12))
+    return QG_ECUDA;
+  if (qg::launch_pdl(select_merge_kernel, dim3(static_cast<unsigned>(N)), dim3(kMergeThreads), smem, s, a) != cudaSuccess)
+    return QG_ECUDA;
+  return cudaGetLastError() == cudaSuccess ? QG_OK : QG_ECUDA;
+}
+
+}  // extern "C"

@@ -98,5 +98,8 @@ unsigned int read_status_head(bool clear);
 unsigned int read_status_moetc(bool clear);
 unsigned int read_status_moe(bool clear);
 unsigned int read_status_gemm(bool clear);
+unsigned int read_status_kv(bool clear);
+unsigned int read_status_attn(bool clear);
+unsigned int read_status_attn_tc(bool clear);
 
 }  // namespace qg

@@ -303,6 +303,122 @@ QG_API qg_status moe_layer_ex(int type, const float *xn, const float *wr, const 
                               float *act, float *x_inout, void *workspace, size_t workspace_bytes,
                               qg_stream_t stream);
 
+/* ---- paged key/value cache ------------------------------------------------------------------
+ * The steps between a layer's q/k/v projections and its output projection, and the beam search
+ * that follows the head (qkNormRope, kvStore, attnScore / softmax / attnOut and their batched
+ * forms on the pages; the pages keep one sequence in one f16 buffer, this cache keeps many in
+ * pages).  A cache is a pool of n_pages pages for the keys and one for the values of a layer;
+ * token s of a sequence lives in row s % page_size of page table[s / page_size].
+ *   - Element (page p, row r, head h, i) is at p*page_stride + r*token_stride + h*head_stride + i
+ *     (strides in elements, the same for k and v), so token-major and head-major pools and
+ *     pools interleaved in one allocation are all described.
+ *   - k, v 16-byte aligned, strides multiples of 8 elements and not negative, page_size a power
+ *     of two up to 65536, head_dim 64, 128 or 256.  Distinct elements must not overlap.
+ * Both structs are HOST structs, read during the call. */
+enum { QG_DT_F32 = 0, QG_DT_F16 = 1, QG_DT_BF16 = 2 };
+
+typedef struct qg_kv_cache {
+  void *k, *v;       /* device */
+  int dtype;         /* QG_DT_F16 or QG_DT_BF16 */
+  int n_pages, page_size, n_heads, head_dim;
+  int64_t page_stride, token_stride, head_stride;
+} qg_kv_cache;
+
+/* A batch of n_seqs sequences with n_tokens new tokens in all.  The new tokens of sequence b
+ * are rows q_start[b] .. q_start[b+1]-1 of the token tensors (q_start NULL: one token per
+ * sequence, n_tokens == n_seqs); kv_len[b] counts the sequence's own cached tokens WITH the new
+ * ones, so new token i of n sits in slot kv_len[b] - n + i of the sequence's page list.
+ * Groups (n_groups 0: none) share a prefix: sequences group_start[g] .. group_start[g+1]-1 are
+ * preceded by the prefix_len[g] tokens of prefix_pages[g], stored once.  A token's position is
+ * (its group's prefix length) + (its slot).
+ *   - pages: int32 [n_seqs][max_pages]; prefix_pages: int32 [n_groups][max_prefix_pages].
+ *   - q_start and group_start rise and start at 0; all arrays are device memory, 4-byte
+ *     aligned, and read by the kernels (a captured graph sees later contents).
+ *   - Lengths past the page lists, negative lengths, page ids outside [0, n_pages) and new tokens
+ *     without a slot set QG_EDEVICE_ID in the device status; nothing out of range is accessed.
+ * Limits: n_seqs, n_groups <= 65535, n_groups <= n_seqs, n_tokens <= 2^24.  A call on a batch
+ * without tokens (without sequences for qg_beam_reorder) enqueues nothing. */
+typedef struct qg_kv_batch {
+  int n_seqs, n_tokens, n_groups, max_pages, max_prefix_pages;
+  const int32_t *q_start;      /* [n_seqs + 1] or NULL */
+  const int32_t *kv_len;       /* [n_seqs] */
+  int32_t *pages;              /* written by qg_beam_reorder only */
+  const int32_t *group_start;  /* [n_groups + 1] */
+  const int32_t *prefix_len;   /* [n_groups] */
+  const int32_t *prefix_pages; /* qg_kv_append does not read it */
+} qg_kv_batch;
+
+/* Position-rotation table for qg_kv_append: out[i] = round(2^64 * f_i / (2 pi)), the turns per
+ * position of pair i < rot/2 as a 64-bit fraction, f_i = theta^(-2 i / rot) / factors[i] (HOST
+ * arrays; factors NULL: 1; theta > 1, rot even and positive).  A position times such an entry,
+ * modulo 2^64, is the pair's angle as a fraction of a turn, exact to 2^-64 turns per position
+ * at any distance, without 64-bit floating point in the kernel.  An f_i above 2 pi is refused. */
+QG_API qg_status qg_rope_freqs(int rot, double theta, const float *factors, uint64_t *out);
+
+/* Rotate and append (qkNormRope, then kvStore): for each new token t of the batch, with q, k, v
+ * its f32 projection rows (head h of q at q + t*q_stride + h*D, and so on; strides in floats),
+ *   x <- x / sqrt(mean_D x^2 + eps) * w     per head of q and k, where q_norm / k_norm (f32[D]) are given
+ *   (x_a, x_b) <- (x_a c - x_b s, x_a s + x_b c)   c, s of angle position * f_i, for the pairs i < rot/2:
+ *     rope_pairs 0: a = i, b = i + rot/2;  rope_pairs 1: a = 2i, b = 2i + 1; the rest of a head unchanged
+ * then the rotated k and the v go to the token's row of the cache and the rotated q to
+ * q_out[t][h][D] (the cache's type), each rounded once from f32.  q may be NULL (with q_out NULL
+ * and Hq 0): append only.  freqs: device, rot/2 entries of qg_rope_freqs (may be NULL when rot
+ * is 0).  Hq a multiple of the cache's heads; 0 <= rot <= D, rot % 8 == 0; row strides multiples of 4
+ * floats that hold a row; f32 pointers and q_out 16-byte aligned, freqs 8-byte. */
+QG_API qg_status qg_kv_append(const qg_kv_cache *cache, const qg_kv_batch *batch, int Hq, const float *q,
+                              int64_t q_stride, const float *k, int64_t k_stride, const float *v, int64_t v_stride,
+                              const float *q_norm, const float *k_norm, float eps, const uint64_t *freqs, int rot,
+                              int rope_pairs, void *q_out, qg_stream_t stream);
+
+/* Causal attention over the cache: for new token t at position p and query head h,
+ *   out[t][h] = sum_j softmax_j(scale * q[t][h] . K[j][h / (Hq / n_heads)]) V[j][..],
+ * j over the positions 0 .. p of its group's prefix and its own tokens.  A group's prefix is read
+ * once for all its sequences.  A token that sees no key (p < 0) gets zeros.
+ *   - q: device, the cache's type, head h of token t at q + t*q_stride + h*D (q_stride in elements,
+ *     a multiple of 8, at least Hq*D), 16-byte aligned.
+ *   - out: device [n_tokens][Hq][D], 16-byte aligned, of out_dtype: QG_DT_F32 or the cache's type.
+ *     Scores and sums are f32.  The tensor cores take the softmax weights in the cache's type:
+ *     one rounding (2^-9 of a weight in bf16, 2^-12 in f16) for a 16-bit output, and for an f32
+ *     output two terms, which leave 2^-18 (bf16) or 2^-24 (f16).
+ *   - Rows past a sequence's length are never read: whatever they hold has no effect.
+ * Hq a multiple of n_heads, at most 16 query heads per cached head.  Workspace: qg_attn_workspace_size
+ * bytes, 16-byte aligned, contents irrelevant; one call at a time may use it. */
+QG_API size_t qg_attn_workspace_size(const qg_kv_cache *cache, const qg_kv_batch *batch, int Hq);
+QG_API qg_status qg_attn_paged(const qg_kv_cache *cache, const qg_kv_batch *batch, int Hq, const void *q,
+                               int64_t q_stride, float scale, void *out, int out_dtype, void *workspace,
+                               size_t workspace_bytes, qg_stream_t stream);
+
+/* ---- beam search -------------------------------------------------------------------------------
+ * One selection: for each of N requests with W beams, the K best of the W*V continuations
+ *   score[w] + log softmax(logits[w])[v]
+ * in falling order, equal ones by the lowest w*V + v.  logits: f32 [N*W][V]; scores: f32 [N*W], sums of
+ * log-probabilities so far (-inf: a beam that must not be continued).  An ended beam (done[w] != 0;
+ * done may be NULL) has one continuation, the token eos at its score unchanged.
+ *   - out_scores f32 [N][K], parents int32 [N][K] (w of the pick), tokens int32 [N][K], done_out
+ *     u8 [N][K] or NULL: the parent had ended or the token is eos (eos < 0: no end token).
+ *   - NaN logits and NaN or +inf scores count as -inf; a row whose largest logit is infinite has no
+ *     distribution, its continuations are -inf.  Sums over the vocabulary are f32 per slice
+ *     and joined in 64 bits; candidates are ranked in 64 bits.
+ * 1 <= W <= 64, 1 <= K <= 64, K <= W*V, V <= 2^20, 0 <= N, N*W <= 65535.  Outputs may be the arrays of the
+ * next call's inputs, not of this one's.  Workspace: beam_workspace_size bytes, 16-byte aligned. */
+QG_API size_t qg_beam_workspace_size(int N, int W, int K, int64_t V);
+QG_API qg_status qg_beam_select(const float *logits, const float *scores, const uint8_t *done, int eos, int N, int W,
+                                int K, int64_t V, float *out_scores, int32_t *parents, int32_t *tokens,
+                                uint8_t *done_out, void *workspace, size_t workspace_bytes, qg_stream_t stream);
+
+/* The matching reorder of the cached states: beam i of request n continues the tokens of beam
+ * parents[n][i] (int32 [N][W], several i may name one parent).  Per request, with len = kv_len (equal for its W
+ * sequences n*W .. n*W+W-1; otherwise QG_EDEVICE_ID and the request is left as it is):
+ *   - the first len / page_size columns of the W page lists are permuted: full pages are shared;
+ *   - the len % page_size rows begun in the next page are copied, in every layer, from the parent's
+ *     page to the beam's own page, all beams as if at once.
+ * Every beam must have its own page in the column being filled; full pages must not be written
+ * again.  caches: HOST array of n_layers (<= 128) caches with one geometry.  batch: n_seqs (= N*W), kv_len,
+ * pages, max_pages; the rest is ignored.  1 <= W <= 32.  A parent outside [0, W) sets QG_EDEVICE_ID and the
+ * beam keeps its own state. */
+QG_API qg_status qg_beam_reorder(const qg_kv_cache *caches, int n_layers, const qg_kv_batch *batch, int W,
+                                 const int32_t *parents, qg_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
