@@ -271,6 +271,7 @@ struct Pieces {
   const float2 *ml;
   size_t first;
   int count, rows, row;
+  int halves;  // 2: each slot holds two partial results of the row, kWideHalf rows apart
 };
 
 QG_DEVICE Pieces pieces_of(const AttnArgs &a, int s, int t, int h, int gq) {
@@ -293,7 +294,16 @@ QG_DEVICE Pieces pieces_of(const AttnArgs &a, int s, int t, int h, int gq) {
   p.first = static_cast<size_t>(l.seg_unit[s] + h * rt + r) + static_cast<size_t>(w0);
   p.count = w1 - w0 + 1;
   p.rows = l.rows;
-  p.row = (t - g.t0 - r * l.tpt) * a.Gq + gq;
+  const int i = t - g.t0 - r * l.tpt;
+  p.halves = 1;
+  if (nar) {
+    p.row = i * a.Gq + gq;
+  } else {
+    const int half = l.tpt / 2;
+    p.row = (i / half) * kWideHalf + (i % half) * a.Gq + gq;
+    // one half's rows alone: the kernel's two streams took the key tiles in turn
+    if (g.nt - r * l.tpt <= half) p.halves = 2;
+  }
   return p;
 }
 
@@ -304,17 +314,21 @@ struct Acc {
 };
 template <int NV>
 QG_DEVICE void acc_add(Acc<NV> &x, float m, float l, const float (&o)[NV]) {
+  if (m == -INFINITY) return;  // nothing seen (and o not written)
   const float mn = fmaxf(x.m, m);
-  if (mn == -INFINITY) return;
   const float fa = ex2(x.m - mn), fb = ex2(m - mn);
   x.m = mn;
   x.l = x.l * fa + l * fb;
 #pragma unroll
   for (int i = 0; i < NV; ++i) x.o[i] = x.o[i] * fa + o[i] * fb;
 }
+QG_DEVICE size_t piece_row(const Pieces &p, int i) {
+  const int slot = p.halves == 2 ? i >> 1 : i, half = p.halves == 2 ? i & 1 : 0;
+  return (p.first + slot) * p.rows + p.row + half * kWideHalf;
+}
 template <int D>
 QG_DEVICE void load_o(const Pieces &p, int i, int lane, float (&v)[D / 32]) {
-  const float *src = p.o + ((p.first + i) * p.rows + p.row) * D + lane * (D / 32);
+  const float *src = p.o + piece_row(p, i) * D + lane * (D / 32);
   if constexpr (D == 64) {
     const float2 u = __ldcg(reinterpret_cast<const float2 *>(src));
     v[0] = u.x;
@@ -333,20 +347,21 @@ QG_DEVICE void load_o(const Pieces &p, int i, int lane, float (&v)[D / 32]) {
 template <int D>
 QG_DEVICE void acc_pieces(Acc<D / 32> &x, const Pieces &p, int i0, int step, int lane) {
   constexpr int U = 4;  // pieces in flight
-  for (int i = i0; i < p.count; i += U * step) {
+  const int count = p.count * p.halves;
+  for (int i = i0; i < count; i += U * step) {
     float v[U][D / 32];
     float2 ml[U];
 #pragma unroll
     for (int k = 0; k < U; ++k) {
       ml[k] = make_float2(-INFINITY, 0.f);
-      if (i + k * step < p.count) {
-        ml[k] = __ldcg(p.ml + (p.first + i + k * step) * p.rows + p.row);
+      if (i + k * step < count) {
+        ml[k] = __ldcg(p.ml + piece_row(p, i + k * step));
         load_o<D>(p, i + k * step, lane, v[k]);
       }
     }
 #pragma unroll
     for (int k = 0; k < U; ++k)
-      if (i + k * step < p.count) acc_add(x, ml[k].x, ml[k].y, v[k]);
+      if (i + k * step < count) acc_add(x, ml[k].x, ml[k].y, v[k]);
   }
 }
 
@@ -385,9 +400,10 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
   const int h = ROW ? hh / a.Gq : hh;
   Pieces own, pre;
   own.count = pre.count = 0;
+  own.halves = pre.halves = 1;
   if (b >= 0) own = pieces_of(a, a.b.G + b, t, h, ROW ? hh % a.Gq : 0);
   if (gr >= 0) pre = pieces_of(a, gr, t, h, ROW ? hh % a.Gq : 0);
-  if (own.count == 1 && pre.count == 0) return;  // its worker wrote the row
+  if (own.count == 1 && own.halves == 1 && pre.count == 0) return;  // its worker wrote the row
   if constexpr (ROW) {
     __shared__ float so[8][D];
     __shared__ float2 sml[8];
@@ -440,7 +456,7 @@ struct Plan {
 // rows bound: a unit per (cached head, row tile); tiles of a segment: tokens / tpt + 1
 Plan make_plan(const KvPool &pool, const KvBatch &b, int Gq, int sms) {
   Plan p = {};
-  const int tn = kNarrowRows / Gq, tw = kWideRows / Gq;
+  const int tn = kNarrowRows / Gq, tw = 2 * (kWideHalf / Gq);
   const long long nseg = static_cast<long long>(b.G) + b.B;
   const bool wide = attn_wide_supported(pool.D) && b.T > tn;
   p.narrow_workers = sms * (pool.D == 256 ? 4 : 8);
@@ -566,7 +582,7 @@ qg_status qg_attn_paged(const qg_kv_cache *cache, const qg_kv_batch *batch, int 
     Line l = {};
     l.rows = rows;
     l.keys = keys;
-    l.tpt = rows / a.Gq;
+    l.tpt = rows == kNarrowRows ? rows / a.Gq : 2 * (kWideHalf / a.Gq);
     l.workers = workers;
     l.seg_pos = reinterpret_cast<long long *>(ws + pos);
     l.seg_unit = reinterpret_cast<int *>(ws + unit);

@@ -12,7 +12,7 @@
 // to piece, so u + w numbers the pieces' slots in the workspace without gaps mattering.
 //
 // Two kernels with a line each share a call: segments with few rows (at most one row tile of 16)
-// and segments with more (row tiles of 128).  The joining kernel reads both lines.
+// and segments with more (row tiles of two times 128).  The joining kernel reads both lines.
 #pragma once
 
 #include "qg_kv.cuh"
@@ -20,12 +20,12 @@
 namespace qg {
 
 constexpr int kNarrowRows = 16, kNarrowKeys = 16;
-constexpr int kWideRows = 128, kWideKeys = 128;
+constexpr int kWideHalf = 128, kWideRows = 2 * kWideHalf, kWideKeys = 128;
 
 // A line of tiles: row and key tile sizes, and which segments belong to it.
 struct Line {
   int rows, keys;        // rows and keys per tile
-  int tpt;               // tokens per row tile: rows / Gq
+  int tpt;               // tokens per row tile: rows / Gq (wide: two halves of 128 / Gq)
   int lo, hi;            // segments with lo < tokens <= hi belong to it
   int workers;
   float *part_o;         // [slot][rows][D]
