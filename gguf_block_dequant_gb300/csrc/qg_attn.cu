@@ -57,26 +57,25 @@ __global__ void __launch_bounds__(NarrowCfg<D>::NW * 32, 1) attn_narrow_kernel(c
   const int nw = line_workers(ln, total);
   const int w = warp * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
   if (w >= nw) return;
-  long long at = line_start(w, total, nw);
+  const long long at = line_start(w, total, nw);
   const long long end = line_start(w + 1, total, nw);
   if (at >= end) return;
-  Place pl;
-  if (!place_find(a, ln, scan, at, &pl)) return;
+  Cursor cur;
+  if (!cursor_find(a, ln, scan, at, &cur)) return;
 
   const uint32_t ring = smem_u32(smem) + static_cast<uint32_t>(warp) * (C::NST * 2 * C::TILE);
   const int shift = a.pool.page_shift;
   const int qr = lane >> 2, qc = lane & 3;      // fragment row and column pair
   const int crow = lane / CH, cchunk = lane % CH;  // copy: row within an instruction, chunk
 
-  while (at < end) {
-    while (at >= pl.pos + a.pool.Hkv * pl.cost)
-      if (!place_next(a, ln, &pl)) return;
-    const UnitAt u = unit_at(ln, pl, at - pl.pos);
-    const int j0 = u.j, j1 = static_cast<int>(min(static_cast<long long>(u.n), u.j + (end - at)));
-    const Seg g = pl.g;
+  for (bool more = true; more && cur.pos < end; more = cursor_next(a, ln, &cur)) {
+    int j0, j1, n_tiles;
+    cursor_tiles(ln, cur, at, end, &j0, &j1, &n_tiles);
+    if (j0 >= j1) continue;
+    const Seg g = cur.g;
 
     // ---- this lane's two rows: query fragments and key limits
-    const int tile_t0 = u.r * ln.tpt;
+    const int tile_t0 = cur.r * ln.tpt;
     const int tokens = min(ln.tpt, g.nt - tile_t0);
     const int nrows = tokens * a.Gq;
     int lim[2];
@@ -89,7 +88,7 @@ __global__ void __launch_bounds__(NarrowCfg<D>::NW * 32, 1) attn_narrow_kernel(c
       if (row < nrows) {
         const int t = g.t0 + tile_t0 + row / a.Gq;
         lim[e] = row_limit(a, g, t);
-        qp = a.q + t * a.q_stride + static_cast<long long>(u.h * a.Gq + row % a.Gq) * D + 2 * qc;
+        qp = a.q + t * a.q_stride + static_cast<long long>(cur.h * a.Gq + row % a.Gq) * D + 2 * qc;
       }
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
@@ -102,7 +101,7 @@ __global__ void __launch_bounds__(NarrowCfg<D>::NW * 32, 1) attn_narrow_kernel(c
     all = __reduce_min_sync(0xFFFFFFFFu, all);
 
     // lane r < 16: element offset of key row 16 j + r, -1 past the end
-    const long long hoff = u.h * a.pool.head_stride;
+    const long long hoff = cur.h * a.pool.head_stride;
     auto row_off = [&](int j) -> long long {
       const int key = 16 * j + (lane & 15);
       if (key >= g.len || j >= j1) return -1;
@@ -227,11 +226,8 @@ __global__ void __launch_bounds__(NarrowCfg<D>::NW * 32, 1) attn_narrow_kernel(c
     __syncwarp();  // every lane has read the last tiles: the next piece's copies may replace them
 
     // ---- write the piece
-    const bool alone = !g.prefix && j0 == 0 && j1 == u.n && [&] {
-      const int gr = kv_group_of(a.b, pl.s - a.b.G);
-      return gr < 0 || kv_clamp(__ldg(a.b.prefix_len + gr), 0, kv_cap(a.b.max_prefix_pages, shift)) == 0;
-    }();
-    const size_t slot = static_cast<size_t>(pl.unit + u.h * pl.rt + u.r) + static_cast<size_t>(w);
+    const bool alone = !g.prefix && j0 == 0 && j1 == n_tiles && !has_prefix(a, cur.s - a.b.G);
+    const size_t slot = static_cast<size_t>(cur.unit) + static_cast<size_t>(w);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       float ls = l[e];
@@ -242,7 +238,7 @@ __global__ void __launch_bounds__(NarrowCfg<D>::NW * 32, 1) attn_narrow_kernel(c
       if (alone) {
         const float inv = ls > 0.f ? 1.0f / ls : 0.f;
         const int t = g.t0 + tile_t0 + row / a.Gq;
-        const size_t base = (static_cast<size_t>(t) * a.Hq + u.h * a.Gq + row % a.Gq) * D + 2 * qc;
+        const size_t base = (static_cast<size_t>(t) * a.Hq + cur.h * a.Gq + row % a.Gq) * D + 2 * qc;
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
           if constexpr (OUT32)
@@ -260,7 +256,6 @@ __global__ void __launch_bounds__(NarrowCfg<D>::NW * 32, 1) attn_narrow_kernel(c
         if (qc == 0) ln.part_ml[slot * kNarrowRows + row] = make_float2(m[e], ls);
       }
     }
-    at += j1 - j0;
   }
 }
 
@@ -282,13 +277,16 @@ QG_DEVICE Pieces pieces_of(const AttnArgs &a, int s, int t, int h, int gq) {
   if (!nar && !(a.wide.workers && seg_in(a.wide, g))) return p;
   const Line &l = nar ? a.narrow : a.wide;
   const int r = (t - g.t0) / l.tpt;
-  const int n = unit_cost(l, g, r);
-  if (n == 0) return p;
+  const int x = unit_keys(g, l.tpt, r);
+  if (x == 0) return p;
   const long long total = l.seg_pos[a.b.G + a.b.B];
   const int nw = line_workers(l, total);
   const int rt = seg_tiles(l, g);
   const long long p0 = l.seg_pos[s] + h * seg_cost_to(l, g, rt) + seg_cost_to(l, g, r);
-  const int w0 = line_owner(p0, total, nw), w1 = line_owner(p0 + n - 1, total, nw);
+  const int w0 = line_owner(p0, total, nw);
+  int w1 = line_owner(p0 + x - 1, total, nw);
+  // the last one's part may lie within the last key tile, which is then its neighbour's
+  if (w1 > w0 && (line_start(w1, total, nw) - p0 + l.keys - 1) / l.keys >= (x + l.keys - 1) / l.keys) --w1;
   p.o = l.part_o;
   p.ml = l.part_ml;
   p.first = static_cast<size_t>(l.seg_unit[s] + h * rt + r) + static_cast<size_t>(w0);

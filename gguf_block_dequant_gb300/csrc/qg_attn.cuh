@@ -4,12 +4,14 @@
 // all tokens of the group's sequences, or a sequence's own keys with its own tokens.  The rows
 // of a segment and a cached head are its (token, query head of that cached head) pairs; they
 // are cut into ROW TILES of `tpt` whole tokens.  A UNIT is (segment, cached head, row tile),
-// and its cost is the number of key tiles its last row sees.  All units in (segment, head, row
-// tile) order, tile by tile, form one line of tiles; worker w of n takes the part
-// [w*total/n, (w+1)*total/n) of it.  So ragged lengths balance without the host knowing
-// them, and every kernel can work out from the lengths alone who did what.  A worker's part of
-// one unit is a PIECE; unit u and worker w rise along the line and one of them rises from piece
-// to piece, so u + w numbers the pieces' slots in the workspace without gaps mattering.
+// and its cost is the number of keys its last row sees.  All units in (segment, head, row
+// tile) order, key by key, form one LINE; worker w of n takes the part
+// [w*total/n, (w+1)*total/n) of it, its ends raised to whole key tiles of their units.  So ragged
+// lengths balance without the host knowing them, and every kernel can work out from the lengths
+// alone who did what: costs in keys rather than tiles make a segment's cost an arithmetic series
+// (the sum of rounded-up tile counts took tens of thousands of cycles to invert).  A worker's
+// part of one unit is a PIECE; unit u and worker w rise along the line and one of them rises
+// from piece to piece, so u + w numbers the pieces' slots in the workspace without gaps mattering.
 //
 // Two kernels with a line each share a call: segments with few rows (at most one row tile of 16)
 // and segments with more (row tiles of two times 128).  The joining kernel reads both lines.
@@ -22,7 +24,7 @@ namespace qg {
 constexpr int kNarrowRows = 16, kNarrowKeys = 16;
 constexpr int kWideHalf = 128, kWideRows = 2 * kWideHalf, kWideKeys = 128;
 
-// A line of tiles: row and key tile sizes, and which segments belong to it.
+// A line: row and key tile sizes, and which segments belong to it.
 struct Line {
   int rows, keys;        // rows and keys per tile
   int tpt;               // tokens per row tile: rows / Gq (wide: two halves of 128 / Gq)
@@ -30,7 +32,7 @@ struct Line {
   int workers;
   float *part_o;         // [slot][rows][D]
   float2 *part_ml;       // [slot][rows]: running maximum (log2 units) and sum
-  long long *seg_pos;    // [segments + 1] first tile of each segment
+  long long *seg_pos;    // [segments + 1] place of each segment's first key on the line
   int *seg_unit;         // [segments + 1] first unit of each segment
 };
 
@@ -77,52 +79,26 @@ QG_DEVICE Seg seg_load(const AttnArgs &a, int s) {
 QG_DEVICE bool seg_in(const Line &l, const Seg &g) { return g.nt > l.lo && g.nt <= l.hi && g.len > 0; }
 QG_DEVICE int seg_tiles(const Line &l, const Seg &g) { return (g.nt + l.tpt - 1) / l.tpt; }  // row tiles
 
-// key tiles of row tile r: up to the last key its last token sees
-QG_DEVICE int unit_cost(const Line &l, const Seg &g, int r) {
-  int seen = g.len;
-  if (!g.prefix) seen = kv_clamp(g.len - g.nt + min(g.nt, (r + 1) * l.tpt), 0, g.len);
-  return (seen + l.keys - 1) / l.keys;
+// keys of row tile r: up to the last key its last token sees
+QG_DEVICE int unit_keys(const Seg &g, int tpt, int r) {
+  return g.prefix ? g.len : kv_clamp(g.len - g.nt + min(g.nt, (r + 1) * tpt), 0, g.len);
 }
-// sum of floor((a i + b) / m) over i < n, by the Euclidean recursion (a, b, n >= 0, m > 0)
-QG_DEVICE long long floor_sum(long long n, int m, int a, int b) {
-  long long r = 0;
-  while (n > 0) {
-    if (a >= m) {
-      r += n * (n - 1) / 2 * (a / m);
-      a %= m;
-    }
-    if (b >= m) {
-      r += n * (b / m);
-      b %= m;
-    }
-    const long long y = a * n + b;
-    if (y < m) break;
-    n = y / m;
-    b = static_cast<int>(y % m);
-    const int t = m;
-    m = a;
-    a = t;
-  }
-  return r;
-}
-
-// key tiles of row tiles 0 .. r-1
+// keys of row tiles 0 .. r-1
 QG_DEVICE long long seg_cost_to(const Line &l, const Seg &g, int r) {
-  const int rt = seg_tiles(l, g);
-  if (g.prefix || rt == 1) return static_cast<long long>(r) * unit_cost(l, g, 0);
+  if (g.prefix) return static_cast<long long>(r) * g.len;
   // own keys: tile i < rt - 1 sees base + (i + 1) tpt of them (none while that is not positive)
-  const int base = g.len - g.nt;
-  const int m = min(r, rt - 1);
+  const int rt = seg_tiles(l, g), base = g.len - g.nt, m = min(r, rt - 1);
   const int i0 = base < 0 ? min(m, -base / l.tpt) : 0;  // tiles that see nothing
-  long long c = floor_sum(m - i0, l.keys, l.tpt, base + (i0 + 1) * l.tpt + l.keys - 1);
-  if (r == rt) c += unit_cost(l, g, rt - 1);
+  const long long n = m - i0;
+  long long c = n * (base + (i0 + 1) * l.tpt) + n * (n - 1) / 2 * l.tpt;
+  if (r == rt) c += g.len;
   return c;
 }
 
-// workers that take part: at least `kMinTiles` tiles each
+// workers that take part: at least `kMinTiles` tiles each, and never less than one
 constexpr int kMinTiles = 2;
 QG_DEVICE int line_workers(const Line &l, long long total) {
-  const long long n = (total + kMinTiles - 1) / kMinTiles;
+  const long long n = (total + kMinTiles * l.keys - 1) / (kMinTiles * l.keys);
   return n < l.workers ? static_cast<int>(n) : l.workers;
 }
 QG_DEVICE long long line_start(long long w, long long total, int n) { return w * total / n; }
@@ -142,7 +118,7 @@ QG_DEVICE int row_limit(const AttnArgs &a, const Seg &g, int t) {
 
 // ---- the block's view of a line ---------------------------------------------------------------
 // Thread i of the block owns segments [i*chunk, (i+1)*chunk); pos[i], unit[i] are the line's
-// tiles and units before them.  Filled by all threads of the block.
+// keys and units before them.  Filled by all threads of the block.
 template <int NT>
 struct LineScan {
   long long pos[NT + 1];
@@ -216,37 +192,43 @@ QG_DEVICE long long line_scan(const AttnArgs &a, const Line &l, LineScan<NT> *sc
   return sc->pos[NT];
 }
 
-// A place on the line: segment s (g), its first tile and unit, head, row tile and key tile.
-struct Place {
+// A unit on the line and the segment it is of.
+struct Cursor {
   int s;
   Seg g;
-  long long pos;   // first tile of the segment
-  int unit;        // first unit of the segment
-  long long cost;  // tiles of one head of the segment
-  int rt;          // row tiles
+  long long pos;   // place of the unit's first key
+  int unit;        // the unit's number
+  int rt;          // row tiles of the segment
+  int h, r, x;     // head, row tile, keys
 };
 
-// moves to the next segment of the line at or after s
-QG_DEVICE bool place_at(const AttnArgs &a, const Line &l, Place *p, int s) {
+// to the first unit of a segment at or after s (pos and unit are those of s)
+QG_DEVICE bool cursor_seg(const AttnArgs &a, const Line &l, Cursor *c, int s) {
   const int nseg = a.b.G + a.b.B;
   for (; s < nseg; ++s) {
-    p->g = seg_load(a, s);
-    if (!seg_in(l, p->g)) continue;
-    p->s = s;
-    p->rt = seg_tiles(l, p->g);
-    p->cost = seg_cost_to(l, p->g, p->rt);
-    if (p->cost > 0) return true;
-    p->unit += a.pool.Hkv * p->rt;
+    c->g = seg_load(a, s);
+    if (!seg_in(l, c->g)) continue;
+    c->s = s;
+    c->rt = seg_tiles(l, c->g);
+    c->h = c->r = 0;
+    c->x = unit_keys(c->g, l.tpt, 0);
+    return true;
   }
   return false;
 }
-QG_DEVICE bool place_next(const AttnArgs &a, const Line &l, Place *p) {
-  p->pos += a.pool.Hkv * p->cost;
-  p->unit += a.pool.Hkv * p->rt;
-  return place_at(a, l, p, p->s + 1);
+QG_DEVICE bool cursor_next(const AttnArgs &a, const Line &l, Cursor *c) {
+  c->pos += c->x;
+  ++c->unit;
+  if (++c->r == c->rt) {
+    c->r = 0;
+    if (++c->h == a.pool.Hkv) return cursor_seg(a, l, c, c->s + 1);
+  }
+  c->x = unit_keys(c->g, l.tpt, c->r);
+  return true;
 }
+// to the unit that holds place `at`
 template <int NT>
-QG_DEVICE bool place_find(const AttnArgs &a, const Line &l, const LineScan<NT> &sc, long long at, Place *p) {
+QG_DEVICE bool cursor_find(const AttnArgs &a, const Line &l, const LineScan<NT> &sc, long long at, Cursor *c) {
   int lo = 0, hi = NT;  // the last thread whose segments start at or before `at`
   while (hi - lo > 1) {
     const int m = (lo + hi) / 2;
@@ -254,39 +236,44 @@ QG_DEVICE bool place_find(const AttnArgs &a, const Line &l, const LineScan<NT> &
     else hi = m;
   }
   const int chunk = (a.b.G + a.b.B + NT - 1) / NT;
-  p->pos = sc.pos[lo];
-  p->unit = sc.unit[lo];
-  if (!place_at(a, l, p, lo * chunk)) return false;
-  while (p->pos + a.pool.Hkv * p->cost <= at)
-    if (!place_next(a, l, p)) return false;
-  return true;
-}
-
-// unit of the segment that holds its tile `local`: head, row tile, key tile, tiles of the unit
-struct UnitAt {
-  int h, r, j, n;
-};
-QG_DEVICE UnitAt unit_at(const Line &l, const Place &p, long long local) {
-  UnitAt u;
-  u.h = static_cast<int>(local / p.cost);
-  const long long rem = local - u.h * p.cost;
-  if (p.rt == 1 || p.g.prefix) {
-    u.n = unit_cost(l, p.g, 0);
-    u.r = static_cast<int>(rem / u.n);
-    u.j = static_cast<int>(rem - static_cast<long long>(u.r) * u.n);
-    return u;
+  c->pos = sc.pos[lo];
+  c->unit = sc.unit[lo];
+  if (!cursor_seg(a, l, c, lo * chunk)) return false;
+  long long cost;
+  while (true) {  // the segment
+    cost = seg_cost_to(l, c->g, c->rt);
+    if (c->pos + a.pool.Hkv * cost > at) break;
+    c->pos += a.pool.Hkv * cost;
+    c->unit += a.pool.Hkv * c->rt;
+    if (!cursor_seg(a, l, c, c->s + 1)) return false;
   }
-  int lo = 0, hi = p.rt;  // the last row tile that starts at or before rem
+  c->h = static_cast<int>((at - c->pos) / cost);
+  c->pos += c->h * cost;
+  lo = 0, hi = c->rt;  // the last row tile that starts at or before `at`
   while (hi - lo > 1) {
     const int m = (lo + hi) / 2;
-    if (seg_cost_to(l, p.g, m) <= rem) lo = m;
+    if (c->pos + seg_cost_to(l, c->g, m) <= at) lo = m;
     else hi = m;
   }
-  u.r = lo;
-  u.n = unit_cost(l, p.g, lo);
-  const long long c = seg_cost_to(l, p.g, lo);
-  u.j = static_cast<int>(rem - c);
-  return u;
+  c->r = lo;
+  c->pos += seg_cost_to(l, c->g, lo);
+  c->unit += c->h * c->rt + lo;
+  c->x = unit_keys(c->g, l.tpt, lo);
+  return true;
+}
+// the key tiles [j0, j1) of the cursor's unit in the part [at, end) of the line (none: j0 == j1);
+// n: tiles of the unit
+QG_DEVICE void cursor_tiles(const Line &l, const Cursor &c, long long at, long long end, int *j0, int *j1, int *n) {
+  const long long o0 = at > c.pos ? at - c.pos : 0, o1 = end - c.pos < c.x ? end - c.pos : c.x;
+  *j0 = static_cast<int>((o0 + l.keys - 1) / l.keys);
+  *j1 = static_cast<int>((o1 + l.keys - 1) / l.keys);
+  *n = (c.x + l.keys - 1) / l.keys;
+}
+
+// whether a sequence's rows have a prefix besides its own keys
+QG_DEVICE bool has_prefix(const AttnArgs &a, int seq) {
+  const int g = kv_group_of(a.b, seq);
+  return g >= 0 && kv_clamp(__ldg(a.b.prefix_len + g), 0, kv_cap(a.b.max_prefix_pages, a.pool.page_shift)) > 0;
 }
 
 // attention over many rows per segment on the tcgen05 tensor cores (qg_attn_tc.cu)

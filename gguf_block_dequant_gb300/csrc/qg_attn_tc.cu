@@ -61,36 +61,50 @@ struct Piece {
   size_t slot;
 };
 struct Walk {
-  Place pl;
+  Cursor cur;
   long long at, end;
   int w;
 };
 QG_DEVICE bool walk_next(const AttnArgs &a, Walk *k, Piece *p) {
   const Line &l = a.wide;
-  if (k->at >= k->end) return false;
-  while (k->at >= k->pl.pos + a.pool.Hkv * k->pl.cost)
-    if (!place_next(a, l, &k->pl)) return false;
-  const UnitAt u = unit_at(l, k->pl, k->at - k->pl.pos);
-  p->g = k->pl.g;
-  p->h = u.h;
-  p->t0 = p->g.t0 + u.r * l.tpt;
-  p->tokens = min(l.tpt, p->g.nt - u.r * l.tpt);
-  p->j0 = u.j;
-  p->j1 = static_cast<int>(min(static_cast<long long>(u.n), u.j + (k->end - k->at)));
-  p->paired = p->tokens > l.tpt / 2;
-  p->alone = false;
-  if (p->paired && !p->g.prefix && p->j0 == 0 && p->j1 == u.n) {
-    const int gr = kv_group_of(a.b, k->pl.s - a.b.G);
-    p->alone = gr < 0 || kv_clamp(__ldg(a.b.prefix_len + gr), 0, kv_cap(a.b.max_prefix_pages, a.pool.page_shift)) == 0;
+  Cursor &c = k->cur;
+  while (c.pos < k->end) {
+    int n;
+    cursor_tiles(l, c, k->at, k->end, &p->j0, &p->j1, &n);
+    const bool some = p->j0 < p->j1;
+    if (some) {
+      p->g = c.g;
+      p->h = c.h;
+      p->t0 = c.g.t0 + c.r * l.tpt;
+      p->tokens = min(l.tpt, c.g.nt - c.r * l.tpt);
+      p->paired = p->tokens > l.tpt / 2;
+      p->alone = p->paired && !c.g.prefix && p->j0 == 0 && p->j1 == n && !has_prefix(a, c.s - a.b.G);
+      p->slot = static_cast<size_t>(c.unit) + static_cast<size_t>(k->w);
+    }
+    if (!cursor_next(a, l, &c)) c.pos = k->end;
+    if (some) return true;
   }
-  p->slot = static_cast<size_t>(k->pl.unit + u.h * k->pl.rt + u.r) + static_cast<size_t>(k->w);
-  k->at += p->j1 - p->j0;
-  return true;
+  return false;
 }
 
+// Bounded wait by the SM's own clock: gives up when another role has, or after about a quarter
+// of a second.
+constexpr long long kWaitCycles = 1LL << 29;
+QG_DEVICE bool clock_wait(uint64_t *b, uint32_t parity, volatile int *abort) {
+  if (mbar_try_wait(b, parity)) return true;
+  const long long t0 = clock64();
+  while (true) {
+    if (mbar_try_wait(b, parity)) return true;
+    if (*abort) return false;
+    if (clock64() - t0 > kWaitCycles) break;
+  }
+  *abort = 1;
+  atomicOr(&g_qg_status_attn_tc, QG_STATUS_BIT_TIMEOUT);
+  return false;
+}
 // the whole warp waits, and gives up as a whole
 QG_DEVICE bool warp_wait(uint64_t *b, uint32_t parity, volatile int *abort) {
-  return __all_sync(0xFFFFFFFFu, wait_or_abort(b, parity, abort, &g_qg_status_attn_tc));
+  return __all_sync(0xFFFFFFFFu, clock_wait(b, parity, abort));
 }
 
 // ---- producer ---------------------------------------------------------------------------------
@@ -202,7 +216,7 @@ QG_DEVICE void issue_mma(const AttnArgs &a, Walk walk, uint32_t smem, WideBars *
   volatile int *abort = &bar->abort;
   const uint32_t tmem = bar->tmem;
   auto wait = [&](uint64_t *b, uint32_t parity) {
-    const bool r = wait_or_abort(b, parity, abort, &g_qg_status_attn_tc);
+    const bool r = clock_wait(b, parity, abort);
     tc_fence_after();
     return r;
   };
@@ -463,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const __grid_con
   if (total == 0 || walk.w >= nw) return;
   walk.at = line_start(walk.w, total, nw);
   walk.end = line_start(walk.w + 1, total, nw);
-  if (walk.at >= walk.end || !place_find(a, ln, *scan, walk.at, &walk.pl)) return;  // the same for the whole block
+  if (walk.at >= walk.end || !cursor_find(a, ln, *scan, walk.at, &walk.cur)) return;  // the same for the whole block
   if (warp == kMmaWarp) tmem_alloc(&bar->tmem, C::COLS);
   tc_fence_before();
   __syncthreads();
