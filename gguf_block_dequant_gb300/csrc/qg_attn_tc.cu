@@ -7,8 +7,11 @@
 //   warps 0-3, 4-7  two softmax streams, a thread per row: scores from tensor memory, running
 //                   maximum and sum, weights back in 16 bits, at the end the piece's output;
 //   warp 8          TMEM allocation and the single MMA-issuing thread;
-//   warps 9-11      producers: gather K and V rows through the page list (16-byte cp.async, the
-//                   pages may be of any size and stride) into 128-byte-swizzled tiles.
+//   warp 9          the TMA producer: query tiles, and key and value tiles gathered page by page
+//                   (a box is 64 elements of the rows a page has in the tile) into
+//                   128-byte-swizzled shared memory;
+//   warps 10, 11    idle: they complete the warpgroup whose registers the softmax warps take over
+//                   (a thread holds its row's 128 scores).
 // Two streams keep the tensor cores busy during the exponentials.  With more than 128 rows the
 // streams take 128 rows each and share every key tile; with fewer they take the key tiles in
 // turn, each with its own maximum, sum and output, joined later like any two pieces.
@@ -16,8 +19,13 @@
 // The running maximum a row's weights refer to is raised (and its output rescaled) only when the
 // row's maximum has grown by more than 2^8: weights stay below 2^8, exact in their ratios, and
 // the output in tensor memory is hardly ever touched between the products.
+#include <cuda.h>
+
+#include <mutex>
+
 #include "qg_attn.cuh"
 #include "qg_mma.cuh"
+#include "qg_pipe.cuh"
 #include "qg_tc.cuh"
 
 __device__ unsigned int g_qg_status_attn_tc;  // this translation unit's device status word
@@ -26,15 +34,17 @@ namespace {
 
 using namespace qg;
 
-constexpr int kSoftWarps = 8, kMmaWarp = 8, kProdWarps = 3;  // 12 warps: 168 registers a thread
-constexpr int kThreads = (kSoftWarps + 1 + kProdWarps) * 32;
-constexpr int kLag = 2;  // copies a producer keeps in flight behind the newest
+constexpr int kSoftWarps = 8, kMmaWarp = 8, kProdWarp = 9;
+constexpr int kThreads = 12 * 32;
+// registers: launched with 168 a thread; two warpgroups go up to 208, the third down to 88
+constexpr int kRegs = 168, kRegsSoft = 208, kRegsRest = 88;
+static_assert(2 * kRegsSoft + kRegsRest <= 3 * kRegs, "the warpgroups' shares come from the launch's total");
 
 template <int D>
 struct WideCfg {
   static constexpr uint32_t HALF = 128 * 128;             // bytes of 128 rows x 64 elements
   static constexpr uint32_t TILE = HALF * (D / 64);       // a key, value or query tile
-  static constexpr int NST = D == 64 ? 8 : 4;
+  static constexpr int NST = D == 64 ? 8 : 5;
   static constexpr uint32_t OFF_Q = 0;
   static constexpr uint32_t OFF_KV = 2 * TILE;
   static constexpr uint32_t OFF_BAR = OFF_KV + NST * TILE;
@@ -44,7 +54,7 @@ struct WideCfg {
 
 struct WideBars {
   uint64_t full[8], empty[8];
-  uint64_t q_full, q_empty;
+  uint64_t q_full, q_empty, tail;
   uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];
   uint32_t tmem;
   int abort;
@@ -108,104 +118,98 @@ QG_DEVICE bool warp_wait(uint64_t *b, uint32_t parity, volatile int *abort) {
 }
 
 // ---- producer ---------------------------------------------------------------------------------
-// 16-byte chunk c of row r of a tile: half c / 8, 128-byte rows, chunks swizzled by r & 7
-QG_DEVICE uint32_t tile_off(int r, int c) {
-  return static_cast<uint32_t>(c >> 3) * (128u * 128u) + static_cast<uint32_t>(r) * 128u +
-         static_cast<uint32_t>(((c & 7) ^ (r & 7)) * 16);
+QG_DEVICE void tma_4d(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, int c3, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];" ::"r"(dst),
+      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
+      : "memory");
+}
+QG_DEVICE void tma_3d(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+      "[%5];" ::"r"(dst),
+      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
+      : "memory");
 }
 
+// Tensor maps of a call: queries (D, Hq, tokens), keys and values (D, page rows, heads, pages).  A page
+// number outside the pool is a coordinate outside the map and reads zeros.
+struct WideMaps {
+  CUtensorMap q, k, v;
+};
+
 template <int D>
-QG_DEVICE void produce(const AttnArgs &a, Walk walk, uint32_t smem, WideBars *bar, int tid) {
+QG_DEVICE void produce(const AttnArgs &a, const WideMaps &maps, Walk walk, uint8_t *smem, WideBars *bar, int lane) {
   using C = WideCfg<D>;
-  constexpr int CH = D / 8;            // chunks per row
-  constexpr int RPT = kProdWarps * 32 / CH;     // rows the producers cover at once
-  constexpr int NR = (128 + RPT - 1) / RPT;     // and the times they do
-  const int c = tid % CH, r0 = tid / CH;
+  constexpr int H = D / 64;              // 64-element halves of a row
   volatile int *abort = &bar->abort;
-  // copies are reported to their barriers kLag commits later: until then they may be in flight
-  uint64_t *pend[kLag] = {};
-  auto report = [&](uint64_t *b) {
-    fence_proxy_async_smem();  // copied through the generic proxy, read by the tensor cores
-    __syncwarp();
-    if (b && (threadIdx.x & 31) == 0) mbar_arrive(b);
-  };
-  auto push = [&](uint64_t *b) {
-    cp_async_commit();
-    cp_async_wait<kLag>();
-    report(pend[0]);
-#pragma unroll
-    for (int i = 0; i + 1 < kLag; ++i) pend[i] = pend[i + 1];
-    pend[kLag - 1] = b;
-  };
-  auto flush = [&] {
-    cp_async_wait<0>();
-#pragma unroll
-    for (int i = 0; i < kLag; ++i) {
-      report(pend[i]);
-      pend[i] = nullptr;
-    }
-  };
-  // a wait that may last: what others need to end it may be among the copies not yet reported
-  auto acquire = [&](uint64_t *b, uint32_t parity) {
-    if (__all_sync(0xFFFFFFFFu, mbar_try_wait(b, parity))) return true;
-    flush();
-    return warp_wait(b, parity, abort);
-  };
-  const int shift = a.pool.page_shift, mask = (1 << shift) - 1;
+  const uint32_t sb = smem_u32(smem);
+  const int shift = a.pool.page_shift;
+  const int bshift = min(shift, 7), rows = 1 << bshift;  // rows of a box
+  const int half = a.wide.tpt / 2;
   long long it = 0;
-  int np = 0;
-  bool ok = true;
+  int np = 0, ntail = 0;
   Piece p;
-  for (; ok && walk_next(a, &walk, &p); ++np) {
-    if (!acquire(&bar->q_empty, static_cast<uint32_t>((np & 1) ^ 1))) break;
-    const int half = a.wide.tpt / 2;
-    for (int s = 0; s < (p.paired ? 2 : 1); ++s) {
-      const int tok = min(half, p.tokens - s * half), rows = tok * a.Gq;
-#pragma unroll 4
-      for (int r = r0; r < 128; r += RPT) {
-        const bool in = r < rows;
-        const int t = p.t0 + s * half + (in ? r / a.Gq : 0);
-        const uint16_t *src = a.q + t * a.q_stride + static_cast<long long>(p.h * a.Gq + (in ? r % a.Gq : 0)) * D + 8 * c;
-        cp_async16_zfill(smem + C::OFF_Q + s * C::TILE + tile_off(r, c), src, in ? 16u : 0u);
-      }
-    }
-    push(&bar->q_full);
-    const long long hoff = p.h * a.pool.head_stride + 8 * c;
-    for (int j = p.j0; j < p.j1 && ok; ++j) {
-      // this thread's rows of the key tile: r0, r0 + RPT, ...
-      long long off[NR];
+  for (; walk_next(a, &walk, &p); ++np) {
+    if (!warp_wait(&bar->q_empty, static_cast<uint32_t>((np & 1) ^ 1), abort)) return;
+    const int ns = p.paired ? 2 : 1;
+    if (lane == 0) mbar_arrive_expect_tx(&bar->q_full, static_cast<uint32_t>(ns * H * half * a.Gq) * 128u);
+    __syncwarp();
+    // a box is half a row tile: its rows are tokens by heads, the order of the tile's rows
+    // (tokens past the unit's belong to rows that nobody reads)
+    if (lane < ns * H)
+      tma_3d(sb + C::OFF_Q + lane * C::HALF, &maps.q, 64 * (lane % H), p.h * a.Gq, p.t0 + (lane / H) * half, &bar->q_full);
+    for (int j = p.j0; j < p.j1; ++j) {
+      const int left = min(kWideKeys, p.g.len - j * kWideKeys);
+      const int boxes = (left + rows - 1) >> bshift;
+      int page[4];  // this lane's boxes: lane, lane + 32, ...
       bool bad = false;
 #pragma unroll
-      for (int i = 0; i < NR; ++i) {
-        const int r = r0 + i * RPT, key = j * kWideKeys + r;
-        off[i] = -1;
-        if (r < 128 && key < p.g.len) {
-          const int page = __ldg(p.g.table + (key >> shift));
-          if (page >= 0 && page < a.pool.n_pages)
-            off[i] = page * a.pool.page_stride + (key & mask) * a.pool.token_stride + hoff;
-          else
-            bad = true;
+      for (int i = 0; i < 4; ++i) {
+        page[i] = 0;
+        if (lane + 32 * i < boxes) {
+          page[i] = __ldg(p.g.table + ((j * kWideKeys + ((lane + 32 * i) << bshift)) >> shift));
+          bad |= page[i] < 0 || page[i] >= a.pool.n_pages;
         }
       }
       if (bad) atomicOr(&g_qg_status_attn_tc, QG_STATUS_BIT_ID);
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv, ++it) {
         const int st = static_cast<int>(it % C::NST);
-        if (!acquire(&bar->empty[st], static_cast<uint32_t>(((it / C::NST) & 1) ^ 1))) {
-          ok = false;
-          break;
-        }
-        const uint16_t *base = kv ? a.pool.v : a.pool.k;
-        const uint32_t dst = smem + C::OFF_KV + static_cast<uint32_t>(st) * C::TILE;
+        if (!warp_wait(&bar->empty[st], static_cast<uint32_t>(((it / C::NST) & 1) ^ 1), abort)) return;
+        // values past the last key become zeros: what their rows hold (or the stage held) could
+        // be infinite, and zero times that is not zero.  Keys may be anything: their scores are
+        // replaced.
+        const bool tail = kv && left < kWideKeys;
+        uint64_t *land = tail ? &bar->tail : &bar->full[st];
+        if (lane == 0) mbar_arrive_expect_tx(land, static_cast<uint32_t>(boxes * H * rows) * 128u);
+        __syncwarp();
+        const uint32_t off = C::OFF_KV + static_cast<uint32_t>(st) * C::TILE;
 #pragma unroll
-        for (int i = 0; i < NR; ++i)
-          if (r0 + i * RPT < 128)
-            cp_async16_zfill(dst + tile_off(r0 + i * RPT, c), base + (off[i] < 0 ? 0 : off[i]), off[i] < 0 ? 0u : 16u);
-        push(&bar->full[st]);
+        for (int i = 0; i < 4; ++i) {
+          const int b = lane + 32 * i;
+          if (b < boxes) {
+            const int row = (j * kWideKeys + (b << bshift)) & ((1 << shift) - 1);
+#pragma unroll
+            for (int h = 0; h < H; ++h)
+              tma_4d(sb + off + h * C::HALF + static_cast<uint32_t>(b << bshift) * 128u, kv ? &maps.v : &maps.k, 64 * h, row,
+                     p.h, page[i], land);
+          }
+        }
+        if (tail) {
+          if (!warp_wait(&bar->tail, ntail++ & 1, abort)) return;
+#pragma unroll
+          for (int h = 0; h < H; ++h)
+            for (int x = left * 8 + lane; x < kWideKeys * 8; x += 32)
+              *reinterpret_cast<uint4 *>(smem + off + h * C::HALF + x * 16) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();  // stored through the generic proxy, read by the tensor cores
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar->full[st]);
+        }
       }
     }
   }
-  flush();
 }
 
 // ---- MMA issue --------------------------------------------------------------------------------
@@ -327,23 +331,26 @@ QG_DEVICE void softmax(const AttnArgs &a, Walk walk, WideBars *bar, int s, int w
       tc_fence_after();
       const int left = lim - j * kWideKeys;  // keys of the tile that the row sees
       const bool masked = j * kWideKeys + kWideKeys > all;
-      float mx = -INFINITY;
+      float x[kWideKeys];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        float x[32];
-        tmem_ld32(ts + 32 * c, x);
-        if (neg) {
+      for (int c = 0; c < 4; ++c) tmem_ld32_nowait(ts + 32 * c, &x[32 * c]);
+      tmem_ld_wait(x);
+      if (neg) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = -x[i];
-        }
-        if (masked) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (32 * c + i >= left) x[i] = -INFINITY;
-        }
-#pragma unroll
-        for (int i = 0; i < 32; i += 2) mx = fmaxf(mx, fmaxf(x[i], x[i + 1]));
+        for (int i = 0; i < kWideKeys; ++i) x[i] = -x[i];
       }
+      if (masked) {
+#pragma unroll
+        for (int i = 0; i < kWideKeys; ++i)
+          if (i >= left) x[i] = -INFINITY;
+      }
+      float mx4[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+      for (int i = 4; i < kWideKeys; i += 4) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx4[e] = fmaxf(mx4[e], x[i + e]);
+      }
+      const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
       // the reference maximum moves when the row's outgrew it by 2^8 (or it is the first)
       const bool move = mx > m && (m == -INFINITY || (mx - m) * sl > 8.0f);
       float al = 1.0f;
@@ -354,48 +361,44 @@ QG_DEVICE void softmax(const AttnArgs &a, Walk walk, WideBars *bar, int s, int w
       }
       if (j != first && __any_sync(0xFFFFFFFFu, move)) {
         // every product into O has finished: S's barrier came after them
+#pragma unroll 1
+        for (int c = 0; c < D / 16; ++c) {
+          float o[16];
+          tmem_ld16(to + 16 * c, o);
+          uint32_t r[16];
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          float o[32];
-          tmem_ld32(to + 32 * c, o);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] *= al;
-          tmem_st32(to + 32 * c, o);
+          for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(o[i] * al);
+          tmem_st16(to + 16 * c, r);
         }
       }
       const float nm = m == -INFINITY ? 0.f : -m * sl;
       f2 sum = mk2(0.f, 0.f);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        float x[32];
-        tmem_ld32(ts + 32 * c, x);
-        if (neg) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = -x[i];
-        }
+        float *y = &x[32 * c];
 #pragma unroll
         for (int i = 0; i < 32; i += 2) {
-          const f2 y = fma2(mk2(x[i], x[i + 1]), mk2(sl, sl), mk2(nm, nm));
-          x[i] = ex2(y.x);
-          x[i + 1] = ex2(y.y);
+          const f2 e = fma2(mk2(y[i], y[i + 1]), mk2(sl, sl), mk2(nm, nm));
+          y[i] = ex2(e.x);
+          y[i + 1] = ex2(e.y);
         }
         if (masked) {
 #pragma unroll
           for (int i = 0; i < 32; ++i)
-            if (32 * c + i >= left) x[i] = 0.f;
+            if (32 * c + i >= left) y[i] = 0.f;
         }
         uint32_t hi[16];
 #pragma unroll
         for (int i = 0; i < 32; i += 2) {
-          sum = add2(sum, mk2(x[i], x[i + 1]));
-          hi[i / 2] = pack16<BF16>(x[i], x[i + 1]);
+          sum = add2(sum, mk2(y[i], y[i + 1]));
+          hi[i / 2] = pack16<BF16>(y[i], y[i + 1]);
         }
         tmem_st16(ts + 32 * c, hi);
         if constexpr (OUT32) {  // what the rounding left
           uint32_t lo[16];
 #pragma unroll
           for (int i = 0; i < 32; i += 2)
-            lo[i / 2] = pack16<BF16>(x[i] - lo16<BF16>(hi[i / 2]), x[i + 1] - hi16<BF16>(hi[i / 2]));
+            lo[i / 2] = pack16<BF16>(y[i] - lo16<BF16>(hi[i / 2]), y[i + 1] - hi16<BF16>(hi[i / 2]));
           tmem_st16(ts + 32 * c + 16, lo);
         }
       }
@@ -444,7 +447,8 @@ QG_DEVICE void softmax(const AttnArgs &a, Walk walk, WideBars *bar, int s, int w
 }
 
 template <int D, bool BF16, bool OUT32>
-__global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const __grid_constant__ AttnArgs a,
+                                                                   const __grid_constant__ WideMaps maps) {
   using C = WideCfg<D>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -453,10 +457,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const __grid_con
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::NST; ++i) {
-      mbar_init(&bar->full[i], kProdWarps);
+      mbar_init(&bar->full[i], 1);
       mbar_init(&bar->empty[i], 1);
     }
-    mbar_init(&bar->q_full, kProdWarps);
+    mbar_init(&bar->q_full, 1);
+    mbar_init(&bar->tail, 1);
     mbar_init(&bar->q_empty, 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bar->s_full[s], 1);
@@ -479,25 +484,33 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const __grid_con
   walk.end = line_start(walk.w + 1, total, nw);
   if (walk.at >= walk.end || !cursor_find(a, ln, *scan, walk.at, &walk.cur)) return;  // the same for the whole block
   if (warp == kMmaWarp) tmem_alloc(&bar->tmem, C::COLS);
+  fence_proxy_async_smem();  // the scan's words make way for tiles
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t sb = smem_u32(smem);
   if (warp < kSoftWarps) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
     softmax<D, BF16, OUT32>(a, walk, bar, warp >> 2, warp & 3, lane);
-  } else if (warp == kMmaWarp) {
-    if (lane == 0) {
-      issue_mma<D, BF16, OUT32>(a, walk, sb, bar);
-      // after an abort the products in flight finish before the tensor memory is released (a
-      // normal run waited for each); q_empty counts pieces, so any further phase will do
-      if (bar->abort) {
-        const uint64_t st = *reinterpret_cast<volatile uint64_t *>(&bar->q_empty);
-        tc_commit(&bar->q_empty);
-        for (uint32_t i = 0; i < (1u << 16) && *reinterpret_cast<volatile uint64_t *>(&bar->q_empty) == st; ++i) __nanosleep(32);
-      }
-    }
   } else {
-    produce<D>(a, walk, sb, bar, static_cast<int>(threadIdx.x) - 32 * (kMmaWarp + 1));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+    if (warp == kMmaWarp) {
+      if (lane == 0) {
+        issue_mma<D, BF16, OUT32>(a, walk, sb, bar);
+        // after an abort the products in flight finish before the tensor memory is released (a
+        // normal run waited for each); q_empty counts pieces, so any further phase will do
+        if (*static_cast<volatile int *>(&bar->abort)) {
+          const uint64_t st = *reinterpret_cast<volatile uint64_t *>(&bar->q_empty);
+          tc_commit(&bar->q_empty);
+          for (uint32_t i = 0; i < (1u << 16) && *reinterpret_cast<volatile uint64_t *>(&bar->q_empty) == st; ++i)
+            __nanosleep(32);
+        }
+      }
+    } else if (warp == kProdWarp) {
+      produce<D>(a, maps, walk, smem, bar, lane);
+      // after an abort the copies in flight land before the CTA's shared memory is released
+      if (*static_cast<volatile int *>(&bar->abort)) __nanosleep(1000000);
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -507,11 +520,48 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const __grid_con
   }
 }
 
+// the register split above needs the launch's registers to be what it was made for
+bool split_fits(const void *kernel) {
+  cudaFuncAttributes f;
+  return cudaFuncGetAttributes(&f, kernel) == cudaSuccess && f.numRegs == kRegs;
+}
+
+bool make_maps(const AttnArgs &a, bool bf16, WideMaps *m) {
+  const auto enc = encode_fn();
+  if (!enc) return false;
+  const CUtensorMapDataType type = bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  const cuuint64_t D = static_cast<cuuint64_t>(a.D), ps = 1ull << a.pool.page_shift;
+  {
+    const cuuint64_t dim[3] = {D, static_cast<cuuint64_t>(a.Hq), static_cast<cuuint64_t>(a.b.T)};
+    const cuuint64_t stride[2] = {D * 2, static_cast<cuuint64_t>(a.q_stride) * 2};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(a.Gq), static_cast<cuuint32_t>(a.wide.tpt / 2)};
+    if (enc(&m->q, type, 3, const_cast<uint16_t *>(a.q), dim, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return false;
+  }
+  const cuuint64_t dim[4] = {D, ps, static_cast<cuuint64_t>(a.pool.Hkv), static_cast<cuuint64_t>(a.pool.n_pages)};
+  // a dimension of one has no stride of its own: any valid one
+  const cuuint64_t stride[3] = {ps > 1 ? static_cast<cuuint64_t>(a.pool.token_stride) * 2 : D * 2,
+                                a.pool.Hkv > 1 ? static_cast<cuuint64_t>(a.pool.head_stride) * 2 : D * 2,
+                                a.pool.n_pages > 1 ? static_cast<cuuint64_t>(a.pool.page_stride) * 2 : D * 2};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(ps < kWideKeys ? ps : kWideKeys), 1, 1};
+  for (int i = 0; i < 2; ++i)
+    if (enc(i ? &m->v : &m->k, type, 4, i ? a.pool.v : a.pool.k, dim, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return false;
+  return true;
+}
+
 template <int D, bool BF16, bool OUT32>
 qg_status wide_run(const AttnArgs &a, cudaStream_t s) {
-  auto k = attn_wide_kernel<D, BF16, OUT32>;
-  if (!set_smem_attr(reinterpret_cast<const void *>(k), WideCfg<D>::SMEM)) return QG_ECUDA;
-  return launch_pdl(k, dim3(static_cast<unsigned>(a.wide.workers)), dim3(kThreads), WideCfg<D>::SMEM, s, a) == cudaSuccess
+  const auto k = attn_wide_kernel<D, BF16, OUT32>;
+  static const bool fits = split_fits(reinterpret_cast<const void *>(k));
+  WideMaps maps;
+  if (!fits || !make_maps(a, BF16, &maps) || !set_smem_attr(reinterpret_cast<const void *>(k), WideCfg<D>::SMEM))
+    return QG_ECUDA;
+  return launch_pdl(k, dim3(static_cast<unsigned>(a.wide.workers)), dim3(kThreads), WideCfg<D>::SMEM, s, a, maps) ==
+                 cudaSuccess
              ? QG_OK
              : QG_ECUDA;
 }

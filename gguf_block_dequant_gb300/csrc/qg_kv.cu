@@ -289,7 +289,7 @@ qg_status kv_check_cache(const qg_kv_cache *c, KvPool *pool) {
   if (c->n_pages < 1 || c->n_heads < 1 || c->n_heads > 1024 || c->page_size < 1 || c->page_size > 65536 ||
       (c->page_size & (c->page_size - 1)))
     return QG_EINVAL_SHAPE;
-  const int64_t lim = int64_t(1) << 40;  // keeps every product of index and stride inside 64 bits
+  const int64_t lim = int64_t(1) << 38;  // products with an index stay inside 64 bits, bytes inside a tensor map's 2^40
   if (c->page_stride < 0 || c->token_stride < 0 || c->head_stride < 0 || c->page_stride > lim ||
       c->token_stride > lim || c->head_stride > lim)
     return QG_EINVAL_SHAPE;

@@ -90,6 +90,14 @@ def test_page_sizes(qg, page, layout):
     check(qg, bt, 4, "bf16", "same")
 
 
+@pytest.mark.parametrize("page", [1, 2, 4, 8, 32, 64, 256])
+@pytest.mark.parametrize("layout,D", [("nhd", 128), ("hnd", 64)])
+def test_page_sizes_of_many_rows(qg, page, layout, D):
+    """Enough rows for the tensor-core row tiles, lists that end inside a page and inside a key tile."""
+    bt = Batch([70, 1, 33], [300, 9, 61], 2, D, page, "bf16", ((0, 2, 131), (2, 3, 256)), layout=layout)
+    check(qg, bt, 8, "bf16", "f32")
+
+
 QUERIES = {
     "two each": ([2, 2, 2], [2, 50, 9], ()),
     "ragged few": ([1, 3, 0, 5, 2], [40, 3, 12, 33, 2], ((0, 5, 77),)),
