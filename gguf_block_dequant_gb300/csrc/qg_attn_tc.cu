@@ -52,6 +52,19 @@ struct WideCfg {
   static constexpr uint32_t COLS = 512;                   // S0 S1 (128 each), O0 O1 (D each)
 };
 
+// A place in the tile ring and the parity of its present use.
+template <int N>
+struct Ring {
+  int st = 0;
+  uint32_t par = 0;
+  QG_DEVICE void next() {
+    if (++st == N) {
+      st = 0;
+      par ^= 1u;
+    }
+  }
+};
+
 struct WideBars {
   uint64_t full[8], empty[8];
   uint64_t q_full, q_empty, tail;
@@ -148,7 +161,7 @@ QG_DEVICE void produce(const AttnArgs &a, const WideMaps &maps, Walk walk, uint8
   const int shift = a.pool.page_shift;
   const int bshift = min(shift, 7), rows = 1 << bshift;  // rows of a box
   const int half = a.wide.tpt / 2;
-  long long it = 0;
+  Ring<C::NST> ring;
   int np = 0, ntail = 0;
   Piece p;
   for (; walk_next(a, &walk, &p); ++np) {
@@ -175,9 +188,9 @@ QG_DEVICE void produce(const AttnArgs &a, const WideMaps &maps, Walk walk, uint8
       }
       if (bad) atomicOr(&g_qg_status_attn_tc, QG_STATUS_BIT_ID);
 #pragma unroll
-      for (int kv = 0; kv < 2; ++kv, ++it) {
-        const int st = static_cast<int>(it % C::NST);
-        if (!warp_wait(&bar->empty[st], static_cast<uint32_t>(((it / C::NST) & 1) ^ 1), abort)) return;
+      for (int kv = 0; kv < 2; ++kv, ring.next()) {
+        const int st = ring.st;
+        if (!warp_wait(&bar->empty[st], ring.par ^ 1u, abort)) return;
         // values past the last key become zeros: what their rows hold (or the stage held) could
         // be infinite, and zero times that is not zero.  Keys may be anything: their scores are
         // replaced.
@@ -224,34 +237,33 @@ QG_DEVICE void issue_mma(const AttnArgs &a, Walk walk, uint32_t smem, WideBars *
     tc_fence_after();
     return r;
   };
-  long long it = 0;           // ring position of the piece's first key tile
   int np = 0;
   uint32_t n_p[2] = {0, 0};   // weights taken from each stream
   uint32_t n_o[2] = {0, 0};   // outputs begun for each stream
-  auto scores = [&](int s, int qt, int j) {  // S_s = Q_qt K_j^T
-    const uint32_t q = smem + C::OFF_Q + qt * C::TILE;
-    const uint32_t k = smem + C::OFF_KV + static_cast<uint32_t>((it + 2 * j) % C::NST) * C::TILE;
+  // descriptors differ in their start address alone (low word, 16-byte units)
+  const uint64_t dq = sw128_desc(smem + C::OFF_Q), dk = sw128_desc(smem + C::OFF_KV),
+                 dv = sw128_desc_mn(smem + C::OFF_KV, C::HALF);
+  auto scores = [&](int s, int qt, int st) {  // S_s = Q_qt K^T
+    const uint64_t q = dq + static_cast<uint32_t>(qt) * (C::TILE / 16), k = dk + static_cast<uint32_t>(st) * (C::TILE / 16);
 #pragma unroll
     for (int x = 0; x < D / 16; ++x) {
-      const uint32_t o = (x >> 2) * C::HALF + (x & 3) * 32;
-      tc_mma_bf16(tmem + 128u * s, sw128_desc(q + o), sw128_desc(k + o), id_s, x != 0);
+      const uint32_t o = ((x >> 2) * C::HALF + (x & 3) * 32) / 16;
+      tc_mma_bf16(tmem + 128u * s, q + o, k + o, id_s, x != 0);
     }
     tc_commit(&bar->s_full[s]);
   };
-  auto output = [&](int s, int j, bool first) {  // O_s += P_s V_j
-    const uint32_t v = smem + C::OFF_KV + static_cast<uint32_t>((it + 2 * j + 1) % C::NST) * C::TILE;
+  auto output = [&](int s, int st, bool first) {  // O_s += P_s V
+    const uint64_t v = dv + static_cast<uint32_t>(st) * (C::TILE / 16);
+    const uint32_t ps = tmem + 128u * s, o = tmem + 256u + D * s;
 #pragma unroll
     for (int x = 0; x < kWideKeys / 16; ++x) {
-      const uint32_t p = tmem + 128u * s + 32u * (x >> 1) + 8u * (x & 1);
-      const uint64_t d = sw128_desc_mn(v + x * 2048, C::HALF);
-      tc_mma_ta(tmem + 256u + D * s, p, d, id_o, !(first && x == 0));
-      if constexpr (OUT32) tc_mma_ta(tmem + 256u + D * s, p + 16u, d, id_o, 1);
+      const uint32_t p = ps + 32u * (x >> 1) + 8u * (x & 1);
+      tc_mma_ta(o, p, v + x * (2048 / 16), id_o, x == 0 ? !first : 1u);
+      if constexpr (OUT32) tc_mma_ta(o, p + 16u, v + x * (2048 / 16), id_o, 1);
     }
   };
-  auto full = [&](int i) {  // ring position it + i has landed
-    return wait(&bar->full[(it + i) % C::NST], static_cast<uint32_t>(((it + i) / C::NST) & 1));
-  };
-  auto free_tile = [&](int i) { tc_commit(&bar->empty[(it + i) % C::NST]); };
+  auto landed = [&](const Ring<C::NST> &r) { return wait(&bar->full[r.st], r.par); };
+  auto release = [&](const Ring<C::NST> &r) { tc_commit(&bar->empty[r.st]); };
   // weights of stream s are in tensor memory; before its first output of the piece, the last
   // piece's has been read
   auto weights = [&](int s, bool first) {
@@ -259,49 +271,59 @@ QG_DEVICE void issue_mma(const AttnArgs &a, Walk walk, uint32_t smem, WideBars *
     if (first && !wait(&bar->o_empty[s], (n_o[s]++ & 1) ^ 1)) return false;
     return true;
   };
-  bool ok = true;
+  // tiles come as K0 V0 K1 V1 ...; kt and vt are the next key and value tiles to be used
+  Ring<C::NST> kt, vt;
+  vt.next();
   Piece p;
-  for (; ok && walk_next(a, &walk, &p); ++np) {
+  for (; walk_next(a, &walk, &p); ++np) {
     const int n = p.j1 - p.j0;
-    ok = wait(&bar->q_full, np & 1);
+    if (!wait(&bar->q_full, np & 1)) return;
     if (p.paired) {
-      for (int j = 0; j <= n && ok; ++j) {
-        if (j < n) ok = full(2 * j);
-        if (j > 0) ok = ok && full(2 * j - 1);
-        for (int s = 0; s < 2 && ok; ++s) {
+      for (int j = 0; j <= n; ++j) {
+        if (j < n && !landed(kt)) return;
+        if (j > 0 && !landed(vt)) return;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
           if (j > 0) {
-            ok = weights(s, j == 1);
-            if (!ok) break;
-            output(s, j - 1, j == 1);
+            if (!weights(s, j == 1)) return;
+            output(s, vt.st, j == 1);
             if (j == n) tc_commit(&bar->o_full[s]);
           }
-          if (j < n) scores(s, s, j);
+          if (j < n) scores(s, s, kt.st);
         }
-        if (!ok) break;
-        if (j < n) free_tile(2 * j);
-        if (j > 0) free_tile(2 * j - 1);
-        if (j == n - 1) tc_commit(&bar->q_empty);
+        if (j < n) {
+          release(kt);
+          kt.next();
+          kt.next();
+          if (j == n - 1) tc_commit(&bar->q_empty);
+        }
+        if (j > 0) {
+          release(vt);
+          vt.next();
+          vt.next();
+        }
       }
     } else {
-      for (int j = 0; j < n + 2 && ok; ++j) {
+      for (int j = 0; j < n + 2; ++j) {
         const int s = j & 1;
         if (j >= 2 && j - 2 < n) {
-          ok = full(2 * (j - 2) + 1) && weights(s, j - 2 < 2);
-          if (!ok) break;
-          output(s, j - 2, j - 2 < 2);
-          free_tile(2 * (j - 2) + 1);
+          if (!landed(vt) || !weights(s, j < 4)) return;
+          output(s, vt.st, j < 4);
+          release(vt);
+          vt.next();
+          vt.next();
           if (j >= n) tc_commit(&bar->o_full[s]);
         }
         if (j < n) {
-          ok = full(2 * j);
-          if (!ok) break;
-          scores(s, 0, j);
-          free_tile(2 * j);
+          if (!landed(kt)) return;
+          scores(s, 0, kt.st);
+          release(kt);
+          kt.next();
+          kt.next();
           if (j == n - 1) tc_commit(&bar->q_empty);
         }
       }
     }
-    it += 2 * n;
   }
 }
 
