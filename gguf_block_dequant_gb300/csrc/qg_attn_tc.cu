@@ -231,9 +231,9 @@ QG_DEVICE void issue_mma(const AttnArgs &a, Walk walk, uint32_t smem, WideBars *
   using C = WideCfg<D>;
   constexpr uint32_t id_s = make_idesc16(128, kWideKeys, BF16, false), id_o = make_idesc16(128, D, BF16, true);
   volatile int *abort = &bar->abort;
-  const uint32_t tmem = bar->tmem;
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, bar->tmem, 0), el = elect_lane();
   auto wait = [&](uint64_t *b, uint32_t parity) {
-    const bool r = clock_wait(b, parity, abort);
+    const bool r = warp_wait(b, parity, abort);
     tc_fence_after();
     return r;
   };
@@ -248,9 +248,9 @@ QG_DEVICE void issue_mma(const AttnArgs &a, Walk walk, uint32_t smem, WideBars *
 #pragma unroll
     for (int x = 0; x < D / 16; ++x) {
       const uint32_t o = ((x >> 2) * C::HALF + (x & 3) * 32) / 16;
-      tc_mma_bf16(tmem + 128u * s, q + o, k + o, id_s, x != 0);
+      tc_mma_el(el, tmem + 128u * s, q + o, k + o, id_s, x != 0);
     }
-    tc_commit(&bar->s_full[s]);
+    tc_commit_el(el, &bar->s_full[s]);
   };
   auto output = [&](int s, int st, bool first) {  // O_s += P_s V
     const uint64_t v = dv + static_cast<uint32_t>(st) * (C::TILE / 16);
@@ -258,12 +258,12 @@ QG_DEVICE void issue_mma(const AttnArgs &a, Walk walk, uint32_t smem, WideBars *
 #pragma unroll
     for (int x = 0; x < kWideKeys / 16; ++x) {
       const uint32_t p = ps + 32u * (x >> 1) + 8u * (x & 1);
-      tc_mma_ta(o, p, v + x * (2048 / 16), id_o, x == 0 ? !first : 1u);
-      if constexpr (OUT32) tc_mma_ta(o, p + 16u, v + x * (2048 / 16), id_o, 1);
+      tc_mma_ta_el(el, o, p, v + x * (2048 / 16), id_o, x == 0 ? !first : 1u);
+      if constexpr (OUT32) tc_mma_ta_el(el, o, p + 16u, v + x * (2048 / 16), id_o, 1);
     }
   };
   auto landed = [&](const Ring<C::NST> &r) { return wait(&bar->full[r.st], r.par); };
-  auto release = [&](const Ring<C::NST> &r) { tc_commit(&bar->empty[r.st]); };
+  auto release = [&](const Ring<C::NST> &r) { tc_commit_el(el, &bar->empty[r.st]); };
   // weights of stream s are in tensor memory; before its first output of the piece, the last
   // piece's has been read
   auto weights = [&](int s, bool first) {
@@ -287,7 +287,7 @@ QG_DEVICE void issue_mma(const AttnArgs &a, Walk walk, uint32_t smem, WideBars *
           if (j > 0) {
             if (!weights(s, j == 1)) return;
             output(s, vt.st, j == 1);
-            if (j == n) tc_commit(&bar->o_full[s]);
+            if (j == n) tc_commit_el(el, &bar->o_full[s]);
           }
           if (j < n) scores(s, s, kt.st);
         }
@@ -295,7 +295,7 @@ QG_DEVICE void issue_mma(const AttnArgs &a, Walk walk, uint32_t smem, WideBars *
           release(kt);
           kt.next();
           kt.next();
-          if (j == n - 1) tc_commit(&bar->q_empty);
+          if (j == n - 1) tc_commit_el(el, &bar->q_empty);
         }
         if (j > 0) {
           release(vt);
@@ -312,7 +312,7 @@ QG_DEVICE void issue_mma(const AttnArgs &a, Walk walk, uint32_t smem, WideBars *
           release(vt);
           vt.next();
           vt.next();
-          if (j >= n) tc_commit(&bar->o_full[s]);
+          if (j >= n) tc_commit_el(el, &bar->o_full[s]);
         }
         if (j < n) {
           if (!landed(kt)) return;
@@ -320,7 +320,7 @@ QG_DEVICE void issue_mma(const AttnArgs &a, Walk walk, uint32_t smem, WideBars *
           release(kt);
           kt.next();
           kt.next();
-          if (j == n - 1) tc_commit(&bar->q_empty);
+          if (j == n - 1) tc_commit_el(el, &bar->q_empty);
         }
       }
     }
@@ -517,8 +517,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const __grid_con
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
     if (warp == kMmaWarp) {
+      issue_mma<D, BF16, OUT32>(a, walk, sb, bar);
       if (lane == 0) {
-        issue_mma<D, BF16, OUT32>(a, walk, sb, bar);
         // after an abort the products in flight finish before the tensor memory is released (a
         // normal run waited for each); q_empty counts pieces, so any further phase will do
         if (*static_cast<volatile int *>(&bar->abort)) {
