@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(NarrowCfg<D>::NW * 32, 1) attn_narrow_kernel(c
     __syncwarp();  // every lane has read the last tiles: the next piece's copies may replace them
 
     // ---- write the piece
-    const bool alone = !g.prefix && j0 == 0 && j1 == n_tiles && !has_prefix(a, cur.s - a.b.G);
+    const bool alone = j0 == 0 && j1 == n_tiles && seg_whole(a, g, cur.s >> 1);
     const size_t slot = static_cast<size_t>(cur.unit) + static_cast<size_t>(w);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -277,16 +277,16 @@ QG_DEVICE Pieces pieces_of(const AttnArgs &a, int s, int t, int h, int gq) {
   if (!nar && !(a.wide.workers && seg_in(a.wide, g))) return p;
   const Line &l = nar ? a.narrow : a.wide;
   const int r = (t - g.t0) / l.tpt;
-  const int x = unit_keys(g, l.tpt, r);
+  const int x = unit_keys(l, g, r);
   if (x == 0) return p;
-  const long long total = l.seg_pos[a.b.G + a.b.B];
+  const long long total = l.seg_pos[2 * a.b.B];
   const int nw = line_workers(l, total);
   const int rt = seg_tiles(l, g);
   const long long p0 = l.seg_pos[s] + h * seg_cost_to(l, g, rt) + seg_cost_to(l, g, r);
   const int w0 = line_owner(p0, total, nw);
   int w1 = line_owner(p0 + x - 1, total, nw);
   // the last one's part may lie within the last key tile, which is then its neighbour's
-  if (w1 > w0 && (line_start(w1, total, nw) - p0 + l.keys - 1) / l.keys >= (x + l.keys - 1) / l.keys) --w1;
+  if (w1 > w0 && tiles_of(l, static_cast<int>(line_start(w1, total, nw) - p0)) >= tiles_of(l, x)) --w1;
   p.o = l.part_o;
   p.ml = l.part_ml;
   p.first = static_cast<size_t>(l.seg_unit[s] + h * rt + r) + static_cast<size_t>(w0);
@@ -399,8 +399,8 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
   Pieces own, pre;
   own.count = pre.count = 0;
   own.halves = pre.halves = 1;
-  if (b >= 0) own = pieces_of(a, a.b.G + b, t, h, ROW ? hh % a.Gq : 0);
-  if (gr >= 0) pre = pieces_of(a, gr, t, h, ROW ? hh % a.Gq : 0);
+  if (b >= 0) own = pieces_of(a, 2 * b + 1, t, h, ROW ? hh % a.Gq : 0);
+  if (gr >= 0 && !seq_long(a, b)) pre = pieces_of(a, 2 * run_first(a, gr, b), t, h, ROW ? hh % a.Gq : 0);
   if (own.count == 1 && own.halves == 1 && pre.count == 0) return;  // its worker wrote the row
   if constexpr (ROW) {
     __shared__ float so[8][D];
@@ -455,13 +455,16 @@ struct Plan {
 Plan make_plan(const KvPool &pool, const KvBatch &b, int Gq, int sms) {
   Plan p = {};
   const int tn = kNarrowRows / Gq, tw = 2 * (kWideHalf / Gq);
-  const long long nseg = static_cast<long long>(b.G) + b.B;
+  const long long nseg = 2LL * b.B;
   const bool wide = attn_wide_supported(pool.D) && b.T > tn;
   p.narrow_workers = sms * (pool.D == 256 ? 4 : 8);
   p.wide_workers = wide ? sms : 0;
-  // a token is in its own segment and in its group's: 2 T tokens at most over all segments
-  long long un = nseg;                                            // wide line there: one row tile each
-  if (!wide) un = nseg + (b.G ? 2 : 1) * (static_cast<long long>(b.T) / tn);
+  // long sequences have more than kWideHalf / Gq tokens; runs: one per group and one after each
+  // long sequence.  A token is in its own segment and in at most one run.
+  const long long longs = b.q_start ? std::min<long long>(b.B, b.T / (kWideHalf / Gq + 1)) : 0;
+  const long long runs = b.G ? std::min<long long>(b.B, b.G + (wide ? longs : 0)) : 0;
+  long long un = b.B + runs;                                      // wide line there: one row tile each
+  if (!wide) un += (b.G ? 2 : 1) * (static_cast<long long>(b.T) / tn);
   const long long sn = un * pool.Hkv + p.narrow_workers;
   size_t at = 0;
   auto take = [&](size_t n) {
@@ -474,11 +477,10 @@ Plan make_plan(const KvPool &pool, const KvBatch &b, int Gq, int sms) {
   p.n_ml = take(static_cast<size_t>(sn) * kNarrowRows * 8);
   p.n_o = take(static_cast<size_t>(sn) * kNarrowRows * pool.D * 4);
   if (wide) {
-    // segments of more than tn tokens: at most T / (tn + 1) sequences (none when each has one
-    // token), and every group
-    const long long segs = b.G + (b.q_start ? std::min<long long>(b.B, b.T / (tn + 1)) : 0);
-    const long long uw = segs + (b.G ? 1 : 0) * (static_cast<long long>(b.T) / tw) +
-                         (b.q_start ? static_cast<long long>(b.T) / tw : 0);
+    // of each kind, at most T / (tn + 1) segments have the more than tn tokens of the wide line
+    const long long most = b.T / (tn + 1), tiles = static_cast<long long>(b.T) / tw;
+    const long long uw = (b.q_start ? std::min<long long>(b.B, most) + tiles : 0) +
+                         (b.G ? std::min<long long>(runs, most) + tiles : 0);
     const long long sw = uw * pool.Hkv + p.wide_workers;
     p.w_pos = take((nseg + 1) * 8);
     p.w_unit = take((nseg + 1) * 4);
@@ -576,10 +578,10 @@ qg_status qg_attn_paged(const qg_kv_cache *cache, const qg_kv_batch *batch, int 
   a.out32 = out_dtype == QG_DT_F32;
   a.scale_log2 = scale * 1.4426950408889634f;
   uint8_t *ws = static_cast<uint8_t *>(workspace);
-  auto line = [&](int rows, int keys, int workers, size_t pos, size_t unit, size_t o, size_t ml) {
+  auto line = [&](int rows, int kshift, int workers, size_t pos, size_t unit, size_t o, size_t ml) {
     Line l = {};
     l.rows = rows;
-    l.keys = keys;
+    l.kshift = kshift;
     l.tpt = rows == kNarrowRows ? rows / a.Gq : 2 * (kWideHalf / a.Gq);
     l.workers = workers;
     l.seg_pos = reinterpret_cast<long long *>(ws + pos);
@@ -588,10 +590,11 @@ qg_status qg_attn_paged(const qg_kv_cache *cache, const qg_kv_batch *batch, int 
     l.part_ml = reinterpret_cast<float2 *>(ws + ml);
     return l;
   };
-  a.narrow = line(kNarrowRows, kNarrowKeys, p.narrow_workers, p.n_pos, p.n_unit, p.n_o, p.n_ml);
+  a.narrow = line(kNarrowRows, kNarrowShift, p.narrow_workers, p.n_pos, p.n_unit, p.n_o, p.n_ml);
+  a.long_tokens = p.wide_workers ? kWideHalf / a.Gq : INT32_MAX;
   a.narrow.hi = p.wide_workers ? a.narrow.tpt : INT32_MAX;
   if (p.wide_workers) {
-    a.wide = line(kWideRows, kWideKeys, p.wide_workers, p.w_pos, p.w_unit, p.w_o, p.w_ml);
+    a.wide = line(kWideRows, kWideShift, p.wide_workers, p.w_pos, p.w_unit, p.w_o, p.w_ml);
     a.wide.lo = a.narrow.tpt;
     a.wide.hi = INT32_MAX;
   }

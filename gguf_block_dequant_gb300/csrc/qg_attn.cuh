@@ -1,7 +1,10 @@
 // qg_attn.cuh -- the work of one attention call, as its kernels share it.
 //
 // A SEGMENT is a list of cached keys with the query tokens that read it: a group's prefix with
-// all tokens of the group's sequences, or a sequence's own keys with its own tokens.  The rows
+// the tokens of a run of the group's sequences, or a sequence's own keys with its own tokens.  A
+// LONG sequence, with more query rows than the 128 of a tensor-core tile, gains nothing from
+// sharing the read of a prefix: its own segment has the prefix's keys first, and its rows need
+// no joining; runs are what long sequences leave of a group.  The rows
 // of a segment and a cached head are its (token, query head of that cached head) pairs; they
 // are cut into ROW TILES of `tpt` whole tokens.  A UNIT is (segment, cached head, row tile),
 // and its cost is the number of keys its last row sees.  All units in (segment, head, row
@@ -21,19 +24,19 @@
 
 namespace qg {
 
-constexpr int kNarrowRows = 16, kNarrowKeys = 16;
-constexpr int kWideHalf = 128, kWideRows = 2 * kWideHalf, kWideKeys = 128;
+constexpr int kNarrowRows = 16, kNarrowShift = 4, kNarrowKeys = 1 << kNarrowShift;
+constexpr int kWideHalf = 128, kWideRows = 2 * kWideHalf, kWideShift = 7, kWideKeys = 1 << kWideShift;
 
 // A line: row and key tile sizes, and which segments belong to it.
 struct Line {
-  int rows, keys;        // rows and keys per tile
+  int rows, kshift;      // rows per tile, keys per tile (its logarithm)
   int tpt;               // tokens per row tile: rows / Gq (wide: two halves of 128 / Gq)
   int lo, hi;            // segments with lo < tokens <= hi belong to it
   int workers;
   float *part_o;         // [slot][rows][D]
   float2 *part_ml;       // [slot][rows]: running maximum (log2 units) and sum
-  long long *seg_pos;    // [segments + 1] place of each segment's first key on the line
-  int *seg_unit;         // [segments + 1] first unit of each segment
+  long long *seg_pos;    // [2 B + 1] place of each segment's first key on the line
+  int *seg_unit;         // [2 B + 1] first unit of each segment
 };
 
 struct AttnArgs {
@@ -45,43 +48,75 @@ struct AttnArgs {
   float scale_log2;      // scale * log2(e): exponentials are powers of two
   int Hq, Gq, D;
   int out32;
-  Line narrow, wide;     // wide.workers == 0: the narrow line has every segment
+  int long_tokens;       // sequences of more new tokens are long
+  Line narrow, wide;     // wide.workers == 0: the narrow line has every segment, nothing is long
 };
 
 struct Seg {
   int t0, nt;            // token rows
-  int len;               // keys
-  int prefix;
-  const int32_t *table;
+  int prefix;            // 1: a run of a group's sequences and the group's prefix
+  int len;               // keys (own ones of a sequence)
+  int plen;              // a long sequence's keys before its own
+  const int32_t *table, *ptable;
 };
 
+QG_DEVICE int kv_prefix_len(const AttnArgs &a, int g) {
+  return kv_clamp(__ldg(a.b.prefix_len + g), 0, kv_cap(a.b.max_prefix_pages, a.pool.page_shift));
+}
+QG_DEVICE const int32_t *kv_prefix_table(const AttnArgs &a, int g) {
+  return a.b.prefix_pages + static_cast<size_t>(g) * a.b.max_prefix_pages;
+}
+QG_DEVICE bool seq_long(const AttnArgs &a, int b) {
+  return a.b.q_start && kv_tok(a.b, b + 1) - kv_tok(a.b, b) > a.long_tokens;
+}
+// first sequence of the run that b, not long, of group g is in
+QG_DEVICE int run_first(const AttnArgs &a, int g, int b) {
+  const int lo = kv_clamp(__ldg(a.b.group_start + g), 0, b);
+  if (!a.b.q_start || !a.wide.workers) return lo;
+  while (b > lo && !seq_long(a, b - 1)) --b;
+  return b;
+}
+
+// segment 2 b: the run of sequences that starts at b (empty when none does); 2 b + 1: b's own
 QG_DEVICE Seg seg_load(const AttnArgs &a, int s) {
+  const int b = s >> 1;
   Seg g;
-  int b0, b1;
-  if (s < a.b.G) {
-    b0 = kv_clamp(__ldg(a.b.group_start + s), 0, a.b.B);
-    b1 = kv_clamp(__ldg(a.b.group_start + s + 1), b0, a.b.B);
-    g.len = kv_clamp(__ldg(a.b.prefix_len + s), 0, kv_cap(a.b.max_prefix_pages, a.pool.page_shift));
-    g.table = a.b.prefix_pages + static_cast<size_t>(s) * a.b.max_prefix_pages;
-    g.prefix = 1;
-  } else {
-    b0 = s - a.b.G;
-    b1 = b0 + 1;
-    g.len = kv_own_len(a.b, a.pool.page_shift, b0);
-    g.table = a.b.pages + static_cast<size_t>(b0) * a.b.max_pages;
-    g.prefix = 0;
+  g.prefix = !(s & 1);
+  g.nt = g.len = g.plen = 0;
+  g.table = g.ptable = nullptr;
+  g.t0 = kv_tok(a.b, b);
+  const int gr = kv_group_of(a.b, b);
+  const bool lg = seq_long(a, b);
+  if (s & 1) {
+    g.nt = max(0, kv_tok(a.b, b + 1) - g.t0);
+    g.len = kv_own_len(a.b, a.pool.page_shift, b);
+    g.table = a.b.pages + static_cast<size_t>(b) * a.b.max_pages;
+    if (lg && gr >= 0) {
+      g.plen = kv_prefix_len(a, gr);
+      g.ptable = kv_prefix_table(a, gr);
+    }
+  } else if (gr >= 0 && !lg) {
+    const int lo = __ldg(a.b.group_start + gr), hi = kv_clamp(__ldg(a.b.group_start + gr + 1), b + 1, a.b.B);
+    if (b != max(lo, 0) && !seq_long(a, b - 1)) return g;  // the run began earlier
+    int e = hi;
+    if (a.b.q_start && a.wide.workers)
+      for (e = b + 1; e < hi && !seq_long(a, e);) ++e;
+    g.nt = max(0, kv_tok(a.b, e) - g.t0);
+    g.len = kv_prefix_len(a, gr);
+    g.table = kv_prefix_table(a, gr);
   }
-  g.t0 = kv_tok(a.b, b0);
-  g.nt = max(0, kv_tok(a.b, b1) - g.t0);
   return g;
 }
 
-QG_DEVICE bool seg_in(const Line &l, const Seg &g) { return g.nt > l.lo && g.nt <= l.hi && g.len > 0; }
+QG_DEVICE bool seg_in(const Line &l, const Seg &g) { return g.nt > l.lo && g.nt <= l.hi && (g.len | g.plen) > 0; }
 QG_DEVICE int seg_tiles(const Line &l, const Seg &g) { return (g.nt + l.tpt - 1) / l.tpt; }  // row tiles
 
-// keys of row tile r: up to the last key its last token sees
-QG_DEVICE int unit_keys(const Seg &g, int tpt, int r) {
-  return g.prefix ? g.len : kv_clamp(g.len - g.nt + min(g.nt, (r + 1) * tpt), 0, g.len);
+QG_DEVICE int tiles_of(const Line &l, int keys) { return (keys + (1 << l.kshift) - 1) >> l.kshift; }
+// keys of row tile r: up to the last key its last token sees (a long sequence's prefix counts
+// in whole tiles, so that its own keys start one)
+QG_DEVICE int unit_keys(const Line &l, const Seg &g, int r) {
+  if (g.prefix) return g.len;
+  return (tiles_of(l, g.plen) << l.kshift) + kv_clamp(g.len - g.nt + min(g.nt, (r + 1) * l.tpt), 0, g.len);
 }
 // keys of row tiles 0 .. r-1
 QG_DEVICE long long seg_cost_to(const Line &l, const Seg &g, int r) {
@@ -92,13 +127,13 @@ QG_DEVICE long long seg_cost_to(const Line &l, const Seg &g, int r) {
   const long long n = m - i0;
   long long c = n * (base + (i0 + 1) * l.tpt) + n * (n - 1) / 2 * l.tpt;
   if (r == rt) c += g.len;
-  return c;
+  return c + static_cast<long long>(r) * (tiles_of(l, g.plen) << l.kshift);
 }
 
 // workers that take part: at least `kMinTiles` tiles each, and never less than one
 constexpr int kMinTiles = 2;
 QG_DEVICE int line_workers(const Line &l, long long total) {
-  const long long n = (total + kMinTiles * l.keys - 1) / (kMinTiles * l.keys);
+  const long long n = (total + (kMinTiles << l.kshift) - 1) / (kMinTiles << l.kshift);
   return n < l.workers ? static_cast<int>(n) : l.workers;
 }
 QG_DEVICE long long line_start(long long w, long long total, int n) { return w * total / n; }
@@ -106,7 +141,7 @@ QG_DEVICE int line_owner(long long p, long long total, int n) {
   return static_cast<int>(((p + 1) * n + total - 1) / total - 1);
 }
 
-// keys of the segment that token t sees (t in the segment's token rows)
+// keys of the segment's (own) list that token t sees (t in the segment's token rows)
 QG_DEVICE int row_limit(const AttnArgs &a, const Seg &g, int t) {
   if (!g.prefix) return kv_clamp(g.len - g.nt + (t - g.t0) + 1, 0, g.len);
   const int b = kv_seq_of(a.b, t);
@@ -114,6 +149,11 @@ QG_DEVICE int row_limit(const AttnArgs &a, const Seg &g, int t) {
   const int t0 = kv_tok(a.b, b), n = kv_tok(a.b, b + 1) - t0;
   const long long seen = static_cast<long long>(g.len) + kv_own_len(a.b, a.pool.page_shift, b) - n + (t - t0) + 1;
   return seen < 0 ? 0 : seen > g.len ? g.len : static_cast<int>(seen);
+}
+// keys of a long sequence's prefix that token t sees
+QG_DEVICE int row_prefix_limit(const Seg &g, int t) {
+  const long long seen = static_cast<long long>(g.plen) + g.len - g.nt + (t - g.t0) + 1;
+  return seen < 0 ? 0 : seen > g.plen ? g.plen : static_cast<int>(seen);
 }
 
 // ---- the block's view of a line ---------------------------------------------------------------
@@ -127,7 +167,7 @@ struct LineScan {
 
 template <int NT>
 QG_DEVICE long long line_scan(const AttnArgs &a, const Line &l, LineScan<NT> *sc, bool publish) {
-  const int nseg = a.b.G + a.b.B;
+  const int nseg = 2 * a.b.B;
   const int chunk = (nseg + NT - 1) / NT;
   const int s0 = min(nseg, static_cast<int>(threadIdx.x) * chunk), s1 = min(nseg, s0 + chunk);
   long long c = 0;
@@ -204,14 +244,14 @@ struct Cursor {
 
 // to the first unit of a segment at or after s (pos and unit are those of s)
 QG_DEVICE bool cursor_seg(const AttnArgs &a, const Line &l, Cursor *c, int s) {
-  const int nseg = a.b.G + a.b.B;
+  const int nseg = 2 * a.b.B;
   for (; s < nseg; ++s) {
     c->g = seg_load(a, s);
     if (!seg_in(l, c->g)) continue;
     c->s = s;
     c->rt = seg_tiles(l, c->g);
     c->h = c->r = 0;
-    c->x = unit_keys(c->g, l.tpt, 0);
+    c->x = unit_keys(l, c->g, 0);
     return true;
   }
   return false;
@@ -223,7 +263,7 @@ QG_DEVICE bool cursor_next(const AttnArgs &a, const Line &l, Cursor *c) {
     c->r = 0;
     if (++c->h == a.pool.Hkv) return cursor_seg(a, l, c, c->s + 1);
   }
-  c->x = unit_keys(c->g, l.tpt, c->r);
+  c->x = unit_keys(l, c->g, c->r);
   return true;
 }
 // to the unit that holds place `at`
@@ -235,7 +275,7 @@ QG_DEVICE bool cursor_find(const AttnArgs &a, const Line &l, const LineScan<NT> 
     if (sc.pos[m] <= at) lo = m;
     else hi = m;
   }
-  const int chunk = (a.b.G + a.b.B + NT - 1) / NT;
+  const int chunk = (2 * a.b.B + NT - 1) / NT;
   c->pos = sc.pos[lo];
   c->unit = sc.unit[lo];
   if (!cursor_seg(a, l, c, lo * chunk)) return false;
@@ -258,22 +298,26 @@ QG_DEVICE bool cursor_find(const AttnArgs &a, const Line &l, const LineScan<NT> 
   c->r = lo;
   c->pos += seg_cost_to(l, c->g, lo);
   c->unit += c->h * c->rt + lo;
-  c->x = unit_keys(c->g, l.tpt, lo);
+  c->x = unit_keys(l, c->g, lo);
   return true;
 }
 // the key tiles [j0, j1) of the cursor's unit in the part [at, end) of the line (none: j0 == j1);
 // n: tiles of the unit
 QG_DEVICE void cursor_tiles(const Line &l, const Cursor &c, long long at, long long end, int *j0, int *j1, int *n) {
-  const long long o0 = at > c.pos ? at - c.pos : 0, o1 = end - c.pos < c.x ? end - c.pos : c.x;
-  *j0 = static_cast<int>((o0 + l.keys - 1) / l.keys);
-  *j1 = static_cast<int>((o1 + l.keys - 1) / l.keys);
-  *n = (c.x + l.keys - 1) / l.keys;
+  const int up = (1 << l.kshift) - 1;
+  const int o0 = at > c.pos ? static_cast<int>(at - c.pos) : 0;
+  const int o1 = end - c.pos < c.x ? static_cast<int>(end - c.pos) : c.x;
+  *j0 = (o0 + up) >> l.kshift;
+  *j1 = (o1 + up) >> l.kshift;
+  *n = (c.x + up) >> l.kshift;
 }
 
-// whether a sequence's rows have a prefix besides its own keys
-QG_DEVICE bool has_prefix(const AttnArgs &a, int seq) {
-  const int g = kv_group_of(a.b, seq);
-  return g >= 0 && kv_clamp(__ldg(a.b.prefix_len + g), 0, kv_cap(a.b.max_prefix_pages, a.pool.page_shift)) > 0;
+// whether the own segment g of sequence b has all the keys its rows see
+QG_DEVICE bool seg_whole(const AttnArgs &a, const Seg &g, int b) {
+  if (g.prefix) return false;
+  if (seq_long(a, b)) return true;
+  const int gr = kv_group_of(a.b, b);
+  return gr < 0 || kv_prefix_len(a, gr) == 0;
 }
 
 // attention over many rows per segment on the tcgen05 tensor cores (qg_attn_tc.cu)

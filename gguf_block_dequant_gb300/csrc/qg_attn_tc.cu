@@ -78,7 +78,7 @@ struct Piece {
   Seg g;
   int h, t0;       // cached head, first token row of the unit
   int tokens;      // of the unit
-  int j0, j1;      // key tiles
+  int j0, j1, jp;  // key tiles; the first jp of the unit are those of a long sequence's prefix
   bool paired;     // two halves of rows; otherwise the streams take the key tiles in turn
   bool alone;      // the piece is all there is of its rows
   size_t slot;
@@ -101,7 +101,8 @@ QG_DEVICE bool walk_next(const AttnArgs &a, Walk *k, Piece *p) {
       p->t0 = c.g.t0 + c.r * l.tpt;
       p->tokens = min(l.tpt, c.g.nt - c.r * l.tpt);
       p->paired = p->tokens > l.tpt / 2;
-      p->alone = p->paired && !c.g.prefix && p->j0 == 0 && p->j1 == n && !has_prefix(a, c.s - a.b.G);
+      p->jp = tiles_of(l, c.g.plen);
+      p->alone = p->paired && p->j0 == 0 && p->j1 == n && seg_whole(a, c.g, c.s >> 1);
       p->slot = static_cast<size_t>(c.unit) + static_cast<size_t>(k->w);
     }
     if (!cursor_next(a, l, &c)) c.pos = k->end;
@@ -174,7 +175,10 @@ QG_DEVICE void produce(const AttnArgs &a, const WideMaps &maps, Walk walk, uint8
     if (lane < ns * H)
       tma_3d(sb + C::OFF_Q + lane * C::HALF, &maps.q, 64 * (lane % H), p.h * a.Gq, p.t0 + (lane / H) * half, &bar->q_full);
     for (int j = p.j0; j < p.j1; ++j) {
-      const int left = min(kWideKeys, p.g.len - j * kWideKeys);
+      const bool pre = j < p.jp;
+      const int key0 = (pre ? j : j - p.jp) * kWideKeys;
+      const int32_t *table = pre ? p.g.ptable : p.g.table;
+      const int left = min(kWideKeys, (pre ? p.g.plen : p.g.len) - key0);
       const int boxes = (left + rows - 1) >> bshift;
       int page[4];  // this lane's boxes: lane, lane + 32, ...
       bool bad = false;
@@ -182,7 +186,7 @@ QG_DEVICE void produce(const AttnArgs &a, const WideMaps &maps, Walk walk, uint8
       for (int i = 0; i < 4; ++i) {
         page[i] = 0;
         if (lane + 32 * i < boxes) {
-          page[i] = __ldg(p.g.table + ((j * kWideKeys + ((lane + 32 * i) << bshift)) >> shift));
+          page[i] = __ldg(table + ((key0 + ((lane + 32 * i) << bshift)) >> shift));
           bad |= page[i] < 0 || page[i] >= a.pool.n_pages;
         }
       }
@@ -203,7 +207,7 @@ QG_DEVICE void produce(const AttnArgs &a, const WideMaps &maps, Walk walk, uint8
         for (int i = 0; i < 4; ++i) {
           const int b = lane + 32 * i;
           if (b < boxes) {
-            const int row = (j * kWideKeys + (b << bshift)) & ((1 << shift) - 1);
+            const int row = (key0 + (b << bshift)) & ((1 << shift) - 1);
 #pragma unroll
             for (int h = 0; h < H; ++h)
               tma_4d(sb + off + h * C::HALF + static_cast<uint32_t>(b << bshift) * 128u, kv ? &maps.v : &maps.k, 64 * h, row,
@@ -344,15 +348,18 @@ QG_DEVICE void softmax(const AttnArgs &a, Walk walk, WideBars *bar, int s, int w
     const int tok = min(half, p.tokens - sub * half);
     const bool valid = row < tok * a.Gq;
     const int t = p.t0 + sub * half + (valid ? row / a.Gq : 0);
-    const int lim = valid ? row_limit(a, p.g, t) : 0;
+    const int lim = valid ? row_limit(a, p.g, t) : 0, limp = valid ? row_prefix_limit(p.g, t) : 0;
     const int all = __reduce_min_sync(0xFFFFFFFFu, valid ? lim : 0x7FFFFFFF);
+    const int allp = __reduce_min_sync(0xFFFFFFFFu, valid ? limp : 0x7FFFFFFF);
     float m = -INFINITY, l = 0.f;
     const int step = p.paired ? 1 : 2, first = p.paired ? p.j0 : p.j0 + s;
     for (int j = first; j < p.j1; j += step) {
       if (!warp_wait(&bar->s_full[s], n_s++ & 1, abort)) return;
       tc_fence_after();
-      const int left = lim - j * kWideKeys;  // keys of the tile that the row sees
-      const bool masked = j * kWideKeys + kWideKeys > all;
+      const bool pre = j < p.jp;
+      const int key0 = (pre ? j : j - p.jp) * kWideKeys;
+      const int left = (pre ? limp : lim) - key0;  // keys of the tile that the row sees
+      const bool masked = key0 + kWideKeys > (pre ? allp : all);
       float x[kWideKeys];
 #pragma unroll
       for (int c = 0; c < 4; ++c) tmem_ld32_nowait(ts + 32 * c, &x[32 * c]);

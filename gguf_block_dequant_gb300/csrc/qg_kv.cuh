@@ -27,10 +27,10 @@ QG_DEVICE int kv_tok(const KvBatch &a, int b) {
   return a.q_start ? kv_clamp(__ldg(a.q_start + b), 0, a.T) : min(b, a.T);
 }
 
-// the page lists' capacity in tokens (at most 2^31 - 1)
+// the page lists' capacity in tokens (at most 2^30 - 1, so that sums of two stay in 32 bits)
 QG_DEVICE int kv_cap(int pages, int shift) {
   const long long c = static_cast<long long>(pages) << shift;
-  return c > 0x7FFFFFFFLL ? 0x7FFFFFFF : static_cast<int>(c);
+  return c > 0x3FFFFFFFLL ? 0x3FFFFFFF : static_cast<int>(c);
 }
 QG_DEVICE int kv_own_len(const KvBatch &a, int shift, int b) {
   return kv_clamp(__ldg(a.kv_len + b), 0, kv_cap(a.max_pages, shift));

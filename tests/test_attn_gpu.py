@@ -109,6 +109,9 @@ QUERIES = {
     "prompts under prefixes": ([70, 33, 64], [70, 40, 129], ((0, 1, 128), (1, 3, 129))),
     "many short under a prefix": ([3] * 40, [3] * 40, ((0, 40, 600),)),
     "a prompt that sees little": ([150], [20], ((0, 1, 30),)),
+    "short ones among prompts": ([1, 2, 90, 1, 1, 130, 3, 1, 140, 7], [9, 2, 90, 70, 1, 200, 3, 5, 141, 300],
+                                 ((0, 7, 300), (7, 9, 77))),
+    "a short prefix before prompts": ([133, 129, 1], [133, 500, 40], ((0, 3, 5),)),
 }
 
 
