@@ -260,49 +260,75 @@ __global__ void __launch_bounds__(NarrowCfg<D>::NW * 32, 1) attn_narrow_kernel(c
 }
 
 // ---- joining ------------------------------------------------------------------------------------
-// The pieces of one row: slots first, first + 1, ... (count of them), row `row` of a `rows`-row tile.
+// One token's rows in one segment: what its pieces' slots follow from, for every head.
+struct RowSeg {
+  const Line *l;            // null: no keys there
+  long long p0, cost;       // place of head 0's unit, places per head
+  long long total;
+  int unit, rt, x, nw;      // head 0's unit, units per head, keys of a unit, workers
+  int row, halves;          // first row in the tile; 2: each slot holds two partial results of a row
+};
+
+QG_DEVICE RowSeg row_seg(const AttnArgs &a, int s, int t) {
+  RowSeg q;
+  q.l = nullptr;
+  const Seg g = seg_load(a, s);
+  const bool nar = seg_in(a.narrow, g);
+  if (!nar && !(a.wide.workers && seg_in(a.wide, g))) return q;
+  const Line &l = nar ? a.narrow : a.wide;
+  const int r = (t - g.t0) / l.tpt, i = t - g.t0 - r * l.tpt;
+  q.x = unit_keys(l, g, r);
+  if (q.x == 0) return q;
+  q.l = &l;
+  q.total = l.seg_pos[2 * a.b.B];
+  q.nw = line_workers(l, q.total);
+  q.rt = seg_tiles(l, g);
+  q.p0 = l.seg_pos[s] + seg_cost_to(l, g, r);
+  q.cost = seg_cost_to(l, g, q.rt);
+  q.unit = l.seg_unit[s] + r;
+  q.halves = 1;
+  if (nar) {
+    q.row = i * a.Gq;
+  } else {
+    const int half = l.tpt / 2;
+    q.row = (i / half) * kWideHalf + (i % half) * a.Gq;
+    // one half's rows alone: the kernel's two streams took the key tiles in turn
+    if (g.nt - r * l.tpt <= half) q.halves = 2;
+  }
+  return q;
+}
+
+// The pieces of one row: slots first, first + 1, ... (count of them), row `row` of a `rows`-row
+// tile (and the one kWideHalf rows on, with two halves).
 struct Pieces {
   const float *o;
   const float2 *ml;
   size_t first;
-  int count, rows, row;
-  int halves;  // 2: each slot holds two partial results of the row, kWideHalf rows apart
+  int count, rows, row, halves;
 };
-
-QG_DEVICE Pieces pieces_of(const AttnArgs &a, int s, int t, int h, int gq) {
+QG_DEVICE Pieces pieces_of(const RowSeg &q, int h, int gq) {
   Pieces p;
   p.count = 0;
-  const Seg g = seg_load(a, s);
-  const bool nar = seg_in(a.narrow, g);
-  if (!nar && !(a.wide.workers && seg_in(a.wide, g))) return p;
-  const Line &l = nar ? a.narrow : a.wide;
-  const int r = (t - g.t0) / l.tpt;
-  const int x = unit_keys(l, g, r);
-  if (x == 0) return p;
-  const long long total = l.seg_pos[2 * a.b.B];
-  const int nw = line_workers(l, total);
-  const int rt = seg_tiles(l, g);
-  const long long p0 = l.seg_pos[s] + h * seg_cost_to(l, g, rt) + seg_cost_to(l, g, r);
-  const int w0 = line_owner(p0, total, nw);
-  int w1 = line_owner(p0 + x - 1, total, nw);
+  p.halves = 1;
+  if (!q.l) return p;
+  const Line &l = *q.l;
+  const long long p0 = q.p0 + h * q.cost;
+  const int w0 = line_owner(p0, q.total, q.nw);
+  int w1 = line_owner(p0 + q.x - 1, q.total, q.nw);
   // the last one's part may lie within the last key tile, which is then its neighbour's
-  if (w1 > w0 && tiles_of(l, static_cast<int>(line_start(w1, total, nw) - p0)) >= tiles_of(l, x)) --w1;
+  if (w1 > w0 && tiles_of(l, static_cast<int>(line_start(w1, q.total, q.nw) - p0)) >= tiles_of(l, q.x)) --w1;
   p.o = l.part_o;
   p.ml = l.part_ml;
-  p.first = static_cast<size_t>(l.seg_unit[s] + h * rt + r) + static_cast<size_t>(w0);
+  p.first = static_cast<size_t>(q.unit + h * q.rt) + static_cast<size_t>(w0);
   p.count = w1 - w0 + 1;
   p.rows = l.rows;
-  const int i = t - g.t0 - r * l.tpt;
-  p.halves = 1;
-  if (nar) {
-    p.row = i * a.Gq + gq;
-  } else {
-    const int half = l.tpt / 2;
-    p.row = (i / half) * kWideHalf + (i % half) * a.Gq + gq;
-    // one half's rows alone: the kernel's two streams took the key tiles in turn
-    if (g.nt - r * l.tpt <= half) p.halves = 2;
-  }
+  p.row = q.row + gq;
+  p.halves = q.halves;
   return p;
+}
+// whether a worker wrote the row itself: all its keys are in one piece
+QG_DEVICE bool written(const Pieces &own, const Pieces &pre) {
+  return own.count == 1 && own.halves == 1 && pre.count == 0;
 }
 
 // Online softmax over pieces i0, i0 + step, ...: lane holds D/32 consecutive outputs.
@@ -381,29 +407,28 @@ QG_DEVICE void write_row(const AttnArgs &a, int t, int hq, int lane, const Acc<D
 }
 
 // ROW: one block of 8 warps per row, the row's pieces spread over the warps (few rows, many
-// pieces each); otherwise a warp per (token, cached head) (many rows, a piece or two each).
+// pieces each); otherwise a warp per token, its lanes asking which heads need joining at all
+// (many rows, most of them written by their workers).
 template <int D, bool BF16, bool OUT32, bool ROW>
 __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ AttnArgs a) {
   constexpr int NV = D / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
   pdl_launch_dependents();
-  long long id = ROW ? blockIdx.x : static_cast<long long>(blockIdx.x) * 8 + warp;
-  const int per = ROW ? a.Hq : a.pool.Hkv;
-  const int t = static_cast<int>(id / per), hh = static_cast<int>(id - static_cast<long long>(t) * per);
+  const int t = ROW ? static_cast<int>(blockIdx.x) / a.Hq : static_cast<int>(blockIdx.x) * 8 + warp;
   if (t >= a.b.T) return;
   const int b = kv_seq_of(a.b, t);
   const int gr = b >= 0 ? kv_group_of(a.b, b) : -1;
   if (b < 0 && (ROW ? threadIdx.x == 0 : lane == 0)) atomicOr(&g_qg_status_attn, QG_STATUS_BIT_ID);
-  const int h = ROW ? hh / a.Gq : hh;
-  Pieces own, pre;
-  own.count = pre.count = 0;
-  own.halves = pre.halves = 1;
-  if (b >= 0) own = pieces_of(a, 2 * b + 1, t, h, ROW ? hh % a.Gq : 0);
-  if (gr >= 0 && !seq_long(a, b)) pre = pieces_of(a, 2 * run_first(a, gr, b), t, h, ROW ? hh % a.Gq : 0);
-  if (own.count == 1 && own.halves == 1 && pre.count == 0) return;  // its worker wrote the row
+  RowSeg so, sp;
+  so.l = sp.l = nullptr;
+  if (b >= 0) so = row_seg(a, 2 * b + 1, t);
+  if (gr >= 0 && !seq_long(a, b)) sp = row_seg(a, 2 * run_first(a, gr, b), t);
   if constexpr (ROW) {
-    __shared__ float so[8][D];
+    const int hq = static_cast<int>(blockIdx.x) % a.Hq;
+    const Pieces own = pieces_of(so, hq / a.Gq, hq % a.Gq), pre = pieces_of(sp, hq / a.Gq, hq % a.Gq);
+    if (written(own, pre)) return;
+    __shared__ float sh[8][D];
     __shared__ float2 sml[8];
     Acc<NV> x;
     x.m = -INFINITY;
@@ -413,7 +438,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
     acc_pieces<D>(x, own, warp, 8, lane);
     acc_pieces<D>(x, pre, warp, 8, lane);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) so[warp][lane * NV + i] = x.o[i];
+    for (int i = 0; i < NV; ++i) sh[warp][lane * NV + i] = x.o[i];
     if (lane == 0) sml[warp] = make_float2(x.m, x.l);
     __syncthreads();
     if (warp) return;
@@ -421,22 +446,30 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
     for (int q = 1; q < 8; ++q) {
       float v[NV];
 #pragma unroll
-      for (int i = 0; i < NV; ++i) v[i] = so[q][lane * NV + i];
+      for (int i = 0; i < NV; ++i) v[i] = sh[q][lane * NV + i];
       acc_add(x, sml[q].x, sml[q].y, v);
     }
-    write_row<D, BF16, OUT32>(a, t, hh, lane, x);
+    write_row<D, BF16, OUT32>(a, t, hq, lane, x);
   } else {
-    for (int q = 0; q < a.Gq; ++q) {
-      Acc<NV> x;
-      x.m = -INFINITY;
-      x.l = 0.f;
+    for (int h0 = 0; h0 < a.pool.Hkv; h0 += 32) {
+      const int hl = h0 + lane;
+      uint32_t todo = __ballot_sync(0xFFFFFFFFu, hl < a.pool.Hkv && !written(pieces_of(so, hl, 0), pieces_of(sp, hl, 0)));
+      for (; todo; todo &= todo - 1) {
+        const int h = h0 + __ffs(static_cast<int>(todo)) - 1;
+        Pieces own = pieces_of(so, h, 0), pre = pieces_of(sp, h, 0);
+        for (int q = 0; q < a.Gq; ++q) {
+          Acc<NV> x;
+          x.m = -INFINITY;
+          x.l = 0.f;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) x.o[i] = 0.f;
-      acc_pieces<D>(x, own, 0, 1, lane);
-      acc_pieces<D>(x, pre, 0, 1, lane);
-      write_row<D, BF16, OUT32>(a, t, h * a.Gq + q, lane, x);
-      ++own.row;
-      ++pre.row;
+          for (int i = 0; i < NV; ++i) x.o[i] = 0.f;
+          acc_pieces<D>(x, own, 0, 1, lane);
+          acc_pieces<D>(x, pre, 0, 1, lane);
+          write_row<D, BF16, OUT32>(a, t, h * a.Gq + q, lane, x);
+          ++own.row;
+          ++pre.row;
+        }
+      }
     }
   }
 }
@@ -515,12 +548,12 @@ qg_status attn_run(const AttnArgs &a, int sms, cudaStream_t s) {
     const qg_status st = attn_wide_launch(a, BF16, s);
     if (st != QG_OK) return st;
   }
-  const long long rows = static_cast<long long>(a.b.T) * a.Hq, tasks = static_cast<long long>(a.b.T) * a.pool.Hkv;
+  const long long rows = static_cast<long long>(a.b.T) * a.Hq;
   cudaError_t e;
   if (rows <= 8192)
     e = launch_pdl(attn_join_kernel<D, BF16, OUT32, true>, dim3(static_cast<unsigned>(rows)), dim3(256), 0, s, a);
   else
-    e = launch_pdl(attn_join_kernel<D, BF16, OUT32, false>, dim3(static_cast<unsigned>((tasks + 7) / 8)), dim3(256), 0, s,
+    e = launch_pdl(attn_join_kernel<D, BF16, OUT32, false>, dim3(static_cast<unsigned>((a.b.T + 7) / 8)), dim3(256), 0, s,
                    a);
   if (e != cudaSuccess) return QG_ECUDA;
   return cudaGetLastError() == cudaSuccess ? QG_OK : QG_ECUDA;
