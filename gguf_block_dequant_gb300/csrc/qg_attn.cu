@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(NarrowCfg<D>::NW * 32, 1) attn_narrow_kernel(c
   const int qr = lane >> 2, qc = lane & 3;      // fragment row and column pair
   const int crow = lane / CH, cchunk = lane % CH;  // copy: row within an instruction, chunk
 
-  for (bool more = true; more && cur.pos < end; more = cursor_next(a, ln, &cur)) {
+  for (bool more = true; more; more = cursor_next(a, ln, &cur, end)) {
     int j0, j1, n_tiles;
     cursor_tiles(ln, cur, at, end, &j0, &j1, &n_tiles);
     if (j0 >= j1) continue;

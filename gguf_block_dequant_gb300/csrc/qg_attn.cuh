@@ -256,7 +256,10 @@ QG_DEVICE bool cursor_seg(const AttnArgs &a, const Line &l, Cursor *c, int s) {
   }
   return false;
 }
-QG_DEVICE bool cursor_next(const AttnArgs &a, const Line &l, Cursor *c) {
+// to the next unit; false when the part of the line that ends at `end` has no more (asked first:
+// a walk over the empty segments at the end of the line is a chain of loads)
+QG_DEVICE bool cursor_next(const AttnArgs &a, const Line &l, Cursor *c, long long end) {
+  if (c->pos + c->x >= end) return false;
   c->pos += c->x;
   ++c->unit;
   if (++c->r == c->rt) {

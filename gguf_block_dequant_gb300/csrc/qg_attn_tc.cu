@@ -105,7 +105,7 @@ QG_DEVICE bool walk_next(const AttnArgs &a, Walk *k, Piece *p) {
       p->alone = p->paired && p->j0 == 0 && p->j1 == n && seg_whole(a, c.g, c.s >> 1);
       p->slot = static_cast<size_t>(c.unit) + static_cast<size_t>(k->w);
     }
-    if (!cursor_next(a, l, &c)) c.pos = k->end;
+    if (!cursor_next(a, l, &c, k->end)) c.pos = k->end;
     if (some) return true;
   }
   return false;
