@@ -37,6 +37,8 @@ def lib_path() -> str:
 def load():
     """Load libggufdq.so (no fallback: raises if it is missing)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -96,21 +98,32 @@ def strerror(status: int) -> str:
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
+
+
+_raw_stream = None  # the current stream's handle, without a Stream object where torch offers it
+
+
+def _current_stream():
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        device = torch.cuda.current_device
+        current = torch.cuda.current_stream
+        _raw_stream = (lambda: raw(device())) if raw else (lambda: current().cuda_stream)
+    return _raw_stream()
 
 
 def _stream(stream):
     if stream is None:
-        import torch
-
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
-    if isinstance(stream, int):
-        return ctypes.c_void_p(stream)
-    return ctypes.c_void_p(stream.cuda_stream)
+        return _current_stream()
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _call(name, *args):
-    rc = getattr(load(), name)(*args)
+    rc = getattr(_lib or load(), name)(*args)
     if rc != QG_OK:
         raise QGError(rc, name)
 
@@ -319,11 +332,16 @@ def moe_layer(qtype, xn, wr, w_gate, w_up, w_down, expert_stride, slots, n_slots
 DT_F32, DT_F16, DT_BF16 = 0, 1, 2
 
 
-def _dtype(t):
-    import torch
+_dtypes = {}
 
+
+def _dtype(t):
+    if not _dtypes:
+        import torch
+
+        _dtypes.update({torch.float32: DT_F32, torch.float16: DT_F16, torch.bfloat16: DT_BF16})
     try:
-        return {torch.float32: DT_F32, torch.float16: DT_F16, torch.bfloat16: DT_BF16}[t.dtype]
+        return _dtypes[t.dtype]
     except KeyError:
         raise ValueError(f"unsupported dtype {t.dtype}") from None
 
@@ -421,11 +439,12 @@ def _rows(t, T, n, what):
     """Row stride of a tensor whose T rows of n elements may be slices of wider ones."""
     if t is None:
         return 0
-    if t.dim() == 3 and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2])):
+    shape, st = t.shape, t.stride()
+    if len(shape) == 3 and (st[2] != 1 or (shape[1] > 1 and st[1] != shape[2])):
         raise ValueError(f"{what}: a token's heads must lie side by side")
-    if t.dim() not in (2, 3) or t.stride(-1) != 1 or t.shape[0] != T or t.numel() != T * n:
+    if len(shape) not in (2, 3) or st[-1] != 1 or shape[0] != T or t.numel() != T * n:
         raise ValueError(f"{what} must have {T} rows of {n} elements")
-    return t.stride(0) if T > 1 else n
+    return st[0] if T > 1 else n
 
 
 def kv_append(cache, batch, q, k, v, q_out, freqs, pairs=False, q_norm=None, k_norm=None, eps=1e-6, stream=None):
