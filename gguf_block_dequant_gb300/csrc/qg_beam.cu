@@ -1,11 +1,12 @@
 // qg_beam.cu -- one beam-search selection: the K best continuations of each request's W beams
 // over the vocabulary.
 //
-// cand(w, v) = score_w + (logit[w][v] - m_w) - log sum_v exp(logit[w][v] - m_w).  Within a row the order is the logits' order, so the
-// first kernel needs one pass over the logits (the bytes that bound it): each CTA takes a slice
-// of one row into registers, forms the slice's maximum and sum of exponentials and keeps its K
-// largest (logit, lowest index first).  The second joins a request's slices: the row sums in 64
-// bits, each row's K best, then the K best of W*K candidates ranked in 64 bits.
+// cand(w, v) = score_w + (logit[w][v] - m_w) - log sum_v exp(logit[w][v] - m_w).  Within a row the
+// order is the logits' order, so the first kernel needs one pass over the logits (the bytes that
+// bound it): a CTA streams a slice of one row through registers, keeps the slice's maximum and
+// sum of exponentials, and a short list of the values above the K-th best so far, which after
+// the first chunk hardly any value joins.  The second joins a request's slices: the row sums in
+// 64 bits, each row's K best, then the K best of W*K candidates ranked in 64 bits.
 #include <math.h>
 
 #include <algorithm>
@@ -15,9 +16,11 @@
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kPT = 16;                  // values per thread and chunk
+constexpr int kChunk = kThreads * kPT;
 constexpr int kMaxK = 64;
-constexpr int kList = 1024;  // candidates a slice can hold before the exact fallback
+constexpr int kList = 2048;              // candidates a slice holds
 
 // f32 -> unsigned that rises with the value; NaN counts as -inf
 QG_DEVICE uint32_t ord_of(float x) {
@@ -55,14 +58,49 @@ QG_DEVICE unsigned long long warp_max64(unsigned long long v) {
   return v;
 }
 
-// PT values per thread: the slice is PT * 256 values.  Value i of thread t is element
-// 1024 (i / 4) + 4 t + i % 4 of the slice.
-template <int PT>
-__global__ void __launch_bounds__(kThreads) select_slice_kernel(const SelectArgs a) {
-  __shared__ float red[8];
-  __shared__ uint32_t wmax[8], wmin[8];
-  __shared__ unsigned long long list[kList], best[8];
-  __shared__ int count;
+// The slice's candidates and what it takes to thin them out to the K best, in falling order.
+struct SliceShared {
+  unsigned long long list[kList], best[kMaxK], top[kWarps];
+  float red[kWarps];
+  int count;
+};
+QG_DEVICE void thin(SliceShared &sh, int K) {  // by the whole CTA; keys differ, so a key's rank is the number of larger ones
+  __syncthreads();
+  const int c = sh.count;
+  for (int i = threadIdx.x; i < c; i += kThreads) {
+    const unsigned long long k = sh.list[i];
+    int r = 0;
+    for (int j = 0; j < c; ++j) r += sh.list[j] > k;
+    if (r < K) sh.best[r] = k;
+  }
+  __syncthreads();
+  const int n = min(c, K);
+  if (threadIdx.x < n) sh.list[threadIdx.x] = sh.best[threadIdx.x];
+  if (threadIdx.x == 0) sh.count = n;
+  __syncthreads();
+}
+
+// Value i of thread t of a chunk is its element 4 (kThreads (i / 4) + t) + i % 4.
+QG_DEVICE int chunk_elem(int i) { return 4 * (kThreads * (i >> 2) + static_cast<int>(threadIdx.x)) + (i & 3); }
+QG_DEVICE void load_chunk(const SelectArgs &a, const float *x, int n, float (&v)[kPT]) {
+#pragma unroll
+  for (int i = 0; i < kPT; i += 4) {
+    const int e = chunk_elem(i);
+    if (a.vec4 && e + 4 <= n) {
+      const float4 q = __ldg(reinterpret_cast<const float4 *>(x + e));
+      v[i] = q.x;
+      v[i + 1] = q.y;
+      v[i + 2] = q.z;
+      v[i + 3] = q.w;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[i + j] = e + j < n ? __ldg(x + e + j) : -INFINITY;
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, 2) select_slice_kernel(const SelectArgs a) {
+  __shared__ SliceShared sh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
   pdl_launch_dependents();
@@ -91,133 +129,143 @@ __global__ void __launch_bounds__(kThreads) select_slice_kernel(const SelectArgs
     return;
   }
   const long long base = static_cast<long long>(sl) * a.slice;
-  const int n = static_cast<int>(min(static_cast<long long>(a.slice), a.V - base));
+  const int len = static_cast<int>(min(static_cast<long long>(a.slice), a.V - base));
   const float *x = a.logits + static_cast<size_t>(row) * a.V + base;
-  float v[PT];
+  if (threadIdx.x == 0) sh.count = 0;
+  float m = -INFINITY, sum = 0.f;      // this thread's maximum and sum of exp(x - m)
+  bool full = false;                   // the list holds K: only values above tau can matter
+  uint32_t tau = 0;                    // order word of the K-th best
+  float v[kPT], w[kPT];
+  load_chunk(a, x, len, w);
+  for (int c0 = 0; c0 < len; c0 += kChunk) {
+    const int n = len - c0;
 #pragma unroll
-  for (int i = 0; i < PT; i += 4) {
-    const int e = 256 * i + 4 * static_cast<int>(threadIdx.x);
-    if (a.vec4 && e + 4 <= n) {
-      const float4 q = __ldg(reinterpret_cast<const float4 *>(x + e));
-      v[i] = q.x + 0.0f;  // -0 and +0 are one value
-      v[i + 1] = q.y + 0.0f;
-      v[i + 2] = q.z + 0.0f;
-      v[i + 3] = q.w + 0.0f;
-    } else {
+    for (int i = 0; i < kPT; ++i) v[i] = w[i] + 0.0f;  // -0 and +0 are one value
+    if (c0 + kChunk < len) load_chunk(a, x + c0 + kChunk, n - kChunk, w);
+    float mx = -INFINITY;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[i + j] = e + j < n ? __ldg(x + e + j) + 0.0f : -INFINITY;
+    for (int i = 0; i < kPT; ++i) mx = fmaxf(mx, v[i]);  // fmaxf drops NaN
+    const uint32_t mo = ord_of(mx);
+    if (mx > m) {
+      sum *= expf(m - mx);  // 0 from -inf (and of +inf - +inf never: mx > m)
+      m = mx;
     }
-  }
-  // ---- maximum and sum of exponentials
-  float mx = -INFINITY;
+    if (m > -INFINITY && m < INFINITY) {
+      float part = 0.f;
 #pragma unroll
-  for (int i = 0; i < PT; ++i) mx = fmaxf(mx, v[i]);  // fmaxf drops NaN
-  const uint32_t mo = ord_of(mx);
-  const uint32_t wm = __reduce_max_sync(0xFFFFFFFFu, mo), wn = __reduce_min_sync(0xFFFFFFFFu, mo);
-  if (lane == 0) {
-    wmax[warp] = wm;
-    wmin[warp] = wn;
-  }
-  if (threadIdx.x == 0) count = 0;
-  __syncthreads();
-  uint32_t hi = 0, lo = 0xFFFFFFFFu;
+      for (int i = 0; i < kPT; ++i) {
+        const float e = expf(v[i] - m);
+        part += isnan(v[i]) ? 0.f : e;
+      }
+      sum += part;
+    }
+    // ---- candidates.  A later value equal to the K-th best loses to it by its index.
+    uint32_t t = full ? tau + 1u : 0u;
+    const bool any = full ? mo >= t : chunk_elem(0) < n;
+    const int have = sh.count;  // nobody adds to the list before the barrier
+    int hits = __syncthreads_count(any);
+    if (hits == 0) continue;
+    const int K = min(a.K, n);
+    bool exact = false;
+    if (hits * kPT > kList - kMaxK) {
+      // raise t while at least K threads' maxima reach it (so K values do): few values pass
+      uint32_t lo = t, hi = 0xFFFFFFFFu;
+      while (hi - lo > 1) {
+        const uint32_t mid = lo + (hi - lo) / 2;
+        const int c = __syncthreads_count(mo >= mid && any);
+        if (c >= K) {
+          lo = mid;
+          hits = c;
+          if (c <= K + 16) break;
+        } else {
+          hi = mid;
+        }
+      }
+      t = lo;
+      exact = hits * kPT > kList - kMaxK;  // many equal maxima
+    }
+    if (have + (exact ? K : hits * kPT) > kList) thin(sh, a.K);
+    if (!exact) {
+      if (any && mo >= t) {
 #pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    hi = max(hi, wmax[q]);
-    lo = min(lo, wmin[q]);
-  }
-  const float bm = ord_val(hi);
-  float sum = 0.f;
-  if (isfinite(bm)) {
+        for (int i = 0; i < kPT; ++i) {
+          const int e = chunk_elem(i);
+          if (e < n && ord_of(v[i]) >= t) sh.list[atomicAdd(&sh.count, 1)] = key_of(v[i], static_cast<uint32_t>(base + c0 + e));
+        }
+      }
+    } else {
+      // the chunk's K best, one maximum at a time
+      unsigned long long last = ~0ull;
+      for (int r = 0; r < K; ++r) {
+        unsigned long long k = 0;
 #pragma unroll
-    for (int i = 0; i < PT; ++i) sum += isnan(v[i]) ? 0.f : expf(v[i] - bm);
-  }
-  sum = warp_sum(sum);
-  if (lane == 0) red[warp] = sum;
-
-  // ---- a value t that at least K threads' maxima reach (so K values do), as high as a few
-  // halvings of [lowest, highest maximum] bring it: few values pass it
-  const int K = min(a.K, n);
-  uint32_t tl = lo, th = hi;  // count(tl) >= K; th not known to have it
-  {
-    int c = __syncthreads_count(mo >= th);
-    if (c >= K) tl = th;
-    while (tl < th && th - tl > 1) {
-      const uint32_t m = tl + (th - tl) / 2;
-      c = __syncthreads_count(mo >= m);
-      if (c >= K) {
-        tl = m;
-        if (c <= K + 16) break;
-      } else {
-        th = m;
+        for (int i = 0; i < kPT; ++i) {
+          const int e = chunk_elem(i);
+          if (e < n) {
+            const unsigned long long u = key_of(v[i], static_cast<uint32_t>(base + c0 + e));
+            if (u < last && u > k) k = u;
+          }
+        }
+        k = warp_max64(k);
+        if (lane == 0) sh.top[warp] = k;
+        __syncthreads();
+        k = sh.top[0];
+#pragma unroll
+        for (int q = 1; q < kWarps; ++q) k = sh.top[q] > k ? sh.top[q] : k;
+        last = k;
+        if (threadIdx.x == 0) sh.list[sh.count++] = k;
+        __syncthreads();
       }
     }
+    __syncthreads();
+    // a short list makes a high tau: thin it early, and whenever it has grown
+    if (sh.count >= a.K && (!full || sh.count > a.K + 32)) {
+      thin(sh, a.K);
+      full = true;
+      tau = static_cast<uint32_t>(sh.list[a.K - 1] >> 32);
+    }
   }
+  thin(sh, a.K);
+  for (int i = threadIdx.x; i < a.K; i += kThreads) keys[i] = i < sh.count ? sh.list[i] : 0;
+  // ---- the slice's maximum and sum
+  float bm = m;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) bm = fmaxf(bm, __shfl_xor_sync(0xFFFFFFFFu, bm, o));
+  if (lane == 0) sh.red[warp] = bm;
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < kWarps; ++q) bm = fmaxf(bm, sh.red[q]);
+  __syncthreads();
+  sum = warp_sum(sum > 0.f ? sum * expf(m - bm) : 0.f);
+  if (lane == 0) sh.red[warp] = sum;
+  __syncthreads();
   if (threadIdx.x == 0) {
     float s = 0.f;
 #pragma unroll
-    for (int q = 0; q < 8; ++q) s += red[q];
+    for (int q = 0; q < kWarps; ++q) s += sh.red[q];
     a.ms[out] = make_float2(bm, s);
   }
-  if (mo >= tl) {
-#pragma unroll
-    for (int i = 0; i < PT; ++i) {
-      const int e = 256 * (i & ~3) + 4 * static_cast<int>(threadIdx.x) + (i & 3);
-      if (e < n && ord_of(v[i]) >= tl) {
-        const int at = atomicAdd(&count, 1);
-        if (at < kList) list[at] = key_of(v[i], static_cast<uint32_t>(base + e));
-      }
-    }
-  }
-  __syncthreads();
-  const int c = count;
-  if (c >= K && c <= kList) {
-    // keys differ, so a key's rank is the number of larger ones
-    for (int i = threadIdx.x; i < c; i += kThreads) {
-      const unsigned long long k = list[i];
-      int r = 0;
-      for (int j = 0; j < c; ++j) r += list[j] > k;
-      if (r < K) keys[r] = k;
-    }
-  } else {
-    // many equal values (or fewer threads than K hold values): one maximum at a time
-    unsigned long long last = ~0ull;
-    for (int r = 0; r < K; ++r) {
-      unsigned long long k = 0;
-#pragma unroll
-      for (int i = 0; i < PT; ++i) {
-        const int e = 256 * (i & ~3) + 4 * static_cast<int>(threadIdx.x) + (i & 3);
-        if (e < n) {
-          const unsigned long long u = key_of(v[i], static_cast<uint32_t>(base + e));
-          if (u < last && u > k) k = u;
-        }
-      }
-      k = warp_max64(k);
-      if (lane == 0) best[warp] = k;
-      __syncthreads();
-      k = best[0];
-#pragma unroll
-      for (int q = 1; q < 8; ++q) k = best[q] > k ? best[q] : k;
-      if (threadIdx.x == 0) keys[r] = k;
-      last = k;
-      __syncthreads();
-    }
-  }
-  for (int i = K + threadIdx.x; i < a.K; i += kThreads) keys[i] = 0;
 }
 
-// One CTA per request.  A warp takes a row at a time: its slices' sums, then its K best keys (the
-// slices' lists fall, so a list's next key is the only one that can come next; lane q holds the
-// heads of lists q, q + 32, ...), then all W*K candidates are ranked against each other.
+// One CTA per request, all its slices' lists in shared memory.  A warp takes a row at a time: its
+// slices' sums, then its K best keys (the lists fall, so a list's next key is the only one that
+// can come next; lane q holds the heads of lists q, q + 32, ...), then all W*K candidates are
+// ranked against each other.
 constexpr int kMergeThreads = 512;
+constexpr int kMaxSlices = 128;
 __global__ void __launch_bounds__(kMergeThreads) select_merge_kernel(const SelectArgs a) {
   extern __shared__ uint8_t smem[];
-  double *cand = reinterpret_cast<double *>(smem);                                      // [W*K]
-  uint32_t *tok = reinterpret_cast<uint32_t *>(cand + static_cast<size_t>(a.W) * a.K);  // [W*K]
+  const int per_row = a.S * a.K;
+  unsigned long long *lists = reinterpret_cast<unsigned long long *>(smem);            // [W][S][K]
+  double *cand = reinterpret_cast<double *>(lists + static_cast<size_t>(a.W) * per_row);  // [W*K]
+  uint32_t *tok = reinterpret_cast<uint32_t *>(cand + static_cast<size_t>(a.W) * a.K);    // [W*K]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nwarps = kMergeThreads / 32;
   pdl_wait();
   pdl_launch_dependents();
   const int req = blockIdx.x;
+  for (int i = threadIdx.x; i < a.W * per_row; i += kMergeThreads)
+    lists[i] = __ldcg(a.keys + static_cast<size_t>(req) * a.W * per_row + i);
+  __syncthreads();
   for (int w = warp; w < a.W; w += nwarps) {
     const int row = req * a.W + w;
     const float2 *ms = a.ms + static_cast<size_t>(row) * a.S;
@@ -237,7 +285,7 @@ __global__ void __launch_bounds__(kMergeThreads) select_merge_kernel(const Selec
     const bool none = !isfinite(m) || !isfinite(sc);  // no distribution, or a beam not continued
     // candidate = off + (logit - m): a row of huge equal logits would absorb the rest otherwise
     const double off = none ? 0.0 : static_cast<double>(sc) - log(sum);
-    const unsigned long long *kr = a.keys + static_cast<size_t>(row) * a.S * a.K;
+    const unsigned long long *kr = lists + w * per_row;
     if (none) {
       for (int i = lane; i < a.K; i += 32) {
         cand[w * a.K + i] = -INFINITY;
@@ -245,15 +293,15 @@ __global__ void __launch_bounds__(kMergeThreads) select_merge_kernel(const Selec
       }
       continue;
     }
-    // lane's lists: positions and heads (S <= 32 * kHeads lists)
-    constexpr int kHeads = 4;
+    // lane's lists: positions and heads
+    constexpr int kHeads = kMaxSlices / 32;
     int at[kHeads];
     unsigned long long head[kHeads];
 #pragma unroll
     for (int q = 0; q < kHeads; ++q) {
       const int s = lane + 32 * q;
       at[q] = 0;
-      head[q] = s < a.S ? __ldcg(kr + static_cast<size_t>(s) * a.K) : 0ull;
+      head[q] = s < a.S ? kr[s * a.K] : 0ull;
     }
     for (int r = 0; r < a.K; ++r) {
       unsigned long long k = 0;
@@ -269,7 +317,7 @@ __global__ void __launch_bounds__(kMergeThreads) select_merge_kernel(const Selec
         for (int q = 0; q < kHeads; ++q)
           if (head[q] == k) {
             ++at[q];
-            head[q] = at[q] < a.K ? __ldcg(kr + static_cast<size_t>(lane + 32 * q) * a.K + at[q]) : 0ull;
+            head[q] = at[q] < a.K ? kr[(lane + 32 * q) * a.K + at[q]] : 0ull;
           }
       }
     }
@@ -303,14 +351,18 @@ __global__ void __launch_bounds__(kMergeThreads) select_merge_kernel(const Selec
   }
 }
 
-// Values per thread of a slice: as many slices as fill the device twice, 8 to 32 values a thread,
-// and no more than 128 slices a row (what the merge holds).
-int slice_values(long long rows, long long V, int sms) {
-  int pt = 8;
-  while (pt < 32 && rows * ((V + kThreads * pt - 1) / (kThreads * pt)) > 8LL * sms) pt *= 2;
-  while (pt < 512 && (V + kThreads * pt - 1) / (kThreads * pt) > 128) pt *= 2;
-  return pt;
+// Slices of a row: two CTAs for every SM in all, but no slice under 2048 values, and lists that
+// fit the merge's shared memory.
+struct Slices {
+  int S, slice;
+};
+Slices make_slices(long long rows, long long W, long long K, long long V, int sms) {
+  long long S = std::min<long long>({2LL * sms / rows, (V + 2047) / 2048, kMaxSlices, 16384 / (W * K)});
+  S = std::max<long long>(S, 1);
+  const long long slice = ((V + S - 1) / S + 3) / 4 * 4;
+  return {static_cast<int>((V + slice - 1) / slice), static_cast<int>(slice)};
 }
+size_t merge_smem(int W, int K, int S) { return static_cast<size_t>(W) * K * (8 * static_cast<size_t>(S) + 12); }
 
 bool select_shape(int N, int W, int K, int64_t V) {
   return N >= 0 && W >= 1 && W <= 64 && K >= 1 && K <= kMaxK && V >= 1 && V <= (1 << 20) &&
@@ -325,8 +377,7 @@ size_t qg_beam_workspace_size(int N, int W, int K, int64_t V) {
   if (!select_shape(N, W, K, V)) return 0;
   const qg::DeviceInfo &dev = qg::device_info();
   const long long rows = static_cast<long long>(N) * W;
-  const int slice = kThreads * slice_values(rows, V, dev.ok ? dev.sms : 152);
-  const size_t S = static_cast<size_t>((V + slice - 1) / slice);
+  const size_t S = static_cast<size_t>(make_slices(std::max(rows, 1LL), W, K, V, dev.ok ? dev.sms : 152).S);
   return (rows * S * 8 + 255) / 256 * 256 + rows * S * K * 8;
 }
 
@@ -344,9 +395,9 @@ qg_status qg_beam_select(const float *logits, const float *scores, const uint8_t
   if (!dev.ok) return QG_ECUDA;
   SelectArgs a = {};
   const long long rows = static_cast<long long>(N) * W;
-  const int pt = slice_values(rows, V, dev.sms);
-  a.slice = kThreads * pt;
-  a.S = static_cast<int>((V + a.slice - 1) / a.slice);
+  const Slices sl = make_slices(rows, W, K, V, dev.sms);
+  a.slice = sl.slice;
+  a.S = sl.S;
   a.logits = logits;
   a.scores = scores;
   a.done = done;
@@ -365,14 +416,10 @@ qg_status qg_beam_select(const float *logits, const float *scores, const uint8_t
   a.vec4 = V % 4 == 0 && qg::aligned16(logits);
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const dim3 grid(static_cast<unsigned>(a.S), static_cast<unsigned>(rows)), block(kThreads);
-  cudaError_t e;
-  if (pt == 8) e = qg::launch_pdl(select_slice_kernel<8>, grid, block, 0, s, a);
-  else if (pt == 16) e = qg::launch_pdl(select_slice_kernel<16>, grid, block, 0, s, a);
-  else e = qg::launch_pdl(select_slice_kernel<32>, grid, block, 0, s, a);
-  if (e != cudaSuccess) return QG_ECUDA;
-  const size_t smem = static_cast<size_t>(W) * K * 12;
-  if (smem > 48 * 1024 && !qg::set_smem_attr(reinterpret_cast<const void *>(select_merge_kernel), 64 * 64 * 12))
+  const size_t smem = merge_smem(W, K, a.S);
+  if (smem > 48 * 1024 && !qg::set_smem_attr(reinterpret_cast<const void *>(select_merge_kernel), static_cast<uint32_t>(smem)))
     return QG_ECUDA;
+  if (qg::launch_pdl(select_slice_kernel, grid, block, 0, s, a) != cudaSuccess) return QG_ECUDA;
   if (qg::launch_pdl(select_merge_kernel, dim3(static_cast<unsigned>(N)), dim3(kMergeThreads), smem, s, a) != cudaSuccess)
     return QG_ECUDA;
   return cudaGetLastError() == cudaSuccess ? QG_OK : QG_ECUDA;

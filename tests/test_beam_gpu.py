@@ -62,8 +62,8 @@ def check(qg, logits, scores, N, W, K, done=None, eos=-1):
     got, ref = select(qg, logits, scores, N, W, K, done, eos), ref_select(logits, scores, N, W, K, done, eos)
     assert torch.equal(got[1], ref[1]) and torch.equal(got[2], ref[2]), (got[1], ref[1], got[2], ref[2])
     assert torch.equal(got[3], ref[3])
-    # f32 sums of exponentials: a slice adds at most 32 values a thread and 8 + 5 partials within
-    # 2^-24 each, expf is within 2^-22; then the result's own rounding
+    # f32 sums of exponentials: a thread adds 16 values of each of at most 19 chunks here, and 5 + 16
+    # partials follow, each within 2^-24, expf within 2^-22; then the result's own rounding
     fin = torch.isfinite(ref[0])
     assert torch.equal(fin, torch.isfinite(got[0]))
     err = (got[0].double() - ref[0]).abs()[fin]
