@@ -13,6 +13,7 @@
 
 #include "qg_common.cuh"
 #include "qg_host.h"
+#include "qg_mma.cuh"
 
 namespace {
 
@@ -22,10 +23,9 @@ constexpr int kChunk = kThreads * kPT;
 constexpr int kMaxK = 64;
 constexpr int kList = 2048;              // candidates a slice holds
 
-// f32 -> unsigned that rises with the value; NaN counts as -inf
+// f32 (no NaN) -> unsigned that rises with the value; both zeros are one
 QG_DEVICE uint32_t ord_of(float x) {
-  if (isnan(x)) x = -INFINITY;
-  const uint32_t u = __float_as_uint(x);
+  const uint32_t u = __float_as_uint(x + 0.0f);
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 QG_DEVICE float ord_val(uint32_t o) { return __uint_as_float(o & 0x80000000u ? o & 0x7FFFFFFFu : ~o); }
@@ -49,13 +49,11 @@ struct SelectArgs {
   int N, W, K, S, eos, slice, vec4;
 };
 
+// largest key of the warp: the largest upper word, then the largest lower one beside it
 QG_DEVICE unsigned long long warp_max64(unsigned long long v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const unsigned long long u = __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    v = u > v ? u : v;
-  }
-  return v;
+  const uint32_t h = __reduce_max_sync(0xFFFFFFFFu, static_cast<uint32_t>(v >> 32));
+  const uint32_t l = __reduce_max_sync(0xFFFFFFFFu, static_cast<uint32_t>(v >> 32) == h ? static_cast<uint32_t>(v) : 0u);
+  return static_cast<unsigned long long>(h) << 32 | l;
 }
 
 // The slice's candidates and what it takes to thin them out to the K best, in falling order.
@@ -83,10 +81,11 @@ QG_DEVICE void thin(SliceShared &sh, int K) {  // by the whole CTA; keys differ,
 // Value i of thread t of a chunk is its element 4 (kThreads (i / 4) + t) + i % 4.
 QG_DEVICE int chunk_elem(int i) { return 4 * (kThreads * (i >> 2) + static_cast<int>(threadIdx.x)) + (i & 3); }
 QG_DEVICE void load_chunk(const SelectArgs &a, const float *x, int n, float (&v)[kPT]) {
+  const bool whole = a.vec4 && n >= kChunk;
 #pragma unroll
   for (int i = 0; i < kPT; i += 4) {
     const int e = chunk_elem(i);
-    if (a.vec4 && e + 4 <= n) {
+    if (whole || (a.vec4 && e + 4 <= n)) {
       const float4 q = __ldg(reinterpret_cast<const float4 *>(x + e));
       v[i] = q.x;
       v[i + 1] = q.y;
@@ -140,24 +139,29 @@ __global__ void __launch_bounds__(kThreads, 2) select_slice_kernel(const SelectA
   for (int c0 = 0; c0 < len; c0 += kChunk) {
     const int n = len - c0;
 #pragma unroll
-    for (int i = 0; i < kPT; ++i) v[i] = w[i] + 0.0f;  // -0 and +0 are one value
+    for (int i = 0; i < kPT; ++i) v[i] = fmaxf(w[i], -INFINITY);  // NaN counts as -inf
     if (c0 + kChunk < len) load_chunk(a, x + c0 + kChunk, n - kChunk, w);
     float mx = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < kPT; ++i) mx = fmaxf(mx, v[i]);  // fmaxf drops NaN
+    for (int i = 0; i < kPT; ++i) mx = fmaxf(mx, v[i]);
     const uint32_t mo = ord_of(mx);
     if (mx > m) {
       sum *= expf(m - mx);  // 0 from -inf (and of +inf - +inf never: mx > m)
       m = mx;
     }
     if (m > -INFINITY && m < INFINITY) {
-      float part = 0.f;
+      // 2^((x - m) log2 e), two values an instruction.  The exponent's rounding is relative to x - m, and
+      // a term's share of the sum falls faster than that grows: a few 2^-24 of the sum.
+      const f2 nm = mk2(-m, -m), l2e = mk2(1.4426950408889634f, 1.4426950408889634f);
+      f2 p0 = mk2(0.f, 0.f), p1 = p0;
 #pragma unroll
-      for (int i = 0; i < kPT; ++i) {
-        const float e = expf(v[i] - m);
-        part += isnan(v[i]) ? 0.f : e;
+      for (int i = 0; i < kPT; i += 4) {
+        const f2 y0 = mul2(add2(mk2(v[i], v[i + 1]), nm), l2e), y1 = mul2(add2(mk2(v[i + 2], v[i + 3]), nm), l2e);
+        p0 = add2(p0, mk2(ex2(y0.x), ex2(y0.y)));
+        p1 = add2(p1, mk2(ex2(y1.x), ex2(y1.y)));
       }
-      sum += part;
+      p0 = add2(p0, p1);
+      sum += p0.x + p0.y;
     }
     // ---- candidates.  A later value equal to the K-th best loses to it by its index.
     uint32_t t = full ? tau + 1u : 0u;
@@ -252,48 +256,56 @@ __global__ void __launch_bounds__(kThreads, 2) select_slice_kernel(const SelectA
 // can come next; lane q holds the heads of lists q, q + 32, ...), then all W*K candidates are
 // ranked against each other.
 constexpr int kMergeThreads = 512;
-constexpr int kMaxSlices = 128;
+constexpr int kMaxSlices = 128, kMaxW = 64;
 __global__ void __launch_bounds__(kMergeThreads) select_merge_kernel(const SelectArgs a) {
   extern __shared__ uint8_t smem[];
-  const int per_row = a.S * a.K;
-  unsigned long long *lists = reinterpret_cast<unsigned long long *>(smem);            // [W][S][K]
-  double *cand = reinterpret_cast<double *>(lists + static_cast<size_t>(a.W) * per_row);  // [W*K]
-  uint32_t *tok = reinterpret_cast<uint32_t *>(cand + static_cast<size_t>(a.W) * a.K);    // [W*K]
+  const int per_row = a.S * a.K, total = a.W * a.K;
+  unsigned long long *lists = reinterpret_cast<unsigned long long *>(smem);           // [W][S][K]
+  unsigned long long *rank = lists + static_cast<size_t>(a.W) * per_row;              // [W*K] order word of a candidate
+  float *val = reinterpret_cast<float *>(rank + total);                               // [W*K] its logit
+  uint32_t *tok = reinterpret_cast<uint32_t *>(val + total);                          // [W*K] its token
+  __shared__ float row_max[kMaxW], row_sum[kMaxW];
+  __shared__ double row_off[kMaxW];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nwarps = kMergeThreads / 32;
   pdl_wait();
   pdl_launch_dependents();
   const int req = blockIdx.x;
   for (int i = threadIdx.x; i < a.W * per_row; i += kMergeThreads)
     lists[i] = __ldcg(a.keys + static_cast<size_t>(req) * a.W * per_row + i);
-  __syncthreads();
   for (int w = warp; w < a.W; w += nwarps) {
-    const int row = req * a.W + w;
-    const float2 *ms = a.ms + static_cast<size_t>(row) * a.S;
-    float m = -INFINITY;
+    const float2 *ms = a.ms + static_cast<size_t>(req * a.W + w) * a.S;
+    float m = -INFINITY, sum = 0.f;
     for (int s = lane; s < a.S; s += 32) m = fmaxf(m, __ldcg(&ms[s]).x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-    double sum = 0.0;
     if (isfinite(m))
       for (int s = lane; s < a.S; s += 32) {
         const float2 p = __ldcg(&ms[s]);
-        if (p.y > 0.f) sum += static_cast<double>(p.y) * static_cast<double>(expf(p.x - m));
+        if (p.y > 0.f) sum += p.y * expf(p.x - m);
       }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    const float sc = __ldg(a.scores + row);
-    const bool none = !isfinite(m) || !isfinite(sc);  // no distribution, or a beam not continued
-    // candidate = off + (logit - m): a row of huge equal logits would absorb the rest otherwise
-    const double off = none ? 0.0 : static_cast<double>(sc) - log(sum);
-    const unsigned long long *kr = lists + w * per_row;
-    if (none) {
+    sum = warp_sum(sum);
+    if (lane == 0) {
+      row_max[w] = m;
+      row_sum[w] = sum;
+    }
+  }
+  __syncthreads();
+  // 64-bit arithmetic is scarce on this part: one warp's worth of logarithms, two sums a
+  // candidate, and integer comparisons of the results' order words
+  if (threadIdx.x < a.W)
+    row_off[threadIdx.x] = static_cast<double>(__ldg(a.scores + req * a.W + threadIdx.x)) -
+                           log(static_cast<double>(row_sum[threadIdx.x]));
+  for (int w = warp; w < a.W; w += nwarps) {
+    const float sc = __ldg(a.scores + req * a.W + w);
+    if (!isfinite(row_max[w]) || !isfinite(sc)) {  // no distribution, or a beam not continued
       for (int i = lane; i < a.K; i += 32) {
-        cand[w * a.K + i] = -INFINITY;
+        val[w * a.K + i] = -INFINITY;
         tok[w * a.K + i] = i < a.V ? static_cast<uint32_t>(i) : 0xFFFFFFFFu;
       }
       continue;
     }
     // lane's lists: positions and heads
+    const unsigned long long *kr = lists + w * per_row;
     constexpr int kHeads = kMaxSlices / 32;
     int at[kHeads];
     unsigned long long head[kHeads];
@@ -309,7 +321,7 @@ __global__ void __launch_bounds__(kMergeThreads) select_merge_kernel(const Selec
       for (int q = 0; q < kHeads; ++q) k = head[q] > k ? head[q] : k;
       k = warp_max64(k);
       if (lane == 0) {
-        cand[w * a.K + r] = k ? off + (static_cast<double>(key_val(k)) - static_cast<double>(m)) : -INFINITY;
+        val[w * a.K + r] = k ? key_val(k) : -INFINITY;
         tok[w * a.K + r] = k ? key_idx(k) : 0xFFFFFFFFu;
       }
       if (k) {
@@ -323,26 +335,34 @@ __global__ void __launch_bounds__(kMergeThreads) select_merge_kernel(const Selec
     }
   }
   __syncthreads();
-  const int total = a.W * a.K;
   for (int i = threadIdx.x; i < total; i += kMergeThreads) {
-    const double x = cand[i];
-    const uint32_t v = tok[i];
-    if (v == 0xFFFFFFFFu) continue;
     const int w = i / a.K;
+    // off + (logit - m): a row of huge equal logits would absorb the rest otherwise
+    const double x = val[i] == -INFINITY ? -INFINITY
+                                         : row_off[w] + (static_cast<double>(val[i]) - static_cast<double>(row_max[w]));
+    const unsigned long long u = static_cast<unsigned long long>(__double_as_longlong(x + 0.0));
+    // 0, below every real candidate, for a place without one
+    rank[i] = tok[i] == 0xFFFFFFFFu ? 0ull : u >> 63 ? ~u : u | 0x8000000000000000ull;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < total; i += kMergeThreads) {
+    const unsigned long long x = rank[i];
+    if (x == 0) continue;
+    const int w = i / a.K;
+    const uint32_t v = tok[i];
     int r = 0;
     for (int j = 0; j < total; ++j) {
-      const double y = cand[j];
-      if (y > x) {
-        ++r;
-      } else if (y == x) {
-        const uint32_t u = tok[j];
+      const unsigned long long y = rank[j];
+      r += y > x;
+      if (y == x && j != i) {  // equal: the lowest beam, then the lowest token
         const int wj = j / a.K;
-        if (u != 0xFFFFFFFFu && (wj < w || (wj == w && u < v))) ++r;
+        r += wj < w || (wj == w && tok[j] < v);
       }
     }
     if (r < a.K) {
       const size_t o = static_cast<size_t>(req) * a.K + r;
-      a.out_scores[o] = static_cast<float>(x);
+      const unsigned long long u = x >> 63 ? x & 0x7FFFFFFFFFFFFFFFull : ~x;
+      a.out_scores[o] = static_cast<float>(__longlong_as_double(static_cast<long long>(u)));
       a.parents[o] = w;
       a.tokens[o] = static_cast<int32_t>(v);
       if (a.done_out)
@@ -362,7 +382,7 @@ Slices make_slices(long long rows, long long W, long long K, long long V, int sm
   const long long slice = ((V + S - 1) / S + 3) / 4 * 4;
   return {static_cast<int>((V + slice - 1) / slice), static_cast<int>(slice)};
 }
-size_t merge_smem(int W, int K, int S) { return static_cast<size_t>(W) * K * (8 * static_cast<size_t>(S) + 12); }
+size_t merge_smem(int W, int K, int S) { return static_cast<size_t>(W) * K * (8 * static_cast<size_t>(S) + 16); }
 
 bool select_shape(int N, int W, int K, int64_t V) {
   return N >= 0 && W >= 1 && W <= 64 && K >= 1 && K <= kMaxK && V >= 1 && V <= (1 << 20) &&

@@ -397,8 +397,8 @@ QG_API qg_status qg_attn_paged(const qg_kv_cache *cache, const qg_kv_batch *batc
  *   - out_scores f32 [N][K], parents int32 [N][K] (w of the pick), tokens int32 [N][K], done_out
  *     u8 [N][K] or NULL: the parent had ended or the token is eos (eos < 0: no end token).
  *   - NaN logits and NaN or +inf scores count as -inf; a row whose largest logit is infinite has no
- *     distribution, its continuations are -inf.  Sums over the vocabulary are f32 per slice
- *     and joined in 64 bits; candidates are ranked in 64 bits.
+ *     distribution, its continuations are -inf.  Sums over the vocabulary are f32;
+ *     candidates are ranked in 64 bits.
  * 1 <= W <= 64, 1 <= K <= 64, K <= W*V, V <= 2^20, 0 <= N, N*W <= 65535.  Outputs may be the arrays of the
  * next call's inputs, not of this one's.  Workspace: beam_workspace_size bytes, 16-byte aligned. */
 QG_API size_t qg_beam_workspace_size(int N, int W, int K, int64_t V);

@@ -62,8 +62,9 @@ def check(qg, logits, scores, N, W, K, done=None, eos=-1):
     got, ref = select(qg, logits, scores, N, W, K, done, eos), ref_select(logits, scores, N, W, K, done, eos)
     assert torch.equal(got[1], ref[1]) and torch.equal(got[2], ref[2]), (got[1], ref[1], got[2], ref[2])
     assert torch.equal(got[3], ref[3])
-    # f32 sums of exponentials: a thread adds 16 values of each of at most 19 chunks here, and 5 + 16
-    # partials follow, each within 2^-24, expf within 2^-22; then the result's own rounding
+    # f32 sums of exponentials, in units of 2^-24: a thread's 16 values of a chunk in four sums (4 + 2), at
+    # most 19 chunks here, 5 + 16 partials; the exponential 4; its argument 1.5 log2(e) E[max - x]
+    # (mean under the distribution, 5 for these logits): 61.  Then the result's own rounding.
     fin = torch.isfinite(ref[0])
     assert torch.equal(fin, torch.isfinite(got[0]))
     err = (got[0].double() - ref[0]).abs()[fin]
