@@ -20,8 +20,10 @@ using qg::KvPool;
 // A row (one head of one token: D floats in, D 16-bit values out) is one warp's work; lane l
 // holds D/64 pairs, so a rotation never leaves its lane.  Angles: position * freq as a 64-bit
 // fraction of a turn (the product's overflow is whole turns), its top bits rounded once to
-// f32, then the sine and cosine of pi times twice that.  They depend on the token alone, so a
-// warp forms them once and uses them for its rows of all heads.
+// f32, then the sine and cosine of pi times twice that.  They depend on the token alone, as does
+// the search for its sequence, page and row: a warp does all that once for its rows, so with many
+// tokens (where bytes and then instructions are the bound) two warps share a token's rows, and
+// with few (where latency is) eight do and a token's rows spread over several blocks.
 struct AppendArgs {
   KvPool pool;
   KvBatch b;
@@ -31,10 +33,11 @@ struct AppendArgs {
   uint16_t *q_out;
   float eps;
   int Hq, rot, rows_per_block;
+  int wpt;  // warps per token: 2 or 8
 };
 
 constexpr int kAppendWarps = 8;
-constexpr int kAppendRows = 4;  // rows a warp has in flight
+constexpr int kAppendRows = 2;  // rows a warp works on while as many are under way (2: 78 us, 3: 82, 4: 80)
 
 template <int NP>
 struct Pairs {
@@ -93,10 +96,48 @@ __global__ void __launch_bounds__(kAppendWarps * 32) kv_append_kernel(const Appe
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
   pdl_launch_dependents();
-  const int t = blockIdx.x;
+  const int tpb = kAppendWarps / a.wpt, sub = warp % a.wpt;
+  const int t = static_cast<int>(blockIdx.x) * tpb + warp / a.wpt;
+  if (t >= a.b.T) return;
+  const bool teller = sub == 0 && lane == 0;
+  // this lane's pairs: those below rot/2 turn, the others (elements rot .. D-1) stay
+  const int p0 = NP * lane, hr = a.rot / 2;
+  int ea, eb;
+  if (PAIRS) {
+    ea = 2 * p0;
+    eb = 0;
+  } else if (p0 < hr) {
+    ea = p0;
+    eb = p0 + hr;
+  } else {
+    ea = a.rot + (p0 - hr);
+    eb = ea + (D - a.rot) / 2;
+  }
+  const int rows = a.Hq + 2 * a.pool.Hkv;
+  const int r_end = min(rows, (static_cast<int>(blockIdx.y) + 1) * a.rows_per_block);
+  auto load_rows = [&](int r0, Pairs<NP> (&x)[kAppendRows]) {
+#pragma unroll
+    for (int j = 0; j < kAppendRows; ++j) {
+      const int r = r0 + j * a.wpt;
+      if (r < r_end) {
+        const float *p = r < a.Hq ? a.q + t * a.q_stride + static_cast<long long>(r) * D
+                         : r < a.Hq + a.pool.Hkv
+                             ? a.k + t * a.k_stride + static_cast<long long>(r - a.Hq) * D
+                             : a.v + t * a.v_stride + static_cast<long long>(r - a.Hq - a.pool.Hkv) * D;
+        x[j] = load_pairs<NP, PAIRS>(p, ea, eb);
+      }
+    }
+  };
+  // the first rows are under way while the token's place is looked up (a chain of loads)
+  Pairs<NP> x[kAppendRows];
+  int r0 = static_cast<int>(blockIdx.y) * a.rows_per_block + sub;
+  load_rows(r0, x);
+  Pairs<NP> wq, wk;
+  if (a.q_norm) wq = load_pairs<NP, PAIRS>(a.q_norm, ea, eb);
+  if (a.k_norm) wk = load_pairs<NP, PAIRS>(a.k_norm, ea, eb);
   const int b = qg::kv_seq_of(a.b, t);
   if (b < 0) {
-    if (threadIdx.x == 0) atomicOr(&g_qg_status_kv, QG_STATUS_BIT_ID);
+    if (teller) atomicOr(&g_qg_status_kv, QG_STATUS_BIT_ID);
     return;
   }
   const int t0 = a.b.q_start ? __ldg(a.b.q_start + b) : b;
@@ -112,21 +153,8 @@ __global__ void __launch_bounds__(kAppendWarps * 32) kv_append_kernel(const Appe
     if (page >= 0 && page < a.pool.n_pages)
       row = page * a.pool.page_stride + (slot & ((1LL << shift) - 1)) * a.pool.token_stride;
   }
-  if (row < 0 && threadIdx.x == 0) atomicOr(&g_qg_status_kv, QG_STATUS_BIT_ID);
+  if (row < 0 && teller) atomicOr(&g_qg_status_kv, QG_STATUS_BIT_ID);
 
-  // this lane's pairs: those below rot/2 turn, the others (elements rot .. D-1) stay
-  const int p0 = NP * lane, hr = a.rot / 2;
-  int ea, eb;
-  if (PAIRS) {
-    ea = 2 * p0;
-    eb = 0;
-  } else if (p0 < hr) {
-    ea = p0;
-    eb = p0 + hr;
-  } else {
-    ea = a.rot + (p0 - hr);
-    eb = ea + (D - a.rot) / 2;
-  }
   float cs[NP], sn[NP];
   if (p0 < hr) {  // hr is a multiple of 4: a lane's pairs all turn or all stay
 #pragma unroll
@@ -137,38 +165,24 @@ __global__ void __launch_bounds__(kAppendWarps * 32) kv_append_kernel(const Appe
     }
   }
 
-  const int rows = a.Hq + 2 * a.pool.Hkv;
-  const int r_end = min(rows, (static_cast<int>(blockIdx.y) + 1) * a.rows_per_block);
-  for (int r0 = blockIdx.y * a.rows_per_block + warp; r0 < r_end; r0 += kAppendWarps * kAppendRows) {
-    Pairs<NP> x[kAppendRows];
+  for (; r0 < r_end; r0 += a.wpt * kAppendRows) {
+    Pairs<NP> next[kAppendRows];
+    load_rows(r0 + a.wpt * kAppendRows, next);
 #pragma unroll
     for (int j = 0; j < kAppendRows; ++j) {
-      const int r = r0 + j * kAppendWarps;
-      if (r < r_end) {
-        const float *p = r < a.Hq ? a.q + t * a.q_stride + static_cast<long long>(r) * D
-                         : r < a.Hq + a.pool.Hkv
-                             ? a.k + t * a.k_stride + static_cast<long long>(r - a.Hq) * D
-                             : a.v + t * a.v_stride + static_cast<long long>(r - a.Hq - a.pool.Hkv) * D;
-        x[j] = load_pairs<NP, PAIRS>(p, ea, eb);
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < kAppendRows; ++j) {
-      const int r = r0 + j * kAppendWarps;
+      const int r = r0 + j * a.wpt;
       if (r >= r_end) continue;
       const bool is_q = r < a.Hq, is_v = r >= a.Hq + a.pool.Hkv;
       if (!is_v) {
-        const float *w = is_q ? a.q_norm : a.k_norm;
-        if (w) {
+        if (is_q ? a.q_norm : a.k_norm) {
           float ss = 0.f;
 #pragma unroll
           for (int i = 0; i < NP; ++i) ss = fmaf(x[j].a[i], x[j].a[i], fmaf(x[j].b[i], x[j].b[i], ss));
-          const float s = 1.0f / sqrtf(warp_sum(ss) / static_cast<float>(D) + a.eps);
-          const Pairs<NP> wv = load_pairs<NP, PAIRS>(w, ea, eb);
+          const float s = rsqrtf(warp_sum(ss) * (1.0f / D) + a.eps);
 #pragma unroll
           for (int i = 0; i < NP; ++i) {
-            x[j].a[i] = x[j].a[i] * s * wv.a[i];
-            x[j].b[i] = x[j].b[i] * s * wv.b[i];
+            x[j].a[i] = x[j].a[i] * s * (is_q ? wq.a[i] : wk.a[i]);
+            x[j].b[i] = x[j].b[i] * s * (is_q ? wq.b[i] : wk.b[i]);
           }
         }
         if (p0 < hr) {
@@ -187,6 +201,8 @@ __global__ void __launch_bounds__(kAppendWarps * 32) kv_append_kernel(const Appe
         store_pairs<NP, PAIRS, BF16>((is_v ? a.pool.v : a.pool.k) + row + h * a.pool.head_stride, ea, eb, x[j]);
       }
     }
+#pragma unroll
+    for (int j = 0; j < kAppendRows; ++j) x[j] = next[j];
   }
 }
 
@@ -402,12 +418,16 @@ qg_status qg_kv_append(const qg_kv_cache *cache, const qg_kv_batch *batch, int H
   a.eps = eps;
   a.Hq = Hq;
   a.rot = rot;
-  // a block per token; with few tokens a token's rows go to several blocks, one row per warp
+  // two warps per token from eight tokens for every SM on (11604 tokens of 48 rows: 95 us with
+  // eight, 78 with two); with few tokens their rows go to several blocks, one row per warp
   const int rows = Hq + 2 * Hkv;
+  a.wpt = a.b.T >= 8 * dev.sms ? 2 : kAppendWarps;
   const int most = (rows + kAppendWarps - 1) / kAppendWarps;
-  const int gy = std::max(1, std::min(most, 2 * dev.sms / a.b.T));
+  const int gy = a.wpt == 2 ? 1 : std::max(1, std::min(most, 2 * dev.sms / a.b.T));
   a.rows_per_block = (rows + gy - 1) / gy;
-  const dim3 grid(static_cast<unsigned>(a.b.T), static_cast<unsigned>((rows + a.rows_per_block - 1) / a.rows_per_block));
+  const int tpb = kAppendWarps / a.wpt;
+  const dim3 grid(static_cast<unsigned>((a.b.T + tpb - 1) / tpb),
+                  static_cast<unsigned>((rows + a.rows_per_block - 1) / a.rows_per_block));
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool bf16 = cache->dtype == QG_DT_BF16;
   cudaError_t e;
