@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(NarrowCfg<D>::NW * 32, 1) attn_narrow_kernel(c
   const int qr = lane >> 2, qc = lane & 3;      // fragment row and column pair
   const int crow = lane / CH, cchunk = lane % CH;  // copy: row within an instruction, chunk
 
-  for (bool more = true; more; more = cursor_next(a, ln, &cur, end)) {
+  for (bool more = true; more; more = cursor_next(a, ln, scan, &cur, end)) {
     int j0, j1, n_tiles;
     cursor_tiles(ln, cur, at, end, &j0, &j1, &n_tiles);
     if (j0 >= j1) continue;
@@ -406,26 +406,43 @@ QG_DEVICE void write_row(const AttnArgs &a, int t, int hq, int lane, const Acc<D
   }
 }
 
-// ROW: one block of 8 warps per row, the row's pieces spread over the warps (few rows, many
-// pieces each); otherwise a warp per token, its lanes asking which heads need joining at all
-// (many rows, most of them written by their workers).
-template <int D, bool BF16, bool OUT32, bool ROW>
+// How the rows are shared out:
+//   kRowBlock    a block of 8 warps per row, the row's pieces spread over the warps: few rows with
+//                many pieces each;
+//   kRowWarp     a warp per row: a batch's decode step;
+//   kTokenWarp   a warp per token, its lanes asking which heads need joining at all: prompts, most
+//                of whose rows their workers wrote.
+enum { kRowBlock, kRowWarp, kTokenWarp };
+template <int D, bool BF16, bool OUT32, int MODE>
 __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ AttnArgs a) {
   constexpr int NV = D / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
   pdl_launch_dependents();
-  const int t = ROW ? static_cast<int>(blockIdx.x) / a.Hq : static_cast<int>(blockIdx.x) * 8 + warp;
+  const int item = MODE == kRowBlock ? static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x) * 8 + warp;
+  const int t = MODE == kTokenWarp ? item : item / a.Hq;
   if (t >= a.b.T) return;
   const int b = kv_seq_of(a.b, t);
   const int gr = b >= 0 ? kv_group_of(a.b, b) : -1;
-  if (b < 0 && (ROW ? threadIdx.x == 0 : lane == 0)) atomicOr(&g_qg_status_attn, QG_STATUS_BIT_ID);
+  if (b < 0 && lane == 0) atomicOr(&g_qg_status_attn, QG_STATUS_BIT_ID);
   RowSeg so, sp;
   so.l = sp.l = nullptr;
   if (b >= 0) so = row_seg(a, 2 * b + 1, t);
   if (gr >= 0 && !seq_long(a, b)) sp = row_seg(a, 2 * run_first(a, gr, b), t);
-  if constexpr (ROW) {
-    const int hq = static_cast<int>(blockIdx.x) % a.Hq;
+  if constexpr (MODE == kRowWarp) {
+    const int hq = item - t * a.Hq;
+    const Pieces own = pieces_of(so, hq / a.Gq, hq % a.Gq), pre = pieces_of(sp, hq / a.Gq, hq % a.Gq);
+    if (written(own, pre)) return;
+    Acc<NV> x;
+    x.m = -INFINITY;
+    x.l = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) x.o[i] = 0.f;
+    acc_pieces<D>(x, own, 0, 1, lane);
+    acc_pieces<D>(x, pre, 0, 1, lane);
+    write_row<D, BF16, OUT32>(a, t, hq, lane, x);
+  } else if constexpr (MODE == kRowBlock) {
+    const int hq = item - t * a.Hq;
     const Pieces own = pieces_of(so, hq / a.Gq, hq % a.Gq), pre = pieces_of(sp, hq / a.Gq, hq % a.Gq);
     if (written(own, pre)) return;
     __shared__ float sh[8][D];
@@ -550,11 +567,14 @@ qg_status attn_run(const AttnArgs &a, int sms, cudaStream_t s) {
   }
   const long long rows = static_cast<long long>(a.b.T) * a.Hq;
   cudaError_t e;
-  if (rows <= 8192)
-    e = launch_pdl(attn_join_kernel<D, BF16, OUT32, true>, dim3(static_cast<unsigned>(rows)), dim3(256), 0, s, a);
+  // 2048 rows of about 20 pieces: 30 us with a block per row, XX with a warp
+  if (rows <= 3LL * sms)
+    e = launch_pdl(attn_join_kernel<D, BF16, OUT32, kRowBlock>, dim3(static_cast<unsigned>(rows)), dim3(256), 0, s, a);
+  else if (rows <= 8192)
+    e = launch_pdl(attn_join_kernel<D, BF16, OUT32, kRowWarp>, dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0, s, a);
   else
-    e = launch_pdl(attn_join_kernel<D, BF16, OUT32, false>, dim3(static_cast<unsigned>((a.b.T + 7) / 8)), dim3(256), 0, s,
-                   a);
+    e = launch_pdl(attn_join_kernel<D, BF16, OUT32, kTokenWarp>, dim3(static_cast<unsigned>((a.b.T + 7) / 8)), dim3(256), 0,
+                   s, a);
   if (e != cudaSuccess) return QG_ECUDA;
   return cudaGetLastError() == cudaSuccess ? QG_OK : QG_ECUDA;
 }

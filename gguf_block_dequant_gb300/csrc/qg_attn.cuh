@@ -163,6 +163,7 @@ template <int NT>
 struct LineScan {
   long long pos[NT + 1];
   int unit[NT + 1];
+  Seg seg[NT];  // the thread's segment, where each thread owns one
 };
 
 template <int NT>
@@ -174,6 +175,7 @@ QG_DEVICE long long line_scan(const AttnArgs &a, const Line &l, LineScan<NT> *sc
   int u = 0;
   for (int s = s0; s < s1; ++s) {
     const Seg g = seg_load(a, s);
+    if (chunk == 1) sc->seg[s] = g;
     if (!seg_in(l, g)) continue;
     const int rt = seg_tiles(l, g);
     c += a.pool.Hkv * seg_cost_to(l, g, rt);
@@ -217,6 +219,7 @@ QG_DEVICE long long line_scan(const AttnArgs &a, const Line &l, LineScan<NT> *sc
     for (int s = s0; s < s1; ++s) {
       l.seg_pos[s] = p;
       l.seg_unit[s] = uu;
+      if (chunk == 1) continue;
       const Seg g = seg_load(a, s);
       if (!seg_in(l, g)) continue;
       const int rt = seg_tiles(l, g);
@@ -243,10 +246,11 @@ struct Cursor {
 };
 
 // to the first unit of a segment at or after s (pos and unit are those of s)
-QG_DEVICE bool cursor_seg(const AttnArgs &a, const Line &l, Cursor *c, int s) {
+template <int NT>
+QG_DEVICE bool cursor_seg(const AttnArgs &a, const Line &l, const LineScan<NT> &sc, Cursor *c, int s) {
   const int nseg = 2 * a.b.B;
   for (; s < nseg; ++s) {
-    c->g = seg_load(a, s);
+    c->g = nseg <= NT ? sc.seg[s] : seg_load(a, s);
     if (!seg_in(l, c->g)) continue;
     c->s = s;
     c->rt = seg_tiles(l, c->g);
@@ -258,13 +262,14 @@ QG_DEVICE bool cursor_seg(const AttnArgs &a, const Line &l, Cursor *c, int s) {
 }
 // to the next unit; false when the part of the line that ends at `end` has no more (asked first:
 // a walk over the empty segments at the end of the line is a chain of loads)
-QG_DEVICE bool cursor_next(const AttnArgs &a, const Line &l, Cursor *c, long long end) {
+template <int NT>
+QG_DEVICE bool cursor_next(const AttnArgs &a, const Line &l, const LineScan<NT> &sc, Cursor *c, long long end) {
   if (c->pos + c->x >= end) return false;
   c->pos += c->x;
   ++c->unit;
   if (++c->r == c->rt) {
     c->r = 0;
-    if (++c->h == a.pool.Hkv) return cursor_seg(a, l, c, c->s + 1);
+    if (++c->h == a.pool.Hkv) return cursor_seg(a, l, sc, c, c->s + 1);
   }
   c->x = unit_keys(l, c->g, c->r);
   return true;
@@ -281,14 +286,14 @@ QG_DEVICE bool cursor_find(const AttnArgs &a, const Line &l, const LineScan<NT> 
   const int chunk = (2 * a.b.B + NT - 1) / NT;
   c->pos = sc.pos[lo];
   c->unit = sc.unit[lo];
-  if (!cursor_seg(a, l, c, lo * chunk)) return false;
+  if (!cursor_seg(a, l, sc, c, lo * chunk)) return false;
   long long cost;
   while (true) {  // the segment
     cost = seg_cost_to(l, c->g, c->rt);
     if (c->pos + a.pool.Hkv * cost > at) break;
     c->pos += a.pool.Hkv * cost;
     c->unit += a.pool.Hkv * c->rt;
-    if (!cursor_seg(a, l, c, c->s + 1)) return false;
+    if (!cursor_seg(a, l, sc, c, c->s + 1)) return false;
   }
   c->h = static_cast<int>((at - c->pos) / cost);
   c->pos += c->h * cost;

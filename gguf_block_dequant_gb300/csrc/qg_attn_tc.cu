@@ -40,15 +40,18 @@ constexpr int kThreads = 12 * 32;
 constexpr int kRegs = 168, kRegsSoft = 208, kRegsRest = 88;
 static_assert(2 * kRegsSoft + kRegsRest <= 3 * kRegs, "the warpgroups' shares come from the launch's total");
 
+constexpr uint32_t SCAN_BYTES = (sizeof(LineScan<kThreads>) + 15) / 16 * 16;
+
 template <int D>
 struct WideCfg {
   static constexpr uint32_t HALF = 128 * 128;             // bytes of 128 rows x 64 elements
   static constexpr uint32_t TILE = HALF * (D / 64);       // a key, value or query tile
-  static constexpr int NST = D == 64 ? 8 : 5;
+  static constexpr int NST = D == 64 ? 8 : 4;
   static constexpr uint32_t OFF_Q = 0;
   static constexpr uint32_t OFF_KV = 2 * TILE;
   static constexpr uint32_t OFF_BAR = OFF_KV + NST * TILE;
-  static constexpr uint32_t SMEM = OFF_BAR + 256 + 1024;  // + alignment slack
+  static constexpr uint32_t OFF_SCAN = OFF_BAR + 256;
+  static constexpr uint32_t SMEM = OFF_SCAN + SCAN_BYTES + 1024;  // + alignment slack
   static constexpr uint32_t COLS = 512;                   // S0 S1 (128 each), O0 O1 (D each)
 };
 
@@ -83,7 +86,9 @@ struct Piece {
   bool alone;      // the piece is all there is of its rows
   size_t slot;
 };
+using Scan = LineScan<kThreads>;
 struct Walk {
+  const Scan *scan;
   Cursor cur;
   long long at, end;
   int w;
@@ -105,7 +110,7 @@ QG_DEVICE bool walk_next(const AttnArgs &a, Walk *k, Piece *p) {
       p->alone = p->paired && p->j0 == 0 && p->j1 == n && seg_whole(a, c.g, c.s >> 1);
       p->slot = static_cast<size_t>(c.unit) + static_cast<size_t>(k->w);
     }
-    if (!cursor_next(a, l, &c, k->end)) c.pos = k->end;
+    if (!cursor_next(a, l, *k->scan, &c, k->end)) c.pos = k->end;
     if (some) return true;
   }
   return false;
@@ -482,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const __grid_con
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   WideBars *bar = reinterpret_cast<WideBars *>(smem + C::OFF_BAR);
-  LineScan<kThreads> *scan = reinterpret_cast<LineScan<kThreads> *>(smem);  // before any tile
+  Scan *scan = reinterpret_cast<Scan *>(smem + C::OFF_SCAN);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::NST; ++i) {
@@ -507,13 +512,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const __grid_con
   const long long total = line_scan<kThreads>(a, ln, scan, blockIdx.x == 0);
   const int nw = line_workers(ln, total);
   Walk walk;
+  walk.scan = scan;
   walk.w = static_cast<int>(blockIdx.x);
   if (total == 0 || walk.w >= nw) return;
   walk.at = line_start(walk.w, total, nw);
   walk.end = line_start(walk.w + 1, total, nw);
   if (walk.at >= walk.end || !cursor_find(a, ln, *scan, walk.at, &walk.cur)) return;  // the same for the whole block
   if (warp == kMmaWarp) tmem_alloc(&bar->tmem, C::COLS);
-  fence_proxy_async_smem();  // the scan's words make way for tiles
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
