@@ -57,8 +57,8 @@ __global__ void __launch_bounds__(NarrowCfg<D>::NW * 32, 1) attn_narrow_kernel(c
   const int nw = line_workers(ln, total);
   const int w = warp * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
   if (w >= nw) return;
-  const long long at = line_start(w, total, nw);
-  const long long end = line_start(w + 1, total, nw);
+  const Cut cut = line_cut(total, nw);
+  const long long at = line_start(cut, w), end = line_start(cut, w + 1);
   if (at >= end) return;
   Cursor cur;
   if (!cursor_find(a, ln, scan, at, &cur)) return;
@@ -264,8 +264,8 @@ __global__ void __launch_bounds__(NarrowCfg<D>::NW * 32, 1) attn_narrow_kernel(c
 struct RowSeg {
   const Line *l;            // null: no keys there
   long long p0, cost;       // place of head 0's unit, places per head
-  long long total;
-  int unit, rt, x, nw;      // head 0's unit, units per head, keys of a unit, workers
+  Cut cut;                  // the line's parts
+  int unit, rt, x;          // head 0's unit, units per head, keys of a unit
   int row, halves;          // first row in the tile; 2: each slot holds two partial results of a row
 };
 
@@ -280,8 +280,8 @@ QG_DEVICE RowSeg row_seg(const AttnArgs &a, int s, int t) {
   q.x = unit_keys(l, g, r);
   if (q.x == 0) return q;
   q.l = &l;
-  q.total = l.seg_pos[2 * a.b.B];
-  q.nw = line_workers(l, q.total);
+  const long long total = l.seg_pos[2 * a.b.B];
+  q.cut = line_cut(total, line_workers(l, total));
   q.rt = seg_tiles(l, g);
   q.p0 = l.seg_pos[s] + seg_cost_to(l, g, r);
   q.cost = seg_cost_to(l, g, q.rt);
@@ -313,10 +313,10 @@ QG_DEVICE Pieces pieces_of(const RowSeg &q, int h, int gq) {
   if (!q.l) return p;
   const Line &l = *q.l;
   const long long p0 = q.p0 + h * q.cost;
-  const int w0 = line_owner(p0, q.total, q.nw);
-  int w1 = line_owner(p0 + q.x - 1, q.total, q.nw);
+  const int w0 = line_owner(q.cut, p0);
+  int w1 = line_owner(q.cut, p0 + q.x - 1);
   // the last one's part may lie within the last key tile, which is then its neighbour's
-  if (w1 > w0 && tiles_of(l, static_cast<int>(line_start(w1, q.total, q.nw) - p0)) >= tiles_of(l, q.x)) --w1;
+  if (w1 > w0 && tiles_of(l, static_cast<int>(line_start(q.cut, w1) - p0)) >= tiles_of(l, q.x)) --w1;
   p.o = l.part_o;
   p.ml = l.part_ml;
   p.first = static_cast<size_t>(q.unit + h * q.rt) + static_cast<size_t>(w0);

@@ -8,8 +8,8 @@
 // of a segment and a cached head are its (token, query head of that cached head) pairs; they
 // are cut into ROW TILES of `tpt` whole tokens.  A UNIT is (segment, cached head, row tile),
 // and its cost is the number of keys its last row sees.  All units in (segment, head, row
-// tile) order, key by key, form one LINE; worker w of n takes the part
-// [w*total/n, (w+1)*total/n) of it, its ends raised to whole key tiles of their units.  So ragged
+// tile) order, key by key, form one LINE; worker w of n takes the w-th of n
+// equal parts of it, the part's ends raised to whole key tiles of their units.  So ragged
 // lengths balance without the host knowing them, and every kernel can work out from the lengths
 // alone who did what: costs in keys rather than tiles make a segment's cost an arithmetic series
 // (the sum of rounded-up tile counts took tens of thousands of cycles to invert).  A worker's
@@ -136,9 +136,35 @@ QG_DEVICE int line_workers(const Line &l, long long total) {
   const long long n = (total + (kMinTiles << l.kshift) - 1) / (kMinTiles << l.kshift);
   return n < l.workers ? static_cast<int>(n) : l.workers;
 }
-QG_DEVICE long long line_start(long long w, long long total, int n) { return w * total / n; }
-QG_DEVICE int line_owner(long long p, long long total, int n) {
-  return static_cast<int>(((p + 1) * n + total - 1) / total - 1);
+// quotient of non-negative numbers, in 32 bits where they fit (a 64-bit division is a call)
+QG_DEVICE long long div_pos(long long x, long long y) {
+  if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
+  return x / y;
+}
+// The line cut into n parts: part w starts at floor(w * total / n), evenly spread, so that equal
+// units end where parts do whenever their numbers allow it.
+struct Cut {
+  long long size, total;
+  int rest, n;
+};
+QG_DEVICE Cut line_cut(long long total, int n) {
+  Cut c;
+  c.n = n;
+  c.total = total;
+  c.size = div_pos(total, n);
+  c.rest = static_cast<int>(total - c.size * n);
+  return c;
+}
+QG_DEVICE long long line_start(const Cut &c, int w) {
+  return w * c.size + static_cast<uint32_t>(w * c.rest) / static_cast<uint32_t>(c.n);
+}
+QG_DEVICE int line_owner(const Cut &c, long long p) {
+  // the estimate's relative error is a few 2^-24 and there are a few thousand workers at most
+  int w = static_cast<int>(static_cast<float>(p) * (static_cast<float>(c.n) / static_cast<float>(c.total)));
+  w = min(w, c.n - 1);
+  while (w > 0 && line_start(c, w) > p) --w;
+  while (w + 1 < c.n && line_start(c, w + 1) <= p) ++w;
+  return w;
 }
 
 // keys of the segment's (own) list that token t sees (t in the segment's token rows)
@@ -159,11 +185,12 @@ QG_DEVICE int row_prefix_limit(const Seg &g, int t) {
 // ---- the block's view of a line ---------------------------------------------------------------
 // Thread i of the block owns segments [i*chunk, (i+1)*chunk); pos[i], unit[i] are the line's
 // keys and units before them.  Filled by all threads of the block.
+constexpr int kKeptSegs = 128;
 template <int NT>
 struct LineScan {
   long long pos[NT + 1];
   int unit[NT + 1];
-  Seg seg[NT];  // the thread's segment, where each thread owns one
+  Seg seg[kKeptSegs];  // the segments themselves, where there are no more (a thread owns one each)
 };
 
 template <int NT>
@@ -175,7 +202,7 @@ QG_DEVICE long long line_scan(const AttnArgs &a, const Line &l, LineScan<NT> *sc
   int u = 0;
   for (int s = s0; s < s1; ++s) {
     const Seg g = seg_load(a, s);
-    if (chunk == 1) sc->seg[s] = g;
+    if (nseg <= kKeptSegs) sc->seg[s] = g;
     if (!seg_in(l, g)) continue;
     const int rt = seg_tiles(l, g);
     c += a.pool.Hkv * seg_cost_to(l, g, rt);
@@ -219,7 +246,7 @@ QG_DEVICE long long line_scan(const AttnArgs &a, const Line &l, LineScan<NT> *sc
     for (int s = s0; s < s1; ++s) {
       l.seg_pos[s] = p;
       l.seg_unit[s] = uu;
-      if (chunk == 1) continue;
+      if (chunk == 1) continue;  // nothing of this thread's follows
       const Seg g = seg_load(a, s);
       if (!seg_in(l, g)) continue;
       const int rt = seg_tiles(l, g);
@@ -250,7 +277,7 @@ template <int NT>
 QG_DEVICE bool cursor_seg(const AttnArgs &a, const Line &l, const LineScan<NT> &sc, Cursor *c, int s) {
   const int nseg = 2 * a.b.B;
   for (; s < nseg; ++s) {
-    c->g = nseg <= NT ? sc.seg[s] : seg_load(a, s);
+    c->g = nseg <= kKeptSegs ? sc.seg[s] : seg_load(a, s);
     if (!seg_in(l, c->g)) continue;
     c->s = s;
     c->rt = seg_tiles(l, c->g);
@@ -295,7 +322,7 @@ QG_DEVICE bool cursor_find(const AttnArgs &a, const Line &l, const LineScan<NT> 
     c->unit += a.pool.Hkv * c->rt;
     if (!cursor_seg(a, l, sc, c, c->s + 1)) return false;
   }
-  c->h = static_cast<int>((at - c->pos) / cost);
+  c->h = static_cast<int>(div_pos(at - c->pos, cost));
   c->pos += c->h * cost;
   lo = 0, hi = c->rt;  // the last row tile that starts at or before `at`
   while (hi - lo > 1) {

@@ -40,6 +40,11 @@ constexpr int kThreads = 12 * 32;
 constexpr int kRegs = 168, kRegsSoft = 208, kRegsRest = 88;
 static_assert(2 * kRegsSoft + kRegsRest <= 3 * kRegs, "the warpgroups' shares come from the launch's total");
 
+// epilogue staging: 32 rows of 64 bytes per softmax warp, 80 bytes apart
+constexpr uint32_t kStagePitch = 80, kStageBytes = 32 * kStagePitch;
+QG_DEVICE void sts_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
 constexpr uint32_t SCAN_BYTES = (sizeof(LineScan<kThreads>) + 15) / 16 * 16;
 
 template <int D>
@@ -51,7 +56,9 @@ struct WideCfg {
   static constexpr uint32_t OFF_KV = 2 * TILE;
   static constexpr uint32_t OFF_BAR = OFF_KV + NST * TILE;
   static constexpr uint32_t OFF_SCAN = OFF_BAR + 256;
-  static constexpr uint32_t SMEM = OFF_SCAN + SCAN_BYTES + 1024;  // + alignment slack
+  static constexpr uint32_t OFF_STAGE = OFF_SCAN + SCAN_BYTES;
+  static constexpr uint32_t SMEM = OFF_STAGE + kSoftWarps * kStageBytes + 1024;  // + alignment slack
+  static_assert(SMEM <= 226 * 1024, "one CTA's shared memory");
   static constexpr uint32_t COLS = 512;                   // S0 S1 (128 each), O0 O1 (D each)
 };
 
@@ -338,7 +345,7 @@ QG_DEVICE void issue_mma(const AttnArgs &a, Walk walk, uint32_t smem, WideBars *
 
 // ---- softmax ----------------------------------------------------------------------------------
 template <int D, bool BF16, bool OUT32>
-QG_DEVICE void softmax(const AttnArgs &a, Walk walk, WideBars *bar, int s, int warp4, int lane) {
+QG_DEVICE void softmax(const AttnArgs &a, Walk walk, WideBars *bar, int s, int warp4, int lane, uint32_t stage) {
   volatile int *abort = &bar->abort;
   const uint32_t lanes = static_cast<uint32_t>(32 * warp4) << 16;
   const uint32_t ts = bar->tmem + lanes + 128u * s, to = bar->tmem + lanes + 256u + D * s;
@@ -450,28 +457,49 @@ QG_DEVICE void softmax(const AttnArgs &a, Walk walk, WideBars *bar, int s, int w
     }
     const float inv = p.alone ? (l > 0.f ? 1.0f / l : 0.f) : 1.0f;
     const size_t prow = p.slot * kWideRows + s * kWideHalf + row;
-    const size_t orow = (static_cast<size_t>(t) * a.Hq + p.h * a.Gq + (valid ? row % a.Gq : 0)) * D;
     if (valid && !p.alone) a.wide.part_ml[prow] = make_float2(m == -INFINITY ? m : m * sl, l);
     if (any) {
+      const bool wide_out = !p.alone || OUT32;  // f32 values; otherwise 16-bit ones
+      const size_t orow = (static_cast<size_t>(t) * a.Hq + p.h * a.Gq + (valid ? row % a.Gq : 0)) * D;
+      uint8_t *mine = nullptr;
+      if (valid)
+        mine = !p.alone ? reinterpret_cast<uint8_t *>(a.wide.part_o + prow * D)
+               : OUT32  ? reinterpret_cast<uint8_t *>(static_cast<float *>(a.out) + orow)
+                        : reinterpret_cast<uint8_t *>(static_cast<uint16_t *>(a.out) + orow);
+      // 64 bytes of every row at a time through the warp's staging rows, so that four lanes write
+      // a row's 64 bytes together: a thread writing its own row costs a cache line per lane and
+      // store, and held up every other warp's loads for thousands of cycles
+      uint8_t *dst[4];
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
+      for (int i = 0; i < 4; ++i)
+        dst[i] = reinterpret_cast<uint8_t *>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(mine), 8 * i + (lane >> 2)));
+      const uint32_t put = stage + lane * kStagePitch, get = stage + (lane >> 2) * kStagePitch + (lane & 3) * 16;
+      const int cols = wide_out ? 16 : 32;
+#pragma unroll 1
+      for (int c = 0; c < D; c += cols) {
         float o[32];
-        tmem_ld32(to + 32 * c, o);
-        if (valid) {
-          if (!p.alone || OUT32) {
-            float4 *dst = reinterpret_cast<float4 *>((p.alone ? static_cast<float *>(a.out) + orow
-                                                              : a.wide.part_o + prow * D) + 32 * c);
+        uint32_t q[16];
+        tmem_ld16(to + c, reinterpret_cast<float(&)[16]>(o[0]));
+        if (wide_out) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 4)
-              dst[i / 4] = make_float4(o[i] * inv, o[i + 1] * inv, o[i + 2] * inv, o[i + 3] * inv);
-          } else {
-            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + orow + 32 * c);
+          for (int i = 0; i < 16; ++i) q[i] = __float_as_uint(o[i] * inv);
+        } else {
+          tmem_ld16(to + c + 16, reinterpret_cast<float(&)[16]>(o[16]));
 #pragma unroll
-            for (int i = 0; i < 32; i += 8)
-              dst[i / 8] = make_uint4(pack16<BF16>(o[i] * inv, o[i + 1] * inv), pack16<BF16>(o[i + 2] * inv, o[i + 3] * inv),
-                                      pack16<BF16>(o[i + 4] * inv, o[i + 5] * inv), pack16<BF16>(o[i + 6] * inv, o[i + 7] * inv));
+          for (int i = 0; i < 16; ++i) q[i] = pack16<BF16>(o[2 * i] * inv, o[2 * i + 1] * inv);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sts_v4(put + 16 * i, q[4 * i], q[4 * i + 1], q[4 * i + 2], q[4 * i + 3]);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint4 v = lds_v4(get + 8 * i * kStagePitch);
+          if (dst[i]) {
+            *reinterpret_cast<uint4 *>(dst[i] + (lane & 3) * 16) = v;
+            dst[i] += 64;
           }
         }
+        __syncwarp();
       }
       tc_fence_before();
       __syncwarp();
@@ -515,8 +543,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const __grid_con
   walk.scan = scan;
   walk.w = static_cast<int>(blockIdx.x);
   if (total == 0 || walk.w >= nw) return;
-  walk.at = line_start(walk.w, total, nw);
-  walk.end = line_start(walk.w + 1, total, nw);
+  const Cut cut = line_cut(total, nw);
+  walk.at = line_start(cut, walk.w);
+  walk.end = line_start(cut, walk.w + 1);
   if (walk.at >= walk.end || !cursor_find(a, ln, *scan, walk.at, &walk.cur)) return;  // the same for the whole block
   if (warp == kMmaWarp) tmem_alloc(&bar->tmem, C::COLS);
   tc_fence_before();
@@ -525,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const __grid_con
   const uint32_t sb = smem_u32(smem);
   if (warp < kSoftWarps) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
-    softmax<D, BF16, OUT32>(a, walk, bar, warp >> 2, warp & 3, lane);
+    softmax<D, BF16, OUT32>(a, walk, bar, warp >> 2, warp & 3, lane, sb + C::OFF_STAGE + warp * kStageBytes);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
     if (warp == kMmaWarp) {
