@@ -10,7 +10,9 @@
 //   warp 9          the TMA producer: query tiles, and key and value tiles gathered page by page
 //                   (a box is 64 elements of the rows a page has in the tile) into
 //                   128-byte-swizzled shared memory;
-//   warps 10, 11    idle: they complete the warpgroup whose registers the softmax warps take over
+//   warp 10         walks the CTA's part of the line and leaves each piece's description in a small
+//                   ring, so that the others keep none of that in registers;
+//   warp 11         idle: it completes the warpgroup whose registers the softmax warps take over
 //                   (a thread holds its row's 128 scores).
 // Two streams keep the tensor cores busy during the exponentials.  With more than 128 rows the
 // streams take 128 rows each and share every key tile; with fewer they take the key tiles in
@@ -34,7 +36,8 @@ namespace {
 
 using namespace qg;
 
-constexpr int kSoftWarps = 8, kMmaWarp = 8, kProdWarp = 9;
+constexpr int kSoftWarps = 8, kMmaWarp = 8, kProdWarp = 9, kWalkWarp = 10;
+constexpr int kPieces = 2;  // descriptions in the ring
 constexpr int kThreads = 12 * 32;
 // registers: launched with 168 a thread; two warpgroups go up to 208, the third down to 88
 constexpr int kRegs = 168, kRegsSoft = 208, kRegsRest = 88;
@@ -55,7 +58,7 @@ struct WideCfg {
   static constexpr uint32_t OFF_Q = 0;
   static constexpr uint32_t OFF_KV = 2 * TILE;
   static constexpr uint32_t OFF_BAR = OFF_KV + NST * TILE;
-  static constexpr uint32_t OFF_SCAN = OFF_BAR + 256;
+  static constexpr uint32_t OFF_SCAN = OFF_BAR + 512;
   static constexpr uint32_t OFF_STAGE = OFF_SCAN + SCAN_BYTES;
   static constexpr uint32_t SMEM = OFF_STAGE + kSoftWarps * kStageBytes + 1024;  // + alignment slack
   static_assert(SMEM <= 226 * 1024, "one CTA's shared memory");
@@ -75,15 +78,7 @@ struct Ring {
   }
 };
 
-struct WideBars {
-  uint64_t full[8], empty[8];
-  uint64_t q_full, q_empty, tail;
-  uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];
-  uint32_t tmem;
-  int abort;
-};
-
-// A worker's part of one unit, as every role of the CTA works it out for itself.
+// A worker's part of one unit (j0 == j1: there is no more).
 struct Piece {
   Seg g;
   int h, t0;       // cached head, first token row of the unit
@@ -93,6 +88,16 @@ struct Piece {
   bool alone;      // the piece is all there is of its rows
   size_t slot;
 };
+struct WideBars {
+  Piece piece[kPieces];
+  uint64_t piece_full[kPieces], piece_empty[kPieces];
+  uint64_t full[8], empty[8];
+  uint64_t q_full, q_empty, tail;
+  uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];
+  uint32_t tmem;
+  int abort;
+};
+
 using Scan = LineScan<kThreads>;
 struct Walk {
   const Scan *scan;
@@ -143,6 +148,35 @@ QG_DEVICE bool warp_wait(uint64_t *b, uint32_t parity, volatile int *abort) {
   return __all_sync(0xFFFFFFFFu, clock_wait(b, parity, abort));
 }
 
+// ---- the walk -----------------------------------------------------------------------------------
+QG_DEVICE void walk_line(const AttnArgs &a, Walk walk, WideBars *bar, int lane) {
+  volatile int *abort = &bar->abort;
+  for (uint32_t n = 0;; ++n) {
+    Piece p;
+    const bool more = walk_next(a, &walk, &p);
+    if (!more) p.j0 = p.j1 = 0;
+    const uint32_t i = n % kPieces;
+    if (!warp_wait(&bar->piece_empty[i], ((n / kPieces) & 1) ^ 1, abort)) return;
+    if (lane == 0) {
+      bar->piece[i] = p;
+      mbar_arrive(&bar->piece_full[i]);
+    }
+    __syncwarp();
+    if (!more) return;
+  }
+}
+// the n-th piece, nullptr at the end (or after an abort)
+QG_DEVICE const Piece *piece_get(WideBars *bar, uint32_t n) {
+  const uint32_t i = n % kPieces;
+  if (!warp_wait(&bar->piece_full[i], (n / kPieces) & 1, &bar->abort)) return nullptr;
+  const Piece *p = &bar->piece[i];
+  return p->j0 < p->j1 ? p : nullptr;
+}
+QG_DEVICE void piece_done(WideBars *bar, uint32_t n, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&bar->piece_empty[n % kPieces]);
+}
+
 // ---- producer ---------------------------------------------------------------------------------
 QG_DEVICE void tma_4d(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, int c3, uint64_t *bar) {
   asm volatile(
@@ -166,7 +200,7 @@ struct WideMaps {
 };
 
 template <int D>
-QG_DEVICE void produce(const AttnArgs &a, const WideMaps &maps, Walk walk, uint8_t *smem, WideBars *bar, int lane) {
+QG_DEVICE void produce(const AttnArgs &a, const WideMaps &maps, uint8_t *smem, WideBars *bar, int lane) {
   using C = WideCfg<D>;
   constexpr int H = D / 64;              // 64-element halves of a row
   volatile int *abort = &bar->abort;
@@ -175,10 +209,10 @@ QG_DEVICE void produce(const AttnArgs &a, const WideMaps &maps, Walk walk, uint8
   const int bshift = min(shift, 7), rows = 1 << bshift;  // rows of a box
   const int half = a.wide.tpt / 2;
   Ring<C::NST> ring;
-  int np = 0, ntail = 0;
-  Piece p;
-  for (; walk_next(a, &walk, &p); ++np) {
-    if (!warp_wait(&bar->q_empty, static_cast<uint32_t>((np & 1) ^ 1), abort)) return;
+  uint32_t np = 0, ntail = 0;
+  for (const Piece *pp; (pp = piece_get(bar, np)) != nullptr; piece_done(bar, np++, lane)) {
+    const Piece p = *pp;
+    if (!warp_wait(&bar->q_empty, (np & 1) ^ 1, abort)) return;
     const int ns = p.paired ? 2 : 1;
     if (lane == 0) mbar_arrive_expect_tx(&bar->q_full, static_cast<uint32_t>(ns * H * half * a.Gq) * 128u);
     __syncwarp();
@@ -243,7 +277,7 @@ QG_DEVICE void produce(const AttnArgs &a, const WideMaps &maps, Walk walk, uint8
 
 // ---- MMA issue --------------------------------------------------------------------------------
 template <int D, bool BF16, bool OUT32>
-QG_DEVICE void issue_mma(const AttnArgs &a, Walk walk, uint32_t smem, WideBars *bar) {
+QG_DEVICE void issue_mma(uint32_t smem, WideBars *bar, int lane) {
   using C = WideCfg<D>;
   constexpr uint32_t id_s = make_idesc16(128, kWideKeys, BF16, false), id_o = make_idesc16(128, D, BF16, true);
   volatile int *abort = &bar->abort;
@@ -253,7 +287,7 @@ QG_DEVICE void issue_mma(const AttnArgs &a, Walk walk, uint32_t smem, WideBars *
     tc_fence_after();
     return r;
   };
-  int np = 0;
+  uint32_t np = 0;
   uint32_t n_p[2] = {0, 0};   // weights taken from each stream
   uint32_t n_o[2] = {0, 0};   // outputs begun for each stream
   // descriptors differ in their start address alone (low word, 16-byte units)
@@ -290,11 +324,12 @@ QG_DEVICE void issue_mma(const AttnArgs &a, Walk walk, uint32_t smem, WideBars *
   // tiles come as K0 V0 K1 V1 ...; kt and vt are the next key and value tiles to be used
   Ring<C::NST> kt, vt;
   vt.next();
-  Piece p;
-  for (; walk_next(a, &walk, &p); ++np) {
-    const int n = p.j1 - p.j0;
+  for (const Piece *pp; (pp = piece_get(bar, np)) != nullptr; ++np) {
+    const int n = pp->j1 - pp->j0;
+    const bool paired = pp->paired;
+    piece_done(bar, np, lane);
     if (!wait(&bar->q_full, np & 1)) return;
-    if (p.paired) {
+    if (paired) {
       for (int j = 0; j <= n; ++j) {
         if (j < n && !landed(kt)) return;
         if (j > 0 && !landed(vt)) return;
@@ -345,16 +380,16 @@ QG_DEVICE void issue_mma(const AttnArgs &a, Walk walk, uint32_t smem, WideBars *
 
 // ---- softmax ----------------------------------------------------------------------------------
 template <int D, bool BF16, bool OUT32>
-QG_DEVICE void softmax(const AttnArgs &a, Walk walk, WideBars *bar, int s, int warp4, int lane, uint32_t stage) {
+QG_DEVICE void softmax(const AttnArgs &a, WideBars *bar, int s, int warp4, int lane, uint32_t stage) {
   volatile int *abort = &bar->abort;
   const uint32_t lanes = static_cast<uint32_t>(32 * warp4) << 16;
   const uint32_t ts = bar->tmem + lanes + 128u * s, to = bar->tmem + lanes + 256u + D * s;
   const int row = 32 * warp4 + lane, half = a.wide.tpt / 2;
   const float sl = fabsf(a.scale_log2);
   const bool neg = a.scale_log2 < 0.f;
-  uint32_t n_s = 0, n_o = 0;
-  Piece p;
-  while (walk_next(a, &walk, &p)) {
+  uint32_t n_s = 0, n_o = 0, np = 0;
+  for (const Piece *pp; (pp = piece_get(bar, np)) != nullptr; piece_done(bar, np++, lane)) {
+    const Piece &p = *pp;
     // this thread's row
     const int sub = p.paired ? s : 0;
     const int tok = min(half, p.tokens - sub * half);
@@ -364,12 +399,12 @@ QG_DEVICE void softmax(const AttnArgs &a, Walk walk, WideBars *bar, int s, int w
     const int all = __reduce_min_sync(0xFFFFFFFFu, valid ? lim : 0x7FFFFFFF);
     const int allp = __reduce_min_sync(0xFFFFFFFFu, valid ? limp : 0x7FFFFFFF);
     float m = -INFINITY, l = 0.f;
-    const int step = p.paired ? 1 : 2, first = p.paired ? p.j0 : p.j0 + s;
-    for (int j = first; j < p.j1; j += step) {
+    const int step = p.paired ? 1 : 2, first = p.paired ? p.j0 : p.j0 + s, j1 = p.j1, jp = p.jp;
+    for (int j = first; j < j1; j += step) {
       if (!warp_wait(&bar->s_full[s], n_s++ & 1, abort)) return;
       tc_fence_after();
-      const bool pre = j < p.jp;
-      const int key0 = (pre ? j : j - p.jp) * kWideKeys;
+      const bool pre = j < jp;
+      const int key0 = (pre ? j : j - jp) * kWideKeys;
       const int left = (pre ? limp : lim) - key0;  // keys of the tile that the row sees
       const bool masked = key0 + kWideKeys > (pre ? allp : all);
       float x[kWideKeys];
@@ -450,7 +485,7 @@ QG_DEVICE void softmax(const AttnArgs &a, Walk walk, WideBars *bar, int s, int w
       if (lane == 0) mbar_arrive(&bar->p_full[s]);
     }
     // ---- the piece's output
-    const bool any = first < p.j1;
+    const bool any = first < j1;
     if (any) {
       if (!warp_wait(&bar->o_full[s], n_o++ & 1, abort)) return;
       tc_fence_after();
@@ -522,6 +557,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const __grid_con
       mbar_init(&bar->full[i], 1);
       mbar_init(&bar->empty[i], 1);
     }
+    for (int i = 0; i < kPieces; ++i) {
+      mbar_init(&bar->piece_full[i], 1);
+      mbar_init(&bar->piece_empty[i], kSoftWarps + 2);
+    }
     mbar_init(&bar->q_full, 1);
     mbar_init(&bar->tail, 1);
     mbar_init(&bar->q_empty, 1);
@@ -554,11 +593,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const __grid_con
   const uint32_t sb = smem_u32(smem);
   if (warp < kSoftWarps) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
-    softmax<D, BF16, OUT32>(a, walk, bar, warp >> 2, warp & 3, lane, sb + C::OFF_STAGE + warp * kStageBytes);
+    softmax<D, BF16, OUT32>(a, bar, warp >> 2, warp & 3, lane, sb + C::OFF_STAGE + warp * kStageBytes);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
     if (warp == kMmaWarp) {
-      issue_mma<D, BF16, OUT32>(a, walk, sb, bar);
+      issue_mma<D, BF16, OUT32>(sb, bar, lane);
       if (lane == 0) {
         // after an abort the products in flight finish before the tensor memory is released (a
         // normal run waited for each); q_empty counts pieces, so any further phase will do
@@ -570,9 +609,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const __grid_con
         }
       }
     } else if (warp == kProdWarp) {
-      produce<D>(a, maps, walk, smem, bar, lane);
+      produce<D>(a, maps, smem, bar, lane);
       // after an abort the copies in flight land before the CTA's shared memory is released
       if (*static_cast<volatile int *>(&bar->abort)) __nanosleep(1000000);
+    } else if (warp == kWalkWarp) {
+      walk_line(a, walk, bar, lane);
     }
   }
   tc_fence_before();
@@ -615,6 +656,8 @@ bool make_maps(const AttnArgs &a, bool bf16, WideMaps *m) {
       return false;
   return true;
 }
+
+static_assert(sizeof(WideBars) <= 512, "barriers and descriptions");
 
 template <int D, bool BF16, bool OUT32>
 qg_status wide_run(const AttnArgs &a, cudaStream_t s) {
