@@ -351,8 +351,8 @@ QG_DEVICE size_t piece_row(const Pieces &p, int i) {
   return (p.first + slot) * p.rows + p.row + half * kWideHalf;
 }
 template <int D>
-QG_DEVICE void load_o(const Pieces &p, int i, int lane, float (&v)[D / 32]) {
-  const float *src = p.o + piece_row(p, i) * D + lane * (D / 32);
+QG_DEVICE void load_o(const Pieces &p, int i, int r, int lane, float (&v)[D / 32]) {
+  const float *src = p.o + (piece_row(p, i) + r) * D + lane * (D / 32);
   if constexpr (D == 64) {
     const float2 u = __ldcg(reinterpret_cast<const float2 *>(src));
     v[0] = u.x;
@@ -368,24 +368,38 @@ QG_DEVICE void load_o(const Pieces &p, int i, int lane, float (&v)[D / 32]) {
     }
   }
 }
-template <int D>
-QG_DEVICE void acc_pieces(Acc<D / 32> &x, const Pieces &p, int i0, int step, int lane) {
-  constexpr int U = 4;  // pieces in flight
+// R neighbouring rows of the tile (the first nr of them), U pieces of each in flight.
+template <int D, int R, int U>
+QG_DEVICE void acc_pieces(Acc<D / 32> (&x)[R], int nr, const Pieces &p, int i0, int step, int lane) {
   const int count = p.count * p.halves;
   for (int i = i0; i < count; i += U * step) {
-    float v[U][D / 32];
-    float2 ml[U];
+    float v[R][U][D / 32];
+    float2 ml[R][U];
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-      ml[k] = make_float2(-INFINITY, 0.f);
-      if (i + k * step < count) {
-        ml[k] = __ldcg(p.ml + piece_row(p, i + k * step));
-        load_o<D>(p, i + k * step, lane, v[k]);
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        ml[r][k] = make_float2(-INFINITY, 0.f);
+        if (r < nr && i + k * step < count) {
+          ml[r][k] = __ldcg(p.ml + piece_row(p, i + k * step) + r);
+          load_o<D>(p, i + k * step, r, lane, v[r][k]);
+        }
       }
-    }
 #pragma unroll
-    for (int k = 0; k < U; ++k)
-      if (i + k * step < count) acc_add(x, ml[k].x, ml[k].y, v[k]);
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int k = 0; k < U; ++k)
+        if (r < nr && i + k * step < count) acc_add(x[r], ml[r][k].x, ml[r][k].y, v[r][k]);
+  }
+}
+template <int NV, int R>
+QG_DEVICE void acc_clear(Acc<NV> (&x)[R]) {
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    x[r].m = -INFINITY;
+    x[r].l = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) x[r].o[i] = 0.f;
   }
 }
 
@@ -406,88 +420,99 @@ QG_DEVICE void write_row(const AttnArgs &a, int t, int hq, int lane, const Acc<D
   }
 }
 
+// The two segments of token t that hold keys for it: its sequence's own, and its run's.
+QG_DEVICE void token_segs(const AttnArgs &a, int t, RowSeg *own, RowSeg *pre) {
+  own->l = pre->l = nullptr;
+  const int b = kv_seq_of(a.b, t);
+  if (b < 0) {
+    atomicOr(&g_qg_status_attn, QG_STATUS_BIT_ID);
+    return;
+  }
+  *own = row_seg(a, 2 * b + 1, t);
+  const int gr = kv_group_of(a.b, b);
+  if (gr >= 0 && !seq_long(a, b)) *pre = row_seg(a, 2 * run_first(a, gr, b), t);
+}
+
 // How the rows are shared out:
-//   kRowBlock    a block of 8 warps per row, the row's pieces spread over the warps: few rows with
-//                many pieces each;
-//   kRowWarp     a warp per row: a batch's decode step;
-//   kTokenWarp   a warp per token, its lanes asking which heads need joining at all: prompts, most
-//                of whose rows their workers wrote.
-enum { kRowBlock, kRowWarp, kTokenWarp };
+//   kRowBlock  a block of 8 warps per row, the row's pieces spread over the warps: few rows with
+//              many pieces each;
+//   kRowWarp   a warp per row: a batch's decode step;
+//   kTokens    a block per 32 tokens: its threads ask which (token, cached head) need joining at
+//              all, its warps join those: prompts, most of whose rows their workers wrote.
+enum { kRowBlock, kRowWarp, kTokens };
+struct JoinItem {
+  Pieces own, pre;
+  int t, h;
+};
 template <int D, bool BF16, bool OUT32, int MODE>
 __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ AttnArgs a) {
   constexpr int NV = D / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
   pdl_launch_dependents();
-  const int item = MODE == kRowBlock ? static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x) * 8 + warp;
-  const int t = MODE == kTokenWarp ? item : item / a.Hq;
-  if (t >= a.b.T) return;
-  const int b = kv_seq_of(a.b, t);
-  const int gr = b >= 0 ? kv_group_of(a.b, b) : -1;
-  if (b < 0 && lane == 0) atomicOr(&g_qg_status_attn, QG_STATUS_BIT_ID);
   RowSeg so, sp;
-  so.l = sp.l = nullptr;
-  if (b >= 0) so = row_seg(a, 2 * b + 1, t);
-  if (gr >= 0 && !seq_long(a, b)) sp = row_seg(a, 2 * run_first(a, gr, b), t);
-  if constexpr (MODE == kRowWarp) {
-    const int hq = item - t * a.Hq;
-    const Pieces own = pieces_of(so, hq / a.Gq, hq % a.Gq), pre = pieces_of(sp, hq / a.Gq, hq % a.Gq);
-    if (written(own, pre)) return;
-    Acc<NV> x;
-    x.m = -INFINITY;
-    x.l = 0.f;
+  if constexpr (MODE == kTokens) {
+    __shared__ JoinItem items[256];
+    __shared__ int n_items;
+    const int t = static_cast<int>(blockIdx.x) * 32 + static_cast<int>(threadIdx.x >> 3);
+    so.l = sp.l = nullptr;
+    if (t < a.b.T) token_segs(a, t, &so, &sp);
+    for (int h0 = 0; h0 < a.pool.Hkv; h0 += 8) {
+      if (threadIdx.x == 0) n_items = 0;
+      __syncthreads();
+      const int h = h0 + static_cast<int>(threadIdx.x & 7);
+      if (t < a.b.T && h < a.pool.Hkv) {
+        const Pieces own = pieces_of(so, h, 0), pre = pieces_of(sp, h, 0);
+        if (!written(own, pre)) items[atomicAdd(&n_items, 1)] = JoinItem{own, pre, t, h};
+      }
+      __syncthreads();
+      constexpr int R = 4;  // a head's query rows, four at a time
+      const int groups = (a.Gq + R - 1) / R, tasks = n_items * groups;
+      for (int k = warp; k < tasks; k += 8) {
+        const JoinItem &it = items[k / groups];
+        const int q0 = (k % groups) * R, nr = min(R, a.Gq - q0);
+        Pieces own = it.own, pre = it.pre;
+        own.row += q0;
+        pre.row += q0;
+        Acc<NV> x[R];
+        acc_clear(x);
+        acc_pieces<D, R, 2>(x, nr, own, 0, 1, lane);
+        acc_pieces<D, R, 2>(x, nr, pre, 0, 1, lane);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) x.o[i] = 0.f;
-    acc_pieces<D>(x, own, 0, 1, lane);
-    acc_pieces<D>(x, pre, 0, 1, lane);
-    write_row<D, BF16, OUT32>(a, t, hq, lane, x);
-  } else if constexpr (MODE == kRowBlock) {
-    const int hq = item - t * a.Hq;
-    const Pieces own = pieces_of(so, hq / a.Gq, hq % a.Gq), pre = pieces_of(sp, hq / a.Gq, hq % a.Gq);
-    if (written(own, pre)) return;
-    __shared__ float sh[8][D];
-    __shared__ float2 sml[8];
-    Acc<NV> x;
-    x.m = -INFINITY;
-    x.l = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) x.o[i] = 0.f;
-    acc_pieces<D>(x, own, warp, 8, lane);
-    acc_pieces<D>(x, pre, warp, 8, lane);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) sh[warp][lane * NV + i] = x.o[i];
-    if (lane == 0) sml[warp] = make_float2(x.m, x.l);
-    __syncthreads();
-    if (warp) return;
-#pragma unroll
-    for (int q = 1; q < 8; ++q) {
-      float v[NV];
-#pragma unroll
-      for (int i = 0; i < NV; ++i) v[i] = sh[q][lane * NV + i];
-      acc_add(x, sml[q].x, sml[q].y, v);
+        for (int r = 0; r < R; ++r)
+          if (r < nr) write_row<D, BF16, OUT32>(a, it.t, it.h * a.Gq + q0 + r, lane, x[r]);
+      }
+      __syncthreads();
     }
-    write_row<D, BF16, OUT32>(a, t, hq, lane, x);
   } else {
-    for (int h0 = 0; h0 < a.pool.Hkv; h0 += 32) {
-      const int hl = h0 + lane;
-      uint32_t todo = __ballot_sync(0xFFFFFFFFu, hl < a.pool.Hkv && !written(pieces_of(so, hl, 0), pieces_of(sp, hl, 0)));
-      for (; todo; todo &= todo - 1) {
-        const int h = h0 + __ffs(static_cast<int>(todo)) - 1;
-        Pieces own = pieces_of(so, h, 0), pre = pieces_of(sp, h, 0);
-        for (int q = 0; q < a.Gq; ++q) {
-          Acc<NV> x;
-          x.m = -INFINITY;
-          x.l = 0.f;
+    const int item = MODE == kRowBlock ? static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x) * 8 + warp;
+    const int t = item / a.Hq, hq = item - t * a.Hq;
+    if (t >= a.b.T) return;
+    token_segs(a, t, &so, &sp);
+    const Pieces own = pieces_of(so, hq / a.Gq, hq % a.Gq), pre = pieces_of(sp, hq / a.Gq, hq % a.Gq);
+    if (written(own, pre)) return;
+    Acc<NV> x[1];
+    acc_clear(x);
+    constexpr int W = MODE == kRowBlock ? 8 : 1;  // warps per row
+    acc_pieces<D, 1, 4>(x, 1, own, MODE == kRowBlock ? warp : 0, W, lane);
+    acc_pieces<D, 1, 4>(x, 1, pre, MODE == kRowBlock ? warp : 0, W, lane);
+    if constexpr (MODE == kRowBlock) {
+      __shared__ float sh[8][D];
+      __shared__ float2 sml[8];
 #pragma unroll
-          for (int i = 0; i < NV; ++i) x.o[i] = 0.f;
-          acc_pieces<D>(x, own, 0, 1, lane);
-          acc_pieces<D>(x, pre, 0, 1, lane);
-          write_row<D, BF16, OUT32>(a, t, h * a.Gq + q, lane, x);
-          ++own.row;
-          ++pre.row;
-        }
+      for (int i = 0; i < NV; ++i) sh[warp][lane * NV + i] = x[0].o[i];
+      if (lane == 0) sml[warp] = make_float2(x[0].m, x[0].l);
+      __syncthreads();
+      if (warp) return;
+#pragma unroll
+      for (int q = 1; q < 8; ++q) {
+        float v[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) v[i] = sh[q][lane * NV + i];
+        acc_add(x[0], sml[q].x, sml[q].y, v);
       }
     }
+    write_row<D, BF16, OUT32>(a, t, hq, lane, x[0]);
   }
 }
 
@@ -567,14 +592,15 @@ qg_status attn_run(const AttnArgs &a, int sms, cudaStream_t s) {
   }
   const long long rows = static_cast<long long>(a.b.T) * a.Hq;
   cudaError_t e;
-  // 2048 rows of about 20 pieces: 30 us with a block per row, XX with a warp
+  // 2048 rows of about 20 pieces: 30 us with a block per row, 12 with a warp; 7832 tokens of 32
+  // rows, few to be joined: 57 us with a warp per token, 14 with blocks of 32 tokens
   if (rows <= 3LL * sms)
     e = launch_pdl(attn_join_kernel<D, BF16, OUT32, kRowBlock>, dim3(static_cast<unsigned>(rows)), dim3(256), 0, s, a);
   else if (rows <= 8192)
     e = launch_pdl(attn_join_kernel<D, BF16, OUT32, kRowWarp>, dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0, s, a);
   else
-    e = launch_pdl(attn_join_kernel<D, BF16, OUT32, kTokenWarp>, dim3(static_cast<unsigned>((a.b.T + 7) / 8)), dim3(256), 0,
-                   s, a);
+    e = launch_pdl(attn_join_kernel<D, BF16, OUT32, kTokens>, dim3(static_cast<unsigned>((a.b.T + 31) / 32)), dim3(256), 0, s,
+                   a);
   if (e != cudaSuccess) return QG_ECUDA;
   return cudaGetLastError() == cudaSuccess ? QG_OK : QG_ECUDA;
 }
