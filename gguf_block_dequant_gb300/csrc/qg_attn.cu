@@ -437,52 +437,55 @@ QG_DEVICE void token_segs(const AttnArgs &a, int t, RowSeg *own, RowSeg *pre) {
 //   kRowBlock  a block of 8 warps per row, the row's pieces spread over the warps: few rows with
 //              many pieces each;
 //   kRowWarp   a warp per row: a batch's decode step;
-//   kTokens    a block per 32 tokens: its threads ask which (token, cached head) need joining at
-//              all, its warps join those: prompts, most of whose rows their workers wrote.
+//   kTokens    a block per 32 tokens and cached head: its first warp's lanes ask which tokens need
+//              joining at all, its warps join those: prompts, most of whose rows their workers
+//              wrote.  (A block for all heads was slower: a cut falls on all of a tile's tokens.)
 enum { kRowBlock, kRowWarp, kTokens };
 struct JoinItem {
   Pieces own, pre;
-  int t, h;
+  int t;
 };
+constexpr int kTokensThreads = 128;
 template <int D, bool BF16, bool OUT32, int MODE>
-__global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(MODE == kTokens ? kTokensThreads : 256) attn_join_kernel(const __grid_constant__ AttnArgs a) {
   constexpr int NV = D / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
   pdl_launch_dependents();
   RowSeg so, sp;
   if constexpr (MODE == kTokens) {
-    __shared__ JoinItem items[256];
+    __shared__ JoinItem items[32];
     __shared__ int n_items;
-    const int t = static_cast<int>(blockIdx.x) * 32 + static_cast<int>(threadIdx.x >> 3);
-    so.l = sp.l = nullptr;
-    if (t < a.b.T) token_segs(a, t, &so, &sp);
-    for (int h0 = 0; h0 < a.pool.Hkv; h0 += 8) {
-      if (threadIdx.x == 0) n_items = 0;
-      __syncthreads();
-      const int h = h0 + static_cast<int>(threadIdx.x & 7);
-      if (t < a.b.T && h < a.pool.Hkv) {
-        const Pieces own = pieces_of(so, h, 0), pre = pieces_of(sp, h, 0);
-        if (!written(own, pre)) items[atomicAdd(&n_items, 1)] = JoinItem{own, pre, t, h};
+    const int h = static_cast<int>(blockIdx.y);
+    if (warp == 0) {
+      const int t = static_cast<int>(blockIdx.x) * 32 + lane;
+      JoinItem it;
+      bool need = false;
+      if (t < a.b.T) {
+        token_segs(a, t, &so, &sp);
+        it = JoinItem{pieces_of(so, h, 0), pieces_of(sp, h, 0), t};
+        need = !written(it.own, it.pre);
       }
-      __syncthreads();
-      constexpr int R = 4;  // a head's query rows, four at a time
-      const int groups = (a.Gq + R - 1) / R, tasks = n_items * groups;
-      for (int k = warp; k < tasks; k += 8) {
-        const JoinItem &it = items[k / groups];
-        const int q0 = (k % groups) * R, nr = min(R, a.Gq - q0);
-        Pieces own = it.own, pre = it.pre;
-        own.row += q0;
-        pre.row += q0;
-        Acc<NV> x[R];
-        acc_clear(x);
-        acc_pieces<D, R, 2>(x, nr, own, 0, 1, lane);
-        acc_pieces<D, R, 2>(x, nr, pre, 0, 1, lane);
+      const uint32_t all = __ballot_sync(0xFFFFFFFFu, need);
+      if (need) items[__popc(all & ((1u << lane) - 1u))] = it;
+      if (lane == 0) n_items = __popc(all);
+    }
+    __syncthreads();
+    constexpr int R = 2;  // a head's query rows, two at a time
+    const int groups = (a.Gq + R - 1) / R, tasks = n_items * groups;
+    for (int k = warp; k < tasks; k += kTokensThreads / 32) {
+      const JoinItem &it = items[k / groups];
+      const int q0 = (k % groups) * R, nr = min(R, a.Gq - q0);
+      Pieces own = it.own, pre = it.pre;
+      own.row += q0;
+      pre.row += q0;
+      Acc<NV> x[R];
+      acc_clear(x);
+      acc_pieces<D, R, 2>(x, nr, own, 0, 1, lane);
+      acc_pieces<D, R, 2>(x, nr, pre, 0, 1, lane);
 #pragma unroll
-        for (int r = 0; r < R; ++r)
-          if (r < nr) write_row<D, BF16, OUT32>(a, it.t, it.h * a.Gq + q0 + r, lane, x[r]);
-      }
-      __syncthreads();
+      for (int r = 0; r < R; ++r)
+        if (r < nr) write_row<D, BF16, OUT32>(a, it.t, h * a.Gq + q0 + r, lane, x[r]);
     }
   } else {
     const int item = MODE == kRowBlock ? static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x) * 8 + warp;
@@ -599,8 +602,8 @@ qg_status attn_run(const AttnArgs &a, int sms, cudaStream_t s) {
   else if (rows <= 8192)
     e = launch_pdl(attn_join_kernel<D, BF16, OUT32, kRowWarp>, dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0, s, a);
   else
-    e = launch_pdl(attn_join_kernel<D, BF16, OUT32, kTokens>, dim3(static_cast<unsigned>((a.b.T + 31) / 32)), dim3(256), 0, s,
-                   a);
+    e = launch_pdl(attn_join_kernel<D, BF16, OUT32, kTokens>, dim3(static_cast<unsigned>((a.b.T + 31) / 32), a.pool.Hkv),
+                   dim3(kTokensThreads), 0, s, a);
   if (e != cudaSuccess) return QG_ECUDA;
   return cudaGetLastError() == cudaSuccess ? QG_OK : QG_ECUDA;
 }

@@ -573,19 +573,26 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const __grid_con
     bar->abort = 0;
     fence_mbar_init();
   }
-  pdl_wait();
-  pdl_launch_dependents();
+  // No wait for the narrow kernel here: it has waited for all that came before the call, and this
+  // one reads and writes nothing of its.  A CTA starts as soon as its SM is free; the wait at the
+  // end keeps the order for what follows.
   const Line &ln = a.wide;
   const long long total = line_scan<kThreads>(a, ln, scan, blockIdx.x == 0);
   const int nw = line_workers(ln, total);
   Walk walk;
   walk.scan = scan;
   walk.w = static_cast<int>(blockIdx.x);
-  if (total == 0 || walk.w >= nw) return;
+  if (total == 0 || walk.w >= nw) {
+    pdl_wait();
+    return;
+  }
   const Cut cut = line_cut(total, nw);
   walk.at = line_start(cut, walk.w);
   walk.end = line_start(cut, walk.w + 1);
-  if (walk.at >= walk.end || !cursor_find(a, ln, *scan, walk.at, &walk.cur)) return;  // the same for the whole block
+  if (walk.at >= walk.end || !cursor_find(a, ln, *scan, walk.at, &walk.cur)) {  // the same for the whole block
+    pdl_wait();
+    return;
+  }
   if (warp == kMmaWarp) tmem_alloc(&bar->tmem, C::COLS);
   tc_fence_before();
   __syncthreads();
@@ -622,6 +629,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const __grid_con
     tc_fence_after();
     tmem_dealloc(bar->tmem, C::COLS);
   }
+  pdl_wait();
+  pdl_launch_dependents();
 }
 
 // the register split above needs the launch's registers to be what it was made for
