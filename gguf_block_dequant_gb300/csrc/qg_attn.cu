@@ -263,15 +263,18 @@ __global__ void __launch_bounds__(NarrowCfg<D>::NW * 32, 1) attn_narrow_kernel(c
 // One token's rows in one segment: what its pieces' slots follow from, for every head.
 struct RowSeg {
   const Line *l;            // null: no keys there
+  int s;                    // the segment
   long long p0, cost;       // place of head 0's unit, places per head
   Cut cut;                  // the line's parts
   int unit, rt, x;          // head 0's unit, units per head, keys of a unit
   int row, halves;          // first row in the tile; 2: each slot holds two partial results of a row
 };
 
+// from the lengths alone; row_seg_place adds what the attention kernels published
 QG_DEVICE RowSeg row_seg(const AttnArgs &a, int s, int t) {
   RowSeg q;
   q.l = nullptr;
+  q.s = s;
   const Seg g = seg_load(a, s);
   const bool nar = seg_in(a.narrow, g);
   if (!nar && !(a.wide.workers && seg_in(a.wide, g))) return q;
@@ -280,12 +283,10 @@ QG_DEVICE RowSeg row_seg(const AttnArgs &a, int s, int t) {
   q.x = unit_keys(l, g, r);
   if (q.x == 0) return q;
   q.l = &l;
-  const long long total = l.seg_pos[2 * a.b.B];
-  q.cut = line_cut(total, line_workers(l, total));
   q.rt = seg_tiles(l, g);
-  q.p0 = l.seg_pos[s] + seg_cost_to(l, g, r);
+  q.p0 = seg_cost_to(l, g, r);
   q.cost = seg_cost_to(l, g, q.rt);
-  q.unit = l.seg_unit[s] + r;
+  q.unit = r;
   q.halves = 1;
   if (nar) {
     q.row = i * a.Gq;
@@ -296,6 +297,14 @@ QG_DEVICE RowSeg row_seg(const AttnArgs &a, int s, int t) {
     if (g.nt - r * l.tpt <= half) q.halves = 2;
   }
   return q;
+}
+
+QG_DEVICE void row_seg_place(const AttnArgs &a, RowSeg *q) {
+  if (!q->l) return;
+  const long long total = __ldcg(q->l->seg_pos + 2 * a.b.B);
+  q->cut = line_cut(total, line_workers(*q->l, total));
+  q->p0 += __ldcg(q->l->seg_pos + q->s);
+  q->unit += __ldcg(q->l->seg_unit + q->s);
 }
 
 // The pieces of one row: slots first, first + 1, ... (count of them), row `row` of a `rows`-row
@@ -450,9 +459,16 @@ template <int D, bool BF16, bool OUT32, int MODE>
 __global__ void __launch_bounds__(MODE == kTokens ? kTokensThreads : 256) attn_join_kernel(const __grid_constant__ AttnArgs a) {
   constexpr int NV = D / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  pdl_wait();
-  pdl_launch_dependents();
+  // What follows from the lengths is worked out while the attention kernels drain: their own wait
+  // came after everything before the call.
   RowSeg so, sp;
+  so.l = sp.l = nullptr;
+  auto place = [&] {
+    pdl_wait();
+    pdl_launch_dependents();
+    row_seg_place(a, &so);
+    row_seg_place(a, &sp);
+  };
   if constexpr (MODE == kTokens) {
     __shared__ JoinItem items[32];
     __shared__ int n_items;
@@ -461,14 +477,17 @@ __global__ void __launch_bounds__(MODE == kTokens ? kTokensThreads : 256) attn_j
       const int t = static_cast<int>(blockIdx.x) * 32 + lane;
       JoinItem it;
       bool need = false;
+      if (t < a.b.T) token_segs(a, t, &so, &sp);
+      place();
       if (t < a.b.T) {
-        token_segs(a, t, &so, &sp);
         it = JoinItem{pieces_of(so, h, 0), pieces_of(sp, h, 0), t};
         need = !written(it.own, it.pre);
       }
       const uint32_t all = __ballot_sync(0xFFFFFFFFu, need);
       if (need) items[__popc(all & ((1u << lane) - 1u))] = it;
       if (lane == 0) n_items = __popc(all);
+    } else {
+      pdl_wait();
     }
     __syncthreads();
     constexpr int R = 2;  // a head's query rows, two at a time
@@ -490,8 +509,9 @@ __global__ void __launch_bounds__(MODE == kTokens ? kTokensThreads : 256) attn_j
   } else {
     const int item = MODE == kRowBlock ? static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x) * 8 + warp;
     const int t = item / a.Hq, hq = item - t * a.Hq;
+    if (t < a.b.T) token_segs(a, t, &so, &sp);
+    place();
     if (t >= a.b.T) return;
-    token_segs(a, t, &so, &sp);
     const Pieces own = pieces_of(so, hq / a.Gq, hq % a.Gq), pre = pieces_of(sp, hq / a.Gq, hq % a.Gq);
     if (written(own, pre)) return;
     Acc<NV> x[1];

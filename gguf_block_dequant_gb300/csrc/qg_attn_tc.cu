@@ -630,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const __grid_con
     tmem_dealloc(bar->tmem, C::COLS);
   }
   pdl_wait();
-  pdl_launch_dependents();
+  pdl_launch_dependents();  // not before: blocks that wait beside this kernel cost it 5 %
 }
 
 // the register split above needs the launch's registers to be what it was made for
