@@ -111,6 +111,7 @@ QUERIES = {
     "a prompt that sees little": ([150], [20], ((0, 1, 30),)),
     "short ones among prompts": ([1, 2, 90, 1, 1, 130, 3, 1, 140, 7], [9, 2, 90, 70, 1, 200, 3, 5, 141, 300],
                                  ((0, 7, 300), (7, 9, 77))),
+    "whole and half tiles in turn": ([64, 33, 65, 40, 1, 129, 20, 64], [64, 333, 65, 300, 1, 400, 20, 900], ((0, 8, 140),)),
     "a short prefix before prompts": ([133, 129, 1], [133, 500, 40], ((0, 3, 5),)),
 }
 
