@@ -371,13 +371,14 @@ __global__ void __launch_bounds__(kMergeThreads) select_merge_kernel(const Selec
   }
 }
 
-// Slices of a row: two CTAs for every SM in all, but no slice under 2048 values, and lists that
+// Slices of a row: two CTAs for every SM in all, but no slice under 4096 values (4 rows of 151936: 12.2 us at 2048, 10.7 at 4096, 10.9 at 8192; 128 rows: one
+// CTA an SM 43 us, two 35, three 41), and lists that
 // fit the merge's shared memory.
 struct Slices {
   int S, slice;
 };
 Slices make_slices(long long rows, long long W, long long K, long long V, int sms) {
-  long long S = std::min<long long>({2LL * sms / rows, (V + 2047) / 2048, kMaxSlices, 16384 / (W * K)});
+  long long S = std::min<long long>({2LL * sms / rows, (V + 4095) / 4096, kMaxSlices, 16384 / (W * K)});
   S = std::max<long long>(S, 1);
   const long long slice = ((V + S - 1) / S + 3) / 4 * 4;
   return {static_cast<int>((V + slice - 1) / slice), static_cast<int>(slice)};
