@@ -1,8 +1,8 @@
 // qg_attn.cu -- causal attention over the paged cache: the kernel for few rows per segment (a
 // decode step's tokens), the kernel that joins the pieces of a row, and the entry points.
 //
-// o = sum_j p_j V_j / sum_j p_j with p_j = 2^(c q.K_j - m), m the running maximum, in one pass over
-// the keys.  A decode step reads every cached row once and does 4 operations per cached value
+// o = sum_j p_j V_j / sum_j p_j with p_j = 2^(c q.K_j - m), m from the running maximum, in one pass
+// over the keys.  A decode step reads every cached row once and does 4 operations per cached value
 // and query head, far below the tensor cores' rate, so HBM bounds it: the design keeps
 // asynchronous copies in flight on every SM and spends few instructions per byte.
 #include <math.h>
@@ -134,6 +134,9 @@ __global__ void __launch_bounds__(NarrowCfg<D>::NW * 32, 1) attn_narrow_kernel(c
     for (int d = 0; d < DT; ++d)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[d][e] = 0.f;
+    // m: the reference of the row's weights, its running maximum less what f16 weights are
+    // raised by (2^14: the second term of a small one would otherwise lie among the subnormals)
+    constexpr float RAISE = BF16 ? 0.f : 14.f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 
     long long off = row_off(j0);
@@ -185,7 +188,7 @@ __global__ void __launch_bounds__(NarrowCfg<D>::NW * 32, 1) attn_narrow_kernel(c
         float mx = fmaxf(fmaxf(x[0][2 * e], x[0][2 * e + 1]), fmaxf(x[1][2 * e], x[1][2 * e + 1]));
         mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
-        const float mn = fmaxf(m[e], mx);
+        const float mn = fmaxf(m[e], mx - RAISE);
         const float ms = mn == -INFINITY ? 0.f : mn;
         if (__any_sync(0xFFFFFFFFu, mn > m[e])) {
           const float al = ex2(m[e] - ms);

@@ -398,7 +398,12 @@ QG_DEVICE void softmax(const AttnArgs &a, WideBars *bar, int s, int warp4, int l
     const int lim = valid ? row_limit(a, p.g, t) : 0, limp = valid ? row_prefix_limit(p.g, t) : 0;
     const int all = __reduce_min_sync(0xFFFFFFFFu, valid ? lim : 0x7FFFFFFF);
     const int allp = __reduce_min_sync(0xFFFFFFFFu, valid ? limp : 0x7FFFFFFF);
-    float m = -INFINITY, l = 0.f;
+    // the row's maximum that its weights refer to, and the reference itself: the maximum in log2
+    // units less what f16 weights are raised by (2^7, up to 2^15 with the lag: the second term of a
+    // small one would otherwise lie among the subnormals).  Rescaling uses the references as they
+    // were rounded.
+    constexpr float RAISE = BF16 ? 0.f : 7.f;
+    float m = -INFINITY, ref = -INFINITY, l = 0.f;
     const int step = p.paired ? 1 : 2, first = p.paired ? p.j0 : p.j0 + s, j1 = p.j1, jp = p.jp;
     for (int j = first; j < j1; j += step) {
       if (!warp_wait(&bar->s_full[s], n_s++ & 1, abort)) return;
@@ -431,8 +436,10 @@ QG_DEVICE void softmax(const AttnArgs &a, WideBars *bar, int s, int warp4, int l
       const bool move = mx > m && (m == -INFINITY || (mx - m) * sl > 8.0f);
       float al = 1.0f;
       if (move) {
-        al = m == -INFINITY ? 0.f : ex2((m - mx) * sl);
+        const float r = fmaf(mx, sl, -RAISE);
+        al = ex2(ref - r);  // 0 from -inf
         m = mx;
+        ref = r;
         l *= al;
       }
       if (j != first && __any_sync(0xFFFFFFFFu, move)) {
@@ -447,7 +454,7 @@ QG_DEVICE void softmax(const AttnArgs &a, WideBars *bar, int s, int warp4, int l
           tmem_st16(to + 16 * c, r);
         }
       }
-      const float nm = m == -INFINITY ? 0.f : -m * sl;
+      const float nm = ref == -INFINITY ? 0.f : -ref;
       f2 sum = mk2(0.f, 0.f);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
@@ -492,7 +499,7 @@ QG_DEVICE void softmax(const AttnArgs &a, WideBars *bar, int s, int warp4, int l
     }
     const float inv = p.alone ? (l > 0.f ? 1.0f / l : 0.f) : 1.0f;
     const size_t prow = p.slot * kWideRows + s * kWideHalf + row;
-    if (valid && !p.alone) a.wide.part_ml[prow] = make_float2(m == -INFINITY ? m : m * sl, l);
+    if (valid && !p.alone) a.wide.part_ml[prow] = make_float2(ref, l);
     if (any) {
       const bool wide_out = !p.alone || OUT32;  // f32 values; otherwise 16-bit ones
       const size_t orow = (static_cast<size_t>(t) * a.Hq + p.h * a.Gq + (valid ? row % a.Gq : 0)) * D;
