@@ -21,6 +21,15 @@
 // The running maximum a row's weights refer to is raised (and its output rescaled) only when the
 // row's maximum has grown by more than 2^8: weights stay below 2^8, exact in their ratios, and
 // the output in tensor memory is hardly ever touched between the products.
+//
+// Measured (one GB300, whole calls replayed from a graph): prompts of 7832 tokens under a prefix of
+// 4001, 32 heads over 8 of 128, bf16: 594 us, 1.17 PFLOP/s (0.61 of the measured cuBLAS rate); 64
+// one-token sequences under a prefix of 32768 (512 rows a cached head): 74 us, of which this
+// kernel 37.  What bounds it: a pair of 128-row tiles and 128 keys takes about 3700 cycles, of
+// which the products alone need 3080 (2048 at the tensor cores' full rate: Q K^T reads both
+// operands from shared memory, 8 KB for 64 cycles' work) and a stream's softmax about 2000.
+// Tried and slower: an MMA warp per stream (757 us), weights handed over in halves (645), more
+// chains for the maximum and sum (620).
 #include <cuda.h>
 
 #include <mutex>
