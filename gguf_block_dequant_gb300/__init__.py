@@ -361,6 +361,14 @@ class KVBatch(ctypes.Structure):
                 ("prefix_len", ctypes.c_void_p), ("prefix_pages", ctypes.c_void_p)]
 
 
+def _check(t, dtype, what):
+    """A contiguous tensor of the named torch dtype (None passes)."""
+    import torch
+
+    if t is not None and (t.dtype is not getattr(torch, dtype) or not t.is_contiguous()):
+        raise ValueError(f"{what} must be contiguous and {dtype}")
+
+
 def kv_cache(k, v):
     """A qg_kv_cache of two pools [pages][tokens][heads][D] of one f16 or bf16 type (any strides
     with the last one 1: a head-major pool is passed as its permuted view).  Keeps them alive."""
@@ -456,8 +464,9 @@ def kv_append(cache, batch, q, k, v, q_out, freqs, pairs=False, q_norm=None, k_n
     for t, what in ((q, "q"), (k, "k"), (v, "v"), (q_norm, "q_norm"), (k_norm, "k_norm")):
         if t is not None and _dtype(t) != DT_F32:
             raise ValueError(f"{what} must be f32")
-    if q is not None and (_dtype(q_out) != cache.dtype or not q_out.is_contiguous()):
-        raise ValueError("q_out must be contiguous and of the cache's type")
+    if q is not None and (_dtype(q_out) != cache.dtype or not q_out.is_contiguous() or q_out.numel() != T * Hq * D):
+        raise ValueError("q_out must be contiguous, of the cache's type and have whole heads for every token")
+    _check(freqs, "int64", "freqs")
     for t, what in ((q_norm, "q_norm"), (k_norm, "k_norm")):
         if t is not None and (t.numel() != D or not t.is_contiguous()):
             raise ValueError(f"{what} must have head_dim elements")
@@ -493,8 +502,12 @@ def beam_select(logits, scores, N, W, out_scores, parents, tokens, workspace, do
                 stream=None):
     """The K best continuations of N requests' W beams (qg_beam_select); K from the outputs' [N][K]."""
     V, K = logits.shape[-1], out_scores.shape[-1]
-    if logits.numel() != N * W * V or scores.numel() != N * W or not logits.is_contiguous():
-        raise ValueError("logits must be contiguous [N*W][V] and scores [N*W]")
+    if logits.numel() != N * W * V or scores.numel() != N * W:
+        raise ValueError("logits must be [N*W][V] and scores [N*W]")
+    for t, dtype, what in ((logits, "float32", "logits"), (scores, "float32", "scores"),
+                           (out_scores, "float32", "out_scores"), (parents, "int32", "parents"),
+                           (tokens, "int32", "tokens"), (done, "uint8", "done"), (done_out, "uint8", "done_out")):
+        _check(t, dtype, what)
     if any(t is not None and t.numel() != N * K for t in (out_scores, parents, tokens, done_out)):
         raise ValueError("outputs must be [N][K]")
     if done is not None and done.numel() != N * W:
@@ -509,4 +522,5 @@ def beam_reorder(caches, batch, parents, W, stream=None):
     caches: kv_caches of all layers; batch: kv_batch(kv_len, pages)."""
     if parents.numel() != batch.n_seqs:
         raise ValueError("parents must be [N][W]")
+    _check(parents, "int32", "parents")
     _call("qg_beam_reorder", caches, len(caches), ctypes.byref(batch), W, _ptr(parents), _stream(stream))

@@ -238,7 +238,11 @@ __global__ void __launch_bounds__(NarrowCfg<D>::NW * 32, 1) attn_narrow_kernel(c
 
     // ---- write the piece
     const bool alone = j0 == 0 && j1 == n_tiles && seg_whole(a, g, cur.s >> 1);
-    const size_t slot = static_cast<size_t>(cur.unit) + static_cast<size_t>(w);
+    const long long slot = piece_slot(ln, cur.unit, w);
+    if (slot < 0 && !alone) {
+      if (lane == 0) atomicOr(&g_qg_status_attn, QG_STATUS_BIT_ID);
+      continue;
+    }
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       float ls = l[e];
@@ -290,6 +294,7 @@ QG_DEVICE RowSeg row_seg(const AttnArgs &a, int s, int t) {
   const bool nar = seg_in(a.narrow, g);
   if (!nar && !(a.wide.workers && seg_in(a.wide, g))) return q;
   const Line &l = nar ? a.narrow : a.wide;
+  if (t < g.t0 || t >= g.t0 + g.nt) return q;  // starts that do not rise
   const int r = (t - g.t0) / l.tpt, i = t - g.t0 - r * l.tpt;
   q.x = unit_keys(l, g, r);
   if (q.x == 0) return q;
@@ -344,6 +349,7 @@ QG_DEVICE Pieces pieces_of(const RowSeg &q, int h, int gq) {
   p.rows = l.rows;
   p.row = q.row + gq;
   p.halves = q.halves;
+  if (piece_slot(l, q.unit + h * q.rt, w1) < 0) p.count = 0;  // not written
   return p;
 }
 // whether a worker wrote the row itself: all its keys are in one piece
@@ -555,6 +561,7 @@ constexpr size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 struct Plan {
   size_t bytes;
+  long long n_slots, w_slots;       // pieces the two lines can have
   size_t n_pos, n_unit, n_o, n_ml;  // offsets of the narrow line's arrays
   size_t w_pos, w_unit, w_o, w_ml;  // of the wide line's
   int wide_workers, narrow_workers;
@@ -575,6 +582,7 @@ Plan make_plan(const KvPool &pool, const KvBatch &b, int Gq, int sms) {
   long long un = b.B + runs;                                      // wide line there: one row tile each
   if (!wide) un += (b.G ? 2 : 1) * (static_cast<long long>(b.T) / tn);
   const long long sn = un * pool.Hkv + p.narrow_workers;
+  p.n_slots = sn;
   size_t at = 0;
   auto take = [&](size_t n) {
     const size_t r = at;
@@ -591,6 +599,7 @@ Plan make_plan(const KvPool &pool, const KvBatch &b, int Gq, int sms) {
     const long long uw = (b.q_start ? std::min<long long>(b.B, most) + tiles : 0) +
                          (b.G ? std::min<long long>(runs, most) + tiles : 0);
     const long long sw = uw * pool.Hkv + p.wide_workers;
+    p.w_slots = sw;
     p.w_pos = take((nseg + 1) * 8);
     p.w_unit = take((nseg + 1) * 4);
     p.w_ml = take(static_cast<size_t>(sw) * kWideRows * 8);
@@ -691,23 +700,24 @@ qg_status qg_attn_paged(const qg_kv_cache *cache, const qg_kv_batch *batch, int 
   a.out32 = out_dtype == QG_DT_F32;
   a.scale_log2 = scale * 1.4426950408889634f;
   uint8_t *ws = static_cast<uint8_t *>(workspace);
-  auto line = [&](int rows, int kshift, int workers, size_t pos, size_t unit, size_t o, size_t ml) {
+  auto line = [&](int rows, int kshift, int workers, long long slots, size_t pos, size_t unit, size_t o, size_t ml) {
     Line l = {};
     l.rows = rows;
     l.kshift = kshift;
     l.tpt = rows == kNarrowRows ? rows / a.Gq : 2 * (kWideHalf / a.Gq);
     l.workers = workers;
+    l.slots = slots;
     l.seg_pos = reinterpret_cast<long long *>(ws + pos);
     l.seg_unit = reinterpret_cast<int *>(ws + unit);
     l.part_o = reinterpret_cast<float *>(ws + o);
     l.part_ml = reinterpret_cast<float2 *>(ws + ml);
     return l;
   };
-  a.narrow = line(kNarrowRows, kNarrowShift, p.narrow_workers, p.n_pos, p.n_unit, p.n_o, p.n_ml);
+  a.narrow = line(kNarrowRows, kNarrowShift, p.narrow_workers, p.n_slots, p.n_pos, p.n_unit, p.n_o, p.n_ml);
   a.long_tokens = p.wide_workers ? kWideHalf / a.Gq : INT32_MAX;
   a.narrow.hi = p.wide_workers ? a.narrow.tpt : INT32_MAX;
   if (p.wide_workers) {
-    a.wide = line(kWideRows, kWideShift, p.wide_workers, p.w_pos, p.w_unit, p.w_o, p.w_ml);
+    a.wide = line(kWideRows, kWideShift, p.wide_workers, p.w_slots, p.w_pos, p.w_unit, p.w_o, p.w_ml);
     a.wide.lo = a.narrow.tpt;
     a.wide.hi = INT32_MAX;
   }

@@ -33,6 +33,7 @@ struct Line {
   int tpt;               // tokens per row tile: rows / Gq (wide: two halves of 128 / Gq)
   int lo, hi;            // segments with lo < tokens <= hi belong to it
   int workers;
+  long long slots;       // capacity of the pieces' arrays
   float *part_o;         // [slot][rows][D]
   float2 *part_ml;       // [slot][rows]: running maximum (log2 units) and sum
   long long *seg_pos;    // [2 B + 1] place of each segment's first key on the line
@@ -106,6 +107,13 @@ QG_DEVICE Seg seg_load(const AttnArgs &a, int s) {
     g.table = kv_prefix_table(a, gr);
   }
   return g;
+}
+
+// A piece's slot, -1 past the arrays: only where token or group starts do not rise, so that
+// segments hold more tokens than there are.
+QG_DEVICE long long piece_slot(const Line &l, long long unit, int w) {
+  const long long s = unit + w;
+  return s < l.slots ? s : -1;
 }
 
 QG_DEVICE bool seg_in(const Line &l, const Seg &g) { return g.nt > l.lo && g.nt <= l.hi && (g.len | g.plen) > 0; }

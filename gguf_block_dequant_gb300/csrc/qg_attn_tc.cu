@@ -95,7 +95,7 @@ struct Piece {
   int j0, j1, jp;  // key tiles; the first jp of the unit are those of a long sequence's prefix
   bool paired;     // two halves of rows; otherwise the streams take the key tiles in turn
   bool alone;      // the piece is all there is of its rows
-  size_t slot;
+  long long slot;  // -1: the workspace has none (token starts that do not rise)
 };
 struct WideBars {
   Piece piece[kPieces];
@@ -129,7 +129,7 @@ QG_DEVICE bool walk_next(const AttnArgs &a, Walk *k, Piece *p) {
       p->paired = p->tokens > l.tpt / 2;
       p->jp = tiles_of(l, c.g.plen);
       p->alone = p->paired && p->j0 == 0 && p->j1 == n && seg_whole(a, c.g, c.s >> 1);
-      p->slot = static_cast<size_t>(c.unit) + static_cast<size_t>(k->w);
+      p->slot = piece_slot(l, c.unit, k->w);
     }
     if (!cursor_next(a, l, *k->scan, &c, k->end)) c.pos = k->end;
     if (some) return true;
@@ -164,6 +164,7 @@ QG_DEVICE void walk_line(const AttnArgs &a, Walk walk, WideBars *bar, int lane) 
     Piece p;
     const bool more = walk_next(a, &walk, &p);
     if (!more) p.j0 = p.j1 = 0;
+    else if (p.slot < 0 && !p.alone && lane == 0) atomicOr(&g_qg_status_attn_tc, QG_STATUS_BIT_ID);
     const uint32_t i = n % kPieces;
     if (!warp_wait(&bar->piece_empty[i], ((n / kPieces) & 1) ^ 1, abort)) return;
     if (lane == 0) {
@@ -402,7 +403,7 @@ QG_DEVICE void softmax(const AttnArgs &a, WideBars *bar, int s, int warp4, int l
     // this thread's row
     const int sub = p.paired ? s : 0;
     const int tok = min(half, p.tokens - sub * half);
-    const bool valid = row < tok * a.Gq;
+    const bool valid = row < tok * a.Gq && (p.alone || p.slot >= 0);
     const int t = p.t0 + sub * half + (valid ? row / a.Gq : 0);
     const int lim = valid ? row_limit(a, p.g, t) : 0, limp = valid ? row_prefix_limit(p.g, t) : 0;
     const int all = __reduce_min_sync(0xFFFFFFFFu, valid ? lim : 0x7FFFFFFF);

@@ -335,7 +335,8 @@ typedef struct qg_kv_cache {
  *   - q_start and group_start rise and start at 0; all arrays are device memory, 4-byte
  *     aligned, and read by the kernels (a captured graph sees later contents).
  *   - Lengths past the page lists, negative lengths, page ids outside [0, n_pages) and new tokens
- *     without a slot set QG_EDEVICE_ID in the device status; nothing out of range is accessed.
+ *     without a slot set QG_EDEVICE_ID in the device status; nothing out of range is accessed,
+ *     whatever the arrays hold.
  * Limits: n_seqs, n_groups <= 65535, n_groups <= n_seqs, n_tokens <= 2^24.  A call on a batch
  * without tokens (without sequences for qg_beam_reorder) enqueues nothing. */
 typedef struct qg_kv_batch {

@@ -150,6 +150,43 @@ def test_peaked_scores(qg, big, n):
     assert ((got - ref).abs() <= tol).all(), ((got - ref).abs() / tol).max()
 
 
+@pytest.mark.parametrize("scale", [-0.07, 0.0, 1e-3])
+@pytest.mark.parametrize("n", [1, 100])
+def test_any_scale(qg, scale, n):
+    """A negative scale turns the order of the scores round, zero makes every weight equal."""
+    bt = Batch([n, 1], [200 + n, 40], 2, 128, 16, "f16", ((0, 2, 60),))
+    q = queries(bt.T, 8, 128, "f16")
+    got = attend(qg, bt, q, torch.float32, scale=scale).double()
+    ref, *terms = attention_ref(bt, q, scale)
+    assert ((got - ref).abs() <= attention_tol(ref, *terms, 128, "f16", torch.float32)).all()
+
+
+@pytest.mark.parametrize("n,G", [(1, 4), (3, 8)])
+def test_hundreds_of_sequences(qg, n, G):
+    """More segments than a block has threads, a few prompts among them, in three groups."""
+    B = 330
+    ns = [n] * B
+    for b in (0, 100, 101, 329):
+        ns[b] = 45
+    own = [ns[b] + (11 * b) % 60 for b in range(B)]
+    bt = Batch(ns, own, 1, 64, 8, "bf16", ((0, 90, 100), (90, 91, 17), (91, 320, 333)))
+    check(qg, bt, G, "bf16", "f32")
+
+
+@pytest.mark.parametrize("D", [64, 256])
+def test_starts_that_do_not_rise_reach_nothing(qg, D):
+    """Overlapping token ranges give segments more tokens than there are: reported, and the
+    workspace's end is kept (attend checks it)."""
+    bt = Batch([60] * 12, [100] * 12, 2, D, 16, "f16", ((0, 6, 50), (6, 12, 50)), stale=0.0)
+    q = queries(bt.T, 32, D, "f16")
+    bt.q_start = torch.tensor([0, 720] * 6 + [0], dtype=torch.int32, device="cuda")
+    attend(qg, bt, q, torch.float32)
+    bt.q_start = torch.tensor([720, -5] * 6 + [1 << 30], dtype=torch.int32, device="cuda")
+    bt.group_start = torch.tensor([9, -3, 1 << 30], dtype=torch.int32, device="cuda")
+    attend(qg, bt, q, torch.float32)
+    qg.device_status()
+
+
 @pytest.mark.parametrize("n", [1, 64])
 def test_infinite_scores_of_masked_keys(qg, n):
     """Keys past the length hold infinities and NaN, in the page's tail and in unused pages; the

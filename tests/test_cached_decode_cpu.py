@@ -181,3 +181,39 @@ def test_binding_checks(qg):
                  (i32(3), i32(3, 5), None, 3, i32(2), i32(1), i32(2, 2))):
         with pytest.raises(ValueError):
             qg.kv_batch(*args)
+
+
+def test_binding_refuses_tensors_of_other_types_and_shapes(qg):
+    """What the C side cannot see: a tensor of another type would be read past its end."""
+    torch = pytest.importorskip("torch")
+    k = torch.zeros((4, 16, 2, 64), dtype=torch.float16)
+    c = qg.kv_cache(k, k.clone())
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    b = qg.kv_batch(i32(3), i32(3, 5))
+    q, kv, qo, fr = torch.zeros(3, 256), torch.zeros(3, 128), torch.zeros((3, 4, 64), dtype=torch.float16), qg.rope_freqs(64, 1e4)
+    bad = [dict(q=q.double()), dict(q=q[:2]), dict(q=torch.zeros(3, 192)), dict(k=kv.half()), dict(v=kv[:, :64]),
+           dict(k=torch.zeros(128, 3).T), dict(q_out=qo.float()), dict(q_out=qo.transpose(0, 1)), dict(freqs=fr.float()),
+           dict(q_norm=torch.zeros(32)), dict(k_norm=torch.zeros(64, dtype=torch.float64)),
+           dict(q_out=torch.zeros(800, dtype=torch.float16))]
+    for kw in bad:
+        a = dict(q=q, k=kv, v=kv, q_out=qo, freqs=fr)
+        a.update(kw)
+        with pytest.raises(ValueError):
+            qg.kv_append(c, b, stream=0, **a)
+    ws = torch.zeros(1 << 20, dtype=torch.uint8)
+    for qq, oo in ((qo.float(), qo), (qo[:2], qo), (qo, torch.zeros(3, 300)), (qo, torch.zeros(4, 64, 3).permute(2, 0, 1)),
+                   (qo, qo.double())):
+        with pytest.raises(ValueError):
+            qg.attn_paged(c, b, qq, oo, 0.1, ws, stream=0)
+    f, i, u = (torch.zeros(2, 3, dtype=t) for t in (torch.float32, torch.int32, torch.uint8))
+    x = torch.zeros(6, 50)
+    for kw in (dict(logits=x.half()), dict(logits=x[:5]), dict(logits=torch.zeros(50, 6).T), dict(scores=f.double()),
+               dict(scores=f[0]), dict(out_scores=f.half()), dict(parents=i.long()), dict(tokens=f), dict(tokens=i[0]),
+               dict(done=i), dict(done=u[0]), dict(done_out=i)):
+        a = dict(logits=x, scores=f, N=2, W=3, out_scores=f, parents=i, tokens=i, workspace=ws, stream=0)
+        a.update(kw)
+        with pytest.raises(ValueError):
+            qg.beam_select(**a)
+    for p in (i32(2), i32(3).long(), torch.zeros(3)):
+        with pytest.raises(ValueError):
+            qg.beam_reorder(qg.kv_caches([k], [k.clone()]), b, p, 3, stream=0)
