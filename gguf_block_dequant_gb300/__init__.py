@@ -361,6 +361,18 @@ class KVBatch(ctypes.Structure):
                 ("prefix_len", ctypes.c_void_p), ("prefix_pages", ctypes.c_void_p)]
 
 
+_f32_i64 = None
+
+
+def _types():
+    global _f32_i64
+    if _f32_i64 is None:
+        import torch
+
+        _f32_i64 = (torch.float32, torch.int64)
+    return _f32_i64
+
+
 def _check(t, dtype, what):
     """A contiguous tensor of the named torch dtype (None passes)."""
     import torch
@@ -460,16 +472,18 @@ def kv_append(cache, batch, q, k, v, q_out, freqs, pairs=False, q_norm=None, k_n
     may be slices of one projection's; q_out [T][Hq][D] of the cache's type; freqs a device copy of
     rope_freqs (None: no rotation)."""
     T, D, Hkv = batch.n_tokens, cache.head_dim, cache.n_heads
-    Hq = 0 if q is None else q_out.numel() // max(T * D, 1) if T else Hkv
-    for t, what in ((q, "q"), (k, "k"), (v, "v"), (q_norm, "q_norm"), (k_norm, "k_norm")):
-        if t is not None and _dtype(t) != DT_F32:
-            raise ValueError(f"{what} must be f32")
-    if q is not None and (_dtype(q_out) != cache.dtype or not q_out.is_contiguous() or q_out.numel() != T * Hq * D):
-        raise ValueError("q_out must be contiguous, of the cache's type and have whole heads for every token")
-    _check(freqs, "int64", "freqs")
-    for t, what in ((q_norm, "q_norm"), (k_norm, "k_norm")):
-        if t is not None and (t.numel() != D or not t.is_contiguous()):
-            raise ValueError(f"{what} must have head_dim elements")
+    f32, i64 = _types()
+    if (k.dtype is not f32 or v.dtype is not f32 or (q is not None and q.dtype is not f32) or
+            (freqs is not None and (freqs.dtype is not i64 or not freqs.is_contiguous()))):
+        raise ValueError("q, k and v must be f32 and freqs contiguous int64")
+    Hq = 0
+    if q is not None:
+        Hq = q_out.numel() // (T * D) if T else Hkv
+        if _dtype(q_out) != cache.dtype or not q_out.is_contiguous() or q_out.numel() != T * Hq * D:
+            raise ValueError("q_out must be contiguous, of the cache's type and have whole heads for every token")
+    for t in (q_norm, k_norm):
+        if t is not None and (t.dtype is not f32 or t.numel() != D or not t.is_contiguous()):
+            raise ValueError("q_norm and k_norm must be contiguous f32 of head_dim elements")
     _call("qg_kv_append", ctypes.byref(cache), ctypes.byref(batch), Hq, _ptr(q), _rows(q, T, Hq * D, "q"), _ptr(k),
           _rows(k, T, Hkv * D, "k"), _ptr(v), _rows(v, T, Hkv * D, "v"), _ptr(q_norm), _ptr(k_norm), float(eps),
           _ptr(freqs), 0 if freqs is None else 2 * freqs.numel(), int(bool(pairs)), _ptr(q_out), _stream(stream))
