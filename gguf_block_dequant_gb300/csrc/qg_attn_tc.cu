@@ -414,10 +414,15 @@ QG_DEVICE void softmax(const AttnArgs &a, WideBars *bar, int s, int warp4, int l
     // were rounded.
     constexpr float RAISE = BF16 ? 0.f : 7.f;
     float m = -INFINITY, ref = -INFINITY, l = 0.f;
+    const bool idle = !__any_sync(0xFFFFFFFFu, valid);  // no row of this warp is anyone's: whatever its weights are
     const int step = p.paired ? 1 : 2, first = p.paired ? p.j0 : p.j0 + s, j1 = p.j1, jp = p.jp;
     for (int j = first; j < j1; j += step) {
       if (!warp_wait(&bar->s_full[s], n_s++ & 1, abort)) return;
       tc_fence_after();
+      if (idle) {
+        if (lane == 0) mbar_arrive(&bar->p_full[s]);
+        continue;
+      }
       const bool pre = j < jp;
       const int key0 = (pre ? j : j - jp) * kWideKeys;
       const int left = (pre ? limp : lim) - key0;  // keys of the tile that the row sees

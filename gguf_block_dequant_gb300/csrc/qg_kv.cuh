@@ -36,29 +36,36 @@ QG_DEVICE int kv_own_len(const KvBatch &a, int shift, int b) {
   return kv_clamp(__ldg(a.kv_len + b), 0, kv_cap(a.max_pages, shift));
 }
 
-// the largest i in [lo, hi) with f(i) <= x (f rising), or lo - 1 when there is none
-template <typename F>
-QG_DEVICE int kv_search(int lo, int hi, int x, F f) {
-  int a = lo - 1, b = hi;
-  while (b - a > 1) {
-    const int m = a + (b - a) / 2;
-    if (f(m) <= x) a = m;
-    else b = m;
+// the i < n with start[i] <= x < start[i + 1] (start rising, n + 1 entries), -1 when there is none.
+// Each round loads seven places at once: the search costs load latencies, one per factor of
+// eight.
+QG_DEVICE int kv_search(const int32_t *start, int n, int x) {
+  int lo = -1, hi = n + 1;  // start[lo] <= x < start[hi], as far as is known
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 7) / 8;
+    int v[7];
+#pragma unroll
+    for (int i = 0; i < 7; ++i) {
+      const int at = lo + (i + 1) * step;
+      v[i] = at < hi ? __ldg(start + at) : 0x7FFFFFFF;
+    }
+    int below = 0;  // places up to the first one above x
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+      if (below == i && v[i] <= x && lo + (i + 1) * step < hi) below = i + 1;
+    const int base = lo;
+    lo = base + below * step;
+    hi = min(hi, base + (below + 1) * step);
   }
-  return a;
+  return lo < n ? lo : -1;
 }
 // sequence of token t, -1 when no sequence holds it
 QG_DEVICE int kv_seq_of(const KvBatch &a, int t) {
   if (!a.q_start) return t < a.B ? t : -1;
-  const int b = kv_search(0, a.B, t, [&](int i) { return __ldg(a.q_start + i); });
-  return b >= 0 && t < __ldg(a.q_start + b + 1) ? b : -1;
+  return kv_search(a.q_start, a.B, t);
 }
 // group of sequence b, -1 when it has none
-QG_DEVICE int kv_group_of(const KvBatch &a, int b) {
-  if (a.G == 0) return -1;
-  const int g = kv_search(0, a.G, b, [&](int i) { return __ldg(a.group_start + i); });
-  return g >= 0 && b < __ldg(a.group_start + g + 1) ? g : -1;
-}
+QG_DEVICE int kv_group_of(const KvBatch &a, int b) { return a.G ? kv_search(a.group_start, a.G, b) : -1; }
 
 // host checks shared by the calls; on QG_OK *pool and *kb are filled.  prefix: the call reads
 // the prefix page lists.  tokens: the call has token rows (q_start, n_tokens).
