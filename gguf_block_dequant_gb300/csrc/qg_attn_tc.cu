@@ -23,13 +23,15 @@
 // the output in tensor memory is hardly ever touched between the products.
 //
 // Measured (one GB300, whole calls replayed from a graph): prompts of 7832 tokens under a prefix of
-// 4001, 32 heads over 8 of 128, bf16: 594 us, 1.17 PFLOP/s (0.61 of the measured cuBLAS rate); 64
+// 4001, 32 heads over 8 of 128, bf16: 563 us, 1.23 PFLOP/s (0.64 of the measured cuBLAS rate); 64
 // one-token sequences under a prefix of 32768 (512 rows a cached head): 74 us, of which this
-// kernel 37.  What bounds it: a pair of 128-row tiles and 128 keys takes about 3700 cycles, of
+// kernel 37.  What bounds it: a pair of 128-row tiles and 128 keys takes about 3500 cycles, of
 // which the products alone need 3080 (2048 at the tensor cores' full rate: Q K^T reads both
 // operands from shared memory, 8 KB for 64 cycles' work) and a stream's softmax about 2000.
-// Tried and slower: an MMA warp per stream (757 us), weights handed over in halves (645), more
-// chains for the maximum and sum (620).
+// The issuing warp's own instructions count: asking for the tiles' barriers while products are
+// queued, and letting go of V before the next scores, took 580 us to 563.  Tried and slower: an MMA
+// warp per stream (594 to 757), weights handed over in halves (636 to 645), more chains for the
+// maximum and sum (611 to 620), test_wait for try_wait (579 to 612).
 #include <cuda.h>
 
 #include <mutex>
@@ -341,27 +343,31 @@ QG_DEVICE void issue_mma(uint32_t smem, WideBars *bar, int lane) {
     if (!wait(&bar->q_full, np & 1)) return;
     if (paired) {
       for (int j = 0; j <= n; ++j) {
-        if (j < n && !landed(kt)) return;
-        if (j > 0 && !landed(vt)) return;
+        // The tiles' barriers are asked while products are queued, not between a stream's weights and
+        // its products: K_j before its first scores, V_j (the next to be used) before its second.
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           if (j > 0) {
             if (!weights(s, j == 1)) return;
             output(s, vt.st, j == 1);
             if (j == n) tc_commit_el(el, &bar->o_full[s]);
+            if (s == 1) {
+              release(vt);
+              vt.next();
+              vt.next();
+            }
           }
-          if (j < n) scores(s, s, kt.st);
+          if (j < n) {
+            if (s == 0 && !landed(kt)) return;
+            if (s == 1 && !landed(vt)) return;
+            scores(s, s, kt.st);
+          }
         }
         if (j < n) {
           release(kt);
           kt.next();
           kt.next();
           if (j == n - 1) tc_commit_el(el, &bar->q_empty);
-        }
-        if (j > 0) {
-          release(vt);
-          vt.next();
-          vt.next();
         }
       }
     } else {
