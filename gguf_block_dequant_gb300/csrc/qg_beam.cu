@@ -8,9 +8,9 @@
 // the first chunk hardly any value joins.  The second joins a request's slices: the row sums in
 // 64 bits, each row's K best, then the K best of W*K candidates ranked in 64 bits.
 //
-// Measured: 16 requests of 8 beams over 151936 tokens (72 MB) 35 us, floor 10.7 (a chunk's barriers
-// and 12 instructions a value are what it spends above the bytes); one request of 4 beams 10.7
-// us, two launches.
+// Measured: 16 requests of 8 beams over 151936 tokens (72 MB) 27 us, floor 10.7 (what it spends above
+// the bytes: 12 instructions a value, a chunk's barriers, 256 CTAs on 152 SMs, the merge's 5 us);
+// one request of 4 beams 10.2 us, two launches.
 #include <math.h>
 
 #include <algorithm>
@@ -194,11 +194,17 @@ __global__ void __launch_bounds__(kThreads, 2) select_slice_kernel(const SelectA
     }
     if (have + (exact ? K : hits * kPT) > kList) thin(sh, a.K);
     if (!exact) {
+      // few threads have any, and those mostly one: a mask of them, then each read again (16 copies of
+      // the append took two fifths of the kernel's time)
       if (any && mo >= t) {
+        const float tf = t ? ord_val(t) : -INFINITY;
+        uint32_t mask = 0;
 #pragma unroll
-        for (int i = 0; i < kPT; ++i) {
-          const int e = chunk_elem(i);
-          if (e < n && ord_of(v[i]) >= t) sh.list[atomicAdd(&sh.count, 1)] = key_of(v[i], static_cast<uint32_t>(base + c0 + e));
+        for (int i = 0; i < kPT; ++i) mask |= (chunk_elem(i) < n && v[i] >= tf ? 1u : 0u) << i;
+        for (; mask; mask &= mask - 1) {
+          const int e = chunk_elem(__ffs(static_cast<int>(mask)) - 1);
+          const float f = fmaxf(__ldg(x + c0 + e), -INFINITY);
+          sh.list[atomicAdd(&sh.count, 1)] = key_of(f, static_cast<uint32_t>(base + c0 + e));
         }
       }
     } else {
@@ -308,8 +314,31 @@ __global__ void __launch_bounds__(kMergeThreads) select_merge_kernel(const Selec
       }
       continue;
     }
-    // lane's lists: positions and heads
     const unsigned long long *kr = lists + w * per_row;
+    if (per_row <= 64) {  // few keys: each one's rank is the number of larger ones
+      for (int i = lane; i < a.K; i += 32) {
+        val[w * a.K + i] = -INFINITY;
+        tok[w * a.K + i] = 0xFFFFFFFFu;
+      }
+      __syncwarp();
+      const unsigned long long k0 = lane < per_row ? kr[lane] : 0ull, k1 = lane + 32 < per_row ? kr[lane + 32] : 0ull;
+      int r0 = 0, r1 = 0;
+      for (int j = 0; j < per_row; ++j) {
+        const unsigned long long k = kr[j];
+        r0 += k > k0;
+        r1 += k > k1;
+      }
+      if (k0 && r0 < a.K) {
+        val[w * a.K + r0] = key_val(k0);
+        tok[w * a.K + r0] = key_idx(k0);
+      }
+      if (k1 && r1 < a.K) {
+        val[w * a.K + r1] = key_val(k1);
+        tok[w * a.K + r1] = key_idx(k1);
+      }
+      continue;
+    }
+    // lane's lists: positions and heads
     constexpr int kHeads = kMaxSlices / 32;
     int at[kHeads];
     unsigned long long head[kHeads];
@@ -349,20 +378,27 @@ __global__ void __launch_bounds__(kMergeThreads) select_merge_kernel(const Selec
     rank[i] = tok[i] == 0xFFFFFFFFu ? 0ull : u >> 63 ? ~u : u | 0x8000000000000000ull;
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < total; i += kMergeThreads) {
-    const unsigned long long x = rank[i];
-    if (x == 0) continue;
+  // eight threads count a candidate's betters
+  const int part = static_cast<int>(threadIdx.x) & 7;
+  for (int i0 = 0; i0 < total; i0 += kMergeThreads / 8) {
+    const int i = i0 + (static_cast<int>(threadIdx.x) >> 3);
+    const unsigned long long x = i < total ? rank[i] : 0ull;
     const int w = i / a.K;
-    const uint32_t v = tok[i];
+    const uint32_t v = i < total ? tok[i] : 0u;
     int r = 0;
-    for (int j = 0; j < total; ++j) {
-      const unsigned long long y = rank[j];
-      r += y > x;
-      if (y == x && j != i) {  // equal: the lowest beam, then the lowest token
-        const int wj = j / a.K;
-        r += wj < w || (wj == w && tok[j] < v);
+    if (x) {
+      for (int j = part; j < total; j += 8) {
+        const unsigned long long y = rank[j];
+        r += y > x;
+        if (y == x && j != i) {  // equal: the lowest beam, then the lowest token
+          const int wj = j / a.K;
+          r += wj < w || (wj == w && tok[j] < v);
+        }
       }
     }
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) r += __shfl_xor_sync(0xFFFFFFFFu, r, o);
+    if (x == 0 || part) continue;
     if (r < a.K) {
       const size_t o = static_cast<size_t>(req) * a.K + r;
       const unsigned long long u = x >> 63 ? x & 0x7FFFFFFFFFFFFFFFull : ~x;
@@ -375,8 +411,9 @@ __global__ void __launch_bounds__(kMergeThreads) select_merge_kernel(const Selec
   }
 }
 
-// Slices of a row: two CTAs for every SM in all, but no slice under 4096 values (4 rows of 151936: 12.2 us at 2048, 10.7 at 4096, 10.9 at 8192; 128 rows: one
-// CTA an SM 43 us, two 35, three 41), and lists that
+// Slices of a row: two CTAs for every SM in all, but no slice under 4096 values (4 rows of 151936: 12.2 us at 2048, 10.7 at 4096,
+// 10.9 at 8192; 128 rows: one CTA an SM 43 us, two 35, three 41; before the appends were made
+// cheaper), and lists that
 // fit the merge's shared memory.
 struct Slices {
   int S, slice;
