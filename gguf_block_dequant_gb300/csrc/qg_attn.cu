@@ -7,9 +7,9 @@
 // asynchronous copies in flight on every SM and spends few instructions per byte.
 //
 // Measured (one GB300, calls replayed from a graph; floor: bytes at the measured copy bandwidth):
-//   64 ragged sequences of up to 8191 tokens, 8 cached heads of 128, bf16   197 us, floor 177 (the kernel
+//   64 ragged sequences of up to 8191 tokens, 8 cached heads of 128, bf16   196 us, floor 177 (the kernel
 //     alone 185: 6.5 TB/s, 96 % of the copy)
-//   one sequence of 4097 tokens, f16 cache, f32 output                      15.9 us, floor 2.5: two
+//   one sequence of 4097 tokens, f16 cache, f32 output                      16.5 us, floor 2.5: two
 //     launches whose fixed parts (the scan, the look-ups, cold code) take most of it
 #include <math.h>
 
