@@ -140,6 +140,7 @@ __global__ void __launch_bounds__(kThreads, 2) select_slice_kernel(const SelectA
   uint32_t tau = 0;                    // order word of the K-th best
   float v[kPT], w[kPT];
   load_chunk(a, x, len, w);
+  __syncthreads();  // the list is empty before any thread asks how long it is
   for (int c0 = 0; c0 < len; c0 += kChunk) {
     const int n = len - c0;
 #pragma unroll

@@ -192,3 +192,27 @@ def test_picks_feed_the_next_call(qg):
     qg.beam_select(x, s, N, W, *o, ws, stream=st)
     torch.cuda.synchronize()
     assert all(torch.equal(a.cpu(), b) for a, b in zip(o, want))
+
+
+def test_shared_memory_of_an_earlier_kernel(qg):
+    """The list of candidates starts empty whatever a kernel before left in its place: attention fills
+    every SM's shared memory with a large pattern, the selection follows at once."""
+    pat = torch.full((64, 64, 8, 128), 0x7BFF, dtype=torch.int16, device="cuda").view(torch.float16)
+    cache = qg.kv_cache(pat, pat)
+    lens = torch.full((4,), 1000, dtype=torch.int32, device="cuda")
+    batch = qg.kv_batch(lens, torch.arange(64, dtype=torch.int32, device="cuda").view(4, 16))
+    q = torch.zeros((4, 8, 128), dtype=torch.float16, device="cuda")
+    out = torch.empty((4, 8, 128), device="cuda")
+    aws = torch.empty(qg.attn_workspace_size(cache, batch, 8), dtype=torch.uint8, device="cuda")
+    N, W, K, V = 8, 8, 8, 30000
+    x, s = rand(N, W, V, seed=12)
+    ref = ref_select(x, s, N, W, K)
+    ws = torch.empty(qg.beam_workspace_size(N, W, K, V), dtype=torch.uint8, device="cuda")
+    outs = [[torch.empty((N, K), device="cuda"), *[torch.empty((N, K), dtype=torch.int32, device="cuda") for _ in range(2)]]
+            for _ in range(40)]
+    for o in outs:
+        qg.attn_paged(cache, batch, q, out, 0.1, aws)
+        qg.beam_select(x, s, N, W, *o, ws)
+    torch.cuda.synchronize()
+    for o in outs:
+        assert torch.equal(o[1].cpu(), ref[1]) and torch.equal(o[2].cpu(), ref[2])
