@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(NarrowCfg<D>::NW * 32, 1) attn_narrow_kernel(c
       const int row = qr + 8 * e;
       if (row >= nrows) continue;
       if (alone) {
-        const float inv = ls > 0.f ? 1.0f / ls : 0.f;
+        const float inv = ls == 0.f ? 0.f : 1.0f / ls;
         const int t = g.t0 + tile_t0 + row / a.Gq;
         const size_t base = (static_cast<size_t>(t) * a.Hq + cur.h * a.Gq + row % a.Gq) * D + 2 * qc;
 #pragma unroll
@@ -364,7 +364,7 @@ struct Acc {
 };
 template <int NV>
 QG_DEVICE void acc_add(Acc<NV> &x, float m, float l, const float (&o)[NV]) {
-  if (m == -INFINITY) return;  // nothing seen (and o not written)
+  if (l == 0.f) return;  // nothing seen (and o not written); the sum of NaN scores is NaN, under a maximum of -inf
   const float mn = fmaxf(x.m, m);
   const float fa = ex2(x.m - mn), fb = ex2(m - mn);
   x.m = mn;
@@ -432,7 +432,7 @@ QG_DEVICE void acc_clear(Acc<NV> (&x)[R]) {
 template <int D, bool BF16, bool OUT32>
 QG_DEVICE void write_row(const AttnArgs &a, int t, int hq, int lane, const Acc<D / 32> &x) {
   constexpr int NV = D / 32;
-  const float inv = x.l > 0.f ? 1.0f / x.l : 0.f;
+  const float inv = x.l == 0.f ? 0.f : 1.0f / x.l;
   const size_t base = (static_cast<size_t>(t) * a.Hq + hq) * D + lane * NV;
   if constexpr (OUT32) {
 #pragma unroll

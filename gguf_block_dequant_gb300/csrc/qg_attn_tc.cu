@@ -518,7 +518,7 @@ QG_DEVICE void softmax(const AttnArgs &a, WideBars *bar, int s, int warp4, int l
       if (!warp_wait(&bar->o_full[s], n_o++ & 1, abort)) return;
       tc_fence_after();
     }
-    const float inv = p.alone ? (l > 0.f ? 1.0f / l : 0.f) : 1.0f;
+    const float inv = !p.alone ? 1.0f : l == 0.f ? 0.f : 1.0f / l;
     const size_t prow = p.slot * kWideRows + s * kWideHalf + row;
     if (valid && !p.alone) a.wide.part_ml[prow] = make_float2(ref, l);
     if (any) {

@@ -374,7 +374,8 @@ QG_API qg_status qg_kv_append(const qg_kv_cache *cache, const qg_kv_batch *batch
 /* Causal attention over the cache: for new token t at position p and query head h,
  *   out[t][h] = sum_j softmax_j(scale * q[t][h] . K[j][h / (Hq / n_heads)]) V[j][..],
  * j over the positions 0 .. p of its group's prefix and its own tokens.  A group's prefix is read
- * once for all its sequences.  A token that sees no key (p < 0) gets zeros.
+ * once for all its sequences.  A token that sees no key (p < 0), or only scores of -inf, gets zeros; one
+ * that sees a NaN or +inf score gets NaN.
  *   - q: device, the cache's type, head h of token t at q + t*q_stride + h*D (q_stride in elements,
  *     a multiple of 8, at least Hq*D), 16-byte aligned.
  *   - out: device [n_tokens][Hq][D], 16-byte aligned, of out_dtype: QG_DT_F32 or the cache's type.
