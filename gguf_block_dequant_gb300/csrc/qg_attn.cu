@@ -32,6 +32,28 @@ struct NarrowCfg {
   static constexpr uint32_t SMEM = NW * NST * 2 * TILE;       // 192 KB
 };
 
+// The products multiply every value of a tile by every row's weight, and zero times infinity is NaN.  So
+// where some row must not see a key that is there, infinite and NaN values of the tile leave it
+// before the product and are added to the rows that do see them (by the warp; its lanes' columns
+// are 8 d + 2 qc and the one after; 16 keys from key0 on; lim: keys that the lane's two rows see).
+template <int D, bool BF16>
+QG_DEVICE void add_nonfinite(const uint8_t *v, int key0, int qc, const int (&lim)[2], float (&o)[D / 8][4]) {
+#pragma unroll 1
+  for (int k = 0; k < kNarrowKeys; ++k) {
+#pragma unroll
+    for (int d = 0; d < D / 8; ++d) {
+      const uint32_t w = *reinterpret_cast<const uint32_t *>(v + k * (D * 2) + (d ^ (k & 7)) * 16 + 4 * qc);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        if (!nonfinite16<BF16>(c ? w >> 16 : w)) continue;
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (key0 + k < lim[e]) o[d][2 * e + c] += c ? hi16<BF16>(w) : lo16<BF16>(w);
+      }
+    }
+  }
+}
+
 // Each warp is a worker of its own: it walks its pieces with a private ring of key and value
 // tiles (16 keys, cp.async, no barrier wider than the warp), the piece's 16 query rows in
 // mma fragments, and writes the piece's unnormalised output, maximum and sum.  mma.sync
@@ -219,6 +241,17 @@ __global__ void __launch_bounds__(NarrowCfg<D>::NW * 32, 1) attn_narrow_kernel(c
         }
       }
       // ---- o += p V
+      if (all < min(g.len, 16 * j + 16)) {
+        uint4 *vt = reinterpret_cast<uint4 *>(smem + (vb - smem_u32(smem)));
+        uint32_t some = 0;
+        for (int i = lane; i < kNarrowKeys * CH; i += 32) some |= any_nonfinite<BF16>(vt[i]);
+        if (__any_sync(0xFFFFFFFFu, some)) {
+          add_nonfinite<D, BF16>(reinterpret_cast<const uint8_t *>(vt), 16 * j, qc, lim, o);
+          __syncwarp();
+          for (int i = lane; i < kNarrowKeys * CH; i += 32) vt[i] = make_finite<BF16>(vt[i]);
+          __syncwarp();
+        }
+      }
       const int vrow = (lane & 7) + ((mat & 1) << 3);
       const uint32_t va = vb + static_cast<uint32_t>(vrow) * (D * 2);
 #pragma unroll
@@ -564,6 +597,7 @@ struct Plan {
   long long n_slots, w_slots;       // pieces the two lines can have
   size_t n_pos, n_unit, n_o, n_ml;  // offsets of the narrow line's arrays
   size_t w_pos, w_unit, w_o, w_ml;  // of the wide line's
+  size_t flags;                     // of value_flags
   int wide_workers, narrow_workers;
 };
 
@@ -604,6 +638,7 @@ Plan make_plan(const KvPool &pool, const KvBatch &b, int Gq, int sms) {
     p.w_unit = take((nseg + 1) * 4);
     p.w_ml = take(static_cast<size_t>(sw) * kWideRows * 8);
     p.w_o = take(static_cast<size_t>(sw) * kWideRows * pool.D * 4);
+    p.flags = take(b.q_start ? static_cast<size_t>(2 * pool.Hkv) * ((b.T + 31) / 32) * 4 : 0);
   }
   p.bytes = at;
   return p;
@@ -627,6 +662,10 @@ qg_status attn_run(const AttnArgs &a, int sms, cudaStream_t s) {
   using C = NarrowCfg<D>;
   auto narrow = attn_narrow_kernel<D, BF16, OUT32>;
   if (!set_smem_attr(reinterpret_cast<const void *>(narrow), C::SMEM)) return QG_ECUDA;
+  if (a.value_flags) {
+    const qg_status st = attn_flags_launch(a, BF16, s);
+    if (st != QG_OK) return st;
+  }
   if (launch_pdl(narrow, dim3(static_cast<unsigned>(sms)), dim3(C::NW * 32), C::SMEM, s, a) != cudaSuccess)
     return QG_ECUDA;
   if (a.wide.workers) {
@@ -720,6 +759,8 @@ qg_status qg_attn_paged(const qg_kv_cache *cache, const qg_kv_batch *batch, int 
     a.wide = line(kWideRows, kWideShift, p.wide_workers, p.w_slots, p.w_pos, p.w_unit, p.w_o, p.w_ml);
     a.wide.lo = a.narrow.tpt;
     a.wide.hi = INT32_MAX;
+    // without q_start no token comes after another of its sequence
+    if (a.b.q_start) a.value_flags = reinterpret_cast<uint32_t *>(ws + p.flags);
   }
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool bf16 = cache->dtype == QG_DT_BF16;

@@ -52,6 +52,7 @@ struct AttnArgs {
   int Hq, Gq, D;
   int out32;
   int long_tokens;       // sequences of more new tokens are long
+  uint32_t *value_flags; // [2][heads][tokens / 32] (qg_attn_tc.cu); null without q_start or a wide line
   Line narrow, wide;     // wide.workers == 0: the narrow line has every segment, nothing is long
 };
 
@@ -367,6 +368,7 @@ QG_DEVICE bool seg_whole(const AttnArgs &a, const Seg &g, int b) {
 }
 
 // attention over many rows per segment on the tcgen05 tensor cores (qg_attn_tc.cu)
+qg_status attn_flags_launch(const AttnArgs &a, bool bf16, cudaStream_t s);
 qg_status attn_wide_launch(const AttnArgs &a, bool bf16, cudaStream_t s);
 bool attn_wide_supported(int D);
 

@@ -59,6 +59,7 @@ constexpr uint32_t kStagePitch = 80, kStageBytes = 32 * kStagePitch;
 QG_DEVICE void sts_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
+constexpr uint32_t BAR_BYTES = 640;
 constexpr uint32_t SCAN_BYTES = (sizeof(LineScan<kThreads>) + 15) / 16 * 16;
 
 template <int D>
@@ -69,7 +70,7 @@ struct WideCfg {
   static constexpr uint32_t OFF_Q = 0;
   static constexpr uint32_t OFF_KV = 2 * TILE;
   static constexpr uint32_t OFF_BAR = OFF_KV + NST * TILE;
-  static constexpr uint32_t OFF_SCAN = OFF_BAR + 512;
+  static constexpr uint32_t OFF_SCAN = OFF_BAR + BAR_BYTES;
   static constexpr uint32_t OFF_STAGE = OFF_SCAN + SCAN_BYTES;
   static constexpr uint32_t SMEM = OFF_STAGE + kSoftWarps * kStageBytes + 1024;  // + alignment slack
   static_assert(SMEM <= 226 * 1024, "one CTA's shared memory");
@@ -97,7 +98,10 @@ struct Piece {
   int j0, j1, jp;  // key tiles; the first jp of the unit are those of a long sequence's prefix
   bool paired;     // two halves of rows; otherwise the streams take the key tiles in turn
   bool alone;      // the piece is all there is of its rows
+  bool dirty;      // z0, z1 hold something
   long long slot;  // -1: the workspace has none (token starts that do not rise)
+  int z0[2], z1[2];  // of a long sequence's prefix and of the list: first key and end of what loses its infinite
+                     // and NaN values (nothing: equal)
 };
 struct WideBars {
   Piece piece[kPieces];
@@ -160,6 +164,40 @@ QG_DEVICE bool warp_wait(uint64_t *b, uint32_t parity, volatile int *abort) {
 }
 
 // ---- the walk -----------------------------------------------------------------------------------
+// Zero times an infinite or NaN value is not zero.  So where some row of a unit must not see a key,
+// such values of its leave the tile before the product, and the softmax warps add them to the rows
+// that do see it.  The keys in question are those at the new tokens' own positions, since a token
+// sees all before its own: value_flags_kernel has a bit for each.
+//
+QG_DEVICE bool any_flag(const AttnArgs &a, int row, int ta, int tb, int lane) {  // of tokens [ta, tb), and of a few around them
+  const uint32_t *flags = a.value_flags + static_cast<size_t>(row) * ((a.b.T + 31) / 32);
+  uint32_t f = 0;
+#pragma unroll 1
+  for (int w = (ta >> 5) + lane; 32 * w < tb; w += 32) f |= __ldcg(flags + w);
+  return __any_sync(0xFFFFFFFFu, f != 0);
+}
+QG_DEVICE void piece_values(const AttnArgs &a, Piece *p, int lane) {
+  p->dirty = false;
+  p->z0[0] = p->z1[0] = p->z0[1] = p->z1[1] = 0;
+  if (!a.value_flags) return;
+  const Seg &g = p->g;
+  const int h = p->h, te = g.t0 + g.nt;
+  // own positions: token t has key t + d
+  const int d = g.len - g.nt - g.t0;
+  const int ta = max(p->t0 + 1, (max(p->j0 - p->jp, 0) << kWideShift) - d), tb = min(te, ((p->j1 - p->jp) << kWideShift) - d);
+  if (!g.prefix && any_flag(a, a.pool.Hkv + h, ta, tb, lane)) {
+    p->dirty = true;
+    p->z0[1] = max(ta + d, 0);
+    p->z1[1] = tb + d;
+  }
+  // positions in a prefix, of tokens before their sequence's first slot: under a shared one the unit's
+  // tokens and those that follow of its last sequence, else the long sequence's.  Rare: all of the prefix is taken.
+  if ((g.prefix || (g.plen && g.len < g.nt)) &&
+      any_flag(a, h, p->t0, g.prefix ? min(te, p->t0 + p->tokens + a.wide.tpt / 2) : te, lane)) {
+    p->dirty = true;
+    (g.prefix ? p->z1[1] : p->z1[0]) = g.prefix ? g.len : g.plen;
+  }
+}
 QG_DEVICE void walk_line(const AttnArgs &a, Walk walk, WideBars *bar, int lane) {
   volatile int *abort = &bar->abort;
   for (uint32_t n = 0;; ++n) {
@@ -167,6 +205,7 @@ QG_DEVICE void walk_line(const AttnArgs &a, Walk walk, WideBars *bar, int lane) 
     const bool more = walk_next(a, &walk, &p);
     if (!more) p.j0 = p.j1 = 0;
     else if (p.slot < 0 && !p.alone && lane == 0) atomicOr(&g_qg_status_attn_tc, QG_STATUS_BIT_ID);
+    if (more) piece_values(a, &p, lane);
     const uint32_t i = n % kPieces;
     if (!warp_wait(&bar->piece_empty[i], ((n / kPieces) & 1) ^ 1, abort)) return;
     if (lane == 0) {
@@ -211,7 +250,7 @@ struct WideMaps {
   CUtensorMap q, k, v;
 };
 
-template <int D>
+template <int D, bool BF16>
 QG_DEVICE void produce(const AttnArgs &a, const WideMaps &maps, uint8_t *smem, WideBars *bar, int lane) {
   using C = WideCfg<D>;
   constexpr int H = D / 64;              // 64-element halves of a row
@@ -253,11 +292,16 @@ QG_DEVICE void produce(const AttnArgs &a, const WideMaps &maps, uint8_t *smem, W
       for (int kv = 0; kv < 2; ++kv, ring.next()) {
         const int st = ring.st;
         if (!warp_wait(&bar->empty[st], ring.par ^ 1u, abort)) return;
-        // values past the last key become zeros: what their rows hold (or the stage held) could
-        // be infinite, and zero times that is not zero.  Keys may be anything: their scores are
+        // a value tile is held back when values past the last key are to become zeros (whatever their
+        // rows or the stage held), or infinite and NaN ones.  Keys may be anything: their scores are
         // replaced.
-        const bool tail = kv && left < kWideKeys;
-        uint64_t *land = tail ? &bar->tail : &bar->full[st];
+        int z0 = 0, z1 = 0;  // rows of the latter
+        if (kv && p.dirty) {
+          z0 = max((pre ? p.z0[0] : p.z0[1]) - key0, 0);
+          z1 = min((pre ? p.z1[0] : p.z1[1]) - key0, left);
+        }
+        const bool held = kv && (left < kWideKeys || z0 < z1);
+        uint64_t *land = held ? &bar->tail : &bar->full[st];
         if (lane == 0) mbar_arrive_expect_tx(land, static_cast<uint32_t>(boxes * H * rows) * 128u);
         __syncwarp();
         const uint32_t off = C::OFF_KV + static_cast<uint32_t>(st) * C::TILE;
@@ -272,12 +316,14 @@ QG_DEVICE void produce(const AttnArgs &a, const WideMaps &maps, uint8_t *smem, W
                      p.h, page[i], land);
           }
         }
-        if (tail) {
+        if (held) {
           if (!warp_wait(&bar->tail, ntail++ & 1, abort)) return;
 #pragma unroll
-          for (int h = 0; h < H; ++h)
-            for (int x = left * 8 + lane; x < kWideKeys * 8; x += 32)
-              *reinterpret_cast<uint4 *>(smem + off + h * C::HALF + x * 16) = make_uint4(0, 0, 0, 0);
+          for (int h = 0; h < H; ++h) {
+            uint4 *v = reinterpret_cast<uint4 *>(smem + off + h * C::HALF);
+            for (int x = left * 8 + lane; x < kWideKeys * 8; x += 32) v[x] = make_uint4(0, 0, 0, 0);
+            for (int x = z0 * 8 + lane; x < z1 * 8; x += 32) v[x] = make_finite<BF16>(v[x]);
+          }
           fence_proxy_async_smem();  // stored through the generic proxy, read by the tensor cores
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar->full[st]);
@@ -395,6 +441,51 @@ QG_DEVICE void issue_mma(uint32_t smem, WideBars *bar, int lane) {
 }
 
 // ---- softmax ----------------------------------------------------------------------------------
+// Adds the values that left the piece's tiles to the rows that see them (infinite
+// or NaN: whatever their positive weight is).  Rare, and read from the cache once more.  lim_*: keys
+// that this thread's row sees of a long sequence's prefix and of the list.
+template <int D, bool BF16>
+__device__ __noinline__ void add_zeroed(const AttnArgs &a, const Piece &p, uint32_t to, int s, int lim_prefix, int lim_list) {
+  const int shift = a.pool.page_shift;
+#pragma unroll 1
+  for (int part = 0; part < 2; ++part) {
+    const int lim = part ? lim_list : lim_prefix;
+    const int z0 = p.z0[part], z1 = min(p.z1[part], __reduce_max_sync(0xFFFFFFFFu, lim));
+    const int32_t *table = part ? p.g.table : p.g.ptable;
+#pragma unroll 1
+    for (int c = 0; c < D && z0 < z1; c += 16) {
+      float o[16];
+      tmem_ld16(to + c, o);
+#pragma unroll 1
+      for (int key = z0; key < z1; ++key) {
+        const int j = (key >> kWideShift) + (part ? p.jp : 0);
+        if (!p.paired && ((j - p.j0) & 1) != s) continue;  // the other stream's tile
+        const int page = __ldg(table + (key >> shift));
+        if (page < 0 || page >= a.pool.n_pages) continue;
+        const uint4 *v = reinterpret_cast<const uint4 *>(a.pool.v + page * a.pool.page_stride +
+                                                         (key & ((1 << shift) - 1)) * a.pool.token_stride +
+                                                         p.h * a.pool.head_stride + c);
+        const bool sees = key < lim;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint4 q = __ldg(v + i);
+          const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (sees && nonfinite16<BF16>(w[e])) o[8 * i + 2 * e] += lo16<BF16>(w[e]);
+            if (sees && nonfinite16<BF16>(w[e] >> 16)) o[8 * i + 2 * e + 1] += hi16<BF16>(w[e]);
+          }
+        }
+      }
+      uint32_t r[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(o[i]);
+      tmem_st16(to + c, r);
+      tmem_st_wait();
+    }
+  }
+}
+
 template <int D, bool BF16, bool OUT32>
 QG_DEVICE void softmax(const AttnArgs &a, WideBars *bar, int s, int warp4, int lane, uint32_t stage) {
   volatile int *abort = &bar->abort;
@@ -517,6 +608,7 @@ QG_DEVICE void softmax(const AttnArgs &a, WideBars *bar, int s, int warp4, int l
     if (any) {
       if (!warp_wait(&bar->o_full[s], n_o++ & 1, abort)) return;
       tc_fence_after();
+      if (p.dirty) add_zeroed<D, BF16>(a, p, to, s, limp, lim);
     }
     const float inv = !p.alone ? 1.0f : l == 0.f ? 0.f : 1.0f / l;
     const size_t prow = p.slot * kWideRows + s * kWideHalf + row;
@@ -568,6 +660,59 @@ QG_DEVICE void softmax(const AttnArgs &a, WideBars *bar, int s, int warp4, int l
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar->o_empty[s]);
     }
+  }
+}
+
+// A bit for each new token and cached head: the value at the token's position has infinite or NaN elements.
+// Positions in the prefix (of tokens before their sequence's first slot) and own ones have words of
+// their own, [2][heads][tokens / 32].  A warp per 32 tokens and head; reads the new tokens' values once (prompts of
+// 7832 tokens, 16 MB: the call takes 10 us longer for it, a launch and a chain of look-ups more than the bytes).
+// Looked up inside the wide kernel, a piece ahead or in the landed tiles, it cost the call 40 to 120 us.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(256) value_flags_kernel(const __grid_constant__ AttnArgs a) {
+  constexpr int CH = D / 8, RPL = 32 / CH;  // 16-byte chunks of a row, rows a load of the warp takes
+  const int lane = threadIdx.x & 31, words = (a.b.T + 31) / 32;
+  pdl_wait();
+  pdl_launch_dependents();
+  const long long item = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (item >= static_cast<long long>(words) * a.pool.Hkv) return;
+  const int h = static_cast<int>(item / words), w = static_cast<int>(item - static_cast<long long>(h) * words);
+  // lane's token: where its value lies (-1: nowhere)
+  long long off = -1;
+  bool in_prefix = false;
+  const int t = 32 * w + lane, shift = a.pool.page_shift;
+  const int b = t < a.b.T ? kv_seq_of(a.b, t) : -1;
+  if (b >= 0) {
+    int slot = kv_own_len(a.b, shift, b) - (kv_tok(a.b, b + 1) - t);
+    const int32_t *table = a.b.pages + static_cast<size_t>(b) * a.b.max_pages;
+    if (slot < 0) {
+      const int g = kv_group_of(a.b, b);
+      if (g >= 0) {
+        in_prefix = true;
+        slot += kv_prefix_len(a, g);
+        table = kv_prefix_table(a, g);
+      }
+    }
+    if (slot >= 0) {
+      const int page = __ldg(table + (slot >> shift));
+      if (page >= 0 && page < a.pool.n_pages)
+        off = page * a.pool.page_stride + (slot & ((1 << shift) - 1)) * a.pool.token_stride + h * a.pool.head_stride;
+    }
+  }
+  uint32_t f = 0;
+#pragma unroll 8
+  for (int i = 0; i < 32 / RPL; ++i) {
+    const long long o = __shfl_sync(0xFFFFFFFFu, off, i * RPL + lane / CH);
+    const uint4 v = o < 0 ? make_uint4(0, 0, 0, 0) : __ldg(reinterpret_cast<const uint4 *>(a.pool.v + o) + lane % CH);
+    const uint32_t some = __ballot_sync(0xFFFFFFFFu, any_nonfinite<BF16>(v) != 0);
+#pragma unroll
+    for (int r = 0; r < RPL; ++r)
+      if (some >> (CH * r) & ((1u << CH) - 1u)) f |= 1u << (i * RPL + r);
+  }
+  const uint32_t pre = __ballot_sync(0xFFFFFFFFu, in_prefix);
+  if (lane == 0) {
+    a.value_flags[static_cast<size_t>(h) * words + w] = f & pre;
+    a.value_flags[static_cast<size_t>(a.pool.Hkv + h) * words + w] = f & ~pre;
   }
 }
 
@@ -644,7 +789,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const __grid_con
         }
       }
     } else if (warp == kProdWarp) {
-      produce<D>(a, maps, smem, bar, lane);
+      produce<D, BF16>(a, maps, smem, bar, lane);
       // after an abort the copies in flight land before the CTA's shared memory is released
       if (*static_cast<volatile int *>(&bar->abort)) __nanosleep(1000000);
     } else if (warp == kWalkWarp) {
@@ -694,7 +839,7 @@ bool make_maps(const AttnArgs &a, bool bf16, WideMaps *m) {
   return true;
 }
 
-static_assert(sizeof(WideBars) <= 512, "barriers and descriptions");
+static_assert(sizeof(WideBars) <= BAR_BYTES, "barriers and descriptions");
 
 template <int D, bool BF16, bool OUT32>
 qg_status wide_run(const AttnArgs &a, cudaStream_t s) {
@@ -714,6 +859,16 @@ qg_status wide_run(const AttnArgs &a, cudaStream_t s) {
 namespace qg {
 
 bool attn_wide_supported(int D) { return D == 64 || D == 128; }
+
+// before the narrow kernel, whose wait orders it before the wide one
+qg_status attn_flags_launch(const AttnArgs &a, bool bf16, cudaStream_t s) {
+  const long long items = static_cast<long long>((a.b.T + 31) / 32) * a.pool.Hkv;
+  const dim3 grid(static_cast<unsigned>((items + 7) / 8)), block(256);
+  cudaError_t e;
+  if (a.D == 64) e = bf16 ? launch_pdl(value_flags_kernel<64, true>, grid, block, 0, s, a) : launch_pdl(value_flags_kernel<64, false>, grid, block, 0, s, a);
+  else e = bf16 ? launch_pdl(value_flags_kernel<128, true>, grid, block, 0, s, a) : launch_pdl(value_flags_kernel<128, false>, grid, block, 0, s, a);
+  return e == cudaSuccess ? QG_OK : QG_ECUDA;
+}
 
 qg_status attn_wide_launch(const AttnArgs &a, bool bf16, cudaStream_t s) {
   if (a.D == 64) {

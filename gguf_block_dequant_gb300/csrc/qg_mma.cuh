@@ -23,6 +23,28 @@ QG_DEVICE float hi16(uint32_t v) {
   return BF16 ? __uint_as_float(v & 0xFFFF0000u) : h2f(v >> 16);
 }
 
+// whether the low 16-bit value is infinite or NaN: its exponent is all ones
+template <bool BF16>
+QG_DEVICE bool nonfinite16(uint32_t v) {
+  constexpr uint32_t E = BF16 ? 0x7F80u : 0x7C00u;
+  return (v & E) == E;
+}
+// not zero if there are such values among eight: adding one to an exponent of ones carries into the
+// sign's place
+template <bool BF16>
+QG_DEVICE uint32_t any_nonfinite(uint4 v) {
+  constexpr uint32_t E = BF16 ? 0x7F807F80u : 0x7C007C00u, ONE = BF16 ? 0x00800080u : 0x04000400u;
+  return (((v.x & E) + ONE) | ((v.y & E) + ONE) | ((v.z & E) + ONE) | ((v.w & E) + ONE)) & 0x80008000u;
+}
+// eight values with zeros in the places of such
+template <bool BF16>
+QG_DEVICE uint4 make_finite(uint4 v) {
+  auto fin = [](uint32_t x) {
+    return (nonfinite16<BF16>(x) ? 0u : x & 0xFFFFu) | (nonfinite16<BF16>(x >> 16) ? 0u : x & 0xFFFF0000u);
+  };
+  return make_uint4(fin(v.x), fin(v.y), fin(v.z), fin(v.w));
+}
+
 // 2^x on the special function unit (relative error about 2^-22; 2^-inf = 0)
 QG_DEVICE float ex2(float x) {
   float r;

@@ -382,7 +382,9 @@ QG_API qg_status qg_kv_append(const qg_kv_cache *cache, const qg_kv_batch *batch
  *     Scores and sums are f32.  The tensor cores take the softmax weights in the cache's type:
  *     one rounding (2^-9 of a weight in bf16, 2^-12 in f16) for a 16-bit output, and for an f32
  *     output two terms, which leave 2^-18 (bf16) or 2^-24 (f16).
- *   - Rows past a sequence's length are never read: whatever they hold has no effect.
+ *   - Rows past a sequence's length are never read: whatever they hold has no effect.  Nor do the keys and
+ *     values of positions after a token's own.  An infinite or NaN value that a token sees makes that
+ *     element of its output infinite or NaN.
  * Hq a multiple of n_heads, at most 16 query heads per cached head.  Workspace: qg_attn_workspace_size
  * bytes, 16-byte aligned, contents irrelevant; one call at a time may use it. */
 QG_API size_t qg_attn_workspace_size(const qg_kv_cache *cache, const qg_kv_batch *batch, int Hq);

@@ -1,5 +1,5 @@
 """NaN and infinities in attention over the paged cache: a NaN score makes its row NaN however the
-row's keys were cut into pieces."""
+row's keys were cut into pieces, and a value that a token must not see has no effect on it."""
 import pytest
 import torch
 
@@ -95,3 +95,51 @@ def test_nan_in_a_run_of_keys(qg, name, dtype, out, D, G):
         compare(attend(qg, bt, q, out_dtype), ref, terms, D, dtype, out_dtype)
         if which >= 3:
             break
+
+
+MASKED = {
+    "a draft": ([3], [40], ()),
+    "drafts under a prefix": ([1, 3, 2, 4], [9, 30, 2, 64], ((0, 4, 77),)),
+    "more queries than tokens": ([4, 6], [2, 0], ((0, 1, 10),)),
+    "half a row tile": ([20], [300], ()),
+    "a prompt": ([300], [300], ()),
+    "prompts of every kind": ([130, 65, 1, 20], [130, 70, 6, 200], ((0, 4, 260),)),
+    "a prompt that sees little": ([150], [20], ((0, 1, 30),)),
+    "short ones of which some see little": ([3] * 40, [3 if i % 2 else 1 for i in range(40)], ((0, 40, 6),)),
+}
+
+
+@pytest.mark.parametrize("name", MASKED)
+@pytest.mark.parametrize("dtype,out,D,G", [("f16", "f32", 128, 4), ("bf16", "same", 128, 8), ("bf16", "f32", 64, 5),
+                                           ("f16", "same", 256, 2), ("bf16", "f32", 128, 1)])
+def test_values_a_token_must_not_see(qg, name, dtype, out, D, G):
+    """Infinite and NaN values of tokens past a token's own: its output keeps its bits.  Tokens that see
+    one have no finite output in that element, and the same bits in all others."""
+    n, own, groups = MASKED[name]
+    out_dtype = torch.float32 if out == "f32" else DT[dtype]
+    bt = Batch(n, own, 2, D, 16, dtype, groups)
+    q = queries(bt.T, 2 * G, D, dtype)
+    want = attend(qg, bt, q, out_dtype)
+    assert torch.isfinite(want).all()
+    hit = torch.zeros((bt.T, 2 * G, D), dtype=torch.bool)
+    vals = [float("inf"), float("-inf"), float("nan")]
+    c = 0
+    for which in range(len(n) + len(groups)):
+        ln = own[which] if which < len(n) else groups[which - len(n)][2]
+        last = range(max(0, ln - (n[which] if which < len(n) else 5)), ln)
+        for s in [*last[:1], *last[len(last) // 2:len(last) // 2 + 1], *last[-1:]]:
+            h, col = c % 2, (37 * c + 5) % D
+            bt.v[(*place(bt, which, s), h, col)] = vals[c % 3]
+            c += 1
+            for b in range(len(n)):
+                g, pre = bt.group(b)
+                mine = which == b or (g >= 0 and which == len(n) + g)
+                for i in range(n[b] if mine else 0):
+                    seen = (own[b] if which == b else pre + own[b]) - n[b] + i + 1
+                    if s < seen:
+                        hit[bt.qs[b] + i, h * G:(h + 1) * G, col] = True
+    got = attend(qg, bt, q, out_dtype)
+    hit = hit.cuda()
+    same = (got == want) | hit
+    assert same.all(), torch.nonzero(~same)[:4].tolist()
+    assert not torch.isfinite(got[hit]).any()
