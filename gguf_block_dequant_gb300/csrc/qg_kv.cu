@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(256) beam_reorder_kernel(const __grid_constant
     par[i] = p;
     if (p != i) moved = 1;
     page[i] = 0;
-    if (pool < a.n_pools && !bad && rem) {
+    if (!bad && rem) {  // the lists' blocks ask as well: a request moves as a whole or not at all
       const int pg = a.pages[s * a.max_pages + full];
       page[i] = pg;
       if (pg < 0 || pg >= a.n_pages) bad = true;

@@ -419,7 +419,8 @@ QG_API qg_status qg_beam_select(const float *logits, const float *scores, const 
  * Every beam must have its own page in the column being filled; full pages must not be written
  * again.  caches: HOST array of n_layers (<= 128) caches with one geometry.  batch: n_seqs (= N*W), kv_len,
  * pages, max_pages; the rest is ignored.  1 <= W <= 32.  A parent outside [0, W) sets QG_EDEVICE_ID and the
- * beam keeps its own state. */
+ * beam keeps its own state; a page id outside the pool in the column being filled, of any of the W beams,
+ * sets it and leaves the request as it is. */
 QG_API qg_status qg_beam_reorder(const qg_kv_cache *caches, int n_layers, const qg_kv_batch *batch, int W,
                                  const int32_t *parents, qg_stream_t stream);
 

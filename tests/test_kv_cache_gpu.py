@@ -280,3 +280,22 @@ def test_reorder_bad_pages_and_lengths(qg):
         assert torch.equal(pool, before)
         if what != "page":
             assert torch.equal(pages, own)
+
+
+def test_reorder_bad_page_leaves_the_lists_too(qg):
+    """A bad page in the column being filled: no block of the request moves anything, the page lists'
+    among them (full pages of one beam with the begun page of another would be a mixed history)."""
+    W, page = 3, 8
+    for lens in ([13, 21], [21, 13]):
+        pool, pages, kv_len = reorder_case(2, W, lens, page)
+        pages[1, lens[0] // page] = -1
+        before, own = pool.clone(), pages.clone()
+        par = torch.tensor([[1, 0, 2], [2, 0, 1]], dtype=torch.int32).cuda()
+        want = [tokens_of(pool, pages, W + p, lens[1], page) for p in (2, 0, 1)]
+        run_reorder(qg, pool, pages, kv_len, par, W)
+        assert qg.device_status() == 1 << qg.QG_EDEVICE_ID
+        assert torch.equal(pages[:W], own[:W])
+        used = own[:W][own[:W] >= 0].long()
+        assert torch.equal(pool[:, used], before[:, used])
+        for i in range(W):  # the other request moves
+            assert torch.equal(tokens_of(pool, pages, W + i, lens[1], page), want[i])
