@@ -348,6 +348,7 @@ def _dtype(t):
 
 class KVCache(ctypes.Structure):
     """qg_kv_cache: one layer's page pools."""
+    device = None  # the pools' GPU (kv_cache sets it: what goes with the cache has to be there too)
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("dtype", ctypes.c_int), ("n_pages", ctypes.c_int),
                 ("page_size", ctypes.c_int), ("n_heads", ctypes.c_int), ("head_dim", ctypes.c_int),
                 ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
@@ -355,6 +356,7 @@ class KVCache(ctypes.Structure):
 
 class KVBatch(ctypes.Structure):
     """qg_kv_batch: the sequences, their lengths and page lists, and the prefixes they share."""
+    device = None
     _fields_ = [("n_seqs", ctypes.c_int), ("n_tokens", ctypes.c_int), ("n_groups", ctypes.c_int),
                 ("max_pages", ctypes.c_int), ("max_prefix_pages", ctypes.c_int), ("q_start", ctypes.c_void_p),
                 ("kv_len", ctypes.c_void_p), ("pages", ctypes.c_void_p), ("group_start", ctypes.c_void_p),
@@ -381,6 +383,25 @@ def _check(t, dtype, what):
         raise ValueError(f"{what} must be contiguous and {dtype}")
 
 
+def _on(device, names, *tensors):
+    """Refuses tensors that are not on the GPU `device` (None: unknown, from a struct filled by hand): the
+    kernels take addresses, and one of host memory or of another GPU would fault."""
+    if device is None:
+        return
+    if device < 0:
+        raise ValueError("the cached-decode calls take GPU tensors")
+    for i, t in enumerate(tensors):
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"{names.split()[i]} must be on GPU {device} with the rest")
+
+
+def _cache_device(cache, batch):
+    d, b = cache.device, batch.device
+    if d is not None and b is not None and d != b:
+        raise ValueError("the batch must be on the cache's GPU")
+    return b if d is None else d
+
+
 def kv_cache(k, v):
     """A qg_kv_cache of two pools [pages][tokens][heads][D] of one f16 or bf16 type (any strides
     with the last one 1: a head-major pool is passed as its permuted view).  Keeps them alive."""
@@ -392,14 +413,26 @@ def kv_cache(k, v):
         raise ValueError("k and v must be on one device")
     c = KVCache(k.data_ptr(), v.data_ptr(), _dtype(k), *k.shape, *k.stride()[:3])
     c.tensors = (k, v)
+    c.device = k.get_device()
     return c
 
 
 def kv_caches(ks, vs):
-    """The layers' caches as one array (beam_reorder)."""
+    """The layers' caches as one array (beam_reorder), each of them a cache for the other calls."""
     cs = [kv_cache(k, v) for k, v in zip(ks, vs, strict=True)]
-    arr = (KVCache * len(cs))(*cs)
+    if any(c.device != cs[0].device for c in cs):
+        raise ValueError("the layers' pools must be on one device")
+
+    class Caches(KVCache * len(cs)):
+        def __getitem__(self, i):
+            c = super().__getitem__(i)
+            if isinstance(c, KVCache):
+                c.device = self.device
+            return c
+
+    arr = Caches(*cs)
     arr.tensors = [c.tensors for c in cs]
+    arr.device = cs[0].device if cs else None
     return arr
 
 
@@ -440,6 +473,7 @@ def kv_batch(kv_len, pages, q_start=None, n_tokens=None, group_start=None, prefi
                 *[None if t is None else t.data_ptr()
                   for t in (q_start, kv_len, pages, group_start, prefix_len, prefix_pages)])
     b.tensors = (kv_len, pages, q_start, group_start, prefix_len, prefix_pages)
+    b.device = kv_len.get_device()
     return b
 
 
@@ -484,8 +518,10 @@ def kv_append(cache, batch, q, k, v, q_out, freqs, pairs=False, q_norm=None, k_n
     for t in (q_norm, k_norm):
         if t is not None and (t.dtype is not f32 or t.numel() != D or not t.is_contiguous()):
             raise ValueError("q_norm and k_norm must be contiguous f32 of head_dim elements")
-    _call("qg_kv_append", ctypes.byref(cache), ctypes.byref(batch), Hq, _ptr(q), _rows(q, T, Hq * D, "q"), _ptr(k),
-          _rows(k, T, Hkv * D, "k"), _ptr(v), _rows(v, T, Hkv * D, "v"), _ptr(q_norm), _ptr(k_norm), float(eps),
+    qs, ks, vs = _rows(q, T, Hq * D, "q"), _rows(k, T, Hkv * D, "k"), _rows(v, T, Hkv * D, "v")
+    _on(_cache_device(cache, batch), "k v q q_out freqs q_norm k_norm", k, v, q, q_out, freqs, q_norm, k_norm)
+    _call("qg_kv_append", ctypes.byref(cache), ctypes.byref(batch), Hq, _ptr(q), qs, _ptr(k),
+          ks, _ptr(v), vs, _ptr(q_norm), _ptr(k_norm), float(eps),
           _ptr(freqs), 0 if freqs is None else 2 * freqs.numel(), int(bool(pairs)), _ptr(q_out), _stream(stream))
     return q_out
 
@@ -503,7 +539,9 @@ def attn_paged(cache, batch, q, out, scale, workspace, stream=None):
         raise ValueError("q must be of the cache's type and out contiguous")
     if out.numel() != T * Hq * D:
         raise ValueError(f"out must have {T} rows of whole heads")
-    _call("qg_attn_paged", ctypes.byref(cache), ctypes.byref(batch), Hq, _ptr(q), _rows(q, T, Hq * D, "q"), float(scale),
+    qs = _rows(q, T, Hq * D, "q")
+    _on(_cache_device(cache, batch), "q out workspace", q, out, workspace)
+    _call("qg_attn_paged", ctypes.byref(cache), ctypes.byref(batch), Hq, _ptr(q), qs, float(scale),
           _ptr(out), _dtype(out), _ptr(workspace), _nbytes(workspace), _stream(stream))
     return out
 
@@ -526,6 +564,8 @@ def beam_select(logits, scores, N, W, out_scores, parents, tokens, workspace, do
         raise ValueError("outputs must be [N][K]")
     if done is not None and done.numel() != N * W:
         raise ValueError("done must be [N*W]")
+    _on(logits.get_device(), "scores out_scores parents tokens done done_out workspace", scores, out_scores, parents, tokens,
+        done, done_out, workspace)
     _call("qg_beam_select", _ptr(logits), _ptr(scores), _ptr(done), int(eos), N, W, K, V, _ptr(out_scores),
           _ptr(parents), _ptr(tokens), _ptr(done_out), _ptr(workspace), _nbytes(workspace), _stream(stream))
     return out_scores, parents, tokens
@@ -537,4 +577,5 @@ def beam_reorder(caches, batch, parents, W, stream=None):
     if parents.numel() != batch.n_seqs:
         raise ValueError("parents must be [N][W]")
     _check(parents, "int32", "parents")
+    _on(_cache_device(caches, batch), "parents", parents)
     _call("qg_beam_reorder", caches, len(caches), ctypes.byref(batch), W, _ptr(parents), _stream(stream))

@@ -217,3 +217,69 @@ def test_binding_refuses_tensors_of_other_types_and_shapes(qg):
     for p in (i32(2), i32(3).long(), torch.zeros(3)):
         with pytest.raises(ValueError):
             qg.beam_reorder(qg.kv_caches([k], [k.clone()]), b, p, 3, stream=0)
+
+
+def test_binding_refuses_tensors_off_the_gpu(qg):
+    """Host tensors (rope_freqs returns one) and those of another GPU are refused before the C call,
+    which sees addresses only.  A subclass stands in for tensors of a GPU; nothing is called with it."""
+    torch = pytest.importorskip("torch")
+
+    class There(torch.Tensor):
+        where = 0
+
+        def get_device(self):
+            return self.where
+
+    class Elsewhere(There):
+        where = 1
+
+    g = lambda t: t.as_subclass(There)  # noqa: E731
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    k = torch.zeros((4, 16, 2, 64), dtype=torch.float16)
+    c, caches = qg.kv_cache(g(k), g(k.clone())), qg.kv_caches([g(k)], [g(k.clone())])
+    b = qg.kv_batch(g(i32(3)), g(i32(3, 5)))
+    assert c.device == b.device == caches.device == caches[0].device == [x.device for x in caches][0] == 0
+    host = qg.kv_cache(k, k.clone())
+    hostb = qg.kv_batch(i32(3), i32(3, 5))
+    away = qg.kv_batch(i32(3).as_subclass(Elsewhere), i32(3, 5))
+    f32 = lambda *s: g(torch.zeros(s))  # noqa: E731
+    qo, ws = g(torch.zeros((3, 4, 64), dtype=torch.float16)), g(torch.zeros(1 << 20, dtype=torch.uint8))
+    plain = lambda t: t.as_subclass(torch.Tensor)  # noqa: E731
+
+    def refused(f, args, names, what):
+        for n in names:
+            for to in (plain, lambda t: t.as_subclass(Elsewhere)):
+                a = dict(args)
+                a[n] = to(a[n])
+                with pytest.raises(ValueError, match=f"{what.get(n, n)} must be on"):
+                    f(**a)
+
+    a = dict(cache=c, batch=b, q=f32(3, 256), k=f32(3, 128), v=f32(3, 128), q_out=qo, freqs=g(qg.rope_freqs(64, 1e4)),
+             q_norm=f32(64), k_norm=f32(64), stream=0)
+    refused(qg.kv_append, a, ["q", "k", "v", "q_out", "freqs", "q_norm", "k_norm"], {})
+    for kw in (dict(cache=host, batch=hostb), dict(batch=hostb), dict(batch=away)):
+        with pytest.raises(ValueError, match="GPU"):
+            qg.kv_append(**{**a, **kw})
+    a = dict(cache=c, batch=b, q=qo, out=g(torch.zeros((3, 4, 64))), scale=0.1, workspace=ws, stream=0)
+    refused(qg.attn_paged, a, ["q", "out", "workspace"], {})
+    for kw in (dict(cache=host, batch=hostb), dict(batch=hostb), dict(cache=host)):
+        with pytest.raises(ValueError, match="GPU"):
+            qg.attn_paged(**{**a, **kw})
+    gi, gu = g(i32(2, 3)), g(torch.zeros((2, 3), dtype=torch.uint8))
+    a = dict(logits=f32(6, 50), scores=f32(2, 3), N=2, W=3, out_scores=f32(2, 3), parents=gi, tokens=gi, workspace=ws,
+             done=gu, done_out=gu, stream=0)
+    refused(qg.beam_select, a, ["scores", "out_scores", "parents", "tokens", "workspace", "done", "done_out"], {})
+    with pytest.raises(ValueError, match="GPU"):
+        qg.beam_select(**{**a, "logits": plain(a["logits"])})
+    refused(lambda **kw: qg.beam_reorder(caches, b, W=3, stream=0, **kw), dict(parents=g(i32(3))), ["parents"], {})
+    for cs, bb in ((caches, hostb), (qg.kv_caches([k], [k.clone()]), b)):
+        with pytest.raises(ValueError, match="GPU"):
+            qg.beam_reorder(cs, bb, g(i32(3)), 3, stream=0)
+    with pytest.raises(ValueError, match="one device"):
+        qg.kv_caches([g(k), k], [g(k), k])
+    # what was refused for its type or shape still is, with every tensor in place
+    good = dict(cache=c, batch=b, q=f32(3, 256), k=f32(3, 128), v=f32(3, 128), q_out=qo, freqs=g(qg.rope_freqs(64, 1e4)), stream=0)
+    for kw, msg in ((dict(q=f32(3, 256).double()), "f32"), (dict(k=f32(3, 64)), "k must have"),
+                    (dict(q_out=g(torch.zeros(3, 4, 64))), "cache's type"), (dict(q_norm=f32(32)), "head_dim")):
+        with pytest.raises(ValueError, match=msg):
+            qg.kv_append(**{**good, **kw})
