@@ -111,6 +111,7 @@ struct WideBars {
   uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];
   uint32_t tmem;
   int abort;
+  long long limit;  // of a wait, in cycles
 };
 
 using Scan = LineScan<kThreads>;
@@ -143,24 +144,27 @@ QG_DEVICE bool walk_next(const AttnArgs &a, Walk *k, Piece *p) {
   return false;
 }
 
-// Bounded wait by the SM's own clock: gives up when another role has, or after about a quarter
-// of a second.
-constexpr long long kWaitCycles = 1LL << 29;
-QG_DEVICE bool clock_wait(uint64_t *b, uint32_t parity, volatile int *abort) {
+// Bounded wait by the SM's own clock: gives up when another role has, or after bar->limit cycles.  The
+// walking warp waits for whole pieces, and the others for it while it passes over empty segments, so the
+// limit grows with the CTA's keys and with the segments: a quarter of a second, kWaitKey cycles a key (about 27
+// are needed, thousands where add_zeroed reads a key's values again) and kWaitSeg a segment.
+constexpr long long kWaitCycles = 1LL << 29, kWaitKey = 1LL << 13, kWaitSeg = 1LL << 14;
+QG_DEVICE bool clock_wait(uint64_t *b, uint32_t parity, WideBars *bar) {
   if (mbar_try_wait(b, parity)) return true;
   const long long t0 = clock64();
+  volatile int *abort = &bar->abort;
   while (true) {
     if (mbar_try_wait(b, parity)) return true;
     if (*abort) return false;
-    if (clock64() - t0 > kWaitCycles) break;
+    if (clock64() - t0 > bar->limit) break;
   }
   *abort = 1;
   atomicOr(&g_qg_status_attn_tc, QG_STATUS_BIT_TIMEOUT);
   return false;
 }
 // the whole warp waits, and gives up as a whole
-QG_DEVICE bool warp_wait(uint64_t *b, uint32_t parity, volatile int *abort) {
-  return __all_sync(0xFFFFFFFFu, clock_wait(b, parity, abort));
+QG_DEVICE bool warp_wait(uint64_t *b, uint32_t parity, WideBars *bar) {
+  return __all_sync(0xFFFFFFFFu, clock_wait(b, parity, bar));
 }
 
 // ---- the walk -----------------------------------------------------------------------------------
@@ -199,7 +203,6 @@ QG_DEVICE void piece_values(const AttnArgs &a, Piece *p, int lane) {
   }
 }
 QG_DEVICE void walk_line(const AttnArgs &a, Walk walk, WideBars *bar, int lane) {
-  volatile int *abort = &bar->abort;
   for (uint32_t n = 0;; ++n) {
     Piece p;
     const bool more = walk_next(a, &walk, &p);
@@ -207,7 +210,7 @@ QG_DEVICE void walk_line(const AttnArgs &a, Walk walk, WideBars *bar, int lane) 
     else if (p.slot < 0 && !p.alone && lane == 0) atomicOr(&g_qg_status_attn_tc, QG_STATUS_BIT_ID);
     if (more) piece_values(a, &p, lane);
     const uint32_t i = n % kPieces;
-    if (!warp_wait(&bar->piece_empty[i], ((n / kPieces) & 1) ^ 1, abort)) return;
+    if (!warp_wait(&bar->piece_empty[i], ((n / kPieces) & 1) ^ 1, bar)) return;
     if (lane == 0) {
       bar->piece[i] = p;
       mbar_arrive(&bar->piece_full[i]);
@@ -219,7 +222,7 @@ QG_DEVICE void walk_line(const AttnArgs &a, Walk walk, WideBars *bar, int lane) 
 // the n-th piece, nullptr at the end (or after an abort)
 QG_DEVICE const Piece *piece_get(WideBars *bar, uint32_t n) {
   const uint32_t i = n % kPieces;
-  if (!warp_wait(&bar->piece_full[i], (n / kPieces) & 1, &bar->abort)) return nullptr;
+  if (!warp_wait(&bar->piece_full[i], (n / kPieces) & 1, bar)) return nullptr;
   const Piece *p = &bar->piece[i];
   return p->j0 < p->j1 ? p : nullptr;
 }
@@ -254,7 +257,6 @@ template <int D, bool BF16>
 QG_DEVICE void produce(const AttnArgs &a, const WideMaps &maps, uint8_t *smem, WideBars *bar, int lane) {
   using C = WideCfg<D>;
   constexpr int H = D / 64;              // 64-element halves of a row
-  volatile int *abort = &bar->abort;
   const uint32_t sb = smem_u32(smem);
   const int shift = a.pool.page_shift;
   const int bshift = min(shift, 7), rows = 1 << bshift;  // rows of a box
@@ -263,7 +265,7 @@ QG_DEVICE void produce(const AttnArgs &a, const WideMaps &maps, uint8_t *smem, W
   uint32_t np = 0, ntail = 0;
   for (const Piece *pp; (pp = piece_get(bar, np)) != nullptr; piece_done(bar, np++, lane)) {
     const Piece p = *pp;
-    if (!warp_wait(&bar->q_empty, (np & 1) ^ 1, abort)) return;
+    if (!warp_wait(&bar->q_empty, (np & 1) ^ 1, bar)) return;
     const int ns = p.paired ? 2 : 1;
     if (lane == 0) mbar_arrive_expect_tx(&bar->q_full, static_cast<uint32_t>(ns * H * half * a.Gq) * 128u);
     __syncwarp();
@@ -291,7 +293,7 @@ QG_DEVICE void produce(const AttnArgs &a, const WideMaps &maps, uint8_t *smem, W
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv, ring.next()) {
         const int st = ring.st;
-        if (!warp_wait(&bar->empty[st], ring.par ^ 1u, abort)) return;
+        if (!warp_wait(&bar->empty[st], ring.par ^ 1u, bar)) return;
         // a value tile is held back when values past the last key are to become zeros (whatever their
         // rows or the stage held), or infinite and NaN ones.  Keys may be anything: their scores are
         // replaced.
@@ -317,7 +319,7 @@ QG_DEVICE void produce(const AttnArgs &a, const WideMaps &maps, uint8_t *smem, W
           }
         }
         if (held) {
-          if (!warp_wait(&bar->tail, ntail++ & 1, abort)) return;
+          if (!warp_wait(&bar->tail, ntail++ & 1, bar)) return;
 #pragma unroll
           for (int h = 0; h < H; ++h) {
             uint4 *v = reinterpret_cast<uint4 *>(smem + off + h * C::HALF);
@@ -338,10 +340,9 @@ template <int D, bool BF16, bool OUT32>
 QG_DEVICE void issue_mma(uint32_t smem, WideBars *bar, int lane) {
   using C = WideCfg<D>;
   constexpr uint32_t id_s = make_idesc16(128, kWideKeys, BF16, false), id_o = make_idesc16(128, D, BF16, true);
-  volatile int *abort = &bar->abort;
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, bar->tmem, 0), el = elect_lane();
   auto wait = [&](uint64_t *b, uint32_t parity) {
-    const bool r = warp_wait(b, parity, abort);
+    const bool r = warp_wait(b, parity, bar);
     tc_fence_after();
     return r;
   };
@@ -488,7 +489,6 @@ __device__ __noinline__ void add_zeroed(const AttnArgs &a, const Piece &p, uint3
 
 template <int D, bool BF16, bool OUT32>
 QG_DEVICE void softmax(const AttnArgs &a, WideBars *bar, int s, int warp4, int lane, uint32_t stage) {
-  volatile int *abort = &bar->abort;
   const uint32_t lanes = static_cast<uint32_t>(32 * warp4) << 16;
   const uint32_t ts = bar->tmem + lanes + 128u * s, to = bar->tmem + lanes + 256u + D * s;
   const int row = 32 * warp4 + lane, half = a.wide.tpt / 2;
@@ -514,7 +514,7 @@ QG_DEVICE void softmax(const AttnArgs &a, WideBars *bar, int s, int warp4, int l
     const bool idle = !__any_sync(0xFFFFFFFFu, valid);  // no row of this warp is anyone's: whatever its weights are
     const int step = p.paired ? 1 : 2, first = p.paired ? p.j0 : p.j0 + s, j1 = p.j1, jp = p.jp;
     for (int j = first; j < j1; j += step) {
-      if (!warp_wait(&bar->s_full[s], n_s++ & 1, abort)) return;
+      if (!warp_wait(&bar->s_full[s], n_s++ & 1, bar)) return;
       tc_fence_after();
       if (idle) {
         if (lane == 0) mbar_arrive(&bar->p_full[s]);
@@ -606,7 +606,7 @@ QG_DEVICE void softmax(const AttnArgs &a, WideBars *bar, int s, int warp4, int l
     // ---- the piece's output
     const bool any = first < j1;
     if (any) {
-      if (!warp_wait(&bar->o_full[s], n_o++ & 1, abort)) return;
+      if (!warp_wait(&bar->o_full[s], n_o++ & 1, bar)) return;
       tc_fence_after();
       if (p.dirty) add_zeroed<D, BF16>(a, p, to, s, limp, lim);
     }
@@ -766,6 +766,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const __grid_con
     pdl_wait();
     return;
   }
+  if (threadIdx.x == 0) bar->limit = kWaitCycles + kWaitKey * (walk.end - walk.at) + kWaitSeg * 2 * a.b.B;
   if (warp == kMmaWarp) tmem_alloc(&bar->tmem, C::COLS);
   tc_fence_before();
   __syncthreads();

@@ -285,3 +285,22 @@ def test_no_tokens(qg):
     qg.attn_paged(cache, batch, q, torch.empty((0, 4, 64), device="cuda"), 1.0, ws)
     torch.cuda.synchronize()
     assert qg.device_status() == 0
+
+
+def test_pieces_of_tens_of_millions_of_keys(qg):
+    """A worker's piece may take longer than a quarter of a second: no role gives up on another that is at
+    work.  One page again and again, so 50 million keys need 16 MB; every value is 1."""
+    T, D, G, keys = 2 * 152 * 16, 64, 16, 48 << 20
+    k = torch.randn((1, 65536, 1, D), generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda()
+    v = torch.ones_like(k)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    batch = qg.kv_batch(i32([keys]), torch.zeros((1, keys >> 16), dtype=torch.int32, device="cuda"), i32([0, T]), T)
+    cache = qg.kv_cache(k, v)
+    q = queries(T, G, D, "bf16")
+    out = torch.zeros((T, G, D), device="cuda")
+    ws = torch.empty(qg.attn_workspace_size(cache, batch, G), dtype=torch.uint8, device="cuda")
+    qg.attn_paged(cache, batch, q, out, scale_of(D), ws)
+    torch.cuda.synchronize()
+    assert qg.device_status() == 0
+    # sums of cnt / 16 + 32 additions within 2^-23, in numerator and denominator alike
+    assert ((out - 1).abs() <= 2 * (keys / 16 + 32) * 2.0 ** -23).all()
