@@ -628,10 +628,12 @@ Plan make_plan(const KvPool &pool, const KvBatch &b, int Gq, int sms) {
   p.n_ml = take(static_cast<size_t>(sn) * kNarrowRows * 8);
   p.n_o = take(static_cast<size_t>(sn) * kNarrowRows * pool.D * 4);
   if (wide) {
-    // of each kind, at most T / (tn + 1) segments have the more than tn tokens of the wide line
-    const long long most = b.T / (tn + 1), tiles = static_cast<long long>(b.T) / tw;
-    const long long uw = (b.q_start ? std::min<long long>(b.B, most) + tiles : 0) +
-                         (b.G ? std::min<long long>(runs, most) + tiles : 0);
+    // of each kind, at most T / (tn + 1) segments have the more than tn tokens of the wide line; n tokens make
+    // at most 1 + n / tw tiles, own segments of sequences that are not long one, and long sequences' tokens are in
+    // no run: so all the tiles beyond a segment's first come from T tokens, each counted once
+    const long long most = b.T / (tn + 1);
+    const long long uw = (b.q_start ? std::min<long long>(b.B, most) : 0) + (b.G ? std::min<long long>(runs, most) : 0) +
+                         (b.q_start || b.G ? static_cast<long long>(b.T) / tw : 0);
     const long long sw = uw * pool.Hkv + p.wide_workers;
     p.w_slots = sw;
     p.w_pos = take((nseg + 1) * 8);

@@ -283,3 +283,15 @@ def test_binding_refuses_tensors_off_the_gpu(qg):
                     (dict(q_out=g(torch.zeros(3, 4, 64))), "cache's type"), (dict(q_norm=f32(32)), "head_dim")):
         with pytest.raises(ValueError, match=msg):
             qg.kv_append(**{**good, **kw})
+
+
+def test_workspace_counts_a_prompts_tiles_once(qg):
+    """A long prompt's tokens are in its own row tiles and in no run of a group: a shared prefix before it
+    adds what the group's runs may need, not the prompt's tiles again."""
+    c = cache(qg, n_heads=8, head_stride=128, token_stride=1024, page_stride=16 * 1024)
+    g = dict(n_groups=1, group_start=A, prefix_len=A, prefix_pages=A, max_prefix_pages=4)
+    for n, T in ((1, 131072), (4, 20000), (64, 5000)):
+        one = qg.attn_workspace_size(c, batch(qg, n_seqs=n, n_tokens=T, q_start=A), 32)
+        both = qg.attn_workspace_size(c, batch(qg, n_seqs=n, n_tokens=T, q_start=A, **g), 32)
+        # a run per group and one after each long sequence, each a row tile of 256 rows and one of 16, per cached head
+        assert one < both <= one + (n + 1) * 8 * (256 + 16) * (128 + 2) * 4 + (1 << 16)
