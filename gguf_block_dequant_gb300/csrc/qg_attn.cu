@@ -14,11 +14,13 @@
 #include <math.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "qg_attn.cuh"
 #include "qg_mma.cuh"
 
 __device__ unsigned int g_qg_status_attn;  // this translation unit's device status word
+static std::atomic<bool> g_launched{false};   // whether a kernel that may set it has been launched
 
 namespace {
 
@@ -664,6 +666,7 @@ qg_status attn_run(const AttnArgs &a, int sms, cudaStream_t s) {
   using C = NarrowCfg<D>;
   auto narrow = attn_narrow_kernel<D, BF16, OUT32>;
   if (!set_smem_attr(reinterpret_cast<const void *>(narrow), C::SMEM)) return QG_ECUDA;
+  g_launched = true;
   if (a.value_flags) {
     const qg_status st = attn_flags_launch(a, BF16, s);
     if (st != QG_OK) return st;
@@ -700,6 +703,7 @@ qg_status attn_dispatch(const AttnArgs &a, bool bf16, int sms, cudaStream_t s) {
 namespace qg {
 unsigned int read_status_attn(bool clear) {
   unsigned int v = 0;
+  if (!g_launched) return v;
   if (cudaMemcpyFromSymbol(&v, g_qg_status_attn, sizeof(v)) != cudaSuccess) return 0xFFFFFFFFu;
   if (clear) {
     const unsigned int z = 0;

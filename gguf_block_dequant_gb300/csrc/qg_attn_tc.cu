@@ -34,6 +34,7 @@
 // maximum and sum (611 to 620), test_wait for try_wait (579 to 612).
 #include <cuda.h>
 
+#include <atomic>
 #include <mutex>
 
 #include "qg_attn.cuh"
@@ -42,6 +43,7 @@
 #include "qg_tc.cuh"
 
 __device__ unsigned int g_qg_status_attn_tc;  // this translation unit's device status word
+static std::atomic<bool> g_launched{false};   // whether a kernel that may set it has been launched
 
 namespace {
 
@@ -849,6 +851,7 @@ qg_status wide_run(const AttnArgs &a, cudaStream_t s) {
   WideMaps maps;
   if (!fits || !make_maps(a, BF16, &maps) || !set_smem_attr(reinterpret_cast<const void *>(k), WideCfg<D>::SMEM))
     return QG_ECUDA;
+  g_launched = true;
   return launch_pdl(k, dim3(static_cast<unsigned>(a.wide.workers)), dim3(kThreads), WideCfg<D>::SMEM, s, a, maps) ==
                  cudaSuccess
              ? QG_OK
@@ -882,6 +885,7 @@ qg_status attn_wide_launch(const AttnArgs &a, bool bf16, cudaStream_t s) {
 
 unsigned int read_status_attn_tc(bool clear) {
   unsigned int v = 0;
+  if (!g_launched) return v;
   if (cudaMemcpyFromSymbol(&v, g_qg_status_attn_tc, sizeof(v)) != cudaSuccess) return 0xFFFFFFFFu;
   if (clear) {
     const unsigned int z = 0;

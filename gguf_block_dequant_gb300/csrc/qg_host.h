@@ -91,6 +91,8 @@ qg_status gemv_mt_launch(int nmat, const void *const *w, const float *x, float *
 
 qg_status gemv_multi_dispatch(int type, int n, const void *const *w, const float *x, float *const *y,
                               const int64_t *M, int64_t N, int T, cudaStream_t s);
+// A unit's device status word: 0xFFFFFFFF when it cannot be read.  Each costs a copy from the device, so
+// the units of the cached decode leave out theirs until one of their kernels has been launched.
 unsigned int read_status_gemv(bool clear);
 unsigned int read_status_gemv1(bool clear);
 unsigned int read_status_mt(bool clear);

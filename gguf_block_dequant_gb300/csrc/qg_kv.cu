@@ -4,12 +4,14 @@
 #include <math.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "qg_kv.cuh"
 #include "qg_mma.cuh"
 
 __device__ unsigned int g_qg_status_kv;  // this translation unit's device status word
+static std::atomic<bool> g_launched{false};   // whether a kernel that may set it has been launched
 
 namespace {
 
@@ -359,6 +361,7 @@ qg_status kv_check_batch(const qg_kv_batch *b, bool tokens, bool prefix, KvBatch
 
 unsigned int read_status_kv(bool clear) {
   unsigned int v = 0;
+  if (!g_launched) return v;
   if (cudaMemcpyFromSymbol(&v, g_qg_status_kv, sizeof(v)) != cudaSuccess) return 0xFFFFFFFFu;
   if (clear) {
     const unsigned int z = 0;
@@ -433,6 +436,7 @@ qg_status qg_kv_append(const qg_kv_cache *cache, const qg_kv_batch *batch, int H
                   static_cast<unsigned>((rows + a.rows_per_block - 1) / a.rows_per_block));
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool bf16 = cache->dtype == QG_DT_BF16;
+  g_launched = true;
   cudaError_t e;
   if (D == 64) e = rope_pairs ? append_launch<64, true>(bf16, grid, s, a) : append_launch<64, false>(bf16, grid, s, a);
   else if (D == 128) e = rope_pairs ? append_launch<128, true>(bf16, grid, s, a) : append_launch<128, false>(bf16, grid, s, a);
@@ -484,6 +488,7 @@ qg_status qg_beam_reorder(const qg_kv_cache *caches, int n_layers, const qg_kv_b
   const dim3 grid(static_cast<unsigned>((a.n_pools + 1) * a.N),
                   static_cast<unsigned>(std::min<long long>(64, (places + 255) / 256)));
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  g_launched = true;
   cudaError_t e;
   if (W <= 4) e = qg::launch_pdl(beam_reorder_kernel<4>, grid, dim3(256), 0, s, a);
   else if (W <= 8) e = qg::launch_pdl(beam_reorder_kernel<8>, grid, dim3(256), 0, s, a);
