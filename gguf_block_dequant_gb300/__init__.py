@@ -478,11 +478,11 @@ def kv_batch(kv_len, pages, q_start=None, n_tokens=None, group_start=None, prefi
 
 
 def rope_freqs(rot, theta, factors=None):
-    """The rotation table of kv_append (qg_rope_freqs), int64 [rot / 2] on the host."""
+    """The rotation table of kv_append (qg_rope_freqs), int64 [rot / 2] on the host; factors from anywhere."""
     import torch
 
     out = torch.empty((max(rot // 2, 1),), dtype=torch.int64)
-    f = None if factors is None else torch.as_tensor(factors, dtype=torch.float32).contiguous()
+    f = None if factors is None else torch.as_tensor(factors, dtype=torch.float32, device="cpu").contiguous()
     if f is not None and f.numel() != rot // 2:
         raise ValueError("one factor per pair")
     _call("qg_rope_freqs", rot, float(theta), _ptr(f), _ptr(out))

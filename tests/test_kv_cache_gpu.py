@@ -299,3 +299,10 @@ def test_reorder_bad_page_leaves_the_lists_too(qg):
         assert torch.equal(pool[:, used], before[:, used])
         for i in range(W):  # the other request moves
             assert torch.equal(tokens_of(pool, pages, W + i, lens[1], page), want[i])
+
+
+def test_frequency_factors_on_the_gpu(qg):
+    """The table is made on the host: factors that lie on the GPU (a loaded rope_freqs tensor) come over first."""
+    f = torch.linspace(1.0, 8.0, 32)
+    assert torch.equal(qg.rope_freqs(64, 10000.0, f.cuda()), qg.rope_freqs(64, 10000.0, f))
+    assert torch.equal(qg.rope_freqs(64, 10000.0, f.double().cuda()), qg.rope_freqs(64, 10000.0, f.tolist()))
