@@ -765,6 +765,11 @@ qg_status qg_attn_paged(const qg_kv_cache *cache, const qg_kv_batch *batch, int 
     a.wide = line(kWideRows, kWideShift, p.wide_workers, p.w_slots, p.w_pos, p.w_unit, p.w_o, p.w_ml);
     a.wide.lo = a.narrow.tpt;
     a.wide.hi = INT32_MAX;
+    // The warp that walks the line waits for whole pieces, and the others for it while it passes over empty
+    // segments: a quarter of a second, 2^13 cycles for each key that a piece can have by the page lists (about
+    // 27 are needed, thousands where an infinite value is read again) and 2^14 for each segment, a minute at most.
+    const long long most = static_cast<long long>(a.b.max_pages + static_cast<long long>(a.b.max_prefix_pages)) << a.pool.page_shift;
+    a.wait_cycles = std::min((1LL << 29) + (most << 13) + (static_cast<long long>(a.b.B) << 15), 1LL << 37);
     // without q_start no token comes after another of its sequence
     if (a.b.q_start) a.value_flags = reinterpret_cast<uint32_t *>(ws + p.flags);
   }

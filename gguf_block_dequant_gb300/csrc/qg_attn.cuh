@@ -52,6 +52,7 @@ struct AttnArgs {
   int Hq, Gq, D;
   int out32;
   int long_tokens;       // sequences of more new tokens are long
+  long long wait_cycles; // limit of a wait inside the wide kernel
   uint32_t *value_flags; // [2][heads][tokens / 32] (qg_attn_tc.cu); null without q_start or a wide line
   Line narrow, wide;     // wide.workers == 0: the narrow line has every segment, nothing is long
 };

@@ -113,7 +113,6 @@ struct WideBars {
   uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];
   uint32_t tmem;
   int abort;
-  long long limit;  // of a wait, in cycles
 };
 
 using Scan = LineScan<kThreads>;
@@ -146,27 +145,23 @@ QG_DEVICE bool walk_next(const AttnArgs &a, Walk *k, Piece *p) {
   return false;
 }
 
-// Bounded wait by the SM's own clock: gives up when another role has, or after bar->limit cycles.  The
-// walking warp waits for whole pieces, and the others for it while it passes over empty segments, so the
-// limit grows with the CTA's keys and with the segments: a quarter of a second, kWaitKey cycles a key (about 27
-// are needed, thousands where add_zeroed reads a key's values again) and kWaitSeg a segment.
-constexpr long long kWaitCycles = 1LL << 29, kWaitKey = 1LL << 13, kWaitSeg = 1LL << 14;
-QG_DEVICE bool clock_wait(uint64_t *b, uint32_t parity, WideBars *bar) {
+// Bounded wait by the SM's own clock: gives up when another role has, or after a.wait_cycles.
+QG_DEVICE bool clock_wait(const AttnArgs &a, uint64_t *b, uint32_t parity, WideBars *bar) {
   if (mbar_try_wait(b, parity)) return true;
   const long long t0 = clock64();
   volatile int *abort = &bar->abort;
   while (true) {
     if (mbar_try_wait(b, parity)) return true;
     if (*abort) return false;
-    if (clock64() - t0 > bar->limit) break;
+    if (clock64() - t0 > a.wait_cycles) break;
   }
   *abort = 1;
   atomicOr(&g_qg_status_attn_tc, QG_STATUS_BIT_TIMEOUT);
   return false;
 }
 // the whole warp waits, and gives up as a whole
-QG_DEVICE bool warp_wait(uint64_t *b, uint32_t parity, WideBars *bar) {
-  return __all_sync(0xFFFFFFFFu, clock_wait(b, parity, bar));
+QG_DEVICE bool warp_wait(const AttnArgs &a, uint64_t *b, uint32_t parity, WideBars *bar) {
+  return __all_sync(0xFFFFFFFFu, clock_wait(a, b, parity, bar));
 }
 
 // ---- the walk -----------------------------------------------------------------------------------
@@ -212,7 +207,7 @@ QG_DEVICE void walk_line(const AttnArgs &a, Walk walk, WideBars *bar, int lane) 
     else if (p.slot < 0 && !p.alone && lane == 0) atomicOr(&g_qg_status_attn_tc, QG_STATUS_BIT_ID);
     if (more) piece_values(a, &p, lane);
     const uint32_t i = n % kPieces;
-    if (!warp_wait(&bar->piece_empty[i], ((n / kPieces) & 1) ^ 1, bar)) return;
+    if (!warp_wait(a, &bar->piece_empty[i], ((n / kPieces) & 1) ^ 1, bar)) return;
     if (lane == 0) {
       bar->piece[i] = p;
       mbar_arrive(&bar->piece_full[i]);
@@ -222,9 +217,9 @@ QG_DEVICE void walk_line(const AttnArgs &a, Walk walk, WideBars *bar, int lane) 
   }
 }
 // the n-th piece, nullptr at the end (or after an abort)
-QG_DEVICE const Piece *piece_get(WideBars *bar, uint32_t n) {
+QG_DEVICE const Piece *piece_get(const AttnArgs &a, WideBars *bar, uint32_t n) {
   const uint32_t i = n % kPieces;
-  if (!warp_wait(&bar->piece_full[i], (n / kPieces) & 1, bar)) return nullptr;
+  if (!warp_wait(a, &bar->piece_full[i], (n / kPieces) & 1, bar)) return nullptr;
   const Piece *p = &bar->piece[i];
   return p->j0 < p->j1 ? p : nullptr;
 }
@@ -265,9 +260,9 @@ QG_DEVICE void produce(const AttnArgs &a, const WideMaps &maps, uint8_t *smem, W
   const int half = a.wide.tpt / 2;
   Ring<C::NST> ring;
   uint32_t np = 0, ntail = 0;
-  for (const Piece *pp; (pp = piece_get(bar, np)) != nullptr; piece_done(bar, np++, lane)) {
+  for (const Piece *pp; (pp = piece_get(a, bar, np)) != nullptr; piece_done(bar, np++, lane)) {
     const Piece p = *pp;
-    if (!warp_wait(&bar->q_empty, (np & 1) ^ 1, bar)) return;
+    if (!warp_wait(a, &bar->q_empty, (np & 1) ^ 1, bar)) return;
     const int ns = p.paired ? 2 : 1;
     if (lane == 0) mbar_arrive_expect_tx(&bar->q_full, static_cast<uint32_t>(ns * H * half * a.Gq) * 128u);
     __syncwarp();
@@ -295,7 +290,7 @@ QG_DEVICE void produce(const AttnArgs &a, const WideMaps &maps, uint8_t *smem, W
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv, ring.next()) {
         const int st = ring.st;
-        if (!warp_wait(&bar->empty[st], ring.par ^ 1u, bar)) return;
+        if (!warp_wait(a, &bar->empty[st], ring.par ^ 1u, bar)) return;
         // a value tile is held back when values past the last key are to become zeros (whatever their
         // rows or the stage held), or infinite and NaN ones.  Keys may be anything: their scores are
         // replaced.
@@ -321,11 +316,13 @@ QG_DEVICE void produce(const AttnArgs &a, const WideMaps &maps, uint8_t *smem, W
           }
         }
         if (held) {
-          if (!warp_wait(&bar->tail, ntail++ & 1, bar)) return;
-#pragma unroll
+          if (!warp_wait(a, &bar->tail, ntail++ & 1, bar)) return;
+#pragma unroll 1
           for (int h = 0; h < H; ++h) {
             uint4 *v = reinterpret_cast<uint4 *>(smem + off + h * C::HALF);
+#pragma unroll 4
             for (int x = left * 8 + lane; x < kWideKeys * 8; x += 32) v[x] = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
             for (int x = z0 * 8 + lane; x < z1 * 8; x += 32) v[x] = make_finite<BF16>(v[x]);
           }
           fence_proxy_async_smem();  // stored through the generic proxy, read by the tensor cores
@@ -339,12 +336,12 @@ QG_DEVICE void produce(const AttnArgs &a, const WideMaps &maps, uint8_t *smem, W
 
 // ---- MMA issue --------------------------------------------------------------------------------
 template <int D, bool BF16, bool OUT32>
-QG_DEVICE void issue_mma(uint32_t smem, WideBars *bar, int lane) {
+QG_DEVICE void issue_mma(const AttnArgs &a, uint32_t smem, WideBars *bar, int lane) {
   using C = WideCfg<D>;
   constexpr uint32_t id_s = make_idesc16(128, kWideKeys, BF16, false), id_o = make_idesc16(128, D, BF16, true);
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, bar->tmem, 0), el = elect_lane();
   auto wait = [&](uint64_t *b, uint32_t parity) {
-    const bool r = warp_wait(b, parity, bar);
+    const bool r = warp_wait(a, b, parity, bar);
     tc_fence_after();
     return r;
   };
@@ -385,7 +382,7 @@ QG_DEVICE void issue_mma(uint32_t smem, WideBars *bar, int lane) {
   // tiles come as K0 V0 K1 V1 ...; kt and vt are the next key and value tiles to be used
   Ring<C::NST> kt, vt;
   vt.next();
-  for (const Piece *pp; (pp = piece_get(bar, np)) != nullptr; ++np) {
+  for (const Piece *pp; (pp = piece_get(a, bar, np)) != nullptr; ++np) {
     const int n = pp->j1 - pp->j0;
     const bool paired = pp->paired;
     piece_done(bar, np, lane);
@@ -497,7 +494,7 @@ QG_DEVICE void softmax(const AttnArgs &a, WideBars *bar, int s, int warp4, int l
   const float sl = fabsf(a.scale_log2);
   const bool neg = a.scale_log2 < 0.f;
   uint32_t n_s = 0, n_o = 0, np = 0;
-  for (const Piece *pp; (pp = piece_get(bar, np)) != nullptr; piece_done(bar, np++, lane)) {
+  for (const Piece *pp; (pp = piece_get(a, bar, np)) != nullptr; piece_done(bar, np++, lane)) {
     const Piece &p = *pp;
     // this thread's row
     const int sub = p.paired ? s : 0;
@@ -516,7 +513,7 @@ QG_DEVICE void softmax(const AttnArgs &a, WideBars *bar, int s, int warp4, int l
     const bool idle = !__any_sync(0xFFFFFFFFu, valid);  // no row of this warp is anyone's: whatever its weights are
     const int step = p.paired ? 1 : 2, first = p.paired ? p.j0 : p.j0 + s, j1 = p.j1, jp = p.jp;
     for (int j = first; j < j1; j += step) {
-      if (!warp_wait(&bar->s_full[s], n_s++ & 1, bar)) return;
+      if (!warp_wait(a, &bar->s_full[s], n_s++ & 1, bar)) return;
       tc_fence_after();
       if (idle) {
         if (lane == 0) mbar_arrive(&bar->p_full[s]);
@@ -608,7 +605,7 @@ QG_DEVICE void softmax(const AttnArgs &a, WideBars *bar, int s, int warp4, int l
     // ---- the piece's output
     const bool any = first < j1;
     if (any) {
-      if (!warp_wait(&bar->o_full[s], n_o++ & 1, bar)) return;
+      if (!warp_wait(a, &bar->o_full[s], n_o++ & 1, bar)) return;
       tc_fence_after();
       if (p.dirty) add_zeroed<D, BF16>(a, p, to, s, limp, lim);
     }
@@ -768,7 +765,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const __grid_con
     pdl_wait();
     return;
   }
-  if (threadIdx.x == 0) bar->limit = kWaitCycles + kWaitKey * (walk.end - walk.at) + kWaitSeg * 2 * a.b.B;
   if (warp == kMmaWarp) tmem_alloc(&bar->tmem, C::COLS);
   tc_fence_before();
   __syncthreads();
@@ -780,7 +776,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const __grid_con
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
     if (warp == kMmaWarp) {
-      issue_mma<D, BF16, OUT32>(sb, bar, lane);
+      issue_mma<D, BF16, OUT32>(a, sb, bar, lane);
       if (lane == 0) {
         // after an abort the products in flight finish before the tensor memory is released (a
         // normal run waited for each); q_empty counts pieces, so any further phase will do
