@@ -7,9 +7,9 @@
 // asynchronous copies in flight on every SM and spends few instructions per byte.
 //
 // Measured (one GB300, calls replayed from a graph; floor: bytes at the measured copy bandwidth):
-//   64 ragged sequences of up to 8191 tokens, 8 cached heads of 128, bf16   196 us, floor 177 (the kernel
-//     alone 185: 6.5 TB/s, 96 % of the copy)
-//   one sequence of 4097 tokens, f16 cache, f32 output                      16.5 us, floor 2.5: two
+//   64 ragged sequences of up to 8191 tokens, 8 cached heads of 128, bf16   199 us, floor 177 (the kernel
+//     alone 191: 6.3 TB/s, 93 % of the copy)
+//   one sequence of 4097 tokens, f16 cache, f32 output                      16.9 us, floor 2.5: two
 //     launches whose fixed parts (the scan, the look-ups, cold code) take most of it
 #include <math.h>
 
@@ -60,7 +60,7 @@ QG_DEVICE void add_nonfinite(const uint8_t *v, int key0, int qc, const int (&lim
 // tiles (16 keys, cp.async, no barrier wider than the warp), the piece's 16 query rows in
 // mma fragments, and writes the piece's unnormalised output, maximum and sum.  mma.sync
 // m16n8k16 fits here where tcgen05's 128-row tiles would be nearly empty: it runs at a fifth of
-// its rate beside the copies (tensor pipe 19 %, issue 26 % busy at 6.5 TB/s).  Eight warps of three
+// its rate beside the copies (tensor pipe 18 %, issue 26 % busy at 6.3 TB/s).  Eight warps of three
 // 8 KB stages keep 128 KB in flight on an SM, three times what its share of the bandwidth needs.
 template <int D, bool BF16, bool OUT32>
 __global__ void __launch_bounds__(NarrowCfg<D>::NW * 32, 1) attn_narrow_kernel(const __grid_constant__ AttnArgs a) {

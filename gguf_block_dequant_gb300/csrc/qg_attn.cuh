@@ -18,8 +18,8 @@
 //
 // Two kernels with a line each share a call: segments with few rows (at most one row tile of 16)
 // and segments with more (row tiles of two times 128).  The joining kernel reads both lines.  The
-// border, measured on 8 groups under 2999 tokens each: groups of 24 rows a head take 59 us on the
-// wide kernel and 62 as two narrow row tiles, groups of 32 rows 60 and 97.
+// border, measured on 8 groups under 2999 tokens each: groups of 24 rows a head take 60 us on the
+// wide kernel and 64 as two narrow row tiles, groups of 32 rows 61 and 99.
 #pragma once
 
 #include "qg_kv.cuh"

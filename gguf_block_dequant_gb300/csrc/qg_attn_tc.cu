@@ -20,14 +20,20 @@
 //
 // The running maximum a row's weights refer to is raised (and its output rescaled) only when the
 // row's maximum has grown by more than 2^8: weights stay below 2^8, exact in their ratios, and
-// the output in tensor memory is hardly ever touched between the products.
+// the output in tensor memory is hardly ever touched between the products.  Those sums are the tensor
+// cores' f32, whose additions round towards zero: n keys are n / 16 of them (twice that with two
+// weight terms), each low by up to 2^-23, which at 1 M keys of equal values a piece is 0.3 to 0.5 %.
 //
 // Measured (one GB300, whole calls replayed from a graph): prompts of 7832 tokens under a prefix of
-// 4001, 32 heads over 8 of 128, bf16: 563 us, 1.23 PFLOP/s (0.64 of the measured cuBLAS rate); 64
-// one-token sequences under a prefix of 32768 (512 rows a cached head): 74 us, of which this
-// kernel 37.  What bounds it: a pair of 128-row tiles and 128 keys takes about 3500 cycles, of
-// which the products alone need 3080 (2048 at the tensor cores' full rate: Q K^T reads both
-// operands from shared memory, 8 KB for 64 cycles' work) and a stream's softmax about 2000.
+// 4001, 32 heads over 8 of 128, bf16: 595 us, 1.17 PFLOP/s (0.61 of the measured cuBLAS rate); 64
+// one-token sequences under a prefix of 32768 (512 rows a cached head): 77 us, of which this
+// kernel about 40.  What bounds it: a pair of 128-row tiles and 128 keys takes about 3500 cycles, with the softmax
+// left out 3080 (2048 at the tensor cores' full rate: Q K^T reads both operands from shared
+// memory, 8 KB for 64 cycles' work), with a quarter of the products 3200.  So two chains of about one
+// length, the products' and scores -> weights -> P V -> next scores (the weights overwrite the
+// scores' columns), overlap only to 3500: shortening one alone gains a tenth at most.
+// The kernel's time also depends on how much code lies around its hot loops: parts that never run
+// cost up to 28 us of the prompts' 595.
 // The issuing warp's own instructions count: asking for the tiles' barriers while products are
 // queued, and letting go of V before the next scores, took 580 us to 563.  Tried and slower: an MMA
 // warp per stream (594 to 757), weights handed over in halves (636 to 645), more chains for the

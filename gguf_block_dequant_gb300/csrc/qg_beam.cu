@@ -6,11 +6,12 @@
 // bound it): a CTA streams a slice of one row through registers, keeps the slice's maximum and
 // sum of exponentials, and a short list of the values above the K-th best so far, which after
 // the first chunk hardly any value joins.  The second joins a request's slices: the row sums in
-// 64 bits, each row's K best, then the K best of W*K candidates ranked in 64 bits.
+// f32 (their logarithms in 64 bits), each row's K best, then the K best of W*K candidates ranked in
+// 64 bits.  So candidates of one row are in exact order, and those of two rows to about 1e-7, the sums' error.
 //
 // Measured: 16 requests of 8 beams over 151936 tokens (72 MB) 27 us, floor 10.7 (what it spends above
 // the bytes: 12 instructions a value, a chunk's barriers, 256 CTAs on 152 SMs, the merge's 5 us);
-// one request of 4 beams 10.2 us, two launches.
+// one request of 4 beams 10.5 us, two launches.
 #include <math.h>
 
 #include <algorithm>
