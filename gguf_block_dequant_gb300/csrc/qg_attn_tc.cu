@@ -670,9 +670,9 @@ QG_DEVICE void softmax(const AttnArgs &a, WideBars *bar, int s, int warp4, int l
 
 // A bit for each new token and cached head: the value at the token's position has infinite or NaN elements.
 // Positions in the prefix (of tokens before their sequence's first slot) and own ones have words of
-// their own, [2][heads][tokens / 32].  A warp per 32 tokens and head; reads the new tokens' values once (prompts of
-// 7832 tokens, 16 MB: the call takes 10 us longer for it, a launch and a chain of look-ups more than the bytes).
-// Looked up inside the wide kernel, a piece ahead or in the landed tiles, it cost the call 40 to 120 us.
+// their own, [2][heads][tokens / 32].  A warp per 32 tokens and head; reads the new tokens' values once
+// (prompts of 7832 tokens, 16 MB: 8.5 us, a launch and a chain of look-ups more than the bytes).  Looked up
+// inside the wide kernel, a piece ahead or in the landed tiles, it cost the call 40 to 120 us.
 template <int D, bool BF16>
 __global__ void __launch_bounds__(256) value_flags_kernel(const __grid_constant__ AttnArgs a) {
   constexpr int CH = D / 8, RPL = 32 / CH;  // 16-byte chunks of a row, rows a load of the warp takes
