@@ -419,7 +419,7 @@ def _own_verify(c, st):
 
 def _own_branch(c, st):
     qg = _package()
-    qg.kv_fork(st["batch"], st["refs"], src=st["src"])
+    qg.kv_fork(st["caches"], st["batch"], st["refs"], src=st["src"])
     qg.kv_reserve(st["caches"], st["batch"], st["refs"], st["add"], st["short"], st["ws"])
     return st["pages"], st["kv_len"], st["refs"], st["short"], st["pool"]
 
