@@ -80,6 +80,14 @@ def load():
             "qg_beam_workspace_size": ([I, I, I, I64], SZ),
             "qg_beam_select": ([P, P, P, I, I, I, I, I64, P, P, P, P, P, SZ, S], I),
             "qg_beam_reorder": ([P, I, P, I, P, S], I),
+            "qg_delta_workspace_size": ([P], SZ),
+            "qg_delta_rule": ([P, P, SZ, S], I),
+            "qg_token_probs": ([P, P, I, I64, P, S], I),
+            "qg_draft_verify": ([P, P, P, P, P, P, I, I, I64, P, P, P, P, S], I),
+            "qg_kv_fork": ([P, P, P, P, P, S], I),
+            "qg_kv_reserve_workspace_size": ([P, P], SZ),
+            "qg_kv_reserve": ([P, I, P, P, P, P, P, SZ, S], I),
+            "qg_kv_compact": ([P, I, P, P, P, P, I, S], I),
         }
         for name, (args, res) in sig.items():
             if hasattr(L, name):
@@ -579,3 +587,161 @@ def beam_reorder(caches, batch, parents, W, stream=None):
     _check(parents, "int32", "parents")
     _on(_cache_device(caches, batch), "parents", parents)
     _call("qg_beam_reorder", caches, len(caches), ctypes.byref(batch), W, _ptr(parents), _stream(stream))
+
+
+# ---- drafted decode ----------------------------------------------------------------------------
+
+class DeltaArgs(ctypes.Structure):
+    """qg_delta_args: one call of the gated delta rule."""
+    _fields_ = [*[(n, ctypes.c_int) for n in ("n_seqs", "n_tokens", "max_new", "Hk", "Hv", "Dk", "Dv", "head_order", "l2norm",
+                                              "n_slots")],
+                ("eps", ctypes.c_float), ("scale", ctypes.c_float),
+                *[(n, ctypes.c_void_p) for n in ("q_start", "q", "k", "v", "a", "b")],
+                *[(n, ctypes.c_int64) for n in ("q_stride", "k_stride", "v_stride", "a_stride", "b_stride")],
+                *[(n, ctypes.c_void_p) for n in ("a_scale", "a_bias", "states")], ("slot_stride", ctypes.c_int64),
+                *[(n, ctypes.c_void_p) for n in ("state_in", "state_out", "state_each", "out")],
+                ("out_stride", ctypes.c_int64)]
+
+
+def _gpu(t, what):
+    """The GPU of the tensor that the others of a call have to be with."""
+    d = t.get_device()
+    if d < 0:
+        raise ValueError(f"{what} must be on a GPU")
+    return d
+
+
+def _ints(t, n, what):
+    """A contiguous int32 tensor of n elements (None passes)."""
+    _check(t, "int32", what)
+    if t is not None and t.numel() != n:
+        raise ValueError(f"{what} must have {n} elements")
+
+
+def _seqs(q_start, T):
+    if q_start is None:
+        return T
+    _check(q_start, "int32", "q_start")
+    if q_start.dim() != 1 or q_start.numel() < 1:
+        raise ValueError("q_start must have n_seqs + 1 elements")
+    return q_start.numel() - 1
+
+
+def delta_workspace_size(T, n_seqs, Hk, Hv, Dk, Dv, max_new=0) -> int:
+    """Workspace of delta_rule for T tokens in n_seqs sequences, of at most max_new tokens each (0: not known)."""
+    g = DeltaArgs(n_seqs=n_seqs, n_tokens=T, max_new=max_new, Hk=Hk, Hv=Hv, Dk=Dk, Dv=Dv, q_stride=Hk * Dk, k_stride=Hk * Dk,
+                  v_stride=Hv * Dv, a_stride=Hv, b_stride=Hv, out_stride=Hv * Dv, q_start=16)
+    return int(load().qg_delta_workspace_size(ctypes.byref(g)))
+
+
+def delta_rule(q, k, v, a, b, states, state_in, state_out, out, workspace=None, q_start=None, max_new=0, state_each=None,
+               a_scale=None, a_bias=None, l2norm_eps=None, scale=1.0, tiled=False, stream=None):
+    """The gated delta rule (qg_delta_rule).  q, k [T][Hk][Dk] and v [T][Hv][Dv] f32, a, b [T][Hv] f32 (rows may be slices
+    of wider ones); states f32 [slots][Hv][Dk][Dv], state_in and state_out int32 [n_seqs] or None, state_each int32 [T]
+    or None; out f32 [T][Hv][Dv]; q_start int32 [n_seqs + 1] (None: one token per sequence).  a_scale and a_bias:
+    f32 [Hv], a and b are then raw; l2norm_eps: q and k are normalised; tiled: value head h takes key head h % Hk."""
+    if q.dim() != 3 or v.dim() != 3 or q.shape != k.shape or v.shape[0] != q.shape[0]:
+        raise ValueError("q and k must be [T][Hk][Dk] and v [T][Hv][Dv]")
+    (T, Hk, Dk), (Hv, Dv) = q.shape, v.shape[1:]
+    f32 = _types()[0]
+    for t, what in ((q, "q"), (k, "k"), (v, "v"), (a, "a"), (b, "b"), (out, "out"), (states, "states")):
+        if t is not None and t.dtype is not f32:
+            raise ValueError(f"{what} must be f32")
+    n = _seqs(q_start, T)
+    _ints(state_in, n, "state_in")
+    _ints(state_out, n, "state_out")
+    _ints(state_each, T, "state_each")
+    for t, what in ((a_scale, "a_scale"), (a_bias, "a_bias")):
+        _check(t, "float32", what)
+        if t is not None and t.numel() != Hv:
+            raise ValueError(f"{what} must have an element per value head")
+    slots, slot = 0, 0
+    if states is not None:
+        if states.dim() != 4 or tuple(states.shape[1:]) != (Hv, Dk, Dv) or (
+                states.shape[0] and not states[0].is_contiguous()):
+            raise ValueError("states must be [slots][Hv][Dk][Dv], contiguous in each slot")
+        slots, slot = states.shape[0], states.stride(0) if states.shape[0] > 1 else Hv * Dk * Dv
+    strides = [_rows(t, T, w, what) for t, w, what in ((q, Hk * Dk, "q"), (k, Hk * Dk, "k"), (v, Hv * Dv, "v"), (a, Hv, "a"),
+                                                       (b, Hv, "b"), (out, Hv * Dv, "out"))]
+    _on(_gpu(q, "q"), "k v a b states state_in state_out state_each out q_start a_scale a_bias workspace", k, v, a, b, states,
+        state_in, state_out, state_each, out, q_start, a_scale, a_bias, workspace)
+    g = DeltaArgs(n, T, int(max_new), Hk, Hv, Dk, Dv, int(bool(tiled)), int(l2norm_eps is not None), slots,
+                  float(l2norm_eps or 0.0), float(scale), _ptr(q_start), _ptr(q), _ptr(k), _ptr(v), _ptr(a), _ptr(b),
+                  *strides[:5], _ptr(a_scale), _ptr(a_bias), _ptr(states), slot, _ptr(state_in), _ptr(state_out),
+                  _ptr(state_each), _ptr(out), strides[5])
+    _call("qg_delta_rule", ctypes.byref(g), _ptr(workspace), _nbytes(workspace), _stream(stream))
+    return out
+
+
+def token_probs(logits, probs, temperature=None, stream=None):
+    """probs[t] = softmax(logits[t] / temperature[t]) (qg_token_probs); probs may be logits."""
+    T, V = (1, logits.shape[-1]) if logits.dim() == 1 else logits.shape
+    for t, what in ((logits, "logits"), (probs, "probs"), (temperature, "temperature")):
+        _check(t, "float32", what)
+    if probs.numel() != T * V or (temperature is not None and temperature.numel() != T):
+        raise ValueError("probs must have the logits' shape and temperature an element per row")
+    _on(_gpu(logits, "logits"), "probs temperature", probs, temperature)
+    _call("qg_token_probs", _ptr(logits), _ptr(temperature), T, V, _ptr(probs), _stream(stream))
+    return probs
+
+
+def draft_verify(probs, tokens, u, u_next, accepted, next_token, draft_probs=None, q_start=None, kv_len=None, kept_len=None,
+                 stream=None):
+    """How many drafted tokens of each sequence the target accepts, and the token drawn behind them (qg_draft_verify).
+    probs, draft_probs f32 [T][V]; tokens int32 [T], u f32 [T]; u_next f32, accepted and next_token int32 [n_seqs];
+    q_start int32 [n_seqs + 1] (None: one row each, a sampler); kv_len, kept_len int32 [n_seqs]."""
+    T, V = probs.shape
+    n = _seqs(q_start, T)
+    for t, size, dtype, what in ((probs, T * V, "float32", "probs"), (draft_probs, T * V, "float32", "draft_probs"),
+                                 (tokens, T, "int32", "tokens"), (u, T, "float32", "u"), (u_next, n, "float32", "u_next"),
+                                 (accepted, n, "int32", "accepted"), (next_token, n, "int32", "next_token"),
+                                 (kv_len, n, "int32", "kv_len"), (kept_len, n, "int32", "kept_len")):
+        _check(t, dtype, what)
+        if t is not None and t.numel() != size:
+            raise ValueError(f"{what} must have {size} elements")
+    _on(_gpu(probs, "probs"), "tokens u u_next accepted next_token draft_probs q_start kv_len kept_len", tokens, u, u_next,
+        accepted, next_token, draft_probs, q_start, kv_len, kept_len)
+    _call("qg_draft_verify", _ptr(probs), _ptr(draft_probs), _ptr(tokens), _ptr(u), _ptr(u_next), _ptr(q_start), n, T, V,
+          _ptr(accepted), _ptr(next_token), _ptr(kv_len), _ptr(kept_len), _stream(stream))
+    return accepted, next_token
+
+
+def _page_call(caches, batch, refs):
+    if refs.numel() != caches[0].n_pages:
+        raise ValueError("refs must have an element per page")
+    return _cache_device(caches, batch)
+
+
+def kv_fork(caches, batch, refs, src=None, keep=None, stream=None):
+    """Sequence b becomes the first keep[b] tokens of sequence src[b], in place: shared, truncated or freed (qg_kv_fork).
+    caches: kv_caches of all layers; refs: int32 [n_pages], the holders of each page."""
+    _check(refs, "int32", "refs")
+    _ints(src, batch.n_seqs, "src")
+    _ints(keep, batch.n_seqs, "keep")
+    _on(_page_call(caches, batch, refs), "refs src keep", refs, src, keep)
+    _call("qg_kv_fork", caches, ctypes.byref(batch), _ptr(refs), _ptr(src), _ptr(keep), _stream(stream))
+
+
+def reserve_workspace_size(caches, batch) -> int:
+    return int(load().qg_kv_reserve_workspace_size(caches, ctypes.byref(batch)))
+
+
+def kv_reserve(caches, batch, refs, add, missing, workspace, stream=None):
+    """Room for add[b] new tokens of each sequence (qg_kv_reserve).  caches: kv_caches of all layers; missing: int32 [1],
+    how many pages were too few (then nothing has changed)."""
+    _check(refs, "int32", "refs")
+    _ints(add, batch.n_seqs, "add")
+    _ints(missing, 1, "missing")
+    _on(_page_call(caches, batch, refs), "refs add missing workspace", refs, add, missing, workspace)
+    _call("qg_kv_reserve", caches, len(caches), ctypes.byref(batch), _ptr(refs), _ptr(add), _ptr(missing), _ptr(workspace),
+          _nbytes(workspace), _stream(stream))
+
+
+def kv_compact(caches, batch, src, keep_start, keep, stream=None):
+    """Slot i of sequence b receives the token in slot keep[keep_start[b] + i] of sequence src[b] (qg_kv_compact)."""
+    _ints(src, batch.n_seqs, "src")
+    _ints(keep_start, batch.n_seqs + 1, "keep_start")
+    _check(keep, "int32", "keep")
+    _on(_cache_device(caches, batch), "src keep_start keep", src, keep_start, keep)
+    _call("qg_kv_compact", caches, len(caches), ctypes.byref(batch), _ptr(src), _ptr(keep_start), _ptr(keep), keep.numel(),
+          _stream(stream))

@@ -1,0 +1,36 @@
+// qg_delta.cuh -- the gated delta rule's call as its kernels see it.
+#pragma once
+
+#include "qg_common.cuh"
+#include "qg_host.h"
+
+namespace qg {
+
+struct DeltaArgs {
+  int B, T, Hk, Hv, Dk, Dv, tiled, l2norm, n_slots;
+  float eps, scale;
+  const int32_t *q_start, *state_in, *state_out, *state_each;
+  const float *q, *k, *v, *a, *b, *a_scale, *a_bias;
+  long long q_stride, k_stride, v_stride, a_stride, b_stride, slot_stride, out_stride;
+  float *states, *out;
+};
+
+// first token row of sequence b (b = B: the end)
+QG_DEVICE int delta_tok(const DeltaArgs &a, int b) {
+  return a.q_start ? max(0, min(a.T, __ldg(a.q_start + b))) : min(b, a.T);
+}
+QG_DEVICE int delta_key_head(const DeltaArgs &a, int h) { return a.tiled ? h % a.Hk : h / (a.Hv / a.Hk); }
+
+// log decay and step of value head h at token t.  Log decays below -110 count as -110: e^g is 0 in f32, and
+// sums of them stay finite (fmaxf would turn NaN into -110).
+QG_DEVICE float2 delta_gates(const DeltaArgs &a, int t, int h) {
+  float g = __ldg(a.a + t * a.a_stride + h), beta = __ldg(a.b + t * a.b_stride + h);
+  if (a.a_scale) {
+    const float x = g + __ldg(a.a_bias + h);
+    g = __ldg(a.a_scale + h) * (x > 0.f ? x + log1pf(expf(-x)) : log1pf(expf(x)));
+    beta = 1.f / (1.f + expf(-beta));
+  }
+  return make_float2(g < -110.f ? -110.f : g, beta);
+}
+
+}  // namespace qg

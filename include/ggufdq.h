@@ -342,8 +342,8 @@ typedef struct qg_kv_cache {
 typedef struct qg_kv_batch {
   int n_seqs, n_tokens, n_groups, max_pages, max_prefix_pages;
   const int32_t *q_start;      /* [n_seqs + 1] or NULL */
-  const int32_t *kv_len;       /* [n_seqs] */
-  int32_t *pages;              /* written by qg_beam_reorder only */
+  const int32_t *kv_len;       /* [n_seqs]; written by qg_kv_fork and qg_kv_reserve only */
+  int32_t *pages;              /* written by these and qg_beam_reorder only */
   const int32_t *group_start;  /* [n_groups + 1] */
   const int32_t *prefix_len;   /* [n_groups] */
   const int32_t *prefix_pages; /* qg_kv_append does not read it */
@@ -424,6 +424,135 @@ QG_API qg_status qg_beam_select(const float *logits, const float *scores, const 
  * sets it and leaves the request as it is. */
 QG_API qg_status qg_beam_reorder(const qg_kv_cache *caches, int n_layers, const qg_kv_batch *batch, int W,
                                  const int32_t *parents, qg_stream_t stream);
+
+/* ---- drafted decode ----------------------------------------------------------------------------
+ * The steps of a server that drafts tokens, verifies them with the target model and branches its contexts,
+ * and the recurrent layers of hybrid decoders (gdnStep / gdnStepR and the DFlash runner on the pages).
+ *
+ * The gated delta rule of a linear-attention layer.  Every value head h of a sequence has a state matrix
+ * S [Dk][Dv]; a token with query q, key k, value v, log decay g and step beta does
+ *   S <- e^g S,   u = beta (v - S^T k),   S <- S + k u^T,   out = scale S^T q.
+ *   - Value head h takes the query and key of key head h / (Hv / Hk) (QG_HEADS_GROUPED) or h % Hk
+ *     (QG_HEADS_TILED).  Hv a multiple of Hk, Hv <= 1024; Dk 64 or 128; Dv a multiple of 32 up to 1024.
+ *   - a, b: with a_scale and a_bias (f32[Hv] each), g = a_scale[h] softplus(a + a_bias[h]) and beta =
+ *     sigmoid(b); with neither, g = a and beta = b.  Log decays below -110, -inf among them, count as -110: their e^g is 0.
+ *   - l2norm: q and k are first divided by sqrt(sum of squares + eps), eps >= 0.
+ *   - Rows: head h of token t's q at q + t*q_stride + h*Dk (k alike; v and out with Dv; a and b one float per value
+ *     head), strides in floats.  q, k, v, out 16-byte aligned with strides a multiple of 4; a and b 4-byte aligned.
+ *   - States live in n_slots slots; slot s, value head h, row i, column j is at
+ *     states[s*slot_stride + (h*Dk + i)*Dv + j] (16-byte aligned, slot_stride a multiple of 4).  Sequence
+ *     b starts from slot state_in[b], or from zeros where that is -1 (state_in NULL: all from zeros), and leaves
+ *     its last state in slot state_out[b], or nowhere (-1; NULL: none does).  state_each, NULL or int32[n_tokens],
+ *     names a slot for the state after each single token (-1: not kept): a server that drafts takes the one after the
+ *     last token it keeps as the next call's state_in.  A slot may be read and then written by the same sequence;
+ *     no slot may be written by one sequence and used by another in one call.  A sequence without tokens writes none.
+ *   - q_start: device int32[n_seqs + 1], the first token row of each sequence, rising from 0 (NULL: one token each,
+ *     n_tokens == n_seqs).  Rows behind the last sequence are left as they are.
+ *   - max_new: the most tokens that a sequence of the call has, as far as the caller knows (0: not known).  It
+ *     chooses between kernels; results are right whatever it says.
+ *   - A slot outside [-1, n_slots) sets QG_EDEVICE_ID: a state_in of that kind counts as -1, the others as not kept.
+ *   - A NaN or an infinity in a token's inputs reaches the tokens from that one on, never earlier ones nor other
+ *     sequences or heads, and one in column j of v only column j of the outputs.
+ * All sums and states are f32.  Prompts go through the tensor cores 32 tokens at a time, their operands as sums
+ * of two f16 terms with a power of two per row (22 bits).  Workspace: qg_delta_workspace_size bytes, 16-byte
+ * aligned, contents irrelevant, NULL where that is 0; one call at a time may use it.  args is a HOST struct.
+ * Limits: n_seqs <= 65535, n_tokens <= 2^24. */
+enum { QG_HEADS_GROUPED = 0, QG_HEADS_TILED = 1 };
+
+typedef struct qg_delta_args {
+  int n_seqs, n_tokens, max_new;
+  int Hk, Hv, Dk, Dv;
+  int head_order;                      /* QG_HEADS_GROUPED or QG_HEADS_TILED */
+  int l2norm;                          /* 0 or 1 */
+  int n_slots;
+  float eps, scale;
+  const int32_t *q_start;              /* [n_seqs + 1] or NULL */
+  const float *q, *k, *v, *a, *b;
+  int64_t q_stride, k_stride, v_stride, a_stride, b_stride;
+  const float *a_scale, *a_bias;       /* both or neither */
+  float *states;
+  int64_t slot_stride;
+  const int32_t *state_in, *state_out; /* [n_seqs] or NULL */
+  const int32_t *state_each;           /* [n_tokens] or NULL */
+  float *out;
+  int64_t out_stride;
+} qg_delta_args;
+
+QG_API size_t qg_delta_workspace_size(const qg_delta_args *args);
+QG_API qg_status qg_delta_rule(const qg_delta_args *args, void *workspace, size_t workspace_bytes,
+                               qg_stream_t stream);
+
+/* Probabilities of the next token: probs[t] = softmax(logits[t] / temperature[t]) over V values, f32.
+ *   - temperature: device f32[T], or NULL for 1 everywhere.  A temperature that is not above 0 (0, negative, NaN)
+ *     gives 1 to the lowest index of the largest logit and 0 to the rest; an infinite one, equal shares of all
+ *     finite logits.
+ *   - NaN logits count as -inf; a row whose largest logit is infinite has no distribution and gets zeros.
+ * Rows are contiguous; probs may be logits.  Pointers 16-byte aligned; 1 <= V <= 2^20, 0 <= T <= 65535. */
+QG_API qg_status qg_token_probs(const float *logits, const float *temperature, int T, int64_t V, float *probs,
+                                qg_stream_t stream);
+
+/* Verification of drafted tokens (the accept step of the DFlash and FlashMap runners, for sampled tokens).  Rows
+ * q_start[b] .. q_start[b+1]-1 belong to sequence b: tokens[] there are its pending token and then its drafts, and row t of
+ * probs (f32 [n_rows][V]) is the target's distribution of the token AFTER row t.  draft_probs, of the same shape,
+ * is what the drafter drew the token after row t from (its last row per sequence is not read); NULL: the drafts were
+ * certain.  With x = tokens[t + 1], q = draft_probs[t][x] (or 1), p = probs[t][x], a draft is accepted while
+ *   u[t] q < p.
+ * At the first row where it is not, the next token is drawn from max(probs - draft_probs, 0) (in f32; for certain drafts
+ * probs less 1 at x); if all are accepted, from the last row's probs; where nothing is left of the difference, from probs.
+ * The draw is the lowest v with  sum of r[w], w <= v,  >  u_next[b] * (sum of all r)  and r[v] > 0, or the last v with r[v]
+ * > 0 where there is none; sums and comparisons carry at least 48 bits.
+ *   - accepted int32[n_seqs]: how many drafts; next_token int32[n_seqs]: the drawn token, -1 where the row has no mass.
+ *   - kv_len, kept_len (both or neither; int32[n_seqs]): kept_len[b] = kv_len[b] - (drafts not accepted), what qg_kv_fork
+ *     is to leave of a cache that holds all of the step's rows.  They may be one array.
+ *   - Negative and NaN probabilities count as 0, those above 2^100 as 2^100, NaN and negative random numbers as
+ *     0.  A drafted token outside [0, V) is not accepted, sets QG_EDEVICE_ID, and nothing is taken from probs.
+ *   - A sequence without rows gets 0, -1 and its kv_len.  q_start NULL: one row each (a sampler; tokens and u may be NULL).
+ * probs, draft_probs 16-byte aligned, the rest 4-byte.  1 <= V <= 2^20, n_seqs <= 65535, n_rows <= 2^24. */
+QG_API qg_status qg_draft_verify(const float *probs, const float *draft_probs, const int32_t *tokens, const float *u,
+                                 const float *u_next, const int32_t *q_start, int n_seqs, int n_rows, int64_t V,
+                                 int32_t *accepted, int32_t *next_token, const int32_t *kv_len, int32_t *kept_len,
+                                 qg_stream_t stream);
+
+/* Pages with holders.  refs (device int32[n_pages]) counts the sequences whose page lists hold each page; a page
+ * with 0 is free.  The batch's sequences are rows of its tables: kv_len and pages are READ AND WRITTEN; q_start and
+ * groups are ignored.  A sequence holds the first (kv_len + page_size - 1) / page_size pages of its row; what lies behind
+ * in a row stays as it is.  Counting is by integer atomics on whole calls, so results do not depend on any order.
+ *
+ * Fork, truncate, free: sequence b becomes the first keep[b] tokens of sequence src[b].
+ *   - src[b] == b (src NULL: everywhere): truncated; src[b] == -1: freed, as with keep[b] 0; another src[b]: what b
+ *     held is released and it shares the source's pages, the last one too if it is begun.  keep NULL, keep[b] -1 or above
+ *     the source's length: all of it.
+ *   - A sequence that others take as their source must stay as it is in that call, with src its own number and keep -1 (or
+ *     NULL); a src[b] that does not, or one outside [-1, n_seqs), a keep[b] below -1, and lengths past the page lists set
+ *     QG_EDEVICE_ID and leave b as it is.  A page id
+ *     outside [0, n_pages) sets it and is not counted; nor does a count fall below 0.
+ * cache: any layer's (the number of pages and their size count). */
+QG_API qg_status qg_kv_fork(const qg_kv_cache *cache, const qg_kv_batch *batch, int32_t *refs, const int32_t *src,
+                            const int32_t *keep, qg_stream_t stream);
+
+/* Room for new tokens: kv_len[b] grows by add[b] (int32[n_seqs]), for qg_kv_append to fill.
+ *   - A sequence whose last page is begun and had more than one holder when the call began gets a page of its own
+ *     in its place, with the begun rows copied, in every layer; then follow the pages that the new length needs.  New pages are
+ *     the lowest free ones, in the order of the sequences and their columns, each with one holder.
+ *   - missing (device int32[1]): 0, or how many free pages were too few; then the call changes nothing else.
+ *   - A negative add[b], a length that is negative or would pass the page list, and a begun page outside the pool set
+ *     QG_EDEVICE_ID and leave b as it is.
+ * caches: HOST array of n_layers (<= 128) caches of one geometry.  Workspace: qg_kv_reserve_workspace_size bytes,
+ * 16-byte aligned, contents irrelevant; one call at a time may use it. */
+QG_API size_t qg_kv_reserve_workspace_size(const qg_kv_cache *caches, const qg_kv_batch *batch);
+QG_API qg_status qg_kv_reserve(const qg_kv_cache *caches, int n_layers, const qg_kv_batch *batch, int32_t *refs,
+                               const int32_t *add, int32_t *missing, void *workspace, size_t workspace_bytes,
+                               qg_stream_t stream);
+
+/* Compaction: slot i of sequence b receives the cached token in slot keep[keep_start[b] + i] of sequence src[b], in every
+ * layer, for i < keep_start[b+1] - keep_start[b]; src[b] -1: nothing.  keep_start: int32[n_seqs + 1], rising from 0 to at
+ * most n_keep, the length of keep.  Keys stay rotated as they are.
+ *   - The receiving pages must hold nothing that the call reads (pages from qg_kv_reserve, for instance); src[b] == b,
+ *     src[b] outside [-1, n_seqs), more tokens than b's kv_len, slots outside the source's kv_len and pages outside
+ *     the pool set QG_EDEVICE_ID, and those tokens are not copied.
+ * caches as in qg_kv_reserve.  n_keep <= 2^24. */
+QG_API qg_status qg_kv_compact(const qg_kv_cache *caches, int n_layers, const qg_kv_batch *batch, const int32_t *src,
+                               const int32_t *keep_start, const int32_t *keep, int n_keep, qg_stream_t stream);
 
 #ifdef __cplusplus
 }
