@@ -144,7 +144,7 @@ qg_status qg_device_status(uint32_t *status_out, int clear) {
                             qg::read_status_moetc(clear != 0), qg::read_status_kv(clear != 0),
                             qg::read_status_attn(clear != 0), qg::read_status_attn_tc(clear != 0),
                             qg::read_status_draft(clear != 0), qg::read_status_pages(clear != 0),
-                            qg::read_status_delta(clear != 0)};
+                            qg::read_status_delta(clear != 0), qg::read_status_delta_chunk(clear != 0)};
   unsigned int all = 0;
   for (const unsigned int v : w) {
     if (v == 0xFFFFFFFFu) return QG_ECUDA;

@@ -210,6 +210,13 @@ qg_status check(const qg_delta_args *g, DeltaArgs *a) {
   return QG_OK;
 }
 
+// whether the call's longer sequences go in chunks: single tokens, calls said to be short, and those that keep each
+// token's state go token after token
+bool in_chunks(const qg_delta_args &g) {
+  const int most = g.max_new > 0 ? std::min(g.max_new, g.n_tokens) : g.n_tokens;
+  return g.q_start && !g.state_each && most >= qg::kDeltaFirstLen;
+}
+
 }  // namespace
 
 namespace qg {
@@ -231,8 +238,8 @@ extern "C" {
 
 size_t qg_delta_workspace_size(const qg_delta_args *args) {
   DeltaArgs a;
-  if (check(args, &a) != QG_OK) return 0;
-  return 0;
+  if (check(args, &a) != QG_OK || !in_chunks(*args)) return 0;
+  return qg::delta_chunk_workspace(a);
 }
 
 qg_status qg_delta_rule(const qg_delta_args *args, void *workspace, size_t workspace_bytes, qg_stream_t stream) {
@@ -250,8 +257,9 @@ qg_status qg_delta_rule(const qg_delta_args *args, void *workspace, size_t works
   if (!dev.ok) return QG_ECUDA;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   g_launched = true;
-  const int first_len = 0x7FFFFFFF;
-  const cudaError_t e = a.Dk == 64 ? tokens_launch<64>(a, first_len, dev.sms, s) : tokens_launch<128>(a, first_len, dev.sms, s);
+  const int first_len = in_chunks(*args) ? qg::kDeltaFirstLen : 0x7FFFFFFF;
+  cudaError_t e = a.Dk == 64 ? tokens_launch<64>(a, first_len, dev.sms, s) : tokens_launch<128>(a, first_len, dev.sms, s);
+  if (e == cudaSuccess && in_chunks(*args)) e = qg::delta_chunks(a, first_len, workspace, s);
   if (e != cudaSuccess) return QG_ECUDA;
   return cudaGetLastError() == cudaSuccess ? QG_OK : QG_ECUDA;
 }

@@ -15,6 +15,14 @@ struct DeltaArgs {
   float *states, *out;
 };
 
+constexpr int kDeltaChunk = 32;  // tokens of a chunk
+// sequences from this many tokens on go in chunks
+constexpr int kDeltaFirstLen = 24;
+
+// the chunk kernels (qg_delta_chunk.cu), for sequences of first_len tokens and more
+size_t delta_chunk_workspace(const DeltaArgs &a);
+cudaError_t delta_chunks(const DeltaArgs &a, int first_len, void *ws, cudaStream_t s);
+
 // first token row of sequence b (b = B: the end)
 QG_DEVICE int delta_tok(const DeltaArgs &a, int b) {
   return a.q_start ? max(0, min(a.T, __ldg(a.q_start + b))) : min(b, a.T);

@@ -1,0 +1,681 @@
+// qg_delta_chunk.cu -- the gated delta rule over prompts, 32 tokens at a time on the tensor cores.
+//
+// With G_i the sum of the log decays of a chunk's tokens up to i and S0 the state before the chunk, the updates u_i of
+// the definition solve
+//   u_i + sum_{j<i} beta_i e^{G_i - G_j} (k_i . k_j) u_j = beta_i (v_i - e^{G_i} S0^T k_i),
+// a unit lower triangular system (1 + A) U = diag(beta) (...).  With T = (1 + A)^-1 diag(beta):
+//   R = V - diag(e^G) K S0,   U = T R,
+//   O = diag(e^G) Q S0 + [e^{G_i - G_j} q_i . k_j, j <= i] U,   S = e^{G_C} S0 + K^T diag(e^{G_C - G}) U.
+// Everything that does not need S0 (norms, T, the decayed Q K^T) comes from one kernel, parallel over chunks and heads;
+// a second one walks the chunks of each head with the state in registers.  No exponent is above 0 while log
+// decays are not; sums of them are kept in two terms, so that decays between neighbours stay exact after strong ones.
+//
+// Products run on mma.sync in f16 with f32 sums.  Each operand is x = s (hi + lo), s a power of two per row that
+// brings the row's largest magnitude to [2^7, 2^8), hi the f16 nearest x/s and lo the one nearest the rest: 22
+// bits; hi hi + hi lo + lo hi leaves 2^-22 of each product.  (bf16 terms would leave 2^-16, tf32 ones cost twice.)
+#include <algorithm>
+#include <atomic>
+
+#include "qg_delta.cuh"
+#include "qg_mma.cuh"
+
+__device__ unsigned int g_qg_status_delta_chunk;  // this translation unit's device status word
+static std::atomic<bool> g_launched{false};       // whether a kernel that may set it has been launched
+
+namespace {
+
+using qg::DeltaArgs;
+constexpr int C = qg::kDeltaChunk;
+static_assert(C == 32, "a lane per token");
+
+// ---- the workspace ------------------------------------------------------------------------------
+// Sequence b's chunks have the numbers q_start[b] / 32 + b, and on: they rise, and ceil(n / 32) of them fit
+// before the next sequence's.  Per (chunk, key head): K hi, K lo, Q hi, Q lo, [32][DK] f16 each.  Per (chunk, value head):
+// T hi, T lo, A hi, A lo, [32][32] f16 each, and the factors below.  Tiles are stored as shared memory wants them:
+// 16-byte pieces of a row exchanged so that eight rows of one piece lie in all banks.
+template <int DK>
+struct Tiles {
+  static constexpr int kKQ = C * DK * 2;             // bytes of one key or query tile
+  static constexpr int kKQAll = 4 * kKQ;
+};
+constexpr int kSq = C * C * 2;  // bytes of one square tile
+struct Factors {
+  float fk[C];     // e^{G_j} sk_j: what K S0 is multiplied by
+  float fq[C];     // e^{G_i} sq_i
+  float st[C];     // row scales of T
+  float sa[C];     // row scales of the decayed Q K^T
+  float wk[C];     // e^{G_C - G_j} sk_j
+  float alpha[C], beta[C], sk[C], sq[C];  // token by token, for chunks with infinite or NaN values
+  float dec;       // e^{G_C}
+  float pad[31];
+};
+constexpr int kTA = 4 * kSq + static_cast<int>(sizeof(Factors));
+static_assert(kTA % 16 == 0, "bulk copies");
+
+template <int DK>
+QG_DEVICE uint32_t kq_at(int row, int piece) {  // byte offset of 16-byte piece `piece` of a row
+  return row * (DK * 2) + ((piece ^ (row & 7)) << 4);
+}
+QG_DEVICE uint32_t sq_at(int row, int piece) { return row * (C * 2) + ((piece ^ ((row >> 1) & 3)) << 4); }
+
+// the power of two that brings magnitude bits m to [2^7, 2^8), and its inverse; 1 for infinities and NaN
+QG_DEVICE void row_scale(uint32_t m, float &s, float &inv) {
+  const uint32_t e = max(m >> 23, 8u);
+  s = e == 255u ? 1.f : __uint_as_float((e - 7u) << 23);
+  inv = e == 255u ? 1.f : __uint_as_float((261u - e) << 23);
+}
+QG_DEVICE uint32_t mag(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+constexpr uint32_t kInfBits = 0x7F800000u;
+
+// two values as packed f16 hi and lo terms
+QG_DEVICE void split2(float x, float y, uint32_t &hi, uint32_t &lo) {
+  hi = pack16<false>(x, y);
+  lo = pack16<false>(x - lo16<false>(hi), y - hi16<false>(hi));
+}
+
+QG_DEVICE void mma3(float (&c)[4], const uint32_t (&ah)[4], const uint32_t (&al)[4], uint32_t bh0, uint32_t bh1,
+                    uint32_t bl0, uint32_t bl1) {
+  mma16816<false>(c, al, bh0, bh1);
+  mma16816<false>(c, ah, bl0, bl1);
+  mma16816<false>(c, ah, bh0, bh1);
+}
+
+QG_DEVICE int chunk_base(const DeltaArgs &a, int b) { return qg::delta_tok(a, b) / C + b; }
+
+struct ChunkArgs {
+  DeltaArgs d;
+  unsigned char *kq, *ta;
+  int first_len;  // shorter sequences are not this kernel's
+  int slots;      // chunk numbers there is room for
+};
+
+// ---- what does not need the state -------------------------------------------------------------------
+// A CTA of four warps per chunk and key head.  Rows are normalised and split by a warp each; the products of keys with keys and
+// queries with keys take a warp per 16 rows; then a warp per value head solves for T, a lane per column.
+constexpr int kPrepWarps = 4;
+
+template <int DK>
+__global__ void __launch_bounds__(kPrepWarps * 32) delta_prep_kernel(const ChunkArgs a) {
+  extern __shared__ __align__(128) unsigned char tile[];  // K hi, K lo, Q hi, Q lo
+  __shared__ float kk[C][C + 1], qk[C][C + 1];
+  __shared__ float scale_k[C], scale_q[C];
+  __shared__ __align__(16) float mat[kPrepWarps][C][C + 4];
+  __shared__ float2 gsum[kPrepWarps][C];
+  __shared__ float sbeta[kPrepWarps][C];
+  constexpr int KQ = Tiles<DK>::kKQ;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int slot = static_cast<int>(blockIdx.x) / a.d.Hk, hk = static_cast<int>(blockIdx.x) % a.d.Hk;
+  pdl_wait();
+  pdl_launch_dependents();
+  // the sequence whose chunk this is
+  int lo = 0, hi = a.d.B;  // chunk_base(lo) <= slot < chunk_base(hi), as far as is known
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (chunk_base(a.d, mid) <= slot) lo = mid;
+    else hi = mid;
+  }
+  const int t00 = qg::delta_tok(a.d, lo), n = qg::delta_tok(a.d, lo + 1) - t00;
+  const int first = (slot - chunk_base(a.d, lo)) * C;
+  if (n < a.first_len || first < 0 || first >= n) return;
+  const int len = min(C, n - first), t0 = t00 + first;
+
+  // rows: 8 of K and 8 of Q a warp
+  constexpr int E = DK / 32;
+  for (int r = warp; r < 2 * C; r += kPrepWarps) {
+    const bool is_q = r >= C;
+    const int i = r & (C - 1);
+    float x[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] = 0.f;
+    if (i < len) {
+      const float *p = (is_q ? a.d.q + (t0 + i) * a.d.q_stride : a.d.k + (t0 + i) * a.d.k_stride) + hk * DK + lane * E;
+      if constexpr (E == 4) {
+        const float4 v = __ldg(reinterpret_cast<const float4 *>(p));
+        x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+      } else {
+        const float2 v = __ldg(reinterpret_cast<const float2 *>(p));
+        x[0] = v.x, x[1] = v.y;
+      }
+    }
+    float f = is_q ? a.d.scale : 1.f;
+    if (a.d.l2norm) {
+      float ss = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) ss = fmaf(x[e], x[e], ss);
+      ss = warp_sum(ss) + a.d.eps;
+      if (i < len) f *= 1.f / sqrtf(ss);
+    }
+    uint32_t m = 0;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      x[e] *= f;
+      m = max(m, mag(x[e]));
+    }
+    m = __reduce_max_sync(0xFFFFFFFFu, m);
+    float s, inv;
+    row_scale(m, s, inv);
+    unsigned char *t = tile + (is_q ? 2 * KQ : 0);
+    const int byte = lane * E * 2;  // of the row
+    const uint32_t at = kq_at<DK>(i, byte >> 4) + (byte & 15);
+#pragma unroll
+    for (int e = 0; e < E; e += 2) {
+      uint32_t h, l;
+      split2(x[e] * inv, x[e + 1] * inv, h, l);
+      *reinterpret_cast<uint32_t *>(t + at + 2 * e) = h;
+      *reinterpret_cast<uint32_t *>(t + KQ + at + 2 * e) = l;
+    }
+    if (lane == 0) (is_q ? scale_q : scale_k)[i] = s;
+  }
+  __syncthreads();
+  {
+    uint4 *dst = reinterpret_cast<uint4 *>(a.kq + (static_cast<size_t>(slot) * a.d.Hk + hk) * Tiles<DK>::kKQAll);
+    const uint4 *src = reinterpret_cast<const uint4 *>(tile);
+    for (int i = tid; i < Tiles<DK>::kKQAll / 16; i += kPrepWarps * 32) dst[i] = src[i];
+  }
+  // products: warps 0, 1 keys with keys, 2, 3 queries with keys; 16 rows each
+  {
+    const uint32_t k0 = smem_u32(tile), rows = k0 + (warp >= 2 ? 2 * KQ : 0);
+    const int r0 = (warp & 1) * 16;
+    float c[4][4] = {};
+#pragma unroll
+    for (int ks = 0; ks < DK / 16; ++ks) {
+      uint32_t ah[4], al[4];
+      const uint32_t at = kq_at<DK>(r0 + (lane & 15), 2 * ks + (lane >> 4));
+      ldsm4(ah, rows + at);
+      ldsm4(al, rows + KQ + at);
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        uint32_t bh[4], bl[4];
+        const uint32_t bt = kq_at<DK>(16 * p + (lane & 7) + ((lane >> 4) << 3), 2 * ks + ((lane >> 3) & 1));
+        ldsm4(bh, k0 + bt);
+        ldsm4(bl, k0 + KQ + bt);
+        mma3(c[2 * p], ah, al, bh[0], bh[1], bl[0], bl[1]);
+        mma3(c[2 * p + 1], ah, al, bh[2], bh[3], bl[2], bl[3]);
+      }
+    }
+    float(*out)[C + 1] = warp >= 2 ? qk : kk;
+    const float *sr = warp >= 2 ? scale_q : scale_k;
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int i = r0 + (lane >> 2) + 8 * (e >> 1), j = 8 * t + 2 * (lane & 3) + (e & 1);
+        out[i][j] = c[t][e] * sr[i] * scale_k[j];
+      }
+  }
+  __syncthreads();
+
+  const int group = a.d.Hv / a.d.Hk;
+  for (int r = warp; r < group; r += kPrepWarps) {
+    const int h = a.d.tiled ? hk + r * a.d.Hk : hk * group + r;
+    float(*const M)[C + 4] = mat[warp];
+    float2 ga = make_float2(0.f, 0.f);
+    if (lane < len) ga = qg::delta_gates(a.d, t0 + lane, h);
+    double sum = ga.x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const double y = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+      if (lane >= o) sum += y;
+    }
+    const float g_hi = static_cast<float>(sum), g_lo = static_cast<float>(sum - g_hi);
+    __syncwarp();
+    gsum[warp][lane] = make_float2(g_hi, g_lo);
+    sbeta[warp][lane] = ga.y;
+    __syncwarp();
+    // a lane per row i: decays from j to i, and the system's row
+    float dec[C];
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      const float2 gj = gsum[warp][j];
+      dec[j] = j <= lane ? expf((g_hi - gj.x) + (g_lo - gj.y)) : 0.f;
+      M[lane][j] = j < lane ? ga.y * dec[j] * kk[lane][j] : 0.f;
+    }
+    __syncwarp();
+    // a lane per column: (1 + A) X = 1 from the top
+    float x[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      float acc = i == lane ? 1.f : 0.f;
+#pragma unroll
+      for (int j4 = 0; j4 < i; j4 += 4) {
+        const float4 m = *reinterpret_cast<const float4 *>(&M[i][j4]);
+        acc = fmaf(-m.x, x[j4], acc);
+        if (j4 + 1 < i) acc = fmaf(-m.y, x[j4 + 1], acc);
+        if (j4 + 2 < i) acc = fmaf(-m.z, x[j4 + 2], acc);
+        if (j4 + 3 < i) acc = fmaf(-m.w, x[j4 + 3], acc);
+      }
+      x[i] = i < lane ? 0.f : acc;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < C; ++i) M[i][lane] = i < lane ? 0.f : x[i] * ga.y;
+    __syncwarp();
+    // a lane per row: both square tiles
+    unsigned char *ta = a.ta + (static_cast<size_t>(slot) * a.d.Hv + h) * kTA;
+    Factors *f = reinterpret_cast<Factors *>(ta + 4 * kSq);
+    auto write_row = [&](float (&v)[C], unsigned char *dst, float *scales) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int j = 0; j < C; ++j) m = max(m, mag(v[j]));
+      float s, inv;
+      row_scale(m, s, inv);
+      scales[lane] = s;
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        uint32_t h4[4], l4[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) split2(v[8 * p + 2 * e] * inv, v[8 * p + 2 * e + 1] * inv, h4[e], l4[e]);
+        *reinterpret_cast<uint4 *>(dst + sq_at(lane, p)) = make_uint4(h4[0], h4[1], h4[2], h4[3]);
+        *reinterpret_cast<uint4 *>(dst + kSq + sq_at(lane, p)) = make_uint4(l4[0], l4[1], l4[2], l4[3]);
+      }
+    };
+    {
+      float v[C];
+#pragma unroll
+      for (int j = 0; j < C; j += 4) {
+        const float4 m = *reinterpret_cast<const float4 *>(&M[lane][j]);
+        v[j] = m.x, v[j + 1] = m.y, v[j + 2] = m.z, v[j + 3] = m.w;
+      }
+      write_row(v, ta, f->st);
+#pragma unroll
+      for (int j = 0; j < C; ++j) v[j] = j <= lane ? dec[j] * qk[lane][j] : 0.f;
+      write_row(v, ta + 2 * kSq, f->sa);
+    }
+    const float2 gl = gsum[warp][C - 1];
+    const float eg = expf(g_hi + g_lo);
+    f->fk[lane] = eg * scale_k[lane];
+    f->fq[lane] = eg * scale_q[lane];
+    f->wk[lane] = expf((gl.x - g_hi) + (gl.y - g_lo)) * scale_k[lane];
+    f->alpha[lane] = expf(ga.x);
+    f->beta[lane] = ga.y;
+    f->sk[lane] = scale_k[lane];
+    f->sq[lane] = scale_q[lane];
+    if (lane == 0) f->dec = expf(gl.x + gl.y);
+    __syncwarp();
+  }
+}
+
+// ---- the walk ------------------------------------------------------------------------------------------
+// A warp owns 16 columns of a head's state, as S^T in the accumulator layout (rows: columns of S): it is the left operand of
+// both products with the old state, U^T in turn the left operand of the next two, so nothing but the tiles from the
+// kernel above passes through shared memory, and warps never wait for one another.  The tiles come through a ring of
+// bulk copies; the warp that leaves a stage last asks for its next contents.
+template <int DK, int W, int NST>
+struct WalkSmem {
+  static constexpr int kStage = Tiles<DK>::kKQAll + kTA;
+  static constexpr int kBytes = NST * kStage + 128;
+};
+
+template <int DK, int W, int NST>
+__global__ void __launch_bounds__(W * 32) delta_walk_kernel(const ChunkArgs a) {
+  extern __shared__ __align__(128) unsigned char ring[];
+  __shared__ uint64_t full[NST];
+  __shared__ int left[NST];  // warps that are done with a stage's contents
+  constexpr int KQ = Tiles<DK>::kKQ, kStage = WalkSmem<DK, W, NST>::kStage;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int parts = a.d.Dv / (16 * W);
+  const int part = static_cast<int>(blockIdx.x) % parts, bh = static_cast<int>(blockIdx.x) / parts;
+  const int h = bh % a.d.Hv, b = bh / a.d.Hv;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int t00 = qg::delta_tok(a.d, b), n = qg::delta_tok(a.d, b + 1) - t00;
+  if (n < a.first_len || n <= 0) return;
+  const int chunks = (n + C - 1) / C;
+  if (tid == 0) {
+    for (int i = 0; i < NST; ++i) {
+      mbar_init(&full[i], 1);
+      left[i] = 0;
+    }
+    fence_mbar_init();
+  }
+  __syncthreads();
+  const int slot0 = chunk_base(a.d, b), hk = qg::delta_key_head(a.d, h);
+  if (slot0 + chunks > a.slots) return;
+
+  auto ask = [&](int c) {
+    unsigned char *dst = ring + (c % NST) * kStage;
+    uint64_t *bar = &full[c % NST];
+    mbar_arrive_expect_tx(bar, kStage);
+    bulk_g2s(dst, a.kq + (static_cast<size_t>(slot0 + c) * a.d.Hk + hk) * Tiles<DK>::kKQAll, Tiles<DK>::kKQAll, bar);
+    bulk_g2s(dst + Tiles<DK>::kKQAll, a.ta + (static_cast<size_t>(slot0 + c) * a.d.Hv + h) * kTA, kTA, bar);
+  };
+  if (tid == 0) {
+    asm volatile("fence.proxy.async;" ::: "memory");  // the tiles were written by plain stores
+    for (int c = 0; c < min(NST, chunks); ++c) ask(c);
+  }
+
+  const int q4 = lane & 3, r8 = lane >> 2;
+  const int d0 = h * a.d.Dv + (part * W + warp) * 16 + r8;  // this lane's columns of S: d0 and d0 + 8
+  const bool teller = tid == 0 && part == 0 && h == 0;
+  // the state: s[ct] holds rows 8 ct + 2 q4, + 1 of S for column d0, then for d0 + 8
+  float s[DK / 8][4];
+  {
+    const int in = a.d.state_in ? __ldg(a.d.state_in + b) : -1;
+    if (teller && (in < -1 || in >= a.d.n_slots)) atomicOr(&g_qg_status_delta_chunk, QG_STATUS_BIT_ID);
+    const bool have = in >= 0 && in < a.d.n_slots;
+    const float *p = a.d.states + (have ? in : 0) * a.d.slot_stride + static_cast<long long>(h) * DK * a.d.Dv + (d0 - h * a.d.Dv);
+#pragma unroll
+    for (int ct = 0; ct < DK / 8; ++ct)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        s[ct][e] = have ? p[static_cast<long long>(8 * ct + 2 * q4 + (e & 1)) * a.d.Dv + 8 * (e >> 1)] : 0.f;
+  }
+  const float *vp = a.d.v + d0;
+  float *op = a.d.out + d0;
+  auto load_v = [&](int c, float (&v)[4][4]) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int j = c * C + 8 * t + 2 * q4 + (e & 1);
+        v[t][e] = j < n ? __ldg(vp + static_cast<long long>(t00 + j) * a.d.v_stride + 8 * (e >> 1)) : 0.f;
+      }
+  };
+  float v[4][4];
+  load_v(0, v);
+
+  for (int c = 0; c < chunks; ++c) {
+    const int st = c % NST;
+    if (!mbar_wait(&full[st], (c / NST) & 1)) {
+      if (lane == 0) atomicOr(&g_qg_status_delta_chunk, QG_STATUS_BIT_TIMEOUT);
+      return;
+    }
+    const uint32_t kt = smem_u32(ring + st * kStage), qt = kt + 2 * KQ, tt = kt + Tiles<DK>::kKQAll, at = tt + 2 * kSq;
+    const Factors *f = reinterpret_cast<const Factors *>(ring + st * kStage + Tiles<DK>::kKQAll + 4 * kSq);
+    float o[4][4] = {};
+    bool odd = false;
+    {
+      // rows of S^T in two terms
+      uint32_t m0 = 0, m1 = 0;
+#pragma unroll
+      for (int ct = 0; ct < DK / 8; ++ct) {
+        m0 = max(m0, max(mag(s[ct][0]), mag(s[ct][1])));
+        m1 = max(m1, max(mag(s[ct][2]), mag(s[ct][3])));
+      }
+      m0 = max(m0, __shfl_xor_sync(0xFFFFFFFFu, m0, 1));
+      m1 = max(m1, __shfl_xor_sync(0xFFFFFFFFu, m1, 1));
+      m0 = max(m0, __shfl_xor_sync(0xFFFFFFFFu, m0, 2));
+      m1 = max(m1, __shfl_xor_sync(0xFFFFFFFFu, m1, 2));
+      float s0, i0, s1, i1;
+      row_scale(m0, s0, i0);
+      row_scale(m1, s1, i1);
+      float x[4][4] = {};
+#pragma unroll
+      for (int ks = 0; ks < DK / 16; ++ks) {
+        uint32_t ah[4], al[4];
+        split2(s[2 * ks][0] * i0, s[2 * ks][1] * i0, ah[0], al[0]);
+        split2(s[2 * ks][2] * i1, s[2 * ks][3] * i1, ah[1], al[1]);
+        split2(s[2 * ks + 1][0] * i0, s[2 * ks + 1][1] * i0, ah[2], al[2]);
+        split2(s[2 * ks + 1][2] * i1, s[2 * ks + 1][3] * i1, ah[3], al[3]);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          uint32_t bh[4], bl[4];
+          const uint32_t off = kq_at<DK>(16 * p + (lane & 7) + ((lane >> 4) << 3), 2 * ks + ((lane >> 3) & 1));
+          ldsm4(bh, kt + off);
+          ldsm4(bl, kt + KQ + off);
+          mma3(x[2 * p], ah, al, bh[0], bh[1], bl[0], bl[1]);
+          mma3(x[2 * p + 1], ah, al, bh[2], bh[3], bl[2], bl[3]);
+          ldsm4(bh, qt + off);
+          ldsm4(bl, qt + KQ + off);
+          mma3(o[2 * p], ah, al, bh[0], bh[1], bl[0], bl[1]);
+          mma3(o[2 * p + 1], ah, al, bh[2], bh[3], bl[2], bl[3]);
+        }
+      }
+      // R^T = V^T - e^G (K S0)^T, in v; O^T = e^G (Q S0)^T
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const float2 fk = *reinterpret_cast<const float2 *>(f->fk + 8 * t + 2 * q4);
+        const float2 fq = *reinterpret_cast<const float2 *>(f->fq + 8 * t + 2 * q4);
+        v[t][0] = fmaf(-fk.x * s0, x[t][0], v[t][0]);
+        v[t][1] = fmaf(-fk.y * s0, x[t][1], v[t][1]);
+        v[t][2] = fmaf(-fk.x * s1, x[t][2], v[t][2]);
+        v[t][3] = fmaf(-fk.y * s1, x[t][3], v[t][3]);
+        o[t][0] *= fq.x * s0;
+        o[t][1] *= fq.y * s0;
+        o[t][2] *= fq.x * s1;
+        o[t][3] *= fq.y * s1;
+      }
+    }
+    // scales of the rows of a [16][32] accumulator; whether all of it is finite
+    auto scales = [&](const float (&w)[4][4], float &s0, float &i0, float &s1, float &i1) {
+      uint32_t m0 = 0, m1 = 0;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        m0 = max(m0, max(mag(w[t][0]), mag(w[t][1])));
+        m1 = max(m1, max(mag(w[t][2]), mag(w[t][3])));
+      }
+      m0 = max(m0, __shfl_xor_sync(0xFFFFFFFFu, m0, 1));
+      m1 = max(m1, __shfl_xor_sync(0xFFFFFFFFu, m1, 1));
+      m0 = max(m0, __shfl_xor_sync(0xFFFFFFFFu, m0, 2));
+      m1 = max(m1, __shfl_xor_sync(0xFFFFFFFFu, m1, 2));
+      row_scale(m0, s0, i0);
+      row_scale(m1, s1, i1);
+      return !__any_sync(0xFFFFFFFFu, max(m0, m1) >= kInfBits);
+    };
+    auto split = [&](const float (&w)[4][4], float i0, float i1, uint32_t (&ah)[2][4], uint32_t (&al)[2][4]) {
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        split2(w[2 * ks][0] * i0, w[2 * ks][1] * i0, ah[ks][0], al[ks][0]);
+        split2(w[2 * ks][2] * i1, w[2 * ks][3] * i1, ah[ks][1], al[ks][1]);
+        split2(w[2 * ks + 1][0] * i0, w[2 * ks + 1][1] * i0, ah[ks][2], al[ks][2]);
+        split2(w[2 * ks + 1][2] * i1, w[2 * ks + 1][3] * i1, ah[ks][3], al[ks][3]);
+      }
+    };
+    // w (16 x 32) times a lower triangular square tile's transpose
+    auto times_tile = [&](const uint32_t (&ah)[2][4], const uint32_t (&al)[2][4], uint32_t tile, float (&w)[4][4]) {
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int ks = 0; ks <= p; ++ks) {
+          uint32_t bh[4], bl[4];
+          const uint32_t off = sq_at(16 * p + (lane & 7) + ((lane >> 4) << 3), 2 * ks + ((lane >> 3) & 1));
+          ldsm4(bh, tile + off);
+          ldsm4(bl, tile + kSq + off);
+          mma3(w[2 * p], ah[ks], al[ks], bh[0], bh[1], bl[0], bl[1]);
+          mma3(w[2 * p + 1], ah[ks], al[ks], bh[2], bh[3], bl[2], bl[3]);
+        }
+    };
+    float u[4][4] = {};
+    {
+      float s0, i0, s1, i1;
+      odd = !scales(v, s0, i0, s1, i1);
+      if (!odd) {
+        uint32_t ah[2][4], al[2][4];
+        split(v, i0, i1, ah, al);
+        times_tile(ah, al, tt, u);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const float2 x = *reinterpret_cast<const float2 *>(f->st + 8 * t + 2 * q4);
+          u[t][0] *= x.x * s0;
+          u[t][1] *= x.y * s0;
+          u[t][2] *= x.x * s1;
+          u[t][3] *= x.y * s1;
+        }
+        odd = !scales(u, s0, i0, s1, i1);
+      }
+      if (!odd) {
+        uint32_t ah[2][4], al[2][4];
+        split(u, i0, i1, ah, al);
+        float w[4][4] = {};
+        times_tile(ah, al, at, w);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const float2 x = *reinterpret_cast<const float2 *>(f->sa + 8 * t + 2 * q4);
+          o[t][0] = fmaf(x.x * s0, w[t][0], o[t][0]);
+          o[t][1] = fmaf(x.y * s0, w[t][1], o[t][1]);
+          o[t][2] = fmaf(x.x * s1, w[t][2], o[t][2]);
+          o[t][3] = fmaf(x.y * s1, w[t][3], o[t][3]);
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int j = c * C + 8 * t + 2 * q4 + (e & 1);
+            if (j < n) op[static_cast<long long>(t00 + j) * a.d.out_stride + 8 * (e >> 1)] = o[t][e];
+          }
+      }
+    }
+    if (!odd) {
+      if (c + 1 < chunks) load_v(c + 1, v);
+      // S^T <- e^{G_C} S^T + (U^T diag(e^{G_C - G})) K
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const float2 x = *reinterpret_cast<const float2 *>(f->wk + 8 * t + 2 * q4);
+        u[t][0] *= x.x;
+        u[t][1] *= x.y;
+        u[t][2] *= x.x;
+        u[t][3] *= x.y;
+      }
+      float s0, i0, s1, i1;
+      scales(u, s0, i0, s1, i1);
+      uint32_t ah[2][4], al[2][4];
+      split(u, i0, i1, ah, al);
+      const float dec = f->dec;
+#pragma unroll
+      for (int c4 = 0; c4 < DK / 8; c4 += 4) {
+        float w[4][4] = {};
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            uint32_t bh[4], bl[4];
+            const uint32_t off = kq_at<DK>(16 * ks + (lane & 15), c4 + 2 * p + (lane >> 4));
+            ldsm4_t(bh, kt + off);
+            ldsm4_t(bl, kt + KQ + off);
+            mma3(w[2 * p], ah[ks], al[ks], bh[0], bh[1], bl[0], bl[1]);
+            mma3(w[2 * p + 1], ah[ks], al[ks], bh[2], bh[3], bl[2], bl[3]);
+          }
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          s[c4 + t][0] = fmaf(s0, w[t][0], dec * s[c4 + t][0]);
+          s[c4 + t][1] = fmaf(s0, w[t][1], dec * s[c4 + t][1]);
+          s[c4 + t][2] = fmaf(s1, w[t][2], dec * s[c4 + t][2]);
+          s[c4 + t][3] = fmaf(s1, w[t][3], dec * s[c4 + t][3]);
+        }
+      }
+    } else {
+      // an infinite or NaN value among these tokens: one after another, so that none reaches an earlier one
+      const int len = min(C, n - c * C);
+      const unsigned char *tile = ring + st * kStage;
+      for (int j = 0; j < len; ++j) {
+        const float al = f->alpha[j], be = f->beta[j], sk = f->sk[j], sq = f->sq[j];
+        auto both = [&](int ct, float2 &k, float2 &q) {
+          const uint32_t off = kq_at<DK>(j, ct) + 4 * q4;
+          const uint32_t kh = *reinterpret_cast<const uint32_t *>(tile + off);
+          const uint32_t kl = *reinterpret_cast<const uint32_t *>(tile + KQ + off);
+          const uint32_t qh = *reinterpret_cast<const uint32_t *>(tile + 2 * KQ + off);
+          const uint32_t ql = *reinterpret_cast<const uint32_t *>(tile + 3 * KQ + off);
+          k = make_float2(sk * (lo16<false>(kh) + lo16<false>(kl)), sk * (hi16<false>(kh) + hi16<false>(kl)));
+          q = make_float2(sq * (lo16<false>(qh) + lo16<false>(ql)), sq * (hi16<false>(qh) + hi16<false>(ql)));
+        };
+        float x0 = 0.f, x1 = 0.f, y0 = 0.f, y1 = 0.f, z = 0.f;
+#pragma unroll
+        for (int ct = 0; ct < DK / 8; ++ct) {
+          float2 k, q;
+          both(ct, k, q);
+          x0 = fmaf(s[ct][0], k.x, fmaf(s[ct][1], k.y, x0));
+          x1 = fmaf(s[ct][2], k.x, fmaf(s[ct][3], k.y, x1));
+          y0 = fmaf(s[ct][0], q.x, fmaf(s[ct][1], q.y, y0));
+          y1 = fmaf(s[ct][2], q.x, fmaf(s[ct][3], q.y, y1));
+          z = fmaf(k.x, q.x, fmaf(k.y, q.y, z));
+        }
+#pragma unroll
+        for (int m = 1; m <= 2; m <<= 1) {
+          x0 += __shfl_xor_sync(0xFFFFFFFFu, x0, m);
+          x1 += __shfl_xor_sync(0xFFFFFFFFu, x1, m);
+          y0 += __shfl_xor_sync(0xFFFFFFFFu, y0, m);
+          y1 += __shfl_xor_sync(0xFFFFFFFFu, y1, m);
+          z += __shfl_xor_sync(0xFFFFFFFFu, z, m);
+        }
+        const long long row = t00 + c * C + j;
+        const float u0 = be * (__ldg(vp + row * a.d.v_stride) - al * x0);
+        const float u1 = be * (__ldg(vp + row * a.d.v_stride + 8) - al * x1);
+        if (q4 == 0) {
+          op[row * a.d.out_stride] = fmaf(z, u0, al * y0);
+          op[row * a.d.out_stride + 8] = fmaf(z, u1, al * y1);
+        }
+#pragma unroll
+        for (int ct = 0; ct < DK / 8; ++ct) {
+          float2 k, q;
+          both(ct, k, q);
+          s[ct][0] = fmaf(k.x, u0, al * s[ct][0]);
+          s[ct][1] = fmaf(k.y, u0, al * s[ct][1]);
+          s[ct][2] = fmaf(k.x, u1, al * s[ct][2]);
+          s[ct][3] = fmaf(k.y, u1, al * s[ct][3]);
+        }
+      }
+      if (c + 1 < chunks) load_v(c + 1, v);
+    }
+    __syncwarp();
+    if (lane == 0) {
+      __threadfence_block();
+      if (atomicAdd(&left[st], 1) == W - 1) {
+        left[st] = 0;
+        __threadfence_block();
+        if (c + NST < chunks) ask(c + NST);
+      }
+    }
+  }
+
+  if (a.d.state_out) {
+    const int to = __ldg(a.d.state_out + b);
+    if (to >= 0 && to < a.d.n_slots) {
+      float *p = a.d.states + to * a.d.slot_stride + static_cast<long long>(h) * DK * a.d.Dv + (d0 - h * a.d.Dv);
+#pragma unroll
+      for (int ct = 0; ct < DK / 8; ++ct)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) p[static_cast<long long>(8 * ct + 2 * q4 + (e & 1)) * a.d.Dv + 8 * (e >> 1)] = s[ct][e];
+    } else if (to != -1 && teller) {
+      atomicOr(&g_qg_status_delta_chunk, QG_STATUS_BIT_ID);
+    }
+  }
+}
+
+template <int DK, int W, int NST>
+cudaError_t walk(const ChunkArgs &a, cudaStream_t s) {
+  constexpr int smem = WalkSmem<DK, W, NST>::kBytes;
+  if (!qg::set_smem_attr(reinterpret_cast<const void *>(delta_walk_kernel<DK, W, NST>), smem)) return cudaErrorInvalidValue;
+  const dim3 grid(static_cast<unsigned>(a.d.B) * a.d.Hv * (a.d.Dv / (16 * W)));
+  return qg::launch_pdl(delta_walk_kernel<DK, W, NST>, grid, dim3(W * 32), smem, s, a);
+}
+
+template <int DK>
+cudaError_t both(const ChunkArgs &a, cudaStream_t s) {
+  constexpr int smem = Tiles<DK>::kKQAll;
+  if (!qg::set_smem_attr(reinterpret_cast<const void *>(delta_prep_kernel<DK>), smem)) return cudaErrorInvalidValue;
+  cudaError_t e = qg::launch_pdl(delta_prep_kernel<DK>, dim3(static_cast<unsigned>(a.slots) * a.d.Hk), dim3(kPrepWarps * 32), smem, s, a);
+  if (e != cudaSuccess) return e;
+  return a.d.Dv % 128 == 0 ? walk<DK, 8, 3>(a, s) : a.d.Dv % 64 == 0 ? walk<DK, 4, 3>(a, s) : walk<DK, 2, 3>(a, s);
+}
+
+size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
+int chunk_slots(const DeltaArgs &a) { return a.T / C + a.B; }
+size_t kq_bytes(const DeltaArgs &a) { return static_cast<size_t>(chunk_slots(a)) * a.Hk * 4 * C * a.Dk * 2; }
+
+}  // namespace
+
+namespace qg {
+
+size_t delta_chunk_workspace(const DeltaArgs &a) {
+  return round256(kq_bytes(a)) + static_cast<size_t>(chunk_slots(a)) * a.Hv * kTA;
+}
+
+cudaError_t delta_chunks(const DeltaArgs &d, int first_len, void *ws, cudaStream_t s) {
+  unsigned char *p = static_cast<unsigned char *>(ws);
+  const ChunkArgs a{d, p, p + round256(kq_bytes(d)), first_len, chunk_slots(d)};
+  g_launched = true;
+  return d.Dk == 64 ? both<64>(a, s) : both<128>(a, s);
+}
+
+unsigned int read_status_delta_chunk(bool clear) {
+  unsigned int v = 0;
+  if (!g_launched) return v;
+  if (cudaMemcpyFromSymbol(&v, g_qg_status_delta_chunk, sizeof(v)) != cudaSuccess) return 0xFFFFFFFFu;
+  if (clear) {
+    const unsigned int z = 0;
+    cudaMemcpyToSymbol(g_qg_status_delta_chunk, &z, sizeof(z));
+  }
+  return v;
+}
+
+}  // namespace qg

@@ -106,5 +106,6 @@ unsigned int read_status_attn_tc(bool clear);
 unsigned int read_status_draft(bool clear);
 unsigned int read_status_pages(bool clear);
 unsigned int read_status_delta(bool clear);
+unsigned int read_status_delta_chunk(bool clear);
 
 }  // namespace qg
