@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 from . import build as _build
@@ -603,6 +604,9 @@ class DeltaArgs(ctypes.Structure):
                 ("out_stride", ctypes.c_int64)]
 
 
+_delta_pack = struct.Struct("10i2f6P5q3Pq4Pq").pack  # the same fields in one go: a structure's cost more than the call
+
+
 def _gpu(t, what):
     """The GPU of the tensor that the others of a call have to be with."""
     d = t.get_device()
@@ -611,20 +615,34 @@ def _gpu(t, what):
     return d
 
 
+def _addr(t):
+    return 0 if t is None else t.data_ptr()
+
+
+_i32_type = None
+
+
 def _ints(t, n, what):
     """A contiguous int32 tensor of n elements (None passes)."""
-    _check(t, "int32", what)
-    if t is not None and t.numel() != n:
-        raise ValueError(f"{what} must have {n} elements")
+    global _i32_type
+    if t is None:
+        return
+    if _i32_type is None:
+        import torch
+
+        _i32_type = torch.int32
+    if t.dtype is not _i32_type or not t.is_contiguous() or t.numel() != n:
+        raise ValueError(f"{what} must be contiguous int32 with {n} elements")
 
 
 def _seqs(q_start, T):
     if q_start is None:
         return T
-    _check(q_start, "int32", "q_start")
-    if q_start.dim() != 1 or q_start.numel() < 1:
+    n = q_start.numel()
+    _ints(q_start, n, "q_start")
+    if n < 1:
         raise ValueError("q_start must have n_seqs + 1 elements")
-    return q_start.numel() - 1
+    return n - 1
 
 
 def delta_workspace_size(T, n_seqs, Hk, Hv, Dk, Dv, max_new=0) -> int:
@@ -640,36 +658,35 @@ def delta_rule(q, k, v, a, b, states, state_in, state_out, out, workspace=None, 
     of wider ones); states f32 [slots][Hv][Dk][Dv], state_in and state_out int32 [n_seqs] or None, state_each int32 [T]
     or None; out f32 [T][Hv][Dv]; q_start int32 [n_seqs + 1] (None: one token per sequence).  a_scale and a_bias:
     f32 [Hv], a and b are then raw; l2norm_eps: q and k are normalised; tiled: value head h takes key head h % Hk."""
-    if q.dim() != 3 or v.dim() != 3 or q.shape != k.shape or v.shape[0] != q.shape[0]:
+    shape, vshape = q.shape, v.shape
+    if len(shape) != 3 or len(vshape) != 3 or shape != k.shape or vshape[0] != shape[0]:
         raise ValueError("q and k must be [T][Hk][Dk] and v [T][Hv][Dv]")
-    (T, Hk, Dk), (Hv, Dv) = q.shape, v.shape[1:]
+    (T, Hk, Dk), (_, Hv, Dv) = shape, vshape
     f32 = _types()[0]
-    for t, what in ((q, "q"), (k, "k"), (v, "v"), (a, "a"), (b, "b"), (out, "out"), (states, "states")):
-        if t is not None and t.dtype is not f32:
-            raise ValueError(f"{what} must be f32")
+    if not (q.dtype is k.dtype is v.dtype is a.dtype is b.dtype is out.dtype is f32):
+        raise ValueError("q, k, v, a, b and out must be f32")
     n = _seqs(q_start, T)
     _ints(state_in, n, "state_in")
     _ints(state_out, n, "state_out")
     _ints(state_each, T, "state_each")
     for t, what in ((a_scale, "a_scale"), (a_bias, "a_bias")):
-        _check(t, "float32", what)
-        if t is not None and t.numel() != Hv:
-            raise ValueError(f"{what} must have an element per value head")
+        if t is not None and (t.dtype is not f32 or t.numel() != Hv or not t.is_contiguous()):
+            raise ValueError(f"{what} must be contiguous f32 with an element per value head")
     slots, slot = 0, 0
     if states is not None:
-        if states.dim() != 4 or tuple(states.shape[1:]) != (Hv, Dk, Dv) or (
-                states.shape[0] and not states[0].is_contiguous()):
-            raise ValueError("states must be [slots][Hv][Dk][Dv], contiguous in each slot")
-        slots, slot = states.shape[0], states.stride(0) if states.shape[0] > 1 else Hv * Dk * Dv
-    strides = [_rows(t, T, w, what) for t, w, what in ((q, Hk * Dk, "q"), (k, Hk * Dk, "k"), (v, Hv * Dv, "v"), (a, Hv, "a"),
-                                                       (b, Hv, "b"), (out, Hv * Dv, "out"))]
+        sshape, st = states.shape, states.stride()
+        if len(sshape) != 4 or sshape[1:] != (Hv, Dk, Dv) or states.dtype is not f32 or st[3] != 1 or st[2] != Dv or (
+                Hv > 1 and st[1] != Dk * Dv):
+            raise ValueError("states must be f32 [slots][Hv][Dk][Dv], contiguous in each slot")
+        slots, slot = sshape[0], st[0] if sshape[0] > 1 else Hv * Dk * Dv
     _on(_gpu(q, "q"), "k v a b states state_in state_out state_each out q_start a_scale a_bias workspace", k, v, a, b, states,
         state_in, state_out, state_each, out, q_start, a_scale, a_bias, workspace)
-    g = DeltaArgs(n, T, int(max_new), Hk, Hv, Dk, Dv, int(bool(tiled)), int(l2norm_eps is not None), slots,
-                  float(l2norm_eps or 0.0), float(scale), _ptr(q_start), _ptr(q), _ptr(k), _ptr(v), _ptr(a), _ptr(b),
-                  *strides[:5], _ptr(a_scale), _ptr(a_bias), _ptr(states), slot, _ptr(state_in), _ptr(state_out),
-                  _ptr(state_each), _ptr(out), strides[5])
-    _call("qg_delta_rule", ctypes.byref(g), _ptr(workspace), _nbytes(workspace), _stream(stream))
+    p = _addr
+    g = _delta_pack(n, T, int(max_new), Hk, Hv, Dk, Dv, 1 if tiled else 0, 0 if l2norm_eps is None else 1, slots,
+                    float(l2norm_eps or 0.0), float(scale), p(q_start), p(q), p(k), p(v), p(a), p(b), _rows(q, T, Hk * Dk, "q"),
+                    _rows(k, T, Hk * Dk, "k"), _rows(v, T, Hv * Dv, "v"), _rows(a, T, Hv, "a"), _rows(b, T, Hv, "b"), p(a_scale),
+                    p(a_bias), p(states), slot, p(state_in), p(state_out), p(state_each), p(out), _rows(out, T, Hv * Dv, "out"))
+    _call("qg_delta_rule", g, _ptr(workspace), _nbytes(workspace), _stream(stream))
     return out
 
 
@@ -692,13 +709,15 @@ def draft_verify(probs, tokens, u, u_next, accepted, next_token, draft_probs=Non
     q_start int32 [n_seqs + 1] (None: one row each, a sampler); kv_len, kept_len int32 [n_seqs]."""
     T, V = probs.shape
     n = _seqs(q_start, T)
-    for t, size, dtype, what in ((probs, T * V, "float32", "probs"), (draft_probs, T * V, "float32", "draft_probs"),
-                                 (tokens, T, "int32", "tokens"), (u, T, "float32", "u"), (u_next, n, "float32", "u_next"),
-                                 (accepted, n, "int32", "accepted"), (next_token, n, "int32", "next_token"),
-                                 (kv_len, n, "int32", "kv_len"), (kept_len, n, "int32", "kept_len")):
-        _check(t, dtype, what)
-        if t is not None and t.numel() != size:
-            raise ValueError(f"{what} must have {size} elements")
+    f32 = _types()[0]
+    for t, size, what in ((probs, T * V, "probs"), (draft_probs, T * V, "draft_probs"), (u, T, "u"), (u_next, n, "u_next")):
+        if t is not None and (t.dtype is not f32 or t.numel() != size or not t.is_contiguous()):
+            raise ValueError(f"{what} must be contiguous f32 with {size} elements")
+    _ints(tokens, T, "tokens")
+    _ints(accepted, n, "accepted")
+    _ints(next_token, n, "next_token")
+    _ints(kv_len, n, "kv_len")
+    _ints(kept_len, n, "kept_len")
     _on(_gpu(probs, "probs"), "tokens u u_next accepted next_token draft_probs q_start kv_len kept_len", tokens, u, u_next,
         accepted, next_token, draft_probs, q_start, kv_len, kept_len)
     _call("qg_draft_verify", _ptr(probs), _ptr(draft_probs), _ptr(tokens), _ptr(u), _ptr(u_next), _ptr(q_start), n, T, V,
@@ -707,15 +726,13 @@ def draft_verify(probs, tokens, u, u_next, accepted, next_token, draft_probs=Non
 
 
 def _page_call(caches, batch, refs):
-    if refs.numel() != caches[0].n_pages:
-        raise ValueError("refs must have an element per page")
+    _ints(refs, caches[0].n_pages, "refs")
     return _cache_device(caches, batch)
 
 
 def kv_fork(caches, batch, refs, src=None, keep=None, stream=None):
     """Sequence b becomes the first keep[b] tokens of sequence src[b], in place: shared, truncated or freed (qg_kv_fork).
     caches: kv_caches of all layers; refs: int32 [n_pages], the holders of each page."""
-    _check(refs, "int32", "refs")
     _ints(src, batch.n_seqs, "src")
     _ints(keep, batch.n_seqs, "keep")
     _on(_page_call(caches, batch, refs), "refs src keep", refs, src, keep)
@@ -729,7 +746,6 @@ def reserve_workspace_size(caches, batch) -> int:
 def kv_reserve(caches, batch, refs, add, missing, workspace, stream=None):
     """Room for add[b] new tokens of each sequence (qg_kv_reserve).  caches: kv_caches of all layers; missing: int32 [1],
     how many pages were too few (then nothing has changed)."""
-    _check(refs, "int32", "refs")
     _ints(add, batch.n_seqs, "add")
     _ints(missing, 1, "missing")
     _on(_page_call(caches, batch, refs), "refs add missing workspace", refs, add, missing, workspace)
@@ -741,7 +757,7 @@ def kv_compact(caches, batch, src, keep_start, keep, stream=None):
     """Slot i of sequence b receives the token in slot keep[keep_start[b] + i] of sequence src[b] (qg_kv_compact)."""
     _ints(src, batch.n_seqs, "src")
     _ints(keep_start, batch.n_seqs + 1, "keep_start")
-    _check(keep, "int32", "keep")
+    _ints(keep, keep.numel(), "keep")
     _on(_cache_device(caches, batch), "src keep_start keep", src, keep_start, keep)
     _call("qg_kv_compact", caches, len(caches), ctypes.byref(batch), _ptr(src), _ptr(keep_start), _ptr(keep), keep.numel(),
           _stream(stream))

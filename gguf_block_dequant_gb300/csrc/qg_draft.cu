@@ -5,6 +5,7 @@
 
 #include "qg_common.cuh"
 #include "qg_host.h"
+#include "qg_mma.cuh"
 
 __device__ unsigned int g_qg_status_draft;   // this translation unit's device status word
 static std::atomic<bool> g_launched{false};  // whether a kernel that may set it has been launched
@@ -23,11 +24,6 @@ QG_DEVICE uint32_t remote_addr(const void *p, uint32_t rank) {
 QG_DEVICE float remote_f32(const float *p, uint32_t rank) {
   float v;
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(remote_addr(p, rank)) : "memory");
-  return v;
-}
-QG_DEVICE double remote_f64(const double *p, uint32_t rank) {
-  double v;
-  asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(remote_addr(p, rank)) : "memory");
   return v;
 }
 QG_DEVICE int remote_s32(const int *p, uint32_t rank) {
@@ -55,12 +51,14 @@ cudaError_t launch_cluster(void (*kern)(KArgs...), unsigned blocks, unsigned thr
 }
 
 // ---- probabilities ------------------------------------------------------------------------------
-// A row is split over a cluster of CTAs; each keeps its slice in shared memory, so a logit is read once
-// and a probability written once (8 bytes an element: HBM bounds it).  Slices are laid out as in global
-// memory modulo 16 bytes, so that rows of odd lengths still move 16 bytes at a time.  Each CTA sums
-// exp((x - its own maximum) / t); one exchange of (maximum, sum) gives every CTA its factor.  What does
-// not fit (vocabularies over 8 x kKeep) is read again.
+// A row is split over a cluster of CTAs; each keeps its slice in registers, so a logit is read once and a
+// probability written once (8 bytes an element: HBM bounds it).  Slices start at 16-byte boundaries of the
+// whole tensor, so that rows of odd lengths still move 16 bytes at a time; only a row's two ends are moved by
+// elements.  Each CTA sums the exponentials against its own maximum; one exchange of (maximum, sum) gives every
+// CTA its factor.  Exponentials are powers of two of (x/2 - m/2) (2 log2(e) / t): the half difference stays finite, six
+// instructions an element.
 constexpr int kProbThreads = 512;
+constexpr int kProbWarps = kProbThreads / 32;
 constexpr int kKeep = 48 * 1024;  // floats of a slice that stay in shared memory
 
 struct ProbArgs {
@@ -73,6 +71,141 @@ QG_DEVICE void cp_async4(uint32_t dst, const void *src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 
+// the best of the CTA's (value, index) pairs, the lowest index among equals
+QG_DEVICE void best_of(float &m, int &at, float *red, int *redi) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    const float y = __shfl_xor_sync(0xFFFFFFFFu, m, o);
+    const int j = __shfl_xor_sync(0xFFFFFFFFu, at, o);
+    if (y > m || (y == m && j < at)) m = y, at = j;
+  }
+  if (lane == 0) red[warp] = m, redi[warp] = at;
+  __syncthreads();
+  m = red[lane & (kProbWarps - 1)];
+  at = redi[lane & (kProbWarps - 1)];
+#pragma unroll
+  for (int o = kProbWarps / 2; o; o >>= 1) {
+    const float y = __shfl_xor_sync(0xFFFFFFFFu, m, o);
+    const int j = __shfl_xor_sync(0xFFFFFFFFu, at, o);
+    if (y > m || (y == m && j < at)) m = y, at = j;
+  }
+}
+
+template <int NV>
+__global__ void __launch_bounds__(kProbThreads) probs_kernel(const ProbArgs a) {
+  __shared__ float red[kProbWarps], reds[kProbWarps];
+  __shared__ int redi[kProbWarps];
+  __shared__ float cta_m, cta_s;
+  __shared__ int cta_i;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int row = static_cast<int>(blockIdx.x) / a.cs, rank = static_cast<int>(blockIdx.x) % a.cs;
+  pdl_wait();
+  pdl_launch_dependents();
+  const long long r0 = static_cast<long long>(row) * a.V, r1 = r0 + a.V;  // elements of the tensor
+  const long long g0 = (r0 & ~3LL) + static_cast<long long>(rank) * a.slice;
+  const int count = static_cast<int>(min(static_cast<long long>(a.slice), r1 - g0));  // may be negative: an empty slice
+  float4 x[NV];
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int i = 4 * (tid + k * kProbThreads);
+    const long long g = g0 + i;
+    x[k] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+    if (i < count) {
+      if (g >= r0 && g + 4 <= r1) {
+        x[k] = *reinterpret_cast<const float4 *>(a.logits + g);
+      } else {
+        if (g >= r0) x[k].x = a.logits[g];
+        if (g + 1 >= r0 && g + 1 < r1) x[k].y = a.logits[g + 1];
+        if (g + 2 >= r0 && g + 2 < r1) x[k].z = a.logits[g + 2];
+        if (g + 3 >= r0 && g + 3 < r1) x[k].w = a.logits[g + 3];
+      }
+    }
+  }
+  const float tau = a.temperature ? __ldg(a.temperature + row) : 1.f;
+  const bool greedy = !(tau > 0.f);
+  // fmaxf leaves NaN out
+  float m = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < NV; ++k) m = fmaxf(m, fmaxf(fmaxf(x[k].x, x[k].y), fmaxf(x[k].z, x[k].w)));
+  int at = 0x7FFFFFFF;
+  if (greedy) {  // the lowest index of this thread's largest
+#pragma unroll
+    for (int k = NV - 1; k >= 0; --k) {
+      const int i = 4 * (tid + k * kProbThreads) + static_cast<int>(g0 - r0);
+      if (x[k].w == m) at = i + 3;
+      if (x[k].z == m) at = i + 2;
+      if (x[k].y == m) at = i + 1;
+      if (x[k].x == m) at = i;
+    }
+  }
+  best_of(m, at, red, redi);
+  const bool finite = m > -INFINITY && m < INFINITY;
+  // 2 log2(e) / t within f32: a difference of 0 stays 0 and an infinite one infinite
+  const float c = fminf(fmaxf(2.8853900817779268f / tau, 1e-44f), 3e38f), hm = -0.5f * m;
+  float s = 0.f;
+  if (!greedy && finite) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      auto power = [&](float y) { return ex2(fmaxf(fmaf(0.5f, y, hm) * c, -200.f)); };  // NaN counts as -inf
+      x[k] = make_float4(power(x[k].x), power(x[k].y), power(x[k].z), power(x[k].w));
+      s += (x[k].x + x[k].y) + (x[k].z + x[k].w);
+    }
+  }
+  s = warp_sum(s);
+  if (lane == 0) reds[warp] = s;
+  __syncthreads();
+  s = reds[lane & (kProbWarps - 1)];
+#pragma unroll
+  for (int o = kProbWarps / 2; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+  float M = m, S = s;
+  int best = at;
+  if (a.cs > 1) {
+    if (tid == 0) cta_m = m, cta_s = s, cta_i = at;
+    cluster_sync();
+    // a lane per CTA
+    const uint32_t r = lane & (a.cs - 1);
+    const float om = remote_f32(&cta_m, r), os = remote_f32(&cta_s, r);
+    const int oi = remote_s32(&cta_i, r);
+    M = om;
+    best = oi;
+    for (int o = a.cs / 2; o; o >>= 1) {
+      const float y = __shfl_xor_sync(0xFFFFFFFFu, M, o);
+      const int j = __shfl_xor_sync(0xFFFFFFFFu, best, o);
+      if (y > M || (y == M && j < best)) M = y, best = j;
+    }
+    S = om > -INFINITY && M < INFINITY ? os * ex2(fmaxf((0.5f * om - 0.5f * M) * c, -200.f)) : 0.f;
+    for (int o = a.cs / 2; o; o >>= 1) S += __shfl_xor_sync(0xFFFFFFFFu, S, o);
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // this CTA has read the others
+  }
+  const bool none = !(M > -INFINITY && M < INFINITY);
+  const float f = none || greedy || !finite ? 0.f : ex2(fmaxf((0.5f * m - 0.5f * M) * c, -200.f)) / S;
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int i = 4 * (tid + k * kProbThreads);
+    const long long g = g0 + i;
+    if (i < count) {
+      float4 y;
+      if (f == 0.f) {
+        const int v = greedy && !none ? best - static_cast<int>(g - r0) : -1;
+        y = make_float4(v == 0 ? 1.f : 0.f, v == 1 ? 1.f : 0.f, v == 2 ? 1.f : 0.f, v == 3 ? 1.f : 0.f);
+      } else {
+        y = make_float4(x[k].x * f, x[k].y * f, x[k].z * f, x[k].w * f);
+      }
+      if (g >= r0 && g + 4 <= r1) {
+        *reinterpret_cast<float4 *>(a.probs + g) = y;
+      } else {
+        if (g >= r0) a.probs[g] = y.x;
+        if (g + 1 >= r0 && g + 1 < r1) a.probs[g + 1] = y.y;
+        if (g + 2 >= r0 && g + 2 < r1) a.probs[g + 2] = y.z;
+        if (g + 3 >= r0 && g + 3 < r1) a.probs[g + 3] = y.w;
+      }
+    }
+  }
+  if (a.cs > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // nobody leaves while it is read
+}
+
+// Vocabularies that eight CTAs' registers do not hold: slices in shared memory, what does not fit is read again.
 __global__ void __launch_bounds__(kProbThreads) token_probs_kernel(const ProbArgs a) {
   extern __shared__ float4 keep4[];
   float *const keep = reinterpret_cast<float *>(keep4);
@@ -203,9 +336,10 @@ __global__ void __launch_bounds__(kProbThreads) token_probs_kernel(const ProbArg
 // ---- verification -------------------------------------------------------------------------------
 // A cluster per sequence.  Every CTA finds the first draft that is not accepted (a gather per draft), then the
 // row of residuals is summed in slices: one read of that row of probs and of draft_probs, which bounds it.
-// The draw must not depend on how the sum is split: each thread sums in two f32 terms (the error of
-// every addition is kept, about 2^-46 of the sum), and threads, warps and CTAs are joined in f64.  The CTA
-// and then the warp whose range holds the threshold are found from their sums; that warp walks its range.
+// The draw must not depend on how the sum is split, so sums are kept in two f32 terms (the error of every addition
+// is kept: 2^-40 of the sum at the least; f64 additions would cost more than the reads here, at two a clock and SM).
+// The CTA and then the warp whose range holds the threshold are found from their sums, by one warp of each CTA
+// with the same additions, and the threads of that CTA search that warp's range.
 constexpr int kVerThreads = 512;
 constexpr int kVerWarps = kVerThreads / 32;
 
@@ -244,17 +378,52 @@ struct Residual {
   }
 };
 
-// (s, e) += x with the rounding error of the addition kept in e
-QG_DEVICE void add_kept(float &s, float &e, float x) {
-  const float t = __fadd_rn(s, x);
-  const float b = __fadd_rn(t, -s);
-  e = __fadd_rn(e, __fadd_rn(__fadd_rn(s, -__fadd_rn(t, -b)), __fadd_rn(x, -b)));
-  s = t;
+// a sum and the rounding errors of its additions; s + e with |e| at most half a step of s
+struct Sum {
+  float s, e;
+};
+QG_DEVICE void add_kept(Sum &a, float x) {  // not brought to normal form: for many additions in a row
+  const float t = __fadd_rn(a.s, x);
+  const float b = __fadd_rn(t, -a.s);
+  a.e = __fadd_rn(a.e, __fadd_rn(__fadd_rn(a.s, -__fadd_rn(t, -b)), __fadd_rn(x, -b)));
+  a.s = t;
+}
+QG_DEVICE Sum normal(float s, float e) {
+  const float t = __fadd_rn(s, e);
+  return {t, __fadd_rn(e, -__fadd_rn(t, -s))};
+}
+QG_DEVICE Sum operator+(Sum a, Sum b) {
+  const float e = __fadd_rn(a.e, b.e);
+  a.e = 0.f;
+  add_kept(a, b.s);
+  return normal(a.s, __fadd_rn(a.e, e));
+}
+QG_DEVICE bool operator<(Sum a, Sum b) { return a.s < b.s || (a.s == b.s && a.e < b.e); }
+QG_DEVICE Sum times(Sum a, float u) {
+  const float p = __fmul_rn(a.s, u);
+  return normal(p, __fmaf_rn(a.e, u, __fmaf_rn(a.s, u, -p)));
+}
+QG_DEVICE Sum shfl_up(Sum a, int o) {
+  return {__shfl_up_sync(0xFFFFFFFFu, a.s, o), __shfl_up_sync(0xFFFFFFFFu, a.e, o)};
+}
+QG_DEVICE Sum shfl_xor(Sum a, int o) {
+  return {__shfl_xor_sync(0xFFFFFFFFu, a.s, o), __shfl_xor_sync(0xFFFFFFFFu, a.e, o)};
+}
+QG_DEVICE Sum shfl(Sum a, int i) { return {__shfl_sync(0xFFFFFFFFu, a.s, i), __shfl_sync(0xFFFFFFFFu, a.e, i)}; }
+// running sums over the lanes
+QG_DEVICE Sum scan(Sum a) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const Sum y = shfl_up(a, o);
+    if (lane >= o) a = y + a;
+  }
+  return a;
 }
 
 __global__ void __launch_bounds__(kVerThreads) draft_verify_kernel(const VerifyArgs a) {
-  __shared__ double wsum[kVerWarps], cta_sum;
-  __shared__ int wlast[kVerWarps], cta_last, stop, found, tail;
+  __shared__ Sum wsum[kVerWarps], cta_sum, s_rest;
+  __shared__ int wlast[kVerWarps], cta_last, stop, found, tail, s_pick;  // s_pick: the warp whose range is searched
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = static_cast<int>(blockIdx.x) / a.cs, rank = static_cast<int>(blockIdx.x) % a.cs;
   pdl_wait();
@@ -269,23 +438,27 @@ __global__ void __launch_bounds__(kVerThreads) draft_verify_kernel(const VerifyA
     }
     return;
   }
-  if (tid == 0) stop = t1 - 1;
-  __syncthreads();
-  for (int t = t0 + tid; t < t1 - 1; t += kVerThreads) {
-    const int x = __ldg(a.tokens + t + 1);
-    bool ok = false;
-    if (x < 0 || x >= a.V) {
-      if (rank == 0) atomicOr(&g_qg_status_draft, QG_STATUS_BIT_ID);
-    } else {
-      const size_t at = static_cast<size_t>(t) * a.V + x;
-      const float un = fmaxf(__ldg(a.u + t), 0.f);
-      const float q = a.draft ? as_prob(__ldg(a.draft + at)) : 1.f;
-      ok = static_cast<double>(un) * q < static_cast<double>(as_prob(__ldg(a.probs + at)));  // exact products
+  const float u = fmaxf(__ldg(a.u_next + b), 0.f);
+  int t = t1 - 1;
+  if (t > t0) {
+    if (tid == 0) stop = t;
+    __syncthreads();
+    for (int i = t0 + tid; i < t1 - 1; i += kVerThreads) {
+      const int x = __ldg(a.tokens + i + 1);
+      bool ok = false;
+      if (x < 0 || x >= a.V) {
+        if (rank == 0) atomicOr(&g_qg_status_draft, QG_STATUS_BIT_ID);
+      } else {
+        const size_t at = static_cast<size_t>(i) * a.V + x;
+        const float un = fmaxf(__ldg(a.u + i), 0.f);
+        const float q = a.draft ? as_prob(__ldg(a.draft + at)) : 1.f;
+        ok = static_cast<double>(un) * q < static_cast<double>(as_prob(__ldg(a.probs + at)));  // exact products
+      }
+      if (!ok) atomicMin(&stop, i);
     }
-    if (!ok) atomicMin(&stop, t);
+    __syncthreads();
+    t = stop;
   }
-  __syncthreads();
-  const int t = stop;
   const bool refused = t < t1 - 1;
   const size_t row = static_cast<size_t>(t) * a.V;
   Residual r{a.probs + row, nullptr, -1};
@@ -293,25 +466,24 @@ __global__ void __launch_bounds__(kVerThreads) draft_verify_kernel(const VerifyA
     if (a.draft) r.q = a.draft + row;
     else r.x = __ldg(a.tokens + t + 1);
   }
-  const double u = fmaxf(__ldg(a.u_next + b), 0.f);
 
   // element v sits at a 16-byte boundary when (row + v) % 4 == 0; slices and warps' ranges start at such places
   const int skew = static_cast<int>((4 - (row & 3)) & 3);
   auto edge = [&](int v) { return v <= 0 ? 0 : min(a.V, v + skew); };
-  const int wlo = edge(rank * a.slice + min(a.slice, warp * a.sub));
-  const int whi = edge(rank * a.slice + min(a.slice, (warp + 1) * a.sub));
+  auto range = [&](int w) { return edge(rank * a.slice + min(a.slice, w * a.sub)); };
+  const int wlo = range(warp), whi = range(warp + 1);
   for (int pass = 0; pass < 2; ++pass) {
     // this warp's sum and its last element with mass
-    float s = 0.f, e = 0.f;
+    Sum s{0.f, 0.f};
     int last = -1;
     auto take = [&](float x, int v) {
-      add_kept(s, e, x);
+      add_kept(s, x);
       if (x > 0.f) last = v;
     };
     const int head = min(whi - wlo, wlo == 0 ? skew : 0);
     const int body = (whi - wlo - head) >> 2, from = wlo + head;
     if (lane < head) take(r.at(wlo + lane), wlo + lane);
-#pragma unroll 4
+#pragma unroll 5
     for (int i = lane; i < body; i += 32) {
       const float4 x = r.at4(from + 4 * i);
       take(x.x, from + 4 * i);
@@ -320,106 +492,94 @@ __global__ void __launch_bounds__(kVerThreads) draft_verify_kernel(const VerifyA
       take(x.w, from + 4 * i + 3);
     }
     for (int v = from + 4 * body + lane; v < whi; v += 32) take(r.at(v), v);
-    double d = static_cast<double>(s) + e;
+    s = normal(s.s, s.e);
 #pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      d += __shfl_xor_sync(0xFFFFFFFFu, d, o);
-      last = max(last, __shfl_xor_sync(0xFFFFFFFFu, last, o));
-    }
+    for (int o = 16; o; o >>= 1) s = s + shfl_xor(s, o);
+    last = __reduce_max_sync(0xFFFFFFFFu, last);
     if (lane == 0) {
-      wsum[warp] = d;
+      wsum[warp] = s;
       wlast[warp] = last;
     }
     __syncthreads();
-    double own = 0.0;  // the same additions in every thread
-    int own_last = -1;
-    for (int w = 0; w < kVerWarps; ++w) {
-      own += wsum[w];
-      own_last = max(own_last, wlast[w]);
-    }
-    double total = own;
-    int all_last = own_last;
+    // running sums of the CTA's warps, in every warp alike
+    Sum run = scan(lane < kVerWarps ? wsum[lane] : Sum{0.f, 0.f});
+    const Sum own = shfl(run, kVerWarps - 1);
+    const int own_last = __reduce_max_sync(0xFFFFFFFFu, lane < kVerWarps ? wlast[lane] : -1);
+    Sum total = own, before{0.f, 0.f};
+    int all_last = own_last, pick = 0;
+    Sum want = times(total, u);
     if (a.cs > 1) {
       if (tid == 0) {
         cta_sum = own;
         cta_last = own_last;
       }
       cluster_sync();
-      total = 0.0;
-      for (int k = 0; k < a.cs; ++k) {
-        total += remote_f64(&cta_sum, k);
-        all_last = max(all_last, remote_s32(&cta_last, k));
+      Sum x{0.f, 0.f};
+      int l = -1;
+      if (lane < a.cs) {
+        x = {remote_f32(&cta_sum.s, lane), remote_f32(&cta_sum.e, lane)};
+        l = remote_s32(&cta_last, lane);
       }
+      const Sum upto = scan(x);
+      total = shfl(upto, a.cs - 1);
+      all_last = __reduce_max_sync(0xFFFFFFFFu, l);
+      // the first CTA whose running sum passes the threshold: every CTA finds the same
+      want = times(total, u);
+      const unsigned over = __ballot_sync(0xFFFFFFFFu, lane < a.cs && want < upto);
+      pick = over ? __ffs(over) - 1 : a.cs;
+      if (pick > 0) before = shfl(upto, pick - 1);
     }
-    if (!(total > 0.0) && pass == 0 && refused) {  // nothing is left of the difference: the row itself
+    if (!(total.s > 0.f) && pass == 0 && refused) {  // nothing is left of the difference: the row itself
       r.q = nullptr;
       r.x = -1;
       if (a.cs > 1) cluster_sync();  // the sums are written again
       __syncthreads();
       continue;
     }
-    const double want = u * total;
     if (!(want < total)) {  // no mass at all; a random number of 1 or more, or rounding: the last one with mass
-      if (rank == 0 && tid == 0) a.next_token[b] = total > 0.0 ? all_last : -1;
-    } else {
-      // the CTA whose range holds the threshold: every CTA makes the same additions and finds the same one
-      double run = 0.0;
-      int pick = 0;
-      if (a.cs > 1)
-        for (; pick < a.cs - 1; ++pick) {
-          const double x = remote_f64(&cta_sum, pick);
-          if (want < run + x) break;
-          run += x;
-        }
-      if (pick == rank) {
-        const double here = want - run;
-        // its warp's range, in which then every thread takes a few elements
-        int w = -1, some = 0;
-        double rest = INFINITY, at = 0.0;
-        for (int i = 0; i < kVerWarps; ++i) {
-          if (w < 0 && here < at + wsum[i]) {
-            w = i;
-            rest = here - at;
-          }
-          if (wsum[i] > 0.0) some = i;
-          at += wsum[i];
-        }
-        if (w < 0) w = some;  // rounding: the last range with mass, and in it the last element
-        const int lo = edge(rank * a.slice + min(a.slice, w * a.sub));
-        const int hi = edge(rank * a.slice + min(a.slice, (w + 1) * a.sub));
-        const int each = (hi - lo + kVerThreads - 1) / kVerThreads;
-        const int v0 = min(hi, lo + tid * each), v1 = min(hi, v0 + each);
-        double c = 0.0;
-        for (int v = v0; v < v1; ++v) c += r.at(v);
-        double incl = c;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const double y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-          if (lane >= o) incl += y;
-        }
-        __syncthreads();  // everyone has read wsum
-        if (lane == 31) wsum[warp] = incl;
-        if (tid == 0) {
+      if (rank == 0 && tid == 0) a.next_token[b] = total.s > 0.f ? all_last : -1;
+    } else if (pick == rank) {
+      if (warp == 0) {
+        // the first warp's range that passes it; by rounding none may: then the last with mass, and in it the last element
+        const Sum here = want + Sum{-before.s, -before.e};
+        const unsigned over = __ballot_sync(0xFFFFFFFFu, lane < kVerWarps && here < run);
+        const unsigned some = __ballot_sync(0xFFFFFFFFu, lane < kVerWarps && wsum[lane & (kVerWarps - 1)].s > 0.f);
+        const int w = over ? __ffs(over) - 1 : 31 - __clz(some);
+        const Sum upto = shfl(run, max(w - 1, 0));
+        if (lane == 0) {
+          s_pick = w;
+          s_rest = !over ? Sum{INFINITY, 0.f} : w > 0 ? here + Sum{-upto.s, -upto.e} : here;
           found = 0x7FFFFFFF;
           tail = -1;
         }
-        __syncthreads();
-        double sum = __shfl_up_sync(0xFFFFFFFFu, incl, 1);
-        if (lane == 0) sum = 0.0;
-        for (int i = 0; i < warp; ++i) sum += wsum[i];
-        for (int v = v0; v < v1; ++v) {
-          const float x = r.at(v);
-          if (!(x > 0.f)) continue;
-          sum += x;
-          atomicMax(&tail, v);
-          if (sum > rest) {
-            atomicMin(&found, v);
-            break;
-          }
-        }
-        __syncthreads();
-        if (tid == 0) a.next_token[b] = found != 0x7FFFFFFF ? found : tail;
       }
+      __syncthreads();
+      const int lo = range(s_pick), hi = range(s_pick + 1);
+      const Sum rest = s_rest;
+      const int each = (hi - lo + kVerThreads - 1) / kVerThreads;
+      const int v0 = min(hi, lo + tid * each), v1 = min(hi, v0 + each);
+      Sum c{0.f, 0.f};
+      for (int v = v0; v < v1; ++v) add_kept(c, r.at(v));
+      const Sum incl = scan(normal(c.s, c.e));
+      if (lane == 31) wsum[warp] = incl;  // warp 0 has read the ranges' sums
+      __syncthreads();
+      const Sum warps = scan(lane < kVerWarps ? wsum[lane] : Sum{0.f, 0.f});
+      Sum sum = shfl_up(incl, 1);
+      if (lane == 0) sum = {0.f, 0.f};
+      const Sum w0 = shfl(warps, max(warp - 1, 0));
+      if (warp > 0) sum = w0 + sum;
+      for (int v = v0; v < v1; ++v) {
+        const float x = r.at(v);
+        if (!(x > 0.f)) continue;
+        sum = sum + Sum{x, 0.f};
+        atomicMax(&tail, v);
+        if (rest < sum) {
+          atomicMin(&found, v);
+          break;
+        }
+      }
+      __syncthreads();
+      if (tid == 0) a.next_token[b] = found != 0x7FFFFFFF ? found : tail;
     }
     break;
   }
@@ -457,15 +617,27 @@ qg_status qg_token_probs(const float *logits, const float *temperature, int T, i
   if (!qg::aligned16(logits) || !qg::aligned16(probs) || (reinterpret_cast<uintptr_t>(temperature) & 3u)) return QG_EALIGN;
   const qg::DeviceInfo &dev = qg::device_info();
   if (!dev.ok) return QG_ECUDA;
-  // CTAs per row: enough to hold the row at two CTAs per SM, and to occupy the SMs when there are few rows
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  // CTAs per row: as many as hold the row in registers, and more to occupy the SMs when there are few rows
+  constexpr int kHold = 4 * kProbThreads;  // elements a CTA holds in one vector a thread
   int cs = 1;
-  while (cs < 8 && (V > int64_t(cs) * 24 * 1024 || (int64_t(T) * cs < 2 * dev.sms && V > int64_t(cs) * 4096))) cs *= 2;
+  while (cs < 8 && (V + 3 > int64_t(cs) * 10 * kHold || (int64_t(T) * cs < 2 * dev.sms && V > int64_t(cs) * kHold))) cs *= 2;
   ProbArgs a{logits, temperature, probs, T, static_cast<int>(V), cs, 0};
-  a.slice = static_cast<int>((V + cs - 1) / cs + 3) & ~3;
-  const size_t smem = (static_cast<size_t>(std::min(a.slice, kKeep - 4)) + 4) * sizeof(float);
-  if (!qg::set_smem_attr(reinterpret_cast<const void *>(token_probs_kernel), static_cast<uint32_t>(smem))) return QG_ECUDA;
-  const cudaError_t e = launch_cluster(token_probs_kernel, static_cast<unsigned>(T) * cs, kProbThreads, smem, cs,
-                                       reinterpret_cast<cudaStream_t>(stream), a);
+  // slices of whole vectors, from the boundary at or below a row's start
+  a.slice = static_cast<int>((V + 3 + 4 * cs - 1) / (4 * cs)) * 4;
+  const int nv = (a.slice + kHold - 1) / kHold;
+  const unsigned blocks = static_cast<unsigned>(T) * cs;
+  cudaError_t e;
+  if (nv <= 2) e = launch_cluster(probs_kernel<2>, blocks, kProbThreads, 0, cs, st, a);
+  else if (nv <= 5) e = launch_cluster(probs_kernel<5>, blocks, kProbThreads, 0, cs, st, a);
+  else if (nv <= 10) e = launch_cluster(probs_kernel<10>, blocks, kProbThreads, 0, cs, st, a);
+  else if (nv <= 17) e = launch_cluster(probs_kernel<17>, blocks, kProbThreads, 0, cs, st, a);
+  else {
+    a.slice = static_cast<int>((V + cs - 1) / cs + 3) & ~3;
+    const size_t smem = (static_cast<size_t>(std::min(a.slice, kKeep - 4)) + 4) * sizeof(float);
+    if (!qg::set_smem_attr(reinterpret_cast<const void *>(token_probs_kernel), static_cast<uint32_t>(smem))) return QG_ECUDA;
+    e = launch_cluster(token_probs_kernel, blocks, kProbThreads, smem, cs, st, a);
+  }
   if (e != cudaSuccess) return QG_ECUDA;
   return cudaGetLastError() == cudaSuccess ? QG_OK : QG_ECUDA;
 }

@@ -500,7 +500,7 @@ QG_API qg_status qg_token_probs(const float *logits, const float *temperature, i
  * At the first row where it is not, the next token is drawn from max(probs - draft_probs, 0) (in f32; for certain drafts
  * probs less 1 at x); if all are accepted, from the last row's probs; where nothing is left of the difference, from probs.
  * The draw is the lowest v with  sum of r[w], w <= v,  >  u_next[b] * (sum of all r)  and r[v] > 0, or the last v with r[v]
- * > 0 where there is none; sums and comparisons carry at least 48 bits.
+ * > 0 where there is none; sums and comparisons carry at least 40 bits.
  *   - accepted int32[n_seqs]: how many drafts; next_token int32[n_seqs]: the drawn token, -1 where the row has no mass.
  *   - kv_len, kept_len (both or neither; int32[n_seqs]): kept_len[b] = kv_len[b] - (drafts not accepted), what qg_kv_fork
  *     is to leave of a cache that holds all of the step's rows.  They may be one array.
