@@ -11,10 +11,11 @@
 // decays are not; sums of them are kept in two terms, so that decays between neighbours stay exact after strong ones.
 //
 // Products run on mma.sync in f16 with f32 sums.  Each operand is x = s (hi + lo), s a power of two per row that
-// brings the row's largest magnitude to [2^7, 2^8), hi the f16 nearest x/s and lo the one nearest the rest: 22
-// bits; hi hi + hi lo + lo hi leaves 2^-22 of each product.  (bf16 terms would leave 2^-16, tf32 ones cost twice.)
+// brings the row's largest magnitude to [2^7, 2^8), hi the multiple of 2^-3 nearest x/s (for rows of tokens the nearest
+// f16) and lo the f16 nearest the rest: 23 bits of the row's largest; hi hi + hi lo + lo hi leaves 2^-22 of it and its partner's.  (bf16 terms would leave 2^-16, tf32 ones cost twice.)
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "qg_delta.cuh"
 #include "qg_mma.cuh"
@@ -67,17 +68,60 @@ QG_DEVICE void row_scale(uint32_t m, float &s, float &inv) {
 QG_DEVICE uint32_t mag(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 constexpr uint32_t kInfBits = 0x7F800000u;
 
-// two values as packed f16 hi and lo terms
-QG_DEVICE void split2(float x, float y, uint32_t &hi, uint32_t &lo) {
-  hi = pack16<false>(x, y);
-  lo = pack16<false>(x - lo16<false>(hi), y - hi16<false>(hi));
+// x inv and y inv, below 2^8, as packed f16 terms: hi a multiple of 2^-3 (adding 3 2^19 rounds to one; 11 bits), lo the rest
+constexpr float kRound = 1572864.f;
+QG_DEVICE void split2(f2 x, f2 inv, uint32_t &hi, uint32_t &lo) {
+  const f2 h = add2(fma2(x, inv, mk2(kRound, kRound)), mk2(-kRound, -kRound));
+  const f2 l = fma2(x, inv, mk2(-h.x, -h.y));
+  hi = pack16<false>(h.x, h.y);
+  lo = pack16<false>(l.x, l.y);
+}
+QG_DEVICE void split2(float x, float y, float inv, uint32_t &hi, uint32_t &lo) { split2(mk2(x, y), mk2(inv, inv), hi, lo); }
+
+// the same with hi the f16 nearest: what is small beside the row's largest keeps its own 22 bits, so that a token's error
+// does not depend on later, larger tokens of its chunk
+QG_DEVICE void split2_each(float x, float y, float inv, uint32_t &hi, uint32_t &lo) {
+  const f2 p = mul2(mk2(x, y), mk2(inv, inv));
+  hi = pack16<false>(p.x, p.y);
+  lo = pack16<false>(p.x - lo16<false>(hi), p.y - hi16<false>(hi));
 }
 
-QG_DEVICE void mma3(float (&c)[4], const uint32_t (&ah)[4], const uint32_t (&al)[4], uint32_t bh0, uint32_t bh1,
-                    uint32_t bl0, uint32_t bl1) {
-  mma16816<false>(c, al, bh0, bh1);
-  mma16816<false>(c, ah, bl0, bl1);
-  mma16816<false>(c, ah, bh0, bh1);
+// N independent tiles c[i] += (ah + al) (bh + bl), without al bl (FIRST: from 0): the tiles take turns, so that no product waits for the
+// sum of the one before it (24 cycles; one can start every 8)
+template <bool FIRST, int N>
+QG_DEVICE void mma3(float (&c)[N][4], const uint32_t (&ah)[4], const uint32_t (&al)[4], const uint32_t (&bh)[N][2],
+                    const uint32_t (&bl)[N][2]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if constexpr (FIRST)
+      asm volatile(
+          "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, "
+          "%10};"
+          : "=f"(c[i][0]), "=f"(c[i][1]), "=f"(c[i][2]), "=f"(c[i][3])
+          : "r"(al[0]), "r"(al[1]), "r"(al[2]), "r"(al[3]), "r"(bh[i][0]), "r"(bh[i][1]), "f"(0.f));
+    else
+      mma16816<false>(c[i], al, bh[i][0], bh[i][1]);
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) mma16816<false>(c[i], ah, bl[i][0], bl[i][1]);
+#pragma unroll
+  for (int i = 0; i < N; ++i) mma16816<false>(c[i], ah, bh[i][0], bh[i][1]);
+}
+// right operands of two tiles of 8
+template <bool TRANS>
+QG_DEVICE void load2(uint32_t (&b0)[2], uint32_t (&b1)[2], uint32_t addr) {
+  uint32_t r[4];
+  if constexpr (TRANS) ldsm4_t(r, addr);
+  else ldsm4(r, addr);
+  b0[0] = r[0], b0[1] = r[1], b1[0] = r[2], b1[1] = r[3];
+}
+
+// 2^y, y <= 0.  What a state keeps from chunk to chunk multiplies up: a state that hardly decays would gather the error of
+// ex2 (2^-22) hundreds of times in one direction, so factors near 1 come from the series, rounded once.
+QG_DEVICE float chunk_decay(float y) {
+  const float x = y * 0.6931471805599453f;
+  if (x < -0.03125f) return ex2(y);
+  return fmaf(x, fmaf(x, fmaf(x, fmaf(x, 1.f / 24.f, 1.f / 6.f), 0.5f), 1.f), 1.f);
 }
 
 QG_DEVICE int chunk_base(const DeltaArgs &a, int b) { return qg::delta_tok(a, b) / C + b; }
@@ -91,17 +135,18 @@ struct ChunkArgs {
 
 // ---- what does not need the state -------------------------------------------------------------------
 // A CTA of four warps per chunk and key head.  Rows are normalised and split by a warp each; the products of keys with keys and
-// queries with keys take a warp per 16 rows; then a warp per value head solves for T, a lane per column.
+// queries with keys take a warp per 16 rows; then a warp per value head solves for T, a lane per column, and another
+// makes the decayed Q K^T.  Latency bounds it, so registers and shared memory are kept to five CTAs an SM: decays (powers of two of
+// differences of sums in log2) are made again rather than kept, and T is turned in the room of the tiles.
 constexpr int kPrepWarps = 4;
+constexpr int kTurn = C + 4;  // floats of a row there
 
 template <int DK>
-__global__ void __launch_bounds__(kPrepWarps * 32) delta_prep_kernel(const ChunkArgs a) {
+__global__ void __launch_bounds__(kPrepWarps * 32, 5) delta_prep_kernel(const ChunkArgs a) {
   extern __shared__ __align__(128) unsigned char tile[];  // K hi, K lo, Q hi, Q lo
   __shared__ float kk[C][C + 1], qk[C][C + 1];
   __shared__ float scale_k[C], scale_q[C];
-  __shared__ __align__(16) float mat[kPrepWarps][C][C + 4];
   __shared__ float2 gsum[kPrepWarps][C];
-  __shared__ float sbeta[kPrepWarps][C];
   constexpr int KQ = Tiles<DK>::kKQ;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int slot = static_cast<int>(blockIdx.x) / a.d.Hk, hk = static_cast<int>(blockIdx.x) % a.d.Hk;
@@ -119,53 +164,71 @@ __global__ void __launch_bounds__(kPrepWarps * 32) delta_prep_kernel(const Chunk
   if (n < a.first_len || first < 0 || first >= n) return;
   const int len = min(C, n - first), t0 = t00 + first;
 
-  // rows: 8 of K and 8 of Q a warp
+  // rows: 8 of K and 8 of Q a warp, all of them under way at once
   constexpr int E = DK / 32;
-  for (int r = warp; r < 2 * C; r += kPrepWarps) {
-    const bool is_q = r >= C;
-    const int i = r & (C - 1);
-    float x[E];
+  constexpr int R = C / kPrepWarps;
+  float x[2][R][E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) x[e] = 0.f;
-    if (i < len) {
-      const float *p = (is_q ? a.d.q + (t0 + i) * a.d.q_stride : a.d.k + (t0 + i) * a.d.k_stride) + hk * DK + lane * E;
-      if constexpr (E == 4) {
-        const float4 v = __ldg(reinterpret_cast<const float4 *>(p));
-        x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
-      } else {
-        const float2 v = __ldg(reinterpret_cast<const float2 *>(p));
-        x[0] = v.x, x[1] = v.y;
+  for (int z = 0; z < 2; ++z)
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int i = warp * R + r;
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[z][r][e] = 0.f;
+      if (i < len) {
+        const float *p = (z ? a.d.q + (t0 + i) * a.d.q_stride : a.d.k + (t0 + i) * a.d.k_stride) + hk * DK + lane * E;
+        if constexpr (E == 4) {
+          const float4 v = __ldg(reinterpret_cast<const float4 *>(p));
+          x[z][r][0] = v.x, x[z][r][1] = v.y, x[z][r][2] = v.z, x[z][r][3] = v.w;
+        } else {
+          const float2 v = __ldg(reinterpret_cast<const float2 *>(p));
+          x[z][r][0] = v.x, x[z][r][1] = v.y;
+        }
       }
     }
-    float f = is_q ? a.d.scale : 1.f;
-    if (a.d.l2norm) {
+  const int group = a.d.Hv / a.d.Hk;
+  // the gates of this warp's first item, needed at the end
+  auto head_of = [&](int it) {
+    const int r = it < group ? it : it - group;
+    return a.d.tiled ? hk + r * a.d.Hk : hk * group + r;
+  };
+  auto gates_of = [&](int it) {
+    return lane < len && it < 2 * group ? qg::delta_gates(a.d, t0 + lane, head_of(it)) : make_float2(0.f, 0.f);
+  };
+  float2 gates = gates_of(warp);
+#pragma unroll
+  for (int z = 0; z < 2; ++z)
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int i = warp * R + r;
       float ss = 0.f;
+      uint32_t m = 0;
 #pragma unroll
-      for (int e = 0; e < E; ++e) ss = fmaf(x[e], x[e], ss);
-      ss = warp_sum(ss) + a.d.eps;
-      if (i < len) f *= 1.f / sqrtf(ss);
-    }
-    uint32_t m = 0;
+      for (int e = 0; e < E; ++e) {
+        ss = fmaf(x[z][r][e], x[z][r][e], ss);
+        m = max(m, mag(x[z][r][e]));
+      }
+      float f = z ? a.d.scale : 1.f;
+      if (a.d.l2norm) {
+        ss = warp_sum(ss) + a.d.eps;
+        if (i < len) f *= 1.f / sqrtf(ss);
+      }
+      // the largest magnitude of the products with f: rounding keeps the order
+      m = mag(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, m)) * f);
+      float s, inv;
+      row_scale(m, s, inv);
+      unsigned char *t = tile + z * 2 * KQ;
+      const int byte = lane * E * 2;  // of the row
+      const uint32_t at = kq_at<DK>(i, byte >> 4) + (byte & 15);
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      x[e] *= f;
-      m = max(m, mag(x[e]));
+      for (int e = 0; e < E; e += 2) {
+        uint32_t h, l;
+        split2(x[z][r][e] * f, x[z][r][e + 1] * f, inv, h, l);
+        *reinterpret_cast<uint32_t *>(t + at + 2 * e) = h;
+        *reinterpret_cast<uint32_t *>(t + KQ + at + 2 * e) = l;
+      }
+      if (lane == 0) (z ? scale_q : scale_k)[i] = s;
     }
-    m = __reduce_max_sync(0xFFFFFFFFu, m);
-    float s, inv;
-    row_scale(m, s, inv);
-    unsigned char *t = tile + (is_q ? 2 * KQ : 0);
-    const int byte = lane * E * 2;  // of the row
-    const uint32_t at = kq_at<DK>(i, byte >> 4) + (byte & 15);
-#pragma unroll
-    for (int e = 0; e < E; e += 2) {
-      uint32_t h, l;
-      split2(x[e] * inv, x[e + 1] * inv, h, l);
-      *reinterpret_cast<uint32_t *>(t + at + 2 * e) = h;
-      *reinterpret_cast<uint32_t *>(t + KQ + at + 2 * e) = l;
-    }
-    if (lane == 0) (is_q ? scale_q : scale_k)[i] = s;
-  }
   __syncthreads();
   {
     uint4 *dst = reinterpret_cast<uint4 *>(a.kq + (static_cast<size_t>(slot) * a.d.Hk + hk) * Tiles<DK>::kKQAll);
@@ -176,22 +239,22 @@ __global__ void __launch_bounds__(kPrepWarps * 32) delta_prep_kernel(const Chunk
   {
     const uint32_t k0 = smem_u32(tile), rows = k0 + (warp >= 2 ? 2 * KQ : 0);
     const int r0 = (warp & 1) * 16;
-    float c[4][4] = {};
+    float c[4][4];
 #pragma unroll
     for (int ks = 0; ks < DK / 16; ++ks) {
       uint32_t ah[4], al[4];
       const uint32_t at = kq_at<DK>(r0 + (lane & 15), 2 * ks + (lane >> 4));
       ldsm4(ah, rows + at);
       ldsm4(al, rows + KQ + at);
+      uint32_t bh[4][2], bl[4][2];
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
-        uint32_t bh[4], bl[4];
         const uint32_t bt = kq_at<DK>(16 * p + (lane & 7) + ((lane >> 4) << 3), 2 * ks + ((lane >> 3) & 1));
-        ldsm4(bh, k0 + bt);
-        ldsm4(bl, k0 + KQ + bt);
-        mma3(c[2 * p], ah, al, bh[0], bh[1], bl[0], bl[1]);
-        mma3(c[2 * p + 1], ah, al, bh[2], bh[3], bl[2], bl[3]);
+        load2<false>(bh[2 * p], bh[2 * p + 1], k0 + bt);
+        load2<false>(bl[2 * p], bl[2 * p + 1], k0 + KQ + bt);
       }
+      if (ks == 0) mma3<true>(c, ah, al, bh, bl);
+      else mma3<false>(c, ah, al, bh, bl);
     }
     float(*out)[C + 1] = warp >= 2 ? qk : kk;
     const float *sr = warp >= 2 ? scale_q : scale_k;
@@ -205,55 +268,30 @@ __global__ void __launch_bounds__(kPrepWarps * 32) delta_prep_kernel(const Chunk
   }
   __syncthreads();
 
-  const int group = a.d.Hv / a.d.Hk;
-  for (int r = warp; r < group; r += kPrepWarps) {
-    const int h = a.d.tiled ? hk + r * a.d.Hk : hk * group + r;
-    float(*const M)[C + 4] = mat[warp];
-    float2 ga = make_float2(0.f, 0.f);
-    if (lane < len) ga = qg::delta_gates(a.d, t0 + lane, h);
+  // items: T of every value head, then the decayed Q K^T of every value head
+  for (int it = warp; it < 2 * group; it += kPrepWarps) {
+    const int h = head_of(it);
+    unsigned char *ta = a.ta + (static_cast<size_t>(slot) * a.d.Hv + h) * kTA;
+    Factors *f = reinterpret_cast<Factors *>(ta + 4 * kSq);
+    const float2 ga = gates;
+    gates = gates_of(it + kPrepWarps);
     double sum = ga.x;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const double y = __shfl_up_sync(0xFFFFFFFFu, sum, o);
       if (lane >= o) sum += y;
     }
+    sum *= 1.4426950408889634;  // log2(e)
     const float g_hi = static_cast<float>(sum), g_lo = static_cast<float>(sum - g_hi);
     __syncwarp();
     gsum[warp][lane] = make_float2(g_hi, g_lo);
-    sbeta[warp][lane] = ga.y;
     __syncwarp();
-    // a lane per row i: decays from j to i, and the system's row
-    float dec[C];
-#pragma unroll
-    for (int j = 0; j < C; ++j) {
+    auto decay = [&](int j) {  // from token j to this lane's
       const float2 gj = gsum[warp][j];
-      dec[j] = j <= lane ? expf((g_hi - gj.x) + (g_lo - gj.y)) : 0.f;
-      M[lane][j] = j < lane ? ga.y * dec[j] * kk[lane][j] : 0.f;
-    }
-    __syncwarp();
-    // a lane per column: (1 + A) X = 1 from the top
-    float x[C];
-#pragma unroll
-    for (int i = 0; i < C; ++i) {
-      float acc = i == lane ? 1.f : 0.f;
-#pragma unroll
-      for (int j4 = 0; j4 < i; j4 += 4) {
-        const float4 m = *reinterpret_cast<const float4 *>(&M[i][j4]);
-        acc = fmaf(-m.x, x[j4], acc);
-        if (j4 + 1 < i) acc = fmaf(-m.y, x[j4 + 1], acc);
-        if (j4 + 2 < i) acc = fmaf(-m.z, x[j4 + 2], acc);
-        if (j4 + 3 < i) acc = fmaf(-m.w, x[j4 + 3], acc);
-      }
-      x[i] = i < lane ? 0.f : acc;
-    }
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < C; ++i) M[i][lane] = i < lane ? 0.f : x[i] * ga.y;
-    __syncwarp();
-    // a lane per row: both square tiles
-    unsigned char *ta = a.ta + (static_cast<size_t>(slot) * a.d.Hv + h) * kTA;
-    Factors *f = reinterpret_cast<Factors *>(ta + 4 * kSq);
-    auto write_row = [&](float (&v)[C], unsigned char *dst, float *scales) {
+      return j <= lane ? ex2((g_hi - gj.x) + (g_lo - gj.y)) : 0.f;
+    };
+    // a lane per row: its scale and its pieces
+    auto write_row = [&](const float (&v)[C], unsigned char *dst, float *scales) {
       uint32_t m = 0;
 #pragma unroll
       for (int j = 0; j < C; ++j) m = max(m, mag(v[j]));
@@ -264,33 +302,57 @@ __global__ void __launch_bounds__(kPrepWarps * 32) delta_prep_kernel(const Chunk
       for (int p = 0; p < 4; ++p) {
         uint32_t h4[4], l4[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) split2(v[8 * p + 2 * e] * inv, v[8 * p + 2 * e + 1] * inv, h4[e], l4[e]);
+        for (int e = 0; e < 4; ++e) split2(v[8 * p + 2 * e], v[8 * p + 2 * e + 1], inv, h4[e], l4[e]);
         *reinterpret_cast<uint4 *>(dst + sq_at(lane, p)) = make_uint4(h4[0], h4[1], h4[2], h4[3]);
         *reinterpret_cast<uint4 *>(dst + kSq + sq_at(lane, p)) = make_uint4(l4[0], l4[1], l4[2], l4[3]);
       }
     };
-    {
-      float v[C];
+    float w[C];
+    if (it >= group) {
 #pragma unroll
-      for (int j = 0; j < C; j += 4) {
-        const float4 m = *reinterpret_cast<const float4 *>(&M[lane][j]);
-        v[j] = m.x, v[j + 1] = m.y, v[j + 2] = m.z, v[j + 3] = m.w;
-      }
-      write_row(v, ta, f->st);
-#pragma unroll
-      for (int j = 0; j < C; ++j) v[j] = j <= lane ? dec[j] * qk[lane][j] : 0.f;
-      write_row(v, ta + 2 * kSq, f->sa);
+      for (int j = 0; j < C; ++j) w[j] = j <= lane ? decay(j) * qk[lane][j] : 0.f;
+      write_row(w, ta + 2 * kSq, f->sa);
+      const float2 gl = gsum[warp][C - 1];
+      const float eg = ex2(g_hi + g_lo);
+      f->fk[lane] = eg * scale_k[lane];
+      f->fq[lane] = eg * scale_q[lane];
+      f->wk[lane] = ex2((gl.x - g_hi) + (gl.y - g_lo)) * scale_k[lane];
+      f->alpha[lane] = expf(ga.x);
+      f->beta[lane] = ga.y;
+      f->sk[lane] = scale_k[lane];
+      f->sq[lane] = scale_q[lane];
+      if (lane == 0) f->dec = chunk_decay(gl.x + gl.y);
+      continue;
     }
-    const float2 gl = gsum[warp][C - 1];
-    const float eg = expf(g_hi + g_lo);
-    f->fk[lane] = eg * scale_k[lane];
-    f->fq[lane] = eg * scale_q[lane];
-    f->wk[lane] = expf((gl.x - g_hi) + (gl.y - g_lo)) * scale_k[lane];
-    f->alpha[lane] = expf(ga.x);
-    f->beta[lane] = ga.y;
-    f->sk[lane] = scale_k[lane];
-    f->sq[lane] = scale_q[lane];
-    if (lane == 0) f->dec = expf(gl.x + gl.y);
+    float(*const M)[kTurn] = reinterpret_cast<float(*)[kTurn]>(tile + warp * (C * kTurn * 4));
+    // a lane per row of A
+#pragma unroll
+    for (int j = 0; j < C; ++j) M[lane][j] = j < lane ? ga.y * decay(j) * kk[lane][j] : 0.f;
+    __syncwarp();
+    // a lane per column: (1 + A) X = 1 from the top, two sums a row
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      float acc = i == lane ? 1.f : 0.f, acc2 = 0.f;
+#pragma unroll
+      for (int j4 = 0; j4 < i; j4 += 4) {
+        const float4 m = *reinterpret_cast<const float4 *>(&M[i][j4]);
+        acc = fmaf(-m.x, w[j4], acc);
+        if (j4 + 1 < i) acc2 = fmaf(-m.y, w[j4 + 1], acc2);
+        if (j4 + 2 < i) acc = fmaf(-m.z, w[j4 + 2], acc);
+        if (j4 + 3 < i) acc2 = fmaf(-m.w, w[j4 + 3], acc2);
+      }
+      w[i] = i < lane ? 0.f : acc + acc2;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < C; ++i) M[i][lane] = i < lane ? 0.f : w[i] * ga.y;
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < C; j += 4) {
+      const float4 m = *reinterpret_cast<const float4 *>(&M[lane][j]);
+      w[j] = m.x, w[j + 1] = m.y, w[j + 2] = m.z, w[j + 3] = m.w;
+    }
+    write_row(w, ta, f->st);
     __syncwarp();
   }
 }
@@ -303,12 +365,13 @@ __global__ void __launch_bounds__(kPrepWarps * 32) delta_prep_kernel(const Chunk
 template <int DK, int W, int NST>
 struct WalkSmem {
   static constexpr int kStage = Tiles<DK>::kKQAll + kTA;
-  static constexpr int kBytes = NST * kStage + 128;
+  static constexpr int kBytes = NST * kStage;
+  static_assert(kStage % 256 == 0, "rows' pieces are found by exclusive or");
 };
 
 template <int DK, int W, int NST>
 __global__ void __launch_bounds__(W * 32) delta_walk_kernel(const ChunkArgs a) {
-  extern __shared__ __align__(128) unsigned char ring[];
+  extern __shared__ __align__(1024) unsigned char ring[];
   __shared__ uint64_t full[NST];
   __shared__ int left[NST];  // warps that are done with a stage's contents
   constexpr int KQ = Tiles<DK>::kKQ, kStage = WalkSmem<DK, W, NST>::kStage;
@@ -362,17 +425,39 @@ __global__ void __launch_bounds__(W * 32) delta_walk_kernel(const ChunkArgs a) {
   }
   const float *vp = a.d.v + d0;
   float *op = a.d.out + d0;
-  auto load_v = [&](int c, float (&v)[4][4]) {
+  // this lane's tokens of a chunk are 8 t + 2 q4 and the one after
+  const float *vnext = vp + static_cast<long long>(t00 + 2 * q4) * a.d.v_stride;
+  float *onext = op + static_cast<long long>(t00 + 2 * q4) * a.d.out_stride;
+  auto load_v = [&](int c, float (&v)[4][4]) {  // called once for every chunk in turn
+    const float *p = vnext;
+    if ((c + 1) * C <= n) {
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int j = c * C + 8 * t + 2 * q4 + (e & 1);
-        v[t][e] = j < n ? __ldg(vp + static_cast<long long>(t00 + j) * a.d.v_stride + 8 * (e >> 1)) : 0.f;
+      for (int t = 0; t < 4; ++t, p += 8 * a.d.v_stride) {
+        v[t][0] = __ldg(p);
+        v[t][1] = __ldg(p + a.d.v_stride);
+        v[t][2] = __ldg(p + 8);
+        v[t][3] = __ldg(p + a.d.v_stride + 8);
       }
+    } else {
+#pragma unroll
+      for (int t = 0; t < 4; ++t, p += 8 * a.d.v_stride) {
+        const int j = c * C + 8 * t + 2 * q4;
+        v[t][0] = j < n ? __ldg(p) : 0.f;
+        v[t][1] = j + 1 < n ? __ldg(p + a.d.v_stride) : 0.f;
+        v[t][2] = j < n ? __ldg(p + 8) : 0.f;
+        v[t][3] = j + 1 < n ? __ldg(p + a.d.v_stride + 8) : 0.f;
+      }
+    }
+    vnext += C * a.d.v_stride;
   };
   float v[4][4];
   load_v(0, v);
+  // where this lane's rows of the tiles start for ldmatrix: pieces are then found by exclusive or.  Keys and queries as right
+  // operands of S0 (a row per token), keys as right operands of U (turned), square tiles
+  const int brow = (lane & 7) + ((lane >> 4) << 3), bpiece = (lane >> 3) & 1;
+  const uint32_t off_b = brow * (DK * 2) + ((bpiece ^ (brow & 7)) << 4);
+  const uint32_t off_t = (lane & 15) * (DK * 2) + (((lane >> 4) ^ (lane & 7)) << 4);
+  const uint32_t off_s = sq_at(brow, bpiece);
 
   for (int c = 0; c < chunks; ++c) {
     const int st = c % NST;
@@ -380,46 +465,44 @@ __global__ void __launch_bounds__(W * 32) delta_walk_kernel(const ChunkArgs a) {
       if (lane == 0) atomicOr(&g_qg_status_delta_chunk, QG_STATUS_BIT_TIMEOUT);
       return;
     }
-    const uint32_t kt = smem_u32(ring + st * kStage), qt = kt + 2 * KQ, tt = kt + Tiles<DK>::kKQAll, at = tt + 2 * kSq;
+    const uint32_t kt = smem_u32(ring + st * kStage), tt = kt + Tiles<DK>::kKQAll, at = tt + 2 * kSq;
     const Factors *f = reinterpret_cast<const Factors *>(ring + st * kStage + Tiles<DK>::kKQAll + 4 * kSq);
-    float o[4][4] = {};
+    float o[4][4];
     bool odd = false;
     {
-      // rows of S^T in two terms
-      uint32_t m0 = 0, m1 = 0;
+      // rows of S^T in two terms (a NaN does not count for the scale; it makes its row's products NaN)
+      float m0 = 0.f, m1 = 0.f;
 #pragma unroll
       for (int ct = 0; ct < DK / 8; ++ct) {
-        m0 = max(m0, max(mag(s[ct][0]), mag(s[ct][1])));
-        m1 = max(m1, max(mag(s[ct][2]), mag(s[ct][3])));
+        m0 = fmaxf(m0, fmaxf(fabsf(s[ct][0]), fabsf(s[ct][1])));
+        m1 = fmaxf(m1, fmaxf(fabsf(s[ct][2]), fabsf(s[ct][3])));
       }
-      m0 = max(m0, __shfl_xor_sync(0xFFFFFFFFu, m0, 1));
-      m1 = max(m1, __shfl_xor_sync(0xFFFFFFFFu, m1, 1));
-      m0 = max(m0, __shfl_xor_sync(0xFFFFFFFFu, m0, 2));
-      m1 = max(m1, __shfl_xor_sync(0xFFFFFFFFu, m1, 2));
+      m0 = fmaxf(m0, __shfl_xor_sync(0xFFFFFFFFu, m0, 1));
+      m1 = fmaxf(m1, __shfl_xor_sync(0xFFFFFFFFu, m1, 1));
+      m0 = fmaxf(m0, __shfl_xor_sync(0xFFFFFFFFu, m0, 2));
+      m1 = fmaxf(m1, __shfl_xor_sync(0xFFFFFFFFu, m1, 2));
       float s0, i0, s1, i1;
-      row_scale(m0, s0, i0);
-      row_scale(m1, s1, i1);
-      float x[4][4] = {};
+      row_scale(mag(m0), s0, i0);
+      row_scale(mag(m1), s1, i1);
+      float x[8][4];  // (K S0)^T, then (Q S0)^T
 #pragma unroll
       for (int ks = 0; ks < DK / 16; ++ks) {
         uint32_t ah[4], al[4];
-        split2(s[2 * ks][0] * i0, s[2 * ks][1] * i0, ah[0], al[0]);
-        split2(s[2 * ks][2] * i1, s[2 * ks][3] * i1, ah[1], al[1]);
-        split2(s[2 * ks + 1][0] * i0, s[2 * ks + 1][1] * i0, ah[2], al[2]);
-        split2(s[2 * ks + 1][2] * i1, s[2 * ks + 1][3] * i1, ah[3], al[3]);
+        split2(s[2 * ks][0], s[2 * ks][1], i0, ah[0], al[0]);
+        split2(s[2 * ks][2], s[2 * ks][3], i1, ah[1], al[1]);
+        split2(s[2 * ks + 1][0], s[2 * ks + 1][1], i0, ah[2], al[2]);
+        split2(s[2 * ks + 1][2], s[2 * ks + 1][3], i1, ah[3], al[3]);
+        uint32_t bh[8][2], bl[8][2];
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
-          uint32_t bh[4], bl[4];
-          const uint32_t off = kq_at<DK>(16 * p + (lane & 7) + ((lane >> 4) << 3), 2 * ks + ((lane >> 3) & 1));
-          ldsm4(bh, kt + off);
-          ldsm4(bl, kt + KQ + off);
-          mma3(x[2 * p], ah, al, bh[0], bh[1], bl[0], bl[1]);
-          mma3(x[2 * p + 1], ah, al, bh[2], bh[3], bl[2], bl[3]);
-          ldsm4(bh, qt + off);
-          ldsm4(bl, qt + KQ + off);
-          mma3(o[2 * p], ah, al, bh[0], bh[1], bl[0], bl[1]);
-          mma3(o[2 * p + 1], ah, al, bh[2], bh[3], bl[2], bl[3]);
+          const uint32_t at = ((kt + off_b) ^ (ks << 5)) + p * 16 * (DK * 2);
+          load2<false>(bh[2 * p], bh[2 * p + 1], at);
+          load2<false>(bl[2 * p], bl[2 * p + 1], at + KQ);
+          load2<false>(bh[4 + 2 * p], bh[5 + 2 * p], at + 2 * KQ);
+          load2<false>(bl[4 + 2 * p], bl[5 + 2 * p], at + 3 * KQ);
         }
+        if (ks == 0) mma3<true>(x, ah, al, bh, bl);
+        else mma3<false>(x, ah, al, bh, bl);
       }
       // R^T = V^T - e^G (K S0)^T, in v; O^T = e^G (Q S0)^T
 #pragma unroll
@@ -430,10 +513,10 @@ __global__ void __launch_bounds__(W * 32) delta_walk_kernel(const ChunkArgs a) {
         v[t][1] = fmaf(-fk.y * s0, x[t][1], v[t][1]);
         v[t][2] = fmaf(-fk.x * s1, x[t][2], v[t][2]);
         v[t][3] = fmaf(-fk.y * s1, x[t][3], v[t][3]);
-        o[t][0] *= fq.x * s0;
-        o[t][1] *= fq.y * s0;
-        o[t][2] *= fq.x * s1;
-        o[t][3] *= fq.y * s1;
+        o[t][0] = x[4 + t][0] * (fq.x * s0);
+        o[t][1] = x[4 + t][1] * (fq.y * s0);
+        o[t][2] = x[4 + t][2] * (fq.x * s1);
+        o[t][3] = x[4 + t][3] * (fq.y * s1);
       }
     }
     // scales of the rows of a [16][32] accumulator; whether all of it is finite
@@ -452,36 +535,43 @@ __global__ void __launch_bounds__(W * 32) delta_walk_kernel(const ChunkArgs a) {
       row_scale(m1, s1, i1);
       return !__any_sync(0xFFFFFFFFu, max(m0, m1) >= kInfBits);
     };
-    auto split = [&](const float (&w)[4][4], float i0, float i1, uint32_t (&ah)[2][4], uint32_t (&al)[2][4]) {
+    auto split = [&](auto kind, const float (&w)[4][4], float i0, float i1, uint32_t (&ah)[2][4], uint32_t (&al)[2][4]) {
+      auto two = [&](float x, float y, float inv, uint32_t &hi, uint32_t &lo) {
+        if constexpr (decltype(kind)::value) split2_each(x, y, inv, hi, lo);
+        else split2(x, y, inv, hi, lo);
+      };
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
-        split2(w[2 * ks][0] * i0, w[2 * ks][1] * i0, ah[ks][0], al[ks][0]);
-        split2(w[2 * ks][2] * i1, w[2 * ks][3] * i1, ah[ks][1], al[ks][1]);
-        split2(w[2 * ks + 1][0] * i0, w[2 * ks + 1][1] * i0, ah[ks][2], al[ks][2]);
-        split2(w[2 * ks + 1][2] * i1, w[2 * ks + 1][3] * i1, ah[ks][3], al[ks][3]);
+        two(w[2 * ks][0], w[2 * ks][1], i0, ah[ks][0], al[ks][0]);
+        two(w[2 * ks][2], w[2 * ks][3], i1, ah[ks][1], al[ks][1]);
+        two(w[2 * ks + 1][0], w[2 * ks + 1][1], i0, ah[ks][2], al[ks][2]);
+        two(w[2 * ks + 1][2], w[2 * ks + 1][3], i1, ah[ks][3], al[ks][3]);
       }
     };
+    using Each = std::true_type;    // rows of tokens
+    using Whole = std::false_type;  // rows that are summed as a whole
     // w (16 x 32) times a lower triangular square tile's transpose
     auto times_tile = [&](const uint32_t (&ah)[2][4], const uint32_t (&al)[2][4], uint32_t tile, float (&w)[4][4]) {
-#pragma unroll
-      for (int p = 0; p < 2; ++p)
-#pragma unroll
-        for (int ks = 0; ks <= p; ++ks) {
-          uint32_t bh[4], bl[4];
-          const uint32_t off = sq_at(16 * p + (lane & 7) + ((lane >> 4) << 3), 2 * ks + ((lane >> 3) & 1));
-          ldsm4(bh, tile + off);
-          ldsm4(bl, tile + kSq + off);
-          mma3(w[2 * p], ah[ks], al[ks], bh[0], bh[1], bl[0], bl[1]);
-          mma3(w[2 * p + 1], ah[ks], al[ks], bh[2], bh[3], bl[2], bl[3]);
-        }
+      uint32_t bh[4][2], bl[4][2];
+      auto load = [&](int p, int ks) {
+        const uint32_t at = ((tile + off_s) ^ (ks << 5)) + p * 16 * (C * 2);
+        load2<false>(bh[2 * p], bh[2 * p + 1], at);
+        load2<false>(bl[2 * p], bl[2 * p + 1], at + kSq);
+      };
+      load(0, 0);
+      load(1, 0);
+      mma3<true>(w, ah[0], al[0], bh, bl);
+      load(1, 1);  // the first 16 rows end with their diagonal
+      float (&lower)[2][4] = *reinterpret_cast<float(*)[2][4]>(&w[2]);
+      mma3<false>(lower, ah[1], al[1], *reinterpret_cast<uint32_t(*)[2][2]>(&bh[2]), *reinterpret_cast<uint32_t(*)[2][2]>(&bl[2]));
     };
-    float u[4][4] = {};
+    float u[4][4];
     {
       float s0, i0, s1, i1;
       odd = !scales(v, s0, i0, s1, i1);
       if (!odd) {
         uint32_t ah[2][4], al[2][4];
-        split(v, i0, i1, ah, al);
+        split(Each{}, v, i0, i1, ah, al);
         times_tile(ah, al, tt, u);
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
@@ -495,8 +585,8 @@ __global__ void __launch_bounds__(W * 32) delta_walk_kernel(const ChunkArgs a) {
       }
       if (!odd) {
         uint32_t ah[2][4], al[2][4];
-        split(u, i0, i1, ah, al);
-        float w[4][4] = {};
+        split(Each{}, u, i0, i1, ah, al);
+        float w[4][4];
         times_tile(ah, al, at, w);
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
@@ -506,13 +596,13 @@ __global__ void __launch_bounds__(W * 32) delta_walk_kernel(const ChunkArgs a) {
           o[t][2] = fmaf(x.x * s1, w[t][2], o[t][2]);
           o[t][3] = fmaf(x.y * s1, w[t][3], o[t][3]);
         }
+        float *p = onext;
+        const int left_over = n - c * C - 2 * q4;
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int j = c * C + 8 * t + 2 * q4 + (e & 1);
-            if (j < n) op[static_cast<long long>(t00 + j) * a.d.out_stride + 8 * (e >> 1)] = o[t][e];
-          }
+        for (int t = 0; t < 4; ++t, p += 8 * a.d.out_stride) {
+          if (8 * t < left_over) p[0] = o[t][0], p[8] = o[t][2];
+          if (8 * t + 1 < left_over) p[a.d.out_stride] = o[t][1], p[a.d.out_stride + 8] = o[t][3];
+        }
       }
     }
     if (!odd) {
@@ -529,22 +619,24 @@ __global__ void __launch_bounds__(W * 32) delta_walk_kernel(const ChunkArgs a) {
       float s0, i0, s1, i1;
       scales(u, s0, i0, s1, i1);
       uint32_t ah[2][4], al[2][4];
-      split(u, i0, i1, ah, al);
+      split(Whole{}, u, i0, i1, ah, al);
       const float dec = f->dec;
 #pragma unroll
       for (int c4 = 0; c4 < DK / 8; c4 += 4) {
-        float w[4][4] = {};
+        float w[4][4];
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks)
+        for (int ks = 0; ks < 2; ++ks) {
+          uint32_t bh[4][2], bl[4][2];
 #pragma unroll
           for (int p = 0; p < 2; ++p) {
-            uint32_t bh[4], bl[4];
-            const uint32_t off = kq_at<DK>(16 * ks + (lane & 15), c4 + 2 * p + (lane >> 4));
-            ldsm4_t(bh, kt + off);
-            ldsm4_t(bl, kt + KQ + off);
-            mma3(w[2 * p], ah[ks], al[ks], bh[0], bh[1], bl[0], bl[1]);
-            mma3(w[2 * p + 1], ah[ks], al[ks], bh[2], bh[3], bl[2], bl[3]);
+            const uint32_t at = ((kt + off_t) ^ ((c4 + 2 * p) << 4)) + ks * 16 * (DK * 2);
+            load2<true>(bh[2 * p], bh[2 * p + 1], at);
+            load2<true>(bl[2 * p], bl[2 * p + 1], at + KQ);
           }
+          if (ks == 0) mma3<true>(w, ah[ks], al[ks], bh, bl);
+          else mma3<false>(w, ah[ks], al[ks], bh, bl);
+        }
+        // not on the packed unit: it counts denormal states as zero
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
           s[c4 + t][0] = fmaf(s0, w[t][0], dec * s[c4 + t][0]);
@@ -606,6 +698,7 @@ __global__ void __launch_bounds__(W * 32) delta_walk_kernel(const ChunkArgs a) {
       }
       if (c + 1 < chunks) load_v(c + 1, v);
     }
+    onext += C * a.d.out_stride;
     __syncwarp();
     if (lane == 0) {
       __threadfence_block();
@@ -641,7 +734,7 @@ cudaError_t walk(const ChunkArgs &a, cudaStream_t s) {
 
 template <int DK>
 cudaError_t both(const ChunkArgs &a, cudaStream_t s) {
-  constexpr int smem = Tiles<DK>::kKQAll;
+  constexpr int smem = std::max(Tiles<DK>::kKQAll, kPrepWarps * C * kTurn * 4);
   if (!qg::set_smem_attr(reinterpret_cast<const void *>(delta_prep_kernel<DK>), smem)) return cudaErrorInvalidValue;
   cudaError_t e = qg::launch_pdl(delta_prep_kernel<DK>, dim3(static_cast<unsigned>(a.slots) * a.d.Hk), dim3(kPrepWarps * 32), smem, s, a);
   if (e != cudaSuccess) return e;
