@@ -19,6 +19,7 @@
 
 #include "qg_delta.cuh"
 #include "qg_mma.cuh"
+#include "qg_tc.cuh"
 
 __device__ unsigned int g_qg_status_delta_chunk;  // this translation unit's device status word
 static std::atomic<bool> g_launched{false};       // whether a kernel that may set it has been launched
@@ -31,15 +32,16 @@ static_assert(C == 32, "a lane per token");
 
 // ---- the workspace ------------------------------------------------------------------------------
 // Sequence b's chunks have the numbers q_start[b] / 32 + b, and on: they rise, and ceil(n / 32) of them fit
-// before the next sequence's.  Per (chunk, key head): K hi, K lo, Q hi, Q lo, [32][DK] f16 each.  Per (chunk, value head):
-// T hi, T lo, A hi, A lo, [32][32] f16 each, and the factors below.  Tiles are stored as shared memory wants them:
-// 16-byte pieces of a row exchanged so that eight rows of one piece lie in all banks.
+// before the next sequence's.  Per (chunk, key head): K hi, K lo, Q hi, Q lo, each as DK / 64 blocks of [32][64] f16.  Per
+// (chunk, value head): T and A, [32][32 hi, 32 lo] f16 each, and the factors below.  So every row of a block is 128 bytes, and
+// its eight 16-byte pieces are exchanged by the row's low three bits: the 128-byte swizzle of the tensor cores' operands, and
+// free of bank conflicts for ldmatrix, turned or not.
+constexpr int kBlock = C * 128;  // bytes of a block
 template <int DK>
 struct Tiles {
-  static constexpr int kKQ = C * DK * 2;             // bytes of one key or query tile
+  static constexpr int kKQ = DK / 64 * kBlock;       // bytes of one key or query tile
   static constexpr int kKQAll = 4 * kKQ;
 };
-constexpr int kSq = C * C * 2;  // bytes of one square tile
 struct Factors {
   float fk[C];     // e^{G_j} sk_j: what K S0 is multiplied by
   float fq[C];     // e^{G_i} sq_i
@@ -48,16 +50,16 @@ struct Factors {
   float wk[C];     // e^{G_C - G_j} sk_j
   float alpha[C], beta[C], sk[C], sq[C];  // token by token, for chunks with infinite or NaN values
   float dec;       // e^{G_C}
-  float pad[31];
+  int odd;         // such a value among the queries, keys and gates
+  float pad[30];
 };
-constexpr int kTA = 4 * kSq + static_cast<int>(sizeof(Factors));
+constexpr int kTA = 2 * kBlock + static_cast<int>(sizeof(Factors));
 static_assert(kTA % 16 == 0, "bulk copies");
 
-template <int DK>
-QG_DEVICE uint32_t kq_at(int row, int piece) {  // byte offset of 16-byte piece `piece` of a row
-  return row * (DK * 2) + ((piece ^ (row & 7)) << 4);
-}
-QG_DEVICE uint32_t sq_at(int row, int piece) { return row * (C * 2) + ((piece ^ ((row >> 1) & 3)) << 4); }
+// byte offset of piece `piece` (16 bytes) of a row of a block
+QG_DEVICE uint32_t at_piece(int row, int piece) { return row * 128 + ((piece ^ (row & 7)) << 4); }
+// the same in a tile of several blocks
+QG_DEVICE uint32_t kq_at(int row, int piece) { return (piece >> 3) * kBlock + at_piece(row, piece & 7); }
 
 // the power of two that brings magnitude bits m to [2^7, 2^8), and its inverse; 1 for infinities and NaN
 QG_DEVICE void row_scale(uint32_t m, float &s, float &inv) {
@@ -147,6 +149,7 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 5) delta_prep_kernel(const Ch
   __shared__ float kk[C][C + 1], qk[C][C + 1];
   __shared__ float scale_k[C], scale_q[C];
   __shared__ float2 gsum[kPrepWarps][C];
+  __shared__ int bad_rows;
   constexpr int KQ = Tiles<DK>::kKQ;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int slot = static_cast<int>(blockIdx.x) / a.d.Hk, hk = static_cast<int>(blockIdx.x) % a.d.Hk;
@@ -164,6 +167,8 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 5) delta_prep_kernel(const Ch
   if (n < a.first_len || first < 0 || first >= n) return;
   const int len = min(C, n - first), t0 = t00 + first;
 
+  if (tid == 0) bad_rows = 0;
+  __syncthreads();
   // rows: 8 of K and 8 of Q a warp, all of them under way at once
   constexpr int E = DK / 32;
   constexpr int R = C / kPrepWarps;
@@ -219,7 +224,7 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 5) delta_prep_kernel(const Ch
       row_scale(m, s, inv);
       unsigned char *t = tile + z * 2 * KQ;
       const int byte = lane * E * 2;  // of the row
-      const uint32_t at = kq_at<DK>(i, byte >> 4) + (byte & 15);
+      const uint32_t at = kq_at(i, byte >> 4) + (byte & 15);
 #pragma unroll
       for (int e = 0; e < E; e += 2) {
         uint32_t h, l;
@@ -227,7 +232,10 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 5) delta_prep_kernel(const Ch
         *reinterpret_cast<uint32_t *>(t + at + 2 * e) = h;
         *reinterpret_cast<uint32_t *>(t + KQ + at + 2 * e) = l;
       }
-      if (lane == 0) (z ? scale_q : scale_k)[i] = s;
+      if (lane == 0) {
+        (z ? scale_q : scale_k)[i] = s;
+        if (m >= kInfBits) bad_rows = 1;
+      }
     }
   __syncthreads();
   {
@@ -243,13 +251,13 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 5) delta_prep_kernel(const Ch
 #pragma unroll
     for (int ks = 0; ks < DK / 16; ++ks) {
       uint32_t ah[4], al[4];
-      const uint32_t at = kq_at<DK>(r0 + (lane & 15), 2 * ks + (lane >> 4));
+      const uint32_t at = kq_at(r0 + (lane & 15), 2 * ks + (lane >> 4));
       ldsm4(ah, rows + at);
       ldsm4(al, rows + KQ + at);
       uint32_t bh[4][2], bl[4][2];
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
-        const uint32_t bt = kq_at<DK>(16 * p + (lane & 7) + ((lane >> 4) << 3), 2 * ks + ((lane >> 3) & 1));
+        const uint32_t bt = kq_at(16 * p + (lane & 7) + ((lane >> 4) << 3), 2 * ks + ((lane >> 3) & 1));
         load2<false>(bh[2 * p], bh[2 * p + 1], k0 + bt);
         load2<false>(bl[2 * p], bl[2 * p + 1], k0 + KQ + bt);
       }
@@ -272,7 +280,7 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 5) delta_prep_kernel(const Ch
   for (int it = warp; it < 2 * group; it += kPrepWarps) {
     const int h = head_of(it);
     unsigned char *ta = a.ta + (static_cast<size_t>(slot) * a.d.Hv + h) * kTA;
-    Factors *f = reinterpret_cast<Factors *>(ta + 4 * kSq);
+    Factors *f = reinterpret_cast<Factors *>(ta + 2 * kBlock);
     const float2 ga = gates;
     gates = gates_of(it + kPrepWarps);
     double sum = ga.x;
@@ -303,15 +311,15 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 5) delta_prep_kernel(const Ch
         uint32_t h4[4], l4[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) split2(v[8 * p + 2 * e], v[8 * p + 2 * e + 1], inv, h4[e], l4[e]);
-        *reinterpret_cast<uint4 *>(dst + sq_at(lane, p)) = make_uint4(h4[0], h4[1], h4[2], h4[3]);
-        *reinterpret_cast<uint4 *>(dst + kSq + sq_at(lane, p)) = make_uint4(l4[0], l4[1], l4[2], l4[3]);
+        *reinterpret_cast<uint4 *>(dst + at_piece(lane, p)) = make_uint4(h4[0], h4[1], h4[2], h4[3]);
+        *reinterpret_cast<uint4 *>(dst + at_piece(lane, 4 + p)) = make_uint4(l4[0], l4[1], l4[2], l4[3]);
       }
     };
     float w[C];
     if (it >= group) {
 #pragma unroll
       for (int j = 0; j < C; ++j) w[j] = j <= lane ? decay(j) * qk[lane][j] : 0.f;
-      write_row(w, ta + 2 * kSq, f->sa);
+      write_row(w, ta + kBlock, f->sa);
       const float2 gl = gsum[warp][C - 1];
       const float eg = ex2(g_hi + g_lo);
       f->fk[lane] = eg * scale_k[lane];
@@ -321,7 +329,12 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 5) delta_prep_kernel(const Ch
       f->beta[lane] = ga.y;
       f->sk[lane] = scale_k[lane];
       f->sq[lane] = scale_q[lane];
-      if (lane == 0) f->dec = chunk_decay(gl.x + gl.y);
+      const bool bad = !(fabsf(ga.x) < INFINITY) || !(fabsf(ga.y) < INFINITY);
+      const int odd = __any_sync(0xFFFFFFFFu, bad) || bad_rows;
+      if (lane == 0) {
+        f->dec = chunk_decay(gl.x + gl.y);
+        f->odd = odd;
+      }
       continue;
     }
     float(*const M)[kTurn] = reinterpret_cast<float(*)[kTurn]>(tile + warp * (C * kTurn * 4));
@@ -364,9 +377,8 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 5) delta_prep_kernel(const Ch
 // bulk copies; the warp that leaves a stage last asks for its next contents.
 template <int DK, int W, int NST>
 struct WalkSmem {
-  static constexpr int kStage = Tiles<DK>::kKQAll + kTA;
+  static constexpr int kStage = (Tiles<DK>::kKQAll + kTA + 1023) / 1024 * 1024;  // pieces are found by exclusive or
   static constexpr int kBytes = NST * kStage;
-  static_assert(kStage % 256 == 0, "rows' pieces are found by exclusive or");
 };
 
 template <int DK, int W, int NST>
@@ -398,7 +410,7 @@ __global__ void __launch_bounds__(W * 32) delta_walk_kernel(const ChunkArgs a) {
   auto ask = [&](int c) {
     unsigned char *dst = ring + (c % NST) * kStage;
     uint64_t *bar = &full[c % NST];
-    mbar_arrive_expect_tx(bar, kStage);
+    mbar_arrive_expect_tx(bar, Tiles<DK>::kKQAll + kTA);
     bulk_g2s(dst, a.kq + (static_cast<size_t>(slot0 + c) * a.d.Hk + hk) * Tiles<DK>::kKQAll, Tiles<DK>::kKQAll, bar);
     bulk_g2s(dst + Tiles<DK>::kKQAll, a.ta + (static_cast<size_t>(slot0 + c) * a.d.Hv + h) * kTA, kTA, bar);
   };
@@ -453,11 +465,9 @@ __global__ void __launch_bounds__(W * 32) delta_walk_kernel(const ChunkArgs a) {
   float v[4][4];
   load_v(0, v);
   // where this lane's rows of the tiles start for ldmatrix: pieces are then found by exclusive or.  Keys and queries as right
-  // operands of S0 (a row per token), keys as right operands of U (turned), square tiles
+  // operands of S0 (a row per token), keys as right operands of U (turned)
   const int brow = (lane & 7) + ((lane >> 4) << 3), bpiece = (lane >> 3) & 1;
-  const uint32_t off_b = brow * (DK * 2) + ((bpiece ^ (brow & 7)) << 4);
-  const uint32_t off_t = (lane & 15) * (DK * 2) + (((lane >> 4) ^ (lane & 7)) << 4);
-  const uint32_t off_s = sq_at(brow, bpiece);
+  const uint32_t off_b = at_piece(brow, bpiece), off_t = at_piece(lane & 15, lane >> 4);
 
   for (int c = 0; c < chunks; ++c) {
     const int st = c % NST;
@@ -465,8 +475,8 @@ __global__ void __launch_bounds__(W * 32) delta_walk_kernel(const ChunkArgs a) {
       if (lane == 0) atomicOr(&g_qg_status_delta_chunk, QG_STATUS_BIT_TIMEOUT);
       return;
     }
-    const uint32_t kt = smem_u32(ring + st * kStage), tt = kt + Tiles<DK>::kKQAll, at = tt + 2 * kSq;
-    const Factors *f = reinterpret_cast<const Factors *>(ring + st * kStage + Tiles<DK>::kKQAll + 4 * kSq);
+    const uint32_t kt = smem_u32(ring + st * kStage), tt = kt + Tiles<DK>::kKQAll, at = tt + kBlock;
+    const Factors *f = reinterpret_cast<const Factors *>(ring + st * kStage + Tiles<DK>::kKQAll + 2 * kBlock);
     float o[4][4];
     bool odd = false;
     {
@@ -495,7 +505,7 @@ __global__ void __launch_bounds__(W * 32) delta_walk_kernel(const ChunkArgs a) {
         uint32_t bh[8][2], bl[8][2];
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
-          const uint32_t at = ((kt + off_b) ^ (ks << 5)) + p * 16 * (DK * 2);
+          const uint32_t at = ((kt + off_b) ^ ((ks & 3) << 5)) + (ks >> 2) * kBlock + p * 16 * 128;
           load2<false>(bh[2 * p], bh[2 * p + 1], at);
           load2<false>(bl[2 * p], bl[2 * p + 1], at + KQ);
           load2<false>(bh[4 + 2 * p], bh[5 + 2 * p], at + 2 * KQ);
@@ -554,9 +564,9 @@ __global__ void __launch_bounds__(W * 32) delta_walk_kernel(const ChunkArgs a) {
     auto times_tile = [&](const uint32_t (&ah)[2][4], const uint32_t (&al)[2][4], uint32_t tile, float (&w)[4][4]) {
       uint32_t bh[4][2], bl[4][2];
       auto load = [&](int p, int ks) {
-        const uint32_t at = ((tile + off_s) ^ (ks << 5)) + p * 16 * (C * 2);
+        const uint32_t at = ((tile + off_b) ^ (ks << 5)) + p * 16 * 128;
         load2<false>(bh[2 * p], bh[2 * p + 1], at);
-        load2<false>(bl[2 * p], bl[2 * p + 1], at + kSq);
+        load2<false>(bl[2 * p], bl[2 * p + 1], at ^ 64);
       };
       load(0, 0);
       load(1, 0);
@@ -629,7 +639,7 @@ __global__ void __launch_bounds__(W * 32) delta_walk_kernel(const ChunkArgs a) {
           uint32_t bh[4][2], bl[4][2];
 #pragma unroll
           for (int p = 0; p < 2; ++p) {
-            const uint32_t at = ((kt + off_t) ^ ((c4 + 2 * p) << 4)) + ks * 16 * (DK * 2);
+            const uint32_t at = ((kt + off_t) ^ (((c4 + 2 * p) & 7) << 4)) + (c4 >> 3) * kBlock + ks * 16 * 128;
             load2<true>(bh[2 * p], bh[2 * p + 1], at);
             load2<true>(bl[2 * p], bl[2 * p + 1], at + KQ);
           }
@@ -652,7 +662,7 @@ __global__ void __launch_bounds__(W * 32) delta_walk_kernel(const ChunkArgs a) {
       for (int j = 0; j < len; ++j) {
         const float al = f->alpha[j], be = f->beta[j], sk = f->sk[j], sq = f->sq[j];
         auto both = [&](int ct, float2 &k, float2 &q) {
-          const uint32_t off = kq_at<DK>(j, ct) + 4 * q4;
+          const uint32_t off = kq_at(j, ct) + 4 * q4;
           const uint32_t kh = *reinterpret_cast<const uint32_t *>(tile + off);
           const uint32_t kl = *reinterpret_cast<const uint32_t *>(tile + KQ + off);
           const uint32_t qh = *reinterpret_cast<const uint32_t *>(tile + 2 * KQ + off);
@@ -724,6 +734,432 @@ __global__ void __launch_bounds__(W * 32) delta_walk_kernel(const ChunkArgs a) {
   }
 }
 
+// ---- the walk with a head to an SM ---------------------------------------------------------------------
+// For heads of whole 128 columns: a CTA walks 128 columns of a head's state on tcgen05.  Row d of every product is column d of
+// the state, so a lane of tensor memory is one column and its thread works alone: the state stays in registers (two threads
+// a column, half of its rows each), left operands go to tensor memory as f16 pairs (hi in one range of columns, lo in
+// another), right operands are the tiles in shared memory, with K read as it lies for S0^T K^T and turned for U^T K.
+//   both groups  S^T in two terms; S^T <- e^{G_C} S^T + D
+//   group 0      R = V - ..., U, and U with the decays to the chunk's end, each in two terms; the next chunk's values
+//   group 1      the outputs of the chunk before
+//   control      bulk copies into the ring, and the products X = S^T K^T, O = S^T Q^T, U = R T^T, D = U K, O2 = U A^T
+// Every wait ends with its phase or after QG_WAIT_NS, which makes the CTA give up.
+constexpr int kTcThreads = 384;                    // two groups of four warps, control and three idle warps
+constexpr int kTcRegs = 168, kTcRegsWork = 208, kTcRegsRest = 88;
+static_assert(2 * kTcRegsWork + kTcRegsRest <= 3 * kTcRegs, "the warpgroups' shares come from the launch's total");
+constexpr int kTcStages = 4;
+constexpr int kOrder = 128;  // sequences that are put in order, longest first
+// columns of tensor memory
+enum { TX = 0, TO = 32, TU = 64, TO2 = 96, TD = 128, TS = 256, TR = 384, TUA = 416, TW = 448 };
+
+template <int DK>
+struct TcSmem {
+  static constexpr int kStage = (Tiles<DK>::kKQAll + kTA + 1023) / 1024 * 1024;
+  static constexpr int kBytes = kTcStages * kStage + 1024;
+};
+struct TcShared {
+  uint64_t full[kTcStages];
+  uint64_t s_ready, r_ready, u_ready, w_ready, o_free;  // by the working warps
+  uint64_t x_done, u_done, d_done, o_done;              // by the tensor cores
+  uint32_t tmem;
+  int abort, seq;
+  int odd_chunk, v_odd[2];  // the last chunk that goes token by token; chunks with such values, by their parity
+  float smax[2][128];       // largest of a column's halves
+  float scale_w[128], scale_u[128];
+  float4 ex[2][2][128];     // token by token: partial products of the halves, by the token's parity
+};
+
+template <int DK>
+__global__ void __launch_bounds__(kTcThreads, 1) delta_walk_tc_kernel(const ChunkArgs a) {
+  extern __shared__ unsigned char ring_raw[];
+  __shared__ TcShared sh;
+  constexpr int KQ = Tiles<DK>::kKQ, kStage = TcSmem<DK>::kStage;
+  constexpr int HK = DK / 2;  // rows of the state a thread holds
+  unsigned char *ring = ring_raw + ((1024u - (smem_u32(ring_raw) & 1023u)) & 1023u);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int parts = a.d.Dv / 128, per_seq = a.d.Hv * parts;
+  const int part = static_cast<int>(blockIdx.x) % parts, h = static_cast<int>(blockIdx.x) / parts % a.d.Hv;
+  const int place = static_cast<int>(blockIdx.x) / per_seq;
+  pdl_wait();
+  pdl_launch_dependents();
+  auto length = [&](int i) { return qg::delta_tok(a.d, i + 1) - qg::delta_tok(a.d, i); };
+  // the longest sequences first: theirs is the longest chain of chunks
+  if (tid == 0) sh.seq = place;
+  __syncthreads();
+  if (a.d.B > 1 && a.d.B <= kOrder && tid < a.d.B) {
+    const int mine = length(tid);
+    int rank = 0;
+    for (int i = 0; i < a.d.B; ++i) {
+      const int l = length(i);
+      rank += l > mine || (l == mine && i < tid);
+    }
+    if (rank == place) sh.seq = tid;
+  }
+  __syncthreads();
+  const int b = sh.seq;
+  const int t00 = qg::delta_tok(a.d, b), n = length(b);
+  if (n < a.first_len || n <= 0) return;
+  const int chunks = (n + C - 1) / C, slot0 = chunk_base(a.d, b), hk = qg::delta_key_head(a.d, h);
+  if (slot0 + chunks > a.slots) return;
+
+  if (tid == 0) {
+    for (int i = 0; i < kTcStages; ++i) mbar_init(&sh.full[i], 1);
+    mbar_init(&sh.s_ready, 8);
+    mbar_init(&sh.r_ready, 4);
+    mbar_init(&sh.u_ready, 4);
+    mbar_init(&sh.w_ready, 4);
+    mbar_init(&sh.o_free, 4);
+    mbar_init(&sh.x_done, 1);
+    mbar_init(&sh.u_done, 1);
+    mbar_init(&sh.d_done, 1);
+    mbar_init(&sh.o_done, 1);
+    fence_mbar_init();
+    sh.abort = 0;
+    sh.odd_chunk = sh.v_odd[0] = sh.v_odd[1] = -1;
+  }
+  if (warp == 8) tmem_alloc(&sh.tmem, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tm = sh.tmem;
+  volatile int *const abort_flag = &sh.abort;
+  auto wait = [&](uint64_t *bar, uint32_t parity) {  // the whole warp, and gives up as a whole
+    bool ok = mbar_try_wait(bar, parity);
+    if (!ok) {
+      const uint64_t start = global_ns();
+      while (!(ok = mbar_try_wait(bar, parity))) {
+        if (*abort_flag) break;
+        if (global_ns() - start > QG_WAIT_NS) {
+          *abort_flag = 1;
+          atomicOr(&g_qg_status_delta_chunk, QG_STATUS_BIT_TIMEOUT);
+          break;
+        }
+      }
+    }
+    return __all_sync(0xFFFFFFFFu, ok);
+  };
+  auto factors = [&](int c) { return reinterpret_cast<const Factors *>(ring + (c % kTcStages) * kStage + Tiles<DK>::kKQAll + 2 * kBlock); };
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTcRegsRest));
+    if (warp == 8) {
+      const uint32_t el = elect_lane();
+      auto ask = [&](int c) {
+        if (el) {
+          unsigned char *dst = ring + (c % kTcStages) * kStage;
+          uint64_t *bar = &sh.full[c % kTcStages];
+          mbar_arrive_expect_tx(bar, Tiles<DK>::kKQAll + kTA);
+          bulk_g2s(dst, a.kq + (static_cast<size_t>(slot0 + c) * a.d.Hk + hk) * Tiles<DK>::kKQAll, Tiles<DK>::kKQAll, bar);
+          bulk_g2s(dst + Tiles<DK>::kKQAll, a.ta + (static_cast<size_t>(slot0 + c) * a.d.Hv + h) * kTA, kTA, bar);
+        }
+        __syncwarp();
+      };
+      if (el) asm volatile("fence.proxy.async;" ::: "memory");  // the tiles were written by plain stores
+      __syncwarp();
+      int asked = min(kTcStages, chunks);
+      for (int c = 0; c < asked; ++c) ask(c);
+      constexpr uint32_t id32 = make_idesc16(128, 32, false, false), idk = make_idesc16(128, DK, false, true);
+      // D (+)= (A hi + A lo) (B hi + B lo): the small products first
+      auto product = [&](uint32_t d, uint32_t ta_hi, uint32_t ta_lo, auto desc, uint32_t id, int steps) {
+        for (int term = 0; term < 3; ++term)
+#pragma unroll 1
+          for (int ks = 0; ks < steps; ++ks)
+            tc_mma_ta_el(el, d, (term == 0 ? ta_lo : ta_hi) + 8 * ks, desc(term == 1, ks), id, term || ks);
+      };
+      uint32_t n_r = 0, n_o = 0;  // phases of r_ready (u_ready, w_ready) and of o_free
+      bool before_odd = true;     // no output to be read of a chunk before
+      bool ok = true;
+      for (int c = 0; c < chunks && ok; ++c) {
+        const int st = c % kTcStages;
+        ok = wait(&sh.s_ready, c & 1) && wait(&sh.full[st], (c / kTcStages) & 1);
+        if (!ok) break;
+        const uint32_t kt = smem_u32(ring + st * kStage), tt = kt + Tiles<DK>::kKQAll;
+        auto k_rows = [&](uint32_t tile) {
+          return [=](bool lo, int ks) { return sw128_desc(tile + (lo ? KQ : 0) + (ks >> 2) * kBlock + (ks & 3) * 32); };
+        };
+        auto square = [&](uint32_t tile) {
+          return [=](bool lo, int ks) { return sw128_desc(tile + (lo ? 64 : 0) + ks * 32); };
+        };
+        const bool odd = factors(c)->odd || *reinterpret_cast<volatile int *>(&sh.v_odd[c & 1]) == c;
+        tc_fence_after();
+        if (!odd) {
+          product(tm + TX, tm + TS, tm + TS + DK / 2, k_rows(kt), id32, DK / 16);
+          tc_commit_el(el, &sh.x_done);
+        } else if (el) {
+          sh.odd_chunk = c;
+          __threadfence_block();
+          mbar_arrive(&sh.x_done);
+          mbar_arrive(&sh.d_done);
+        }
+        __syncwarp();
+        if (!before_odd) {
+          if (!(ok = wait(&sh.o_free, n_o++ & 1))) break;
+          tc_fence_after();
+        }
+        // everyone has left the chunk before the last: its stage is free
+        if (c > 1 && asked < chunks) ask(asked++);
+        before_odd = odd;
+        if (odd) continue;
+        product(tm + TO, tm + TS, tm + TS + DK / 2, k_rows(kt + 2 * KQ), id32, DK / 16);
+        if (!(ok = wait(&sh.r_ready, n_r & 1))) break;
+        tc_fence_after();
+        product(tm + TU, tm + TR, tm + TR + 16, square(tt), id32, 2);
+        tc_commit_el(el, &sh.u_done);
+        if (!(ok = wait(&sh.w_ready, n_r & 1))) break;
+        tc_fence_after();
+        product(tm + TD, tm + TW, tm + TW + 16,
+                [=](bool lo, int ks) { return sw128_desc_mn(kt + (lo ? KQ : 0) + ks * 16 * 128, kBlock); }, idk, 2);
+        tc_commit_el(el, &sh.d_done);
+        if (!(ok = wait(&sh.u_ready, n_r & 1))) break;
+        tc_fence_after();
+        product(tm + TO2, tm + TUA, tm + TUA + 16, square(tt + kBlock), id32, 2);
+        tc_commit_el(el, &sh.o_done);
+        ++n_r;
+      }
+      if (!ok)  // copies still under way land before the CTA ends
+        for (int c = max(0, asked - kTcStages); c < asked; ++c) cleanup_wait(&sh.full[c % kTcStages], (c / kTcStages) & 1);
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTcRegsWork));
+    const int group = warp >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = tm + (static_cast<uint32_t>(warp & 3) << 21);  // this warp's lanes of tensor memory
+    const int d0 = h * a.d.Dv + part * 128 + row;
+    const bool teller = tid == 0 && part == 0 && h == 0;
+    float s[HK];  // rows group * HK and on of column d0
+    const long long state_at = (static_cast<long long>(h) * DK + group * HK) * a.d.Dv + part * 128 + row;
+    {
+      const int in = a.d.state_in ? __ldg(a.d.state_in + b) : -1;
+      if (teller && (in < -1 || in >= a.d.n_slots)) atomicOr(&g_qg_status_delta_chunk, QG_STATUS_BIT_ID);
+      const bool have = in >= 0 && in < a.d.n_slots;
+      const float *p = a.d.states + (have ? in : 0) * a.d.slot_stride + state_at;
+#pragma unroll
+      for (int i = 0; i < HK; ++i) s[i] = have ? p[static_cast<long long>(i) * a.d.Dv] : 0.f;
+    }
+    const float *vp = a.d.v + static_cast<long long>(t00) * a.d.v_stride + d0;
+    float *op = a.d.out + static_cast<long long>(t00) * a.d.out_stride + d0;
+    float v[C];
+    auto load_v = [&](int c) {
+      const float *p = vp + static_cast<long long>(c) * C * a.d.v_stride;
+      if ((c + 1) * C <= n) {
+#pragma unroll
+        for (int j = 0; j < C; ++j, p += a.d.v_stride) v[j] = __ldg(p);
+      } else {
+#pragma unroll
+        for (int j = 0; j < C; ++j, p += a.d.v_stride) v[j] = c * C + j < n ? __ldg(p) : 0.f;
+      }
+    };
+    // w (32 values) in two terms to 16 + 16 columns of tensor memory; returns the scale
+    auto put = [&](auto kind, const float (&w)[C], uint32_t col) {
+      float m4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int j = 0; j < C; ++j) m4[j & 3] = fmaxf(m4[j & 3], fabsf(w[j]));
+      float sc, inv;
+      row_scale(mag(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]))), sc, inv);
+      uint32_t hi[16], lo[16];
+#pragma unroll
+      for (int j = 0; j < C; j += 2) {
+        if constexpr (decltype(kind)::value) split2_each(w[j], w[j + 1], inv, hi[j / 2], lo[j / 2]);
+        else split2(w[j], w[j + 1], inv, hi[j / 2], lo[j / 2]);
+      }
+      tmem_st16(lanes + col, hi);
+      tmem_st16(lanes + col + 16, lo);
+      return sc;
+    };
+    using Each = std::true_type;    // rows of tokens
+    using Whole = std::false_type;  // rows that are summed as a whole
+    auto tell = [&](uint64_t *bar) {  // what this warp has put into, or taken from, tensor memory
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
+    if (group == 0) load_v(0);
+    float scale_s = 1.f, scale_before = 1.f;
+    uint32_t n_u = 0;           // phases of u_done and o_done
+    bool pending = false;       // group 1: outputs of the chunk before wait to be written
+    auto outputs = [&](int c, float ss) {  // group 1; ss: the state's scale then
+      if (!wait(&sh.o_done, (n_u - 1) & 1)) return false;
+      tc_fence_after();
+      const Factors *f = factors(c);
+      const float su = sh.scale_u[row];
+      float *p = op + static_cast<long long>(c) * C * a.d.out_stride;
+      const int left = n - c * C;
+      float x[32], y[32];
+      tmem_ld32_nowait(lanes + TO, x);
+      tmem_ld32_nowait(lanes + TO2, y);
+      tmem_ld_wait(x);
+      tmem_ld_wait(y);
+      tell(&sh.o_free);
+#pragma unroll
+      for (int j = 0; j < C; j += 4) {
+        const float4 fq = *reinterpret_cast<const float4 *>(f->fq + j), sa = *reinterpret_cast<const float4 *>(f->sa + j);
+        const float o[4] = {fmaf(fq.x * ss, x[j], sa.x * su * y[j]), fmaf(fq.y * ss, x[j + 1], sa.y * su * y[j + 1]),
+                            fmaf(fq.z * ss, x[j + 2], sa.z * su * y[j + 2]),
+                            fmaf(fq.w * ss, x[j + 3], sa.w * su * y[j + 3])};
+#pragma unroll
+        for (int e = 0; e < 4; ++e, p += a.d.out_stride)
+          if (j + e < left) *p = o[e];
+      }
+      return true;
+    };
+
+    int c = 0;
+    for (; c < chunks; ++c) {
+      // ---- the state in two terms
+      {
+        float m4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < HK; ++i) m4[i & 3] = fmaxf(m4[i & 3], fabsf(s[i]));
+        const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        sh.smax[group][row] = m;
+        if (group == 0) {  // the chunk's values have arrived
+          uint32_t big = 0;
+#pragma unroll
+          for (int j = 0; j < C; ++j) big = max(big, mag(v[j]));
+          if (big >= kInfBits) sh.v_odd[c & 1] = c;
+        }
+        named_bar_sync(1, 256);
+        scale_before = scale_s;
+        float inv;
+        row_scale(mag(fmaxf(m, sh.smax[group ^ 1][row])), scale_s, inv);
+#pragma unroll
+        for (int i = 0; i < HK; i += 32) {
+          uint32_t hi[16], lo[16];
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) split2(s[i + j], s[i + j + 1], inv, hi[j / 2], lo[j / 2]);
+          tmem_st16(lanes + TS + (group * HK + i) / 2, hi);
+          tmem_st16(lanes + TS + DK / 2 + (group * HK + i) / 2, lo);
+        }
+        tmem_st_wait();
+        tell(&sh.s_ready);
+      }
+      const Factors *f = factors(c);
+      bool odd;
+      if (group == 0) {
+        if (!wait(&sh.x_done, c & 1) || !wait(&sh.full[c % kTcStages], (c / kTcStages) & 1)) break;
+        odd = *reinterpret_cast<volatile int *>(&sh.odd_chunk) == c;
+        if (!odd) {
+          tc_fence_after();
+          float x[C];
+          tmem_ld32_nowait(lanes + TX, x);
+          tmem_ld_wait(x);
+#pragma unroll
+          for (int j = 0; j < C; j += 4) {
+            const float4 fk = *reinterpret_cast<const float4 *>(f->fk + j);
+            x[j] = fmaf(-fk.x * scale_s, x[j], v[j]);
+            x[j + 1] = fmaf(-fk.y * scale_s, x[j + 1], v[j + 1]);
+            x[j + 2] = fmaf(-fk.z * scale_s, x[j + 2], v[j + 2]);
+            x[j + 3] = fmaf(-fk.w * scale_s, x[j + 3], v[j + 3]);
+          }
+          const float sr = put(Each{}, x, TR);
+          tmem_st_wait();
+          tell(&sh.r_ready);
+          if (c + 1 < chunks) load_v(c + 1);
+          if (!wait(&sh.u_done, n_u & 1)) break;
+          tc_fence_after();
+          tmem_ld32_nowait(lanes + TU, x);
+          tmem_ld_wait(x);
+          float w[C];
+#pragma unroll
+          for (int j = 0; j < C; j += 4) {
+            const float4 st = *reinterpret_cast<const float4 *>(f->st + j), wk = *reinterpret_cast<const float4 *>(f->wk + j);
+            x[j] *= st.x * sr;
+            x[j + 1] *= st.y * sr;
+            x[j + 2] *= st.z * sr;
+            x[j + 3] *= st.w * sr;
+            w[j] = x[j] * wk.x;
+            w[j + 1] = x[j + 1] * wk.y;
+            w[j + 2] = x[j + 2] * wk.z;
+            w[j + 3] = x[j + 3] * wk.w;
+          }
+          sh.scale_w[row] = put(Whole{}, w, TW);
+          tmem_st_wait();
+          tell(&sh.w_ready);
+          sh.scale_u[row] = put(Each{}, x, TUA);
+          tmem_st_wait();
+          tell(&sh.u_ready);
+          ++n_u;
+        }
+      } else if (pending) {
+        if (!outputs(c - 1, scale_before)) break;
+        pending = false;
+      }
+      if (!wait(&sh.d_done, c & 1) || !wait(&sh.full[c % kTcStages], (c / kTcStages) & 1)) break;
+      odd = *reinterpret_cast<volatile int *>(&sh.odd_chunk) == c;
+      if (!odd) {
+        tc_fence_after();
+        const float dec = f->dec, sw = *reinterpret_cast<volatile float *>(&sh.scale_w[row]);
+#pragma unroll
+        for (int i = 0; i < HK; i += 32) {
+          float x[32];
+          tmem_ld32_nowait(lanes + TD + group * HK + i, x);
+          tmem_ld_wait(x);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) s[i + j] = fmaf(sw, x[j], dec * s[i + j]);
+        }
+        tc_fence_before();
+        if (group == 1) {
+          pending = true;
+          ++n_u;
+        }
+        continue;
+      }
+      // ---- token by token: an infinite or NaN value must not reach an earlier one
+      const int len = min(C, n - c * C);
+      const unsigned char *tile = ring + (c % kTcStages) * kStage;
+      for (int j = 0; j < len; ++j) {
+        const float al = f->alpha[j], be = f->beta[j], sk = f->sk[j], sq = f->sq[j];
+        auto pair = [&](int i, float2 &k, float2 &q) {  // rows i and i + 1 of this thread's half
+          const uint32_t off = kq_at(j, (group * HK + i) >> 3) + (i & 7) * 2;
+          const uint32_t kh = *reinterpret_cast<const uint32_t *>(tile + off);
+          const uint32_t kl = *reinterpret_cast<const uint32_t *>(tile + KQ + off);
+          const uint32_t qh = *reinterpret_cast<const uint32_t *>(tile + 2 * KQ + off);
+          const uint32_t ql = *reinterpret_cast<const uint32_t *>(tile + 3 * KQ + off);
+          k = make_float2(sk * (lo16<false>(kh) + lo16<false>(kl)), sk * (hi16<false>(kh) + hi16<false>(kl)));
+          q = make_float2(sq * (lo16<false>(qh) + lo16<false>(ql)), sq * (hi16<false>(qh) + hi16<false>(ql)));
+        };
+        float x = 0.f, y = 0.f, z = 0.f;
+#pragma unroll
+        for (int i = 0; i < HK; i += 2) {
+          float2 k, q;
+          pair(i, k, q);
+          x = fmaf(s[i], k.x, fmaf(s[i + 1], k.y, x));
+          y = fmaf(s[i], q.x, fmaf(s[i + 1], q.y, y));
+          z = fmaf(k.x, q.x, fmaf(k.y, q.y, z));
+        }
+        sh.ex[j & 1][group][row] = make_float4(x, y, z, 0.f);
+        named_bar_sync(1, 256);
+        const float4 other = sh.ex[j & 1][group ^ 1][row];
+        const long long t = static_cast<long long>(c) * C + j;
+        const float u = be * (__ldg(vp + t * a.d.v_stride) - al * (x + other.x));
+        if (group == 0) op[t * a.d.out_stride] = fmaf(z + other.z, u, al * (y + other.y));
+#pragma unroll
+        for (int i = 0; i < HK; i += 2) {
+          float2 k, q;
+          pair(i, k, q);
+          s[i] = fmaf(k.x, u, al * s[i]);
+          s[i + 1] = fmaf(k.y, u, al * s[i + 1]);
+        }
+      }
+      if (group == 0 && c + 1 < chunks) load_v(c + 1);
+    }
+    if (c == chunks && group == 1 && pending) outputs(chunks - 1, scale_s);
+    if (c == chunks && a.d.state_out) {
+      const int to = __ldg(a.d.state_out + b);
+      if (to >= 0 && to < a.d.n_slots) {
+        float *p = a.d.states + to * a.d.slot_stride + state_at;
+#pragma unroll
+        for (int i = 0; i < HK; ++i) p[static_cast<long long>(i) * a.d.Dv] = s[i];
+      } else if (to != -1 && teller) {
+        atomicOr(&g_qg_status_delta_chunk, QG_STATUS_BIT_ID);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 8) tmem_dealloc(sh.tmem, 512);
+}
+
 template <int DK, int W, int NST>
 cudaError_t walk(const ChunkArgs &a, cudaStream_t s) {
   constexpr int smem = WalkSmem<DK, W, NST>::kBytes;
@@ -738,7 +1174,12 @@ cudaError_t both(const ChunkArgs &a, cudaStream_t s) {
   if (!qg::set_smem_attr(reinterpret_cast<const void *>(delta_prep_kernel<DK>), smem)) return cudaErrorInvalidValue;
   cudaError_t e = qg::launch_pdl(delta_prep_kernel<DK>, dim3(static_cast<unsigned>(a.slots) * a.d.Hk), dim3(kPrepWarps * 32), smem, s, a);
   if (e != cudaSuccess) return e;
-  return a.d.Dv % 128 == 0 ? walk<DK, 8, 3>(a, s) : a.d.Dv % 64 == 0 ? walk<DK, 4, 3>(a, s) : walk<DK, 2, 3>(a, s);
+  if (a.d.Dv % 128 == 0) {
+    constexpr int tc = TcSmem<DK>::kBytes;
+    if (!qg::set_smem_attr(reinterpret_cast<const void *>(delta_walk_tc_kernel<DK>), tc)) return cudaErrorInvalidValue;
+    return qg::launch_pdl(delta_walk_tc_kernel<DK>, dim3(static_cast<unsigned>(a.d.B) * a.d.Hv * (a.d.Dv / 128)), dim3(kTcThreads), tc, s, a);
+  }
+  return a.d.Dv % 64 == 0 ? walk<DK, 4, 2>(a, s) : walk<DK, 2, 2>(a, s);
 }
 
 size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
