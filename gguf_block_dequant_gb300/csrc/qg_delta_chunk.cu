@@ -32,15 +32,15 @@ static_assert(C == 32, "a lane per token");
 
 // ---- the workspace ------------------------------------------------------------------------------
 // Sequence b's chunks have the numbers q_start[b] / 32 + b, and on: they rise, and ceil(n / 32) of them fit
-// before the next sequence's.  Per (chunk, key head): K hi, K lo, Q hi, Q lo, each as DK / 64 blocks of [32][64] f16.  Per
-// (chunk, value head): T and A, [32][32 hi, 32 lo] f16 each, and the factors below.  So every row of a block is 128 bytes, and
+// before the next sequence's.  Per (chunk, key head): DK / 64 blocks of hi terms, then those of lo terms, each [32 rows of K, 32
+// of Q][64] f16.  Per (chunk, value head): T and A, [32][32 hi, 32 lo] f16 each, and the factors below.  So every row of a block is 128 bytes, and
 // its eight 16-byte pieces are exchanged by the row's low three bits: the 128-byte swizzle of the tensor cores' operands, and
 // free of bank conflicts for ldmatrix, turned or not.
-constexpr int kBlock = C * 128;  // bytes of a block
+constexpr int kBlock = C * 128;  // bytes of 32 rows of a block; where Q is in one of K and Q
 template <int DK>
 struct Tiles {
-  static constexpr int kKQ = DK / 64 * kBlock;       // bytes of one key or query tile
-  static constexpr int kKQAll = 4 * kKQ;
+  static constexpr int kLo = DK / 64 * 2 * kBlock;  // from the hi terms to the lo terms
+  static constexpr int kKQAll = 2 * kLo;
 };
 struct Factors {
   float fk[C];     // e^{G_j} sk_j: what K S0 is multiplied by
@@ -58,8 +58,8 @@ static_assert(kTA % 16 == 0, "bulk copies");
 
 // byte offset of piece `piece` (16 bytes) of a row of a block
 QG_DEVICE uint32_t at_piece(int row, int piece) { return row * 128 + ((piece ^ (row & 7)) << 4); }
-// the same in a tile of several blocks
-QG_DEVICE uint32_t kq_at(int row, int piece) { return (piece >> 3) * kBlock + at_piece(row, piece & 7); }
+// the same in the blocks of K and Q
+QG_DEVICE uint32_t kq_at(int row, int piece) { return (piece >> 3) * 2 * kBlock + at_piece(row, piece & 7); }
 
 // the power of two that brings magnitude bits m to [2^7, 2^8), and its inverse; 1 for infinities and NaN
 QG_DEVICE void row_scale(uint32_t m, float &s, float &inv) {
@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 5) delta_prep_kernel(const Ch
   __shared__ float scale_k[C], scale_q[C];
   __shared__ float2 gsum[kPrepWarps][C];
   __shared__ int bad_rows;
-  constexpr int KQ = Tiles<DK>::kKQ;
+  constexpr int LO = Tiles<DK>::kLo;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int slot = static_cast<int>(blockIdx.x) / a.d.Hk, hk = static_cast<int>(blockIdx.x) % a.d.Hk;
   pdl_wait();
@@ -201,40 +201,58 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 5) delta_prep_kernel(const Ch
     return lane < len && it < 2 * group ? qg::delta_gates(a.d, t0 + lane, head_of(it)) : make_float2(0.f, 0.f);
   };
   float2 gates = gates_of(warp);
+  // norms and scales: lane l works for row l / 2 of the warp's sixteen (8 of K, 8 of Q)
+  static_assert(R == 8, "sixteen rows a warp");
+  float ss[2 * R];
+  uint32_t big = 0;
+#pragma unroll
+  for (int z = 0; z < 2; ++z)
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float t = 0.f;
+      uint32_t m = 0;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        t = fmaf(x[z][r][e], x[z][r][e], t);
+        m = max(m, mag(x[z][r][e]));
+      }
+      ss[z * R + r] = t;
+      m = __reduce_max_sync(0xFFFFFFFFu, m);
+      if ((lane >> 1) == z * R + r) big = m;
+    }
+  reduce_scatter(ss, lane);  // ss[0]: the sum of row lane / 2
+  const int mine = lane >> 1;
+  float f = mine >= R ? a.d.scale : 1.f;
+  if (a.d.l2norm && warp * R + (mine & (R - 1)) < len) f *= 1.f / sqrtf(ss[0] + a.d.eps);
+  big = mag(__uint_as_float(big) * f);  // the largest magnitude of the products with f: rounding keeps the order
+  float row_s, row_inv;
+  row_scale(big, row_s, row_inv);
+  float to = f * row_inv;  // a power of two beside f: one rounding
+  if (big >= kInfBits) {
+    bad_rows = 1;
+  } else if (!(fabsf(to) < INFINITY)) {  // rows next to nothing, raised by the norm (zeros, for one)
+    row_s = 0x1p-60f;
+    to = f * 0x1p60f;
+  }
+  if ((lane & 1) == 0) (mine >= R ? scale_q : scale_k)[warp * R + (mine & (R - 1))] = row_s;
 #pragma unroll
   for (int z = 0; z < 2; ++z)
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const int i = warp * R + r;
-      float ss = 0.f;
-      uint32_t m = 0;
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        ss = fmaf(x[z][r][e], x[z][r][e], ss);
-        m = max(m, mag(x[z][r][e]));
-      }
-      float f = z ? a.d.scale : 1.f;
-      if (a.d.l2norm) {
-        ss = warp_sum(ss) + a.d.eps;
-        if (i < len) f *= 1.f / sqrtf(ss);
-      }
-      // the largest magnitude of the products with f: rounding keeps the order
-      m = mag(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, m)) * f);
-      float s, inv;
-      row_scale(m, s, inv);
-      unsigned char *t = tile + z * 2 * KQ;
+      const float w = __shfl_sync(0xFFFFFFFFu, to, 2 * (z * R + r));
+      unsigned char *t = tile + z * kBlock;
       const int byte = lane * E * 2;  // of the row
       const uint32_t at = kq_at(i, byte >> 4) + (byte & 15);
+      uint32_t h[E / 2], l[E / 2];
 #pragma unroll
-      for (int e = 0; e < E; e += 2) {
-        uint32_t h, l;
-        split2(x[z][r][e] * f, x[z][r][e + 1] * f, inv, h, l);
-        *reinterpret_cast<uint32_t *>(t + at + 2 * e) = h;
-        *reinterpret_cast<uint32_t *>(t + KQ + at + 2 * e) = l;
-      }
-      if (lane == 0) {
-        (z ? scale_q : scale_k)[i] = s;
-        if (m >= kInfBits) bad_rows = 1;
+      for (int e = 0; e < E; e += 2) split2(x[z][r][e], x[z][r][e + 1], w, h[e / 2], l[e / 2]);
+      if constexpr (E == 4) {
+        *reinterpret_cast<uint2 *>(t + at) = make_uint2(h[0], h[1]);
+        *reinterpret_cast<uint2 *>(t + LO + at) = make_uint2(l[0], l[1]);
+      } else {
+        *reinterpret_cast<uint32_t *>(t + at) = h[0];
+        *reinterpret_cast<uint32_t *>(t + LO + at) = l[0];
       }
     }
   __syncthreads();
@@ -245,7 +263,7 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 5) delta_prep_kernel(const Ch
   }
   // products: warps 0, 1 keys with keys, 2, 3 queries with keys; 16 rows each
   {
-    const uint32_t k0 = smem_u32(tile), rows = k0 + (warp >= 2 ? 2 * KQ : 0);
+    const uint32_t k0 = smem_u32(tile), rows = k0 + (warp >= 2 ? kBlock : 0);
     const int r0 = (warp & 1) * 16;
     float c[4][4];
 #pragma unroll
@@ -253,13 +271,13 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 5) delta_prep_kernel(const Ch
       uint32_t ah[4], al[4];
       const uint32_t at = kq_at(r0 + (lane & 15), 2 * ks + (lane >> 4));
       ldsm4(ah, rows + at);
-      ldsm4(al, rows + KQ + at);
+      ldsm4(al, rows + LO + at);
       uint32_t bh[4][2], bl[4][2];
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
         const uint32_t bt = kq_at(16 * p + (lane & 7) + ((lane >> 4) << 3), 2 * ks + ((lane >> 3) & 1));
         load2<false>(bh[2 * p], bh[2 * p + 1], k0 + bt);
-        load2<false>(bl[2 * p], bl[2 * p + 1], k0 + KQ + bt);
+        load2<false>(bl[2 * p], bl[2 * p + 1], k0 + LO + bt);
       }
       if (ks == 0) mma3<true>(c, ah, al, bh, bl);
       else mma3<false>(c, ah, al, bh, bl);
@@ -386,7 +404,7 @@ __global__ void __launch_bounds__(W * 32) delta_walk_kernel(const ChunkArgs a) {
   extern __shared__ __align__(1024) unsigned char ring[];
   __shared__ uint64_t full[NST];
   __shared__ int left[NST];  // warps that are done with a stage's contents
-  constexpr int KQ = Tiles<DK>::kKQ, kStage = WalkSmem<DK, W, NST>::kStage;
+  constexpr int LO = Tiles<DK>::kLo, kStage = WalkSmem<DK, W, NST>::kStage;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int parts = a.d.Dv / (16 * W);
   const int part = static_cast<int>(blockIdx.x) % parts, bh = static_cast<int>(blockIdx.x) / parts;
@@ -505,11 +523,11 @@ __global__ void __launch_bounds__(W * 32) delta_walk_kernel(const ChunkArgs a) {
         uint32_t bh[8][2], bl[8][2];
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
-          const uint32_t at = ((kt + off_b) ^ ((ks & 3) << 5)) + (ks >> 2) * kBlock + p * 16 * 128;
+          const uint32_t at = ((kt + off_b) ^ ((ks & 3) << 5)) + (ks >> 2) * 2 * kBlock + p * 16 * 128;
           load2<false>(bh[2 * p], bh[2 * p + 1], at);
-          load2<false>(bl[2 * p], bl[2 * p + 1], at + KQ);
-          load2<false>(bh[4 + 2 * p], bh[5 + 2 * p], at + 2 * KQ);
-          load2<false>(bl[4 + 2 * p], bl[5 + 2 * p], at + 3 * KQ);
+          load2<false>(bl[2 * p], bl[2 * p + 1], at + LO);
+          load2<false>(bh[4 + 2 * p], bh[5 + 2 * p], at + kBlock);
+          load2<false>(bl[4 + 2 * p], bl[5 + 2 * p], at + kBlock + LO);
         }
         if (ks == 0) mma3<true>(x, ah, al, bh, bl);
         else mma3<false>(x, ah, al, bh, bl);
@@ -639,9 +657,9 @@ __global__ void __launch_bounds__(W * 32) delta_walk_kernel(const ChunkArgs a) {
           uint32_t bh[4][2], bl[4][2];
 #pragma unroll
           for (int p = 0; p < 2; ++p) {
-            const uint32_t at = ((kt + off_t) ^ (((c4 + 2 * p) & 7) << 4)) + (c4 >> 3) * kBlock + ks * 16 * 128;
+            const uint32_t at = ((kt + off_t) ^ (((c4 + 2 * p) & 7) << 4)) + (c4 >> 3) * 2 * kBlock + ks * 16 * 128;
             load2<true>(bh[2 * p], bh[2 * p + 1], at);
-            load2<true>(bl[2 * p], bl[2 * p + 1], at + KQ);
+            load2<true>(bl[2 * p], bl[2 * p + 1], at + LO);
           }
           if (ks == 0) mma3<true>(w, ah[ks], al[ks], bh, bl);
           else mma3<false>(w, ah[ks], al[ks], bh, bl);
@@ -664,9 +682,9 @@ __global__ void __launch_bounds__(W * 32) delta_walk_kernel(const ChunkArgs a) {
         auto both = [&](int ct, float2 &k, float2 &q) {
           const uint32_t off = kq_at(j, ct) + 4 * q4;
           const uint32_t kh = *reinterpret_cast<const uint32_t *>(tile + off);
-          const uint32_t kl = *reinterpret_cast<const uint32_t *>(tile + KQ + off);
-          const uint32_t qh = *reinterpret_cast<const uint32_t *>(tile + 2 * KQ + off);
-          const uint32_t ql = *reinterpret_cast<const uint32_t *>(tile + 3 * KQ + off);
+          const uint32_t kl = *reinterpret_cast<const uint32_t *>(tile + LO + off);
+          const uint32_t qh = *reinterpret_cast<const uint32_t *>(tile + kBlock + off);
+          const uint32_t ql = *reinterpret_cast<const uint32_t *>(tile + kBlock + LO + off);
           k = make_float2(sk * (lo16<false>(kh) + lo16<false>(kl)), sk * (hi16<false>(kh) + hi16<false>(kl)));
           q = make_float2(sq * (lo16<false>(qh) + lo16<false>(ql)), sq * (hi16<false>(qh) + hi16<false>(ql)));
         };
@@ -740,40 +758,61 @@ __global__ void __launch_bounds__(W * 32) delta_walk_kernel(const ChunkArgs a) {
 // a column, half of its rows each), left operands go to tensor memory as f16 pairs (hi in one range of columns, lo in
 // another), right operands are the tiles in shared memory, with K read as it lies for S0^T K^T and turned for U^T K.
 //   both groups  S^T in two terms; S^T <- e^{G_C} S^T + D
-//   group 0      R = V - ..., U, and U with the decays to the chunk's end, each in two terms; the next chunk's values
-//   group 1      the outputs of the chunk before
-//   control      bulk copies into the ring, and the products X = S^T K^T, O = S^T Q^T, U = R T^T, D = U K, O2 = U A^T
-// Every wait ends with its phase or after QG_WAIT_NS, which makes the CTA give up.
-constexpr int kTcThreads = 384;                    // two groups of four warps, control and three idle warps
+//   group 0      R = V - ..., U, and U with the decays to the chunk's end, each in two terms
+//   group 1      the outputs of the chunk before; whether the next chunk's values are all finite
+//   a producer   bulk copies into the ring (a row of values each lane: that would hold control up by 1700 cycles)
+//   control      the products X = S^T K^T, O = S^T Q^T, U = R T^T, D = U K, O2 = U A^T
+// Every wait ends with its phase or after kTcWaitCycles, which makes the CTA give up.
+constexpr int kTcThreads = 384;                    // two groups of four warps, control, the producer and two idle warps
 constexpr int kTcRegs = 168, kTcRegsWork = 208, kTcRegsRest = 88;
 static_assert(2 * kTcRegsWork + kTcRegsRest <= 3 * kTcRegs, "the warpgroups' shares come from the launch's total");
-constexpr int kTcStages = 4;
+constexpr int kTcStages = 3;
+constexpr long long kTcWaitCycles = 1LL << 29;  // a quarter of a second: a wait is for microseconds
 constexpr int kOrder = 128;  // sequences that are put in order, longest first
 // columns of tensor memory
-enum { TX = 0, TO = 32, TU = 64, TO2 = 96, TD = 128, TS = 256, TR = 384, TUA = 416, TW = 448 };
+// X and O are in two places by the chunk's parity, since O is read while the next is made.  They are two products: 32 columns
+// take 41 cycles a step and 64 take 70, and only X is waited for.  R's pair makes way for U's, which is written once R's product is done.
+enum { TXO = 0, TU = 128, TO2 = 160, TD = 192, TS = 320, TR = 448, TUA = 448, TW = 480 };
 
 template <int DK>
 struct TcSmem {
-  static constexpr int kStage = (Tiles<DK>::kKQAll + kTA + 1023) / 1024 * 1024;
+  static constexpr int kV = Tiles<DK>::kKQAll + kTA;  // where a stage's values are: [32][128] f32
+  static constexpr int kStage = (kV + C * 512 + 1023) / 1024 * 1024;
   static constexpr int kBytes = kTcStages * kStage + 1024;
 };
 struct TcShared {
-  uint64_t full[kTcStages];
+  uint64_t full[kTcStages], empty[kTcStages];           // by the copies, and by control
   uint64_t s_ready, r_ready, u_ready, w_ready, o_free;  // by the working warps
   uint64_t x_done, u_done, d_done, o_done;              // by the tensor cores
   uint32_t tmem;
   int abort, seq;
   int odd_chunk, v_odd[2];  // the last chunk that goes token by token; chunks with such values, by their parity
   float smax[2][128];       // largest of a column's halves
-  float scale_w[128], scale_u[128];
-  float4 ex[2][2][128];     // token by token: partial products of the halves, by the token's parity
+  float scale_w[128], scale_u[2][128];
+  __align__(16) float4 ex[2][2][128];  // token by token: partial products of the halves, by the token's parity
 };
+
+// D = (A hi + A lo) (B hi + B lo) without lo lo, the small products first.  A: 8 columns of tensor memory a step; B: the
+// descriptor of its hi tile, lo LO bytes behind it; KROWS: the tile's rows are columns of the product, 16 elements of each
+// a step; TURNED: 16 rows a step.  Unrolled, with nothing but sums of constants between the instructions: a loop that
+// makes each descriptor took 70 cycles a product.
+enum { KROWS, TURNED };
+template <int KIND, int STEPS, int LO>
+QG_DEVICE void product(uint32_t el, uint32_t d, uint32_t a_hi, uint32_t a_lo, uint64_t b, uint32_t id) {
+#pragma unroll
+  for (int term = 0; term < 3; ++term)
+#pragma unroll
+    for (int ks = 0; ks < STEPS; ++ks) {
+      const int off = (KIND == TURNED ? ks * 16 * 128 : (ks >> 2) * 2 * kBlock + (ks & 3) * 32) + (term == 1 ? LO : 0);
+      tc_mma_ta_el(el, d, (term == 0 ? a_lo : a_hi) + 8 * ks, b + (off >> 4), id, term || ks);
+    }
+}
 
 template <int DK>
 __global__ void __launch_bounds__(kTcThreads, 1) delta_walk_tc_kernel(const ChunkArgs a) {
   extern __shared__ unsigned char ring_raw[];
   __shared__ TcShared sh;
-  constexpr int KQ = Tiles<DK>::kKQ, kStage = TcSmem<DK>::kStage;
+  constexpr int LO = Tiles<DK>::kLo, kStage = TcSmem<DK>::kStage;
   constexpr int HK = DK / 2;  // rows of the state a thread holds
   unsigned char *ring = ring_raw + ((1024u - (smem_u32(ring_raw) & 1023u)) & 1023u);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -803,7 +842,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) delta_walk_tc_kernel(const Chun
   if (slot0 + chunks > a.slots) return;
 
   if (tid == 0) {
-    for (int i = 0; i < kTcStages; ++i) mbar_init(&sh.full[i], 1);
+    for (int i = 0; i < kTcStages; ++i) {
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], 1);
+    }
     mbar_init(&sh.s_ready, 8);
     mbar_init(&sh.r_ready, 4);
     mbar_init(&sh.u_ready, 4);
@@ -826,10 +868,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) delta_walk_tc_kernel(const Chun
   auto wait = [&](uint64_t *bar, uint32_t parity) {  // the whole warp, and gives up as a whole
     bool ok = mbar_try_wait(bar, parity);
     if (!ok) {
-      const uint64_t start = global_ns();
+      const long long start = clock64();  // the SM's own clock: the global timer takes a microsecond to read
       while (!(ok = mbar_try_wait(bar, parity))) {
         if (*abort_flag) break;
-        if (global_ns() - start > QG_WAIT_NS) {
+        if (clock64() - start > kTcWaitCycles) {
           *abort_flag = 1;
           atomicOr(&g_qg_status_delta_chunk, QG_STATUS_BIT_TIMEOUT);
           break;
@@ -842,30 +884,35 @@ __global__ void __launch_bounds__(kTcThreads, 1) delta_walk_tc_kernel(const Chun
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTcRegsRest));
-    if (warp == 8) {
-      const uint32_t el = elect_lane();
-      auto ask = [&](int c) {
-        if (el) {
-          unsigned char *dst = ring + (c % kTcStages) * kStage;
-          uint64_t *bar = &sh.full[c % kTcStages];
-          mbar_arrive_expect_tx(bar, Tiles<DK>::kKQAll + kTA);
+    if (warp == 9) {
+      auto ask = [&](int c) {  // a lane asks for a token's values
+        unsigned char *dst = ring + (c % kTcStages) * kStage;
+        uint64_t *bar = &sh.full[c % kTcStages];
+        const int rows = min(C, n - c * C);
+        if (lane == 0) mbar_arrive_expect_tx(bar, Tiles<DK>::kKQAll + kTA + 512 * rows);
+        __syncwarp();
+        if (lane < rows)
+          bulk_g2s(dst + TcSmem<DK>::kV + 512 * lane,
+                   a.d.v + (t00 + static_cast<long long>(c) * C + lane) * a.d.v_stride + h * a.d.Dv + part * 128, 512, bar);
+        if (lane == 0) {
           bulk_g2s(dst, a.kq + (static_cast<size_t>(slot0 + c) * a.d.Hk + hk) * Tiles<DK>::kKQAll, Tiles<DK>::kKQAll, bar);
           bulk_g2s(dst + Tiles<DK>::kKQAll, a.ta + (static_cast<size_t>(slot0 + c) * a.d.Hv + h) * kTA, kTA, bar);
         }
         __syncwarp();
       };
-      if (el) asm volatile("fence.proxy.async;" ::: "memory");  // the tiles were written by plain stores
-      __syncwarp();
-      int asked = min(kTcStages, chunks);
-      for (int c = 0; c < asked; ++c) ask(c);
+      asm volatile("fence.proxy.async;" ::: "memory");  // the tiles were written by plain stores
+      int c = 0;
+      for (; c < chunks; ++c) {
+        if (c >= kTcStages && !wait(&sh.empty[c % kTcStages], (c / kTcStages - 1) & 1)) break;
+        ask(c);
+      }
+      if (c < chunks)  // copies still under way land before the CTA ends
+        for (int i = max(0, c - kTcStages); i < c; ++i) cleanup_wait(&sh.full[i % kTcStages], (i / kTcStages) & 1);
+    } else if (warp == 8) {
+      const uint32_t el = elect_lane();
       constexpr uint32_t id32 = make_idesc16(128, 32, false, false), idk = make_idesc16(128, DK, false, true);
-      // D (+)= (A hi + A lo) (B hi + B lo): the small products first
-      auto product = [&](uint32_t d, uint32_t ta_hi, uint32_t ta_lo, auto desc, uint32_t id, int steps) {
-        for (int term = 0; term < 3; ++term)
-#pragma unroll 1
-          for (int ks = 0; ks < steps; ++ks)
-            tc_mma_ta_el(el, d, (term == 0 ? ta_lo : ta_hi) + 8 * ks, desc(term == 1, ks), id, term || ks);
-      };
+      // what the right operands' descriptors say beside the address
+      const uint64_t rows0 = sw128_desc(0), turned0 = sw128_desc_mn(0, 2 * kBlock);
       uint32_t n_r = 0, n_o = 0;  // phases of r_ready (u_ready, w_ready) and of o_free
       bool before_odd = true;     // no output to be read of a chunk before
       bool ok = true;
@@ -874,17 +921,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) delta_walk_tc_kernel(const Chun
         ok = wait(&sh.s_ready, c & 1) && wait(&sh.full[st], (c / kTcStages) & 1);
         if (!ok) break;
         const uint32_t kt = smem_u32(ring + st * kStage), tt = kt + Tiles<DK>::kKQAll;
-        auto k_rows = [&](uint32_t tile) {
-          return [=](bool lo, int ks) { return sw128_desc(tile + (lo ? KQ : 0) + (ks >> 2) * kBlock + (ks & 3) * 32); };
-        };
-        auto square = [&](uint32_t tile) {
-          return [=](bool lo, int ks) { return sw128_desc(tile + (lo ? 64 : 0) + ks * 32); };
-        };
+        const uint64_t kd = rows0 + (kt >> 4), kturned = turned0 + (kt >> 4);
         const bool odd = factors(c)->odd || *reinterpret_cast<volatile int *>(&sh.v_odd[c & 1]) == c;
         tc_fence_after();
         if (!odd) {
-          product(tm + TX, tm + TS, tm + TS + DK / 2, k_rows(kt), id32, DK / 16);
+          product<KROWS, DK / 16, LO>(el, tm + TXO + 64 * (c & 1), tm + TS, tm + TS + DK / 2, kd, id32);
           tc_commit_el(el, &sh.x_done);
+          product<KROWS, DK / 16, LO>(el, tm + TXO + 64 * (c & 1) + 32, tm + TS, tm + TS + DK / 2, kd + (kBlock >> 4), id32);
         } else if (el) {
           sh.odd_chunk = c;
           __threadfence_block();
@@ -892,32 +935,30 @@ __global__ void __launch_bounds__(kTcThreads, 1) delta_walk_tc_kernel(const Chun
           mbar_arrive(&sh.d_done);
         }
         __syncwarp();
-        if (!before_odd) {
-          if (!(ok = wait(&sh.o_free, n_o++ & 1))) break;
-          tc_fence_after();
+        if (odd) {
+          if (!before_odd && !(ok = wait(&sh.o_free, n_o++ & 1))) break;
+          if (c > 0 && el) mbar_arrive(&sh.empty[(c - 1) % kTcStages]);
+          before_odd = true;
+          continue;
         }
-        // everyone has left the chunk before the last: its stage is free
-        if (c > 1 && asked < chunks) ask(asked++);
-        before_odd = odd;
-        if (odd) continue;
-        product(tm + TO, tm + TS, tm + TS + DK / 2, k_rows(kt + 2 * KQ), id32, DK / 16);
         if (!(ok = wait(&sh.r_ready, n_r & 1))) break;
         tc_fence_after();
-        product(tm + TU, tm + TR, tm + TR + 16, square(tt), id32, 2);
+        product<KROWS, 2, 64>(el, tm + TU, tm + TR, tm + TR + 16, rows0 + (tt >> 4), id32);
         tc_commit_el(el, &sh.u_done);
         if (!(ok = wait(&sh.w_ready, n_r & 1))) break;
         tc_fence_after();
-        product(tm + TD, tm + TW, tm + TW + 16,
-                [=](bool lo, int ks) { return sw128_desc_mn(kt + (lo ? KQ : 0) + ks * 16 * 128, kBlock); }, idk, 2);
+        product<TURNED, 2, LO>(el, tm + TD, tm + TW, tm + TW + 16, kturned, idk);
         tc_commit_el(el, &sh.d_done);
+        // everyone has left the chunk before, and its outputs have been read
+        if (!before_odd && !(ok = wait(&sh.o_free, n_o++ & 1))) break;
+        if (c > 0 && el) mbar_arrive(&sh.empty[(c - 1) % kTcStages]);
+        before_odd = false;
         if (!(ok = wait(&sh.u_ready, n_r & 1))) break;
         tc_fence_after();
-        product(tm + TO2, tm + TUA, tm + TUA + 16, square(tt + kBlock), id32, 2);
+        product<KROWS, 2, 64>(el, tm + TO2, tm + TUA, tm + TUA + 16, rows0 + ((tt + kBlock) >> 4), id32);
         tc_commit_el(el, &sh.o_done);
         ++n_r;
       }
-      if (!ok)  // copies still under way land before the CTA ends
-        for (int c = max(0, asked - kTcStages); c < asked; ++c) cleanup_wait(&sh.full[c % kTcStages], (c / kTcStages) & 1);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTcRegsWork));
@@ -937,16 +978,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) delta_walk_tc_kernel(const Chun
     }
     const float *vp = a.d.v + static_cast<long long>(t00) * a.d.v_stride + d0;
     float *op = a.d.out + static_cast<long long>(t00) * a.d.out_stride + d0;
-    float v[C];
-    auto load_v = [&](int c) {
-      const float *p = vp + static_cast<long long>(c) * C * a.d.v_stride;
-      if ((c + 1) * C <= n) {
-#pragma unroll
-        for (int j = 0; j < C; ++j, p += a.d.v_stride) v[j] = __ldg(p);
-      } else {
-#pragma unroll
-        for (int j = 0; j < C; ++j, p += a.d.v_stride) v[j] = c * C + j < n ? __ldg(p) : 0.f;
-      }
+    // a chunk's values of this column, 0 behind the last token.  They come with the tiles: loads of the working warps would
+    // be waited for together with the next barrier or tensor-memory load (4.3 microseconds a chunk)
+    auto value = [&](int c, int j) {
+      const float *p = reinterpret_cast<const float *>(ring + (c % kTcStages) * kStage + TcSmem<DK>::kV);
+      return c * C + j < n ? p[j * 128 + row] : 0.f;
     };
     // w (32 values) in two terms to 16 + 16 columns of tensor memory; returns the scale
     auto put = [&](auto kind, const float (&w)[C], uint32_t col) {
@@ -972,7 +1008,22 @@ __global__ void __launch_bounds__(kTcThreads, 1) delta_walk_tc_kernel(const Chun
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
     };
-    if (group == 0) load_v(0);
+    // whether a chunk's values are all finite, told with the state before that chunk
+    auto look_at_v = [&](int c) {
+      if (!wait(&sh.full[c % kTcStages], (c / kTcStages) & 1)) return;
+      uint32_t big = 0;
+#pragma unroll
+      for (int j = 0; j < C; ++j) big = max(big, mag(value(c, j)));
+      if (big >= kInfBits) sh.v_odd[c & 1] = c;
+    };
+    if (group == 1) look_at_v(0);
+    auto largest = [&] {
+      float m4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < HK; ++i) m4[i & 3] = fmaxf(m4[i & 3], fabsf(s[i]));
+      return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+    };
+    float m = largest();
     float scale_s = 1.f, scale_before = 1.f;
     uint32_t n_u = 0;           // phases of u_done and o_done
     bool pending = false;       // group 1: outputs of the chunk before wait to be written
@@ -980,25 +1031,28 @@ __global__ void __launch_bounds__(kTcThreads, 1) delta_walk_tc_kernel(const Chun
       if (!wait(&sh.o_done, (n_u - 1) & 1)) return false;
       tc_fence_after();
       const Factors *f = factors(c);
-      const float su = sh.scale_u[row];
+      const float su = sh.scale_u[c & 1][row];
       float *p = op + static_cast<long long>(c) * C * a.d.out_stride;
       const int left = n - c * C;
       float x[32], y[32];
-      tmem_ld32_nowait(lanes + TO, x);
+      tmem_ld32_nowait(lanes + TXO + 64 * (c & 1) + 32, x);
       tmem_ld32_nowait(lanes + TO2, y);
       tmem_ld_wait(x);
       tmem_ld_wait(y);
-      tell(&sh.o_free);
 #pragma unroll
       for (int j = 0; j < C; j += 4) {
         const float4 fq = *reinterpret_cast<const float4 *>(f->fq + j), sa = *reinterpret_cast<const float4 *>(f->sa + j);
-        const float o[4] = {fmaf(fq.x * ss, x[j], sa.x * su * y[j]), fmaf(fq.y * ss, x[j + 1], sa.y * su * y[j + 1]),
-                            fmaf(fq.z * ss, x[j + 2], sa.z * su * y[j + 2]),
-                            fmaf(fq.w * ss, x[j + 3], sa.w * su * y[j + 3])};
-#pragma unroll
-        for (int e = 0; e < 4; ++e, p += a.d.out_stride)
-          if (j + e < left) *p = o[e];
+        x[j] = fmaf(fq.x * ss, x[j], sa.x * su * y[j]);
+        x[j + 1] = fmaf(fq.y * ss, x[j + 1], sa.y * su * y[j + 1]);
+        x[j + 2] = fmaf(fq.z * ss, x[j + 2], sa.z * su * y[j + 2]);
+        x[j + 3] = fmaf(fq.w * ss, x[j + 3], sa.w * su * y[j + 3]);
       }
+#pragma unroll
+      for (int j = 0; j < C; ++j) asm volatile("" : "+f"(x[j]));  // the factors are read before the stage is given up
+      tell(&sh.o_free);
+#pragma unroll
+      for (int j = 0; j < C; ++j, p += a.d.out_stride)
+        if (j < left) *p = x[j];
       return true;
     };
 
@@ -1006,17 +1060,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) delta_walk_tc_kernel(const Chun
     for (; c < chunks; ++c) {
       // ---- the state in two terms
       {
-        float m4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < HK; ++i) m4[i & 3] = fmaxf(m4[i & 3], fabsf(s[i]));
-        const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
         sh.smax[group][row] = m;
-        if (group == 0) {  // the chunk's values have arrived
-          uint32_t big = 0;
-#pragma unroll
-          for (int j = 0; j < C; ++j) big = max(big, mag(v[j]));
-          if (big >= kInfBits) sh.v_odd[c & 1] = c;
-        }
         named_bar_sync(1, 256);
         scale_before = scale_s;
         float inv;
@@ -1035,12 +1079,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) delta_walk_tc_kernel(const Chun
       const Factors *f = factors(c);
       bool odd;
       if (group == 0) {
-        if (!wait(&sh.x_done, c & 1) || !wait(&sh.full[c % kTcStages], (c / kTcStages) & 1)) break;
+        if (!wait(&sh.full[c % kTcStages], (c / kTcStages) & 1)) break;
+        float v[C];
+#pragma unroll
+        for (int j = 0; j < C; ++j) v[j] = value(c, j);
+#pragma unroll
+        for (int j = 0; j < C; ++j) asm volatile("" : "+f"(v[j]));  // while the product runs
+        if (!wait(&sh.x_done, c & 1)) break;
         odd = *reinterpret_cast<volatile int *>(&sh.odd_chunk) == c;
         if (!odd) {
           tc_fence_after();
           float x[C];
-          tmem_ld32_nowait(lanes + TX, x);
+          tmem_ld32_nowait(lanes + TXO + 64 * (c & 1), x);
           tmem_ld_wait(x);
 #pragma unroll
           for (int j = 0; j < C; j += 4) {
@@ -1053,7 +1103,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) delta_walk_tc_kernel(const Chun
           const float sr = put(Each{}, x, TR);
           tmem_st_wait();
           tell(&sh.r_ready);
-          if (c + 1 < chunks) load_v(c + 1);
           if (!wait(&sh.u_done, n_u & 1)) break;
           tc_fence_after();
           tmem_ld32_nowait(lanes + TU, x);
@@ -1074,28 +1123,36 @@ __global__ void __launch_bounds__(kTcThreads, 1) delta_walk_tc_kernel(const Chun
           sh.scale_w[row] = put(Whole{}, w, TW);
           tmem_st_wait();
           tell(&sh.w_ready);
-          sh.scale_u[row] = put(Each{}, x, TUA);
+          sh.scale_u[c & 1][row] = put(Each{}, x, TUA);
           tmem_st_wait();
           tell(&sh.u_ready);
           ++n_u;
         }
-      } else if (pending) {
-        if (!outputs(c - 1, scale_before)) break;
+      } else {
+        if (pending && !outputs(c - 1, scale_before)) break;
         pending = false;
+        if (c + 1 < chunks) look_at_v(c + 1);
       }
       if (!wait(&sh.d_done, c & 1) || !wait(&sh.full[c % kTcStages], (c / kTcStages) & 1)) break;
       odd = *reinterpret_cast<volatile int *>(&sh.odd_chunk) == c;
       if (!odd) {
         tc_fence_after();
         const float dec = f->dec, sw = *reinterpret_cast<volatile float *>(&sh.scale_w[row]);
+        float m4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < HK; i += 32) {
           float x[32];
           tmem_ld32_nowait(lanes + TD + group * HK + i, x);
           tmem_ld_wait(x);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) s[i + j] = fmaf(sw, x[j], dec * s[i + j]);
+          for (int j = 0; j < 32; j += 2) {
+            const f2 y = fma2(mk2(sw, sw), mk2(x[j], x[j + 1]), mul2(mk2(dec, dec), mk2(s[i + j], s[i + j + 1])));
+            s[i + j] = y.x;
+            s[i + j + 1] = y.y;
+            m4[(j >> 1) & 3] = fmaxf(m4[(j >> 1) & 3], fmaxf(fabsf(y.x), fabsf(y.y)));
+          }
         }
+        m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
         tc_fence_before();
         if (group == 1) {
           pending = true;
@@ -1111,9 +1168,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) delta_walk_tc_kernel(const Chun
         auto pair = [&](int i, float2 &k, float2 &q) {  // rows i and i + 1 of this thread's half
           const uint32_t off = kq_at(j, (group * HK + i) >> 3) + (i & 7) * 2;
           const uint32_t kh = *reinterpret_cast<const uint32_t *>(tile + off);
-          const uint32_t kl = *reinterpret_cast<const uint32_t *>(tile + KQ + off);
-          const uint32_t qh = *reinterpret_cast<const uint32_t *>(tile + 2 * KQ + off);
-          const uint32_t ql = *reinterpret_cast<const uint32_t *>(tile + 3 * KQ + off);
+          const uint32_t kl = *reinterpret_cast<const uint32_t *>(tile + LO + off);
+          const uint32_t qh = *reinterpret_cast<const uint32_t *>(tile + kBlock + off);
+          const uint32_t ql = *reinterpret_cast<const uint32_t *>(tile + kBlock + LO + off);
           k = make_float2(sk * (lo16<false>(kh) + lo16<false>(kl)), sk * (hi16<false>(kh) + hi16<false>(kl)));
           q = make_float2(sq * (lo16<false>(qh) + lo16<false>(ql)), sq * (hi16<false>(qh) + hi16<false>(ql)));
         };
@@ -1140,7 +1197,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) delta_walk_tc_kernel(const Chun
           s[i + 1] = fmaf(k.y, u, al * s[i + 1]);
         }
       }
-      if (group == 0 && c + 1 < chunks) load_v(c + 1);
+      m = largest();
     }
     if (c == chunks && group == 1 && pending) outputs(chunks - 1, scale_s);
     if (c == chunks && a.d.state_out) {

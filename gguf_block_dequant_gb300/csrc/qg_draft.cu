@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(kProbThreads) token_probs_kernel(const ProbArg
 // is kept: 2^-40 of the sum at the least; f64 additions would cost more than the reads here, at two a clock and SM).
 // The CTA and then the warp whose range holds the threshold are found from their sums, by one warp of each CTA
 // with the same additions, and the threads of that CTA search that warp's range.
-constexpr int kVerThreads = 512;
+constexpr int kVerThreads = 256;  // so that 64 sequences' CTAs are all on the SMs at once (512: 35 us)
 constexpr int kVerWarps = kVerThreads / 32;
 
 struct VerifyArgs {

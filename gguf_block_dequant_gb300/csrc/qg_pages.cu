@@ -78,6 +78,8 @@ __global__ void __launch_bounds__(128) kv_fork_kernel(const ForkArgs a) {
 // counts.  A second kernel copies the begun pages that were shared, its blocks over layers and sequences.
 // Workspace: the number of copies; (old page, new page, rows) of each; the needs' running sums; the free pages.
 constexpr int kBookThreads = 1024;
+constexpr int kBookFree = 4096;  // free pages kept in shared memory
+constexpr int kBookAhead = 4;    // rounds of counts that are loaded ahead
 struct ReserveArgs {
   int32_t *kv_len, *pages, *refs, *missing;
   const int32_t *add;
@@ -142,56 +144,91 @@ QG_DEVICE T block_scan(T v, T *total) {
 }
 
 __global__ void __launch_bounds__(kBookThreads) kv_reserve_kernel(const ReserveArgs a) {
+  __shared__ int s_free[kBookFree];  // the first free pages that are taken
   const int tid = threadIdx.x;
   pdl_wait();
   pdl_launch_dependents();
-  // needs and copies; upto[b]: free pages taken before b
-  long long need = 0, sum;
-  int copies = 0, total;
+  // the counts of the first pages are under way while the needs are worked out (a chain of loads)
+  int ref[kBookAhead];
+#pragma unroll
+  for (int i = 0; i < kBookAhead; ++i) {
+    const int p = i * kBookThreads + tid;
+    ref[i] = p < a.n_pages ? a.refs[p] : 1;
+  }
+  // needs and copies in one sum: the copies above bit 40.  upto[b]: free pages taken before b
+  constexpr int kHigh = 40;
+  long long sums = 0, sum;
+  Need r{0, 0, true, false};
+  int at = 0;
+  const bool one_round = a.B <= kBookThreads;
   for (int b0 = 0; b0 < a.B; b0 += kBookThreads) {
     const int b = b0 + tid;
-    Need r{0, 0, true, false};
-    if (b < a.B) r = need_of(a, b);
+    r = Need{0, 0, true, false};
+    int len = 0, old_page = 0;
+    if (b < a.B) {
+      r = need_of(a, b);
+      if (r.copies) {
+        len = a.kv_len[b];
+        old_page = a.pages[static_cast<size_t>(b) * a.max_pages + r.first];
+      }
+    }
     if (!r.ok) bad();
     // beyond the pool's size there are too few pages in any case
-    const int at = static_cast<int>(min(need + block_scan<long long>(r.n, &sum), static_cast<long long>(a.n_pages)));
-    need += sum;
-    const int c = copies + block_scan<int>(r.copies, &total);
-    copies += total;
+    const long long mine = min(r.n, a.n_pages + 1) + (static_cast<long long>(r.copies) << kHigh);
+    const long long before = sums + block_scan<long long>(mine, &sum);
+    sums += sum;
+    const long long need = before & ((1LL << kHigh) - 1);
+    at = static_cast<int>(min(need, static_cast<long long>(a.n_pages)));
     if (b < a.B) {
-      a.upto[b] = at;
+      if (!one_round) a.upto[b] = at;
       if (r.copies) {
-        a.copies[3 * c] = a.pages[static_cast<size_t>(b) * a.max_pages + r.first];
+        const int c = static_cast<int>(before >> kHigh);
+        a.copies[3 * c] = old_page;
         a.copies[3 * c + 1] = at;  // becomes the page
-        a.copies[3 * c + 2] = a.kv_len[b] & ((1 << a.shift) - 1);
+        a.copies[3 * c + 2] = len & ((1 << a.shift) - 1);
       }
     }
   }
+  const long long need = sums & ((1LL << kHigh) - 1);
+  const int copies = static_cast<int>(sums >> kHigh);
   // the lowest free pages
-  int found = 0;
-  for (int p0 = 0; p0 < a.n_pages && found < need; p0 += kBookThreads) {
+  int found = 0, total;
+  auto look = [&](int p0, int count) {
     const int p = p0 + tid;
-    const bool is_free = p < a.n_pages && a.refs[p] == 0;
-    const int at = found + block_scan<int>(is_free, &total);
+    const bool is_free = p < a.n_pages && count == 0;
+    const int i = found + block_scan<int>(is_free, &total);
     found += total;
-    if (is_free && at < need) a.free_ids[at] = p;
-  }
+    if (is_free && i < need) {
+      if (i < kBookFree) s_free[i] = p;
+      else a.free_ids[i] = p;
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < kBookAhead; ++i)
+    if (i * kBookThreads < a.n_pages && found < need) look(i * kBookThreads, ref[i]);
+  for (int p0 = kBookAhead * kBookThreads; p0 < a.n_pages && found < need; p0 += kBookThreads)
+    look(p0, p0 + tid < a.n_pages ? a.refs[p0 + tid] : 1);
   if (tid == 0) {
     *a.missing = static_cast<int>(max(0LL, min(need - found, 0x7FFFFFFFLL)));
     *a.n_copies = found < need ? 0 : copies;
   }
   if (found < need) return;
   __syncthreads();
-  // a warp per sequence; every sequence's need is worked out before any count changes below it
-  for (int c = tid; c < copies; c += kBookThreads) a.copies[3 * c + 1] = a.free_ids[a.copies[3 * c + 1]];
+  auto free_page = [&](int i) { return i < kBookFree ? s_free[i] : a.free_ids[i]; };
+  // every sequence's need is worked out before any count changes below
+  for (int c = tid; c < copies; c += kBookThreads) a.copies[3 * c + 1] = free_page(a.copies[3 * c + 1]);
   for (int b = tid; b < a.B; b += kBookThreads) {
-    const Need r = need_of(a, b);
+    if (!one_round) {
+      r = need_of(a, b);
+      at = a.upto[b];
+    }
     if (!r.ok) continue;
-    for (int i = 0; i < r.n; ++i) a.pages[static_cast<size_t>(b) * a.max_pages + r.first + i] = a.free_ids[a.upto[b] + i];
-    a.kv_len[b] += __ldg(a.add + b);
+    for (int i = 0; i < r.n; ++i) a.pages[static_cast<size_t>(b) * a.max_pages + r.first + i] = free_page(at + i);
+    const int more = __ldg(a.add + b);
+    if (more) a.kv_len[b] += more;
   }
   __syncthreads();
-  for (int i = tid; i < need; i += kBookThreads) a.refs[a.free_ids[i]] = 1;
+  for (int i = tid; i < need; i += kBookThreads) a.refs[free_page(i)] = 1;
   for (int c = tid; c < copies; c += kBookThreads) atomicSub(a.refs + a.copies[3 * c], 1);
 }
 
