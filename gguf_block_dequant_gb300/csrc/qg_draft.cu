@@ -340,8 +340,6 @@ __global__ void __launch_bounds__(kProbThreads) token_probs_kernel(const ProbArg
 // is kept: 2^-40 of the sum at the least; f64 additions would cost more than the reads here, at two a clock and SM).
 // The CTA and then the warp whose range holds the threshold are found from their sums, by one warp of each CTA
 // with the same additions, and the threads of that CTA search that warp's range.
-constexpr int kVerThreads = 256;  // so that 64 sequences' CTAs are all on the SMs at once (512: 35 us)
-constexpr int kVerWarps = kVerThreads / 32;
 
 struct VerifyArgs {
   const float *probs, *draft, *u, *u_next;
@@ -421,7 +419,11 @@ QG_DEVICE Sum scan(Sum a) {
   return a;
 }
 
-__global__ void __launch_bounds__(kVerThreads) draft_verify_kernel(const VerifyArgs a) {
+// NT threads a CTA: 256 keep 64 sequences' CTAs on the SMs all at once (22 us; 35 with 512), 1024 read a slice in one round of
+// loads where there are few sequences
+template <int NT>
+__global__ void __launch_bounds__(NT, 1024 / NT) draft_verify_kernel(const VerifyArgs a) {
+  constexpr int kVerThreads = NT, kVerWarps = NT / 32;
   __shared__ Sum wsum[kVerWarps], cta_sum, s_rest;
   __shared__ int wlast[kVerWarps], cta_last, stop, found, tail, s_pick;  // s_pick: the warp whose range is searched
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -663,10 +665,14 @@ qg_status qg_draft_verify(const float *probs, const float *draft_probs, const in
   VerifyArgs a{probs, draft_probs, u, u_next, tokens, q_start, kv_len, accepted, next_token, kept_len,
                n_seqs, n_rows, static_cast<int>(V), cs, 0, 0};
   a.slice = static_cast<int>((V + cs - 1) / cs + 3) & ~3;
-  a.sub = ((a.slice + kVerWarps - 1) / kVerWarps + 3) & ~3;
+  const bool few = int64_t(n_seqs) * cs <= dev.sms;
+  const int warps = few ? 32 : 8;
+  a.sub = ((a.slice + warps - 1) / warps + 3) & ~3;
   g_launched = true;
-  const cudaError_t e = launch_cluster(draft_verify_kernel, static_cast<unsigned>(n_seqs) * cs, kVerThreads, 0, cs,
-                                       reinterpret_cast<cudaStream_t>(stream), a);
+  const unsigned blocks = static_cast<unsigned>(n_seqs) * cs;
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = few ? launch_cluster(draft_verify_kernel<1024>, blocks, 1024, 0, cs, st, a)
+                            : launch_cluster(draft_verify_kernel<256>, blocks, 256, 0, cs, st, a);
   if (e != cudaSuccess) return QG_ECUDA;
   return cudaGetLastError() == cudaSuccess ? QG_OK : QG_ECUDA;
 }

@@ -77,9 +77,9 @@ __global__ void __launch_bounds__(128) kv_fork_kernel(const ForkArgs a) {
 // free pages in rising order (a scan over the counts until there are enough), then the page lists and the
 // counts.  A second kernel copies the begun pages that were shared, its blocks over layers and sequences.
 // Workspace: the number of copies; (old page, new page, rows) of each; the needs' running sums; the free pages.
-constexpr int kBookThreads = 1024;
+constexpr int kBookThreads = 512;
 constexpr int kBookFree = 4096;  // free pages kept in shared memory
-constexpr int kBookAhead = 4;    // rounds of counts that are loaded ahead
+constexpr int kBookEach = 8;     // counts of a thread and round
 struct ReserveArgs {
   int32_t *kv_len, *pages, *refs, *missing;
   const int32_t *add;
@@ -130,17 +130,19 @@ QG_DEVICE T block_scan(T v, T *total) {
     const T y = __shfl_up_sync(0xFFFFFFFFu, x, o);
     if (lane >= o) x += y;
   }
+  constexpr int W = kBookThreads / 32;
   __syncthreads();
   if (lane == 31) part[warp] = x;
   __syncthreads();
-  T before = 0, all = 0;
+  T y = part[lane & (W - 1)];
 #pragma unroll
-  for (int w = 0; w < kBookThreads / 32; ++w) {
-    if (w < warp) before += part[w];
-    all += part[w];
+  for (int o = 1; o < W; o <<= 1) {
+    const T z = __shfl_up_sync(0xFFFFFFFFu, y, o);
+    if (lane >= o) y += z;
   }
-  *total = all;
-  return before + x - v;
+  *total = __shfl_sync(0xFFFFFFFFu, y, W - 1);
+  const T before = __shfl_sync(0xFFFFFFFFu, y, warp ? warp - 1 : 0);
+  return (warp ? before : 0) + x - v;
 }
 
 __global__ void __launch_bounds__(kBookThreads) kv_reserve_kernel(const ReserveArgs a) {
@@ -149,12 +151,16 @@ __global__ void __launch_bounds__(kBookThreads) kv_reserve_kernel(const ReserveA
   pdl_wait();
   pdl_launch_dependents();
   // the counts of the first pages are under way while the needs are worked out (a chain of loads)
-  int ref[kBookAhead];
+  constexpr int kRound = kBookThreads * kBookEach;
+  int ref[kBookEach];
+  auto load = [&](int p0) {
 #pragma unroll
-  for (int i = 0; i < kBookAhead; ++i) {
-    const int p = i * kBookThreads + tid;
-    ref[i] = p < a.n_pages ? a.refs[p] : 1;
-  }
+    for (int i = 0; i < kBookEach; ++i) {
+      const int p = p0 + tid * kBookEach + i;
+      ref[i] = p < a.n_pages ? a.refs[p] : 1;
+    }
+  };
+  load(0);
   // needs and copies in one sum: the copies above bit 40.  upto[b]: free pages taken before b
   constexpr int kHigh = 40;
   long long sums = 0, sum;
@@ -193,21 +199,27 @@ __global__ void __launch_bounds__(kBookThreads) kv_reserve_kernel(const ReserveA
   const int copies = static_cast<int>(sums >> kHigh);
   // the lowest free pages
   int found = 0, total;
-  auto look = [&](int p0, int count) {
-    const int p = p0 + tid;
-    const bool is_free = p < a.n_pages && count == 0;
-    const int i = found + block_scan<int>(is_free, &total);
-    found += total;
-    if (is_free && i < need) {
-      if (i < kBookFree) s_free[i] = p;
-      else a.free_ids[i] = p;
-    }
-  };
+  for (int p0 = 0; p0 < a.n_pages && found < need; p0 += kRound) {
+    int mine = 0, now[kBookEach];
 #pragma unroll
-  for (int i = 0; i < kBookAhead; ++i)
-    if (i * kBookThreads < a.n_pages && found < need) look(i * kBookThreads, ref[i]);
-  for (int p0 = kBookAhead * kBookThreads; p0 < a.n_pages && found < need; p0 += kBookThreads)
-    look(p0, p0 + tid < a.n_pages ? a.refs[p0 + tid] : 1);
+    for (int i = 0; i < kBookEach; ++i) {
+      now[i] = ref[i];
+      mine += now[i] == 0;
+    }
+    if (a.n_pages - p0 > kRound) load(p0 + kRound);
+    int i = found + block_scan<int>(mine, &total);
+    found += total;
+#pragma unroll
+    for (int e = 0; e < kBookEach; ++e)
+      if (now[e] == 0) {
+        const int p = p0 + tid * kBookEach + e;
+        if (i < need) {
+          if (i < kBookFree) s_free[i] = p;
+          else a.free_ids[i] = p;
+        }
+        ++i;
+      }
+  }
   if (tid == 0) {
     *a.missing = static_cast<int>(max(0LL, min(need - found, 0x7FFFFFFFLL)));
     *a.n_copies = found < need ? 0 : copies;
