@@ -32,6 +32,15 @@ QG_DEVICE int remote_s32(const int *p, uint32_t rank) {
   return v;
 }
 
+// 16 bytes into the same place of CTA `rank`'s shared memory, counted on its barrier
+QG_DEVICE void tell_remote(const float4 *place, float4 v, const uint64_t *bar, uint32_t rank) {
+  asm volatile(
+      "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
+          remote_addr(place, rank)),
+      "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(remote_addr(bar, rank))
+      : "memory");
+}
+
 template <typename... KArgs, typename... Args>
 cudaError_t launch_cluster(void (*kern)(KArgs...), unsigned blocks, unsigned threads, size_t smem, int cluster,
                            cudaStream_t s, Args &&...args) {
@@ -48,6 +57,31 @@ cudaError_t launch_cluster(void (*kern)(KArgs...), unsigned blocks, unsigned thr
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+}
+
+// how many clusters of a kernel the current device holds at once (asked once a device; the one kernel that asks)
+int clusters_at_once(const void *kern, unsigned threads, size_t smem, int cluster) {
+  static std::atomic<int> known[64];
+  int d = 0;
+  if (cudaGetDevice(&d) != cudaSuccess || d < 0 || d >= 64) return 0;
+  int n = known[d];
+  if (n == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(cluster);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {static_cast<unsigned>(cluster), 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
+      cudaGetLastError();
+      return 0;
+    }
+    known[d] = n;
+  }
+  return n;
 }
 
 // ---- probabilities ------------------------------------------------------------------------------
@@ -203,6 +237,110 @@ __global__ void __launch_bounds__(kProbThreads) probs_kernel(const ProbArgs a) {
     }
   }
   if (a.cs > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // nobody leaves while it is read
+}
+
+// The same for many rows that start at 16-byte boundaries: clusters stay on their SMs and take every so many-th row, and a CTA's slice
+// of the next row is copied to shared memory while this one's, in registers, is worked on and written, so that reads, exchanges and writes
+// of different rows overlap.
+template <int NV>
+__global__ void __launch_bounds__(kProbThreads, 2) probs_stream_kernel(const ProbArgs a, int clusters) {
+  extern __shared__ __align__(128) float4 slice[];
+  __shared__ float red[kProbWarps], reds[kProbWarps];
+  __shared__ int redi[kProbWarps];
+  __shared__ __align__(16) float4 told[2][8];  // (maximum, sum, index) of each CTA, by the row's parity
+  __shared__ uint64_t full, told_bar[2];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = static_cast<int>(blockIdx.x) % a.cs, first = static_cast<int>(blockIdx.x) / a.cs;
+  const int lo = rank * a.slice, n = max(0, min(a.slice, a.V - lo)) / 4;  // vectors
+  if (tid == 0) {
+    mbar_init(&full, 1);
+    mbar_init(&told_bar[0], 1);
+    mbar_init(&told_bar[1], 1);
+    fence_mbar_init();
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+  cluster_sync();  // the barriers stand
+  auto ask = [&](int row) {
+    mbar_arrive_expect_tx(&full, 16 * n);
+    bulk_g2s<true>(slice, a.logits + static_cast<long long>(row) * a.V + lo, 16 * n, &full);
+  };
+  if (tid == 0 && n && first < a.T) ask(first);
+  int k = 0;
+  for (int row = first; row < a.T; row += clusters, ++k) {
+    const int buf = k & 1;
+    const float tau = a.temperature ? __ldg(a.temperature + row) : 1.f;
+    const bool greedy = !(tau > 0.f);
+    if (n && !mbar_wait(&full, k & 1)) atomicOr(&g_qg_status_draft, QG_STATUS_BIT_TIMEOUT);
+    float4 x[NV];
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = tid + i * kProbThreads;
+      x[i] = v < n ? slice[v] : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      m = fmaxf(m, fmaxf(fmaxf(x[i].x, x[i].y), fmaxf(x[i].z, x[i].w)));
+    }
+    int at = 0x7FFFFFFF;
+    if (greedy) {
+#pragma unroll
+      for (int i = NV - 1; i >= 0; --i) {
+        const int e = lo + 4 * (tid + i * kProbThreads);
+        if (x[i].w == m) at = e + 3;
+        if (x[i].z == m) at = e + 2;
+        if (x[i].y == m) at = e + 1;
+        if (x[i].x == m) at = e;
+      }
+    }
+    best_of(m, at, red, redi);  // everyone has read the slice
+    if (tid == 0 && n && row + clusters < a.T) ask(row + clusters);
+    const bool finite = m > -INFINITY && m < INFINITY;
+    const float c = fminf(fmaxf(2.8853900817779268f / tau, 1e-44f), 3e38f), hm = -0.5f * m;
+    float s = 0.f;
+    if (!greedy && finite) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        auto power = [&](float y) { return ex2(fmaxf(fmaf(0.5f, y, hm) * c, -200.f)); };
+        x[i] = make_float4(power(x[i].x), power(x[i].y), power(x[i].z), power(x[i].w));
+        s += (x[i].x + x[i].y) + (x[i].z + x[i].w);
+      }
+    }
+    s = warp_sum(s);
+    if (lane == 0) reds[warp] = s;
+    __syncthreads();
+    s = reds[lane & (kProbWarps - 1)];
+#pragma unroll
+    for (int o = kProbWarps / 2; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    // told to every CTA's shared memory, with its barrier: a cluster barrier would wait for the row before to be written.  Two
+    // places in turn: who is a row ahead has heard from everyone about the row before, after they left this place
+    if (tid == 0) mbar_arrive_expect_tx(&told_bar[buf], 16 * a.cs);
+    if (tid < a.cs) tell_remote(&told[buf][rank], make_float4(m, s, __int_as_float(at), 0.f), &told_bar[buf], tid);
+    if (!mbar_wait(&told_bar[buf], (k >> 1) & 1)) atomicOr(&g_qg_status_draft, QG_STATUS_BIT_TIMEOUT);
+    const float4 other = told[buf][lane & (a.cs - 1)];
+    const float om = other.x, os = other.y;
+    float M = om;
+    int best = __float_as_int(other.z);
+    for (int o = a.cs / 2; o; o >>= 1) {
+      const float y = __shfl_xor_sync(0xFFFFFFFFu, M, o);
+      const int j = __shfl_xor_sync(0xFFFFFFFFu, best, o);
+      if (y > M || (y == M && j < best)) M = y, best = j;
+    }
+    float S = om > -INFINITY && M < INFINITY ? os * ex2(fmaxf((0.5f * om - 0.5f * M) * c, -200.f)) : 0.f;
+    for (int o = a.cs / 2; o; o >>= 1) S += __shfl_xor_sync(0xFFFFFFFFu, S, o);
+    const bool none = !(M > -INFINITY && M < INFINITY);
+    const float f = none || greedy || !finite ? 0.f : ex2(fmaxf((0.5f * m - 0.5f * M) * c, -200.f)) / S;
+    float4 *dst = reinterpret_cast<float4 *>(a.probs + static_cast<long long>(row) * a.V + lo);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = tid + i * kProbThreads;
+      if (v >= n) continue;
+      if (f == 0.f) {
+        const int e = greedy && !none ? best - lo - 4 * v : -1;
+        dst[v] = make_float4(e == 0 ? 1.f : 0.f, e == 1 ? 1.f : 0.f, e == 2 ? 1.f : 0.f, e == 3 ? 1.f : 0.f);
+      } else {
+        dst[v] = make_float4(x[i].x * f, x[i].y * f, x[i].z * f, x[i].w * f);
+      }
+    }
+  }
 }
 
 // Vocabularies that eight CTAs' registers do not hold: slices in shared memory, what does not fit is read again.
@@ -630,7 +768,16 @@ qg_status qg_token_probs(const float *logits, const float *temperature, int T, i
   const int nv = (a.slice + kHold - 1) / kHold;
   const unsigned blocks = static_cast<unsigned>(T) * cs;
   cudaError_t e;
-  if (nv <= 2) e = launch_cluster(probs_kernel<2>, blocks, kProbThreads, 0, cs, st, a);
+  // many rows of whole vectors, not in place (the next row is read early, but that is another row): clusters that stay
+  int clusters = 0;
+  if (V % 4 == 0 && cs == 8 && nv > 5 && nv <= 10 && T >= 4 * (dev.sms / cs)) {
+    constexpr size_t most = sizeof(float) * 10 * kHold;
+    if (!qg::set_smem_attr(reinterpret_cast<const void *>(probs_stream_kernel<10>), static_cast<uint32_t>(most))) return QG_ECUDA;
+    clusters = clusters_at_once(reinterpret_cast<const void *>(probs_stream_kernel<10>), kProbThreads, most, cs);
+  }
+  if (clusters > 0) {
+    e = launch_cluster(probs_stream_kernel<10>, static_cast<unsigned>(std::min(clusters, T)) * cs, kProbThreads, sizeof(float) * a.slice, cs, st, a, std::min(clusters, T));
+  } else if (nv <= 2) e = launch_cluster(probs_kernel<2>, blocks, kProbThreads, 0, cs, st, a);
   else if (nv <= 5) e = launch_cluster(probs_kernel<5>, blocks, kProbThreads, 0, cs, st, a);
   else if (nv <= 10) e = launch_cluster(probs_kernel<10>, blocks, kProbThreads, 0, cs, st, a);
   else if (nv <= 17) e = launch_cluster(probs_kernel<17>, blocks, kProbThreads, 0, cs, st, a);

@@ -78,6 +78,25 @@ def test_probs_largest_vocabulary(qg):
     assert torch.equal(d, out)
 
 
+@pytest.mark.parametrize("T,V", [(90, 90004), (83, 163836), (300, 81940)])
+def test_probs_many_rows(qg, T, V):
+    """Rows that clusters take in turn, in place as well, with greedy rows, rows without a distribution and odd values among them."""
+    g = torch.Generator().manual_seed(T)
+    x = 3 * torch.randn((T, V), generator=g)
+    temp = 0.3 + torch.rand((T,), generator=g)
+    temp[::7] = 0.0
+    x[3], x[11, 5], x[20, ::3] = -math.inf, math.nan, torch.finfo(torch.float32).min
+    x[14, V - 1] = x[14, 9] = 50.0  # a greedy row with a tie
+    x[30, 7] = math.inf
+    out = torch.full((T, V), math.nan, device="cuda")
+    d = x.cuda()
+    qg.token_probs(d, out, temperature=temp.cuda())
+    check_probs(out, x, temp)
+    qg.token_probs(d, d, temperature=temp.cuda())
+    assert torch.equal(d, out)
+    assert qg.device_status() == 0
+
+
 @pytest.mark.parametrize("V", [7, 5003, 60000])
 def test_probs_special_rows(qg, V):
     lo, inf, nan = torch.finfo(torch.float32).min, math.inf, math.nan
