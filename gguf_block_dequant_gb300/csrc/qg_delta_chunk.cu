@@ -51,7 +51,9 @@ struct Factors {
   float alpha[C], beta[C], sk[C], sq[C];  // token by token, for chunks with infinite or NaN values
   float dec;       // e^{G_C}
   int odd;         // such a value among the queries, keys and gates
-  float pad[30];
+  // bounds: |K S0| e^G of a column is at most kappa max |S0|, |T R| at most tau max |R|, wk at most omega
+  float kappa, omega, tau;
+  float pad[27];
 };
 constexpr int kTA = 2 * kBlock + static_cast<int>(sizeof(Factors));
 static_assert(kTA % 16 == 0, "bulk copies");
@@ -147,7 +149,7 @@ template <int DK>
 __global__ void __launch_bounds__(kPrepWarps * 32, 5) delta_prep_kernel(const ChunkArgs a) {
   extern __shared__ __align__(128) unsigned char tile[];  // K hi, K lo, Q hi, Q lo
   __shared__ float kk[C][C + 1], qk[C][C + 1];
-  __shared__ float scale_k[C], scale_q[C];
+  __shared__ float scale_k[C], scale_q[C], norm_k[C];
   __shared__ float2 gsum[kPrepWarps][C];
   __shared__ int bad_rows;
   constexpr int LO = Tiles<DK>::kLo;
@@ -234,7 +236,10 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 5) delta_prep_kernel(const Ch
     row_s = 0x1p-60f;
     to = f * 0x1p60f;
   }
-  if ((lane & 1) == 0) (mine >= R ? scale_q : scale_k)[warp * R + (mine & (R - 1))] = row_s;
+  if ((lane & 1) == 0) {
+    (mine >= R ? scale_q : scale_k)[warp * R + (mine & (R - 1))] = row_s;
+    if (mine < R) norm_k[warp * R + mine] = sqrtf(ss[0]) * fabsf(f);
+  }
 #pragma unroll
   for (int z = 0; z < 2; ++z)
 #pragma unroll
@@ -342,7 +347,11 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 5) delta_prep_kernel(const Ch
       const float eg = ex2(g_hi + g_lo);
       f->fk[lane] = eg * scale_k[lane];
       f->fq[lane] = eg * scale_q[lane];
-      f->wk[lane] = ex2((gl.x - g_hi) + (gl.y - g_lo)) * scale_k[lane];
+      const float wk = ex2((gl.x - g_hi) + (gl.y - g_lo)) * scale_k[lane];
+      f->wk[lane] = wk;
+      // a row of K and a column of S0: the product of their lengths at most
+      const uint32_t kappa = __reduce_max_sync(0xFFFFFFFFu, mag(eg * norm_k[lane]));
+      const uint32_t omega = __reduce_max_sync(0xFFFFFFFFu, mag(wk));
       f->alpha[lane] = expf(ga.x);
       f->beta[lane] = ga.y;
       f->sk[lane] = scale_k[lane];
@@ -352,6 +361,8 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 5) delta_prep_kernel(const Ch
       if (lane == 0) {
         f->dec = chunk_decay(gl.x + gl.y);
         f->odd = odd;
+        f->kappa = __uint_as_float(kappa) * (DK == 64 ? 8.1f : 11.4f);  // sqrt(DK), and 1 in a hundred for roundings
+        f->omega = __uint_as_float(omega);
       }
       continue;
     }
@@ -383,6 +394,11 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 5) delta_prep_kernel(const Ch
       const float4 m = *reinterpret_cast<const float4 *>(&M[lane][j]);
       w[j] = m.x, w[j + 1] = m.y, w[j + 2] = m.z, w[j + 3] = m.w;
     }
+    float row_sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < C; ++j) row_sum += fabsf(w[j]);
+    const uint32_t tau = __reduce_max_sync(0xFFFFFFFFu, mag(row_sum));
+    if (lane == 0) f->tau = __uint_as_float(tau);
     write_row(w, ta, f->st);
     __syncwarp();
   }
@@ -757,9 +773,8 @@ __global__ void __launch_bounds__(W * 32) delta_walk_kernel(const ChunkArgs a) {
 // the state, so a lane of tensor memory is one column and its thread works alone: the state stays in registers (two threads
 // a column, half of its rows each), left operands go to tensor memory as f16 pairs (hi in one range of columns, lo in
 // another), right operands are the tiles in shared memory, with K read as it lies for S0^T K^T and turned for U^T K.
-//   both groups  S^T in two terms; S^T <- e^{G_C} S^T + D
-//   group 0      R = V - ..., U, and U with the decays to the chunk's end, each in two terms
-//   group 1      the outputs of the chunk before; whether the next chunk's values are all finite
+//   both groups  S^T in two terms (each half of its rows); R = V - ..., U, and U with the decays to the chunk's end, each in
+//                two terms (each half of the tokens); the outputs of the chunk before; S^T <- e^{G_C} S^T + D
 //   a producer   bulk copies into the ring (a row of values each lane: that would hold control up by 1700 cycles)
 //   control      the products X = S^T K^T, O = S^T Q^T, U = R T^T, D = U K, O2 = U A^T
 // Every wait ends with its phase or after kTcWaitCycles, which makes the CTA give up.
@@ -788,7 +803,7 @@ struct TcShared {
   int abort, seq;
   int odd_chunk, v_odd[2];  // the last chunk that goes token by token; chunks with such values, by their parity
   float smax[2][128];       // largest of a column's halves
-  float scale_w[128], scale_u[2][128];
+  float vmax[2][2][128];    // the same of a chunk's values, by its parity: halves of its tokens
   __align__(16) float4 ex[2][2][128];  // token by token: partial products of the halves, by the token's parity
 };
 
@@ -847,10 +862,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) delta_walk_tc_kernel(const Chun
       mbar_init(&sh.empty[i], 1);
     }
     mbar_init(&sh.s_ready, 8);
-    mbar_init(&sh.r_ready, 4);
-    mbar_init(&sh.u_ready, 4);
-    mbar_init(&sh.w_ready, 4);
-    mbar_init(&sh.o_free, 4);
+    mbar_init(&sh.r_ready, 8);
+    mbar_init(&sh.u_ready, 8);
+    mbar_init(&sh.w_ready, 8);
+    mbar_init(&sh.o_free, 8);
     mbar_init(&sh.x_done, 1);
     mbar_init(&sh.u_done, 1);
     mbar_init(&sh.d_done, 1);
@@ -984,39 +999,33 @@ __global__ void __launch_bounds__(kTcThreads, 1) delta_walk_tc_kernel(const Chun
       const float *p = reinterpret_cast<const float *>(ring + (c % kTcStages) * kStage + TcSmem<DK>::kV);
       return c * C + j < n ? p[j * 128 + row] : 0.f;
     };
-    // w (32 values) in two terms to 16 + 16 columns of tensor memory; returns the scale
-    auto put = [&](auto kind, const float (&w)[C], uint32_t col) {
-      float m4[4] = {0.f, 0.f, 0.f, 0.f};
+    // this half's 16 tokens in two terms to its 8 + 8 columns of a pair of tensor memory.  The scale is that of a bound, known
+    // before: the halves need not meet for their largest (terms of their own scale keep 22 bits 2^20 below a bound)
+    constexpr int H = C / 2;
+    const int j0 = group * H;
+    auto scale_for = [&](float bound, float &sc, float &inv) { row_scale(mag(fminf(bound, 3e38f)), sc, inv); };
+    auto put = [&](const float (&w)[H], float inv, uint32_t col) {
+      uint32_t hi[H / 2], lo[H / 2];
 #pragma unroll
-      for (int j = 0; j < C; ++j) m4[j & 3] = fmaxf(m4[j & 3], fabsf(w[j]));
-      float sc, inv;
-      row_scale(mag(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]))), sc, inv);
-      uint32_t hi[16], lo[16];
-#pragma unroll
-      for (int j = 0; j < C; j += 2) {
-        if constexpr (decltype(kind)::value) split2_each(w[j], w[j + 1], inv, hi[j / 2], lo[j / 2]);
-        else split2(w[j], w[j + 1], inv, hi[j / 2], lo[j / 2]);
-      }
-      tmem_st16(lanes + col, hi);
-      tmem_st16(lanes + col + 16, lo);
-      return sc;
+      for (int j = 0; j < H; j += 2) split2_each(w[j], w[j + 1], inv, hi[j / 2], lo[j / 2]);
+      tmem_st8(lanes + col + 8 * group, hi);
+      tmem_st8(lanes + col + 16 + 8 * group, lo);
     };
-    using Each = std::true_type;    // rows of tokens
-    using Whole = std::false_type;  // rows that are summed as a whole
     auto tell = [&](uint64_t *bar) {  // what this warp has put into, or taken from, tensor memory
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
     };
-    // whether a chunk's values are all finite, told with the state before that chunk
+    // the largest of a chunk's values, told with the state before that chunk, and whether all are finite
     auto look_at_v = [&](int c) {
       if (!wait(&sh.full[c % kTcStages], (c / kTcStages) & 1)) return;
       uint32_t big = 0;
 #pragma unroll
-      for (int j = 0; j < C; ++j) big = max(big, mag(value(c, j)));
+      for (int j = 0; j < H; ++j) big = max(big, mag(value(c, j0 + j)));
+      sh.vmax[c & 1][group][row] = __uint_as_float(big);
       if (big >= kInfBits) sh.v_odd[c & 1] = c;
     };
-    if (group == 1) look_at_v(0);
+    look_at_v(0);
     auto largest = [&] {
       float m4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -1024,34 +1033,32 @@ __global__ void __launch_bounds__(kTcThreads, 1) delta_walk_tc_kernel(const Chun
       return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
     };
     float m = largest();
-    float scale_s = 1.f, scale_before = 1.f;
-    uint32_t n_u = 0;           // phases of u_done and o_done
-    bool pending = false;       // group 1: outputs of the chunk before wait to be written
-    auto outputs = [&](int c, float ss) {  // group 1; ss: the state's scale then
+    float scale_s = 1.f, scale_before = 1.f, largest_s = 0.f;
+    float scale_u = 1.f;
+    uint32_t n_u = 0;      // phases of u_done and o_done
+    bool pending = false;  // outputs of the chunk before wait to be written
+    auto outputs = [&](int c, float ss) {  // ss: the state's scale then
       if (!wait(&sh.o_done, (n_u - 1) & 1)) return false;
       tc_fence_after();
       const Factors *f = factors(c);
-      const float su = sh.scale_u[c & 1][row];
-      float *p = op + static_cast<long long>(c) * C * a.d.out_stride;
-      const int left = n - c * C;
-      float x[32], y[32];
-      tmem_ld32_nowait(lanes + TXO + 64 * (c & 1) + 32, x);
-      tmem_ld32_nowait(lanes + TO2, y);
-      tmem_ld_wait(x);
-      tmem_ld_wait(y);
+      float *p = op + (static_cast<long long>(c) * C + j0) * a.d.out_stride;
+      const int left = n - c * C - j0;
+      float x[H], y[H];
+      tmem_ld16(lanes + TXO + 64 * (c & 1) + 32 + j0, x);
+      tmem_ld16(lanes + TO2 + j0, y);
 #pragma unroll
-      for (int j = 0; j < C; j += 4) {
-        const float4 fq = *reinterpret_cast<const float4 *>(f->fq + j), sa = *reinterpret_cast<const float4 *>(f->sa + j);
-        x[j] = fmaf(fq.x * ss, x[j], sa.x * su * y[j]);
-        x[j + 1] = fmaf(fq.y * ss, x[j + 1], sa.y * su * y[j + 1]);
-        x[j + 2] = fmaf(fq.z * ss, x[j + 2], sa.z * su * y[j + 2]);
-        x[j + 3] = fmaf(fq.w * ss, x[j + 3], sa.w * su * y[j + 3]);
+      for (int j = 0; j < H; j += 4) {
+        const float4 fq = *reinterpret_cast<const float4 *>(f->fq + j0 + j), sa = *reinterpret_cast<const float4 *>(f->sa + j0 + j);
+        x[j] = fmaf(fq.x * ss, x[j], sa.x * scale_u * y[j]);
+        x[j + 1] = fmaf(fq.y * ss, x[j + 1], sa.y * scale_u * y[j + 1]);
+        x[j + 2] = fmaf(fq.z * ss, x[j + 2], sa.z * scale_u * y[j + 2]);
+        x[j + 3] = fmaf(fq.w * ss, x[j + 3], sa.w * scale_u * y[j + 3]);
       }
 #pragma unroll
-      for (int j = 0; j < C; ++j) asm volatile("" : "+f"(x[j]));  // the factors are read before the stage is given up
+      for (int j = 0; j < H; ++j) asm volatile("" : "+f"(x[j]));  // the factors are read before the stage is given up
       tell(&sh.o_free);
 #pragma unroll
-      for (int j = 0; j < C; ++j, p += a.d.out_stride)
+      for (int j = 0; j < H; ++j, p += a.d.out_stride)
         if (j < left) *p = x[j];
       return true;
     };
@@ -1064,7 +1071,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) delta_walk_tc_kernel(const Chun
         named_bar_sync(1, 256);
         scale_before = scale_s;
         float inv;
-        row_scale(mag(fmaxf(m, sh.smax[group ^ 1][row])), scale_s, inv);
+        largest_s = fmaxf(m, sh.smax[group ^ 1][row]);
+        row_scale(mag(largest_s), scale_s, inv);
 #pragma unroll
         for (int i = 0; i < HK; i += 32) {
           uint32_t hi[16], lo[16];
@@ -1077,76 +1085,72 @@ __global__ void __launch_bounds__(kTcThreads, 1) delta_walk_tc_kernel(const Chun
         tell(&sh.s_ready);
       }
       const Factors *f = factors(c);
-      bool odd;
-      if (group == 0) {
-        if (!wait(&sh.full[c % kTcStages], (c / kTcStages) & 1)) break;
-        float v[C];
+      if (!wait(&sh.full[c % kTcStages], (c / kTcStages) & 1)) break;
+      // while the product runs: this half's values, and the outputs of the chunk before
+      float x[H], w[H];
 #pragma unroll
-        for (int j = 0; j < C; ++j) v[j] = value(c, j);
+      for (int j = 0; j < H; ++j) w[j] = value(c, j0 + j);
 #pragma unroll
-        for (int j = 0; j < C; ++j) asm volatile("" : "+f"(v[j]));  // while the product runs
-        if (!wait(&sh.x_done, c & 1)) break;
-        odd = *reinterpret_cast<volatile int *>(&sh.odd_chunk) == c;
-        if (!odd) {
-          tc_fence_after();
-          float x[C];
-          tmem_ld32_nowait(lanes + TXO + 64 * (c & 1), x);
-          tmem_ld_wait(x);
-#pragma unroll
-          for (int j = 0; j < C; j += 4) {
-            const float4 fk = *reinterpret_cast<const float4 *>(f->fk + j);
-            x[j] = fmaf(-fk.x * scale_s, x[j], v[j]);
-            x[j + 1] = fmaf(-fk.y * scale_s, x[j + 1], v[j + 1]);
-            x[j + 2] = fmaf(-fk.z * scale_s, x[j + 2], v[j + 2]);
-            x[j + 3] = fmaf(-fk.w * scale_s, x[j + 3], v[j + 3]);
-          }
-          const float sr = put(Each{}, x, TR);
-          tmem_st_wait();
-          tell(&sh.r_ready);
-          if (!wait(&sh.u_done, n_u & 1)) break;
-          tc_fence_after();
-          tmem_ld32_nowait(lanes + TU, x);
-          tmem_ld_wait(x);
-          float w[C];
-#pragma unroll
-          for (int j = 0; j < C; j += 4) {
-            const float4 st = *reinterpret_cast<const float4 *>(f->st + j), wk = *reinterpret_cast<const float4 *>(f->wk + j);
-            x[j] *= st.x * sr;
-            x[j + 1] *= st.y * sr;
-            x[j + 2] *= st.z * sr;
-            x[j + 3] *= st.w * sr;
-            w[j] = x[j] * wk.x;
-            w[j + 1] = x[j + 1] * wk.y;
-            w[j + 2] = x[j + 2] * wk.z;
-            w[j + 3] = x[j + 3] * wk.w;
-          }
-          sh.scale_w[row] = put(Whole{}, w, TW);
-          tmem_st_wait();
-          tell(&sh.w_ready);
-          sh.scale_u[c & 1][row] = put(Each{}, x, TUA);
-          tmem_st_wait();
-          tell(&sh.u_ready);
-          ++n_u;
-        }
-      } else {
-        if (pending && !outputs(c - 1, scale_before)) break;
-        pending = false;
-        if (c + 1 < chunks) look_at_v(c + 1);
-      }
-      if (!wait(&sh.d_done, c & 1) || !wait(&sh.full[c % kTcStages], (c / kTcStages) & 1)) break;
-      odd = *reinterpret_cast<volatile int *>(&sh.odd_chunk) == c;
-      if (!odd) {
+      for (int j = 0; j < H; ++j) asm volatile("" : "+f"(w[j]));
+      if (pending && !outputs(c - 1, scale_before)) break;
+      pending = false;
+      float bound = 1.01f * fmaf(f->kappa, largest_s, fmaxf(sh.vmax[c & 1][0][row], sh.vmax[c & 1][1][row]));
+      float scale_r, inv_r, inv_u, scale_w, inv_w;
+      scale_for(bound, scale_r, inv_r);
+      bound *= 1.01f * f->tau;
+      const float bound_w = bound * f->omega;
+      if (!wait(&sh.x_done, c & 1)) break;
+      if (*reinterpret_cast<volatile int *>(&sh.odd_chunk) != c) {
         tc_fence_after();
-        const float dec = f->dec, sw = *reinterpret_cast<volatile float *>(&sh.scale_w[row]);
+        tmem_ld16(lanes + TXO + 64 * (c & 1) + j0, x);
+#pragma unroll
+        for (int j = 0; j < H; j += 4) {
+          const float4 fk = *reinterpret_cast<const float4 *>(f->fk + j0 + j);
+          x[j] = fmaf(-fk.x * scale_s, x[j], w[j]);
+          x[j + 1] = fmaf(-fk.y * scale_s, x[j + 1], w[j + 1]);
+          x[j + 2] = fmaf(-fk.z * scale_s, x[j + 2], w[j + 2]);
+          x[j + 3] = fmaf(-fk.w * scale_s, x[j + 3], w[j + 3]);
+        }
+        put(x, inv_r, TR);
+        tmem_st_wait();
+        tell(&sh.r_ready);
+        scale_for(bound, scale_u, inv_u);
+        scale_for(bound_w, scale_w, inv_w);
+        if (!wait(&sh.u_done, n_u & 1)) break;
+        tc_fence_after();
+        tmem_ld16(lanes + TU + j0, x);
+#pragma unroll
+        for (int j = 0; j < H; j += 4) {
+          const float4 st = *reinterpret_cast<const float4 *>(f->st + j0 + j), wk = *reinterpret_cast<const float4 *>(f->wk + j0 + j);
+          x[j] *= st.x * scale_r;
+          x[j + 1] *= st.y * scale_r;
+          x[j + 2] *= st.z * scale_r;
+          x[j + 3] *= st.w * scale_r;
+          w[j] = x[j] * wk.x;
+          w[j + 1] = x[j + 1] * wk.y;
+          w[j + 2] = x[j + 2] * wk.z;
+          w[j + 3] = x[j + 3] * wk.w;
+        }
+        put(w, inv_w, TW);
+        tmem_st_wait();
+        tell(&sh.w_ready);
+        put(x, inv_u, TUA);
+        tmem_st_wait();
+        tell(&sh.u_ready);
+        ++n_u;
+        if (c + 1 < chunks) look_at_v(c + 1);
+        const float dec = f->dec;
+        if (!wait(&sh.d_done, c & 1)) break;
+        tc_fence_after();
         float m4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < HK; i += 32) {
-          float x[32];
-          tmem_ld32_nowait(lanes + TD + group * HK + i, x);
-          tmem_ld_wait(x);
+          float d[32];
+          tmem_ld32_nowait(lanes + TD + group * HK + i, d);
+          tmem_ld_wait(d);
 #pragma unroll
           for (int j = 0; j < 32; j += 2) {
-            const f2 y = fma2(mk2(sw, sw), mk2(x[j], x[j + 1]), mul2(mk2(dec, dec), mk2(s[i + j], s[i + j + 1])));
+            const f2 y = fma2(mk2(scale_w, scale_w), mk2(d[j], d[j + 1]), mul2(mk2(dec, dec), mk2(s[i + j], s[i + j + 1])));
             s[i + j] = y.x;
             s[i + j + 1] = y.y;
             m4[(j >> 1) & 3] = fmaxf(m4[(j >> 1) & 3], fmaxf(fabsf(y.x), fabsf(y.y)));
@@ -1154,12 +1158,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) delta_walk_tc_kernel(const Chun
         }
         m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
         tc_fence_before();
-        if (group == 1) {
-          pending = true;
-          ++n_u;
-        }
+        pending = true;
         continue;
       }
+      if (!wait(&sh.d_done, c & 1)) break;
       // ---- token by token: an infinite or NaN value must not reach an earlier one
       const int len = min(C, n - c * C);
       const unsigned char *tile = ring + (c % kTcStages) * kStage;
@@ -1198,8 +1200,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) delta_walk_tc_kernel(const Chun
         }
       }
       m = largest();
+      if (c + 1 < chunks) look_at_v(c + 1);
     }
-    if (c == chunks && group == 1 && pending) outputs(chunks - 1, scale_s);
+    if (c == chunks && pending) outputs(chunks - 1, scale_s);
     if (c == chunks && a.d.state_out) {
       const int to = __ldg(a.d.state_out + b);
       if (to >= 0 && to < a.d.n_slots) {
