@@ -16,8 +16,10 @@ struct DeltaArgs {
 };
 
 constexpr int kDeltaChunk = 32;  // tokens of a chunk
-// sequences from this many tokens on go in chunks
-constexpr int kDeltaFirstLen = 24;
+// sequences from this many tokens on go in chunks.  Where the two meet (32 heads of 128, token by token / in chunks): 8 sequences of
+// 16 tokens 34 / 31 us and of 24 tokens 49 / 31, 32 of 16 tokens 80 / 92 and of 24 tokens 115 / 94, one of 24 tokens 18 / 22
+// and of 48 tokens 32 / 26
+constexpr int kDeltaFirstLen = 20;
 
 // the chunk kernels (qg_delta_chunk.cu), for sequences of first_len tokens and more
 size_t delta_chunk_workspace(const DeltaArgs &a);

@@ -157,12 +157,16 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 5) delta_prep_kernel(const Ch
   const int slot = static_cast<int>(blockIdx.x) / a.d.Hk, hk = static_cast<int>(blockIdx.x) % a.d.Hk;
   pdl_wait();
   pdl_launch_dependents();
-  // the sequence whose chunk this is
-  int lo = 0, hi = a.d.B;  // chunk_base(lo) <= slot < chunk_base(hi), as far as is known
+  // the sequence whose chunk this is: chunk_base(lo) <= slot < chunk_base(hi), as far as is known.  32 places a round, since a
+  // round costs a load's latency
+  int lo = 0, hi = a.d.B;
   while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (chunk_base(a.d, mid) <= slot) lo = mid;
-    else hi = mid;
+    const int step = (hi - lo + 31) / 32, at = lo + (lane + 1) * step;
+    const unsigned below = __ballot_sync(0xFFFFFFFFu, at < hi && chunk_base(a.d, min(at, hi - 1)) <= slot);
+    const int k = __ffs(~below) - 1;  // places up to the first above
+    const int base = lo;
+    lo = base + (below == 0xFFFFFFFFu ? 32 : k) * step;
+    hi = min(hi, lo + step);
   }
   const int t00 = qg::delta_tok(a.d, lo), n = qg::delta_tok(a.d, lo + 1) - t00;
   const int first = (slot - chunk_base(a.d, lo)) * C;
@@ -260,12 +264,13 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 5) delta_prep_kernel(const Ch
         *reinterpret_cast<uint32_t *>(t + LO + at) = l[0];
       }
     }
+  fence_proxy_async_smem();
   __syncthreads();
-  {
-    uint4 *dst = reinterpret_cast<uint4 *>(a.kq + (static_cast<size_t>(slot) * a.d.Hk + hk) * Tiles<DK>::kKQAll);
-    const uint4 *src = reinterpret_cast<const uint4 *>(tile);
-    for (int i = tid; i < Tiles<DK>::kKQAll / 16; i += kPrepWarps * 32) dst[i] = src[i];
-  }
+  if (tid == 0)  // the tiles leave as they lie, while the products are made of them
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n\tcp.async.bulk.commit_group;" ::"l"(
+                     a.kq + (static_cast<size_t>(slot) * a.d.Hk + hk) * Tiles<DK>::kKQAll),
+                 "r"(smem_u32(tile)), "r"(Tiles<DK>::kKQAll)
+                 : "memory");
   // products: warps 0, 1 keys with keys, 2, 3 queries with keys; 16 rows each
   {
     const uint32_t k0 = smem_u32(tile), rows = k0 + (warp >= 2 ? kBlock : 0);
@@ -297,6 +302,7 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 5) delta_prep_kernel(const Ch
         out[i][j] = c[t][e] * sr[i] * scale_k[j];
       }
   }
+  if (tid == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // T is turned in the tiles' room
   __syncthreads();
 
   // items: T of every value head, then the decayed Q K^T of every value head
@@ -371,19 +377,19 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 5) delta_prep_kernel(const Ch
 #pragma unroll
     for (int j = 0; j < C; ++j) M[lane][j] = j < lane ? ga.y * decay(j) * kk[lane][j] : 0.f;
     __syncwarp();
-    // a lane per column: (1 + A) X = 1 from the top, two sums a row
+    // a lane per column: (1 + A) X = 1 from the top, four sums a row
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-      float acc = i == lane ? 1.f : 0.f, acc2 = 0.f;
+      float acc[4] = {i == lane ? 1.f : 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int j4 = 0; j4 < i; j4 += 4) {
         const float4 m = *reinterpret_cast<const float4 *>(&M[i][j4]);
-        acc = fmaf(-m.x, w[j4], acc);
-        if (j4 + 1 < i) acc2 = fmaf(-m.y, w[j4 + 1], acc2);
-        if (j4 + 2 < i) acc = fmaf(-m.z, w[j4 + 2], acc);
-        if (j4 + 3 < i) acc2 = fmaf(-m.w, w[j4 + 3], acc2);
+        acc[0] = fmaf(-m.x, w[j4], acc[0]);
+        if (j4 + 1 < i) acc[1] = fmaf(-m.y, w[j4 + 1], acc[1]);
+        if (j4 + 2 < i) acc[2] = fmaf(-m.z, w[j4 + 2], acc[2]);
+        if (j4 + 3 < i) acc[3] = fmaf(-m.w, w[j4 + 3], acc[3]);
       }
-      w[i] = i < lane ? 0.f : acc + acc2;
+      w[i] = i < lane ? 0.f : (acc[0] + acc[1]) + (acc[2] + acc[3]);
     }
     __syncwarp();
 #pragma unroll
@@ -402,6 +408,7 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 5) delta_prep_kernel(const Ch
     write_row(w, ta, f->st);
     __syncwarp();
   }
+  if (tid == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 // ---- the walk ------------------------------------------------------------------------------------------
