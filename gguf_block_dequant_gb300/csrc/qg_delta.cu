@@ -18,12 +18,11 @@ using qg::DeltaArgs;
 // S^T k and S^T q, are summed in one pass over the registers (the output is e^g S^T q + (q . k) u), so a token
 // costs one exchange between warps.  Queries, keys and gates of up to TG tokens are made ready at a time, a warp per
 // token.
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
 constexpr int TG = 16;
 
-template <int DK, int JC>
-__global__ void __launch_bounds__(kThreads) delta_tokens_kernel(const DeltaArgs a, int first_len) {
+template <int DK, int JC, int NT>
+__global__ void __launch_bounds__(NT, NT == 128 ? 5 : 2) delta_tokens_kernel(const DeltaArgs a, int first_len) {
+  constexpr int kWarps = NT / 32;
   constexpr int CG = JC / 4;            // lanes side by side in a row
   constexpr int RPW = 32 / CG;          // row groups of a warp
   constexpr int NR = DK / (kWarps * RPW);  // rows of a thread
@@ -171,13 +170,13 @@ __global__ void __launch_bounds__(kThreads) delta_tokens_kernel(const DeltaArgs 
 
 template <int DK>
 cudaError_t tokens_launch(const DeltaArgs &a, int first_len, int sms, cudaStream_t s) {
-  // columns of a CTA: all that fit a register tile once there are CTAs for every SM, fewer for latency before
-  int jc = a.Dv % 128 == 0 ? 128 : a.Dv % 64 == 0 ? 64 : 32;
-  while (jc > 32 && static_cast<long long>(a.B) * a.Hv * (a.Dv / jc) < 2 * sms) jc /= 2;
-  const dim3 grid(static_cast<unsigned>(a.B) * a.Hv * (a.Dv / jc)), block(kThreads);
-  if (jc == 128) return qg::launch_pdl(delta_tokens_kernel<DK, 128>, grid, block, 0, s, a, first_len);
-  if (jc == 64) return qg::launch_pdl(delta_tokens_kernel<DK, 64>, grid, block, 0, s, a, first_len);
-  return qg::launch_pdl(delta_tokens_kernel<DK, 32>, grid, block, 0, s, a, first_len);
+  // 64 columns to a CTA of four warps, five of which share an SM, so that some read while others exchange or write (64 sequences of
+  // 32 heads of 128 x 128, 268 MB: 49.4 us, 5.4 TB/s; with eight warps 60, with 128 columns and eight warps 57.7, six CTAs an SM
+  // spill: 62.7); 32 columns to one of eight where that does not give two CTAs an SM (one sequence: 3.8 us)
+  const int jc = a.Dv % 64 == 0 && static_cast<long long>(a.B) * a.Hv * (a.Dv / 64) >= 2 * sms ? 64 : 32;
+  const dim3 grid(static_cast<unsigned>(a.B) * a.Hv * (a.Dv / jc));
+  if (jc == 64) return qg::launch_pdl(delta_tokens_kernel<DK, 64, 128>, grid, dim3(128), 0, s, a, first_len);
+  return qg::launch_pdl(delta_tokens_kernel<DK, 32, 256>, grid, dim3(256), 0, s, a, first_len);
 }
 
 qg_status check(const qg_delta_args *g, DeltaArgs *a) {
