@@ -244,42 +244,58 @@ __global__ void __launch_bounds__(kBookThreads) kv_reserve_kernel(const ReserveA
   for (int c = tid; c < copies; c += kBookThreads) atomicSub(a.refs + a.copies[3 * c], 1);
 }
 
+// x / d for x < 2^31 and the d that `mul` and `shift` were made for: mul = ceil(2^shift / d), shift = 31 + ceil(log2 d)
+struct Divisor {
+  unsigned long long mul;
+  int shift;
+  QG_DEVICE int of(int x) const { return static_cast<int>((static_cast<unsigned>(x) * mul) >> shift); }
+};
+Divisor divisor(int d) {
+  int l = 0;
+  while ((1LL << l) < d) ++l;
+  return {((1ULL << (31 + l)) + d - 1) / d, 31 + l};
+}
+
 // one geometry for all layers
 constexpr int kMaxLayers = 128;
 struct Pools {
   uint16_t *pool[2 * kMaxLayers];
   long long page_stride, token_stride, head_stride;
-  int n_pools, n_pages, shift, Hkv, c16;  // c16: 16-byte chunks per head row
+  int n_pools, n_pages, shift, Hkv, per_row, c_shift;  // 16-byte pieces of a token, and log2 of those of a head's row
+  Divisor by_row;                                      // by per_row
 };
+// offset of piece x of a page or token run, and its token
+QG_DEVICE long long piece_at(const Pools &a, int x, int &token) {
+  token = a.by_row.of(x);
+  const int y = x - token * a.per_row, h = y >> a.c_shift;
+  return h * a.head_stride + 8 * (y - (h << a.c_shift));
+}
 
-// A thread moves 16 bytes at a time, four under way; HBM-bound once there is much to move.
+// A thread moves 16 bytes at a time, eight under way; HBM-bound once there is much to move.
 __global__ void __launch_bounds__(256) page_copy_kernel(const __grid_constant__ Pools a, const int32_t *n_copies,
                                                         const int32_t *copies) {
   pdl_wait();
   pdl_launch_dependents();
   uint16_t *pool = a.pool[blockIdx.x];
-  const int n = *n_copies, per_row = a.Hkv * a.c16;
+  const int n = *n_copies;
   for (int c = blockIdx.y; c < n; c += gridDim.y) {
     const uint16_t *from = pool + copies[3 * c] * a.page_stride;
     uint16_t *to = pool + copies[3 * c + 1] * a.page_stride;
-    const long long places = static_cast<long long>(copies[3 * c + 2]) * per_row;
-    auto place = [&](long long x) {
-      const int r = static_cast<int>(x / per_row), y = static_cast<int>(x - static_cast<long long>(r) * per_row);
-      const int h = y / a.c16;
-      return r * a.token_stride + h * a.head_stride + 8 * (y - h * a.c16);
-    };
-    for (long long x = threadIdx.x; x < places; x += 4 * 256) {
-      uint4 v[4];
-      long long o[4];
+    const int pieces = copies[3 * c + 2] * a.per_row;
+    for (int x = threadIdx.x; x < pieces; x += 8 * 256) {
+      uint4 v[8];
+      long long o[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (x + 256 * i < places) {
-          o[i] = place(x + 256 * i);
+      for (int i = 0; i < 8; ++i)
+        if (x + 256 * i < pieces) {
+          int r;
+          o[i] = piece_at(a, x + 256 * i, r);
+          o[i] += r * a.token_stride;
           v[i] = *reinterpret_cast<const uint4 *>(from + o[i]);
         }
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (x + 256 * i < places) *reinterpret_cast<uint4 *>(to + o[i]) = v[i];
+      for (int i = 0; i < 8; ++i)
+        if (x + 256 * i < pieces) *reinterpret_cast<uint4 *>(to + o[i]) = v[i];
     }
   }
 }
@@ -325,9 +341,8 @@ __global__ void __launch_bounds__(256) kv_compact_kernel(const __grid_constant__
     to[tid] = t;
   }
   __syncthreads();
-  const int per_row = a.p.Hkv * a.p.c16, places = kCompactTokens * per_row;
   const int q0 = blockIdx.y * a.pools_per_block, q1 = min(a.p.n_pools, q0 + a.pools_per_block);
-  const int all = (q1 - q0) * places;
+  const int all = (q1 - q0) * kCompactTokens * a.p.per_row;
   for (int x = tid; x < all; x += 8 * 256) {
     uint4 v[8];
     uint16_t *dst[8];
@@ -336,10 +351,11 @@ __global__ void __launch_bounds__(256) kv_compact_kernel(const __grid_constant__
       const int y = x + 256 * i;
       dst[i] = nullptr;
       if (y < all) {
-        const int q = y / places, z = y - q * places, r = z / per_row, w = z - r * per_row, h = w / a.p.c16;
+        int t;  // the tile's tokens in the first pool, then in the next
+        const long long o = piece_at(a.p, y, t);
+        const int r = t % kCompactTokens;
         if (to[r] >= 0) {
-          const long long o = h * a.p.head_stride + 8 * (w - h * a.p.c16);
-          uint16_t *pool = a.p.pool[q0 + q];
+          uint16_t *pool = a.p.pool[q0 + t / kCompactTokens];
           v[i] = *reinterpret_cast<const uint4 *>(pool + from[r] + o);
           dst[i] = pool + to[r] + o;
         }
@@ -374,7 +390,9 @@ qg_status check_pools(const qg_kv_cache *caches, int n_layers, Pools *out) {
   out->n_pages = first.n_pages;
   out->shift = first.page_shift;
   out->Hkv = first.Hkv;
-  out->c16 = first.D / 8;
+  out->per_row = first.Hkv * (first.D / 8);
+  out->c_shift = first.D == 64 ? 3 : first.D == 128 ? 4 : 5;
+  out->by_row = divisor(out->per_row);
   return QG_OK;
 }
 
