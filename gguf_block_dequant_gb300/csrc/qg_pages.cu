@@ -75,7 +75,9 @@ __global__ void __launch_bounds__(128) kv_fork_kernel(const ForkArgs a) {
 // ---- reserve --------------------------------------------------------------------------------------
 // One block does the books: what each sequence needs (a scan gives its place among the free pages), the
 // free pages in rising order (a scan over the counts until there are enough), then the page lists and the
-// counts.  A second kernel copies the begun pages that were shared, its blocks over layers and sequences.
+// counts.  A second kernel copies the begun pages that were shared, its blocks over layers and sequences.  Latency bounds the books
+// (about 4 us for 60 sequences and 160 pages: three loads in a chain, three block scans); a large pool costs a round of
+// kBookThreads x kBookEach counts each, with the next round's on their way.
 // Workspace: the number of copies; (old page, new page, rows) of each; the needs' running sums; the free pages.
 constexpr int kBookThreads = 512;
 constexpr int kBookFree = 4096;  // free pages kept in shared memory
@@ -271,7 +273,8 @@ QG_DEVICE long long piece_at(const Pools &a, int x, int &token) {
   return h * a.head_stride + 8 * (y - (h << a.c_shift));
 }
 
-// A thread moves 16 bytes at a time, eight under way; HBM-bound once there is much to move.
+// A thread moves 16 bytes at a time, eight under way; HBM-bound once there is much to move (48 begun pages in
+// 36 layers, 79 MB: fork, books and copy together 20.3 us, the copy about 13).
 __global__ void __launch_bounds__(256) page_copy_kernel(const __grid_constant__ Pools a, const int32_t *n_copies,
                                                         const int32_t *copies) {
   pdl_wait();
@@ -302,7 +305,8 @@ __global__ void __launch_bounds__(256) page_copy_kernel(const __grid_constant__ 
 
 // ---- compact --------------------------------------------------------------------------------------
 // A block owns a few tokens: it looks their places up once (a chain of loads) and moves them in several
-// pools, 16 bytes a thread and several under way: HBM bounds it.
+// pools, 16 bytes a thread and several under way: HBM bounds it (1550 tokens in 36 layers, 460 MB: 74.2 us, 6.2 TB/s, 0.93 of
+// the copy).
 constexpr int kCompactTokens = 8;
 struct CompactArgs {
   Pools p;
