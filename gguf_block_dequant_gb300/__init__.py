@@ -607,12 +607,27 @@ class DeltaArgs(ctypes.Structure):
 _delta_pack = struct.Struct("10i2f6P5q3Pq4Pq").pack  # the same fields in one go: a structure's cost more than the call
 
 
+_current_device = None
+
+
+def _here(d):
+    """Refuses a GPU that is not the current one: a launch goes to that one, whatever the addresses."""
+    global _current_device
+    if _current_device is None:
+        import torch
+
+        _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    if d is not None and d >= 0 and d != _current_device():
+        raise ValueError(f"the tensors' GPU {d} must be the current one")
+    return d
+
+
 def _gpu(t, what):
     """The GPU of the tensor that the others of a call have to be with."""
     d = t.get_device()
     if d < 0:
         raise ValueError(f"{what} must be on a GPU")
-    return d
+    return _here(d)
 
 
 def _addr(t):
@@ -727,7 +742,7 @@ def draft_verify(probs, tokens, u, u_next, accepted, next_token, draft_probs=Non
 
 def _page_call(caches, batch, refs):
     _ints(refs, caches[0].n_pages, "refs")
-    return _cache_device(caches, batch)
+    return _here(_cache_device(caches, batch))
 
 
 def kv_fork(caches, batch, refs, src=None, keep=None, stream=None):
@@ -758,6 +773,6 @@ def kv_compact(caches, batch, src, keep_start, keep, stream=None):
     _ints(src, batch.n_seqs, "src")
     _ints(keep_start, batch.n_seqs + 1, "keep_start")
     _ints(keep, keep.numel(), "keep")
-    _on(_cache_device(caches, batch), "src keep_start keep", src, keep_start, keep)
+    _on(_here(_cache_device(caches, batch)), "src keep_start keep", src, keep_start, keep)
     _call("qg_kv_compact", caches, len(caches), ctypes.byref(batch), _ptr(src), _ptr(keep_start), _ptr(keep), keep.numel(),
           _stream(stream))

@@ -24,12 +24,36 @@ LENGTHS = [[1], [1, 1, 1], [5], [0, 3, 0, 1], [31, 32, 33], [64, 1, 0, 47], [17,
 
 
 @pytest.mark.parametrize("n", LENGTHS, ids=str)
-@pytest.mark.parametrize("Dk,Dv", [(128, 128), (64, 32), (64, 96), (128, 256), (128, 64)])
+@pytest.mark.parametrize("Dk,Dv", [(128, 128), (64, 32), (64, 96), (128, 256), (128, 64), (64, 128)])
 def test_lengths_and_widths(qg, n, Dk, Dv):
     B = len(n)
     c = Delta(n, Dk=Dk, Dv=Dv, ins=[3 * b + 1 if b % 3 != 2 else -1 for b in range(B)], outs=[3 * b + 2 for b in range(B)], seed=B + n[0])
     c.check(c.run(qg))
     assert qg.device_status() == 0
+
+
+@pytest.mark.parametrize("Dv", [128, 32])
+def test_many_sequences(qg, Dv):
+    """More sequences than are put in order, and than a round of the search looks at; lengths on both sides of the border."""
+    n = [(7 * b) % 67 for b in range(150)]
+    c = Delta(n, Hk=1, Hv=2, Dk=64, Dv=Dv, ins=[b if b % 4 else -1 for b in range(150)], outs=[150 + b for b in range(150)], seed=4)
+    c.check(c.run(qg))
+    assert qg.device_status() == 0
+
+
+@pytest.mark.parametrize("n", [[0], [0, 0, 0]], ids=str)
+def test_nothing_to_do(qg, n):
+    c = Delta(n, Dv=32, ins=[0] * len(n), outs=[1] * len(n), behind=4, seed=3)
+    c.check(c.run(qg))
+
+
+@pytest.mark.parametrize("n", [[19, 20, 21], [52, 63, 65]], ids=str)
+def test_later_magnitudes(qg, n):
+    """Values that grow by a million within a chunk: earlier tokens keep their own precision."""
+    c = Delta(n, ins=[0, 1, 2], outs=[3, 4, 5], seed=2)
+    v = c.parts(c.x, c.ba)[2]
+    v *= torch.logspace(-3, 3, c.T)[:, None, None]
+    c.check(c.run(qg))
 
 
 @pytest.mark.parametrize("Hk,Hv,tiled", [(1, 1, False), (3, 3, True), (2, 8, False), (2, 8, True), (16, 32, False)])
