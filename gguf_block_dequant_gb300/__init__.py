@@ -442,6 +442,7 @@ def kv_caches(ks, vs):
     arr = Caches(*cs)
     arr.tensors = [c.tensors for c in cs]
     arr.device = cs[0].device if cs else None
+    arr.pages = cs[0].n_pages if cs else 0
     return arr
 
 
@@ -677,6 +678,8 @@ def delta_rule(q, k, v, a, b, states, state_in, state_out, out, workspace=None, 
     if len(shape) != 3 or len(vshape) != 3 or shape != k.shape or vshape[0] != shape[0]:
         raise ValueError("q and k must be [T][Hk][Dk] and v [T][Hv][Dv]")
     (T, Hk, Dk), (_, Hv, Dv) = shape, vshape
+    if out.shape != vshape or a.shape != (T, Hv) or b.shape != (T, Hv):
+        raise ValueError("out must be [T][Hv][Dv], a and b [T][Hv]")
     f32 = _types()[0]
     if not (q.dtype is k.dtype is v.dtype is a.dtype is b.dtype is out.dtype is f32):
         raise ValueError("q, k, v, a, b and out must be f32")
@@ -696,11 +699,21 @@ def delta_rule(q, k, v, a, b, states, state_in, state_out, out, workspace=None, 
         slots, slot = sshape[0], st[0] if sshape[0] > 1 else Hv * Dk * Dv
     _on(_gpu(q, "q"), "k v a b states state_in state_out state_each out q_start a_scale a_bias workspace", k, v, a, b, states,
         state_in, state_out, state_each, out, q_start, a_scale, a_bias, workspace)
+
+    def rows(t, H, D):  # a token's heads lie side by side; tokens may be slices of wider rows
+        st = t.stride()
+        if st[2] != 1 or (H > 1 and st[1] != D):
+            raise ValueError("a token's heads must lie side by side")
+        return st[0] if T > 1 else H * D
+
+    ast, bst = a.stride(), b.stride()
+    if Hv > 1 and (ast[1] != 1 or bst[1] != 1):
+        raise ValueError("a token's gates must lie side by side")
     p = _addr
     g = _delta_pack(n, T, int(max_new), Hk, Hv, Dk, Dv, 1 if tiled else 0, 0 if l2norm_eps is None else 1, slots,
-                    float(l2norm_eps or 0.0), float(scale), p(q_start), p(q), p(k), p(v), p(a), p(b), _rows(q, T, Hk * Dk, "q"),
-                    _rows(k, T, Hk * Dk, "k"), _rows(v, T, Hv * Dv, "v"), _rows(a, T, Hv, "a"), _rows(b, T, Hv, "b"), p(a_scale),
-                    p(a_bias), p(states), slot, p(state_in), p(state_out), p(state_each), p(out), _rows(out, T, Hv * Dv, "out"))
+                    float(l2norm_eps or 0.0), float(scale), p(q_start), p(q), p(k), p(v), p(a), p(b), rows(q, Hk, Dk),
+                    rows(k, Hk, Dk), rows(v, Hv, Dv), ast[0] if T > 1 else Hv, bst[0] if T > 1 else Hv, p(a_scale), p(a_bias),
+                    p(states), slot, p(state_in), p(state_out), p(state_each), p(out), rows(out, Hv, Dv))
     _call("qg_delta_rule", g, _ptr(workspace), _nbytes(workspace), _stream(stream))
     return out
 
@@ -741,7 +754,7 @@ def draft_verify(probs, tokens, u, u_next, accepted, next_token, draft_probs=Non
 
 
 def _page_call(caches, batch, refs):
-    _ints(refs, caches[0].n_pages, "refs")
+    _ints(refs, getattr(caches, "pages", None) or caches[0].n_pages, "refs")
     return _here(_cache_device(caches, batch))
 
 
