@@ -130,10 +130,18 @@ template <int NV>
 __global__ void __launch_bounds__(kProbThreads) probs_kernel(const ProbArgs a) {
   __shared__ float red[kProbWarps], reds[kProbWarps];
   __shared__ int redi[kProbWarps];
-  __shared__ float cta_m, cta_s;
-  __shared__ int cta_i;
+  __shared__ __align__(16) float4 told[8];  // (maximum, sum, index) of each CTA
+  __shared__ uint64_t told_bar;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int row = static_cast<int>(blockIdx.x) / a.cs, rank = static_cast<int>(blockIdx.x) % a.cs;
+  if (a.cs > 1) {
+    if (tid == 0) {
+      mbar_init(&told_bar, 1);
+      fence_mbar_init();
+    }
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // its other half is where it is needed
+  }
   pdl_wait();
   pdl_launch_dependents();
   const long long r0 = static_cast<long long>(row) * a.V, r1 = r0 + a.V;  // elements of the tensor
@@ -195,14 +203,15 @@ __global__ void __launch_bounds__(kProbThreads) probs_kernel(const ProbArgs a) {
   float M = m, S = s;
   int best = at;
   if (a.cs > 1) {
-    if (tid == 0) cta_m = m, cta_s = s, cta_i = at;
-    cluster_sync();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (tid == 0) mbar_arrive_expect_tx(&told_bar, 16 * a.cs);
+    if (tid < a.cs) tell_remote(&told[rank], make_float4(m, s, __int_as_float(at), 0.f), &told_bar, tid);
+    if (!mbar_wait(&told_bar, 0)) atomicOr(&g_qg_status_draft, QG_STATUS_BIT_TIMEOUT);
     // a lane per CTA
-    const uint32_t r = lane & (a.cs - 1);
-    const float om = remote_f32(&cta_m, r), os = remote_f32(&cta_s, r);
-    const int oi = remote_s32(&cta_i, r);
+    const float4 other = told[lane & (a.cs - 1)];
+    const float om = other.x, os = other.y;
     M = om;
-    best = oi;
+    best = __float_as_int(other.z);
     for (int o = a.cs / 2; o; o >>= 1) {
       const float y = __shfl_xor_sync(0xFFFFFFFFu, M, o);
       const int j = __shfl_xor_sync(0xFFFFFFFFu, best, o);
@@ -210,7 +219,6 @@ __global__ void __launch_bounds__(kProbThreads) probs_kernel(const ProbArgs a) {
     }
     S = om > -INFINITY && M < INFINITY ? os * ex2(fmaxf((0.5f * om - 0.5f * M) * c, -200.f)) : 0.f;
     for (int o = a.cs / 2; o; o >>= 1) S += __shfl_xor_sync(0xFFFFFFFFu, S, o);
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // this CTA has read the others
   }
   const bool none = !(M > -INFINITY && M < INFINITY);
   const float f = none || greedy || !finite ? 0.f : ex2(fmaxf((0.5f * m - 0.5f * M) * c, -200.f)) / S;
@@ -236,7 +244,6 @@ __global__ void __launch_bounds__(kProbThreads) probs_kernel(const ProbArgs a) {
       }
     }
   }
-  if (a.cs > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // nobody leaves while it is read
 }
 
 // The same for many rows that start at 16-byte boundaries: clusters stay on their SMs and take every so many-th row, and a CTA's slice
@@ -547,11 +554,12 @@ QG_DEVICE Sum shfl_xor(Sum a, int o) {
   return {__shfl_xor_sync(0xFFFFFFFFu, a.s, o), __shfl_xor_sync(0xFFFFFFFFu, a.e, o)};
 }
 QG_DEVICE Sum shfl(Sum a, int i) { return {__shfl_sync(0xFFFFFFFFu, a.s, i), __shfl_sync(0xFFFFFFFFu, a.e, i)}; }
-// running sums over the lanes
+// running sums over the first N lanes
+template <int N>
 QG_DEVICE Sum scan(Sum a) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
+  for (int o = 1; o < N; o <<= 1) {
     const Sum y = shfl_up(a, o);
     if (lane >= o) a = y + a;
   }
@@ -563,15 +571,27 @@ QG_DEVICE Sum scan(Sum a) {
 template <int NT>
 __global__ void __launch_bounds__(NT, 1024 / NT) draft_verify_kernel(const VerifyArgs a) {
   constexpr int kVerThreads = NT, kVerWarps = NT / 32;
-  __shared__ Sum wsum[kVerWarps], cta_sum, s_rest;
-  __shared__ int wlast[kVerWarps], cta_last, stop, found, tail, s_pick;  // s_pick: the warp whose range is searched
+  __shared__ Sum wsum[kVerWarps], s_rest;
+  __shared__ int wlast[kVerWarps], stop, found, tail, s_pick;  // s_pick: the warp whose range is searched
+  __shared__ __align__(16) float4 told[2][8];  // (sum, its error, last element with mass) of each CTA, for both passes
+  __shared__ uint64_t told_bar[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = static_cast<int>(blockIdx.x) / a.cs, rank = static_cast<int>(blockIdx.x) % a.cs;
+  if (a.cs > 1) {
+    if (tid == 0) {
+      mbar_init(&told_bar[0], 1);
+      mbar_init(&told_bar[1], 1);
+      fence_mbar_init();
+    }
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // its other half is where it is needed
+  }
   pdl_wait();
   pdl_launch_dependents();
   auto start = [&](int i) { return a.q_start ? max(0, min(a.T, __ldg(a.q_start + i))) : min(i, a.T); };
   const int t0 = start(b), t1 = start(b + 1);
   if (t1 <= t0) {  // the whole cluster leaves
+    if (a.cs > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     if (rank == 0 && tid == 0) {
       a.accepted[b] = 0;
       a.next_token[b] = -1;
@@ -614,11 +634,11 @@ __global__ void __launch_bounds__(NT, 1024 / NT) draft_verify_kernel(const Verif
   auto range = [&](int w) { return edge(rank * a.slice + min(a.slice, w * a.sub)); };
   const int wlo = range(warp), whi = range(warp + 1);
   for (int pass = 0; pass < 2; ++pass) {
-    // this warp's sum and its last element with mass
-    Sum s{0.f, 0.f};
+    // this warp's sum, in two chains, and its last element with mass
+    Sum s{0.f, 0.f}, s2{0.f, 0.f};
     int last = -1;
     auto take = [&](float x, int v) {
-      add_kept(s, x);
+      add_kept(v & 1 ? s2 : s, x);
       if (x > 0.f) last = v;
     };
     const int head = min(whi - wlo, wlo == 0 ? skew : 0);
@@ -627,13 +647,18 @@ __global__ void __launch_bounds__(NT, 1024 / NT) draft_verify_kernel(const Verif
 #pragma unroll 5
     for (int i = lane; i < body; i += 32) {
       const float4 x = r.at4(from + 4 * i);
-      take(x.x, from + 4 * i);
-      take(x.y, from + 4 * i + 1);
-      take(x.z, from + 4 * i + 2);
-      take(x.w, from + 4 * i + 3);
+      add_kept(s, x.x);
+      add_kept(s2, x.y);
+      add_kept(s, x.z);
+      add_kept(s2, x.w);
+      const int v = from + 4 * i;
+      if (x.x > 0.f) last = v;
+      if (x.y > 0.f) last = v + 1;
+      if (x.z > 0.f) last = v + 2;
+      if (x.w > 0.f) last = v + 3;
     }
     for (int v = from + 4 * body + lane; v < whi; v += 32) take(r.at(v), v);
-    s = normal(s.s, s.e);
+    s = normal(s.s, s.e) + normal(s2.s, s2.e);
 #pragma unroll
     for (int o = 16; o; o >>= 1) s = s + shfl_xor(s, o);
     last = __reduce_max_sync(0xFFFFFFFFu, last);
@@ -643,25 +668,27 @@ __global__ void __launch_bounds__(NT, 1024 / NT) draft_verify_kernel(const Verif
     }
     __syncthreads();
     // running sums of the CTA's warps, in every warp alike
-    Sum run = scan(lane < kVerWarps ? wsum[lane] : Sum{0.f, 0.f});
+    Sum run = scan<kVerWarps>(lane < kVerWarps ? wsum[lane] : Sum{0.f, 0.f});
     const Sum own = shfl(run, kVerWarps - 1);
     const int own_last = __reduce_max_sync(0xFFFFFFFFu, lane < kVerWarps ? wlast[lane] : -1);
     Sum total = own, before{0.f, 0.f};
     int all_last = own_last, pick = 0;
     Sum want = times(total, u);
     if (a.cs > 1) {
-      if (tid == 0) {
-        cta_sum = own;
-        cta_last = own_last;
-      }
-      cluster_sync();
+      // every CTA tells every other
+      if (pass == 0) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+      if (tid == 0) mbar_arrive_expect_tx(&told_bar[pass], 16 * a.cs);
+      if (tid < a.cs)
+        tell_remote(&told[pass][rank], make_float4(own.s, own.e, __int_as_float(own_last), 0.f), &told_bar[pass], tid);
+      if (!mbar_wait(&told_bar[pass], 0)) atomicOr(&g_qg_status_draft, QG_STATUS_BIT_TIMEOUT);
       Sum x{0.f, 0.f};
       int l = -1;
       if (lane < a.cs) {
-        x = {remote_f32(&cta_sum.s, lane), remote_f32(&cta_sum.e, lane)};
-        l = remote_s32(&cta_last, lane);
+        const float4 other = told[pass][lane];
+        x = {other.x, other.y};
+        l = __float_as_int(other.z);
       }
-      const Sum upto = scan(x);
+      const Sum upto = scan<8>(x);
       total = shfl(upto, a.cs - 1);
       all_last = __reduce_max_sync(0xFFFFFFFFu, l);
       // the first CTA whose running sum passes the threshold: every CTA finds the same
@@ -673,7 +700,6 @@ __global__ void __launch_bounds__(NT, 1024 / NT) draft_verify_kernel(const Verif
     if (!(total.s > 0.f) && pass == 0 && refused) {  // nothing is left of the difference: the row itself
       r.q = nullptr;
       r.x = -1;
-      if (a.cs > 1) cluster_sync();  // the sums are written again
       __syncthreads();
       continue;
     }
@@ -701,10 +727,10 @@ __global__ void __launch_bounds__(NT, 1024 / NT) draft_verify_kernel(const Verif
       const int v0 = min(hi, lo + tid * each), v1 = min(hi, v0 + each);
       Sum c{0.f, 0.f};
       for (int v = v0; v < v1; ++v) add_kept(c, r.at(v));
-      const Sum incl = scan(normal(c.s, c.e));
+      const Sum incl = scan<32>(normal(c.s, c.e));
       if (lane == 31) wsum[warp] = incl;  // warp 0 has read the ranges' sums
       __syncthreads();
-      const Sum warps = scan(lane < kVerWarps ? wsum[lane] : Sum{0.f, 0.f});
+      const Sum warps = scan<kVerWarps>(lane < kVerWarps ? wsum[lane] : Sum{0.f, 0.f});
       Sum sum = shfl_up(incl, 1);
       if (lane == 0) sum = {0.f, 0.f};
       const Sum w0 = shfl(warps, max(warp - 1, 0));
@@ -724,7 +750,6 @@ __global__ void __launch_bounds__(NT, 1024 / NT) draft_verify_kernel(const Verif
     }
     break;
   }
-  if (a.cs > 1) cluster_sync();  // nobody leaves while its shared memory is being read
   if (rank == 0 && tid == 0) {
     a.accepted[b] = t - t0;
     if (a.kept_len) a.kept_len[b] = a.kv_len[b] - (t1 - 1 - t);
@@ -760,6 +785,7 @@ qg_status qg_token_probs(const float *logits, const float *temperature, int T, i
   if (!dev.ok) return QG_ECUDA;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   // CTAs per row: as many as hold the row in registers, and more to occupy the SMs when there are few rows
+  g_launched = true;
   constexpr int kHold = 4 * kProbThreads;  // elements a CTA holds in one vector a thread
   int cs = 1;
   while (cs < 8 && (V + 3 > int64_t(cs) * 10 * kHold || (int64_t(T) * cs < 2 * dev.sms && V > int64_t(cs) * kHold))) cs *= 2;
