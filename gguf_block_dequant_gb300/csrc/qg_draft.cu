@@ -88,7 +88,7 @@ int clusters_at_once(const void *kern, unsigned threads, size_t smem, int cluste
 // A row is split over a cluster of CTAs; each keeps its slice in registers, so a logit is read once and a
 // probability written once (8 bytes an element: HBM bounds it).  Slices start at 16-byte boundaries of the
 // whole tensor, so that rows of odd lengths still move 16 bytes at a time; only a row's two ends are moved by
-// elements (5 rows of 151936: 6.2 us, most of it the launch, the reads and the exchange one after another).  Each CTA sums the exponentials against its own maximum; one exchange of (maximum, sum) gives every
+// elements (5 rows of 151936: 4.8 us, the launch, the reads, the exchange and the writes one after another).  Each CTA sums the exponentials against its own maximum; one exchange of (maximum, sum) gives every
 // CTA its factor.  Exponentials are powers of two of (x/2 - m/2) (2 log2(e) / t): the half difference stays finite, six
 // instructions an element.
 constexpr int kProbThreads = 512;
@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(kProbThreads) probs_kernel(const ProbArgs a) {
 
 // The same for many rows that start at 16-byte boundaries: clusters stay on their SMs and take every so many-th row, and a CTA's slice
 // of the next row is copied to shared memory while this one's, in registers, is worked on and written, so that reads, exchanges and writes
-// of different rows overlap (200 rows of 151936, 243 MB: 45.4 us, 5.4 TB/s, 0.80 of the copy; the kernel above 59.8; with a cluster
+// of different rows overlap (200 rows of 151936, 243 MB: 44.7 us, 5.4 TB/s, 0.81 of the copy; the kernel above 59.8; with a cluster
 // barrier for the exchange, which waits for the writes of the row before, 59.4).
 template <int NV>
 __global__ void __launch_bounds__(kProbThreads, 2) probs_stream_kernel(const ProbArgs a, int clusters) {
@@ -566,7 +566,7 @@ QG_DEVICE Sum scan(Sum a) {
   return a;
 }
 
-// NT threads a CTA: 256 keep 64 sequences' CTAs on the SMs all at once (22 us; 35 with 512), 1024 read a slice in one round of
+// NT threads a CTA: 256 keep 64 sequences' CTAs on the SMs all at once (20 us; 35 with 512), 1024 read a slice in one round of
 // loads where there are few sequences
 template <int NT>
 __global__ void __launch_bounds__(NT, 1024 / NT) draft_verify_kernel(const VerifyArgs a) {

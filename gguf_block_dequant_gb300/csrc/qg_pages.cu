@@ -274,7 +274,7 @@ QG_DEVICE long long piece_at(const Pools &a, int x, int &token) {
 }
 
 // A thread moves 16 bytes at a time, eight under way; HBM-bound once there is much to move (48 begun pages in
-// 36 layers, 79 MB: fork, books and copy together 20.3 us, the copy about 13).
+// 36 layers, 79 MB: fork, books and copy together 20.5 us, the copy about 13).
 __global__ void __launch_bounds__(256) page_copy_kernel(const __grid_constant__ Pools a, const int32_t *n_copies,
                                                         const int32_t *copies) {
   pdl_wait();
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(256) page_copy_kernel(const __grid_constant__ 
 
 // ---- compact --------------------------------------------------------------------------------------
 // A block owns a few tokens: it looks their places up once (a chain of loads) and moves them in several
-// pools, 16 bytes a thread and several under way: HBM bounds it (1550 tokens in 36 layers, 460 MB: 74.2 us, 6.2 TB/s, 0.93 of
+// pools, 16 bytes a thread and several under way: HBM bounds it (1550 tokens in 36 layers, 460 MB: 73.5 us, 6.3 TB/s, 0.94 of
 // the copy).
 constexpr int kCompactTokens = 8;
 struct CompactArgs {
