@@ -702,6 +702,7 @@ __global__ void __launch_bounds__(W * 32) delta_walk_kernel(const ChunkArgs a) {
       // an infinite or NaN value among these tokens: one after another, so that none reaches an earlier one
       const int len = min(C, n - c * C);
       const unsigned char *tile = ring + st * kStage;
+      bool gone = false;
       for (int j = 0; j < len; ++j) {
         const float al = f->alpha[j], be = f->beta[j], sk = f->sk[j], sq = f->sq[j];
         auto both = [&](int ct, float2 &k, float2 &q) {
@@ -1177,6 +1178,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) delta_walk_tc_kernel(const Chun
       // ---- token by token: an infinite or NaN value must not reach an earlier one
       const int len = min(C, n - c * C);
       const unsigned char *tile = ring + (c % kTcStages) * kStage;
+      bool gone = false;
       for (int j = 0; j < len; ++j) {
         const float al = f->alpha[j], be = f->beta[j], sk = f->sk[j], sq = f->sq[j];
         auto pair = [&](int i, float2 &k, float2 &q) {  // rows i and i + 1 of this thread's half
@@ -1199,6 +1201,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) delta_walk_tc_kernel(const Chun
         }
         sh.ex[j & 1][group][row] = make_float4(x, y, z, 0.f);
         named_bar_sync(1, 256);
+        gone = __any_sync(0xFFFFFFFFu, *abort_flag != 0);
+        if (gone) break;
         const float4 other = sh.ex[j & 1][group ^ 1][row];
         const long long t = static_cast<long long>(c) * C + j;
         const float u = be * (__ldg(vp + t * a.d.v_stride) - al * (x + other.x));
@@ -1211,9 +1215,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) delta_walk_tc_kernel(const Chun
           s[i + 1] = fmaf(k.y, u, al * s[i + 1]);
         }
       }
+      if (gone) break;
       m = largest();
       if (c + 1 < chunks) look_at_v(c + 1);
     }
+    // a warp that gave up does not keep the others at the barrier that they may be at; behind it they see that it did
+    if (c < chunks) asm volatile("bar.arrive 1, 256;" ::: "memory");
     if (c == chunks && pending) outputs(chunks - 1, scale_s);
     if (c == chunks && a.d.state_out) {
       const int to = __ldg(a.d.state_out + b);
