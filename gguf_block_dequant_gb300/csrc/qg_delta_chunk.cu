@@ -378,23 +378,70 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 5) delta_prep_kernel(const Ch
 #pragma unroll
     for (int j = 0; j < C; ++j) M[lane][j] = j < lane ? ga.y * decay(j) * kk[lane][j] : 0.f;
     __syncwarp();
-    // a lane per column: (1 + A) X = 1 from the top, four sums a row
+    // (1 + A) T = 1 in blocks of 16.  Both diagonal blocks at once, a lane per column, from the top, four sums a row
+    constexpr int H = C / 2;
+    const int blk = lane / H, col = lane % H;
+    float x[H];
 #pragma unroll
-    for (int i = 0; i < C; ++i) {
-      float acc[4] = {i == lane ? 1.f : 0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < H; ++i) {
+      float acc[4] = {i == col ? 1.f : 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int j4 = 0; j4 < i; j4 += 4) {
-        const float4 m = *reinterpret_cast<const float4 *>(&M[i][j4]);
-        acc[0] = fmaf(-m.x, w[j4], acc[0]);
-        if (j4 + 1 < i) acc[1] = fmaf(-m.y, w[j4 + 1], acc[1]);
-        if (j4 + 2 < i) acc[2] = fmaf(-m.z, w[j4 + 2], acc[2]);
-        if (j4 + 3 < i) acc[3] = fmaf(-m.w, w[j4 + 3], acc[3]);
+        const float4 m = *reinterpret_cast<const float4 *>(&M[blk * H + i][blk * H + j4]);
+        acc[0] = fmaf(-m.x, x[j4], acc[0]);
+        if (j4 + 1 < i) acc[1] = fmaf(-m.y, x[j4 + 1], acc[1]);
+        if (j4 + 2 < i) acc[2] = fmaf(-m.z, x[j4 + 2], acc[2]);
+        if (j4 + 3 < i) acc[3] = fmaf(-m.w, x[j4 + 3], acc[3]);
       }
-      w[i] = i < lane ? 0.f : (acc[0] + acc[1]) + (acc[2] + acc[3]);
+      x[i] = i < col ? 0.f : (acc[0] + acc[1]) + (acc[2] + acc[3]);
+    }
+    // then T21 = -T22 (A21 T11): lanes col and col + 16 make column col, rows of one parity each
+    float y[H];
+    {
+      float t[H];
+#pragma unroll
+      for (int j = 0; j < H; ++j) t[j] = __shfl_sync(0xFFFFFFFFu, x[j], col);
+#pragma unroll
+      for (int r = 0; r < H; r += 2) {
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < H; j += 4) {
+          const float4 m = *reinterpret_cast<const float4 *>(&M[H + r + blk][j]);
+          acc[0] = fmaf(-m.x, t[j], acc[0]);
+          acc[1] = fmaf(-m.y, t[j + 1], acc[1]);
+          acc[2] = fmaf(-m.z, t[j + 2], acc[2]);
+          acc[3] = fmaf(-m.w, t[j + 3], acc[3]);
+        }
+        const float own = (acc[0] + acc[1]) + (acc[2] + acc[3]), other = __shfl_xor_sync(0xFFFFFFFFu, own, H);
+        y[r] = blk ? other : own;
+        y[r + 1] = blk ? own : other;
+      }
     }
     __syncwarp();
+    const float beta_col = __shfl_sync(0xFFFFFFFFu, ga.y, col);
 #pragma unroll
-    for (int i = 0; i < C; ++i) M[i][lane] = i < lane ? 0.f : w[i] * ga.y;
+    for (int i = 0; i < H; ++i) M[blk * H + i][lane] = blk ? x[i] : x[i] * ga.y;  // T22 goes into a product first
+    __syncwarp();
+#pragma unroll
+    for (int r = 0; r < H; r += 2) {
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int j = 0; j < r + 2; j += 4) {
+        const float4 m = *reinterpret_cast<const float4 *>(&M[H + r + blk][H + j]);
+        acc[0] = fmaf(m.x, y[j], acc[0]);
+        acc[1] = fmaf(m.y, y[j + 1], acc[1]);
+        if (j + 2 < r + 2) {
+          acc[2] = fmaf(m.z, y[j + 2], acc[2]);
+          acc[3] = fmaf(m.w, y[j + 3], acc[3]);
+        }
+      }
+      M[H + r + blk][col] = beta_col * ((acc[0] + acc[1]) + (acc[2] + acc[3]));
+    }
+    __syncwarp();
+    if (blk) {
+#pragma unroll
+      for (int i = 0; i < H; ++i) M[H + i][lane] = x[i] * ga.y;
+    }
     __syncwarp();
 #pragma unroll
     for (int j = 0; j < C; j += 4) {
