@@ -149,9 +149,9 @@ constexpr int kTurn = C + 4;  // floats of a row there
 template <int DK>
 __global__ void __launch_bounds__(kPrepWarps * 32, 5) delta_prep_kernel(const ChunkArgs a) {
   extern __shared__ __align__(128) unsigned char tile[];  // K hi, K lo, Q hi, Q lo
-  __shared__ float kk[C][C + 1], qk[C][C + 1];
+  __shared__ __align__(16) float kk[C][kTurn], qk[C][kTurn];
   __shared__ float scale_k[C], scale_q[C], norm_k[C];
-  __shared__ float2 gsum[kPrepWarps][C];
+  __shared__ __align__(16) float2 gsum[kPrepWarps][C];
   __shared__ int bad_rows;
   constexpr int LO = Tiles<DK>::kLo;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -293,14 +293,14 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 5) delta_prep_kernel(const Ch
       if (ks == 0) mma3<true>(c, ah, al, bh, bl);
       else mma3<false>(c, ah, al, bh, bl);
     }
-    float(*out)[C + 1] = warp >= 2 ? qk : kk;
+    float(*out)[kTurn] = warp >= 2 ? qk : kk;
     const float *sr = warp >= 2 ? scale_q : scale_k;
 #pragma unroll
     for (int t = 0; t < 4; ++t)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int i = r0 + (lane >> 2) + 8 * (e >> 1), j = 8 * t + 2 * (lane & 3) + (e & 1);
-        out[i][j] = c[t][e] * sr[i] * scale_k[j];
+      for (int e = 0; e < 4; e += 2) {
+        const int i = r0 + (lane >> 2) + 4 * e, j = 8 * t + 2 * (lane & 3);
+        *reinterpret_cast<float2 *>(&out[i][j]) = make_float2(c[t][e] * sr[i] * scale_k[j], c[t][e + 1] * sr[i] * scale_k[j + 1]);
       }
   }
   if (tid == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // T is turned in the tiles' room
@@ -321,14 +321,25 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 5) delta_prep_kernel(const Ch
     }
     sum *= 1.4426950408889634;  // log2(e)
     const float g_hi = static_cast<float>(sum), g_lo = static_cast<float>(sum - g_hi);
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the room is free
     __syncwarp();
     gsum[warp][lane] = make_float2(g_hi, g_lo);
     __syncwarp();
-    auto decay = [&](int j) {  // from token j to this lane's
-      const float2 gj = gsum[warp][j];
-      return j <= lane ? ex2((g_hi - gj.x) + (g_lo - gj.y)) : 0.f;
+    // this lane's row: the decay from token j to the lane's, times p[j], for j <= lane - below
+    auto decayed = [&](float (&v)[C], const float *p, int below) {
+#pragma unroll
+      for (int j = 0; j < C; j += 4) {
+        const float4 g0 = *reinterpret_cast<const float4 *>(&gsum[warp][j]), g1 = *reinterpret_cast<const float4 *>(&gsum[warp][j + 2]);
+        const float4 m = *reinterpret_cast<const float4 *>(p + j);
+        auto one = [&](int i, float hi, float lo, float x) { v[i] = i + below <= lane ? ex2((g_hi - hi) + (g_lo - lo)) * x : 0.f; };
+        one(j, g0.x, g0.y, m.x);
+        one(j + 1, g0.z, g0.w, m.y);
+        one(j + 2, g1.x, g1.y, m.z);
+        one(j + 3, g1.z, g1.w, m.w);
+      }
     };
-    // a lane per row: its scale and its pieces
+    unsigned char *const room = tile + warp * (C * kTurn * 4);
+    // a lane per row: its scale and its pieces, which leave by way of the room, 4 KB at once
     auto write_row = [&](const float (&v)[C], unsigned char *dst, float *scales) {
       uint32_t m = 0;
 #pragma unroll
@@ -341,14 +352,19 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 5) delta_prep_kernel(const Ch
         uint32_t h4[4], l4[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) split2(v[8 * p + 2 * e], v[8 * p + 2 * e + 1], inv, h4[e], l4[e]);
-        *reinterpret_cast<uint4 *>(dst + at_piece(lane, p)) = make_uint4(h4[0], h4[1], h4[2], h4[3]);
-        *reinterpret_cast<uint4 *>(dst + at_piece(lane, 4 + p)) = make_uint4(l4[0], l4[1], l4[2], l4[3]);
+        *reinterpret_cast<uint4 *>(room + at_piece(lane, p)) = make_uint4(h4[0], h4[1], h4[2], h4[3]);
+        *reinterpret_cast<uint4 *>(room + at_piece(lane, 4 + p)) = make_uint4(l4[0], l4[1], l4[2], l4[3]);
       }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0)
+        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n\tcp.async.bulk.commit_group;" ::"l"(dst),
+                     "r"(smem_u32(room)), "r"(C * 128)
+                     : "memory");
     };
     float w[C];
     if (it >= group) {
-#pragma unroll
-      for (int j = 0; j < C; ++j) w[j] = j <= lane ? decay(j) * qk[lane][j] : 0.f;
+      decayed(w, qk[lane], 0);
       write_row(w, ta + kBlock, f->sa);
       const float2 gl = gsum[warp][C - 1];
       const float eg = ex2(g_hi + g_lo);
@@ -373,10 +389,12 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 5) delta_prep_kernel(const Ch
       }
       continue;
     }
-    float(*const M)[kTurn] = reinterpret_cast<float(*)[kTurn]>(tile + warp * (C * kTurn * 4));
+    float(*const M)[kTurn] = reinterpret_cast<float(*)[kTurn]>(room);
     // a lane per row of A
+    decayed(w, kk[lane], 1);
 #pragma unroll
-    for (int j = 0; j < C; ++j) M[lane][j] = j < lane ? ga.y * decay(j) * kk[lane][j] : 0.f;
+    for (int j = 0; j < C; j += 4)
+      *reinterpret_cast<float4 *>(&M[lane][j]) = make_float4(ga.y * w[j], ga.y * w[j + 1], ga.y * w[j + 2], ga.y * w[j + 3]);
     __syncwarp();
     // (1 + A) T = 1 in blocks of 16.  Both diagonal blocks at once, a lane per column, from the top, four sums a row
     constexpr int H = C / 2;
@@ -453,10 +471,10 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 5) delta_prep_kernel(const Ch
     for (int j = 0; j < C; ++j) row_sum += fabsf(w[j]);
     const uint32_t tau = __reduce_max_sync(0xFFFFFFFFu, mag(row_sum));
     if (lane == 0) f->tau = __uint_as_float(tau);
+    __syncwarp();  // rows of T are read before their pieces take the room
     write_row(w, ta, f->st);
-    __syncwarp();
   }
-  if (tid == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 // ---- the walk ------------------------------------------------------------------------------------------
@@ -749,7 +767,6 @@ __global__ void __launch_bounds__(W * 32) delta_walk_kernel(const ChunkArgs a) {
       // an infinite or NaN value among these tokens: one after another, so that none reaches an earlier one
       const int len = min(C, n - c * C);
       const unsigned char *tile = ring + st * kStage;
-      bool gone = false;
       for (int j = 0; j < len; ++j) {
         const float al = f->alpha[j], be = f->beta[j], sk = f->sk[j], sq = f->sq[j];
         auto both = [&](int ct, float2 &k, float2 &q) {
