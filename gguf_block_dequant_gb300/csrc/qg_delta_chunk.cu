@@ -139,10 +139,13 @@ struct ChunkArgs {
 
 // ---- what does not need the state -------------------------------------------------------------------
 // A CTA of four warps per chunk and key head.  Rows are normalised and split by a warp each; the products of keys with keys and
-// queries with keys take a warp per 16 rows; then a warp per value head solves for T, a lane per column, and another
-// makes the decayed Q K^T (30042 tokens, 16 key and 32 value heads: 366 us for 1.27 GB moved, 5200 instructions a value head and chunk
-// at 0.35 an issue slot).  Latency bounds it, so registers and shared memory are kept to five CTAs an SM: decays (powers of two of
-// differences of sums in log2) are made again rather than kept, and T is turned in the room of the tiles.
+// queries with keys take a warp per 16 rows; then a warp per value head solves for T, a lane per column (in blocks of 16: in
+// one block of 32 it all took 39 us more), and another makes the decayed Q K^T.  30042 tokens, 16 key and 32 value heads:
+// 308 us for 1.27 GB moved, 4800 instructions a value head and chunk at 0.4 an issue slot, shared memory's pipe busy half of the
+// time.  Latency bounds it, so registers and shared memory are kept to five CTAs an SM (four: 13 us more): decays (powers of two of
+// differences of sums in log2) are made again rather than kept, and T is turned in the room of the tiles, from which it and Q K^T
+// leave as bulk copies (16 bytes a lane stored to as many lines took 34 us more).  Sums of log decays in two floats rather than
+// doubles took no less.
 constexpr int kPrepWarps = 4;
 constexpr int kTurn = C + 4;  // floats of a row there
 
