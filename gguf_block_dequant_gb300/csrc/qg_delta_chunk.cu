@@ -141,12 +141,15 @@ struct ChunkArgs {
 // A CTA of four warps per chunk and key head.  Rows are normalised and split by a warp each; the products of keys with keys and
 // queries with keys take a warp per 16 rows; then a warp per value head solves for T, a lane per column (in blocks of 16: in
 // one block of 32 it all took 39 us more), and another makes the decayed Q K^T.  30042 tokens, 16 key and 32 value heads:
-// 308 us for 1.27 GB moved, 4800 instructions a value head and chunk at 0.4 an issue slot, shared memory's pipe busy half of the
-// time.  Latency bounds it, so registers and shared memory are kept to five CTAs an SM (four: 13 us more): decays (powers of two of
+// 264 us for 1.27 GB moved, 4800 instructions a value head and chunk at 0.45 an issue slot, shared memory's pipe busy half of the
+// time.  Latency bounds it, so rows of CTAs to come are sent to L2 (48 us less), and registers and shared memory are kept to five
+// CTAs an SM (four: 13 us more): decays (powers of two of
 // differences of sums in log2) are made again rather than kept, and T is turned in the room of the tiles, from which it and Q K^T
 // leave as bulk copies (16 bytes a lane stored to as many lines took 34 us more).  Sums of log decays in two floats rather than
 // doubles took no less.
 constexpr int kPrepWarps = 4;
+// CTAs whose rows a CTA sends to L2 before they start: half of those that run at once (160 to 440 take the same, 80 and 760 20 us more)
+constexpr int kPrepAhead = 380;
 constexpr int kTurn = C + 4;  // floats of a row there
 
 template <int DK>
@@ -201,6 +204,15 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 5) delta_prep_kernel(const Ch
         }
       }
     }
+  // rows of a CTA to come go to L2: 32 of K and of Q, DK / 32 lines each
+  for (int at = tid; at < C * E; at += kPrepWarps * 32) {
+    const int t = t0 + C * (kPrepAhead / a.d.Hk + 1) + at / E;
+    if (t < a.d.T) {
+      const long long off = hk * DK + at % E * 32;
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(a.d.k + t * a.d.k_stride + off));
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(a.d.q + t * a.d.q_stride + off));
+    }
+  }
   const int group = a.d.Hv / a.d.Hk;
   // the gates of this warp's first item, needed at the end
   auto head_of = [&](int it) {
