@@ -869,7 +869,7 @@ __global__ void __launch_bounds__(W * 32) delta_walk_kernel(const ChunkArgs a) {
 // Every wait ends with its phase or after kTcWaitCycles, which makes the CTA give up.
 // The chain of a chunk bounds it, 6000 cycles or 3.2 us where its products alone are 2900: state in two terms 900, X 1000, R 400, U 250,
 // its terms 400, D 600, the state's update 430, and about 200 from each arrival to the waiter (five prompts of 30042 tokens in all, the
-// longest of 7842: 810 us; the tensor cores' pipe is busy 23 % of a head's time).
+// longest of 7842: 820 us; the tensor cores' pipe is busy 23 % of a head's time).
 constexpr int kTcThreads = 384;                    // two groups of four warps, control, the producer and two idle warps
 constexpr int kTcRegs = 168, kTcRegsWork = 208, kTcRegsRest = 88;
 static_assert(2 * kTcRegsWork + kTcRegsRest <= 3 * kTcRegs, "the warpgroups' shares come from the launch's total");
