@@ -40,7 +40,7 @@ class Server:
     def up(self):
         i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
         self.dkv, self.drefs, self.dtable = i32(self.kv), i32(self.refs), i32(self.table)
-        self.batch = self.qg.kv_batch(self.dkv, self.dtable)
+        self.batch = self.qg.kv_batch(self.dkv, self.dtable.reshape(self.B, self.cols))
         self.missing = torch.full((1,), -5, dtype=torch.int32, device="cuda")
         self.ws = torch.full((self.qg.reserve_workspace_size(self.caches, self.batch),), 255, dtype=torch.uint8, device="cuda")
         return self
@@ -163,6 +163,20 @@ def test_reserve_too_few_pages_changes_nothing(qg):
     assert s.missing.item() == 0
     s.same()
     assert s.refs[2] == 0  # both holders have their own now
+
+
+@pytest.mark.parametrize("side", [False, True])
+def test_reserve_without_sequences(qg, side):
+    """Nothing is missing where nothing is asked for: a server whose last sequence has just left."""
+    s = Server(qg, n_pages=6, B=0, cols=8)
+    s.refs = [0, 2, 1, 0, 0, 0]
+    s.up()
+    none = torch.zeros(0, dtype=torch.int32, device="cuda")
+    stream = torch.cuda.Stream() if side else None
+    torch.cuda.synchronize()
+    qg.kv_reserve(s.caches, s.batch, s.drefs, none, s.missing, s.ws, stream=stream)
+    torch.cuda.synchronize()
+    assert s.missing.item() == 0 and s.drefs.tolist() == s.refs
 
 
 def test_every_holder_copies(qg):
