@@ -8,7 +8,7 @@
 //   O = diag(e^G) Q S0 + [e^{G_i - G_j} q_i . k_j, j <= i] U,   S = e^{G_C} S0 + K^T diag(e^{G_C - G}) U.
 // Everything that does not need S0 (norms, T, the decayed Q K^T) comes from one kernel, parallel over chunks and heads;
 // a second one walks the chunks of each head with the state in registers.  No exponent is above 0 while log
-// decays are not; sums of them are kept in two terms, so that decays between neighbours stay exact after strong ones.
+// decays are not (positive ones are allowed); sums of them are kept in two terms, so that decays between neighbours stay exact after strong ones.
 //
 // Products run on mma.sync in f16 with f32 sums.  Each operand is x = s (hi + lo), s a power of two per row that
 // brings the row's largest magnitude to [2^7, 2^8), hi the multiple of 2^-3 nearest x/s (for rows of tokens the nearest
@@ -120,11 +120,11 @@ QG_DEVICE void load2(uint32_t (&b0)[2], uint32_t (&b1)[2], uint32_t addr) {
   b0[0] = r[0], b0[1] = r[1], b1[0] = r[2], b1[1] = r[3];
 }
 
-// 2^y, y <= 0.  What a state keeps from chunk to chunk multiplies up: a state that hardly decays would gather the error of
-// ex2 (2^-22) hundreds of times in one direction, so factors near 1 come from the series, rounded once.
+// 2^y.  What a state keeps from chunk to chunk multiplies up: a state that hardly decays would gather the error of
+// ex2 (2^-22) hundreds of times in one direction, so factors near 1, below and above, come from the series, rounded once.
 QG_DEVICE float chunk_decay(float y) {
   const float x = y * 0.6931471805599453f;
-  if (x < -0.03125f) return ex2(y);
+  if (fabsf(x) > 0.03125f) return ex2(y);
   return fmaf(x, fmaf(x, fmaf(x, fmaf(x, 1.f / 24.f, 1.f / 6.f), 0.5f), 1.f), 1.f);
 }
 

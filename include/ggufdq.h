@@ -435,7 +435,7 @@ QG_API qg_status qg_beam_reorder(const qg_kv_cache *caches, int n_layers, const 
  *   - Value head h takes the query and key of key head h / (Hv / Hk) (QG_HEADS_GROUPED) or h % Hk
  *     (QG_HEADS_TILED).  Hv a multiple of Hk, Hv <= 1024; Dk 64 or 128; Dv a multiple of 32 up to 1024.
  *   - a, b: with a_scale and a_bias (f32[Hv] each), g = a_scale[h] softplus(a + a_bias[h]) and beta =
- *     sigmoid(b); with neither, g = a and beta = b.  Log decays below -110, -inf among them, count as -110: their e^g is 0.
+ *     sigmoid(b); with neither, g = a and beta = b.  g may be positive.  Log decays below -110, -inf among them, count as -110: their e^g is 0.
  *   - l2norm: q and k are first divided by sqrt(sum of squares + eps), eps >= 0.
  *   - Rows: head h of token t's q at q + t*q_stride + h*Dk (k alike; v and out with Dv; a and b one float per value
  *     head), strides in floats.  q, k, v, out 16-byte aligned with strides a multiple of 4; a and b 4-byte aligned.

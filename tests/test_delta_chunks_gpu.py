@@ -1,0 +1,82 @@
+"""The gated delta rule over prompts: where the chunks could go wrong, against the definition in 64 bits."""
+import pytest
+import torch
+
+from drafted_helpers import Delta
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def qg():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import gguf_block_dequant_gb300 as qg
+    from gguf_block_dequant_gb300 import build
+
+    build.build()
+    qg.load()
+    qg.device_status()
+    return qg
+
+
+class Followed(Delta):
+    """A call whose bound follows the state: what a token adds (the helpers' 48 roundings of its column's length) is carried on
+    by e^g max(1, |1 - beta |k|^2|), the most that a later token makes of it, so that it shrinks when the state is
+    forgotten and grows when the state does.  It never looks at later tokens."""
+
+    def reference(self):
+        q, k, v, a, b = [t.double() for t in self.parts(self.x, self.ba)]
+        if self.l2:
+            q = q / torch.sqrt(q.square().sum(-1, keepdim=True) + 1e-6)
+            k = k / torch.sqrt(k.square().sum(-1, keepdim=True) + 1e-6)
+        g, beta = a, b
+        if self.raw:
+            g = self.a_scale.double() * torch.logaddexp(a + self.a_bias.double(), torch.zeros_like(a))
+            beta = torch.sigmoid(b)
+        key = [h % self.Hk if self.tiled else h // (self.Hv // self.Hk) for h in range(self.Hv)]
+        q, k = q[:, key] * self.scale, k[:, key]
+        grow = torch.exp(g) * (1 - beta * k.square().sum(-1)).abs().clamp(min=1)
+        out = torch.full((self.T, self.Hv, self.Dv), float("nan"), dtype=torch.float64)
+        states, size, sizes = self.states.double(), torch.zeros_like(out), torch.zeros(self.slots, self.Hv, 1, self.Dv).double()
+        before = states.clone()
+        for s, n in enumerate(self.n):
+            at = self.ins[s] if self.ins else -1
+            S = before[at].clone() if at >= 0 else torch.zeros_like(states[0])
+            err = torch.zeros_like(size[0])
+            for t in range(self.start[s], self.start[s] + n):
+                S = torch.exp(g[t])[:, None, None] * S
+                held = S.norm(dim=1)
+                u = beta[t][:, None] * (v[t] - torch.einsum("hij,hi->hj", S, k[t]))
+                S = S + k[t][..., None] * u[:, None]
+                out[t] = torch.einsum("hij,hi->hj", S, q[t])
+                err = grow[t][:, None] * err + held + S.norm(dim=1) + v[t].abs()
+                size[t] = err
+            if n and self.outs and self.outs[s] >= 0:
+                states[self.outs[s]], sizes[self.outs[s], :, 0] = S, err
+        return out, states, size, sizes
+
+
+@pytest.mark.parametrize("Dk,Dv", [(128, 128), (64, 128), (128, 64), (64, 32)])
+@pytest.mark.parametrize("g", [0.005, 0.05])
+def test_states_that_grow(qg, Dk, Dv, g):
+    """Positive log decays: the factors of a chunk are above 1, up to e^2.4, and those of one head go both ways."""
+    for n in ([6], [90, 40], [20]):
+        B = len(n)
+        c = Followed(n, Dk=Dk, Dv=Dv, raw=False, ins=list(range(B)), outs=list(range(B, 2 * B)), seed=31)
+        r = torch.rand((c.T, c.Hv), generator=torch.Generator().manual_seed(32))
+        c.ba[:, :c.Hv] = g * (0.5 + r)
+        c.ba[:, 1] = 8 * g * (r[:, 1] - 0.5)
+        c.check(c.run(qg))
+    c = Followed([70], Dk=Dk, Dv=Dv, ins=[0], outs=[1], seed=33)  # raw gates under a positive factor
+    c.a_scale = torch.full((c.Hv,), g)
+    c.check(c.run(qg))
+    assert qg.device_status() == 0
+
+
+@pytest.mark.parametrize("hint", [0, 1, 64])
+def test_the_hint_changes_nothing_where_states_grow(qg, hint):
+    """max_new below, at and above what the sequence has: token by token and in chunks alike."""
+    c = Followed([64], raw=False, ins=[0], outs=[1], seed=34)
+    c.ba[:, :c.Hv] = 0.1
+    c.check(c.run(qg, max_new=hint))
