@@ -10,12 +10,15 @@
 // a second one walks the chunks of each head with the state in registers.  No exponent is above 0 while log
 // decays are not (positive ones are allowed); sums of them are kept in two terms, so that decays between neighbours stay exact after strong ones.
 //
-// Products run on mma.sync in f16 with f32 sums.  Each operand is x = s (hi + lo), s a power of two per row that
-// brings the row's largest magnitude to [2^7, 2^8), hi the multiple of 2^-3 nearest x/s (for rows of tokens the nearest
-// f16) and lo the f16 nearest the rest: 23 bits of the row's largest; hi hi + hi lo + lo hi leaves 2^-22 of it and its partner's.  (bf16 terms would leave 2^-16, tf32 ones cost twice.)
+// Products run on the tensor cores with f32 sums.  Keys, queries, the state and what a chunk adds to it are x = s (hi + lo) in f16,
+// s a power of two per row that brings the row's largest magnitude to [2^7, 2^8), hi the multiple of 2^-3 nearest x/s and lo the
+// f16 nearest the rest: 23 bits of the row's largest; hi hi + hi lo + lo hi leaves 2^-22 of it and its partner's.  (Two bf16 terms would
+// leave 2^-16, tf32 ones cost twice.)  In a row of R and U every element is a token's, in one of T and of the decayed Q K^T every
+// element is what becomes of a token's: a token must not lose bits to later, larger ones, nor to earlier ones that are forgotten, so these
+// have no scale in common.  They are hi + mid + lo in bf16, whose exponents are f32's: all 24 bits of each, and the six largest of
+// their nine products leave 2^-23.
 #include <algorithm>
 #include <atomic>
-#include <type_traits>
 
 #include "qg_delta.cuh"
 #include "qg_mma.cuh"
@@ -33,10 +36,12 @@ static_assert(C == 32, "a lane per token");
 // ---- the workspace ------------------------------------------------------------------------------
 // Sequence b's chunks have the numbers q_start[b] / 32 + b, and on: they rise, and ceil(n / 32) of them fit
 // before the next sequence's.  Per (chunk, key head): DK / 64 blocks of hi terms, then those of lo terms, each [32 rows of K, 32
-// of Q][64] f16.  Per (chunk, value head): T and A, [32][32 hi, 32 lo] f16 each, and the factors below.  So every row of a block is 128 bytes, and
-// its eight 16-byte pieces are exchanged by the row's low three bits: the 128-byte swizzle of the tensor cores' operands, and
-// free of bank conflicts for ldmatrix, turned or not.
-constexpr int kBlock = C * 128;  // bytes of 32 rows of a block; where Q is in one of K and Q
+// of Q][64] f16.  Per (chunk, value head): T and A, [32][32 hi, 32 mid] and [32][32 lo] bf16 each, and the factors below.  So every row of
+// a block is 128 bytes, and its eight 16-byte pieces are exchanged by the row's low three bits: the 128-byte swizzle of the tensor
+// cores' operands, and free of bank conflicts for ldmatrix, turned or not.  Rows of lo terms are 64 bytes, their four pieces exchanged by
+// the row's bits 1 and 2: the 64-byte swizzle.
+constexpr int kBlock = C * 128;           // bytes of 32 rows of a block; where Q is in one of K and Q
+constexpr int kThree = kBlock + C * 64;   // of T or A; its lo terms are kBlock bytes in
 template <int DK>
 struct Tiles {
   static constexpr int kLo = DK / 64 * 2 * kBlock;  // from the hi terms to the lo terms
@@ -45,21 +50,19 @@ struct Tiles {
 struct Factors {
   float fk[C];     // e^{G_j} sk_j: what K S0 is multiplied by
   float fq[C];     // e^{G_i} sq_i
-  float st[C];     // row scales of T
-  float sa[C];     // row scales of the decayed Q K^T
   float wk[C];     // e^{G_C - G_j} sk_j
   float alpha[C], beta[C], sk[C], sq[C];  // token by token, for chunks with infinite or NaN values
   float dec;       // e^{G_C}
   int odd;         // such a value among the queries, keys and gates
-  // bounds: |K S0| e^G of a column is at most kappa max |S0|, |T R| at most tau max |R|, wk at most omega
-  float kappa, omega, tau;
-  float pad[27];
+  float pad[30];
 };
-constexpr int kTA = 2 * kBlock + static_cast<int>(sizeof(Factors));
+constexpr int kTA = 2 * kThree + static_cast<int>(sizeof(Factors));
 static_assert(kTA % 16 == 0, "bulk copies");
 
 // byte offset of piece `piece` (16 bytes) of a row of a block
 QG_DEVICE uint32_t at_piece(int row, int piece) { return row * 128 + ((piece ^ (row & 7)) << 4); }
+// the same for rows of 64 bytes
+QG_DEVICE uint32_t at_piece64(int row, int piece) { return row * 64 + ((piece ^ ((row >> 1) & 3)) << 4); }
 // the same in the blocks of K and Q
 QG_DEVICE uint32_t kq_at(int row, int piece) { return (piece >> 3) * 2 * kBlock + at_piece(row, piece & 7); }
 
@@ -70,7 +73,7 @@ QG_DEVICE void row_scale(uint32_t m, float &s, float &inv) {
   inv = e == 255u ? 1.f : __uint_as_float((261u - e) << 23);
 }
 QG_DEVICE uint32_t mag(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
-constexpr uint32_t kInfBits = 0x7F800000u;
+constexpr uint32_t kInfBits = 0x7F800000u, kNoBf16 = 0x7F7F8000u;  // magnitudes from the second on round to an infinite bf16
 
 // x inv and y inv, below 2^8, as packed f16 terms: hi a multiple of 2^-3 (adding 3 2^19 rounds to one; 11 bits), lo the rest
 constexpr float kRound = 1572864.f;
@@ -82,34 +85,55 @@ QG_DEVICE void split2(f2 x, f2 inv, uint32_t &hi, uint32_t &lo) {
 }
 QG_DEVICE void split2(float x, float y, float inv, uint32_t &hi, uint32_t &lo) { split2(mk2(x, y), mk2(inv, inv), hi, lo); }
 
-// the same with hi the f16 nearest: what is small beside the row's largest keeps its own 22 bits, so that a token's error
-// does not depend on later, larger tokens of its chunk
-QG_DEVICE void split2_each(float x, float y, float inv, uint32_t &hi, uint32_t &lo) {
-  const f2 p = mul2(mk2(x, y), mk2(inv, inv));
-  hi = pack16<false>(p.x, p.y);
-  lo = pack16<false>(p.x - lo16<false>(hi), p.y - hi16<false>(hi));
+// x and y as three packed bf16 terms each: what is left behind two roundings to 8 bits has 8 itself, so nothing is lost
+// down to 2^-126; magnitudes of 2^128 - 2^119 and more have no bf16
+QG_DEVICE void split3(float x, float y, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
+  hi = pack16<true>(x, y);
+  x -= lo16<true>(hi);
+  y -= hi16<true>(hi);
+  mid = pack16<true>(x, y);
+  lo = pack16<true>(x - lo16<true>(mid), y - hi16<true>(mid));
 }
 
-// N independent tiles c[i] += (ah + al) (bh + bl), without al bl (FIRST: from 0): the tiles take turns, so that no product waits for the
-// sum of the one before it (24 cycles; one can start every 8)
-template <bool FIRST, int N>
-QG_DEVICE void mma3(float (&c)[N][4], const uint32_t (&ah)[4], const uint32_t (&al)[4], const uint32_t (&bh)[N][2],
-                    const uint32_t (&bl)[N][2]) {
+// N independent tiles c[i] += a b (FIRST: from 0): the tiles take turns, so that no product waits for the sum of the one before
+// it (24 cycles; one can start every 8)
+template <bool BF16, bool FIRST, int N>
+QG_DEVICE void mma_each(float (&c)[N][4], const uint32_t (&a)[4], const uint32_t (&b)[N][2]) {
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    if constexpr (FIRST)
+    if constexpr (!FIRST)
+      mma16816<BF16>(c[i], a, b[i][0], b[i][1]);
+    else if constexpr (BF16)
+      asm volatile(
+          "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, "
+          "%10, %10};"
+          : "=f"(c[i][0]), "=f"(c[i][1]), "=f"(c[i][2]), "=f"(c[i][3])
+          : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[i][0]), "r"(b[i][1]), "f"(0.f));
+    else
       asm volatile(
           "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, "
           "%10};"
           : "=f"(c[i][0]), "=f"(c[i][1]), "=f"(c[i][2]), "=f"(c[i][3])
-          : "r"(al[0]), "r"(al[1]), "r"(al[2]), "r"(al[3]), "r"(bh[i][0]), "r"(bh[i][1]), "f"(0.f));
-    else
-      mma16816<false>(c[i], al, bh[i][0], bh[i][1]);
+          : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[i][0]), "r"(b[i][1]), "f"(0.f));
   }
-#pragma unroll
-  for (int i = 0; i < N; ++i) mma16816<false>(c[i], ah, bl[i][0], bl[i][1]);
-#pragma unroll
-  for (int i = 0; i < N; ++i) mma16816<false>(c[i], ah, bh[i][0], bh[i][1]);
+}
+// c[i] += (ah + al) (bh + bl), f16, without al bl
+template <bool FIRST, int N>
+QG_DEVICE void mma3(float (&c)[N][4], const uint32_t (&ah)[4], const uint32_t (&al)[4], const uint32_t (&bh)[N][2],
+                    const uint32_t (&bl)[N][2]) {
+  mma_each<false, FIRST>(c, al, bh);
+  mma_each<false, false>(c, ah, bl);
+  mma_each<false, false>(c, ah, bh);
+}
+// c[i] += (a[0] + a[1] + a[2]) (b[0] + b[1] + b[2]), bf16, without the three smallest products
+template <bool FIRST, int N>
+QG_DEVICE void mma6(float (&c)[N][4], const uint32_t (&a)[3][4], const uint32_t (&b)[3][N][2]) {
+  mma_each<true, FIRST>(c, a[2], b[0]);
+  mma_each<true, false>(c, a[0], b[2]);
+  mma_each<true, false>(c, a[1], b[1]);
+  mma_each<true, false>(c, a[1], b[0]);
+  mma_each<true, false>(c, a[0], b[1]);
+  mma_each<true, false>(c, a[0], b[0]);
 }
 // right operands of two tiles of 8
 template <bool TRANS>
@@ -156,7 +180,7 @@ template <int DK>
 __global__ void __launch_bounds__(kPrepWarps * 32, 5) delta_prep_kernel(const ChunkArgs a) {
   extern __shared__ __align__(128) unsigned char tile[];  // K hi, K lo, Q hi, Q lo
   __shared__ __align__(16) float kk[C][kTurn], qk[C][kTurn];
-  __shared__ float scale_k[C], scale_q[C], norm_k[C];
+  __shared__ float scale_k[C], scale_q[C];
   __shared__ __align__(16) float2 gsum[kPrepWarps][C];
   __shared__ int bad_rows;
   constexpr int LO = Tiles<DK>::kLo;
@@ -256,10 +280,7 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 5) delta_prep_kernel(const Ch
     row_s = 0x1p-60f;
     to = f * 0x1p60f;
   }
-  if ((lane & 1) == 0) {
-    (mine >= R ? scale_q : scale_k)[warp * R + (mine & (R - 1))] = row_s;
-    if (mine < R) norm_k[warp * R + mine] = sqrtf(ss[0]) * fabsf(f);
-  }
+  if ((lane & 1) == 0) (mine >= R ? scale_q : scale_k)[warp * R + (mine & (R - 1))] = row_s;
 #pragma unroll
   for (int z = 0; z < 2; ++z)
 #pragma unroll
@@ -325,7 +346,7 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 5) delta_prep_kernel(const Ch
   for (int it = warp; it < 2 * group; it += kPrepWarps) {
     const int h = head_of(it);
     unsigned char *ta = a.ta + (static_cast<size_t>(slot) * a.d.Hv + h) * kTA;
-    Factors *f = reinterpret_cast<Factors *>(ta + 2 * kBlock);
+    Factors *f = reinterpret_cast<Factors *>(ta + 2 * kThree);
     const float2 ga = gates;
     gates = gates_of(it + kPrepWarps);
     double sum = ga.x;
@@ -353,43 +374,34 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 5) delta_prep_kernel(const Ch
         one(j + 3, g1.z, g1.w, m.w);
       }
     };
-    unsigned char *const room = tile + warp * (C * kTurn * 4);
-    // a lane per row: its scale and its pieces, which leave by way of the room, 4 KB at once
-    auto write_row = [&](const float (&v)[C], unsigned char *dst, float *scales) {
-      uint32_t m = 0;
-#pragma unroll
-      for (int j = 0; j < C; ++j) m = max(m, mag(v[j]));
-      float s, inv;
-      row_scale(m, s, inv);
-      scales[lane] = s;
+    unsigned char *const room = tile + warp * kThree;
+    // a lane per row: its pieces leave by way of the room, 6 KB at once
+    auto write_row = [&](const float (&v)[C], unsigned char *dst) {
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
-        uint32_t h4[4], l4[4];
+        uint32_t h4[4], m4[4], l4[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) split2(v[8 * p + 2 * e], v[8 * p + 2 * e + 1], inv, h4[e], l4[e]);
+        for (int e = 0; e < 4; ++e) split3(v[8 * p + 2 * e], v[8 * p + 2 * e + 1], h4[e], m4[e], l4[e]);
         *reinterpret_cast<uint4 *>(room + at_piece(lane, p)) = make_uint4(h4[0], h4[1], h4[2], h4[3]);
-        *reinterpret_cast<uint4 *>(room + at_piece(lane, 4 + p)) = make_uint4(l4[0], l4[1], l4[2], l4[3]);
+        *reinterpret_cast<uint4 *>(room + at_piece(lane, 4 + p)) = make_uint4(m4[0], m4[1], m4[2], m4[3]);
+        *reinterpret_cast<uint4 *>(room + kBlock + at_piece64(lane, p)) = make_uint4(l4[0], l4[1], l4[2], l4[3]);
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0)
         asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n\tcp.async.bulk.commit_group;" ::"l"(dst),
-                     "r"(smem_u32(room)), "r"(C * 128)
+                     "r"(smem_u32(room)), "r"(kThree)
                      : "memory");
     };
     float w[C];
     if (it >= group) {
       decayed(w, qk[lane], 0);
-      write_row(w, ta + kBlock, f->sa);
+      write_row(w, ta + kThree);
       const float2 gl = gsum[warp][C - 1];
       const float eg = ex2(g_hi + g_lo);
       f->fk[lane] = eg * scale_k[lane];
       f->fq[lane] = eg * scale_q[lane];
-      const float wk = ex2((gl.x - g_hi) + (gl.y - g_lo)) * scale_k[lane];
-      f->wk[lane] = wk;
-      // a row of K and a column of S0: the product of their lengths at most
-      const uint32_t kappa = __reduce_max_sync(0xFFFFFFFFu, mag(eg * norm_k[lane]));
-      const uint32_t omega = __reduce_max_sync(0xFFFFFFFFu, mag(wk));
+      f->wk[lane] = ex2((gl.x - g_hi) + (gl.y - g_lo)) * scale_k[lane];
       f->alpha[lane] = expf(ga.x);
       f->beta[lane] = ga.y;
       f->sk[lane] = scale_k[lane];
@@ -399,8 +411,6 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 5) delta_prep_kernel(const Ch
       if (lane == 0) {
         f->dec = chunk_decay(gl.x + gl.y);
         f->odd = odd;
-        f->kappa = __uint_as_float(kappa) * (DK == 64 ? 8.1f : 11.4f);  // sqrt(DK), and 1 in a hundred for roundings
-        f->omega = __uint_as_float(omega);
       }
       continue;
     }
@@ -481,13 +491,8 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 5) delta_prep_kernel(const Ch
       const float4 m = *reinterpret_cast<const float4 *>(&M[lane][j]);
       w[j] = m.x, w[j + 1] = m.y, w[j + 2] = m.z, w[j + 3] = m.w;
     }
-    float row_sum = 0.f;
-#pragma unroll
-    for (int j = 0; j < C; ++j) row_sum += fabsf(w[j]);
-    const uint32_t tau = __reduce_max_sync(0xFFFFFFFFu, mag(row_sum));
-    if (lane == 0) f->tau = __uint_as_float(tau);
     __syncwarp();  // rows of T are read before their pieces take the room
-    write_row(w, ta, f->st);
+    write_row(w, ta);
   }
   if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
@@ -590,7 +595,7 @@ __global__ void __launch_bounds__(W * 32) delta_walk_kernel(const ChunkArgs a) {
   // where this lane's rows of the tiles start for ldmatrix: pieces are then found by exclusive or.  Keys and queries as right
   // operands of S0 (a row per token), keys as right operands of U (turned)
   const int brow = (lane & 7) + ((lane >> 4) << 3), bpiece = (lane >> 3) & 1;
-  const uint32_t off_b = at_piece(brow, bpiece), off_t = at_piece(lane & 15, lane >> 4);
+  const uint32_t off_b = at_piece(brow, bpiece), off_lo = at_piece64(brow, bpiece), off_t = at_piece(lane & 15, lane >> 4);
 
   for (int c = 0; c < chunks; ++c) {
     const int st = c % NST;
@@ -598,8 +603,8 @@ __global__ void __launch_bounds__(W * 32) delta_walk_kernel(const ChunkArgs a) {
       if (lane == 0) atomicOr(&g_qg_status_delta_chunk, QG_STATUS_BIT_TIMEOUT);
       return;
     }
-    const uint32_t kt = smem_u32(ring + st * kStage), tt = kt + Tiles<DK>::kKQAll, at = tt + kBlock;
-    const Factors *f = reinterpret_cast<const Factors *>(ring + st * kStage + Tiles<DK>::kKQAll + 2 * kBlock);
+    const uint32_t kt = smem_u32(ring + st * kStage), tt = kt + Tiles<DK>::kKQAll, at = tt + kThree;
+    const Factors *f = reinterpret_cast<const Factors *>(ring + st * kStage + Tiles<DK>::kKQAll + 2 * kThree);
     float o[4][4];
     bool odd = false;
     {
@@ -652,83 +657,68 @@ __global__ void __launch_bounds__(W * 32) delta_walk_kernel(const ChunkArgs a) {
         o[t][3] = x[4 + t][3] * (fq.y * s1);
       }
     }
-    // scales of the rows of a [16][32] accumulator; whether all of it is finite
-    auto scales = [&](const float (&w)[4][4], float &s0, float &i0, float &s1, float &i1) {
-      uint32_t m0 = 0, m1 = 0;
+    // the largest magnitudes of the two rows of a [16][32] accumulator
+    auto largest = [&](const float (&w)[4][4], uint32_t &m0, uint32_t &m1) {
+      m0 = m1 = 0;
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         m0 = max(m0, max(mag(w[t][0]), mag(w[t][1])));
         m1 = max(m1, max(mag(w[t][2]), mag(w[t][3])));
       }
-      m0 = max(m0, __shfl_xor_sync(0xFFFFFFFFu, m0, 1));
-      m1 = max(m1, __shfl_xor_sync(0xFFFFFFFFu, m1, 1));
-      m0 = max(m0, __shfl_xor_sync(0xFFFFFFFFu, m0, 2));
-      m1 = max(m1, __shfl_xor_sync(0xFFFFFFFFu, m1, 2));
-      row_scale(m0, s0, i0);
-      row_scale(m1, s1, i1);
-      return !__any_sync(0xFFFFFFFFu, max(m0, m1) >= kInfBits);
     };
-    auto split = [&](auto kind, const float (&w)[4][4], float i0, float i1, uint32_t (&ah)[2][4], uint32_t (&al)[2][4]) {
-      auto two = [&](float x, float y, float inv, uint32_t &hi, uint32_t &lo) {
-        if constexpr (decltype(kind)::value) split2_each(x, y, inv, hi, lo);
-        else split2(x, y, inv, hi, lo);
-      };
+    // whether all of it can be split
+    auto fits = [&](const float (&w)[4][4]) {
+      uint32_t m0, m1;
+      largest(w, m0, m1);
+      return !__any_sync(0xFFFFFFFFu, max(m0, m1) >= kNoBf16);
+    };
+    auto split = [&](const float (&w)[4][4], uint32_t (&a)[2][3][4]) {
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        two(w[2 * ks][0], w[2 * ks][1], i0, ah[ks][0], al[ks][0]);
-        two(w[2 * ks][2], w[2 * ks][3], i1, ah[ks][1], al[ks][1]);
-        two(w[2 * ks + 1][0], w[2 * ks + 1][1], i0, ah[ks][2], al[ks][2]);
-        two(w[2 * ks + 1][2], w[2 * ks + 1][3], i1, ah[ks][3], al[ks][3]);
-      }
+      for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float *x = &w[2 * ks + (i >> 1)][2 * (i & 1)];
+          split3(x[0], x[1], a[ks][0][i], a[ks][1][i], a[ks][2][i]);
+        }
     };
-    using Each = std::true_type;    // rows of tokens
-    using Whole = std::false_type;  // rows that are summed as a whole
     // w (16 x 32) times a lower triangular square tile's transpose
-    auto times_tile = [&](const uint32_t (&ah)[2][4], const uint32_t (&al)[2][4], uint32_t tile, float (&w)[4][4]) {
-      uint32_t bh[4][2], bl[4][2];
-      auto load = [&](int p, int ks) {
-        const uint32_t at = ((tile + off_b) ^ (ks << 5)) + p * 16 * 128;
-        load2<false>(bh[2 * p], bh[2 * p + 1], at);
-        load2<false>(bl[2 * p], bl[2 * p + 1], at ^ 64);
-      };
-      load(0, 0);
-      load(1, 0);
-      mma3<true>(w, ah[0], al[0], bh, bl);
-      load(1, 1);  // the first 16 rows end with their diagonal
+    auto times_tile = [&](const uint32_t (&a)[2][3][4], uint32_t tile, float (&w)[4][4]) {
+      uint32_t b[3][4][2];
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const uint32_t at = tile + off_b + p * 16 * 128;
+        load2<false>(b[0][2 * p], b[0][2 * p + 1], at);
+        load2<false>(b[1][2 * p], b[1][2 * p + 1], at ^ 64);
+        load2<false>(b[2][2 * p], b[2][2 * p + 1], tile + kBlock + off_lo + p * 16 * 64);
+      }
+      mma6<true>(w, a[0], b);
+      // the first 16 rows end with their diagonal
       float (&lower)[2][4] = *reinterpret_cast<float(*)[2][4]>(&w[2]);
-      mma3<false>(lower, ah[1], al[1], *reinterpret_cast<uint32_t(*)[2][2]>(&bh[2]), *reinterpret_cast<uint32_t(*)[2][2]>(&bl[2]));
+      uint32_t b2[3][2][2];
+      const uint32_t at = ((tile + off_b) ^ 32) + 16 * 128;
+      load2<false>(b2[0][0], b2[0][1], at);
+      load2<false>(b2[1][0], b2[1][1], at ^ 64);
+      load2<false>(b2[2][0], b2[2][1], ((tile + kBlock + off_lo) ^ 32) + 16 * 64);
+      mma6<false>(lower, a[1], b2);
     };
     float u[4][4];
     {
-      float s0, i0, s1, i1;
-      odd = !scales(v, s0, i0, s1, i1);
+      odd = !fits(v);
       if (!odd) {
-        uint32_t ah[2][4], al[2][4];
-        split(Each{}, v, i0, i1, ah, al);
-        times_tile(ah, al, tt, u);
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const float2 x = *reinterpret_cast<const float2 *>(f->st + 8 * t + 2 * q4);
-          u[t][0] *= x.x * s0;
-          u[t][1] *= x.y * s0;
-          u[t][2] *= x.x * s1;
-          u[t][3] *= x.y * s1;
-        }
-        odd = !scales(u, s0, i0, s1, i1);
+        uint32_t a3[2][3][4];
+        split(v, a3);
+        times_tile(a3, tt, u);
+        odd = !fits(u);
       }
       if (!odd) {
-        uint32_t ah[2][4], al[2][4];
-        split(Each{}, u, i0, i1, ah, al);
+        uint32_t a3[2][3][4];
+        split(u, a3);
         float w[4][4];
-        times_tile(ah, al, at, w);
+        times_tile(a3, at, w);
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const float2 x = *reinterpret_cast<const float2 *>(f->sa + 8 * t + 2 * q4);
-          o[t][0] = fmaf(x.x * s0, w[t][0], o[t][0]);
-          o[t][1] = fmaf(x.y * s0, w[t][1], o[t][1]);
-          o[t][2] = fmaf(x.x * s1, w[t][2], o[t][2]);
-          o[t][3] = fmaf(x.y * s1, w[t][3], o[t][3]);
-        }
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[t][e] += w[t][e];
         float *p = onext;
         const int left_over = n - c * C - 2 * q4;
 #pragma unroll
@@ -749,10 +739,23 @@ __global__ void __launch_bounds__(W * 32) delta_walk_kernel(const ChunkArgs a) {
         u[t][2] *= x.x;
         u[t][3] *= x.y;
       }
+      uint32_t m0, m1;
+      largest(u, m0, m1);
+      m0 = max(m0, __shfl_xor_sync(0xFFFFFFFFu, m0, 1));
+      m1 = max(m1, __shfl_xor_sync(0xFFFFFFFFu, m1, 1));
+      m0 = max(m0, __shfl_xor_sync(0xFFFFFFFFu, m0, 2));
+      m1 = max(m1, __shfl_xor_sync(0xFFFFFFFFu, m1, 2));
       float s0, i0, s1, i1;
-      scales(u, s0, i0, s1, i1);
+      row_scale(m0, s0, i0);
+      row_scale(m1, s1, i1);
       uint32_t ah[2][4], al[2][4];
-      split(Whole{}, u, i0, i1, ah, al);
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float *x = &u[2 * ks + (i >> 1)][2 * (i & 1)];
+          split2(x[0], x[1], i & 1 ? i1 : i0, ah[ks][i], al[ks][i]);
+        }
       const float dec = f->dec;
 #pragma unroll
       for (int c4 = 0; c4 < DK / 8; c4 += 4) {
@@ -862,10 +865,10 @@ __global__ void __launch_bounds__(W * 32) delta_walk_kernel(const ChunkArgs a) {
 // the state, so a lane of tensor memory is one column and its thread works alone: the state stays in registers (two threads
 // a column, half of its rows each), left operands go to tensor memory as f16 pairs (hi in one range of columns, lo in
 // another), right operands are the tiles in shared memory, with K read as it lies for S0^T K^T and turned for U^T K.
-//   both groups  S^T in two terms (each half of its rows); R = V - ..., U, and U with the decays to the chunk's end, each in
-//                two terms (each half of the tokens); the outputs of the chunk before; S^T <- e^{G_C} S^T + D
+//   both groups  S^T in two terms (each half of its rows); R = V - ... and U, in three terms, and W, U with the decays to the
+//                chunk's end, in two (each half of the tokens); the outputs of the chunk before; S^T <- e^{G_C} S^T + D
 //   a producer   bulk copies into the ring (a row of values each lane: that would hold control up by 1700 cycles)
-//   control      the products X = S^T K^T, O = S^T Q^T, U = R T^T, D = U K, O2 = U A^T
+//   control      the products X = S^T K^T, O = S^T Q^T, U = R T^T, D = W K, O2 = U A^T
 // Every wait ends with its phase or after kTcWaitCycles, which makes the CTA give up.
 // The chain of a chunk bounds it, 6000 cycles or 3.2 us where its products alone are 2900: state in two terms 900, X 1000, R 400, U 250,
 // its terms 400, D 600, the state's update 430, and about 200 from each arrival to the waiter (five prompts of 30042 tokens in all, the
@@ -878,8 +881,9 @@ constexpr long long kTcWaitCycles = 1LL << 29;  // a quarter of a second: a wait
 constexpr int kOrder = 128;  // sequences that are put in order, longest first
 // columns of tensor memory
 // X and O are in two places by the chunk's parity, since O is read while the next is made.  They are two products: 32 columns
-// take 41 cycles a step and 64 take 70, and only X is waited for.  R's pair makes way for U's, which is written once R's product is done.
-enum { TXO = 0, TU = 128, TO2 = 160, TD = 192, TS = 320, TR = 448, TUA = 448, TW = 480 };
+// take 41 cycles a step and 64 take 70, and only X is waited for.  R's terms make way for U's, which are written once R's product is
+// done, and U's sums for W's terms: each half of the tokens has its hi and lo terms where it has read its sums.
+enum { TXO = 0, TU = 128, TO2 = 160, TD = 192, TS = 320, TR = 448, TUA = 448, TW = TU };
 
 template <int DK>
 struct TcSmem {
@@ -895,24 +899,33 @@ struct TcShared {
   int abort, seq;
   int odd_chunk, v_odd[2];  // the last chunk that goes token by token; chunks with such values, by their parity
   float smax[2][128];       // largest of a column's halves
-  float vmax[2][2][128];    // the same of a chunk's values, by its parity: halves of its tokens
+  float wmax[2][128];       // the same of W: halves of the tokens
   __align__(16) float4 ex[2][2][128];  // token by token: partial products of the halves, by the token's parity
 };
 
-// D = (A hi + A lo) (B hi + B lo) without lo lo, the small products first.  A: 8 columns of tensor memory a step; B: the
-// descriptor of its hi tile, lo LO bytes behind it; KROWS: the tile's rows are columns of the product, 16 elements of each
-// a step; TURNED: 16 rows a step.  Unrolled, with nothing but sums of constants between the instructions: a loop that
+// D = (A hi + A lo) (B hi + B lo) without lo lo, the small products first.  A: 8 columns of tensor memory a step, STEP from one to
+// the next; B: the descriptor of its hi tile, lo LO bytes behind it; KROWS: the tile's rows are columns of the product, 16 elements of
+// each a step; TURNED: 16 rows a step.  Unrolled, with nothing but sums of constants between the instructions: a loop that
 // makes each descriptor took 70 cycles a product.
 enum { KROWS, TURNED };
-template <int KIND, int STEPS, int LO>
+template <int KIND, int STEPS, int LO, int STEP = 8>
 QG_DEVICE void product(uint32_t el, uint32_t d, uint32_t a_hi, uint32_t a_lo, uint64_t b, uint32_t id) {
 #pragma unroll
   for (int term = 0; term < 3; ++term)
 #pragma unroll
     for (int ks = 0; ks < STEPS; ++ks) {
       const int off = (KIND == TURNED ? ks * 16 * 128 : (ks >> 2) * 2 * kBlock + (ks & 3) * 32) + (term == 1 ? LO : 0);
-      tc_mma_ta_el(el, d, (term == 0 ? a_lo : a_hi) + 8 * ks, b + (off >> 4), id, term || ks);
+      tc_mma_ta_el(el, d, (term == 0 ? a_lo : a_hi) + STEP * ks, b + (off >> 4), id, term || ks);
     }
+}
+// D = A B of three terms each, without the three smallest products: 32 tokens.  A: 16 columns a term; B: its hi and mid terms, its lo
+QG_DEVICE void product3(uint32_t el, uint32_t d, uint32_t a, uint64_t b, uint64_t b_lo, uint32_t id) {
+  constexpr int kA[6] = {2, 0, 1, 1, 0, 0}, kB[6] = {0, 2, 1, 0, 1, 0};
+#pragma unroll
+  for (int i = 0; i < 6; ++i)
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks)
+      tc_mma_ta_el(el, d, a + 16 * kA[i] + 8 * ks, (kB[i] == 2 ? b_lo : b + (64 * kB[i] >> 4)) + (32 * ks >> 4), id, i || ks);
 }
 
 template <int DK>
@@ -987,7 +1000,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) delta_walk_tc_kernel(const Chun
     }
     return __all_sync(0xFFFFFFFFu, ok);
   };
-  auto factors = [&](int c) { return reinterpret_cast<const Factors *>(ring + (c % kTcStages) * kStage + Tiles<DK>::kKQAll + 2 * kBlock); };
+  auto factors = [&](int c) { return reinterpret_cast<const Factors *>(ring + (c % kTcStages) * kStage + Tiles<DK>::kKQAll + 2 * kThree); };
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTcRegsRest));
@@ -1018,8 +1031,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) delta_walk_tc_kernel(const Chun
     } else if (warp == 8) {
       const uint32_t el = elect_lane();
       constexpr uint32_t id32 = make_idesc16(128, 32, false, false), idk = make_idesc16(128, DK, false, true);
+      constexpr uint32_t id3 = make_idesc16(128, 32, true, false);
       // what the right operands' descriptors say beside the address
-      const uint64_t rows0 = sw128_desc(0), turned0 = sw128_desc_mn(0, 2 * kBlock);
+      const uint64_t rows0 = sw128_desc(0), turned0 = sw128_desc_mn(0, 2 * kBlock), lo0 = sw64_desc(0);
       uint32_t n_r = 0, n_o = 0;  // phases of r_ready (u_ready, w_ready) and of o_free
       bool before_odd = true;     // no output to be read of a chunk before
       bool ok = true;
@@ -1050,11 +1064,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) delta_walk_tc_kernel(const Chun
         }
         if (!(ok = wait(&sh.r_ready, n_r & 1))) break;
         tc_fence_after();
-        product<KROWS, 2, 64>(el, tm + TU, tm + TR, tm + TR + 16, rows0 + (tt >> 4), id32);
+        product3(el, tm + TU, tm + TR, rows0 + (tt >> 4), lo0 + ((tt + kBlock) >> 4), id3);
         tc_commit_el(el, &sh.u_done);
         if (!(ok = wait(&sh.w_ready, n_r & 1))) break;
         tc_fence_after();
-        product<TURNED, 2, LO>(el, tm + TD, tm + TW, tm + TW + 16, kturned, idk);
+        product<TURNED, 2, LO, 16>(el, tm + TD, tm + TW, tm + TW + 8, kturned, idk);
         tc_commit_el(el, &sh.d_done);
         // everyone has left the chunk before, and its outputs have been read
         if (!before_odd && !(ok = wait(&sh.o_free, n_o++ & 1))) break;
@@ -1062,7 +1076,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) delta_walk_tc_kernel(const Chun
         before_odd = false;
         if (!(ok = wait(&sh.u_ready, n_r & 1))) break;
         tc_fence_after();
-        product<KROWS, 2, 64>(el, tm + TO2, tm + TUA, tm + TUA + 16, rows0 + ((tt + kBlock) >> 4), id32);
+        product3(el, tm + TO2, tm + TUA, rows0 + ((tt + kThree) >> 4), lo0 + ((tt + kThree + kBlock) >> 4), id3);
         tc_commit_el(el, &sh.o_done);
         ++n_r;
       }
@@ -1091,31 +1105,29 @@ __global__ void __launch_bounds__(kTcThreads, 1) delta_walk_tc_kernel(const Chun
       const float *p = reinterpret_cast<const float *>(ring + (c % kTcStages) * kStage + TcSmem<DK>::kV);
       return c * C + j < n ? p[j * 128 + row] : 0.f;
     };
-    // this half's 16 tokens in two terms to its 8 + 8 columns of a pair of tensor memory.  The scale is that of a bound, known
-    // before: the halves need not meet for their largest (terms of their own scale keep 22 bits 2^20 below a bound)
+    // this half's 16 tokens in three terms to its 8 columns of each
     constexpr int H = C / 2;
     const int j0 = group * H;
-    auto scale_for = [&](float bound, float &sc, float &inv) { row_scale(mag(fminf(bound, 3e38f)), sc, inv); };
-    auto put = [&](const float (&w)[H], float inv, uint32_t col) {
-      uint32_t hi[H / 2], lo[H / 2];
+    auto put = [&](const float (&w)[H], uint32_t col) {
+      uint32_t hi[H / 2], mid[H / 2], lo[H / 2];
 #pragma unroll
-      for (int j = 0; j < H; j += 2) split2_each(w[j], w[j + 1], inv, hi[j / 2], lo[j / 2]);
+      for (int j = 0; j < H; j += 2) split3(w[j], w[j + 1], hi[j / 2], mid[j / 2], lo[j / 2]);
       tmem_st8(lanes + col + 8 * group, hi);
-      tmem_st8(lanes + col + 16 + 8 * group, lo);
+      tmem_st8(lanes + col + 16 + 8 * group, mid);
+      tmem_st8(lanes + col + 32 + 8 * group, lo);
     };
     auto tell = [&](uint64_t *bar) {  // what this warp has put into, or taken from, tensor memory
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
     };
-    // the largest of a chunk's values, told with the state before that chunk, and whether all are finite
+    // whether all of a chunk's values can be split, told with the state before that chunk
     auto look_at_v = [&](int c) {
       if (!wait(&sh.full[c % kTcStages], (c / kTcStages) & 1)) return;
       uint32_t big = 0;
 #pragma unroll
       for (int j = 0; j < H; ++j) big = max(big, mag(value(c, j0 + j)));
-      sh.vmax[c & 1][group][row] = __uint_as_float(big);
-      if (big >= kInfBits) sh.v_odd[c & 1] = c;
+      if (big >= kNoBf16) sh.v_odd[c & 1] = c;
     };
     look_at_v(0);
     auto largest = [&] {
@@ -1125,8 +1137,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) delta_walk_tc_kernel(const Chun
       return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
     };
     float m = largest();
-    float scale_s = 1.f, scale_before = 1.f, largest_s = 0.f;
-    float scale_u = 1.f;
+    float scale_s = 1.f, scale_before = 1.f;
     uint32_t n_u = 0;      // phases of u_done and o_done
     bool pending = false;  // outputs of the chunk before wait to be written
     auto outputs = [&](int c, float ss) {  // ss: the state's scale then
@@ -1140,11 +1151,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) delta_walk_tc_kernel(const Chun
       tmem_ld16(lanes + TO2 + j0, y);
 #pragma unroll
       for (int j = 0; j < H; j += 4) {
-        const float4 fq = *reinterpret_cast<const float4 *>(f->fq + j0 + j), sa = *reinterpret_cast<const float4 *>(f->sa + j0 + j);
-        x[j] = fmaf(fq.x * ss, x[j], sa.x * scale_u * y[j]);
-        x[j + 1] = fmaf(fq.y * ss, x[j + 1], sa.y * scale_u * y[j + 1]);
-        x[j + 2] = fmaf(fq.z * ss, x[j + 2], sa.z * scale_u * y[j + 2]);
-        x[j + 3] = fmaf(fq.w * ss, x[j + 3], sa.w * scale_u * y[j + 3]);
+        const float4 fq = *reinterpret_cast<const float4 *>(f->fq + j0 + j);
+        x[j] = fmaf(fq.x * ss, x[j], y[j]);
+        x[j + 1] = fmaf(fq.y * ss, x[j + 1], y[j + 1]);
+        x[j + 2] = fmaf(fq.z * ss, x[j + 2], y[j + 2]);
+        x[j + 3] = fmaf(fq.w * ss, x[j + 3], y[j + 3]);
       }
 #pragma unroll
       for (int j = 0; j < H; ++j) asm volatile("" : "+f"(x[j]));  // the factors are read before the stage is given up
@@ -1163,8 +1174,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) delta_walk_tc_kernel(const Chun
         named_bar_sync(1, 256);
         scale_before = scale_s;
         float inv;
-        largest_s = fmaxf(m, sh.smax[group ^ 1][row]);
-        row_scale(mag(largest_s), scale_s, inv);
+        row_scale(mag(fmaxf(m, sh.smax[group ^ 1][row])), scale_s, inv);
 #pragma unroll
         for (int i = 0; i < HK; i += 32) {
           uint32_t hi[16], lo[16];
@@ -1186,11 +1196,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) delta_walk_tc_kernel(const Chun
       for (int j = 0; j < H; ++j) asm volatile("" : "+f"(w[j]));
       if (pending && !outputs(c - 1, scale_before)) break;
       pending = false;
-      float bound = 1.01f * fmaf(f->kappa, largest_s, fmaxf(sh.vmax[c & 1][0][row], sh.vmax[c & 1][1][row]));
-      float scale_r, inv_r, inv_u, scale_w, inv_w;
-      scale_for(bound, scale_r, inv_r);
-      bound *= 1.01f * f->tau;
-      const float bound_w = bound * f->omega;
       if (!wait(&sh.x_done, c & 1)) break;
       if (*reinterpret_cast<volatile int *>(&sh.odd_chunk) != c) {
         tc_fence_after();
@@ -1203,30 +1208,36 @@ __global__ void __launch_bounds__(kTcThreads, 1) delta_walk_tc_kernel(const Chun
           x[j + 2] = fmaf(-fk.z * scale_s, x[j + 2], w[j + 2]);
           x[j + 3] = fmaf(-fk.w * scale_s, x[j + 3], w[j + 3]);
         }
-        put(x, inv_r, TR);
+        put(x, TR);
         tmem_st_wait();
         tell(&sh.r_ready);
-        scale_for(bound, scale_u, inv_u);
-        scale_for(bound_w, scale_w, inv_w);
         if (!wait(&sh.u_done, n_u & 1)) break;
         tc_fence_after();
         tmem_ld16(lanes + TU + j0, x);
+        float big = 0.f;
 #pragma unroll
         for (int j = 0; j < H; j += 4) {
-          const float4 st = *reinterpret_cast<const float4 *>(f->st + j0 + j), wk = *reinterpret_cast<const float4 *>(f->wk + j0 + j);
-          x[j] *= st.x * scale_r;
-          x[j + 1] *= st.y * scale_r;
-          x[j + 2] *= st.z * scale_r;
-          x[j + 3] *= st.w * scale_r;
+          const float4 wk = *reinterpret_cast<const float4 *>(f->wk + j0 + j);
           w[j] = x[j] * wk.x;
           w[j + 1] = x[j + 1] * wk.y;
           w[j + 2] = x[j + 2] * wk.z;
           w[j + 3] = x[j + 3] * wk.w;
+          big = fmaxf(fmaxf(big, fmaxf(fabsf(w[j]), fabsf(w[j + 1]))), fmaxf(fabsf(w[j + 2]), fabsf(w[j + 3])));
         }
-        put(w, inv_w, TW);
+        sh.wmax[group][row] = big;
+        named_bar_sync(2 + (warp & 3), 64);  // with the warp that has these columns' other tokens
+        float scale_w, inv_w;
+        row_scale(mag(fmaxf(big, sh.wmax[group ^ 1][row])), scale_w, inv_w);
+        {
+          uint32_t hi[H / 2], lo[H / 2];
+#pragma unroll
+          for (int j = 0; j < H; j += 2) split2(w[j], w[j + 1], inv_w, hi[j / 2], lo[j / 2]);
+          tmem_st8(lanes + TW + 16 * group, hi);
+          tmem_st8(lanes + TW + 16 * group + 8, lo);
+        }
         tmem_st_wait();
         tell(&sh.w_ready);
-        put(x, inv_u, TUA);
+        put(x, TUA);
         tmem_st_wait();
         tell(&sh.u_ready);
         ++n_u;
@@ -1298,8 +1309,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) delta_walk_tc_kernel(const Chun
       m = largest();
       if (c + 1 < chunks) look_at_v(c + 1);
     }
-    // a warp that gave up does not keep the others at the barrier that they may be at; behind it they see that it did
-    if (c < chunks) asm volatile("bar.arrive 1, 256;" ::: "memory");
+    // a warp that gave up does not keep the others at the barriers that they may be at; behind them they see that it did (nothing
+    // that they wait for next comes without this warp)
+    if (c < chunks) {
+      asm volatile("bar.arrive 1, 256;" ::: "memory");
+      asm volatile("bar.arrive %0, 64;" ::"r"(2 + (warp & 3)) : "memory");
+    }
     if (c == chunks && pending) outputs(chunks - 1, scale_s);
     if (c == chunks && a.d.state_out) {
       const int to = __ldg(a.d.state_out + b);
@@ -1328,7 +1343,8 @@ cudaError_t walk(const ChunkArgs &a, cudaStream_t s) {
 
 template <int DK>
 cudaError_t both(const ChunkArgs &a, cudaStream_t s) {
-  constexpr int smem = std::max(Tiles<DK>::kKQAll, kPrepWarps * C * kTurn * 4);
+  constexpr int smem = std::max(Tiles<DK>::kKQAll, kPrepWarps * kThree);
+  static_assert(C * kTurn * 4 <= kThree, "T is turned in a warp's room");
   if (!qg::set_smem_attr(reinterpret_cast<const void *>(delta_prep_kernel<DK>), smem)) return cudaErrorInvalidValue;
   cudaError_t e = qg::launch_pdl(delta_prep_kernel<DK>, dim3(static_cast<unsigned>(a.slots) * a.d.Hk), dim3(kPrepWarps * 32), smem, s, a);
   if (e != cudaSuccess) return e;

@@ -81,6 +81,18 @@ QG_DEVICE uint64_t sw128_desc(uint32_t saddr) {
   return d;
 }
 
+// The same for rows of 64 bytes in the 64-byte swizzled layout (4): 8-row atoms of 512 bytes, in which a row's four 16-byte
+// pieces are exchanged by the row's bits 1 and 2.
+QG_DEVICE uint64_t sw64_desc(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>(1u) << 16;
+  d |= static_cast<uint64_t>((512u >> 4) & 0x3FFFu) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(4u) << 61;
+  return d;
+}
+
 // Shared-memory matrix descriptor of an operand stored K rows by MN columns (MN-major) in the
 // same swizzled layout: rows of 128 bytes hold 64 MN elements of one k; 8-row (1024-byte)
 // atoms follow one another along K, and `mn_stride` bytes lead to the next 64 MN elements.

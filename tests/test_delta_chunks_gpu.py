@@ -58,9 +58,9 @@ class Followed(Delta):
 
 
 @pytest.mark.parametrize("Dk,Dv", [(128, 128), (64, 128), (128, 64), (64, 32)])
-@pytest.mark.parametrize("g", [0.005, 0.05])
+@pytest.mark.parametrize("g", [0.005, 0.05, 0.3])
 def test_states_that_grow(qg, Dk, Dv, g):
-    """Positive log decays: the factors of a chunk are above 1, up to e^2.4, and those of one head go both ways."""
+    """Positive log decays: the factors of a chunk are above 1, up to e^12, and those of one head go both ways."""
     for n in ([6], [90, 40], [20]):
         B = len(n)
         c = Followed(n, Dk=Dk, Dv=Dv, raw=False, ins=list(range(B)), outs=list(range(B, 2 * B)), seed=31)
@@ -80,3 +80,43 @@ def test_the_hint_changes_nothing_where_states_grow(qg, hint):
     c = Followed([64], raw=False, ins=[0], outs=[1], seed=34)
     c.ba[:, :c.Hv] = 0.1
     c.check(c.run(qg, max_new=hint))
+
+
+def by_place(c, f):
+    """Values times f of a token's place in its chunk of 32."""
+    v = c.parts(c.x, c.ba)[2]
+    for s, n in enumerate(c.n):
+        for t in range(n):
+            v[c.start[s] + t] *= f[t % 32]
+
+
+@pytest.mark.parametrize("Dk,Dv", [(128, 128), (64, 128), (128, 64), (64, 32)])
+@pytest.mark.parametrize("power", [6, 12, 30])
+def test_magnitudes_within_a_chunk(qg, Dk, Dv, power):
+    """Values that grow by up to 10^30 within a chunk, from states of zeros: earlier tokens keep their own precision.  Values that
+    shrink as much, under decays that forget them: later tokens have theirs."""
+    f = torch.logspace(-power / 2, power / 2, 32, dtype=torch.float64).float()
+    for n in ([32], [20, 96, 70]):
+        B = len(n)
+        c = Followed(n, Dk=Dk, Dv=Dv, ins=[-1] * B, outs=list(range(B)), seed=35)
+        by_place(c, f)
+        c.check(c.run(qg))
+        c = Followed(n, Dk=Dk, Dv=Dv, raw=False, ins=[-1] * B, outs=list(range(B)), seed=36)
+        by_place(c, f.flip(0))
+        c.ba[:, :c.Hv] = -11.0
+        c.ba[:, 0] = -2.5
+        c.check(c.run(qg))
+    assert qg.device_status() == 0
+
+
+@pytest.mark.parametrize("Dk,Dv", [(128, 128), (64, 128), (128, 64)])
+@pytest.mark.parametrize("reset", [-float("inf"), -40.0])
+def test_a_state_forgotten_within_a_chunk(qg, Dk, Dv, reset):
+    """A state of 10^6 and the values before a token that forgets them do not cost the tokens behind it their precision."""
+    for at in (0, 3, 31, 40, 63):
+        c = Followed([70], Dk=Dk, Dv=Dv, raw=False, ins=[0], outs=[1], seed=37)
+        c.states[0] *= 1e6
+        c.parts(c.x, c.ba)[2][:at] *= 1e6
+        c.ba[:, :c.Hv] = -0.01
+        c.ba[at, :c.Hv] = reset
+        c.check(c.run(qg))
