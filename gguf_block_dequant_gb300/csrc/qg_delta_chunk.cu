@@ -53,7 +53,7 @@ struct Factors {
   float wk[C];     // e^{G_C - G_j} sk_j
   float alpha[C], beta[C], sk[C], sq[C];  // token by token, for chunks with infinite or NaN values
   float dec;       // e^{G_C}
-  int odd;         // such a value among the queries, keys and gates
+  int odd;         // such a value among the queries, keys and gates, or a factor that leaves f32
   float pad[30];
 };
 constexpr int kTA = 2 * kThree + static_cast<int>(sizeof(Factors));
@@ -74,6 +74,13 @@ QG_DEVICE void row_scale(uint32_t m, float &s, float &inv) {
 }
 QG_DEVICE uint32_t mag(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 constexpr uint32_t kInfBits = 0x7F800000u, kNoBf16 = 0x7F7F8000u;  // magnitudes from the second on round to an infinite bf16
+constexpr float kMost = 0x1p127f;  // what is below it can be split
+// the larger one, or NaN where one of them is
+QG_DEVICE float max_nan(float x, float y) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+  return r;
+}
 
 // x inv and y inv, below 2^8, as packed f16 terms: hi a multiple of 2^-3 (adding 3 2^19 rounds to one; 11 bits), lo the rest
 constexpr float kRound = 1572864.f;
@@ -396,17 +403,21 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 5) delta_prep_kernel(const Ch
     float w[C];
     if (it >= group) {
       decayed(w, qk[lane], 0);
+      float top = 0.f;
+#pragma unroll
+      for (int j = 0; j < C; ++j) top = max_nan(top, fabsf(w[j]));
       write_row(w, ta + kThree);
       const float2 gl = gsum[warp][C - 1];
       const float eg = ex2(g_hi + g_lo);
       f->fk[lane] = eg * scale_k[lane];
       f->fq[lane] = eg * scale_q[lane];
-      f->wk[lane] = ex2((gl.x - g_hi) + (gl.y - g_lo)) * scale_k[lane];
+      const float wk = ex2((gl.x - g_hi) + (gl.y - g_lo)) * scale_k[lane];
+      f->wk[lane] = wk;
       f->alpha[lane] = expf(ga.x);
       f->beta[lane] = ga.y;
       f->sk[lane] = scale_k[lane];
       f->sq[lane] = scale_q[lane];
-      const bool bad = !(fabsf(ga.x) < INFINITY) || !(fabsf(ga.y) < INFINITY);
+      const bool bad = !(fabsf(ga.x) < INFINITY && fabsf(ga.y) < INFINITY && top < kMost && eg < kMost && wk < kMost);
       const int odd = __any_sync(0xFFFFFFFFu, bad) || bad_rows;
       if (lane == 0) {
         f->dec = chunk_decay(gl.x + gl.y);
@@ -703,12 +714,19 @@ __global__ void __launch_bounds__(W * 32) delta_walk_kernel(const ChunkArgs a) {
     };
     float u[4][4];
     {
-      odd = !fits(v);
+      odd = f->odd || !fits(v);
       if (!odd) {
         uint32_t a3[2][3][4];
         split(v, a3);
         times_tile(a3, tt, u);
-        odd = !fits(u);
+        float w[4][4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const float2 x = *reinterpret_cast<const float2 *>(f->wk + 8 * t + 2 * q4);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[t][e] = max_nan(fabsf(u[t][e]), fabsf(u[t][e] * (e & 1 ? x.y : x.x)));
+        }
+        odd = !fits(w);
       }
       if (!odd) {
         uint32_t a3[2][3][4];
@@ -782,7 +800,7 @@ __global__ void __launch_bounds__(W * 32) delta_walk_kernel(const ChunkArgs a) {
         }
       }
     } else {
-      // an infinite or NaN value among these tokens: one after another, so that none reaches an earlier one
+      // an infinite or NaN value among these tokens or their updates: one after another, so that none reaches an earlier one
       const int len = min(C, n - c * C);
       const unsigned char *tile = ring + st * kStage;
       for (int j = 0; j < len; ++j) {
@@ -897,7 +915,7 @@ struct TcShared {
   uint64_t x_done, u_done, d_done, o_done;              // by the tensor cores
   uint32_t tmem;
   int abort, seq;
-  int odd_chunk, v_odd[2];  // the last chunk that goes token by token; chunks with such values, by their parity
+  int odd_chunk, u_odd;     // the last chunk that goes token by token; the last one whose updates say that it must
   float smax[2][128];       // largest of a column's halves
   float wmax[2][128];       // the same of W: halves of the tokens
   __align__(16) float4 ex[2][2][128];  // token by token: partial products of the halves, by the token's parity
@@ -977,7 +995,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) delta_walk_tc_kernel(const Chun
     mbar_init(&sh.o_done, 1);
     fence_mbar_init();
     sh.abort = 0;
-    sh.odd_chunk = sh.v_odd[0] = sh.v_odd[1] = -1;
+    sh.odd_chunk = sh.u_odd = -1;
   }
   if (warp == 8) tmem_alloc(&sh.tmem, 512);
   tc_fence_before();
@@ -1043,7 +1061,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) delta_walk_tc_kernel(const Chun
         if (!ok) break;
         const uint32_t kt = smem_u32(ring + st * kStage), tt = kt + Tiles<DK>::kKQAll;
         const uint64_t kd = rows0 + (kt >> 4), kturned = turned0 + (kt >> 4);
-        const bool odd = factors(c)->odd || *reinterpret_cast<volatile int *>(&sh.v_odd[c & 1]) == c;
+        const bool odd = factors(c)->odd;
         tc_fence_after();
         if (!odd) {
           product<KROWS, DK / 16, LO>(el, tm + TXO + 64 * (c & 1), tm + TS, tm + TS + DK / 2, kd, id32);
@@ -1068,17 +1086,28 @@ __global__ void __launch_bounds__(kTcThreads, 1) delta_walk_tc_kernel(const Chun
         tc_commit_el(el, &sh.u_done);
         if (!(ok = wait(&sh.w_ready, n_r & 1))) break;
         tc_fence_after();
-        product<TURNED, 2, LO, 16>(el, tm + TD, tm + TW, tm + TW + 8, kturned, idk);
-        tc_commit_el(el, &sh.d_done);
+        const bool late = *reinterpret_cast<volatile int *>(&sh.u_odd) == c;
+        if (!late) {
+          product<TURNED, 2, LO, 16>(el, tm + TD, tm + TW, tm + TW + 8, kturned, idk);
+          tc_commit_el(el, &sh.d_done);
+        }
         // everyone has left the chunk before, and its outputs have been read
         if (!before_odd && !(ok = wait(&sh.o_free, n_o++ & 1))) break;
         if (c > 0 && el) mbar_arrive(&sh.empty[(c - 1) % kTcStages]);
-        before_odd = false;
+        before_odd = late;
         if (!(ok = wait(&sh.u_ready, n_r & 1))) break;
-        tc_fence_after();
-        product3(el, tm + TO2, tm + TUA, rows0 + ((tt + kThree) >> 4), lo0 + ((tt + kThree + kBlock) >> 4), id3);
-        tc_commit_el(el, &sh.o_done);
         ++n_r;
+        tc_fence_after();
+        if (!late) {
+          product3(el, tm + TO2, tm + TUA, rows0 + ((tt + kThree) >> 4), lo0 + ((tt + kThree + kBlock) >> 4), id3);
+          tc_commit_el(el, &sh.o_done);
+        } else if (el) {  // U's product is done, and with it those before it: nobody reads or writes tensor memory now
+          sh.odd_chunk = c;
+          __threadfence_block();
+          mbar_arrive(&sh.d_done);
+          mbar_arrive(&sh.o_done);
+        }
+        __syncwarp();
       }
     }
   } else {
@@ -1121,23 +1150,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) delta_walk_tc_kernel(const Chun
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
     };
-    // whether all of a chunk's values can be split, told with the state before that chunk
-    auto look_at_v = [&](int c) {
-      if (!wait(&sh.full[c % kTcStages], (c / kTcStages) & 1)) return;
-      uint32_t big = 0;
-#pragma unroll
-      for (int j = 0; j < H; ++j) big = max(big, mag(value(c, j0 + j)));
-      if (big >= kNoBf16) sh.v_odd[c & 1] = c;
-    };
-    look_at_v(0);
     auto largest = [&] {
       float m4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int i = 0; i < HK; ++i) m4[i & 3] = fmaxf(m4[i & 3], fabsf(s[i]));
-      return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+      for (int i = 0; i < HK; ++i) m4[i & 3] = max_nan(m4[i & 3], fabsf(s[i]));
+      return max_nan(max_nan(m4[0], m4[1]), max_nan(m4[2], m4[3]));
     };
     float m = largest();
-    float scale_s = 1.f, scale_before = 1.f;
+    float scale_s = 1.f, scale_before = 1.f, largest_s = 0.f;
     uint32_t n_u = 0;      // phases of u_done and o_done
     bool pending = false;  // outputs of the chunk before wait to be written
     auto outputs = [&](int c, float ss) {  // ss: the state's scale then
@@ -1174,7 +1194,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) delta_walk_tc_kernel(const Chun
         named_bar_sync(1, 256);
         scale_before = scale_s;
         float inv;
-        row_scale(mag(fmaxf(m, sh.smax[group ^ 1][row])), scale_s, inv);
+        largest_s = max_nan(m, sh.smax[group ^ 1][row]);
+        row_scale(mag(largest_s), scale_s, inv);
 #pragma unroll
         for (int i = 0; i < HK; i += 32) {
           uint32_t hi[16], lo[16];
@@ -1197,7 +1218,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) delta_walk_tc_kernel(const Chun
       if (pending && !outputs(c - 1, scale_before)) break;
       pending = false;
       if (!wait(&sh.x_done, c & 1)) break;
-      if (*reinterpret_cast<volatile int *>(&sh.odd_chunk) != c) {
+      const float dec = f->dec;
+      float scale_w = 1.f;
+      auto by_token = [&] { return *reinterpret_cast<volatile int *>(&sh.odd_chunk) == c; };
+      if (!by_token()) {
         tc_fence_after();
         tmem_ld16(lanes + TXO + 64 * (c & 1) + j0, x);
 #pragma unroll
@@ -1214,7 +1238,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) delta_walk_tc_kernel(const Chun
         if (!wait(&sh.u_done, n_u & 1)) break;
         tc_fence_after();
         tmem_ld16(lanes + TU + j0, x);
-        float big = 0.f;
+        float big = 0.f, big_u = 0.f;
+#pragma unroll
+        for (int j = 0; j < H; ++j) big_u = max_nan(big_u, fabsf(x[j]));
 #pragma unroll
         for (int j = 0; j < H; j += 4) {
           const float4 wk = *reinterpret_cast<const float4 *>(f->wk + j0 + j);
@@ -1224,9 +1250,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) delta_walk_tc_kernel(const Chun
           w[j + 3] = x[j + 3] * wk.w;
           big = fmaxf(fmaxf(big, fmaxf(fabsf(w[j]), fabsf(w[j + 1]))), fmaxf(fabsf(w[j + 2]), fabsf(w[j + 3])));
         }
+        // infinite or NaN (a zero of T times an infinite R is): the chunk goes token by token.  Not where the column's state is
+        // that already: then every token's output is
+        if (largest_s < INFINITY && !(big_u < kMost && big < kMost)) sh.u_odd = c;
         sh.wmax[group][row] = big;
         named_bar_sync(2 + (warp & 3), 64);  // with the warp that has these columns' other tokens
-        float scale_w, inv_w;
+        float inv_w;
         row_scale(mag(fmaxf(big, sh.wmax[group ^ 1][row])), scale_w, inv_w);
         {
           uint32_t hi[H / 2], lo[H / 2];
@@ -1241,9 +1270,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) delta_walk_tc_kernel(const Chun
         tmem_st_wait();
         tell(&sh.u_ready);
         ++n_u;
-        if (c + 1 < chunks) look_at_v(c + 1);
-        const float dec = f->dec;
         if (!wait(&sh.d_done, c & 1)) break;
+      } else if (!wait(&sh.d_done, c & 1)) {
+        break;
+      }
+      if (!by_token()) {
         tc_fence_after();
         float m4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -1256,16 +1287,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) delta_walk_tc_kernel(const Chun
             const f2 y = fma2(mk2(scale_w, scale_w), mk2(d[j], d[j + 1]), mul2(mk2(dec, dec), mk2(s[i + j], s[i + j + 1])));
             s[i + j] = y.x;
             s[i + j + 1] = y.y;
-            m4[(j >> 1) & 3] = fmaxf(m4[(j >> 1) & 3], fmaxf(fabsf(y.x), fabsf(y.y)));
+            m4[(j >> 1) & 3] = max_nan(m4[(j >> 1) & 3], max_nan(fabsf(y.x), fabsf(y.y)));
           }
         }
-        m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        m = max_nan(max_nan(m4[0], m4[1]), max_nan(m4[2], m4[3]));
         tc_fence_before();
         pending = true;
         continue;
       }
-      if (!wait(&sh.d_done, c & 1)) break;
-      // ---- token by token: an infinite or NaN value must not reach an earlier one
+      // ---- token by token: an infinite or NaN value must not reach an earlier one.  The state is still the one before the chunk
       const int len = min(C, n - c * C);
       const unsigned char *tile = ring + (c % kTcStages) * kStage;
       bool gone = false;
@@ -1307,7 +1337,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) delta_walk_tc_kernel(const Chun
       }
       if (gone) break;
       m = largest();
-      if (c + 1 < chunks) look_at_v(c + 1);
     }
     // a warp that gave up does not keep the others at the barriers that they may be at; behind them they see that it did (nothing
     // that they wait for next comes without this warp)

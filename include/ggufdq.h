@@ -451,8 +451,8 @@ QG_API qg_status qg_beam_reorder(const qg_kv_cache *caches, int n_layers, const 
  *   - max_new: the most tokens that a sequence of the call has, as far as the caller knows (0: not known).  It
  *     chooses between kernels; results are right whatever it says.
  *   - A slot outside [-1, n_slots) sets QG_EDEVICE_ID: a state_in of that kind counts as -1, the others as not kept.
- *   - A NaN or an infinity in a token's inputs reaches the tokens from that one on, never earlier ones nor other
- *     sequences or heads, and one in column j of v only column j of the outputs.
+ *   - A NaN or an infinity in a token's inputs, or one that finite inputs make of its update or state, reaches the tokens from that one
+ *     on, never earlier ones nor other sequences or heads, and one in column j of v only column j of the outputs.
  * All sums and states are f32; in chunks, state entries below 2^-126 become 0.  Prompts go through the tensor cores 32 tokens at a
  * time: keys, queries, states and what a chunk adds to them as sums of two f16 terms with a power of two per key, query and column of a
  * state (22 bits of its largest), everything else as three bf16 terms (24 bits).  So a token's error is that of its own and its

@@ -120,3 +120,36 @@ def test_a_state_forgotten_within_a_chunk(qg, Dk, Dv, reset):
         c.ba[:, :c.Hv] = -0.01
         c.ba[at, :c.Hv] = reset
         c.check(c.run(qg))
+
+
+@pytest.mark.parametrize("Dk,Dv", [(128, 128), (64, 256), (128, 64), (64, 32)])
+@pytest.mark.parametrize("what", ["v", "k", "growth", "largest"])
+def test_an_overflow_reaches_no_earlier_token(qg, Dk, Dv, what):
+    """Finite inputs whose updates or states leave f32: tokens before the first that does keep their results, and other columns all."""
+    for n, at in (([70, 40], 5), ([70, 40], 40), ([64], 60)):
+        B = len(n)
+        c = Followed(n, Dk=Dk, Dv=Dv, raw=False, l2=False, ins=list(range(B)), outs=list(range(B, 2 * B)), seed=38)
+        q, k, v, a, b = c.parts(c.x, c.ba)
+        h, j, cols = 1, 17, slice(None)
+        if what == "v":  # the step doubles it
+            v[at, h, j], b[at, h], cols = 3e38, 2.0, slice(17, 18)
+        elif what == "largest":  # next to f32's largest, and taken twice by the keys of the next token
+            v[at, h, j], b[at, h], cols = torch.finfo(torch.float32).max, 1.0, slice(17, 18)
+        elif what == "k":  # key head 0: value heads 0 and 1
+            k[at:at + 2, 0] *= 1e25
+        else:
+            a[at:at + 3, h] = 60.0
+        out, states, size, _ = c.reference()
+        o, s = [t.double().cpu() for t in c.run(qg)]
+        ok = (o - out).abs() <= 48 * 2.0 ** -24 * size * c.scale + 1e-37
+        hit = torch.zeros_like(ok)
+        hit[at:n[0], 0 if what == "k" else h:h + 1, cols] = True
+        hit[at:n[0], h, cols] = True
+        assert ok[~hit].all()
+        assert torch.isfinite(o[~hit]).all()
+        if what != "largest":
+            assert not torch.isfinite(o[min(at + 3, n[0] - 1), h, j])
+        for x in range(c.Hv):
+            if x != h and not (what == "k" and x == 0):
+                assert (s[B, x] - states[B, x]).abs().max() <= 1e-3
+    assert qg.device_status() == 0
