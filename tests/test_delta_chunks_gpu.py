@@ -153,3 +153,97 @@ def test_an_overflow_reaches_no_earlier_token(qg, Dk, Dv, what):
             if x != h and not (what == "k" and x == 0):
                 assert (s[B, x] - states[B, x]).abs().max() <= 1e-3
     assert qg.device_status() == 0
+
+
+@pytest.mark.parametrize("Dk,Dv", [(128, 128), (64, 128), (128, 256), (128, 64)])
+@pytest.mark.parametrize("what", ["q", "k", "v", "a", "b"])
+@pytest.mark.parametrize("at", [(2,), (45,), (100,), (145,), (40, 70), (31, 32, 149)], ids=str)
+def test_nonfinite_tokens_of_long_prompts(qg, Dk, Dv, what, at):
+    """A NaN or an infinity in the first, a middle and the last chunk of five, in chunks that follow one another and among
+    chunks without: heads of 128 columns take such a chunk token by token between others on the tensor cores."""
+    n = [150, 6, 70]
+    for value in (float("nan"), float("inf"), -float("inf")):
+        c = Followed(n, Dk=Dk, Dv=Dv, ins=[0, 1, 2], outs=[3, 4, 5], raw=False, seed=39)
+        out, states, size, sizes = c.reference()
+        h, j = 1, 33
+        t = c.parts(c.x, c.ba)["qkvab".index(what)]
+        cols = slice(j, j + 1) if what == "v" else slice(None)
+        heads = [0, 1] if what in "qk" else [h]  # key head 0: value heads 0 and 1
+        hit, shit = torch.zeros_like(out, dtype=torch.bool), torch.zeros_like(states, dtype=torch.bool)
+        if what == "a" and value < 0:  # forgets everything: finite, and the reference knows it
+            for i in at:
+                t[i, h] = value
+            c.check(c.run(qg))
+            continue
+        for i in at:
+            if what in "qk":
+                t[i, 0, 5] = value
+            elif what == "v":
+                t[i, h, j] = value
+            else:
+                t[i, h] = value
+            for x in heads:
+                hit[i:i + 1 if what == "q" else n[0], x, cols] = True
+                if what != "q":
+                    shit[3, x, :, cols] = True
+        o, s = [x.double().cpu() for x in c.run(qg)]
+        assert ((o - out).abs() <= 48 * 2.0 ** -24 * size * c.scale + 1e-37)[~hit].all()
+        assert not torch.isfinite(o[hit]).any()
+        assert ((s - states).abs() <= 48 * 2.0 ** -24 * sizes + 1e-37)[~shit].all()
+    assert qg.device_status() == 0
+
+
+@pytest.mark.parametrize("Dk,Dv", [(128, 128), (64, 256)])
+def test_extremes_of_whole_columns(qg, Dk, Dv):
+    """Heads of whole 128 columns: no decay and decays that leave nothing, steps of 0 to 2, zero rows, columns of 10^25 and 10^-30
+    beside others, states that are not finite."""
+    c = Delta([90], Dk=Dk, Dv=Dv, raw=False, ins=[0], outs=[1], seed=40)
+    g = torch.Generator().manual_seed(41)
+    kinds = torch.tensor([0.0, -float("inf"), -1e30, -104.0, -12.0, -1e-6])
+    c.ba[:, :c.Hv] = kinds[torch.randint(0, len(kinds), (90, c.Hv), generator=g)]
+    c.ba[:, 0], c.ba[:, 1] = 0.0, -11.0
+    c.ba[:, c.Hv:2 * c.Hv] = torch.tensor([0.0, 1.0, 0.5, 2.0])[torch.randint(0, 4, (90, c.Hv), generator=g)]
+    c.check(c.run(qg))
+    for big in (1e-30, 1e25):
+        c = Delta([50, 2], Dk=Dk, Dv=Dv, ins=[0, 1], outs=[2, 3], seed=42)
+        f = torch.where(torch.arange(Dv) % 2 == 0, big, 1.0)
+        c.states *= f
+        c.parts(c.x, c.ba)[2].mul_(f)
+        c.check(c.run(qg))
+    c = Delta([40, 1], Dk=Dk, Dv=Dv, ins=[0, 1], outs=[2, 3], seed=43)
+    q, k, v, _, _ = c.parts(c.x, c.ba)
+    q[3], k[7], k[40], v[9] = 0, 0, 0, 0
+    c.check(c.run(qg))
+    c = Delta([100, 40], Dk=Dk, Dv=Dv, ins=[0, 1], outs=[2, 3], seed=44)
+    out, _, size, _ = c.reference()
+    c.states[0, 1, 3, 7], c.states[1, 0, 9, 40] = float("inf"), float("nan")
+    o = c.run(qg)[0].double().cpu()
+    hit = torch.zeros_like(out, dtype=torch.bool)
+    hit[:100, 1, 7] = hit[100:, 0, 40] = True
+    assert ((o - out).abs() <= 48 * 2.0 ** -24 * size * c.scale + 1e-37)[~hit].all() and not torch.isfinite(o[hit]).any()
+    assert qg.device_status() == 0
+
+
+@pytest.mark.parametrize("Dv", [128, 64])
+def test_starts_that_do_not_rise_write_nothing_else(qg, Dv):
+    """Starts that are negative, fall or pass the rows: rows around, slots that nobody is given and what lies behind the workspace stay
+    as they were."""
+    c = Delta([20, 20, 20], Dv=Dv, ins=[0, 1, 2], outs=[3, 4, 5], seed=45)
+    hold = []
+    c.run(qg, hold=hold)
+    args, kw = list(hold[0]), dict(hold[1])
+    kw["q_start"] = torch.tensor([-5, 70, 30, 1000], dtype=torch.int32, device="cuda")
+    kw["max_new"] = 0
+    out = torch.full((c.T + 64, c.Hv, c.Dv), 7.5, device="cuda")
+    pool = torch.randn((c.slots + 4, c.Hv, c.Dk, c.Dv), device="cuda")
+    pool[2:2 + c.slots] = c.states.cuda()
+    need = qg.delta_workspace_size(c.T, 3, c.Hk, c.Hv, c.Dk, c.Dv)
+    ws = torch.full((need + 4096,), 90, dtype=torch.uint8, device="cuda")
+    before = pool.clone()
+    args[5], args[8], args[9] = pool[2:2 + c.slots], out[32:32 + c.T], ws[:need]
+    qg.delta_rule(*args, **kw)
+    torch.cuda.synchronize()
+    assert (out[:32] == 7.5).all() and (out[32 + c.T:] == 7.5).all() and (ws[need:] == 90).all()
+    kept = [i for i in range(c.slots + 4) if i - 2 not in (3, 5)]  # the second sequence has no rows
+    assert torch.equal(pool[kept], before[kept])
+    assert qg.device_status() == 0
