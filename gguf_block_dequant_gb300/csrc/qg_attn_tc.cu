@@ -811,12 +811,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const __grid_con
   pdl_launch_dependents();  // not before: blocks that wait beside this kernel cost it 5 %
 }
 
-// the register split above needs the launch's registers to be what it was made for
-bool split_fits(const void *kernel) {
-  cudaFuncAttributes f;
-  return cudaFuncGetAttributes(&f, kernel) == cudaSuccess && f.numRegs == kRegs;
-}
-
 bool make_maps(const AttnArgs &a, bool bf16, WideMaps *m) {
   const auto enc = encode_fn();
   if (!enc) return false;
@@ -849,7 +843,7 @@ static_assert(sizeof(WideBars) <= BAR_BYTES, "barriers and descriptions");
 template <int D, bool BF16, bool OUT32>
 qg_status wide_run(const AttnArgs &a, cudaStream_t s) {
   const auto k = attn_wide_kernel<D, BF16, OUT32>;
-  static const bool fits = split_fits(reinterpret_cast<const void *>(k));
+  static const bool fits = qg::split_fits(reinterpret_cast<const void *>(k), kRegs);  // the split above
   WideMaps maps;
   if (!fits || !make_maps(a, BF16, &maps) || !set_smem_attr(reinterpret_cast<const void *>(k), WideCfg<D>::SMEM))
     return QG_ECUDA;

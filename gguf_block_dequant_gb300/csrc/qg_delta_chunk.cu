@@ -1377,7 +1377,9 @@ cudaError_t both(const ChunkArgs &a, cudaStream_t s) {
   if (!qg::set_smem_attr(reinterpret_cast<const void *>(delta_prep_kernel<DK>), smem)) return cudaErrorInvalidValue;
   cudaError_t e = qg::launch_pdl(delta_prep_kernel<DK>, dim3(static_cast<unsigned>(a.slots) * a.d.Hk), dim3(kPrepWarps * 32), smem, s, a);
   if (e != cudaSuccess) return e;
-  if (a.d.Dv % 128 == 0) {
+  // a build of other registers than the split's goes the other way, which takes every width
+  static const bool fits = qg::split_fits(reinterpret_cast<const void *>(delta_walk_tc_kernel<DK>), kTcRegs);
+  if (a.d.Dv % 128 == 0 && fits) {
     constexpr int tc = TcSmem<DK>::kBytes;
     if (!qg::set_smem_attr(reinterpret_cast<const void *>(delta_walk_tc_kernel<DK>), tc)) return cudaErrorInvalidValue;
     return qg::launch_pdl(delta_walk_tc_kernel<DK>, dim3(static_cast<unsigned>(a.d.B) * a.d.Hv * (a.d.Dv / 128)), dim3(kTcThreads), tc, s, a);

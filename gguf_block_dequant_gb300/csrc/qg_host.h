@@ -33,6 +33,13 @@ const DeviceInfo &device_info();
 // Raise a kernel's dynamic shared-memory limit on the current device (cached).
 bool set_smem_attr(const void *func, uint32_t bytes);
 
+// Whether a kernel that splits its registers among its warps (setmaxnreg) was built with the count a thread that its split adds up
+// to: with another the split would wait for ever, so the kernel must not be launched then.
+inline bool split_fits(const void *kernel, int regs) {
+  cudaFuncAttributes f;
+  return cudaFuncGetAttributes(&f, kernel) == cudaSuccess && f.numRegs == regs;
+}
+
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Launch with programmatic stream serialization allowed: the kernel may begin while its
