@@ -163,8 +163,9 @@ __global__ void __launch_bounds__(kBookThreads) kv_reserve_kernel(const ReserveA
     }
   };
   load(0);
-  // needs and copies in one sum: the copies above bit 40.  upto[b]: free pages taken before b
-  constexpr int kHigh = 40;
+  // needs and copies in one sum, the copies above bit 47: 65535 sequences need less than that many pages, and copy fewer than 2^16.
+  // upto[b]: free pages taken before b
+  constexpr int kHigh = 47;
   long long sums = 0, sum;
   Need r{0, 0, true, false};
   int at = 0;
@@ -181,8 +182,7 @@ __global__ void __launch_bounds__(kBookThreads) kv_reserve_kernel(const ReserveA
       }
     }
     if (!r.ok) bad();
-    // beyond the pool's size there are too few pages in any case
-    const long long mine = min(r.n, a.n_pages + 1) + (static_cast<long long>(r.copies) << kHigh);
+    const long long mine = r.n + (static_cast<long long>(r.copies) << kHigh);
     const long long before = sums + block_scan<long long>(mine, &sum);
     sums += sum;
     const long long need = before & ((1LL << kHigh) - 1);

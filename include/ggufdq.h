@@ -536,7 +536,7 @@ QG_API qg_status qg_kv_fork(const qg_kv_cache *cache, const qg_kv_batch *batch, 
  *   - A sequence whose last page is begun and had more than one holder when the call began gets a page of its own
  *     in its place, with the begun rows copied, in every layer; then follow the pages that the new length needs.  New pages are
  *     the lowest free ones, in the order of the sequences and their columns, each with one holder.
- *   - missing (device int32[1]): 0, or how many free pages were too few; then the call changes nothing else. A batch
+ *   - missing (device int32[1]): 0, or how many free pages were too few (at most 2^31 - 1); then the call changes nothing else. A batch
  *     without sequences enqueues nothing and leaves missing as it was.
  *   - A negative add[b], a length that is negative or would pass the page list, and a begun page outside the pool set
  *     QG_EDEVICE_ID and leave b as it is.

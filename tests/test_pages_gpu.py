@@ -374,3 +374,20 @@ def test_graph_and_stream(qg):
         graph.replay()
         torch.cuda.synchronize()
         s.same()
+
+
+def test_more_pages_than_the_pool_has(qg):
+    """What is missing is told in full where one sequence alone needs more pages than there are, and where many do."""
+    s = Server(qg, n_pages=4, B=3, cols=5000, page=1, layers=1)
+    s.up()
+    for add in ([10, 0, 0], [5, 0, 0], [0, 4000, 4999], [3, 3, 0]):
+        want = sum(add) - 4
+        s.call("reserve", add)
+        assert s.missing.item() == want
+        s.same()
+    s = Server(qg, n_pages=7, B=1200, cols=100, page=2, layers=1, Hkv=1)
+    s.refs = [1] * 7
+    s.up()
+    s.call("reserve", [199 + b % 2 for b in range(1200)])
+    assert s.missing.item() == 1200 * 100
+    s.same()
