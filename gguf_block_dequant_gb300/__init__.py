@@ -777,15 +777,14 @@ def kv_reserve(caches, batch, refs, add, missing, workspace, stream=None):
     _ints(add, batch.n_seqs, "add")
     _ints(missing, 1, "missing")
     _on(_page_call(caches, batch, refs), "refs add missing workspace", refs, add, missing, workspace)
-    if batch.n_seqs == 0:  # the call would enqueue nothing and leave missing as it was
+    s = _stream(stream)
+    _call("qg_kv_reserve", caches, len(caches), ctypes.byref(batch), _ptr(refs), _ptr(add), _ptr(missing), _ptr(workspace),
+          _nbytes(workspace), s)
+    if batch.n_seqs == 0:  # the call has looked at its arguments, enqueued nothing and left missing as it was
         import torch
 
-        s = _stream(stream)
         with torch.cuda.stream(torch.cuda.ExternalStream(s) if s else torch.cuda.default_stream()):
             missing.zero_()
-        return
-    _call("qg_kv_reserve", caches, len(caches), ctypes.byref(batch), _ptr(refs), _ptr(add), _ptr(missing), _ptr(workspace),
-          _nbytes(workspace), _stream(stream))
 
 
 def kv_compact(caches, batch, src, keep_start, keep, stream=None):

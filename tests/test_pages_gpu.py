@@ -391,3 +391,14 @@ def test_more_pages_than_the_pool_has(qg):
     s.call("reserve", [199 + b % 2 for b in range(1200)])
     assert s.missing.item() == 1200 * 100
     s.same()
+
+
+def test_reserve_without_sequences_refuses_what_is_refused_otherwise(qg):
+    """Caches of two geometries."""
+    s = Server(qg, n_pages=6, B=0, cols=8)
+    s.up()
+    none = torch.zeros(0, dtype=torch.int32, device="cuda")
+    k, k2 = (torch.zeros((6, 16, h, 64), dtype=torch.float16, device="cuda") for h in (2, 4))
+    with pytest.raises(qg.QGError):
+        qg.kv_reserve(qg.kv_caches([k, k2], [k, k2]), s.batch, s.drefs, none, s.missing, s.ws)
+    assert s.missing.item() == -5
