@@ -507,7 +507,8 @@ QG_API qg_status qg_token_probs(const float *logits, const float *temperature, i
  *   - kv_len, kept_len (both or neither; int32[n_seqs]): kept_len[b] = kv_len[b] - (drafts not accepted), what qg_kv_fork
  *     is to leave of a cache that holds all of the step's rows.  They may be one array.
  *   - Negative and NaN probabilities count as 0, those above 2^100 as 2^100, NaN and negative random numbers as
- *     0.  A drafted token outside [0, V) is not accepted, sets QG_EDEVICE_ID, and nothing is taken from probs.
+ *     0.  A drafted token outside [0, V) is not accepted and sets QG_EDEVICE_ID: with draft_probs the next token is drawn from
+ *     max(probs - draft_probs, 0) as for any other draft, and where drafts are certain from probs, of which nothing is taken.
  *   - A sequence without rows gets 0, -1 and its kv_len.  q_start NULL: one row each (a sampler; tokens and u may be NULL).
  * probs, draft_probs 16-byte aligned, the rest 4-byte.  1 <= V <= 2^20, n_seqs <= 65535, n_rows <= 2^24. */
 QG_API qg_status qg_draft_verify(const float *probs, const float *draft_probs, const int32_t *tokens, const float *u,
@@ -538,8 +539,8 @@ QG_API qg_status qg_kv_fork(const qg_kv_cache *cache, const qg_kv_batch *batch, 
  *     the lowest free ones, in the order of the sequences and their columns, each with one holder.
  *   - missing (device int32[1]): 0, or how many free pages were too few (at most 2^31 - 1); then the call changes nothing else. A batch
  *     without sequences enqueues nothing and leaves missing as it was.
- *   - A negative add[b], a length that is negative or would pass the page list, and a begun page outside the pool set
- *     QG_EDEVICE_ID and leave b as it is.
+ *   - add[b] 0 leaves b as it is, whatever its length and pages.  A negative add[b], a length that is negative or would pass the
+ *     page list, and a begun page outside the pool set QG_EDEVICE_ID and leave b as it is.
  * caches: HOST array of n_layers (<= 128) caches of one geometry.  Workspace: qg_kv_reserve_workspace_size bytes,
  * 16-byte aligned, contents irrelevant; one call at a time may use it. */
 QG_API size_t qg_kv_reserve_workspace_size(const qg_kv_cache *caches, const qg_kv_batch *batch);

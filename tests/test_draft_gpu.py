@@ -337,3 +337,22 @@ def test_graph_and_stream(qg):
     torch.cuda.synchronize()
     ref = verify_reference(probs.cpu().numpy(), q.cpu().numpy(), tokens, u.cpu().numpy(), un.cpu().numpy(), start)
     assert (acc.tolist(), tok.tolist()) == ref[:2]
+
+
+@pytest.mark.parametrize("V", [9, 6001])
+@pytest.mark.parametrize("token", [-1, None])
+def test_a_drafted_token_outside_the_vocabulary(qg, V, token):
+    """It is not accepted: with a drafter's probabilities the difference is drawn from, with certain drafts the target's whole row."""
+    rng = np.random.default_rng(V)
+    p, q, tokens, _, _, start = drafted(rng, [2, 2], V)
+    tokens[1] = tokens[5] = V if token is None else token
+    u, un = np.zeros(6, np.float32), np.array([0.999, 0.001], np.float32)
+    got = run_verify(qg, p, q, tokens, u, un, start)
+    assert got == verify_reference(p, q, tokens, u, un, start) and got[0] == [0, 1]
+    rest = np.maximum(p[0] - q[0], 0)
+    assert rest[got[1][0]] > 0
+    assert qg.device_status() == 1 << qg.QG_EDEVICE_ID
+    got = run_verify(qg, p, None, tokens, u, un, start)
+    assert got == verify_reference(p, None, tokens, u, un, start) and got[0] == [0, 1]
+    assert run_verify(qg, p[[0, 4]], None, np.zeros(2), np.zeros(2), un, [0, 1, 2])[1] == got[1]  # the rows as a sampler takes them
+    assert qg.device_status() == 1 << qg.QG_EDEVICE_ID
