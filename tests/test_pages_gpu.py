@@ -402,3 +402,23 @@ def test_reserve_without_sequences_refuses_what_is_refused_otherwise(qg):
     with pytest.raises(qg.QGError):
         qg.kv_reserve(qg.kv_caches([k, k2], [k, k2]), s.batch, s.drefs, none, s.missing, s.ws)
     assert s.missing.item() == -5
+
+
+@pytest.mark.parametrize("start", [[0, -7, 90, 3, 5, 0, 1 << 20], [5, 4, 3, 2, 1, 0, -1], [-(1 << 31), 0, 0, 0, 0, 0, 2 ** 31 - 1], [9] * 7],
+                         ids=str)
+def test_compact_with_starts_that_do_not_rise(qg, start):
+    """Lists, lengths and every page but the receiver's stay as they are, whatever its tokens are."""
+    s = Server(qg, n_pages=40, B=6, cols=4, seed=7)
+    s.reserve([40, 20, 2, 20, 20, 20])
+    s.up()
+    s.call("compact", [-1, -1, -1, -1, -1, 4], start, [3, 4])
+    assert qg.device_status() in (0, 1 << qg.QG_EDEVICE_ID)
+    held = s.table[5][:2]
+    others = [p for p in range(40) if p not in held]
+    assert (s.dkv.tolist(), s.drefs.tolist(), s.dtable.tolist()) == (s.kv, s.refs, s.table)
+    assert torch.equal(s.dpool.cpu()[:, others].view(torch.int16), s.pool[:, others].view(torch.int16))
+    # what the receiver's pages hold: tokens of the source, or what they held
+    got, old = s.dpool.cpu()[:, held].flatten(1, 2), s.pool[:, held].flatten(1, 2)
+    source = s.pool[:, s.table[4][0]][:, [3, 4]]
+    for i in range(got.shape[1]):
+        assert any(torch.equal(got[:, i], x) for x in (old[:, i], source[:, 0], source[:, 1]))
