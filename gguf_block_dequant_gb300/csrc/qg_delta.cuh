@@ -31,8 +31,10 @@ QG_DEVICE int delta_tok(const DeltaArgs &a, int b) {
 }
 QG_DEVICE int delta_key_head(const DeltaArgs &a, int h) { return a.tiled ? h % a.Hk : h / (a.Hv / a.Hk); }
 
-// log decay and step of value head h at token t.  Log decays below -110 count as -110: e^g is 0 in f32, and
-// sums of them stay finite (fmaxf would turn NaN into -110).
+constexpr float kDeltaForgets = -110.f;  // a log decay of which nothing is left: e^g is 0 in f32
+
+// log decay and step of value head h at token t.  Log decays below kDeltaForgets count as that: sums of them stay finite (fmaxf
+// would turn NaN into it).
 QG_DEVICE float2 delta_gates(const DeltaArgs &a, int t, int h) {
   float g = __ldg(a.a + t * a.a_stride + h), beta = __ldg(a.b + t * a.b_stride + h);
   if (a.a_scale) {
@@ -40,7 +42,7 @@ QG_DEVICE float2 delta_gates(const DeltaArgs &a, int t, int h) {
     g = __ldg(a.a_scale + h) * (x > 0.f ? x + log1pf(expf(-x)) : log1pf(expf(x)));
     beta = 1.f / (1.f + expf(-beta));
   }
-  return make_float2(g < -110.f ? -110.f : g, beta);
+  return make_float2(g < kDeltaForgets ? kDeltaForgets : g, beta);
 }
 
 }  // namespace qg

@@ -53,7 +53,7 @@ struct Factors {
   float wk[C];     // e^{G_C - G_j} sk_j
   float alpha[C], beta[C], sk[C], sq[C];  // token by token, for chunks with infinite or NaN values
   float dec;       // e^{G_C}
-  int odd;         // such a value among the queries, keys and gates, or a factor that leaves f32
+  int odd;         // such a value among the queries, keys and gates, a factor that leaves f32, or a state that is forgotten and grows
   float pad[30];
 };
 constexpr int kTA = 2 * kThree + static_cast<int>(sizeof(Factors));
@@ -418,7 +418,9 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 5) delta_prep_kernel(const Ch
       f->sk[lane] = scale_k[lane];
       f->sq[lane] = scale_q[lane];
       const bool bad = !(fabsf(ga.x) < INFINITY && fabsf(ga.y) < INFINITY && top < kMost && eg < kMost && wk < kMost);
-      const int odd = __any_sync(0xFFFFFFFFu, bad) || bad_rows;
+      // a decay that leaves nothing must not be made up for by ones that grow: sums of log decays cannot tell
+      const bool again = __any_sync(0xFFFFFFFFu, ga.x <= qg::kDeltaForgets) && __any_sync(0xFFFFFFFFu, ga.x > 0.f);
+      const int odd = __any_sync(0xFFFFFFFFu, bad) || again || bad_rows;
       if (lane == 0) {
         f->dec = chunk_decay(gl.x + gl.y);
         f->odd = odd;

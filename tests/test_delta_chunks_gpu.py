@@ -46,11 +46,12 @@ class Followed(Delta):
             err = torch.zeros_like(size[0])
             for t in range(self.start[s], self.start[s] + n):
                 S = torch.exp(g[t])[:, None, None] * S
+                S = torch.where(S.abs() < 2.0 ** -150, 0.0, S)  # states are f32: what is below its least value is gone
                 held = S.norm(dim=1)
                 u = beta[t][:, None] * (v[t] - torch.einsum("hij,hi->hj", S, k[t]))
                 S = S + k[t][..., None] * u[:, None]
                 out[t] = torch.einsum("hij,hi->hj", S, q[t])
-                err = grow[t][:, None] * err + held + S.norm(dim=1) + v[t].abs()
+                err = grow[t][:, None] * err + held + S.norm(dim=1) + v[t].abs() + 2.0 ** -149
                 size[t] = err
             if n and self.outs and self.outs[s] >= 0:
                 states[self.outs[s]], sizes[self.outs[s], :, 0] = S, err
@@ -246,4 +247,21 @@ def test_starts_that_do_not_rise_write_nothing_else(qg, Dv):
     assert (out[:32] == 7.5).all() and (out[32 + c.T:] == 7.5).all() and (ws[need:] == 90).all()
     kept = [i for i in range(c.slots + 4) if i - 2 not in (3, 5)]  # the second sequence has no rows
     assert torch.equal(pool[kept], before[kept])
+    assert qg.device_status() == 0
+
+
+@pytest.mark.parametrize("Dk,Dv", [(128, 128), (64, 256), (128, 64), (64, 32)])
+@pytest.mark.parametrize("reset", [-float("inf"), -200.0, -110.0])
+def test_what_is_forgotten_does_not_grow_back(qg, Dk, Dv, reset):
+    """A decay that leaves nothing, then log decays that add up to more than it took in the same chunk and the next: without
+    new values the state stays 0, and with them it is theirs."""
+    for n, at in (([60], 3), ([60], 40), ([12], 3)):
+        for later, first in ((0.0, 60.0), (0.0, 30.0), (1.0, 5.0)):
+            c = Followed(n, Dk=Dk, Dv=Dv, raw=False, ins=[0], outs=[1], seed=46)
+            c.ba[:, :c.Hv] = -0.1
+            c.ba[at, :c.Hv] = reset
+            c.ba[at + 1:, :c.Hv] = 0.5
+            c.ba[at + 1:at + 3, :c.Hv] = first
+            c.parts(c.x, c.ba)[2][at:] *= later
+            c.check(c.run(qg))
     assert qg.device_status() == 0
