@@ -16,7 +16,8 @@ using qg::DeltaArgs;
 // column group) holds NR rows of four columns in registers, which are read once and written once a call (and once a
 // token that is kept): HBM bounds a batch of single tokens.  Both products with the old state,
 // S^T k and S^T q, are summed in one pass over the registers (the output is e^g S^T q + (q . k) u), so a token
-// costs one exchange between warps.  Queries, keys and gates of up to TG tokens are made ready at a time, a warp per
+// costs one exchange between warps, and the wait for its values and its state's slot, which are loaded when it is its turn (0.6 us in
+// all where one sequence is alone; of 16 sequences of 2 to 7 kept tokens the warps wait for loads most).  Queries, keys and gates of up to TG tokens are made ready at a time, a warp per
 // token.
 constexpr int TG = 16;
 
@@ -172,7 +173,7 @@ template <int DK>
 cudaError_t tokens_launch(const DeltaArgs &a, int first_len, int sms, cudaStream_t s) {
   // 64 columns to a CTA of four warps, five of which share an SM, so that some read while others exchange or write (64 sequences of
   // 32 heads of 128 x 128, 268 MB: 49.4 us, 5.4 TB/s; with eight warps 60, with 128 columns and eight warps 57.7, six CTAs an SM
-  // spill: 62.7); 32 columns to one of eight where that does not give two CTAs an SM (one sequence: 3.8 us)
+  // spill more than two registers: 62.7); 32 columns to one of eight where that does not give two CTAs an SM (one sequence: 3.8 us)
   const int jc = a.Dv % 64 == 0 && static_cast<long long>(a.B) * a.Hv * (a.Dv / 64) >= 2 * sms ? 64 : 32;
   const dim3 grid(static_cast<unsigned>(a.B) * a.Hv * (a.Dv / jc));
   if (jc == 64) return qg::launch_pdl(delta_tokens_kernel<DK, 64, 128>, grid, dim3(128), 0, s, a, first_len);

@@ -17,8 +17,9 @@ struct DeltaArgs {
 
 constexpr int kDeltaChunk = 32;  // tokens of a chunk
 // sequences from this many tokens on go in chunks.  Where the two meet (32 heads of 128, token by token / in chunks): 8 sequences of
-// 16 tokens 34 / 31 us and of 24 tokens 49 / 31, 32 of 16 tokens 80 / 92 and of 24 tokens 115 / 94, one of 24 tokens 18 / 22
-// and of 48 tokens 32 / 26
+// 20 tokens 36 / 27 us and of 24 tokens 42 / 27, 32 of 20 tokens 116 / 96 and of 24 tokens 134 / 97 (of 16 tokens token by
+// token 97).  One sequence alone would rather wait: of 20 tokens 13.5 / 16.8, of 24 tokens 15.3 / 16.8, of 28 tokens 17.8 / 17.0 and of
+// 48 tokens 28 / 20
 constexpr int kDeltaFirstLen = 20;
 
 // the chunk kernels (qg_delta_chunk.cu), for sequences of first_len tokens and more

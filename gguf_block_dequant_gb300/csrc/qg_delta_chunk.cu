@@ -172,8 +172,8 @@ struct ChunkArgs {
 // A CTA of four warps per chunk and key head.  Rows are normalised and split by a warp each; the products of keys with keys and
 // queries with keys take a warp per 16 rows; then a warp per value head solves for T, a lane per column (in blocks of 16: in
 // one block of 32 it all took 39 us more), and another makes the decayed Q K^T.  30042 tokens, 16 key and 32 value heads:
-// 264 us for 1.27 GB moved, 4800 instructions a value head and chunk at 0.45 an issue slot, shared memory's pipe busy half of the
-// time.  Latency bounds it, so rows of CTAs to come are sent to L2 (48 us less), and registers and shared memory are kept to five
+// 285 us for 1.39 GB moved, 4900 instructions a value head and chunk at 0.43 an issue slot, shared memory's pipe busy 57 % of the
+// time, 16 and 18 registers a thread spilled (heads of 128 and of 64).  Latency bounds it, so rows of CTAs to come are sent to L2 (48 us less), and registers and shared memory are kept to five
 // CTAs an SM (four: 13 us more): decays (powers of two of
 // differences of sums in log2) are made again rather than kept, and T is turned in the room of the tiles, from which it and Q K^T
 // leave as bulk copies (16 bytes a lane stored to as many lines took 34 us more).  Sums of log decays in two floats rather than
@@ -514,8 +514,8 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 5) delta_prep_kernel(const Ch
 // A warp owns 16 columns of a head's state, as S^T in the accumulator layout (rows: columns of S): it is the left operand of
 // both products with the old state, U^T in turn the left operand of the next two, so nothing but the tiles from the
 // kernel above passes through shared memory, and warps never wait for one another.  The tiles come through a ring of
-// bulk copies; the warp that leaves a stage last asks for its next contents.  For heads whose columns are no multiple of 128 (a
-// head of 128 takes 4.3 us a chunk here with its eight warps on one SM, 324 products of 8 cycles each, and 3.3 below).
+// bulk copies; the warp that leaves a stage last asks for its next contents.  For heads whose columns are no multiple of 128 (64
+// columns with four warps take 3.9 us a chunk, 360 products of 8 cycles each a warp, where 128 take 3.1 below).
 template <int DK, int W, int NST>
 struct WalkSmem {
   static constexpr int kStage = (Tiles<DK>::kKQAll + kTA + 1023) / 1024 * 1024;  // pieces are found by exclusive or
@@ -890,9 +890,9 @@ __global__ void __launch_bounds__(W * 32) delta_walk_kernel(const ChunkArgs a) {
 //   a producer   bulk copies into the ring (a row of values each lane: that would hold control up by 1700 cycles)
 //   control      the products X = S^T K^T, O = S^T Q^T, U = R T^T, D = W K, O2 = U A^T
 // Every wait ends with its phase or after kTcWaitCycles, which makes the CTA give up.
-// The chain of a chunk bounds it, 6000 cycles or 3.2 us where its products alone are 2900: state in two terms 900, X 1000, R 400, U 250,
-// its terms 400, D 600, the state's update 430, and about 200 from each arrival to the waiter (five prompts of 30042 tokens in all, the
-// longest of 7842: 820 us; the tensor cores' pipe is busy 23 % of a head's time).
+// The chain of a chunk bounds it, 5800 cycles or 3.1 us where its products alone are 3400: state in two terms 740, X and meanwhile the
+// outputs of the chunk before 2050, R 450, U 550, W 510 and U's terms 290, D 750, the state's update 480 (stamps in a copy of the build; five
+// prompts of 30042 tokens in all, the longest of 7842: 761 us; the tensor cores' pipe is busy 26 % of a head's time).
 constexpr int kTcThreads = 384;                    // two groups of four warps, control, the producer and two idle warps
 constexpr int kTcRegs = 168, kTcRegsWork = 208, kTcRegsRest = 88;
 static_assert(2 * kTcRegsWork + kTcRegsRest <= 3 * kTcRegs, "the warpgroups' shares come from the launch's total");

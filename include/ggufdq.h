@@ -446,6 +446,7 @@ QG_API qg_status qg_beam_reorder(const qg_kv_cache *caches, int n_layers, const 
  *     names a slot for the state after each single token (-1: not kept): a server that drafts takes the one after the
  *     last token it keeps as the next call's state_in.  A slot may be read and then written by the same sequence;
  *     no slot may be written by one sequence and used by another in one call.  A sequence without tokens writes none.
+ *   - out and the states overlap no other array of the call.
  *   - q_start: device int32[n_seqs + 1], the first token row of each sequence, rising from 0 (NULL: one token each,
  *     n_tokens == n_seqs).  Rows behind the last sequence are left as they are.
  *   - max_new: the most tokens that a sequence of the call has, as far as the caller knows (0: not known).  It
