@@ -515,7 +515,7 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 5) delta_prep_kernel(const Ch
 // both products with the old state, U^T in turn the left operand of the next two, so nothing but the tiles from the
 // kernel above passes through shared memory, and warps never wait for one another.  The tiles come through a ring of
 // bulk copies; the warp that leaves a stage last asks for its next contents.  For heads whose columns are no multiple of 128 (64
-// columns with four warps take 3.9 us a chunk, 360 products of 8 cycles each a warp, where 128 take 3.1 below).
+// columns with four warps take 3.6 us a chunk, 360 products of 8 cycles each a warp, where 128 take 3.1 below).
 template <int DK, int W, int NST>
 struct WalkSmem {
   static constexpr int kStage = (Tiles<DK>::kKQAll + kTA + 1023) / 1024 * 1024;  // pieces are found by exclusive or
