@@ -8,7 +8,8 @@
 //   O = diag(e^G) Q S0 + [e^{G_i - G_j} q_i . k_j, j <= i] U,   S = e^{G_C} S0 + K^T diag(e^{G_C - G}) U.
 // Everything that does not need S0 (norms, T, the decayed Q K^T) comes from one kernel, parallel over chunks and heads;
 // a second one walks the chunks of each head with the state in registers.  No exponent is above 0 while log
-// decays are not (positive ones are allowed); sums of them are kept in two terms, so that decays between neighbours stay exact after strong ones.
+// decays are not (positive ones are allowed); sums of them are kept in two terms, so that decays between neighbours stay exact
+// after strong ones.
 //
 // Products run on the tensor cores with f32 sums.  Keys, queries, the state and what a chunk adds to it are x = s (hi + lo) in f16,
 // s a power of two per row that brings the row's largest magnitude to [2^7, 2^8), hi the multiple of 2^-3 nearest x/s and lo the
@@ -173,8 +174,8 @@ struct ChunkArgs {
 // queries with keys take a warp per 16 rows; then a warp per value head solves for T, a lane per column (in blocks of 16: in
 // one block of 32 it all took 39 us more), and another makes the decayed Q K^T.  30042 tokens, 16 key and 32 value heads:
 // 285 us for 1.39 GB moved, 4900 instructions a value head and chunk at 0.43 an issue slot, shared memory's pipe busy 57 % of the
-// time, 16 and 18 registers a thread spilled (heads of 128 and of 64).  Latency bounds it, so rows of CTAs to come are sent to L2 (48 us less), and registers and shared memory are kept to five
-// CTAs an SM (four: 13 us more): decays (powers of two of
+// time, 16 and 18 registers a thread spilled (heads of 128 and of 64).  Latency bounds it, so rows of CTAs to come are sent to L2
+// (48 us less), and registers and shared memory are kept to five CTAs an SM (four: 13 us more): decays (powers of two of
 // differences of sums in log2) are made again rather than kept, and T is turned in the room of the tiles, from which it and Q K^T
 // leave as bulk copies (16 bytes a lane stored to as many lines took 34 us more).  Sums of log decays in two floats rather than
 // doubles took no less.
